@@ -447,6 +447,207 @@ int spec_depth_ctl_observe(spec_depth_ctl* c, int32_t d, int32_t n_seq, const in
  * +infinity for depths without a round time); either may be NULL. */
 int spec_depth_ctl_estimates(const spec_depth_ctl* c, double* p, double* r);
 
+/* ===========================================================================
+ * Drafted trees: instead of one chain of drafts per sequence, the target
+ * evaluates a tree of candidates (several tokens per position) in one pass,
+ * and the accepted root-to-node path is committed.  The operators below are
+ * the steps of such a round outside the linear layers: sampling candidates
+ * (spec_sample), attention of the tree's nodes over the cache
+ * (spec_tree_attn), acceptance along the tree (spec_accept_tree) and the
+ * cache's pages (spec_pages_*).
+ *
+ * They allocate nothing and keep nothing between calls: scratch is the
+ * caller's, errors seen on the device go to the caller's `status` array, and
+ * calls may run at the same time on several streams, or be captured into
+ * graphs, as long as the arrays that they write are not shared.
+ * ======================================================================== */
+
+/* A KV cache in pages (HOST struct of DEVICE pointers, all caller-owned; the
+ * struct is read during the call only).  Position p of slot s lives in row
+ * p % page_size of page table[s][p / page_size], in every layer.  A page is
+ * free when its reference count is zero; a page that several slots hold
+ * (after spec_pages_fork) is never written. */
+typedef struct {
+  uint16_t* k; /* fp16 [n_layers][n_pages][n_kv_heads][page_size][head_dim] */
+  uint16_t* v; /* the same layout; both 16-byte aligned */
+  int64_t layer_stride; /* elements from one layer to the next (>= a layer's, a multiple of 8) */
+  int32_t n_layers, n_pages, n_kv_heads, page_size;
+  int32_t head_dim;     /* a multiple of 8 (spec_tree_attn: 64 or 128) */
+  int32_t n_slots, max_pages;
+  int32_t* table; /* [n_slots][max_pages] page ids, -1 from the first entry without a page on */
+  int32_t* refs;  /* [n_pages] slots that hold the page; NULL: pages fixed to their slots */
+  int32_t* len;   /* [n_slots] committed positions */
+} spec_pages;
+
+/* Bits of a `status` entry (0: done).  An entry of a call whose status is not
+ * 0 has changed nothing; the call's other entries are done all the same,
+ * unless the function says otherwise. */
+#define SPEC_ST_SLOT 1   /* slot or page id out of range, or named where it must not be */
+#define SPEC_ST_PAGE 2   /* the table has no valid page where one is needed */
+#define SPEC_ST_SHARED 4 /* the page is held by another slot */
+#define SPEC_ST_FULL 8   /* not enough free pages, or more positions than max_pages hold */
+#define SPEC_ST_TREE 16  /* bad parents, node count or path */
+
+#define SPEC_MAX_TREE 64 /* nodes of a tree */
+
+/* The model's own cache as pages: one page of max_ctx positions per slot
+ * (page id = slot), table, and len = the model's n_past; refs is NULL, so
+ * fork, extend and free refuse it (SPEC_E_UNSUPPORTED), and its pages are
+ * copied from slot to slot by spec_pages_copy.  What spec_pages_commit
+ * writes is what the model's later rounds read. */
+int spec_model_pages(spec_model* m, spec_pages* out);
+
+/* Copies page src[i] to page dst[i] in every layer, i < n (device int32 [n]):
+ * the first n_pos[i] positions of it (device int32 [n], 0 <= n_pos <=
+ * page_size), or all of them if n_pos is NULL.  A dst that is named twice or
+ * is also a src is refused (SPEC_ST_SLOT), each entry that names it.
+ * Reference counts and tables are not looked at. */
+int spec_pages_copy(const spec_pages* kv, int n, const int32_t* src, const int32_t* dst,
+                    const int32_t* n_pos, int32_t* status, void* stream);
+
+/* Slot dst[i] becomes a branch of slot src[i] (device int32 [n]): it gets the
+ * src's length and shares the pages of its committed positions.  dst must
+ * hold no pages, and appear neither twice nor as a src (SPEC_ST_SLOT); src
+ * may be named any number of times. */
+int spec_pages_fork(const spec_pages* kv, int n, const int32_t* src, const int32_t* dst,
+                    int32_t* status, void* stream);
+
+/* Makes positions [len, len + n_new[i]) of slot slots[i] writable (device
+ * int32 [n], slots distinct, n <= 1024): the missing pages are taken, and a
+ * partly filled last page that other slots hold too is replaced by a page of
+ * its own with the filled positions copied -- the last of its holders, when
+ * all of them are extended in one call, keeps it.  The pages taken are the
+ * lowest free ones, in the order of the entries, an entry's copy before its
+ * further pages: the result is a function of the arrays alone.  When the
+ * free pages do not suffice for every entry that is in order, none gets any
+ * (SPEC_ST_FULL).  copies int32 [n][2]: (page, its copy) of each entry, or
+ * (-1, -1).  A shared page behind the last committed position (possible only
+ * if len was lowered) is refused (SPEC_ST_SHARED). */
+int spec_pages_extend(const spec_pages* kv, int n, const int32_t* slots, const int32_t* n_new,
+                      int32_t* copies, int32_t* status, void* stream);
+
+/* Commits rows of new keys and values behind a slot's committed positions, in
+ * every layer: position len + j of slot slots[i] gets row path[i][j] of entry
+ * i, j < n_path[i] (device; slots distinct; path int32 [n][nt], or NULL for
+ * rows 0, 1, ...; 0 <= n_path <= nt).  With the path of spec_accept_tree this
+ * compacts the accepted nodes of a tree into the cache; with path NULL it
+ * appends a prompt.
+ *   k_new, v_new  fp16 [n_layers][n][nt][n_kv_heads][head_dim], 16-byte
+ *                 aligned; new_layer_stride elements from one layer to the
+ *                 next (0: contiguous; a multiple of 8)
+ *   new_len       int32 [n_slots]: new_len[slot] = len[slot] + n_path for the
+ *                 call's slots; NULL: len itself, advanced in place
+ * The pages must be there (spec_pages_extend) and held by this slot alone. */
+int spec_pages_commit(const spec_pages* kv, int n, const int32_t* slots, int nt,
+                      const uint16_t* k_new, const uint16_t* v_new, int64_t new_layer_stride,
+                      const int32_t* path, const int32_t* n_path, int32_t* new_len,
+                      int32_t* status, void* stream);
+
+/* Gives back every page of the slots (device int32 [n], distinct) and sets
+ * their length to 0.  Ids out of range in a slot's row of the table are
+ * dropped (SPEC_ST_PAGE, the slot is empty all the same). */
+int spec_pages_free(const spec_pages* kv, int n, const int32_t* slots, int32_t* status,
+                    void* stream);
+
+/* The trees of one round: n_seq sequences of up to nt nodes. */
+typedef struct {
+  int32_t n_seq, nt;       /* 1 <= nt <= SPEC_MAX_TREE */
+  int32_t n_q_heads;       /* a positive multiple of the cache's n_kv_heads */
+  int32_t window;          /* 0: every earlier position is visible; w > 0: the last w are */
+  int32_t sinks;           /* with a window: the first `sinks` positions stay visible too */
+  float scale;             /* of the scores; 0: 1 / sqrt(head_dim) */
+  const int32_t* slots;    /* device [n_seq]; a slot may be named more than once */
+  const int32_t* parents;  /* device [n_seq][nt]: an earlier node, or -1 (child of the
+                              committed context); NULL: a chain, parent i - 1 */
+  const int32_t* n_nodes;  /* device [n_seq], 0 <= n_nodes <= nt; NULL: nt each */
+} spec_tree;
+
+/* Attention of the trees' nodes over the committed cache of `layer` and over
+ * themselves.  Node i of a sequence sits at position P_i = len + depth_i (a
+ * child of the context has depth 0) and sees the committed positions p < len
+ * and, of the nodes, itself and its ancestors; with a window w, of all these
+ * only positions p < sinks or p > P_i - w.  q, k_new are already rotated to
+ * P_i.  The cache is not written (spec_pages_commit does that for the
+ * accepted path).
+ *   q      fp16 [n_seq][nt][n_q_heads][head_dim], q_stride elements from one
+ *          node's row to the next (0: contiguous)
+ *   k_new, v_new  fp16 [n_seq][nt][n_kv_heads][head_dim], kv_stride elements
+ *          from one node's row to the next (0: contiguous); strides are
+ *          multiples of 8, so the rows may be parts of a fused QKV buffer
+ *   out    fp16 [n_seq][nt][n_q_heads * head_dim]; rows of nodes >= n_nodes
+ *          are left as they were; rows of a sequence whose status is not 0
+ *          are NaN (for its first n_nodes rows, all nt if that is bad too)
+ *   workspace  spec_tree_attn_workspace bytes, 16-byte aligned; its contents
+ *          do not matter before and after the call
+ *   status int32 [n_seq]: SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_TREE
+ * The scores' statistics and sums are fp32.  The same call gives the same
+ * bits; which bits may depend on the other sequences of the call (the work
+ * is cut evenly over the SMs), unlike spec_verify_attn, whose rows do not
+ * depend on the batch. */
+int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,
+                   int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new,
+                   int64_t kv_stride, uint16_t* out, void* workspace, size_t workspace_bytes,
+                   int32_t* status, void* stream);
+
+/* Bytes of workspace for spec_tree_attn on the current device (any slots,
+ * lengths and trees of up to n_seq sequences of up to nt nodes). */
+int spec_tree_attn_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads,
+                             size_t* bytes);
+
+/* Greedy acceptance along the trees: from node 0 (the anchor, parent -1), the
+ * target's argmax at the current node selects the child that carries that
+ * token (the lowest numbered of several), until none does.
+ *   argmax, tokens, parents  int32 [n_seq][nt] (tokens[s][0], the anchor, is
+ *          not looked at); n_nodes int32 [n_seq] or NULL; nt <= SPEC_MAX_TREE
+ *   path   int32 [n_seq][nt]: node 0, then the accepted nodes, -1 behind
+ *   n_path int32 [n_seq]: nodes in the path (1 + accepted drafts); 0 for a
+ *          sequence without nodes, -1 for a tree that is not one (a parent
+ *          not below its node, a count outside [0, nt], parent of node 0
+ *          not -1): path and emitted are -1 then
+ *   emitted int32 [n_seq][nt]: the accepted tokens, then the target's token
+ *          at the last accepted node (n_path in all), -1 behind */
+int spec_accept_tree(const int32_t* argmax, const int32_t* tokens, const int32_t* parents,
+                     const int32_t* n_nodes, int n_seq, int nt, int32_t* path, int32_t* n_path,
+                     int32_t* emitted, void* stream);
+
+/* The value of a filtered-out logit: finite, with weight 0 at any temperature. */
+#define SPEC_FILTERED (-3.402823466e+38f)
+
+/* Samples one token per row from given random words, after temperature,
+ * top-k, top-p and min-p, on the rejection sampler's integer weights
+ * (spec_accept_stochastic): z = l / T, W_v = floor(exp(z_v - max z) * 2^32).
+ * Tokens are ordered by logit, the largest first, equal logits by id.
+ *   1. a logit of -infinity is never kept;
+ *   2. top_k > 0: the first top_k tokens stay (T == 0: the first one);
+ *   3. top_p < 1: of these, token j stays iff the weights before it sum to
+ *      less than floor(top_p * 2^32) / 2^32 of their total, or it is the
+ *      first;
+ *   4. of these, tokens with W < floor(min_p * 2^32) go;
+ *   5. the token drawn is the first kept id, in the order of ids, at which
+ *      the running sum of the kept weights exceeds floor(u * total / 2^32).
+ * All of it is integer arithmetic: results are bit-identical to any correct
+ * implementation of these rules.
+ *   logits  fp32 [R][V], ld elements from row to row (0: V)
+ *   u       32-bit random words [R]
+ *   temperature, top_k, top_p, min_p  per row, fp32 / int32 [R]; each may be
+ *           NULL (1, 0 = off, 1 = off, 0 = off).  T >= 0 finite, top_k >= 0,
+ *           0 <= top_p <= 1, 0 <= min_p <= 1
+ *   token   int32 [R]
+ *   n_kept  int32 [R] or NULL: the tokens that stayed
+ *   filtered  fp32 [R][V] or NULL, ld_filtered elements from row to row (0:
+ *           V): the logits that stayed, SPEC_FILTERED elsewhere; may be
+ *           `logits` itself (with the same ld).  Given to
+ *           spec_accept_stochastic as p_logits / q_logits, filtered rows
+ *           make its rejection sampling lossless for the filtered
+ *           distributions
+ * A row with a NaN or +infinity, without any finite logit, or with a setting
+ * out of range gets token -1, n_kept 0 and a filtered row of NaN (which
+ * spec_accept_stochastic refuses). */
+int spec_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u,
+                const float* temperature, const int32_t* top_k, const float* top_p,
+                const float* min_p, int32_t* token, int32_t* n_kept, float* filtered,
+                int64_t ld_filtered, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

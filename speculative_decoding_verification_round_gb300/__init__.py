@@ -27,6 +27,9 @@ SPEC_E_UNSUPPORTED = -5
 SPEC_E_TIMEOUT = -6
 SPEC_Q4, SPEC_Q6, SPEC_Q8 = 4, 6, 8
 SPEC_MAX_NT = 16
+SPEC_MAX_TREE = 64
+SPEC_FILTERED = -3.4028234663852886e38
+SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_SHARED, SPEC_ST_FULL, SPEC_ST_TREE = 1, 2, 4, 8, 16
 SPEC_PROF_QKV, SPEC_PROF_O, SPEC_PROF_GATE_UP, SPEC_PROF_DOWN = 0, 1, 2, 3
 SPEC_PROF_LM_HEAD, SPEC_PROF_ALL_GEMMS, SPEC_PROF_ATTN = 4, 5, 6
 
@@ -40,11 +43,15 @@ EXPORTED = ["spec_last_error", "spec_qmat_create", "spec_qmat_destroy", "spec_li
             "spec_accept_stochastic", "spec_accept_stochastic_noalloc", "spec_verify_round",
             "spec_verify_round_host", "spec_depth_params_default", "spec_depth_ctl_create",
             "spec_depth_ctl_destroy", "spec_depth_ctl_next", "spec_depth_ctl_observe",
-            "spec_depth_ctl_estimates"]
+            "spec_depth_ctl_estimates", "spec_model_pages", "spec_pages_copy", "spec_pages_fork",
+            "spec_pages_extend", "spec_pages_commit", "spec_pages_free", "spec_tree_attn",
+            "spec_tree_attn_workspace", "spec_accept_tree", "spec_sample"]
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 U64 = ctypes.c_uint64
+I64 = ctypes.c_int64
+SZ = ctypes.c_size_t
 
 
 class SpecError(RuntimeError):
@@ -74,6 +81,17 @@ class spec_depth_params(ctypes.Structure):
     _fields_ = [("d_min", I32), ("d_max", I32), ("prior_accept", ctypes.c_double),
                 ("prior_reject", ctypes.c_double), ("decay", ctypes.c_double),
                 ("hysteresis", ctypes.c_double), ("cost_window", I32)]
+
+
+class spec_pages(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P), ("layer_stride", I64), ("n_layers", I32), ("n_pages", I32),
+                ("n_kv_heads", I32), ("page_size", I32), ("head_dim", I32), ("n_slots", I32),
+                ("max_pages", I32), ("table", P), ("refs", P), ("len", P)]
+
+
+class spec_tree(ctypes.Structure):
+    _fields_ = [("n_seq", I32), ("nt", I32), ("n_q_heads", I32), ("window", I32), ("sinks", I32),
+                ("scale", ctypes.c_float), ("slots", P), ("parents", P), ("n_nodes", P)]
 
 
 class spec_sampling(ctypes.Structure):
@@ -137,6 +155,16 @@ def lib():
                 "spec_depth_ctl_observe": (I32, [P, I32, I32, P, ctypes.c_double,
                                                  ctypes.POINTER(I32)]),
                 "spec_depth_ctl_estimates": (I32, [P, P, P]),
+                "spec_model_pages": (I32, [P, ctypes.POINTER(spec_pages)]),
+                "spec_pages_copy": (I32, [P, I32, P, P, P, P, P]),
+                "spec_pages_fork": (I32, [P, I32, P, P, P, P]),
+                "spec_pages_extend": (I32, [P, I32, P, P, P, P, P]),
+                "spec_pages_commit": (I32, [P, I32, P, I32, P, P, I64, P, P, P, P, P]),
+                "spec_pages_free": (I32, [P, I32, P, P, P]),
+                "spec_tree_attn": (I32, [P, I32, P, P, I64, P, P, I64, P, P, SZ, P, P]),
+                "spec_tree_attn_workspace": (I32, [P, I32, I32, I32, P]),
+                "spec_accept_tree": (I32, [P, P, P, P, I32, I32, P, P, P, P]),
+                "spec_sample": (I32, [P, I32, I32, I64, P, P, P, P, P, P, P, P, I64, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -472,3 +500,122 @@ class DepthController:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------------------
+# drafted trees
+# ---------------------------------------------------------------------------
+class KVPages:
+    """A paged KV cache (spec_pages) over the caller's tensors, which it keeps
+    alive: k, v fp16 [n_layers][n_pages][n_kv_heads][page_size][head_dim]
+    (a layer's pages contiguous), table int32 [n_slots][max_pages], lens
+    int32 [n_slots], refs int32 [n_pages] (None: pages fixed to their slots).
+    Without a table only spec_pages_copy takes it."""
+
+    def __init__(self, k, v, table=None, lens=None, refs=None):
+        n_layers, n_pages, n_kv_heads, page_size, head_dim = k.shape
+        for t, name in ((k, "k"), (v, "v")):
+            if tuple(t.shape) != tuple(k.shape) or t.element_size() != 2 or not t[0].is_contiguous():
+                raise ValueError(f"{name}: a 16-bit tensor [n_layers][n_pages][n_kv_heads][page_size]"
+                                 "[head_dim] with contiguous layers is required")
+        if k.stride(0) != v.stride(0):
+            raise ValueError("k and v must have the same layer stride")
+        n_slots, max_pages = (0, 0) if table is None else table.shape
+        for t, n, name in ((table, n_slots * max_pages, "table"), (lens, n_slots, "lens"),
+                           (refs, n_pages, "refs")):
+            if t is not None and (t.element_size() != 4 or t.is_floating_point()
+                                  or not t.is_contiguous() or t.numel() != n):
+                raise ValueError(f"{name}: a contiguous int32 tensor of {n} values is required")
+        self._keep = (k, v, table, lens, refs)
+        self.pages = spec_pages(k.data_ptr(), v.data_ptr(), k.stride(0), n_layers, n_pages,
+                                n_kv_heads, page_size, head_dim, n_slots, max_pages,
+                                None if table is None else table.data_ptr(),
+                                None if refs is None else refs.data_ptr(),
+                                None if lens is None else lens.data_ptr())
+        self.ref = ctypes.byref(self.pages)
+
+    @classmethod
+    def of_model(cls, m: Model) -> "KVPages":
+        """The model's own slot cache (spec_model_pages): page id = slot."""
+        self = cls.__new__(cls)
+        self._keep = (m,)
+        self.pages = spec_pages()
+        self.ref = ctypes.byref(self.pages)
+        _check(lib().spec_model_pages(m.handle, self.ref))
+        return self
+
+
+def spec_model_pages(m: Model) -> KVPages:
+    return KVPages.of_model(m)
+
+
+def spec_pages_copy(kv: KVPages, n: int, src, dst, status, n_pos=None, stream=None):
+    """Page src[i] to page dst[i], all layers; n_pos: only its first positions."""
+    _check(lib().spec_pages_copy(kv.ref, int(n), _ptr(src), _ptr(dst), _ptr(n_pos), _ptr(status),
+                                 _stream(stream)))
+
+
+def spec_pages_fork(kv: KVPages, n: int, src, dst, status, stream=None):
+    """Slot dst[i] becomes a branch of slot src[i], sharing its pages."""
+    _check(lib().spec_pages_fork(kv.ref, int(n), _ptr(src), _ptr(dst), _ptr(status), _stream(stream)))
+
+
+def spec_pages_extend(kv: KVPages, n: int, slots, n_new, copies, status, stream=None):
+    """Room for n_new[i] more positions of slot slots[i] (copy on write)."""
+    _check(lib().spec_pages_extend(kv.ref, int(n), _ptr(slots), _ptr(n_new), _ptr(copies),
+                                   _ptr(status), _stream(stream)))
+
+
+def spec_pages_commit(kv: KVPages, n: int, slots, nt: int, k_new, v_new, path, n_path, status,
+                      new_len=None, new_layer_stride: int = 0, stream=None):
+    """Rows path[i][:n_path[i]] of k_new / v_new [n_layers][n][nt][n_kv_heads]
+    [head_dim] behind the committed positions of slot slots[i], all layers."""
+    _check(lib().spec_pages_commit(kv.ref, int(n), _ptr(slots), int(nt), _ptr(k_new), _ptr(v_new),
+                                   int(new_layer_stride), _ptr(path), _ptr(n_path), _ptr(new_len),
+                                   _ptr(status), _stream(stream)))
+
+
+def spec_pages_free(kv: KVPages, n: int, slots, status, stream=None):
+    """Gives back every page of the slots."""
+    _check(lib().spec_pages_free(kv.ref, int(n), _ptr(slots), _ptr(status), _stream(stream)))
+
+
+def spec_tree_attn_workspace(kv: KVPages, n_seq: int, nt: int, n_q_heads: int) -> int:
+    """Bytes of workspace that spec_tree_attn needs for trees of this size."""
+    b = SZ()
+    _check(lib().spec_tree_attn_workspace(kv.ref, int(n_seq), int(nt), int(n_q_heads),
+                                          ctypes.byref(b)))
+    return b.value
+
+
+def spec_tree_attn(kv: KVPages, layer: int, n_seq: int, slots, nt: int, n_q_heads: int, q, k_new,
+                   v_new, out, workspace, status, parents=None, n_nodes=None, window: int = 0,
+                   sinks: int = 0, scale: float = 0.0, q_stride: int = 0, kv_stride: int = 0,
+                   stream=None):
+    """Attention of n_seq trees of up to nt nodes over the pages of `layer`
+    and over their own nodes (rules in include/spec_verify.h)."""
+    t = spec_tree(n_seq, nt, n_q_heads, window, sinks, scale, slots.data_ptr(),
+                  None if parents is None else parents.data_ptr(),
+                  None if n_nodes is None else n_nodes.data_ptr())
+    _check(lib().spec_tree_attn(kv.ref, int(layer), ctypes.byref(t), _ptr(q), int(q_stride),
+                                _ptr(k_new), _ptr(v_new), int(kv_stride), _ptr(out),
+                                _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                _ptr(status), _stream(stream)))
+
+
+def spec_accept_tree(argmax, tokens, parents, n_nodes, n_seq: int, nt: int, path, n_path, emitted,
+                     stream=None):
+    """Greedy acceptance along the trees; n_nodes None: nt each."""
+    _check(lib().spec_accept_tree(_ptr(argmax), _ptr(tokens), _ptr(parents), _ptr(n_nodes),
+                                  int(n_seq), int(nt), _ptr(path), _ptr(n_path), _ptr(emitted),
+                                  _stream(stream)))
+
+
+def spec_sample(logits, R: int, V: int, u, token, temperature=None, top_k=None, top_p=None,
+                min_p=None, n_kept=None, filtered=None, ld: int = 0, ld_filtered: int = 0,
+                stream=None):
+    """One token per row from the random words u after temperature, top-k,
+    top-p and min-p; filtered: the logits that stayed (SPEC_FILTERED elsewhere)."""
+    _check(lib().spec_sample(_ptr(logits), int(R), int(V), int(ld), _ptr(u), _ptr(temperature),
+                             _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(n_kept),
+                             _ptr(filtered), int(ld_filtered), _stream(stream)))

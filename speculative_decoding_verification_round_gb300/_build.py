@@ -15,10 +15,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libspecverify.so")
-SOURCES = ["api.cu", "linear.cu", "tcgemm.cu", "attn.cu", "ops.cu", "accept.cu", "depth.cu"]
+SOURCES = ["api.cu", "linear.cu", "tcgemm.cu", "attn.cu", "ops.cu", "accept.cu", "depth.cu",
+           "pages.cu", "tree_attn.cu", "sample.cu"]
 # host code whose doubles must be rounded operation by operation
 FILE_FLAGS = {"depth.cu": ["-Xcompiler", "-ffp-contract=off"]}
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "tc_ops.cuh"),
+           os.path.join(CSRC, "sampler.cuh"),
            os.path.join(os.path.dirname(HERE), "include", "spec_verify.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")

@@ -47,6 +47,8 @@ void attn_init_attrs();
 void accept_init_attrs();
 void linear_init_attrs();
 void tc_init_attrs();
+void tree_init_attrs();
+void sample_init_attrs();
 static std::mutex g_attr_mu;
 static std::vector<int> g_attr_done;
 static void init_attrs_once() {
@@ -58,6 +60,8 @@ static void init_attrs_once() {
   accept_init_attrs();
   linear_init_attrs();
   tc_init_attrs();
+  tree_init_attrs();
+  sample_init_attrs();
   g_attr_done.push_back(dev);
 }
 
@@ -280,6 +284,7 @@ struct spec_model {
   int32_t* n_past = nullptr;
   uint64_t* emit_idx = nullptr;
   int32_t* anchor = nullptr;
+  int32_t* page_table = nullptr;  // [max_seqs]: slot s's one page is page s (spec_model_pages)
   uint32_t* err = nullptr;
   int Rmax = 0;
   float* h = nullptr;
@@ -459,6 +464,14 @@ extern "C" int spec_model_create(const spec_model_desc* desc, const spec_model_w
   TRY(dalloc_t(m, &m->n_past, D.max_seqs));
   TRY(dalloc_t(m, &m->emit_idx, D.max_seqs));
   TRY(dalloc_t(m, &m->anchor, D.max_seqs));
+  TRY(dalloc_t(m, &m->page_table, D.max_seqs));
+  {
+    std::vector<int32_t> ids(D.max_seqs);
+    for (int i = 0; i < D.max_seqs; i++) ids[i] = i;
+    if (cudaMemcpy(m->page_table, ids.data(), sizeof(int32_t) * ids.size(), cudaMemcpyHostToDevice) !=
+        cudaSuccess)
+      TRY(fail(SPEC_E_CUDA, "copy page table"));
+  }
   TRY(dalloc_t(m, &m->err, 1));
   cudaMemsetAsync(m->n_past, 0, sizeof(int32_t) * D.max_seqs, st);
   cudaMemsetAsync(m->emit_idx, 0, sizeof(uint64_t) * D.max_seqs, st);
@@ -1133,4 +1146,85 @@ extern "C" int spec_accept_stochastic(const float* p_logits, const float* q_logi
   stoch_finalize(n_seq, d, n_acc, emitted, emit_idx, w->err, st);
   CUDA_TRY(cudaGetLastError());
   return SPEC_OK;
+}
+
+// ---------------------------------------------------------------------------
+// drafted trees: the model's cache as pages, tree attention, filtered sampling
+// ---------------------------------------------------------------------------
+extern "C" int spec_model_pages(spec_model* m, spec_pages* out) {
+  if (m == nullptr || out == nullptr) return fail(SPEC_E_INVALID, "null argument");
+  if (m->d.n_layers == 0) return fail(SPEC_E_UNSUPPORTED, "a model without layers has no cache");
+  out->k = reinterpret_cast<uint16_t*>(m->kc);
+  out->v = reinterpret_cast<uint16_t*>(m->vc);
+  out->layer_stride = (int64_t)m->layer_elems;
+  out->n_layers = m->d.n_layers;
+  out->n_pages = out->n_slots = m->d.max_seqs;
+  out->n_kv_heads = m->d.n_kv_heads;
+  out->page_size = m->d.max_ctx;
+  out->head_dim = m->d.head_dim;
+  out->max_pages = 1;
+  out->table = m->page_table;
+  out->refs = nullptr;
+  out->len = m->n_past;
+  return SPEC_OK;
+}
+
+extern "C" int spec_tree_attn_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads,
+                                        size_t* bytes) {
+  if (bytes == nullptr) return fail(SPEC_E_INVALID, "null argument");
+  return tree_workspace(kv, n_seq, nt, n_q_heads, bytes);
+}
+
+extern "C" int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,
+                              int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new,
+                              int64_t kv_stride, uint16_t* out, void* workspace,
+                              size_t workspace_bytes, int32_t* status, void* stream) {
+  if (kv == nullptr || t == nullptr || t->slots == nullptr || q == nullptr || k_new == nullptr ||
+      v_new == nullptr || out == nullptr || workspace == nullptr || status == nullptr)
+    return fail(SPEC_E_INVALID, "null argument");
+  size_t need = 0;
+  const int rc = tree_workspace(kv, t->n_seq, t->nt, t->n_q_heads, &need);
+  if (rc != SPEC_OK) return rc;
+  if (layer < 0 || layer >= kv->n_layers) return fail(SPEC_E_SHAPE, "layer out of range");
+  if (t->window < 0 || t->sinks < 0) return fail(SPEC_E_INVALID, "window and sinks must be >= 0");
+  if (!std::isfinite(t->scale)) return fail(SPEC_E_INVALID, "scale must be finite");
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) ||
+      !aligned16(workspace))
+    return fail(SPEC_E_SHAPE, "q, k_new, v_new, out and workspace must be 16-byte aligned");
+  if (q_stride % 8 != 0 || kv_stride % 8 != 0 || q_stride < 0 || kv_stride < 0 ||
+      (q_stride != 0 && q_stride < (int64_t)t->n_q_heads * kv->head_dim) ||
+      (kv_stride != 0 && kv_stride < (int64_t)kv->n_kv_heads * kv->head_dim))
+    return fail(SPEC_E_SHAPE, "row strides must be multiples of 8 that hold a row's heads");
+  if ((double)std::max(q_stride, kv_stride) * t->n_seq * t->nt > 4.0e15)
+    return fail(SPEC_E_SHAPE, "row strides are too large");
+  if (workspace_bytes < need)
+    return fail(SPEC_E_SHAPE, "workspace of " + std::to_string(need) + " bytes required");
+  init_attrs_once();
+  return launch_tree(kv, layer, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status,
+                     as_stream(stream));
+}
+
+extern "C" int spec_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u,
+                           const float* temperature, const int32_t* top_k, const float* top_p,
+                           const float* min_p, int32_t* token, int32_t* n_kept, float* filtered,
+                           int64_t ld_filtered, void* stream) {
+  if (logits == nullptr || u == nullptr || token == nullptr)
+    return fail(SPEC_E_INVALID, "null argument");
+  if (R < 1 || V < 1 || R > (1 << 27) || V > (1 << 30))
+    return fail(SPEC_E_SHAPE, "R in [1, 2^27] and V in [1, 2^30] required");
+  if (ld == 0) ld = V;
+  if (ld_filtered == 0) ld_filtered = V;
+  if (ld < V || ld_filtered < V || ld > (1ll << 40) || ld_filtered > (1ll << 40))
+    return fail(SPEC_E_SHAPE, "row strides below V");
+  if (((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(filtered)) & 3u) != 0)
+    return fail(SPEC_E_SHAPE, "logits and filtered must be 4-byte aligned");
+  if (filtered != nullptr && !(filtered == logits && ld_filtered == ld)) {
+    const size_t in = sizeof(float) * ((size_t)(R - 1) * ld + V),
+                 outb = sizeof(float) * ((size_t)(R - 1) * ld_filtered + V);
+    if (overlaps(filtered, outb, logits, in))
+      return fail(SPEC_E_INVALID, "filtered overlaps logits without being logits");
+  }
+  init_attrs_once();
+  return launch_sample(logits, R, V, ld, u, temperature, top_k, top_p, min_p, token, n_kept, filtered,
+                       ld_filtered, as_stream(stream));
 }

@@ -254,6 +254,20 @@ cudaError_t accept_commit_node_retarget(cudaGraphExec_t ex, cudaGraphNode_t node
                                         const int32_t* draft, const int32_t* seq_ids,
                                         int32_t* n_acc, int32_t* emitted);
 
+// Argument checks of the page operators (pages.cu); book: the table and
+// lengths are used too.
+int check_pages(const spec_pages* kv, bool book);
+
+// Tree attention (tree_attn.cu) and filtered sampling (sample.cu).
+int tree_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads, size_t* bytes);
+int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,
+                int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride,
+                uint16_t* out, void* workspace, int32_t* status, cudaStream_t st);
+int launch_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u,
+                  const float* temperature, const int32_t* top_k, const float* top_p,
+                  const float* min_p, int32_t* token, int32_t* n_kept, float* filtered, int64_t ldf,
+                  cudaStream_t st);
+
 // Whether kernels that can overlap their predecessor's tail are launched as
 // programmatic dependents (default on; SPEC_VERIFY_PDL=0 in the environment
 // turns it off).

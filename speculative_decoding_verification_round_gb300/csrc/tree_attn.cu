@@ -1,0 +1,778 @@
+// tree_attn.cu -- attention of drafted trees over a paged cache, with an
+// optional sliding window and sink positions (spec_tree_attn).
+//
+// Every query row of one (sequence, kv head) -- nodes x GQA group -- reads the
+// same keys, so the rows are the M of an MMA tile and the cache is streamed
+// once per 64 rows: S = Q K^T, a softmax with a running maximum and sum in
+// fp32 (log2 domain), O = P V, over tiles of 64 positions.  The tree's own
+// nodes are the last tile, masked by each node's set of ancestors.
+//
+// Work is cut evenly whatever the lengths are: the (sequence, kv head, row
+// block) units, each of its own number of tiles, are laid end to end, and CTA
+// b of N takes tiles [b T / N, (b + 1) T / N).  The lengths are only known on
+// the device, so every CTA derives the cut from them.  A unit that one CTA
+// holds whole is written by it; the pieces of a cut unit (at most two a CTA)
+// go to the workspace as (max, sum, unnormalised O) and a second kernel, which
+// also checks the sequences and writes their status, joins them in the order
+// of the positions.
+#include <math.h>
+
+#include "common.cuh"
+
+namespace {
+
+constexpr int TT_KEYS = 64;  // positions per tile
+constexpr int TT_THREADS = 128;
+constexpr int TT_STAGES = 3;
+
+struct TreeArgs {
+  const __half* k;  // the layer's cache
+  const __half* v;
+  const int32_t* table;
+  const int32_t* len;
+  int n_slots, max_pages, n_pages, nkv, page_size, page_shift;  // shift -1: not a power of two
+  const int32_t* slots;
+  const int32_t* parents;
+  const int32_t* n_nodes;
+  int n_seq, nt, nq, G, window, sinks;
+  float scale_log2;
+  const __half* q;
+  int64_t q_stride;
+  const __half* k_new;
+  const __half* v_new;
+  int64_t kv_stride;
+  __half* out;
+  float* part_o;    // [N][2][rows][HD]
+  float2* part_ml;  // [N][2][rows]
+  int32_t* status;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+// 16 bytes to shared memory; zeros if !valid (src is then any readable address).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0));
+}
+// Byte offset of 16-byte unit u of row r in a swizzled tile.
+template <int HD>
+__device__ __forceinline__ uint32_t tile_off(int r, int u) {
+  return (uint32_t)(r * (HD * 2) + ((u ^ (r & 7)) << 4));
+}
+
+// ---------------------------------------------------------------------------
+// the cut of the work
+// ---------------------------------------------------------------------------
+// One sequence: its tiles are the sink tiles below the window, the tiles from
+// the window's first position to the last, and the tree's own.
+struct SeqInfo {
+  int slot, len, m;
+  int lo;       // first position that some node's window reaches
+  int sinks;    // positions of the prefix that stay visible under a window
+  int w_tile;   // tile of lo
+  int n_sink;   // sink tiles in front of it
+  int tiles;
+  int units;    // kv heads x row blocks
+  int bad;      // status bits of what is checked here
+  __device__ __forceinline__ long long work() const { return (long long)units * tiles; }
+};
+
+template <int ROWS>
+__device__ __forceinline__ SeqInfo seq_info(const TreeArgs& a, int s) {
+  SeqInfo q;
+  q.slot = a.slots[s];
+  q.m = a.n_nodes != nullptr ? a.n_nodes[s] : a.nt;
+  q.bad = 0;
+  q.len = 0;
+  if (q.slot < 0 || q.slot >= a.n_slots) {
+    q.bad |= SPEC_ST_SLOT;
+  } else {
+    q.len = a.len[q.slot];
+    if (q.len < 0 || q.len > a.max_pages * a.page_size) q.bad |= SPEC_ST_PAGE;
+  }
+  if (q.m < 0 || q.m > a.nt) q.bad |= SPEC_ST_TREE;
+  if (q.bad != 0) q.len = q.m = 0;
+  q.lo = a.window > 0 ? max(0, q.len - a.window + 1) : 0;
+  q.sinks = a.window > 0 ? min(a.sinks, q.len) : 0;
+  const int end = (q.len + TT_KEYS - 1) / TT_KEYS;
+  q.w_tile = q.lo < q.len ? q.lo / TT_KEYS : end;
+  q.n_sink = min((q.sinks + TT_KEYS - 1) / TT_KEYS, q.w_tile);
+  q.tiles = q.n_sink + (end - q.w_tile) + 1;
+  q.units = q.m > 0 ? a.nkv * ((q.m * a.G + ROWS - 1) / ROWS) : 0;
+  return q;
+}
+
+// Exclusive sum over the CTA's threads; *total: the whole.
+template <int THREADS>
+__device__ __forceinline__ long long block_excl(long long v, long long* s_part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_part[warp] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; w++) {
+    if (w < warp) before += s_part[w];
+    all += s_part[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+__device__ __forceinline__ long long cut(long long total, int b, int n) {
+  // total * b / n without overflow: total below 2^53 or so, b and n small
+  return total / n * b + total % n * b / n;
+}
+
+// ---------------------------------------------------------------------------
+// the tree of one sequence: every node's ancestors (with itself) and depth
+// ---------------------------------------------------------------------------
+struct TreeSmem {
+  unsigned long long anc[SPEC_MAX_TREE];
+  int depth[SPEC_MAX_TREE];
+  int par[SPEC_MAX_TREE];
+};
+
+// Every thread of the CTA; returns whether the parents make a tree.
+__device__ __forceinline__ bool load_tree(const TreeArgs& a, int s, int m, TreeSmem& t) {
+  const int i = threadIdx.x;
+  bool bad = false;
+  __syncthreads();  // the last sequence's tree is no longer read
+  if (i < SPEC_MAX_TREE) {
+    int p = -1;
+    if (i < m) {
+      p = a.parents != nullptr ? a.parents[(int64_t)s * a.nt + i] : i - 1;
+      bad = p < -1 || p >= i;
+    }
+    t.par[i] = bad ? -1 : p;
+  }
+  const bool any = __syncthreads_or(bad);
+  if (i < m) {
+    unsigned long long set = 1ull << i;
+    int d = 0;
+    for (int p = t.par[i]; p >= 0; p = t.par[p]) {
+      set |= 1ull << p;
+      d++;
+    }
+    t.anc[i] = set;
+    t.depth[i] = d;
+  }
+  __syncthreads();
+  return !any;
+}
+
+// ---------------------------------------------------------------------------
+// the main kernel.  Four warps = RTW row blocks x KG key groups; a warp holds
+// MT m16 tiles of rows against 64 / KG keys of every tile, with its own
+// running (max, sum, O), joined over the key groups at the end of a piece.
+// ---------------------------------------------------------------------------
+template <int HD, int MT, int RTW>
+struct Shape {
+  static constexpr int ROWS = 16 * MT * RTW;
+  static constexpr int KG = 4 / RTW;
+  static constexpr int KEYS = TT_KEYS / KG;
+  static constexpr int TILE = TT_KEYS * HD * 2;  // bytes of a K (or V) tile
+  static constexpr int XROW = HD + 8;            // floats of an exchange row (padded)
+  static constexpr size_t Q_OFF = (size_t)TT_STAGES * 2 * TILE;
+  static constexpr size_t SMEM = Q_OFF + (size_t)ROWS * HD * 2;
+  static_assert((size_t)KG * ROWS * XROW * 4 <= Q_OFF, "the exchange fits over the tiles");
+};
+
+template <int HD, int MT, int RTW>
+__global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs a) {
+  using Sh = Shape<HD, MT, RTW>;
+  constexpr int ROWS = Sh::ROWS, KG = Sh::KG, KEYS = Sh::KEYS, NB = KEYS / 8, UNITS = HD / 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ TreeSmem s_tree;
+  __shared__ long long s_part[TT_THREADS / 32];
+  __shared__ long long s_off;
+  __shared__ int s_seq;
+  __shared__ float2 s_ml[4][16 * MT];
+  grid_dep_launch();  // the joining kernel may get ready
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int kg = warp % KG, rw = warp / KG;  // this warp's key group and row block
+
+  // ---- this CTA's share of the tiles
+  long long total = 0, first = 0, w0, w1;
+  {
+    long long mine = 0, excl = 0, chunk = 0;
+    for (int base = 0; base < a.n_seq; base += TT_THREADS) {
+      mine = base + tid < a.n_seq ? seq_info<ROWS>(a, base + tid).work() : 0;
+      excl = block_excl<TT_THREADS>(mine, s_part, &chunk);
+      total += chunk;
+    }
+    w0 = cut(total, blockIdx.x, gridDim.x);
+    w1 = cut(total, blockIdx.x + 1, gridDim.x);
+    if (w0 >= w1) return;
+    for (int base = 0; base < a.n_seq; base += TT_THREADS) {
+      if (a.n_seq > TT_THREADS) {
+        mine = base + tid < a.n_seq ? seq_info<ROWS>(a, base + tid).work() : 0;
+        excl = block_excl<TT_THREADS>(mine, s_part, &chunk);
+      }
+      if (first + excl <= w0 && w0 < first + excl + mine) {
+        s_seq = base + tid;
+        s_off = w0 - first - excl;
+      }
+      first += chunk;
+    }
+    __syncthreads();
+  }
+  int s = s_seq;
+  long long off = s_off;
+  SeqInfo q = seq_info<ROWS>(a, s);
+  load_tree(a, s, q.m, s_tree);
+
+  const uint32_t sm0 = smem_u32(smem), qs0 = sm0 + (uint32_t)Sh::Q_OFF;
+  const int lu = tid % UNITS, lr = tid / UNITS;  // this thread's unit and first row of a tile
+  constexpr int LR = TT_THREADS / UNITS;         // rows of a pass
+  for (long long w = w0; w < w1;) {
+    if (off >= q.work()) {  // the next sequence with work
+      s++;
+      off = 0;
+      q = seq_info<ROWS>(a, s);
+      if (q.work() > 0) load_tree(a, s, q.m, s_tree);
+      continue;
+    }
+    const int unit = (int)(off / q.tiles), t0 = (int)(off % q.tiles);
+    const int t1 = (int)min((long long)q.tiles, t0 + (w1 - w));
+    const int kvh = unit % a.nkv, row0 = unit / a.nkv * ROWS, M = q.m * a.G;
+
+    // positions of tile t (context tiles only)
+    const int n_sink = q.n_sink, w_tile = q.w_tile, last = q.tiles - 1;
+    auto tile_base = [&](int t) { return (t < n_sink ? t : w_tile + t - n_sink) * TT_KEYS; };
+    auto load_tile = [&](int t) {
+      const uint32_t ks = sm0 + (uint32_t)(t % TT_STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
+      if (t == last) {  // the tree's nodes
+#pragma unroll
+        for (int i = 0; i < TT_KEYS / LR; i++) {
+          const int r = lr + i * LR;
+          const bool ok = r < q.m;
+          const int64_t at = ((int64_t)s * a.nt + (ok ? r : 0)) * a.kv_stride + kvh * HD + lu * 8;
+          cp16(ks + tile_off<HD>(r, lu), a.k_new + at, ok);
+          cp16(vs + tile_off<HD>(r, lu), a.v_new + at, ok);
+        }
+      } else {
+        const int base = tile_base(t);
+        const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
+        int pages[TT_KEYS / LR], ats[TT_KEYS / LR];
+#pragma unroll
+        for (int i = 0; i < TT_KEYS / LR; i++) {
+          const int pos = min(base + lr + i * LR, q.len - 1);
+          const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+          ats[i] = pos - e * a.page_size;
+          pages[i] = __ldg(row + e);
+        }
+#pragma unroll
+        for (int i = 0; i < TT_KEYS / LR; i++) {
+          const int r = lr + i * LR;
+          const bool ok = base + r < q.len && pages[i] >= 0 && pages[i] < a.n_pages;
+          const int64_t at =
+              (((int64_t)(ok ? pages[i] : 0) * a.nkv + kvh) * a.page_size + (ok ? ats[i] : 0)) * HD + lu * 8;
+          cp16(ks + tile_off<HD>(r, lu), a.k + at, ok);
+          cp16(vs + tile_off<HD>(r, lu), a.v + at, ok);
+        }
+      }
+    };
+
+    // ---- the piece's first tiles, and its q rows
+    __syncthreads();  // the last piece's exchange and q rows have been read
+#pragma unroll
+    for (int i = 0; i < TT_STAGES - 1; i++) {
+      if (t0 + i < t1) load_tile(t0 + i);
+      if (i == 0) {
+        for (int e = tid; e < ROWS * UNITS; e += TT_THREADS) {
+          const int r = e / UNITS, u = e % UNITS, m = row0 + r;
+          const bool ok = m < M;
+          const int node = ok ? m / a.G : 0, h = kvh * a.G + (ok ? m % a.G : 0);
+          cp16(qs0 + tile_off<HD>(r, u), a.q + ((int64_t)s * a.nt + node) * a.q_stride + h * HD + u * 8, ok);
+        }
+      }
+      asm volatile("cp.async.commit_group;");
+    }
+    // this thread's rows: [tile][upper half]
+    int pos[MT][2];
+    unsigned long long anc[MT][2];
+    float mx[MT][2], sum[MT][2], o[MT][HD / 8][4];
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int m = row0 + (rw * MT + i) * 16 + h * 8 + g;
+        const int node = m < M ? m / a.G : 0;
+        pos[i][h] = q.len + s_tree.depth[node];
+        anc[i][h] = m < M ? s_tree.anc[node] : 0ull;
+        mx[i][h] = -INFINITY;
+        sum[i][h] = 0.0f;
+      }
+#pragma unroll
+      for (int d = 0; d < HD / 8; d++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[i][d][e] = 0.0f;
+    }
+    const int q_row = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix row of a q fragment
+
+    for (int t = t0; t < t1; t++) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(TT_STAGES - 2) : "memory");
+      __syncthreads();
+      if (t + TT_STAGES - 1 < t1) load_tile(t + TT_STAGES - 1);
+      asm volatile("cp.async.commit_group;");
+      const uint32_t ks = sm0 + (uint32_t)(t % TT_STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
+      const int key0 = kg * KEYS;
+
+      // ---- S = Q K^T
+      float sc[MT][NB][4];
+#pragma unroll
+      for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) sc[i][nb][e] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; kk += 2) {
+        uint32_t qa[MT][2][4];
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+#pragma unroll
+          for (int j = 0; j < 2; j++)
+            ldsm_x4(qs0 + tile_off<HD>((rw * MT + i) * 16 + q_row, 2 * (kk + j) + (lane >> 4)), qa[i][j]);
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+          uint32_t b[4];
+          ldsm_x4(ks + tile_off<HD>(key0 + 8 * nb + (lane & 7), 2 * kk + (lane >> 3)), b);
+#pragma unroll
+          for (int i = 0; i < MT; i++) {
+            mma_16816(sc[i][nb], qa[i][0], b[0], b[1]);
+            mma_16816(sc[i][nb], qa[i][1], b[2], b[3]);
+          }
+        }
+      }
+      // ---- scale and mask
+      const int base = t == last ? 0 : tile_base(t);
+      const bool masked = t == last || base + TT_KEYS > q.len ||
+                          (a.window > 0 && base + TT_KEYS > q.sinks && base < q.lo + SPEC_MAX_TREE);
+#pragma unroll
+      for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            float x = sc[i][nb][e] * a.scale_log2;
+            if (masked) {
+              const int h = e >> 1, key = key0 + 8 * nb + 2 * t4 + (e & 1);
+              bool see;
+              int p;
+              if (t == last) {
+                see = (anc[i][h] >> key) & 1;
+                p = q.len + (see ? s_tree.depth[key] : 0);
+              } else {
+                p = base + key;
+                see = p < q.len;
+              }
+              if (a.window > 0) see = see && (p < a.sinks || p > pos[i][h] - a.window);
+              x = see ? x : -INFINITY;
+            }
+            sc[i][nb][e] = x;
+          }
+      // ---- running maximum and sum
+#pragma unroll
+      for (int i = 0; i < MT; i++) {
+        float nm[2], al[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          float m2 = mx[i][h];
+#pragma unroll
+          for (int nb = 0; nb < NB; nb++) m2 = fmaxf(m2, fmaxf(sc[i][nb][2 * h], sc[i][nb][2 * h + 1]));
+          m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+          m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
+          nm[h] = m2 == -INFINITY ? 0.0f : m2;  // a row without a visible key so far
+          al[h] = exp2f(mx[i][h] - nm[h]);
+          mx[i][h] = m2;
+          float l = 0.0f;
+#pragma unroll
+          for (int nb = 0; nb < NB; nb++) {
+            sc[i][nb][2 * h] = exp2f(sc[i][nb][2 * h] - nm[h]);
+            sc[i][nb][2 * h + 1] = exp2f(sc[i][nb][2 * h + 1] - nm[h]);
+            l += sc[i][nb][2 * h] + sc[i][nb][2 * h + 1];
+          }
+          sum[i][h] = fmaf(sum[i][h], al[h], l);  // this lane's share of the row
+        }
+        if (__any_sync(0xffffffffu, al[0] != 1.0f || al[1] != 1.0f)) {
+#pragma unroll
+          for (int d = 0; d < HD / 8; d++) {
+            o[i][d][0] *= al[0];
+            o[i][d][1] *= al[0];
+            o[i][d][2] *= al[1];
+            o[i][d][3] *= al[1];
+          }
+        }
+      }
+      // ---- a masked tile's V may hold infinities or NaN that some rows do
+      // ---- not see, and 0 * inf is NaN: such rows of V are added by the
+      // ---- lanes that see them and zeroed for the MMA
+      if (masked) {
+        bool odd = false;
+        for (int e = tid; e < TT_KEYS * UNITS; e += TT_THREADS) {
+          uint32_t v[4];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(vs + e * 16));
+#pragma unroll
+          for (int x = 0; x < 4; x++)
+            odd |= (v[x] & 0x7C00u) == 0x7C00u || (v[x] & 0x7C000000u) == 0x7C000000u;
+        }
+        if (__syncthreads_or(odd)) {
+          for (int key = key0; key < key0 + KEYS; key++) {
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+#pragma unroll
+              for (int nb = 0; nb < NB; nb++) {
+                if ((key - key0) / 8 != nb) continue;
+                const int src = (lane & ~3) | ((key & 7) >> 1);
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                  const float pa = __shfl_sync(0xffffffffu, sc[i][nb][2 * h], src);
+                  const float pb = __shfl_sync(0xffffffffu, sc[i][nb][2 * h + 1], src);
+                  const float p = key & 1 ? pb : pa;
+                  if (p > 0.0f) {
+#pragma unroll
+                    for (int d = 0; d < HD / 8; d++) {
+                      uint32_t v;
+                      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(vs + tile_off<HD>(key, d) + t4 * 4));
+                      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&v));
+                      o[i][d][2 * h] = fmaf(p, f.x, o[i][d][2 * h]);
+                      o[i][d][2 * h + 1] = fmaf(p, f.y, o[i][d][2 * h + 1]);
+                    }
+                  }
+                }
+              }
+          }
+          __syncthreads();
+          for (int e = tid; e < TT_KEYS * UNITS; e += TT_THREADS)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vs + e * 16), "r"(0));
+          __syncthreads();
+        }
+      }
+      // ---- O += P V, with P as an exact pair of fp16 numbers hi + lo
+#pragma unroll
+      for (int kk = 0; kk < KEYS / 16; kk++) {
+        uint32_t hi[MT][4], lo[MT][4];
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+#pragma unroll
+          for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const float p0 = sc[i][2 * kk + n][2 * h], p1 = sc[i][2 * kk + n][2 * h + 1];
+              const __half2 hh = __floats2half2_rn(p0, p1);
+              const float2 f = __half22float2(hh);
+              const __half2 ll = __floats2half2_rn(p0 - f.x, p1 - f.y);
+              hi[i][2 * n + h] = *reinterpret_cast<const uint32_t*>(&hh);
+              lo[i][2 * n + h] = *reinterpret_cast<const uint32_t*>(&ll);
+            }
+#pragma unroll
+        for (int d = 0; d < HD / 8; d += 2) {
+          uint32_t b[4];
+          ldsm_x4_t(vs + tile_off<HD>(key0 + 16 * kk + (lane & 7) + ((lane >> 3) & 1) * 8, d + (lane >> 4)), b);
+#pragma unroll
+          for (int i = 0; i < MT; i++) {
+            mma_16816(o[i][d], hi[i], b[0], b[1]);
+            mma_16816(o[i][d], lo[i], b[0], b[1]);
+            mma_16816(o[i][d + 1], hi[i], b[2], b[3]);
+            mma_16816(o[i][d + 1], lo[i], b[2], b[3]);
+          }
+        }
+      }
+    }
+    // ---- the end of the piece: the key groups' results through shared
+    // ---- memory, added in the order of the groups
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the tiles have been read
+    float* x = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float l = sum[i][h];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const int r = i * 16 + h * 8 + g;
+        if (t4 == 0) s_ml[warp][r] = make_float2(mx[i][h], l);
+        float* dst = x + ((size_t)kg * ROWS + rw * MT * 16 + r) * Sh::XROW + 2 * t4;
+#pragma unroll
+        for (int d = 0; d < HD / 8; d++)
+          *reinterpret_cast<float2*>(dst + 8 * d) = make_float2(o[i][d][2 * h], o[i][d][2 * h + 1]);
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == q.tiles;
+    const size_t slot = (size_t)blockIdx.x * 2 + (w > w0 ? 1 : 0);
+    for (int e = tid; e < ROWS * UNITS; e += TT_THREADS) {
+      const int r = e / UNITS, u = e % UNITS, m = row0 + r;
+      if (m >= M) break;
+      const int rb = r / (16 * MT), rl = r % (16 * MT);
+      float m2 = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < KG; k++) m2 = fmaxf(m2, s_ml[rb * KG + k][rl].x);
+      const float ref = m2 == -INFINITY ? 0.0f : m2;
+      float acc[8] = {}, l = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KG; k++) {
+        const float2 ml = s_ml[rb * KG + k][rl];
+        const float wk = exp2f(ml.x - ref);
+        l = fmaf(ml.y, wk, l);
+        const float* src = x + ((size_t)k * ROWS + r) * Sh::XROW + u * 8;
+#pragma unroll
+        for (int d = 0; d < 8; d++) acc[d] = fmaf(src[d], wk, acc[d]);
+      }
+      if (whole) {
+        const float inv = 1.0f / l;
+        __half2 y[4];
+#pragma unroll
+        for (int d = 0; d < 4; d++) y[d] = __floats2half2_rn(acc[2 * d] * inv, acc[2 * d + 1] * inv);
+        const int node = m / a.G, hd = kvh * a.G + m % a.G;
+        *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + hd) * HD + u * 8) =
+            *reinterpret_cast<const uint4*>(y);
+      } else {
+        float* po = a.part_o + (slot * ROWS + r) * HD + u * 8;
+        *reinterpret_cast<float4*>(po) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        *reinterpret_cast<float4*>(po + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (u == 0) a.part_ml[slot * ROWS + r] = make_float2(m2, l);
+      }
+    }
+    w += t1 - t0;
+    off += t1 - t0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the joining kernel: one warp per output row at a time, a CTA's rows all of
+// one sequence.  Checks the sequence (slot, length, pages, tree) while the
+// main kernel runs; then joins the pieces of the rows' units in the order of
+// the positions, or writes NaN for a sequence in error.
+// ---------------------------------------------------------------------------
+constexpr int TJ_THREADS = 128;
+constexpr int TJ_ROWS = 16;  // output rows (node, head) of a CTA
+
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(TJ_THREADS)
+tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
+  __shared__ TreeSmem s_tree;
+  __shared__ long long s_part[TJ_THREADS / 32];
+  const int s = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long total = 0, before = 0;
+  for (int base = 0; base < a.n_seq; base += TJ_THREADS) {
+    const long long mine = base + tid < a.n_seq ? seq_info<ROWS>(a, base + tid).work() : 0;
+    long long chunk;
+    block_excl<TJ_THREADS>(mine, s_part, &chunk);
+    total += chunk;
+    block_excl<TJ_THREADS>(base + tid < s ? mine : 0, s_part, &chunk);
+    before += chunk;
+  }
+  const SeqInfo q = seq_info<ROWS>(a, s);
+  int st = q.bad;
+  if (st == 0) {
+    if (!load_tree(a, s, q.m, s_tree)) st |= SPEC_ST_TREE;
+    const int held = q.m == 0 || q.len == 0 ? 0 : (q.len - 1) / a.page_size + 1;
+    // with a window, the pages between the sinks and the window may be gone
+    const int e1 = q.sinks > 0 ? (q.sinks - 1) / a.page_size + 1 : 0;
+    const int e0 = q.lo < q.len ? q.lo / a.page_size : held;
+    bool bad = false;
+    for (int e = tid; e < held; e += TJ_THREADS) {
+      if (e >= e1 && e < e0) continue;
+      const int p = a.table[(int64_t)q.slot * a.max_pages + e];
+      bad |= p < 0 || p >= a.n_pages;
+    }
+    if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
+  }
+  if (blk == 0 && tid == 0) a.status[s] = st;
+  const int rows = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
+  grid_dep_wait();
+  constexpr int DPL = HD / 32;  // head dimensions of a lane
+  for (int e = blk * TJ_ROWS + warp; e < min((blk + 1) * TJ_ROWS, rows * a.nq); e += TJ_THREADS / 32) {
+    const int node = e / a.nq, h = e % a.nq;
+    __half* dst = a.out + (((int64_t)s * a.nt + node) * a.nq + h) * HD + lane * DPL;
+    if (st != 0) {
+#pragma unroll
+      for (int d = 0; d < DPL; d++) dst[d] = __ushort_as_half(0x7FFF);
+      continue;
+    }
+    const int kvh = h / a.G, m = node * a.G + h % a.G, r = m % ROWS;
+    const long long u0 = before + (long long)(m / ROWS * a.nkv + kvh) * q.tiles, u1 = u0 + q.tiles;
+    // the CTAs that hold the unit's first and last tile
+    int b0 = (int)(u0 * n_cta / total), b1 = (int)((u1 - 1) * n_cta / total);
+    while (b0 > 0 && cut(total, b0, n_cta) > u0) b0--;
+    while (b0 + 1 < n_cta && cut(total, b0 + 1, n_cta) <= u0) b0++;
+    while (b1 > 0 && cut(total, b1, n_cta) > u1 - 1) b1--;
+    while (b1 + 1 < n_cta && cut(total, b1 + 1, n_cta) <= u1 - 1) b1++;
+    if (b0 == b1) continue;  // whole: written by its CTA
+    auto slot_of = [&](int b) { return (size_t)b * 2 + (cut(total, b, n_cta) < u0 ? 1 : 0); };
+    float mx = -INFINITY;
+    // CTAs without tiles (fewer tiles than CTAs) have written nothing
+    auto works = [&](int b) { return cut(total, b, n_cta) < cut(total, b + 1, n_cta); };
+    for (int b = b0 + lane; b <= b1; b += 32)
+      if (works(b)) mx = fmaxf(mx, __ldcg(a.part_ml + slot_of(b) * ROWS + r).x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    float o[DPL] = {}, l = 0.0f;
+    for (int bb = b0; bb <= b1; bb += 32) {
+      const int n = min(32, b1 + 1 - bb);
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      const bool has = lane < n && works(bb + lane);
+      if (has) ml = __ldcg(a.part_ml + slot_of(bb + lane) * ROWS + r);
+      const float w = has ? exp2f(ml.x - mx) : 0.0f;
+      for (int j = 0; j < n; j++) {
+        const float wj = __shfl_sync(0xffffffffu, w, j), lj = __shfl_sync(0xffffffffu, ml.y, j);
+        if (!__shfl_sync(0xffffffffu, has, j)) continue;
+        l = fmaf(lj, wj, l);
+        const float2* src = reinterpret_cast<const float2*>(
+            a.part_o + (slot_of(bb + j) * ROWS + r) * HD + lane * DPL);
+#pragma unroll
+        for (int d = 0; d < DPL; d += 2) {
+          const float2 v = __ldcg(src + d / 2);
+          o[d] = fmaf(v.x, wj, o[d]);
+          o[d + 1] = fmaf(v.y, wj, o[d + 1]);
+        }
+      }
+    }
+    const float inv = 1.0f / l;
+#pragma unroll
+    for (int d = 0; d < DPL; d++) dst[d] = __float2half_rn(o[d] * inv);
+  }
+}
+
+int rows_of(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
+template <int HD, int MT, int RTW>
+int launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
+  using Sh = Shape<HD, MT, RTW>;
+  tree_attn_kernel<HD, MT, RTW><<<n_cta, TT_THREADS, Sh::SMEM, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    const int blocks = (a.nt * a.nq + TJ_ROWS - 1) / TJ_ROWS;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = programmatic_launch() ? 1 : 0;
+    cfg.gridDim = dim3((unsigned)(a.n_seq * blocks));
+    cfg.blockDim = dim3(TJ_THREADS);
+    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<HD, Sh::ROWS>, a, n_cta, blocks);
+  }
+  if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("tree attention: ") + cudaGetErrorString(e));
+  return SPEC_OK;
+}
+
+template <int HD>
+int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
+  const int rows = rows_of(a.nt * a.G);
+  if (rows == 16) return launch_shape<HD, 1, 1>(a, n_cta, st);
+  if (rows == 32) return launch_shape<HD, 2, 1>(a, n_cta, st);
+  return launch_shape<HD, 2, 2>(a, n_cta, st);
+}
+
+template <int HD, int MT, int RTW>
+void init_shape() {
+  cudaFuncSetAttribute(tree_attn_kernel<HD, MT, RTW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)Shape<HD, MT, RTW>::SMEM);
+}
+
+int device_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+
+// Two CTAs an SM are resident at once.
+int tree_ctas() { return 2 * device_sms(); }
+
+int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
+  int rc = check_pages(kv, true);
+  if (rc != SPEC_OK) return rc;
+  if (kv->head_dim != 64 && kv->head_dim != 128)
+    return fail(SPEC_E_UNSUPPORTED, "tree attention supports head_dim 64 or 128");
+  if (n_seq < 1 || nt < 1 || nt > SPEC_MAX_TREE)
+    return fail(SPEC_E_SHAPE, "n_seq >= 1 and nt in [1, 64] required");
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads != 0)
+    return fail(SPEC_E_SHAPE, "n_q_heads must be a positive multiple of n_kv_heads");
+  if ((int64_t)kv->max_pages * kv->page_size > INT32_MAX - 2 * TT_KEYS)
+    return fail(SPEC_E_SHAPE, "max_pages * page_size must stay below 2^31 - 128 positions");
+  if ((double)n_seq * nt * n_q_heads > INT32_MAX) return fail(SPEC_E_SHAPE, "n_seq * nt * n_q_heads too large");
+  return SPEC_OK;
+}
+
+}  // namespace
+
+void tree_init_attrs() {
+  init_shape<64, 1, 1>();
+  init_shape<64, 2, 1>();
+  init_shape<64, 2, 2>();
+  init_shape<128, 1, 1>();
+  init_shape<128, 2, 1>();
+  init_shape<128, 2, 2>();
+}
+
+int tree_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads, size_t* bytes) {
+  const int rc = check_tree(kv, n_seq, nt, n_q_heads);
+  if (rc != SPEC_OK) return rc;
+  const size_t rows = rows_of(nt * (n_q_heads / kv->n_kv_heads));
+  *bytes = (size_t)tree_ctas() * 2 * rows * (sizeof(float) * kv->head_dim + sizeof(float2));
+  return SPEC_OK;
+}
+
+int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,
+                int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride,
+                uint16_t* out, void* workspace, int32_t* status, cudaStream_t st) {
+  TreeArgs a;
+  a.k = reinterpret_cast<const __half*>(kv->k) + (int64_t)layer * kv->layer_stride;
+  a.v = reinterpret_cast<const __half*>(kv->v) + (int64_t)layer * kv->layer_stride;
+  a.table = kv->table;
+  a.len = kv->len;
+  a.n_slots = kv->n_slots;
+  a.max_pages = kv->max_pages;
+  a.n_pages = kv->n_pages;
+  a.nkv = kv->n_kv_heads;
+  a.page_size = kv->page_size;
+  a.page_shift = -1;
+  for (int b = 0; b < 31; b++)
+    if (kv->page_size == 1 << b) a.page_shift = b;
+  a.slots = t->slots;
+  a.parents = t->parents;
+  a.n_nodes = t->n_nodes;
+  a.n_seq = t->n_seq;
+  a.nt = t->nt;
+  a.nq = t->n_q_heads;
+  a.G = t->n_q_heads / kv->n_kv_heads;
+  a.window = t->window;
+  a.sinks = t->sinks;
+  a.scale_log2 = (t->scale != 0.0f ? t->scale : 1.0f / sqrtf((float)kv->head_dim)) * 1.4426950408889634f;
+  a.q = reinterpret_cast<const __half*>(q);
+  a.q_stride = q_stride != 0 ? q_stride : (int64_t)a.nq * kv->head_dim;
+  a.k_new = reinterpret_cast<const __half*>(k_new);
+  a.v_new = reinterpret_cast<const __half*>(v_new);
+  a.kv_stride = kv_stride != 0 ? kv_stride : (int64_t)a.nkv * kv->head_dim;
+  a.out = reinterpret_cast<__half*>(out);
+  a.status = status;
+  const int n_cta = tree_ctas();
+  const size_t rows = rows_of(a.nt * a.G);
+  a.part_o = reinterpret_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)n_cta * 2 * rows * kv->head_dim);
+  return kv->head_dim == 128 ? launch_hd<128>(a, n_cta, st) : launch_hd<64>(a, n_cta, st);
+}

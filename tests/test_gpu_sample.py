@@ -1,0 +1,213 @@
+"""spec_sample on the GPU against the plain rules of oracle/tree.py: tokens,
+counts and filtered logits, all exactly."""
+import numpy as np
+import pytest
+
+from oracle import tree
+
+pytestmark = pytest.mark.gpu
+
+LOW = np.finfo(np.float32).min
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import torch
+    assert torch.cuda.is_available()
+    return torch.device("cuda:0")
+
+
+def run(dev, logits, u, T=None, k=None, p=None, m=None, ld=0, off=0, in_place=False, filtered=True, stream=None):
+    """The call on rows of stride ld that start `off` floats into a buffer."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    R, V = logits.shape
+    ld = ld or V
+    mk = lambda: torch.full((off + R * ld + 8,), 123.0, device=dev)  # noqa: E731
+    buf = mk()
+    rows = buf[off:off + R * ld].view(R, ld)
+    rows[:, :V] = torch.from_numpy(logits).to(dev)
+    fbuf = buf if in_place else mk()
+    t = lambda a, d: None if a is None else torch.from_numpy(np.asarray(a)).to(d).to(dev)  # noqa: E731
+    token = torch.full((R,), 99, dtype=torch.int32, device=dev)
+    kept = torch.full((R,), 99, dtype=torch.int32, device=dev)
+    uu = torch.from_numpy(np.asarray(u, np.uint32).view(np.int32)).to(dev)
+    sv.spec_sample(rows, R, V, uu, token, temperature=t(T, torch.float32), top_k=t(k, torch.int32),
+                   top_p=t(p, torch.float32), min_p=t(m, torch.float32), n_kept=kept,
+                   filtered=fbuf[off:] if filtered else None, ld=ld, ld_filtered=ld, stream=stream)
+    out = fbuf[off:off + R * ld].view(R, ld)
+    assert (fbuf[:off] == 123.0).all() and (out[:, V:] == 123.0).all() and (fbuf[off + R * ld:] == 123.0).all()
+    return token.cpu().numpy(), kept.cpu().numpy(), out[:, :V].cpu().numpy()
+
+
+def check(orc, dev, logits, u, T=None, k=None, p=None, m=None, **kw):
+    R = logits.shape[0]
+    tok, kept, filt = run(dev, logits, u, T, k, p, m, **kw)
+    at = lambda a, r, d: d if a is None else a[r]  # noqa: E731
+    for r in range(R):
+        ref, ids = tree.sample_row(logits[r], orc.row_weights, u[r], float(np.float32(at(T, r, 1.0))),
+                                   int(at(k, r, 0)), at(p, r, 1.0), at(m, r, 0.0))
+        assert (tok[r], kept[r]) == (ref, len(ids)), (r, at(T, r, 1.0), at(k, r, 0), at(p, r, 1.0), at(m, r, 0.0))
+        want = np.full_like(logits[r], LOW)
+        want[ids] = logits[r, ids]
+        if kw.get("filtered", True):
+            assert np.array_equal(filt[r].view(np.uint32), want.view(np.uint32)), r
+
+
+def settings(g, R, V):
+    """Rows of all kinds: each filter alone, together, at its ends."""
+    T = g.choice([0.0, 0.3, 0.7, 1.0, 1.7, 30.0], R).astype(np.float32)
+    k = g.choice([0, 1, 2, 5, 50, 1000, V - 1, V, V + 1, 2 ** 31 - 1], R).clip(0).astype(np.int32)
+    p = g.choice([0.0, 1e-6, 0.3, 0.9, 0.999, 1.0, 1.0], R).astype(np.float32)
+    m = g.choice([0.0, 0.0, 1e-9, 0.05, 1.0], R).astype(np.float32)
+    return T, k, p, m
+
+
+@pytest.mark.parametrize("V,R,ld,off", [(1, 8, 0, 0), (2, 40, 3, 1), (16, 60, 0, 0), (33, 60, 0, 3), (1000, 60, 1001, 2),
+                                        (4096, 20, 0, 0), (4097, 30, 0, 1), (9000, 24, 0, 0), (32000, 24, 0, 0),
+                                        (32001, 16, 32004, 0), (151936, 6, 0, 0), (248320, 6, 0, 0)])
+def test_rows_of_every_kind(orc, dev, V, R, ld, off):
+    g = np.random.default_rng(V)
+    logits = (g.standard_normal((R, V)) * g.choice([0.1, 2.0, 8.0], (R, 1))).astype(np.float32)
+    u = g.integers(0, 2 ** 32, R, dtype=np.uint64)
+    u[:4] = [0, 2 ** 32 - 1, 1, 2 ** 31][:min(4, R)]
+    check(orc, dev, logits, u, *settings(g, R, V), ld=ld, off=off)
+
+
+@pytest.mark.parametrize("V,levels", [(50, 2), (3000, 1), (3000, 3), (40000, 1), (40000, 7), (248320, 2)])
+def test_equal_logits(orc, dev, V, levels):
+    """Ties go to the lowest id, within bins of far more tokens than are
+    ranked at once, at cuts inside a tie of counts and of masses."""
+    g = np.random.default_rng(V + levels)
+    R = 24 if V < 100000 else 4
+    logits = (g.integers(0, levels, (R, V)) * 0.125 - 3.0).astype(np.float32)
+    logits[logits == 0] *= g.choice([1.0, -1.0])  # zeros of both signs are equal
+    u = g.integers(0, 2 ** 32, R, dtype=np.uint64)
+    check(orc, dev, logits, u, *settings(g, R, V))
+
+
+def test_nearly_equal_logits(orc, dev):
+    """Logits a few ulps apart: one step of z holds them all, their order keys
+    differ in the last bits; and a crowd around zero, where keys are dense."""
+    g = np.random.default_rng(8)
+    V, R = 20000, 24
+    near = (np.float32(1.0) + g.integers(0, 3000, (R // 2, V)).astype(np.float32) * np.float32(2 ** -23))
+    zero = (g.standard_normal((R // 2, V)) * 1e-30).astype(np.float32)
+    logits = np.concatenate([near, zero]).astype(np.float32)
+    u = g.integers(0, 2 ** 32, R, dtype=np.uint64)
+    check(orc, dev, logits, u, *settings(g, R, V))
+
+
+def test_masked_logits(orc, dev):
+    """-infinity and the type's lowest value where a grammar forbids tokens,
+    down to one token that is allowed; none of -infinity is ever kept."""
+    g = np.random.default_rng(9)
+    V, R = 10000, 40
+    logits = (g.standard_normal((R, V)) * 2).astype(np.float32)
+    for r in range(R):
+        gone = g.permutation(V)[:[V - 1, V - 2, V // 2, 10][r % 4]]
+        logits[r, gone] = [-np.inf, LOW][r // 4 % 2]
+    T, k, p, m = settings(g, R, V)
+    T = np.where(T == 0, np.float32(0), np.maximum(T, np.float32(1.0)))  # LOW / T stays finite
+    u = g.integers(0, 2 ** 32, R, dtype=np.uint64)
+    check(orc, dev, logits, u, T, k, p, m)
+    # a row of the lowest value alone is even; with T < 1 it overflows and is refused
+    flat = np.full((2, 64), LOW, np.float32)
+    tok, kept, _ = run(dev, flat, [2 ** 31, 5], T=np.array([1.0, 0.5], np.float32))
+    assert tok.tolist() == [32, -1] and kept.tolist() == [64, 0]
+
+
+def test_refused_rows(orc, dev):
+    """A bad row gets -1, 0 and NaN; its neighbours are served."""
+    g = np.random.default_rng(10)
+    V, R = 5000, 12
+    logits = g.standard_normal((R, V)).astype(np.float32)
+    logits[1, 4999] = np.nan
+    logits[2, 0] = np.inf
+    logits[3, :] = -np.inf
+    T, k = np.ones(R, np.float32), np.full(R, 40, np.int32)
+    p, m = np.full(R, 0.9, np.float32), np.zeros(R, np.float32)
+    T[4], T[5], T[6], k[7], p[8], p[9], m[10] = -1, np.nan, np.inf, -1, 1.5, np.nan, -0.1
+    tok, kept, filt = run(dev, logits, np.arange(R), T, k, p, m)
+    assert (tok[1:11] == -1).all() and (kept[1:11] == 0).all() and np.isnan(filt[1:11]).all()
+    for r in (0, 11):
+        ref, ids = tree.sample_row(logits[r], orc.row_weights, r, 1.0, 40, 0.9)
+        assert (tok[r], kept[r]) == (ref, len(ids)) and np.isfinite(filt[r]).all()
+
+
+def test_in_place_without_outputs_on_a_stream_and_replayed(orc, dev):
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(11)
+    V, R = 33000, 10
+    logits = (g.standard_normal((R, V)) * 2).astype(np.float32)
+    u = g.integers(0, 2 ** 32, R, dtype=np.uint64)
+    T, k, p, m = settings(g, R, V)
+    check(orc, dev, logits, u, T, k, p, m, in_place=True)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        check(orc, dev, logits, u, T, k, p, m, filtered=False)
+    ld, token = torch.from_numpy(logits).to(dev), torch.zeros(R, dtype=torch.int32, device=dev)
+    ud = torch.from_numpy(u.astype(np.uint32).view(np.int32)).to(dev)
+    kd = torch.from_numpy(k).to(dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sv.spec_sample(ld, R, V, ud, token, top_k=kd)
+    for r in range(3):  # new words and settings in the same arrays
+        u2 = g.integers(0, 2 ** 32, R, dtype=np.uint64)
+        k2 = g.integers(0, 60, R).astype(np.int32)
+        ud.copy_(torch.from_numpy(u2.astype(np.uint32).view(np.int32)))
+        kd.copy_(torch.from_numpy(k2))
+        graph.replay()
+        assert token.tolist() == [tree.sample_row(logits[i], orc.row_weights, u2[i], 1.0, int(k2[i]))[0] for i in range(R)]
+
+
+def test_rows_beyond_shared_memory(orc, dev):
+    """A vocabulary that a cluster's shared memory does not hold whole."""
+    g = np.random.default_rng(12)
+    V, R = 600001, 3
+    logits = (g.standard_normal((R, V)) * 2).astype(np.float32)
+    u = g.integers(0, 2 ** 32, R, dtype=np.uint64)
+    T, k = np.array([0.8, 1.0, 1.0], np.float32), np.array([40, 0, 0], np.int32)
+    p, m = np.array([0.9, 0.95, 1.0], np.float32), np.array([0, 0.01, 0], np.float32)
+    check(orc, dev, logits, u, T, k, p, m)
+    check(orc, dev, logits, u, T, k, p, m, in_place=True, off=1)
+
+
+def test_filtered_logits_feed_the_rejection_sampler(orc, dev):
+    """Drafts sampled under filters, target rows filtered alike: the accept of
+    the filtered rows is the oracle's, and no emitted token was filtered out."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(13)
+    n_seq, d, V, T = 6, 5, 3000, 0.8
+    q = (g.standard_normal((n_seq, d, V)) * 2).astype(np.float32)
+    p = np.concatenate([q, q[:, :1]], 1) + (g.standard_normal((n_seq, d + 1, V)) * 0.5).astype(np.float32)
+    full = lambda n, v, t: np.full(n, v, t)  # noqa: E731
+
+    def filt(x, u):
+        R = x.shape[0] * x.shape[1]
+        return run(dev, x.reshape(R, V), u, full(R, T, np.float32), full(R, 30, np.int32), full(R, 0.9, np.float32))
+    draft, _, qf = filt(q, g.integers(0, 2 ** 32, n_seq * d, dtype=np.uint64))
+    _, kept, pf = filt(p, g.integers(0, 2 ** 32, n_seq * (d + 1), dtype=np.uint64))
+    assert (kept <= 30).all()
+    qf, pf, draft = qf.reshape(q.shape), pf.reshape(p.shape), draft.reshape(n_seq, d)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    em = torch.zeros((n_seq, d + 1), dtype=torch.int32, device=dev)
+    n_acc = torch.zeros(n_seq, dtype=torch.int32, device=dev)
+    idx = torch.zeros(n_seq, dtype=torch.int64, device=dev)
+    sv.spec_accept_stochastic(t(pf), t(qf), t(draft), n_seq, d, V, T, 5, t(np.arange(n_seq, dtype=np.int32)), idx,
+                              n_acc, em)
+    assert sv.spec_error_check(None) == 0
+    n_ref, em_ref, _ = orc.accept_stochastic(pf, qf, draft, T, 5, list(range(n_seq)), np.zeros(n_seq, np.uint64))
+    assert np.array_equal(n_acc.cpu().numpy(), n_ref) and np.array_equal(em.cpu().numpy(), em_ref)
+    for s in range(n_seq):
+        for i in range(n_ref[s] + 1):
+            assert pf[s, i, em_ref[s, i]] > LOW
+    # a refused row fails the accept closed
+    bad = t(pf)
+    bad[0] = float("nan")
+    sv.spec_accept_stochastic(bad, t(qf), t(draft), n_seq, d, V, T, 5, t(np.arange(n_seq, dtype=np.int32)), idx,
+                              n_acc, em)
+    assert sv.spec_error_check(None) != 0 and (n_acc == -1).all()
