@@ -487,6 +487,7 @@ typedef struct {
 #define SPEC_ST_SHARED 4 /* the page is held by another slot */
 #define SPEC_ST_FULL 8   /* not enough free pages, or more positions than max_pages hold */
 #define SPEC_ST_TREE 16  /* bad parents, node count or path */
+#define SPEC_ST_TIMEOUT 32 /* a bounded device wait ran out */
 
 #define SPEC_MAX_TREE 64 /* nodes of a tree */
 

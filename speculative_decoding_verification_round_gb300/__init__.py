@@ -29,7 +29,8 @@ SPEC_Q4, SPEC_Q6, SPEC_Q8 = 4, 6, 8
 SPEC_MAX_NT = 16
 SPEC_MAX_TREE = 64
 SPEC_FILTERED = -3.4028234663852886e38
-SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_SHARED, SPEC_ST_FULL, SPEC_ST_TREE = 1, 2, 4, 8, 16
+SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_SHARED, SPEC_ST_FULL, SPEC_ST_TREE, SPEC_ST_TIMEOUT = (
+    1, 2, 4, 8, 16, 32)
 SPEC_PROF_QKV, SPEC_PROF_O, SPEC_PROF_GATE_UP, SPEC_PROF_DOWN = 0, 1, 2, 3
 SPEC_PROF_LM_HEAD, SPEC_PROF_ALL_GEMMS, SPEC_PROF_ATTN = 4, 5, 6
 

@@ -18,34 +18,13 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "tree_attn.cuh"
 
 namespace {
 
-constexpr int TT_KEYS = 64;  // positions per tile
+constexpr int TT_SHIFT = 6, TT_KEYS = 1 << TT_SHIFT;  // positions per tile
 constexpr int TT_THREADS = 128;
 constexpr int TT_STAGES = 3;
-
-struct TreeArgs {
-  const __half* k;  // the layer's cache
-  const __half* v;
-  const int32_t* table;
-  const int32_t* len;
-  int n_slots, max_pages, n_pages, nkv, page_size, page_shift;  // shift -1: not a power of two
-  const int32_t* slots;
-  const int32_t* parents;
-  const int32_t* n_nodes;
-  int n_seq, nt, nq, G, window, sinks;
-  float scale_log2;
-  const __half* q;
-  int64_t q_stride;
-  const __half* k_new;
-  const __half* v_new;
-  int64_t kv_stride;
-  __half* out;
-  float* part_o;    // [N][2][rows][HD]
-  float2* part_ml;  // [N][2][rows]
-  int32_t* status;
-};
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -58,6 +37,24 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
+// Two floats as packed fp16, the first in the low half; and back.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
+  float2 f;
+  asm("{\n .reg .f16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
+      : "=f"(f.x), "=f"(f.y) : "r"(v));
+  return f;
+}
+// 2^x (0 below the normal range, which no sum here can tell apart).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // 16 bytes to shared memory; zeros if !valid (src is then any readable address).
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -67,113 +64,6 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) 
 template <int HD>
 __device__ __forceinline__ uint32_t tile_off(int r, int u) {
   return (uint32_t)(r * (HD * 2) + ((u ^ (r & 7)) << 4));
-}
-
-// ---------------------------------------------------------------------------
-// the cut of the work
-// ---------------------------------------------------------------------------
-// One sequence: its tiles are the sink tiles below the window, the tiles from
-// the window's first position to the last, and the tree's own.
-struct SeqInfo {
-  int slot, len, m;
-  int lo;       // first position that some node's window reaches
-  int sinks;    // positions of the prefix that stay visible under a window
-  int w_tile;   // tile of lo
-  int n_sink;   // sink tiles in front of it
-  int tiles;
-  int units;    // kv heads x row blocks
-  int bad;      // status bits of what is checked here
-  __device__ __forceinline__ long long work() const { return (long long)units * tiles; }
-};
-
-template <int ROWS>
-__device__ __forceinline__ SeqInfo seq_info(const TreeArgs& a, int s) {
-  SeqInfo q;
-  q.slot = a.slots[s];
-  q.m = a.n_nodes != nullptr ? a.n_nodes[s] : a.nt;
-  q.bad = 0;
-  q.len = 0;
-  if (q.slot < 0 || q.slot >= a.n_slots) {
-    q.bad |= SPEC_ST_SLOT;
-  } else {
-    q.len = a.len[q.slot];
-    if (q.len < 0 || q.len > a.max_pages * a.page_size) q.bad |= SPEC_ST_PAGE;
-  }
-  if (q.m < 0 || q.m > a.nt) q.bad |= SPEC_ST_TREE;
-  if (q.bad != 0) q.len = q.m = 0;
-  q.lo = a.window > 0 ? max(0, q.len - a.window + 1) : 0;
-  q.sinks = a.window > 0 ? min(a.sinks, q.len) : 0;
-  const int end = (q.len + TT_KEYS - 1) / TT_KEYS;
-  q.w_tile = q.lo < q.len ? q.lo / TT_KEYS : end;
-  q.n_sink = min((q.sinks + TT_KEYS - 1) / TT_KEYS, q.w_tile);
-  q.tiles = q.n_sink + (end - q.w_tile) + 1;
-  q.units = q.m > 0 ? a.nkv * ((q.m * a.G + ROWS - 1) / ROWS) : 0;
-  return q;
-}
-
-// Exclusive sum over the CTA's threads; *total: the whole.
-template <int THREADS>
-__device__ __forceinline__ long long block_excl(long long v, long long* s_part, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) s_part[warp] = x;
-  __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; w++) {
-    if (w < warp) before += s_part[w];
-    all += s_part[w];
-  }
-  *total = all;
-  return before + x - v;
-}
-
-__device__ __forceinline__ long long cut(long long total, int b, int n) {
-  // total * b / n without overflow: total below 2^53 or so, b and n small
-  return total / n * b + total % n * b / n;
-}
-
-// ---------------------------------------------------------------------------
-// the tree of one sequence: every node's ancestors (with itself) and depth
-// ---------------------------------------------------------------------------
-struct TreeSmem {
-  unsigned long long anc[SPEC_MAX_TREE];
-  int depth[SPEC_MAX_TREE];
-  int par[SPEC_MAX_TREE];
-};
-
-// Every thread of the CTA; returns whether the parents make a tree.
-__device__ __forceinline__ bool load_tree(const TreeArgs& a, int s, int m, TreeSmem& t) {
-  const int i = threadIdx.x;
-  bool bad = false;
-  __syncthreads();  // the last sequence's tree is no longer read
-  if (i < SPEC_MAX_TREE) {
-    int p = -1;
-    if (i < m) {
-      p = a.parents != nullptr ? a.parents[(int64_t)s * a.nt + i] : i - 1;
-      bad = p < -1 || p >= i;
-    }
-    t.par[i] = bad ? -1 : p;
-  }
-  const bool any = __syncthreads_or(bad);
-  if (i < m) {
-    unsigned long long set = 1ull << i;
-    int d = 0;
-    for (int p = t.par[i]; p >= 0; p = t.par[p]) {
-      set |= 1ull << p;
-      d++;
-    }
-    t.anc[i] = set;
-    t.depth[i] = d;
-  }
-  __syncthreads();
-  return !any;
 }
 
 // ---------------------------------------------------------------------------
@@ -190,7 +80,7 @@ struct Shape {
   static constexpr int XROW = HD + 8;            // floats of an exchange row (padded)
   static constexpr size_t Q_OFF = (size_t)TT_STAGES * 2 * TILE;
   static constexpr size_t SMEM = Q_OFF + (size_t)ROWS * HD * 2;
-  static_assert((size_t)KG * ROWS * XROW * 4 <= Q_OFF, "the exchange fits over the tiles");
+  static_assert((size_t)KG * ROWS * (XROW * 4 + 8) <= Q_OFF, "the exchange fits over the tiles");
 };
 
 template <int HD, int MT, int RTW>
@@ -202,40 +92,17 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
   __shared__ long long s_part[TT_THREADS / 32];
   __shared__ long long s_off;
   __shared__ int s_seq;
-  __shared__ float2 s_ml[4][16 * MT];
   grid_dep_launch();  // the joining kernel may get ready
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int kg = warp % KG, rw = warp / KG;  // this warp's key group and row block
 
-  // ---- this CTA's share of the tiles
-  long long total = 0, first = 0, w0, w1;
-  {
-    long long mine = 0, excl = 0, chunk = 0;
-    for (int base = 0; base < a.n_seq; base += TT_THREADS) {
-      mine = base + tid < a.n_seq ? seq_info<ROWS>(a, base + tid).work() : 0;
-      excl = block_excl<TT_THREADS>(mine, s_part, &chunk);
-      total += chunk;
-    }
-    w0 = cut(total, blockIdx.x, gridDim.x);
-    w1 = cut(total, blockIdx.x + 1, gridDim.x);
-    if (w0 >= w1) return;
-    for (int base = 0; base < a.n_seq; base += TT_THREADS) {
-      if (a.n_seq > TT_THREADS) {
-        mine = base + tid < a.n_seq ? seq_info<ROWS>(a, base + tid).work() : 0;
-        excl = block_excl<TT_THREADS>(mine, s_part, &chunk);
-      }
-      if (first + excl <= w0 && w0 < first + excl + mine) {
-        s_seq = base + tid;
-        s_off = w0 - first - excl;
-      }
-      first += chunk;
-    }
-    __syncthreads();
-  }
+  const Range range = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, s_part, &s_seq, &s_off);
+  const long long w0 = range.w0, w1 = range.w1;
+  if (w0 >= w1) return;
   int s = s_seq;
   long long off = s_off;
-  SeqInfo q = seq_info<ROWS>(a, s);
+  SeqInfo q = seq_info(a, s, ROWS, TT_SHIFT);
   load_tree(a, s, q.m, s_tree);
 
   const uint32_t sm0 = smem_u32(smem), qs0 = sm0 + (uint32_t)Sh::Q_OFF;
@@ -245,7 +112,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
     if (off >= q.work()) {  // the next sequence with work
       s++;
       off = 0;
-      q = seq_info<ROWS>(a, s);
+      q = seq_info(a, s, ROWS, TT_SHIFT);
       if (q.work() > 0) load_tree(a, s, q.m, s_tree);
       continue;
     }
@@ -401,13 +268,13 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
           m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
           m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
           nm[h] = m2 == -INFINITY ? 0.0f : m2;  // a row without a visible key so far
-          al[h] = exp2f(mx[i][h] - nm[h]);
+          al[h] = exp2_fast(mx[i][h] - nm[h]);
           mx[i][h] = m2;
           float l = 0.0f;
 #pragma unroll
           for (int nb = 0; nb < NB; nb++) {
-            sc[i][nb][2 * h] = exp2f(sc[i][nb][2 * h] - nm[h]);
-            sc[i][nb][2 * h + 1] = exp2f(sc[i][nb][2 * h + 1] - nm[h]);
+            sc[i][nb][2 * h] = exp2_fast(sc[i][nb][2 * h] - nm[h]);
+            sc[i][nb][2 * h + 1] = exp2_fast(sc[i][nb][2 * h + 1] - nm[h]);
             l += sc[i][nb][2 * h] + sc[i][nb][2 * h + 1];
           }
           sum[i][h] = fmaf(sum[i][h], al[h], l);  // this lane's share of the row
@@ -436,31 +303,30 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
             odd |= (v[x] & 0x7C00u) == 0x7C00u || (v[x] & 0x7C000000u) == 0x7C000000u;
         }
         if (__syncthreads_or(odd)) {
-          for (int key = key0; key < key0 + KEYS; key++) {
 #pragma unroll
-            for (int i = 0; i < MT; i++)
+          for (int i = 0; i < MT; i++)
 #pragma unroll
-              for (int nb = 0; nb < NB; nb++) {
-                if ((key - key0) / 8 != nb) continue;
-                const int src = (lane & ~3) | ((key & 7) >> 1);
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll 1
+              for (int kb = 0; kb < 8; kb++) {
+                const int src = (lane & ~3) | (kb >> 1), key = key0 + 8 * nb + kb;
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                   const float pa = __shfl_sync(0xffffffffu, sc[i][nb][2 * h], src);
                   const float pb = __shfl_sync(0xffffffffu, sc[i][nb][2 * h + 1], src);
-                  const float p = key & 1 ? pb : pa;
+                  const float p = kb & 1 ? pb : pa;
                   if (p > 0.0f) {
 #pragma unroll
                     for (int d = 0; d < HD / 8; d++) {
                       uint32_t v;
                       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(vs + tile_off<HD>(key, d) + t4 * 4));
-                      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&v));
+                      const float2 f = unpack_f16(v);
                       o[i][d][2 * h] = fmaf(p, f.x, o[i][d][2 * h]);
                       o[i][d][2 * h + 1] = fmaf(p, f.y, o[i][d][2 * h + 1]);
                     }
                   }
                 }
               }
-          }
           __syncthreads();
           for (int e = tid; e < TT_KEYS * UNITS; e += TT_THREADS)
             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vs + e * 16), "r"(0));
@@ -478,11 +344,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
 #pragma unroll
             for (int h = 0; h < 2; h++) {
               const float p0 = sc[i][2 * kk + n][2 * h], p1 = sc[i][2 * kk + n][2 * h + 1];
-              const __half2 hh = __floats2half2_rn(p0, p1);
-              const float2 f = __half22float2(hh);
-              const __half2 ll = __floats2half2_rn(p0 - f.x, p1 - f.y);
-              hi[i][2 * n + h] = *reinterpret_cast<const uint32_t*>(&hh);
-              lo[i][2 * n + h] = *reinterpret_cast<const uint32_t*>(&ll);
+              hi[i][2 * n + h] = pack_f16(p0, p1);
+              const float2 f = unpack_f16(hi[i][2 * n + h]);
+              lo[i][2 * n + h] = pack_f16(p0 - f.x, p1 - f.y);
             }
 #pragma unroll
         for (int d = 0; d < HD / 8; d += 2) {
@@ -503,6 +367,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the tiles have been read
     float* x = reinterpret_cast<float*>(smem);
+    float2(*s_ml)[16 * MT] = reinterpret_cast<float2(*)[16 * MT]>(x + (size_t)KG * ROWS * Sh::XROW);
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
@@ -540,12 +405,14 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
       }
       if (whole) {
         const float inv = 1.0f / l;
-        __half2 y[4];
-#pragma unroll
-        for (int d = 0; d < 4; d++) y[d] = __floats2half2_rn(acc[2 * d] * inv, acc[2 * d + 1] * inv);
+        uint4 y;
+        y.x = pack_f16(acc[0] * inv, acc[1] * inv);
+        y.y = pack_f16(acc[2] * inv, acc[3] * inv);
+        y.z = pack_f16(acc[4] * inv, acc[5] * inv);
+        y.w = pack_f16(acc[6] * inv, acc[7] * inv);
         const int node = m / a.G, hd = kvh * a.G + m % a.G;
         *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + hd) * HD + u * 8) =
-            *reinterpret_cast<const uint4*>(y);
+            y;
       } else {
         float* po = a.part_o + (slot * ROWS + r) * HD + u * 8;
         *reinterpret_cast<float4*>(po) = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -565,9 +432,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
 // the positions, or writes NaN for a sequence in error.
 // ---------------------------------------------------------------------------
 constexpr int TJ_THREADS = 128;
-constexpr int TJ_ROWS = 16;  // output rows (node, head) of a CTA
+constexpr int TJ_ROWS = TJ_THREADS / 32;  // output rows (node, head) of a CTA
 
-template <int HD, int ROWS>
+template <int HD>
 __global__ void __launch_bounds__(TJ_THREADS)
 tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
   __shared__ TreeSmem s_tree;
@@ -576,14 +443,15 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long total = 0, before = 0;
   for (int base = 0; base < a.n_seq; base += TJ_THREADS) {
-    const long long mine = base + tid < a.n_seq ? seq_info<ROWS>(a, base + tid).work() : 0;
+    const long long mine = base + tid < a.n_seq ? seq_info(a, base + tid, a.rows, a.tile_shift).work() : 0;
     long long chunk;
     block_excl<TJ_THREADS>(mine, s_part, &chunk);
     total += chunk;
+    if (s < base) continue;
     block_excl<TJ_THREADS>(base + tid < s ? mine : 0, s_part, &chunk);
     before += chunk;
   }
-  const SeqInfo q = seq_info<ROWS>(a, s);
+  const SeqInfo q = seq_info(a, s, a.rows, a.tile_shift);
   int st = q.bad;
   if (st == 0) {
     if (!load_tree(a, s, q.m, s_tree)) st |= SPEC_ST_TREE;
@@ -599,69 +467,101 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
     }
     if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
   }
-  if (blk == 0 && tid == 0) a.status[s] = st;
   const int rows = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
-  grid_dep_wait();
+  // this warp's row: its unit's tiles and the CTAs that hold the first and last
   constexpr int DPL = HD / 32;  // head dimensions of a lane
-  for (int e = blk * TJ_ROWS + warp; e < min((blk + 1) * TJ_ROWS, rows * a.nq); e += TJ_THREADS / 32) {
-    const int node = e / a.nq, h = e % a.nq;
-    __half* dst = a.out + (((int64_t)s * a.nt + node) * a.nq + h) * HD + lane * DPL;
-    if (st != 0) {
-#pragma unroll
-      for (int d = 0; d < DPL; d++) dst[d] = __ushort_as_half(0x7FFF);
-      continue;
+  const int e = blk * TJ_ROWS + warp, node = e / a.nq, h = e % a.nq;
+  const long long share = max(share_of(total, n_cta), 1ll);
+  const int kvh = h / a.G, m = node * a.G + h % a.G, r = m & (a.rows - 1);
+  const long long u0 = before + (long long)(m / a.rows * a.nkv + kvh) * q.tiles, u1 = u0 + q.tiles;
+  const bool live = st == 0 && e < rows * a.nq;
+  const int b0 = live ? (int)((unsigned long long)u0 / (unsigned long long)share) : 0;
+  const int b1 = live ? (int)((unsigned long long)(u1 - 1) / (unsigned long long)share) : 0;
+  grid_dep_wait();
+  if (a.part_err != nullptr) {  // CTAs that gave up on a wait
+    bool gave_up = false;
+    if (live)
+      for (int b = b0 + lane; b <= b1; b += 32) gave_up |= __ldcg(a.part_err + b) != 0u;
+    if (blk == 0 && st == 0) {  // the status speaks for every row
+      const long long f0 = before / share, f1 = (before + max(q.work(), 1ll) - 1) / share;
+      for (long long b = f0 + tid; b <= f1 && b < n_cta; b += TJ_THREADS) gave_up |= __ldcg(a.part_err + b) != 0u;
+      if (__syncthreads_or(gave_up)) st |= SPEC_ST_TIMEOUT;
+    } else if (__any_sync(0xffffffffu, gave_up)) {
+      st |= SPEC_ST_TIMEOUT;
     }
-    const int kvh = h / a.G, m = node * a.G + h % a.G, r = m % ROWS;
-    const long long u0 = before + (long long)(m / ROWS * a.nkv + kvh) * q.tiles, u1 = u0 + q.tiles;
-    // the CTAs that hold the unit's first and last tile
-    int b0 = (int)(u0 * n_cta / total), b1 = (int)((u1 - 1) * n_cta / total);
-    while (b0 > 0 && cut(total, b0, n_cta) > u0) b0--;
-    while (b0 + 1 < n_cta && cut(total, b0 + 1, n_cta) <= u0) b0++;
-    while (b1 > 0 && cut(total, b1, n_cta) > u1 - 1) b1--;
-    while (b1 + 1 < n_cta && cut(total, b1 + 1, n_cta) <= u1 - 1) b1++;
-    if (b0 == b1) continue;  // whole: written by its CTA
-    auto slot_of = [&](int b) { return (size_t)b * 2 + (cut(total, b, n_cta) < u0 ? 1 : 0); };
-    float mx = -INFINITY;
-    // CTAs without tiles (fewer tiles than CTAs) have written nothing
-    auto works = [&](int b) { return cut(total, b, n_cta) < cut(total, b + 1, n_cta); };
-    for (int b = b0 + lane; b <= b1; b += 32)
-      if (works(b)) mx = fmaxf(mx, __ldcg(a.part_ml + slot_of(b) * ROWS + r).x);
+  }
+  if (blk == 0 && tid == 0) a.status[s] = st;
+  if (e >= rows * a.nq) return;
+  __half* dst = a.out + (((int64_t)s * a.nt + node) * a.nq + h) * HD + lane * DPL;
+  if (st != 0) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    float o[DPL] = {}, l = 0.0f;
-    for (int bb = b0; bb <= b1; bb += 32) {
-      const int n = min(32, b1 + 1 - bb);
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      const bool has = lane < n && works(bb + lane);
-      if (has) ml = __ldcg(a.part_ml + slot_of(bb + lane) * ROWS + r);
-      const float w = has ? exp2f(ml.x - mx) : 0.0f;
-      for (int j = 0; j < n; j++) {
-        const float wj = __shfl_sync(0xffffffffu, w, j), lj = __shfl_sync(0xffffffffu, ml.y, j);
-        if (!__shfl_sync(0xffffffffu, has, j)) continue;
-        l = fmaf(lj, wj, l);
-        const float2* src = reinterpret_cast<const float2*>(
-            a.part_o + (slot_of(bb + j) * ROWS + r) * HD + lane * DPL);
+    for (int d = 0; d < DPL; d++) dst[d] = __ushort_as_half(0x7FFF);
+    return;
+  }
+  if (b0 == b1) return;  // whole: written by its CTA
+  // piece of CTA b: its first, unless it began in front of the unit
+  auto slot_of = [&](int b) { return (size_t)b * 2 + (share * b < u0 ? 1 : 0); };
+  float mx = -INFINITY;
+  float2 ml0 = make_float2(-INFINITY, 0.0f);  // of piece b0 + lane
+  if (b0 + lane <= b1) ml0 = __ldcg(a.part_ml + slot_of(b0 + lane) * a.rows + r);
+  mx = ml0.x;
+  for (int b = b0 + 32 + lane; b <= b1; b += 32) mx = fmaxf(mx, __ldcg(a.part_ml + slot_of(b) * a.rows + r).x);
 #pragma unroll
-        for (int d = 0; d < DPL; d += 2) {
-          const float2 v = __ldcg(src + d / 2);
-          o[d] = fmaf(v.x, wj, o[d]);
-          o[d + 1] = fmaf(v.y, wj, o[d + 1]);
+  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  float o[DPL] = {}, l = 0.0f;
+  constexpr int U = 8;  // pieces whose loads are in flight together
+  for (int bb = b0; bb <= b1; bb += 32) {
+    const int n = min(32, b1 + 1 - bb);
+    float2 ml = ml0;
+    if (bb > b0) {
+      ml = make_float2(-INFINITY, 0.0f);
+      if (lane < n) ml = __ldcg(a.part_ml + slot_of(bb + lane) * a.rows + r);
+    }
+    const float w = lane < n ? exp2f(ml.x - mx) : 0.0f;
+    for (int j0 = 0; j0 < n; j0 += U) {
+      float2 v[U][DPL / 2];
+#pragma unroll
+      for (int j = 0; j < U; j++)
+        if (j0 + j < n) {
+          const float2* src = reinterpret_cast<const float2*>(
+              a.part_o + (slot_of(bb + j0 + j) * a.rows + r) * HD + lane * DPL);
+#pragma unroll
+          for (int d = 0; d < DPL / 2; d++) v[j][d] = __ldcg(src + d);
+        }
+#pragma unroll
+      for (int j = 0; j < U; j++) {
+        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+        const float lj = __shfl_sync(0xffffffffu, ml.y, (j0 + j) & 31);
+        if (j0 + j < n) {
+          l = fmaf(lj, wj, l);
+#pragma unroll
+          for (int d = 0; d < DPL / 2; d++) {
+            o[2 * d] = fmaf(v[j][d].x, wj, o[2 * d]);
+            o[2 * d + 1] = fmaf(v[j][d].y, wj, o[2 * d + 1]);
+          }
         }
       }
     }
-    const float inv = 1.0f / l;
-#pragma unroll
-    for (int d = 0; d < DPL; d++) dst[d] = __float2half_rn(o[d] * inv);
   }
+  const float inv = 1.0f / l;
+#pragma unroll
+  for (int d = 0; d < DPL; d += 2)
+    *reinterpret_cast<__half2*>(dst + d) = __floats2half2_rn(o[d] * inv, o[d + 1] * inv);
 }
 
 int rows_of(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
 template <int HD, int MT, int RTW>
-int launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  using Sh = Shape<HD, MT, RTW>;
-  tree_attn_kernel<HD, MT, RTW><<<n_cta, TT_THREADS, Sh::SMEM, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
+  tree_attn_kernel<HD, MT, RTW><<<n_cta, TT_THREADS, Shape<HD, MT, RTW>::SMEM, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int HD>
+int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
+  cudaError_t e = a.rows == 16   ? launch_shape<HD, 1, 1>(a, n_cta, st)
+                  : a.rows == 32 ? launch_shape<HD, 2, 1>(a, n_cta, st)
+                                 : launch_shape<HD, 2, 2>(a, n_cta, st);
   if (e == cudaSuccess) {
     const int blocks = (a.nt * a.nq + TJ_ROWS - 1) / TJ_ROWS;
     cudaLaunchAttribute at[1];
@@ -673,18 +573,10 @@ int launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
     cfg.numAttrs = programmatic_launch() ? 1 : 0;
     cfg.gridDim = dim3((unsigned)(a.n_seq * blocks));
     cfg.blockDim = dim3(TJ_THREADS);
-    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<HD, Sh::ROWS>, a, n_cta, blocks);
+    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<HD>, a, n_cta, blocks);
   }
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("tree attention: ") + cudaGetErrorString(e));
   return SPEC_OK;
-}
-
-template <int HD>
-int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  const int rows = rows_of(a.nt * a.G);
-  if (rows == 16) return launch_shape<HD, 1, 1>(a, n_cta, st);
-  if (rows == 32) return launch_shape<HD, 2, 1>(a, n_cta, st);
-  return launch_shape<HD, 2, 2>(a, n_cta, st);
 }
 
 template <int HD, int MT, int RTW>
@@ -771,7 +663,9 @@ int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint1
   a.out = reinterpret_cast<__half*>(out);
   a.status = status;
   const int n_cta = tree_ctas();
-  const size_t rows = rows_of(a.nt * a.G);
+  const size_t rows = a.rows = rows_of(a.nt * a.G);
+  a.tile_shift = TT_SHIFT;
+  a.part_err = nullptr;
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)n_cta * 2 * rows * kv->head_dim);
   return kv->head_dim == 128 ? launch_hd<128>(a, n_cta, st) : launch_hd<64>(a, n_cta, st);

@@ -1,0 +1,184 @@
+// tree_attn.cuh -- what the tree attention kernels share: their arguments, the
+// cut of the work over the CTAs, a tree's ancestors.  Internal.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+
+struct TreeArgs {
+  const __half* k;  // the layer's cache
+  const __half* v;
+  const int32_t* table;
+  const int32_t* len;
+  int n_slots, max_pages, n_pages, nkv, page_size, page_shift;  // shift -1: not a power of two
+  const int32_t* slots;
+  const int32_t* parents;
+  const int32_t* n_nodes;
+  int n_seq, nt, nq, G, window, sinks;
+  float scale_log2;
+  const __half* q;
+  int64_t q_stride;
+  const __half* k_new;
+  const __half* v_new;
+  int64_t kv_stride;
+  __half* out;
+  int rows;        // query rows of a unit (16 to 256, a power of two)
+  int tile_shift;  // log2 of the positions of a tile
+  float* part_o;    // [N][2][rows][HD]
+  float2* part_ml;  // [N][2][rows]
+  uint32_t* part_err;  // [N]: 1 if the CTA gave up on a wait
+  int32_t* status;
+};
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// the cut of the work
+// ---------------------------------------------------------------------------
+// One sequence: its tiles are the sink tiles below the window, the tiles from
+// the window's first position to the last, and the tree's own.
+struct SeqInfo {
+  int slot, len, m;
+  int lo;       // first position that some node's window reaches
+  int sinks;    // positions of the prefix that stay visible under a window
+  int w_tile;   // tile of lo
+  int n_sink;   // sink tiles in front of it
+  int tiles;
+  int units;    // kv heads x row blocks
+  int bad;      // status bits of what is checked here
+  __device__ __forceinline__ long long work() const { return (long long)units * tiles; }
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const TreeArgs& a, int s, int rows, int tile_shift) {
+  SeqInfo q;
+  q.slot = a.slots[s];
+  q.m = a.n_nodes != nullptr ? a.n_nodes[s] : a.nt;
+  q.bad = 0;
+  q.len = 0;
+  if (q.slot < 0 || q.slot >= a.n_slots) {
+    q.bad |= SPEC_ST_SLOT;
+  } else {
+    q.len = a.len[q.slot];
+    if (q.len < 0 || q.len > a.max_pages * a.page_size) q.bad |= SPEC_ST_PAGE;
+  }
+  if (q.m < 0 || q.m > a.nt) q.bad |= SPEC_ST_TREE;
+  if (q.bad != 0) q.len = q.m = 0;
+  q.lo = a.window > 0 ? max(0, q.len - a.window + 1) : 0;
+  q.sinks = a.window > 0 ? min(a.sinks, q.len) : 0;
+  const int up = (1 << tile_shift) - 1, end = (q.len + up) >> tile_shift;
+  q.w_tile = q.lo < q.len ? q.lo >> tile_shift : end;
+  q.n_sink = min((q.sinks + up) >> tile_shift, q.w_tile);
+  q.tiles = q.n_sink + (end - q.w_tile) + 1;
+  q.units = q.m > 0 ? a.nkv * ((q.m * a.G + rows - 1) / rows) : 0;
+  return q;
+}
+
+// Exclusive sum over the CTA's threads; *total: the whole.
+template <int THREADS>
+__device__ __forceinline__ long long block_excl(long long v, long long* s_part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_part[warp] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; w++) {
+    if (w < warp) before += s_part[w];
+    all += s_part[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// Tiles of a CTA: CTA b takes [b * share, (b + 1) * share) of the total.
+__device__ __forceinline__ long long share_of(long long total, int n) {
+  return (long long)(((unsigned long long)total + n - 1) / (unsigned)n);
+}
+
+// Finds this CTA's first tile: the sequence (*seq, *off tiles into its work)
+// that holds tile b * share; returns its tiles' range, empty if it has none.
+struct Range {
+  long long w0, w1;
+};
+template <int THREADS>
+__device__ __forceinline__ Range find_range(const TreeArgs& a, int rows, int tile_shift,
+                                            long long* s_part, int* s_seq, long long* s_off) {
+  long long total = 0, mine = 0, excl = 0, chunk = 0;
+  const int tid = threadIdx.x;
+  for (int base = 0; base < a.n_seq; base += THREADS) {
+    mine = base + tid < a.n_seq ? seq_info(a, base + tid, rows, tile_shift).work() : 0;
+    excl = block_excl<THREADS>(mine, s_part, &chunk);
+    total += chunk;
+  }
+  const long long share = share_of(total, gridDim.x);
+  Range r;
+  r.w0 = share * blockIdx.x;
+  r.w1 = min(total, r.w0 + share);
+  if (r.w0 >= r.w1) return r;
+  long long first = 0;
+  for (int base = 0; base < a.n_seq; base += THREADS) {
+    if (a.n_seq > THREADS) {
+      mine = base + tid < a.n_seq ? seq_info(a, base + tid, rows, tile_shift).work() : 0;
+      excl = block_excl<THREADS>(mine, s_part, &chunk);
+    }
+    if (first + excl <= r.w0 && r.w0 < first + excl + mine) {
+      *s_seq = base + tid;
+      *s_off = r.w0 - first - excl;
+    }
+    first += chunk;
+  }
+  __syncthreads();
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// the tree of one sequence: every node's ancestors (with itself) and depth
+// ---------------------------------------------------------------------------
+struct TreeSmem {
+  unsigned long long anc[SPEC_MAX_TREE];
+  signed char depth[SPEC_MAX_TREE];
+  signed char par[SPEC_MAX_TREE];
+};
+
+// Every thread of the CTA; returns whether the parents make a tree.
+__device__ __forceinline__ bool load_tree(const TreeArgs& a, int s, int m, TreeSmem& t) {
+  const int i = threadIdx.x;
+  bool bad = false;
+  __syncthreads();  // the last sequence's tree is no longer read
+  if (i < SPEC_MAX_TREE) {
+    int p = -1;
+    if (i < m) {
+      p = a.parents != nullptr ? a.parents[(int64_t)s * a.nt + i] : i - 1;
+      bad = p < -1 || p >= i;
+    }
+    t.par[i] = (signed char)(bad ? -1 : p);
+  }
+  const bool any = __syncthreads_or(bad);
+  if (i < m) {
+    unsigned long long set = 1ull << i;
+    int d = 0;
+    for (int p = t.par[i]; p >= 0; p = t.par[p]) {
+      set |= 1ull << p;
+      d++;
+    }
+    t.anc[i] = set;
+    t.depth[i] = (signed char)d;
+  }
+  __syncthreads();
+  return !any;
+}
+
+}  // namespace
+
+// The kernel for many query rows a kv head (tree_attn_tc.cu): CTAs it runs
+// on, rows of a unit, and the launch of its main kernel.
+int tree_tc_rows(int M);
+int tree_tc_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st);
+void tree_tc_init_attrs();
