@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libspecverify.so")
 SOURCES = ["api.cu", "linear.cu", "tcgemm.cu", "attn.cu", "ops.cu", "accept.cu", "depth.cu",
-           "pages.cu", "tree_attn.cu", "sample.cu"]
+           "pages.cu", "tree_attn.cu", "tree_attn_tc.cu", "sample.cu"]
 # host code whose doubles must be rounded operation by operation
 FILE_FLAGS = {"depth.cu": ["-Xcompiler", "-ffp-contract=off"]}
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "tc_ops.cuh"),

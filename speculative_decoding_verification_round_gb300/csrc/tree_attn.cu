@@ -549,7 +549,10 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
     *reinterpret_cast<__half2*>(dst + d) = __floats2half2_rn(o[d] * inv, o[d + 1] * inv);
 }
 
-int rows_of(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+// Query rows of a unit.  Up to 32 rows run on the mma.sync kernel, more on
+// the tcgen05 one with 128 rows, or 256 shared by one read of the cache.
+int rows_of(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 128 ? 128 : 256; }
+bool on_tc(int rows) { return rows >= 128; }
 
 template <int HD, int MT, int RTW>
 cudaError_t launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
@@ -559,9 +562,9 @@ cudaError_t launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
 
 template <int HD>
 int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  cudaError_t e = a.rows == 16   ? launch_shape<HD, 1, 1>(a, n_cta, st)
-                  : a.rows == 32 ? launch_shape<HD, 2, 1>(a, n_cta, st)
-                                 : launch_shape<HD, 2, 2>(a, n_cta, st);
+  cudaError_t e = on_tc(a.rows)  ? tree_tc_launch(a, HD, n_cta, st)
+                  : a.rows == 16 ? launch_shape<HD, 1, 1>(a, n_cta, st)
+                                 : launch_shape<HD, 2, 1>(a, n_cta, st);
   if (e == cudaSuccess) {
     const int blocks = (a.nt * a.nq + TJ_ROWS - 1) / TJ_ROWS;
     cudaLaunchAttribute at[1];
@@ -592,8 +595,8 @@ int device_sms() {
   return n > 0 ? n : 1;
 }
 
-// Two CTAs an SM are resident at once.
-int tree_ctas() { return 2 * device_sms(); }
+// The resident CTAs: two an SM, or one.
+int tree_ctas(int rows) { return (on_tc(rows) ? 1 : 2) * device_sms(); }
 
 int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
   int rc = check_pages(kv, true);
@@ -615,17 +618,17 @@ int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
 void tree_init_attrs() {
   init_shape<64, 1, 1>();
   init_shape<64, 2, 1>();
-  init_shape<64, 2, 2>();
   init_shape<128, 1, 1>();
   init_shape<128, 2, 1>();
-  init_shape<128, 2, 2>();
+  tree_tc_init_attrs();
 }
 
 int tree_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads, size_t* bytes) {
   const int rc = check_tree(kv, n_seq, nt, n_q_heads);
   if (rc != SPEC_OK) return rc;
   const size_t rows = rows_of(nt * (n_q_heads / kv->n_kv_heads));
-  *bytes = (size_t)tree_ctas() * 2 * rows * (sizeof(float) * kv->head_dim + sizeof(float2));
+  const size_t n = tree_ctas((int)rows);
+  *bytes = n * 2 * rows * (sizeof(float) * kv->head_dim + sizeof(float2)) + n * sizeof(uint32_t);
   return SPEC_OK;
 }
 
@@ -662,11 +665,11 @@ int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint1
   a.kv_stride = kv_stride != 0 ? kv_stride : (int64_t)a.nkv * kv->head_dim;
   a.out = reinterpret_cast<__half*>(out);
   a.status = status;
-  const int n_cta = tree_ctas();
   const size_t rows = a.rows = rows_of(a.nt * a.G);
-  a.tile_shift = TT_SHIFT;
-  a.part_err = nullptr;
+  const int n_cta = tree_ctas(a.rows);
+  a.tile_shift = on_tc(a.rows) ? TREE_TC_SHIFT : TT_SHIFT;
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)n_cta * 2 * rows * kv->head_dim);
+  a.part_err = on_tc(a.rows) ? reinterpret_cast<uint32_t*>(a.part_ml + (size_t)n_cta * 2 * rows) : nullptr;
   return kv->head_dim == 128 ? launch_hd<128>(a, n_cta, st) : launch_hd<64>(a, n_cta, st);
 }

@@ -177,8 +177,8 @@ __device__ __forceinline__ bool load_tree(const TreeArgs& a, int s, int m, TreeS
 
 }  // namespace
 
-// The kernel for many query rows a kv head (tree_attn_tc.cu): CTAs it runs
-// on, rows of a unit, and the launch of its main kernel.
-int tree_tc_rows(int M);
-int tree_tc_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st);
+// The kernel for many query rows a kv head (tree_attn_tc.cu): a.rows 128 or
+// 256, tiles of 128 positions, one CTA an SM.
+constexpr int TREE_TC_SHIFT = 7;
+cudaError_t tree_tc_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st);
 void tree_tc_init_attrs();

@@ -89,7 +89,10 @@ class Case:
         2^-23, of the sum of magnitudes a step, then two roundings), which
         moves every weight by a factor within exp(+-2 ds); exp2 and the hi + lo
         split of the weights, 2^-20; and fp32 sums over the keys, one unit per
-        step of 8 keys: all times the |v| average of the row."""
+        step of 8 keys: all times the |v| average of the row.  With more than
+        32 query rows a kv head the weights are rounded once to fp16: half a
+        step, 2^-11, or 2^-25 below the normals, where a row's largest weight
+        is at least 2^6."""
         for b in range(self.n) if seqs is None else seqs:
             m = int(self.counts[b])
             assert (got[b, m:] == np.float16(7.0)).all(), b  # rows of no node
@@ -101,6 +104,8 @@ class Case:
             scale = self.scale or self.hd ** -0.5
             ds = (self.hd + 4) * 2.0 ** -23 * abs(scale) * dots
             rel = np.expm1(2 * ds) + 2.0 ** -20 + ((self.lens[b] + m) / 8 + 64) * 2.0 ** -23
+            if self.nt * self.nq // self.nkv > 32:
+                rel = rel + 2.0 ** -11 + (self.lens[b] + m) * 2.0 ** -31
             bound = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 1.01 * rel[..., None] * mag
             err = np.abs(got[b, :m].astype(np.float64) - ref)
             assert np.isfinite(got[b, :m]).all() and (err <= bound).all(), (b, float(np.max(err - bound)))
