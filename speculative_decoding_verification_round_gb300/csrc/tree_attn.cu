@@ -90,19 +90,18 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ TreeSmem s_tree;
   __shared__ long long s_part[TT_THREADS / 32];
-  __shared__ long long s_off;
-  __shared__ int s_seq;
+  __shared__ Start s_at;
   grid_dep_launch();  // the joining kernel may get ready
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int kg = warp % KG, rw = warp / KG;  // this warp's key group and row block
 
-  const Range range = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, s_part, &s_seq, &s_off);
+  const Range range = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, s_part, &s_at);
   const long long w0 = range.w0, w1 = range.w1;
   if (w0 >= w1) return;
-  int s = s_seq;
-  long long off = s_off;
-  SeqInfo q = seq_info(a, s, ROWS, TT_SHIFT);
+  int s = s_at.s;
+  long long off = s_at.off;
+  SeqInfo q = s_at.q;
   load_tree(a, s, q.m, s_tree);
 
   const uint32_t sm0 = smem_u32(smem), qs0 = sm0 + (uint32_t)Sh::Q_OFF;
@@ -116,7 +115,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
       if (q.work() > 0) load_tree(a, s, q.m, s_tree);
       continue;
     }
-    const int unit = (int)(off / q.tiles), t0 = (int)(off % q.tiles);
+    const int unit = (int)div_ll(off, q.tiles), t0 = (int)(off - (long long)unit * q.tiles);
     const int t1 = (int)min((long long)q.tiles, t0 + (w1 - w));
     const int kvh = unit % a.nkv, row0 = unit / a.nkv * ROWS, M = q.m * a.G;
 
@@ -475,15 +474,15 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
   const int kvh = h / a.G, m = node * a.G + h % a.G, r = m & (a.rows - 1);
   const long long u0 = before + (long long)(m / a.rows * a.nkv + kvh) * q.tiles, u1 = u0 + q.tiles;
   const bool live = st == 0 && e < rows * a.nq;
-  const int b0 = live ? (int)((unsigned long long)u0 / (unsigned long long)share) : 0;
-  const int b1 = live ? (int)((unsigned long long)(u1 - 1) / (unsigned long long)share) : 0;
+  const int b0 = live ? (int)div_ll(u0, share) : 0;
+  const int b1 = live ? (int)div_ll(u1 - 1, share) : 0;
   grid_dep_wait();
   if (a.part_err != nullptr) {  // CTAs that gave up on a wait
     bool gave_up = false;
     if (live)
       for (int b = b0 + lane; b <= b1; b += 32) gave_up |= __ldcg(a.part_err + b) != 0u;
     if (blk == 0 && st == 0) {  // the status speaks for every row
-      const long long f0 = before / share, f1 = (before + max(q.work(), 1ll) - 1) / share;
+      const long long f0 = div_ll(before, share), f1 = div_ll(before + max(q.work(), 1ll) - 1, share);
       for (long long b = f0 + tid; b <= f1 && b < n_cta; b += TJ_THREADS) gave_up |= __ldcg(a.part_err + b) != 0u;
       if (__syncthreads_or(gave_up)) st |= SPEC_ST_TIMEOUT;
     } else if (__any_sync(0xffffffffu, gave_up)) {
@@ -550,9 +549,11 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
 }
 
 // Query rows of a unit.  Up to 32 rows run on the mma.sync kernel, more on
-// the tcgen05 one with 128 rows, or 256 shared by one read of the cache.
-int rows_of(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 128 ? 128 : 256; }
-bool on_tc(int rows) { return rows >= 128; }
+// the tcgen05 one with 64, 128 or 256 that share one read of the cache.
+int rows_of(int M) {
+  return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+}
+bool on_tc(int rows) { return rows >= 64; }
 
 template <int HD, int MT, int RTW>
 cudaError_t launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {

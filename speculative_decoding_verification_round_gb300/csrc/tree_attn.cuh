@@ -97,23 +97,42 @@ __device__ __forceinline__ long long block_excl(long long v, long long* s_part, 
   return before + x - v;
 }
 
-// Tiles of a CTA: CTA b takes [b * share, (b + 1) * share) of the total.
-__device__ __forceinline__ long long share_of(long long total, int n) {
-  return (long long)(((unsigned long long)total + n - 1) / (unsigned)n);
+// a / b for non-negative values: 64-bit division is a long subroutine, and
+// all but enormous calls have less than 2^32 tiles.
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  if ((((unsigned long long)a | (unsigned long long)b) >> 32) == 0)
+    return (long long)((unsigned)a / (unsigned)b);
+  return a / b;
 }
 
-// Finds this CTA's first tile: the sequence (*seq, *off tiles into its work)
-// that holds tile b * share; returns its tiles' range, empty if it has none.
+// Tiles of a CTA: CTA b takes [b * share, (b + 1) * share) of the total.
+__device__ __forceinline__ long long share_of(long long total, int n) {
+  return div_ll(total + n - 1, n);
+}
+
+// Finds this CTA's first tile: the sequence that holds tile b * share (and
+// how far into its work) goes to *at; returns its tiles' range, empty if it
+// has none.
 struct Range {
   long long w0, w1;
 };
+struct Start {
+  SeqInfo q;
+  long long off;
+  int s;
+};
 template <int THREADS>
 __device__ __forceinline__ Range find_range(const TreeArgs& a, int rows, int tile_shift,
-                                            long long* s_part, int* s_seq, long long* s_off) {
+                                            long long* s_part, Start* at) {
   long long total = 0, mine = 0, excl = 0, chunk = 0;
   const int tid = threadIdx.x;
+  SeqInfo q;
   for (int base = 0; base < a.n_seq; base += THREADS) {
-    mine = base + tid < a.n_seq ? seq_info(a, base + tid, rows, tile_shift).work() : 0;
+    mine = 0;
+    if (base + tid < a.n_seq) {
+      q = seq_info(a, base + tid, rows, tile_shift);
+      mine = q.work();
+    }
     excl = block_excl<THREADS>(mine, s_part, &chunk);
     total += chunk;
   }
@@ -125,12 +144,17 @@ __device__ __forceinline__ Range find_range(const TreeArgs& a, int rows, int til
   long long first = 0;
   for (int base = 0; base < a.n_seq; base += THREADS) {
     if (a.n_seq > THREADS) {
-      mine = base + tid < a.n_seq ? seq_info(a, base + tid, rows, tile_shift).work() : 0;
+      mine = 0;
+      if (base + tid < a.n_seq) {
+        q = seq_info(a, base + tid, rows, tile_shift);
+        mine = q.work();
+      }
       excl = block_excl<THREADS>(mine, s_part, &chunk);
     }
     if (first + excl <= r.w0 && r.w0 < first + excl + mine) {
-      *s_seq = base + tid;
-      *s_off = r.w0 - first - excl;
+      at->q = q;
+      at->off = r.w0 - first - excl;
+      at->s = base + tid;
     }
     first += chunk;
   }

@@ -6,12 +6,12 @@
 // mma.sync (about a quarter of tcgen05's rate) cannot keep up with the HBM.
 // One CTA per SM holds 128 or 256 rows against tiles of 128 positions, in
 // roles that only meet at mbarriers:
-//   warps 8, 9   gather the positions' K and V rows through the page table
-//                into a ring of five 128-position buffers (16-byte cp.async,
-//                written in the MMA's 128-byte-swizzled layout; K as a
-//                K-major operand, V as an MN-major one, so that neither is
-//                transposed)
-//   warp 10      one thread issues S_j = Q_j K^T and O_j += P_j V
+//   warps 8-11   gather the positions' rows through the page table, two
+//                warps K's and two V's, into a ring of five 128-position
+//                buffers (16-byte cp.async, written in the MMA's
+//                128-byte-swizzled layout; K as a K-major operand, V as an
+//                MN-major one, so that neither is transposed)
+//   warp 12      one thread issues S_j = Q_j K^T and O_j += P_j V
 //   warps 0-3, 4-7  two streams j = 0, 1: a thread owns a row; it reads its
 //                scores from tensor memory, keeps the running maximum and sum
 //                in fp32 (log2 domain) and writes P back as fp16, over the
@@ -19,7 +19,9 @@
 // The streams keep the tensor core busy while the other one is in its
 // softmax: with 256 rows they are the two row halves of every tile, with up
 // to 128 they take the even and the odd tiles of the same rows, each with its
-// own (max, sum, O), joined at the end.
+// own (max, sum, O), joined at the end.  With up to 64 the rows stand in the
+// Q tile twice, stream 0 has those of lanes 0-63 and stream 1 those of lanes
+// 64-127, so that the four SM sub-partitions share the softmax evenly.
 //
 // O is only rescaled when a row's maximum has grown by more than 2^8 since
 // the last time (the weights may exceed 1 until then, by less than fp16's
@@ -40,9 +42,12 @@ namespace {
 
 constexpr int TC_SHIFT = TREE_TC_SHIFT, TC_KEYS = 1 << TC_SHIFT;
 constexpr int TC_RING = 5;
-constexpr int TC_THREADS = 384;
-constexpr int PROD_WARP = 8, MMA_WARP = 10, ALLOC_WARP = 11;
-constexpr int PROD_THREADS = 64;
+constexpr int TC_THREADS = 512;
+constexpr int PROD_WARP = 8, MMA_WARP = 12, ALLOC_WARP = 13;
+constexpr int PROD_THREADS = 64;  // of K's loads, and of V's
+// Registers a thread: the softmax keeps a row's 128 scores.  Both pairs of
+// warpgroups together hold the 512 x 128 of the launch.
+constexpr int REGS_SOFTMAX = 200, REGS_OTHER = 56;
 constexpr float P_BIAS = 6.0f;   // log2 of the factor of weights and sum
 constexpr float P_SLACK = 8.0f;  // growth of the maximum before O is rescaled
 
@@ -56,22 +61,21 @@ struct TcShape {
 
 struct TcSmall {
   unsigned long long full[TC_RING], empty[TC_RING];
-  unsigned long long q_full, q_empty, drain;
+  unsigned long long q_full, drain;
   unsigned long long s_full[2], p_ready[2], o_done[2];
   unsigned long long bad[TC_RING][2];  // rows of a masked V tile with a non-finite chunk
   long long part[TC_THREADS / 32];
-  long long off;
-  int seq;
+  Start at;
   uint32_t tmem;
   int abort;
   signed char depth[2][SPEC_MAX_TREE];
-  float2 x_ml[128];
+  float2 x_ml[2][128];
 };
-constexpr int SMALL_MAX = 2048;
+constexpr int SMALL_MAX = 3072;
 static_assert(sizeof(TcSmall) <= SMALL_MAX, "behind the tiles");
 template <int HD>
-constexpr size_t tc_smem() {  // the tiles start at a multiple of 1024 bytes
-  return (size_t)TcShape<HD>::END + SMALL_MAX + 1024;
+constexpr size_t tc_smem() {
+  return (size_t)TcShape<HD>::END + SMALL_MAX;
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
@@ -166,25 +170,41 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t lead) {
          (1ull << 46) | (2ull << 61);
 }
 
+// --- two floats at a time ------------------------------------------------------
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
 // Bits [0, n) of 32.
 __device__ __forceinline__ uint32_t low_bits(long long n) {
   return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << (int)n) - 1u;
 }
 
-template <int HD, bool TWO>
+template <int HD, int ROWS>
 __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeArgs a) {
   using Sh = TcShape<HD>;
-  constexpr int ROWS = TWO ? 256 : 128, UNITS = HD / 8, CH = HD / 32;
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw0 = smem_u32(smem_raw), sm0 = (raw0 + 1023u) & ~1023u;
-  unsigned char* smem = smem_raw + (sm0 - raw0);
+  constexpr bool TWO = ROWS == 256;
+  constexpr int UNITS = HD / 8, CH = HD / 32;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sm0 = smem_u32(smem);
   TcSmall& sh = *reinterpret_cast<TcSmall*>(smem + Sh::END);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_launch();  // the joining kernel may get ready
-  const Range range = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, sh.part, &sh.seq, &sh.off);
+  const Range range = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, sh.part, &sh.at);
   const long long w0 = range.w0, w1 = range.w1;
-  if (w0 >= w1) {
-    if (tid == 0) a.part_err[blockIdx.x] = 0u;
+  if (w0 >= w1 || (sm0 & 1023u) != 0u) {  // no tiles (a base off the swizzle's atoms never happens)
+    if (tid == 0) a.part_err[blockIdx.x] = w0 < w1;
     return;
   }
   auto bar = [&](unsigned long long& b) { return smem_u32(&b); };
@@ -193,8 +213,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       mbar_init(bar(sh.full[i]), PROD_THREADS);
       mbar_init(bar(sh.empty[i]), 1);
     }
-    mbar_init(bar(sh.q_full), PROD_THREADS);
-    mbar_init(bar(sh.q_empty), 256);
+    mbar_init(bar(sh.q_full), 256);
     mbar_init(bar(sh.drain), 1);
     for (int j = 0; j < 2; j++) {
       mbar_init(bar(sh.s_full[j]), 1);
@@ -224,9 +243,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   auto item_k = [](int i) { return TWO ? 2 * i : (i == 0 ? 0 : 2 * i - 1); };
   auto item_v = [](int i, int n) { return TWO ? 2 * i + 1 : min(2 * i + 2, 2 * n - 1); };
 
-  int s = sh.seq;
-  long long off = sh.off;
-  SeqInfo q = seq_info(a, s, ROWS, TC_SHIFT);
+  int s = sh.at.s;
+  long long off = sh.at.off;
+  SeqInfo q = sh.at.q;
   uint32_t item0 = 0, seg = 0;  // ring items and pieces before this one
   // what a piece is
   int t0 = 0, n = 0, kvh = 0, row0 = 0, M = 0;
@@ -236,8 +255,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       off = 0;
       q = seq_info(a, s, ROWS, TC_SHIFT);
     }
-    const int unit = (int)(off / q.tiles);
-    t0 = (int)(off % q.tiles);
+    const int unit = (int)div_ll(off, q.tiles);
+    t0 = (int)(off - (long long)unit * q.tiles);
     n = (int)min((long long)(q.tiles - t0), w1 - w);
     kvh = unit % a.nkv;
     row0 = unit / a.nkv * ROWS;
@@ -251,62 +270,80 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
            (a.window > 0 && base + TC_KEYS > q.sinks && base < q.lo + SPEC_MAX_TREE);
   };
 
-  if (warp >= PROD_WARP && warp < PROD_WARP + 2) {
+  if (warp >= PROD_WARP && warp < PROD_WARP + 4) {
     // ======================================================= the loads
-    const int pw = warp - PROD_WARP;                 // rows 64 pw .. 64 pw + 63 of a tile
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    const bool is_k = warp < PROD_WARP + 2;
+    const int pw = warp & 1;                         // rows 64 pw .. 64 pw + 63 of a tile
     constexpr int RPP = 32 / UNITS, PASSES = 64 / RPP;  // rows a pass of the warp
     const int u = lane % UNITS, sub = lane / UNITS;
-    auto dst_off = [&](int r) { return (uint32_t)((u >> 3) * Sh::SUB) + sw128_off(r, u & 7); };
+    // where this lane's chunk of row RPP p + sub goes: the swizzle repeats every 8 rows
+    uint32_t dst8[8 / RPP];
+#pragma unroll
+    for (int p = 0; p < 8 / RPP; p++)
+      dst8[p] = (uint32_t)((u >> 3) * Sh::SUB) + sw128_off(64 * pw + RPP * p + sub, u & 7);
+    auto dst_off = [&](int p) { return dst8[p % (8 / RPP)] + (uint32_t)(p / (8 / RPP)) * 1024u; };
+    const __half* pool = (is_k ? a.k : a.v) + u * 8;
+    const __half* fresh = (is_k ? a.k_new : a.v_new) + u * 8;
+    struct Rows {
+      uint32_t at[2];  // cache rows of the tile's rows lane and lane + 32 of the warp's 64
+    };
+    auto lookup = [&](int t) {
+      Rows x = {{~0u, ~0u}};
+      if (t == q.tiles - 1) return x;
+      const int base = tile_base(t) + 64 * pw + lane;
+      const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int pos = base + 32 * h;
+        if (pos < q.len) {
+          const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+          const int pg = __ldg(row + e);
+          if (pg >= 0 && pg < a.n_pages)
+            x.at[h] = ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
+        }
+      }
+      return x;
+    };
     for (long long w = w0; w < w1; w += n, off += n, item0 += 2 * n, seg++) {
       next_piece(w);
-      auto load = [&](bool is_k, int i, uint32_t item) {
-        const uint32_t slot = item % TC_RING, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
+      // the rows of the next tile are looked up while this one waits for its buffer
+      Rows next = lookup(t0);
+      for (int i = 0; i < n; i++) {
         const int t = t0 + i;
-        const bool tree = t == q.tiles - 1, scan = !is_k && tile_masked(t);
-        // this lane looks up rows lane and lane + 32 of the warp's 64
-        uint32_t idx[2] = {~0u, ~0u};
-        if (!tree) {
-          const int base = tile_base(t);
-          const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
-#pragma unroll
-          for (int j = 0; j < 2; j++) {
-            const int pos = base + 64 * pw + 32 * j + lane;
-            if (pos < q.len) {
-              const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
-              const int pg = __ldg(row + e);
-              if (pg >= 0 && pg < a.n_pages)
-                idx[j] = (uint32_t)((pg * (int64_t)a.nkv + kvh) * a.page_size + (pos - e * a.page_size));
-            }
-          }
-        }
+        const uint32_t item = item0 + (is_k ? item_k(i) : item_v(i, n));
+        const uint32_t slot = item % TC_RING, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
+        const Rows x = next;
+        if (i + 1 < n) next = lookup(t + 1);
         wait(sh.empty[slot], (item / TC_RING) + 1);
-        const __half* src = is_k ? (tree ? a.k_new : a.k) : (tree ? a.v_new : a.v);
-#pragma unroll 8
-        for (int p = 0; p < PASSES; p++) {
-          const int r = RPP * p + sub;
-          bool ok;
-          int64_t at;
-          if (tree) {
-            ok = 64 * pw + r < q.m;
-            at = ((int64_t)s * a.nt + (ok ? 64 * pw + r : 0)) * a.kv_stride + kvh * HD;
-          } else {
-            const uint32_t x = __shfl_sync(0xffffffffu, p < PASSES / 2 ? idx[0] : idx[1], r & 31);
-            ok = x != ~0u;
-            at = ok ? (int64_t)x * HD : 0;
+        if (t == q.tiles - 1) {
+          const __half* src = fresh + (int64_t)s * a.nt * a.kv_stride + kvh * HD;
+#pragma unroll 4
+          for (int p = 0; p < PASSES; p++) {
+            const int r = 64 * pw + RPP * p + sub;
+            const bool ok = r < q.m;
+            cp16(buf + dst_off(p), src + (ok ? r : 0) * a.kv_stride, ok);
           }
-          cp16(buf + dst_off(64 * pw + r), src + at + u * 8, ok);
+        } else {
+#pragma unroll
+          for (int p = 0; p < PASSES; p++) {
+            const uint32_t at = __shfl_sync(0xffffffffu, x.at[p / (PASSES / 2)], (RPP * p + sub) & 31);
+            const bool ok = at != ~0u;
+            cp16(buf + dst_off(p), pool + (uint64_t)(ok ? at : 0u) * HD, ok);
+          }
         }
-        if (!scan) {
+        if (is_k || !tile_masked(t)) {
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(sh.full[slot])) : "memory");
-          return;
+          continue;
         }
         // a masked tile's V: chunks with infinities or NaN, which 0 * inf
         // would spread to rows that do not see them, are taken out here and
         // added by the rows that do
         asm volatile("cp.async.wait_all;" ::: "memory");
         unsigned long long bad = 0ull;
+#pragma unroll 4
         for (int p = 0; p < PASSES; p++) {
-          const uint32_t at = buf + dst_off(64 * pw + RPP * p + sub);
+          const uint32_t at = buf + dst_off(p);
           uint4 v;
           asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
           if (odd_chunk(v)) {
@@ -319,71 +356,54 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         if (lane == 0) sh.bad[slot][pw] = bad;
         fence_proxy_async();
         mbar_arrive(bar(sh.full[slot]));
-      };
-      for (int i = 0; i < min(LA, n); i++) load(true, i, item0 + item_k(i));
-      wait(sh.q_empty, seg + 1);
-      for (int e = tid - PROD_WARP * 32; e < ROWS * UNITS; e += PROD_THREADS) {
-        const int r = e / UNITS, uu = e % UNITS, m = row0 + r;
-        const bool ok = m < M;
-        const int node = ok ? m / a.G : 0, h = kvh * a.G + (ok ? m % a.G : 0);
-        cp16(sm0 + (r >> 7) * Sh::TILE + (uu >> 3) * Sh::SUB + sw128_off(r & 127, uu & 7),
-             a.q + ((int64_t)s * a.nt + node) * a.q_stride + h * HD + uu * 8, ok);
-      }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(sh.q_full)) : "memory");
-      for (int i = 0; i < n; i++) {
-        load(false, i, item0 + item_v(i, n));
-        if (i + LA < n) load(true, i + LA, item0 + item_k(i + LA));
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == MMA_WARP) {
+  } else if (warp >= MMA_WARP) {
     // ======================================================= the products
-    if (lane == 0) {
-      const uint32_t id_s = idesc_f16(TC_KEYS), id_o = idesc_f16(HD) | (1u << 16);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    if (warp == MMA_WARP && lane == 0) {
+      // a negative scale: the scores' sign is turned by the MMA (negated A),
+      // so that a row's maximum is the maximum of what is read
+      const uint32_t id_s = idesc_f16(TC_KEYS) | (a.scale_log2 < 0.0f ? 1u << 13 : 0u);
+      const uint32_t id_o = idesc_f16(HD) | (1u << 16);
       uint32_t n_p[2] = {0, 0};  // tiles of each stream so far
+      auto scores = [&](int j, uint32_t item) {
+        const uint32_t kb = sm0 + Sh::RING_OFF + item % TC_RING * Sh::TILE, qb = sm0 + (TWO ? j * Sh::TILE : 0);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; kk++) {
+          const uint32_t o = (kk >> 2) * Sh::SUB + (kk & 3) * 32;
+          tc_mma(tmem + j * 128, smem_desc_sw128(qb + o), smem_desc_sw128(kb + o), id_s, kk > 0);
+        }
+        tc_commit(bar(sh.s_full[j]));
+      };
+      auto output = [&](int j, uint32_t item) {
+        const uint32_t vb = sm0 + Sh::RING_OFF + item % TC_RING * Sh::TILE;
+#pragma unroll
+        for (int kk = 0; kk < TC_KEYS / 16; kk++)
+          tc_mma_ta(tmem + 256 + j * 128, tmem + j * 128 + 8 * kk, smem_desc_mn(vb + kk * 2048, Sh::SUB),
+                    id_o, 1u);
+      };
+      auto wait_item = [&](uint32_t item) {
+        wait(sh.full[item % TC_RING], item / TC_RING);
+        fence_proxy_async();  // the copies, to the tensor core's proxy
+      };
+      auto release = [&](uint32_t item) { tc_commit(bar(sh.empty[item % TC_RING])); };
       for (long long w = w0; w < w1; w += n, off += n, item0 += 2 * n, seg++) {
         next_piece(w);
-        auto scores = [&](int j, uint32_t item) {
-          const uint32_t kb = sm0 + Sh::RING_OFF + item % TC_RING * Sh::TILE, qb = sm0 + (TWO ? j * Sh::TILE : 0);
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; kk++) {
-            const uint32_t o = (kk >> 2) * Sh::SUB + (kk & 3) * 32;
-            tc_mma(tmem + j * 128, smem_desc_sw128(qb + o), smem_desc_sw128(kb + o), id_s, kk > 0);
-          }
-          tc_commit(bar(sh.s_full[j]));
-        };
-        auto output = [&](int j, uint32_t item) {
-          const uint32_t vb = sm0 + Sh::RING_OFF + item % TC_RING * Sh::TILE;
-#pragma unroll
-          for (int kk = 0; kk < TC_KEYS / 16; kk++)
-            tc_mma_ta(tmem + 256 + j * 128, tmem + j * 128 + 8 * kk, smem_desc_mn(vb + kk * 2048, Sh::SUB),
-                      id_o, 1u);
-        };
-        auto wait_item = [&](uint32_t item) {
-          wait(sh.full[item % TC_RING], item / TC_RING);
-          fence_proxy_async();  // the copies, to the tensor core's proxy
-        };
-        auto release = [&](uint32_t item) { tc_commit(bar(sh.empty[item % TC_RING])); };
         wait(sh.q_full, seg);
         fence_proxy_async();
-        if (TWO) {
-          const uint32_t k0 = item0 + item_k(0);
-          wait_item(k0);
-          scores(0, k0);
-          scores(1, k0);
-          release(k0);
-        } else {
-          for (int i = 0; i < min(2, n); i++) {
-            const uint32_t ki = item0 + item_k(i);
-            wait_item(ki);
-            scores(i, ki);
-            release(ki);
-          }
+        for (int i = 0; i < min(LA, n); i++) {
+          const uint32_t ki = item0 + item_k(i);
+          wait_item(ki);
+          scores(i, ki);
+          if (TWO) scores(1, ki);
+          release(ki);
         }
         for (int i = 0; i < n; i++) {
           const uint32_t vi = item0 + item_v(i, n), kn = item0 + item_k(i + LA);
-          wait_item(vi);
           for (int j = TWO ? 0 : i & 1; j < (TWO ? 2 : (i & 1) + 1); j++) {
+            if (!TWO || j == 0) wait_item(vi);
             wait(sh.p_ready[j], n_p[j]++);
             tc_fence_after();
             output(j, vi);
@@ -401,21 +421,46 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       wait(sh.drain, 0);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else {
     // ======================================================= the softmax
-    const int j = warp >> 2, r = tid & 127;  // stream, row of its 128
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    const int j = warp >> 2, r = tid & 127;  // stream, lane of tensor memory
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + j * 128, tO = tmem + lanes + 256 + j * 128;
-    const bool neg = a.scale_log2 < 0.0f;
+    const float scale = fabsf(a.scale_log2);
     uint32_t n_s = 0, n_o = 0;  // tiles and pieces of this stream so far
     for (long long w = w0; w < w1; w += n, off += n, item0 += 2 * n, seg++) {
       next_piece(w);
       const int nj = TWO ? n : (n - j + 1) / 2;
-      const int m = row0 + (TWO ? 128 * j : 0) + r;
-      const bool live = m < M;
-      const bool warp_live = row0 + (TWO ? 128 * j : 0) + 32 * (warp & 3) < M;
-      // this row's node, its ancestors, its position
-      const int node = live ? m / a.G : 0;
+      // this thread's row of the unit; its chunks of the q tile
+      const int rr = ROWS == 64 ? r & 63 : ROWS == 128 ? r : 128 * j + r;
+      const int m = row0 + rr;
+      const bool in = m < M;
+      const bool live = in && (ROWS != 64 || (r >> 6) == j);
+      const int wr = 32 * (warp & 3);  // the warp's first lane
+      const bool warp_live = ROWS == 64 ? (wr >> 6) == j && row0 + (wr & 63) < M
+                                        : row0 + (TWO ? 128 * j : 0) + wr < M;
+      const int node = in ? m / a.G : 0, head = kvh * a.G + (in ? m - node * a.G : 0);
+      {
+        const __half* src = a.q + ((int64_t)s * a.nt + node) * a.q_stride + head * HD;
+        constexpr int MINE = TWO ? UNITS : UNITS / 2;  // both groups share a tile of one stream's rows
+        const int u0 = TWO ? 0 : j * MINE;
+        const uint32_t qt = sm0 + (TWO ? j * Sh::TILE : 0);
+#pragma unroll
+        for (int x = 0; x < MINE; x++) {
+          const int u = u0 + x;
+          cp16(qt + (u >> 3) * Sh::SUB + sw128_off(r, u & 7), src + u * 8, in);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(sh.q_full)) : "memory");
+      }
+      if (nj > 0) {
+        uint32_t z[32];
+#pragma unroll
+        for (int c = 0; c < 32; c++) z[c] = 0u;
+#pragma unroll
+        for (int c = 0; c < CH; c++) tm_st32(tO + 32 * c, z);
+      }
+      // the row's node's ancestors and position
       auto parent = [&](int i) {
         const int p = a.parents != nullptr ? __ldg(a.parents + (int64_t)s * a.nt + i) : i - 1;
         return p < i ? p : -1;  // (a tree that is none is refused by the joining kernel)
@@ -441,135 +486,121 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         asm volatile("bar.sync %0, 128;" ::"r"(1 + j) : "memory");
       }
       if (!live) anc = 0ull;
-      float mx = -INFINITY, sum = 0.0f;
       __syncwarp();
-      if (nj > 0) {
-        uint32_t z[32];
-#pragma unroll
-        for (int c = 0; c < 32; c++) z[c] = 0u;
-#pragma unroll
-        for (int c = 0; c < CH; c++) tm_st32(tO + 32 * c, z);
-        tm_wait_st();
-      }
+      tm_wait_st();
+      float mx = -INFINITY, sum = 0.0f;
       for (int c = 0; c < nj; c++) {
         const int i = TWO ? c : 2 * c + j, t = t0 + i;
         wait(sh.s_full[j], n_s++);
         __syncwarp();
         tc_fence_after();
         if (warp_live) {
-          const bool tree = t == q.tiles - 1, masked = tile_masked(t);
-          const int base = tree ? 0 : tile_base(t);
-          // bits of the visible keys 32 b .. 32 b + 31
-          auto seen = [&](int b) -> uint32_t {
-            if (tree) return b == 0 ? (uint32_t)anc : b == 1 ? (uint32_t)(anc >> 32) : 0u;
-            const long long p0 = (long long)base + 32 * b;
-            uint32_t v = low_bits(q.len - p0);
-            if (a.window > 0) v &= low_bits(a.sinks - p0) | ~low_bits((long long)pos - a.window + 1 - p0);
-            return v;
-          };
-          uint32_t v[2][32];
-          const float hidden = neg ? INFINITY : -INFINITY;  // before the scale
-          // ---- the tile's maximum
-          float best = hidden;
-          tm_ld32(tS, v[0]);
+          const bool masked = tile_masked(t);
+          uint32_t v[4][32];
 #pragma unroll
-          for (int b = 0; b < 4; b++) {
-            tm_wait_ld(v[b & 1]);
-            if (b < 3) tm_ld32(tS + 32 * (b + 1), v[(b + 1) & 1]);
-            if (masked) {
-              const uint32_t ok = seen(b);
+          for (int b = 0; b < 4; b++) tm_ld32(tS + 32 * b, v[b]);
+#pragma unroll
+          for (int b = 0; b < 4; b++) tm_wait_ld(v[b]);
+          if (masked) {
+            const bool tree = t == q.tiles - 1;
+            const int base = tree ? 0 : tile_base(t);
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+              uint32_t ok;  // bits of the visible keys 32 b .. 32 b + 31
+              if (tree) {
+                ok = b == 0 ? (uint32_t)anc : b == 1 ? (uint32_t)(anc >> 32) : 0u;
+              } else {
+                const long long p0 = (long long)base + 32 * b;
+                ok = low_bits(q.len - p0);
+                if (a.window > 0)
+                  ok &= low_bits(a.sinks - p0) | ~low_bits((long long)pos - a.window + 1 - p0);
+              }
 #pragma unroll
               for (int e = 0; e < 32; e++)
-                if (!((ok >> e) & 1u)) v[b & 1][e] = __float_as_uint(hidden);
-            }
-            float x[4] = {best, best, best, best};
-            if (neg) {
-#pragma unroll
-              for (int e = 0; e < 32; e++) x[e & 3] = fminf(x[e & 3], __uint_as_float(v[b & 1][e]));
-              best = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e++) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[b & 1][e]));
-              best = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                if (!((ok >> e) & 1u)) v[b][e] = __float_as_uint(-INFINITY);
             }
           }
-          const float top = best * a.scale_log2;
+          // ---- the tile's maximum
+          float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int b = 0; b < 4; b++)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              x[b] = fmaxf(x[b], fmaxf(__uint_as_float(v[b][e]), __uint_as_float(v[b][e + 1])));
+          const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
           const bool grow = top > mx + P_SLACK || (mx == -INFINITY && top > -INFINITY);
-          tm_ld32(tS, v[0]);
           if (__any_sync(0xffffffffu, grow)) {
-            tm_wait_ld(v[0]);
             const float alpha = grow ? exp2_fast(mx - top) : 1.0f;  // 0 at first
             if (grow) mx = top;
             sum *= alpha;
             if (c > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int d = 0; d < CH; d++) {
-                tm_ld32(tO + 32 * d, v[1]);
-                tm_wait_ld(v[1]);
+                uint32_t o[32];
+                tm_ld32(tO + 32 * d, o);
+                tm_wait_ld(o);
 #pragma unroll
-                for (int e = 0; e < 32; e++) v[1][e] = __float_as_uint(__uint_as_float(v[1][e]) * alpha);
-                tm_st32(tO + 32 * d, v[1]);
+                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tm_st32(tO + 32 * d, o);
               }
             }
           }
-          // ---- the weights, as fp16 over the scores that have been read
+          // ---- the weights, as fp16 over the scores
           const float shift = P_BIAS - (mx == -INFINITY ? 0.0f : mx);
-          float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const float2 sc2 = make_float2(scale, scale), sh2 = make_float2(shift, shift);
+          float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
           for (int b = 0; b < 4; b++) {
-            tm_wait_ld(v[b & 1]);
-            if (b < 3) tm_ld32(tS + 32 * (b + 1), v[(b + 1) & 1]);
-            if (masked) {
-              const uint32_t ok = seen(b);
-#pragma unroll
-              for (int e = 0; e < 32; e++)
-                if (!((ok >> e) & 1u)) v[b & 1][e] = __float_as_uint(hidden);
-            }
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float p0 = exp2_fast(fmaf(__uint_as_float(v[b & 1][e]), a.scale_log2, shift));
-              const float p1 = exp2_fast(fmaf(__uint_as_float(v[b & 1][e + 1]), a.scale_log2, shift));
-              l[(e >> 1) & 3] += p0 + p1;
-              pk[e >> 1] = pack_f16(p0, p1);
+              const float2 y = fma2(make_float2(__uint_as_float(v[b][e]), __uint_as_float(v[b][e + 1])), sc2, sh2);
+              const float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+              l[(e >> 1) & 1] = add2(l[(e >> 1) & 1], p);
+              pk[e >> 1] = pack_f16(p.x, p.y);
             }
-            tm_st16(tS + 16 * b, pk);  // columns of scores 16 b .. 16 b + 15, read at b / 2
+            tm_st16(tS + 16 * b, pk);
           }
-          sum += (l[0] + l[1]) + (l[2] + l[3]);
+          l[0] = add2(l[0], l[1]);
+          sum += l[0].x + l[0].y;
           tm_wait_st();
           if (masked) {
             const uint32_t item = item0 + item_v(i, n), slot = item % TC_RING;
             wait(sh.full[slot], item / TC_RING);
             __syncwarp();
-            const unsigned long long bad[2] = {sh.bad[slot][0], sh.bad[slot][1]};
-            if ((bad[0] | bad[1]) != 0ull) {
+            if ((sh.bad[slot][0] | sh.bad[slot][1]) != 0ull) {
+              const bool tree = t == q.tiles - 1;
+#pragma unroll 1
               for (int b = 0; b < 2; b++)
-                for (unsigned long long left = bad[b]; left != 0ull; left &= left - 1ull) {
+#pragma unroll 1
+                for (unsigned long long left = sh.bad[slot][b]; left != 0ull; left &= left - 1ull) {
                   const int key = 64 * b + __ffsll((long long)left) - 1;
                   const float p = half_of(tm_ld1(tS + (key >> 1)), key & 1);
                   const __half* src = a.v;
                   if (tree) {
                     src = a.v_new + ((int64_t)s * a.nt + key) * a.kv_stride + kvh * HD;
                   } else {
-                    const int at = base + key, e = at / a.page_size;
+                    const int at = tile_base(t) + key, e = at / a.page_size;
                     src += (((int64_t)a.table[(int64_t)q.slot * a.max_pages + e] * a.nkv + kvh) * a.page_size +
                             (at - e * a.page_size)) * HD;
                   }
+#pragma unroll 1
                   for (int d = 0; d < CH; d++) {
-                    tm_ld32(tO + 32 * d, v[0]);
-                    tm_wait_ld(v[0]);
+                    uint32_t o[32];
+                    tm_ld32(tO + 32 * d, o);
+                    tm_wait_ld(o);
 #pragma unroll
-                    for (int x = 0; x < 4; x++) {
-                      const uint4 vv = *reinterpret_cast<const uint4*>(src + 32 * d + 8 * x);
+                    for (int y = 0; y < 4; y++) {
+                      const uint4 vv = *reinterpret_cast<const uint4*>(src + 32 * d + 8 * y);
                       if (p > 0.0f && odd_chunk(vv)) {
                         const uint32_t ww[4] = {vv.x, vv.y, vv.z, vv.w};
 #pragma unroll
                         for (int e = 0; e < 8; e++)
-                          v[0][8 * x + e] = __float_as_uint(fmaf(p, half_of(ww[e >> 1], e & 1), __uint_as_float(v[0][8 * x + e])));
+                          o[8 * y + e] = __float_as_uint(fmaf(p, half_of(ww[e >> 1], e & 1), __uint_as_float(o[8 * y + e])));
                       }
                     }
                     __syncwarp();
-                    tm_st32(tO + 32 * d, v[0]);
+                    tm_st32(tO + 32 * d, o);
                     tm_wait_st();
                   }
                 }
@@ -587,9 +618,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       }
       const bool whole = t0 == 0 && n == q.tiles;
       const size_t slot = (size_t)blockIdx.x * 2 + (w > w0 ? 1 : 0);
-      const int hd0 = kvh * a.G + (live ? m % a.G : 0);
-      __half* dst = a.out + (((int64_t)s * a.nt + node) * a.nq + hd0) * HD;
-      float* po = a.part_o + (slot * ROWS + (TWO ? 128 * j : 0) + r) * HD;
+      __half* dst = a.out + (((int64_t)s * a.nt + node) * a.nq + head) * HD;
+      float* po = a.part_o + (slot * ROWS + rr) * HD;
       // 32 dimensions of the row, as they are, or times 1 / sum as fp16
       auto put = [&](int d, const uint32_t (&o)[32], float inv) {
         if (!live) return;
@@ -611,8 +641,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
                 make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
       };
-      if (TWO) {
-        if (warp_live) {
+      if (TWO || n == 1) {  // the row's one stream
+        if (warp_live && nj > 0) {
           const float inv = 1.0f / sum;
 #pragma unroll
           for (int d = 0; d < CH; d++) {
@@ -621,59 +651,48 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
             tm_wait_ld(o);
             put(d, o, inv);
           }
-          if (live && !whole) a.part_ml[slot * ROWS + 128 * j + r] = make_float2(mx, sum);
+          if (live && !whole) a.part_ml[slot * ROWS + rr] = make_float2(mx, sum);
         }
+        if (!TWO) asm volatile("bar.sync 3, 256;" ::: "memory");  // both groups write the next q tile
       } else {
-        // stream 1 hands its share to stream 0 through the second q tile,
-        // half of the dimensions at a time: x[dimension][row]
-        float* x = reinterpret_cast<float*>(smem + Sh::TILE);
-        float w_own = 1.0f, w_other = 0.0f;
-        if (j == 1) sh.x_ml[r] = make_float2(mx, sum);
+        // the streams exchange halves: stream j finishes dimensions
+        // [j HD / 2, (j + 1) HD / 2) of every row and hands the others over
+        // through the q tiles (every S is done): x[dimension][row]
+        float* x_out = reinterpret_cast<float*>(smem + j * Sh::TILE);
+        const float* x_in = reinterpret_cast<const float*>(smem + (1 - j) * Sh::TILE);
+        constexpr int XR = ROWS == 64 ? 64 : 128;
+        if (warp_live) {
+          sh.x_ml[j][rr] = make_float2(mx, sum);
 #pragma unroll
-        for (int half = 0; half < 2; half++) {
-          if (n > 1) {
-            if (half == 1) asm volatile("bar.sync 3, 256;" ::: "memory");  // the first half has been read
-            if (j == 1 && warp_live) {
+          for (int d = 0; d < CH / 2; d++) {
+            uint32_t o[32];
+            tm_ld32(tO + 32 * ((1 - j) * (CH / 2) + d), o);
+            tm_wait_ld(o);
 #pragma unroll
-              for (int d = 0; d < CH / 2; d++) {
-                uint32_t o[32];
-                tm_ld32(tO + 32 * (half * (CH / 2) + d), o);
-                tm_wait_ld(o);
-#pragma unroll
-                for (int e = 0; e < 32; e++) x[(32 * d + e) * 128 + r] = __uint_as_float(o[e]);
-              }
-            }
-            asm volatile("bar.sync 3, 256;" ::: "memory");
-          }
-          if (j == 0 && warp_live) {
-            if (half == 0) {
-              const float2 other = n > 1 ? sh.x_ml[r] : make_float2(-INFINITY, 0.0f);
-              const float m2 = fmaxf(mx, other.x), ref = m2 == -INFINITY ? 0.0f : m2;
-              w_own = exp2_fast(mx - ref);
-              w_other = exp2_fast(other.x - ref);
-              sum = sum * w_own + other.y * w_other;
-              mx = m2;
-              if (live && !whole) a.part_ml[slot * ROWS + r] = make_float2(mx, sum);
-            }
-            const float inv = 1.0f / sum;
-#pragma unroll
-            for (int d = 0; d < CH / 2; d++) {
-              uint32_t o[32];
-              tm_ld32(tO + 32 * (half * (CH / 2) + d), o);
-              tm_wait_ld(o);
-#pragma unroll
-              for (int e = 0; e < 32; e++) {
-                float y = __uint_as_float(o[e]) * w_own;
-                if (n > 1) y = fmaf(x[(32 * d + e) * 128 + r], w_other, y);
-                o[e] = __float_as_uint(y);
-              }
-              put(half * (CH / 2) + d, o, inv);
-            }
+            for (int e = 0; e < 32; e++) x_out[(32 * d + e) * XR + rr] = __uint_as_float(o[e]);
           }
         }
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        if (warp_live) {
+          const float2 other = sh.x_ml[1 - j][rr];
+          const float m2 = fmaxf(mx, other.x), ref = m2 == -INFINITY ? 0.0f : m2;
+          const float w_own = exp2_fast(mx - ref), w_other = exp2_fast(other.x - ref);
+          sum = sum * w_own + other.y * w_other;
+          if (live && !whole && j == 0) a.part_ml[slot * ROWS + rr] = make_float2(m2, sum);
+          const float inv = 1.0f / sum;
+#pragma unroll
+          for (int d = 0; d < CH / 2; d++) {
+            uint32_t o[32];
+            tm_ld32(tO + 32 * (j * (CH / 2) + d), o);
+            tm_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; e++)
+              o[e] = __float_as_uint(fmaf(x_in[(32 * d + e) * XR + rr], w_other, __uint_as_float(o[e]) * w_own));
+            put(j * (CH / 2) + d, o, inv);
+          }
+        }
+        asm volatile("bar.sync 3, 256;" ::: "memory");  // read, before the next q tile
       }
-      tc_fence_before();
-      mbar_arrive(bar(sh.q_empty));
     }
   }
   tc_fence_before();
@@ -684,28 +703,36 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   if (tid == 0) a.part_err[blockIdx.x] = sh.abort != 0 ? 1u : 0u;
 }
 
-template <int HD, bool TWO>
+template <int HD, int ROWS>
 cudaError_t launch(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  tree_attn_tc_kernel<HD, TWO><<<n_cta, TC_THREADS, tc_smem<HD>(), st>>>(a);
+  tree_attn_tc_kernel<HD, ROWS><<<n_cta, TC_THREADS, tc_smem<HD>(), st>>>(a);
   return cudaGetLastError();
 }
 
-template <int HD, bool TWO>
+template <int HD>
+cudaError_t launch_rows(const TreeArgs& a, int n_cta, cudaStream_t st) {
+  return a.rows == 64    ? launch<HD, 64>(a, n_cta, st)
+         : a.rows == 128 ? launch<HD, 128>(a, n_cta, st)
+                         : launch<HD, 256>(a, n_cta, st);
+}
+
+template <int HD, int ROWS>
 void init() {
-  cudaFuncSetAttribute(tree_attn_tc_kernel<HD, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaFuncSetAttribute(tree_attn_tc_kernel<HD, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)tc_smem<HD>());
 }
 
 }  // namespace
 
 cudaError_t tree_tc_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st) {
-  if (hd == 128) return a.rows == 256 ? launch<128, true>(a, n_cta, st) : launch<128, false>(a, n_cta, st);
-  return a.rows == 256 ? launch<64, true>(a, n_cta, st) : launch<64, false>(a, n_cta, st);
+  return hd == 128 ? launch_rows<128>(a, n_cta, st) : launch_rows<64>(a, n_cta, st);
 }
 
 void tree_tc_init_attrs() {
-  init<64, false>();
-  init<64, true>();
-  init<128, false>();
-  init<128, true>();
+  init<64, 64>();
+  init<64, 128>();
+  init<64, 256>();
+  init<128, 64>();
+  init<128, 128>();
+  init<128, 256>();
 }
