@@ -11,7 +11,7 @@
 //                buffers (16-byte cp.async, written in the MMA's
 //                128-byte-swizzled layout; K as a K-major operand, V as an
 //                MN-major one, so that neither is transposed)
-//   warp 12      one thread issues S_j = Q_j K^T and O_j += P_j V
+//   warps 12, 13 issue S_j = Q_j K^T and O_j += P_j V, one stream each
 //   warps 0-3, 4-7  two streams j = 0, 1: a thread owns a row; it reads its
 //                scores from tensor memory, keeps the running maximum and sum
 //                in fp32 (log2 domain) and writes P back as fp16, over the
@@ -43,7 +43,7 @@ namespace {
 constexpr int TC_SHIFT = TREE_TC_SHIFT, TC_KEYS = 1 << TC_SHIFT;
 constexpr int TC_RING = 5;
 constexpr int TC_THREADS = 512;
-constexpr int PROD_WARP = 8, MMA_WARP = 12, ALLOC_WARP = 13;
+constexpr int PROD_WARP = 8, MMA_WARP = 12, ALLOC_WARP = 14;
 constexpr int PROD_THREADS = 64;  // of K's loads, and of V's
 // Registers a thread: the softmax keeps a row's 128 scores.  Both pairs of
 // warpgroups together hold the 512 x 128 of the launch.
@@ -61,7 +61,7 @@ struct TcShape {
 
 struct TcSmall {
   unsigned long long full[TC_RING], empty[TC_RING];
-  unsigned long long q_full, drain;
+  unsigned long long q_full, drain[2];
   unsigned long long s_full[2], p_ready[2], o_done[2];
   unsigned long long bad[TC_RING][2];  // rows of a masked V tile with a non-finite chunk
   long long part[TC_THREADS / 32];
@@ -162,6 +162,11 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t tmem_d, uint32_t tmem_a, uint
       "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ bool elect_one() {  // the same lane each time
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0u;
+}
 // MN-major operand, 128-byte swizzle: 64 of the MN dimension are the 128
 // contiguous bytes, 8 of the K dimension an atom of 1024 bytes (stride byte
 // offset), `lead` bytes from one 64 of MN to the next (leading byte offset).
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sm0 = smem_u32(smem);
   TcSmall& sh = *reinterpret_cast<TcSmall*>(smem + Sh::END);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   grid_dep_launch();  // the joining kernel may get ready
   const Range range = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, sh.part, &sh.at);
   const long long w0 = range.w0, w1 = range.w1;
@@ -211,14 +216,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   if (tid == 0) {
     for (int i = 0; i < TC_RING; i++) {
       mbar_init(bar(sh.full[i]), PROD_THREADS);
-      mbar_init(bar(sh.empty[i]), 1);
+      mbar_init(bar(sh.empty[i]), TWO ? 2 : 1);  // the streams that read it
     }
     mbar_init(bar(sh.q_full), 256);
-    mbar_init(bar(sh.drain), 1);
     for (int j = 0; j < 2; j++) {
       mbar_init(bar(sh.s_full[j]), 1);
       mbar_init(bar(sh.p_ready[j]), 128);
       mbar_init(bar(sh.o_done[j]), 1);
+      mbar_init(bar(sh.drain[j]), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sh.abort = 0;
@@ -238,8 +243,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   auto wait = [&](unsigned long long& b, uint32_t parity) {
     if (!mbar_wait(smem_u32(&b), parity & 1u, LIN_WAIT_TRIES, abort_flag)) *abort_flag = 1;
   };
-  // The ring's order: K runs LA tiles ahead of V.
-  constexpr int LA = TWO ? 1 : 2;
+  // The ring's order: K runs one tile ahead of V, two where the streams alternate.
   auto item_k = [](int i) { return TWO ? 2 * i : (i == 0 ? 0 : 2 * i - 1); };
   auto item_v = [](int i, int n) { return TWO ? 2 * i + 1 : min(2 * i + 2, 2 * n - 1); };
 
@@ -361,64 +365,71 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= MMA_WARP) {
     // ======================================================= the products
+    // One warp per stream, which runs as a whole and issues through one
+    // elected lane: with warp-uniform control an MMA of 128 x 128 x 16 issues
+    // in less than the 64 cycles that it takes, under a branch on the lane in
+    // about 110.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-    if (warp == MMA_WARP && lane == 0) {
+    const int j = warp - MMA_WARP;
+    if (j < 2) {
       // a negative scale: the scores' sign is turned by the MMA (negated A),
       // so that a row's maximum is the maximum of what is read
       const uint32_t id_s = idesc_f16(TC_KEYS) | (a.scale_log2 < 0.0f ? 1u << 13 : 0u);
       const uint32_t id_o = idesc_f16(HD) | (1u << 16);
-      uint32_t n_p[2] = {0, 0};  // tiles of each stream so far
-      auto scores = [&](int j, uint32_t item) {
-        const uint32_t kb = sm0 + Sh::RING_OFF + item % TC_RING * Sh::TILE, qb = sm0 + (TWO ? j * Sh::TILE : 0);
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; kk++) {
-          const uint32_t o = (kk >> 2) * Sh::SUB + (kk & 3) * 32;
-          tc_mma(tmem + j * 128, smem_desc_sw128(qb + o), smem_desc_sw128(kb + o), id_s, kk > 0);
-        }
-        tc_commit(bar(sh.s_full[j]));
-      };
-      auto output = [&](int j, uint32_t item) {
-        const uint32_t vb = sm0 + Sh::RING_OFF + item % TC_RING * Sh::TILE;
-#pragma unroll
-        for (int kk = 0; kk < TC_KEYS / 16; kk++)
-          tc_mma_ta(tmem + 256 + j * 128, tmem + j * 128 + 8 * kk, smem_desc_mn(vb + kk * 2048, Sh::SUB),
-                    id_o, 1u);
-      };
+      const uint64_t d_q = smem_desc_sw128(sm0 + (TWO ? j * Sh::TILE : 0));
+      const uint64_t d_k = smem_desc_sw128(sm0 + Sh::RING_OFF), d_v = smem_desc_mn(sm0 + Sh::RING_OFF, Sh::SUB);
+      const uint32_t tS = tmem + j * 128, tO = tmem + 256 + j * 128;
+      uint32_t n_p = 0;  // the stream's tiles so far
       auto wait_item = [&](uint32_t item) {
         wait(sh.full[item % TC_RING], item / TC_RING);
+        __syncwarp();
         fence_proxy_async();  // the copies, to the tensor core's proxy
       };
-      auto release = [&](uint32_t item) { tc_commit(bar(sh.empty[item % TC_RING])); };
+      auto scores = [&](uint32_t item) {
+        const uint64_t dk = d_k + item % TC_RING * (uint32_t)(Sh::TILE >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; kk++) {
+            const uint32_t o = ((kk >> 2) * Sh::SUB + (kk & 3) * 32) >> 4;
+            tc_mma(tS, d_q + o, dk + o, id_s, kk > 0);
+          }
+          tc_commit(bar(sh.s_full[j]));
+          tc_commit(bar(sh.empty[item % TC_RING]));
+        }
+        __syncwarp();
+      };
       for (long long w = w0; w < w1; w += n, off += n, item0 += 2 * n, seg++) {
         next_piece(w);
+        const int step = TWO ? 1 : 2;
+        int i = TWO ? 0 : j;
+        if (i >= n) continue;
         wait(sh.q_full, seg);
-        fence_proxy_async();
-        for (int i = 0; i < min(LA, n); i++) {
-          const uint32_t ki = item0 + item_k(i);
-          wait_item(ki);
-          scores(i, ki);
-          if (TWO) scores(1, ki);
-          release(ki);
-        }
-        for (int i = 0; i < n; i++) {
-          const uint32_t vi = item0 + item_v(i, n), kn = item0 + item_k(i + LA);
-          for (int j = TWO ? 0 : i & 1; j < (TWO ? 2 : (i & 1) + 1); j++) {
-            if (!TWO || j == 0) wait_item(vi);
-            wait(sh.p_ready[j], n_p[j]++);
-            tc_fence_after();
-            output(j, vi);
-            if (i + LA >= n) tc_commit(bar(sh.o_done[j]));  // the stream's last tile
-            if (!TWO || j == 1) release(vi);
-            if (i + LA < n) {
-              if (!TWO || j == 0) wait_item(kn);
-              scores(j, kn);
-              if (!TWO || j == 1) release(kn);
-            }
+        wait_item(item0 + item_k(i));
+        scores(item0 + item_k(i));
+        for (; i < n; i += step) {
+          const uint32_t vi = item0 + item_v(i, n);
+          const uint64_t dv = d_v + vi % TC_RING * (uint32_t)(Sh::TILE >> 4);
+          wait_item(vi);
+          wait(sh.p_ready[j], n_p++);
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < TC_KEYS / 16; kk++)
+              tc_mma_ta(tO, tS + 8 * kk, dv + ((kk * 2048) >> 4), id_o, 1u);
+            tc_commit(bar(sh.empty[vi % TC_RING]));
+            if (i + step >= n) tc_commit(bar(sh.o_done[j]));  // the stream's last tile
+          }
+          __syncwarp();
+          if (i + step < n) {
+            wait_item(item0 + item_k(i + step));
+            scores(item0 + item_k(i + step));
           }
         }
       }
-      tc_commit(bar(sh.drain));
-      wait(sh.drain, 0);
+      if (elect_one()) tc_commit(bar(sh.drain[j]));
+      __syncwarp();
+      wait(sh.drain[j], 0);
     }
     __syncwarp();
   } else {
