@@ -385,8 +385,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
     const bool whole = t0 == 0 && t1 == q.tiles;
     const size_t slot = (size_t)blockIdx.x * 2 + (w > w0 ? 1 : 0);
     for (int e = tid; e < ROWS * UNITS; e += TT_THREADS) {
-      const int r = e / UNITS, u = e % UNITS, m = row0 + r;
-      if (m >= M) break;
+      // rows of the output are contiguous, rows of a piece are neighbours
+      const int r = whole ? e / UNITS : e % ROWS, u = whole ? e % UNITS : e / ROWS, m = row0 + r;
+      if (m >= M) continue;
       const int rb = r / (16 * MT), rl = r % (16 * MT);
       float m2 = -INFINITY;
 #pragma unroll
@@ -413,9 +414,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
         *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + hd) * HD + u * 8) =
             y;
       } else {
-        float* po = a.part_o + (slot * ROWS + r) * HD + u * 8;
-        *reinterpret_cast<float4*>(po) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        *reinterpret_cast<float4*>(po + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        float4* po = reinterpret_cast<float4*>(a.part_o) + (slot * (HD / 4) + 2 * u) * ROWS + r;
+        po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        po[ROWS] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         if (u == 0) a.part_ml[slot * ROWS + r] = make_float2(m2, l);
       }
     }
@@ -425,20 +426,24 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
 }
 
 // ---------------------------------------------------------------------------
-// the joining kernel: one warp per output row at a time, a CTA's rows all of
-// one sequence.  Checks the sequence (slot, length, pages, tree) while the
-// main kernel runs; then joins the pieces of the rows' units in the order of
-// the positions, or writes NaN for a sequence in error.
+// the joining kernel: a CTA has 32 rows (node, head) of one kv head and 32 of
+// their dimensions, a lane a row and 8 dimensions.  Checks the sequence (slot,
+// length, pages, tree) while the main kernel runs; then joins the pieces of
+// the rows' unit in the order of the positions, eight pieces' loads in flight
+// together, or writes NaN for a sequence in error.
 // ---------------------------------------------------------------------------
 constexpr int TJ_THREADS = 128;
-constexpr int TJ_ROWS = TJ_THREADS / 32;  // output rows (node, head) of a CTA
+constexpr int TJ_ROWS = 32, TJ_DIMS = 8 * TJ_THREADS / 32;
 
 template <int HD>
 __global__ void __launch_bounds__(TJ_THREADS)
 tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
   __shared__ TreeSmem s_tree;
   __shared__ long long s_part[TJ_THREADS / 32];
-  const int s = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+  constexpr int SLICES = HD / TJ_DIMS;
+  const int slice = blockIdx.x % SLICES, kvh = blockIdx.x / SLICES % a.nkv;
+  const int blk = blockIdx.x / (SLICES * a.nkv) % blocks, s = blockIdx.x / (SLICES * a.nkv) / blocks;
+  const bool first = slice == 0 && kvh == 0 && blk == 0;  // writes the status
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long total = 0, before = 0;
   for (int base = 0; base < a.n_seq; base += TJ_THREADS) {
@@ -466,86 +471,76 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
     }
     if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
   }
-  const int rows = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
-  // this warp's row: its unit's tiles and the CTAs that hold the first and last
-  constexpr int DPL = HD / 32;  // head dimensions of a lane
-  const int e = blk * TJ_ROWS + warp, node = e / a.nq, h = e % a.nq;
+  const int nodes = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
+  // the rows' unit (one for all of them: blocks do not cross units), its
+  // tiles and the CTAs that hold the first and last
+  const int m = blk * TJ_ROWS + lane, r = m & (a.rows - 1);
   const long long share = max(share_of(total, n_cta), 1ll);
-  const int kvh = h / a.G, m = node * a.G + h % a.G, r = m & (a.rows - 1);
-  const long long u0 = before + (long long)(m / a.rows * a.nkv + kvh) * q.tiles, u1 = u0 + q.tiles;
-  const bool live = st == 0 && e < rows * a.nq;
-  const int b0 = live ? (int)div_ll(u0, share) : 0;
-  const int b1 = live ? (int)div_ll(u1 - 1, share) : 0;
+  const long long u0 = before + (long long)(blk * TJ_ROWS / a.rows * a.nkv + kvh) * q.tiles, u1 = u0 + q.tiles;
+  const bool any = blk * TJ_ROWS < nodes * a.G, live = m < nodes * a.G;
+  const int b0 = st == 0 && any ? (int)div_ll(u0, share) : 0;
+  const int b1 = st == 0 && any ? (int)div_ll(u1 - 1, share) : 0;
   grid_dep_wait();
-  if (a.part_err != nullptr) {  // CTAs that gave up on a wait
+  if (a.part_err != nullptr && st == 0) {  // CTAs that gave up on a wait
     bool gave_up = false;
-    if (live)
-      for (int b = b0 + lane; b <= b1; b += 32) gave_up |= __ldcg(a.part_err + b) != 0u;
-    if (blk == 0 && st == 0) {  // the status speaks for every row
-      const long long f0 = div_ll(before, share), f1 = div_ll(before + max(q.work(), 1ll) - 1, share);
-      for (long long b = f0 + tid; b <= f1 && b < n_cta; b += TJ_THREADS) gave_up |= __ldcg(a.part_err + b) != 0u;
-      if (__syncthreads_or(gave_up)) st |= SPEC_ST_TIMEOUT;
-    } else if (__any_sync(0xffffffffu, gave_up)) {
-      st |= SPEC_ST_TIMEOUT;
+    if (any)
+      for (int b = b0 + tid; b <= b1; b += TJ_THREADS) gave_up |= __ldcg(a.part_err + b) != 0u;
+    if (first && q.work() > 0) {  // the status speaks for every row
+      const long long f1 = div_ll(before + q.work() - 1, share);
+      for (long long b = div_ll(before, share) + tid; b <= f1; b += TJ_THREADS)
+        gave_up |= __ldcg(a.part_err + b) != 0u;
     }
+    if (__syncthreads_or(gave_up)) st |= SPEC_ST_TIMEOUT;
   }
-  if (blk == 0 && tid == 0) a.status[s] = st;
-  if (e >= rows * a.nq) return;
-  __half* dst = a.out + (((int64_t)s * a.nt + node) * a.nq + h) * HD + lane * DPL;
+  if (first && tid == 0) a.status[s] = st;
+  if (!any || (st == 0 && b0 == b1)) return;  // no rows, or whole: written by its CTA
+  const int node = live ? m / a.G : 0, d0 = slice * TJ_DIMS + warp * 8;
+  uint4* dst = reinterpret_cast<uint4*>(
+      a.out + (((int64_t)s * a.nt + node) * a.nq + kvh * a.G + (m - node * a.G)) * HD + d0);
   if (st != 0) {
-#pragma unroll
-    for (int d = 0; d < DPL; d++) dst[d] = __ushort_as_half(0x7FFF);
+    if (live) *dst = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
     return;
   }
-  if (b0 == b1) return;  // whole: written by its CTA
-  // piece of CTA b: its first, unless it began in front of the unit
-  auto slot_of = [&](int b) { return (size_t)b * 2 + (share * b < u0 ? 1 : 0); };
-  float mx = -INFINITY;
-  float2 ml0 = make_float2(-INFINITY, 0.0f);  // of piece b0 + lane
-  if (b0 + lane <= b1) ml0 = __ldcg(a.part_ml + slot_of(b0 + lane) * a.rows + r);
-  mx = ml0.x;
-  for (int b = b0 + 32 + lane; b <= b1; b += 32) mx = fmaxf(mx, __ldcg(a.part_ml + slot_of(b) * a.rows + r).x);
+  const float4* po = reinterpret_cast<const float4*>(a.part_o) + (size_t)(d0 / 4) * a.rows + r;
+  const size_t piece = (size_t)a.rows * (HD / 4);
+  constexpr int U = 8;
+  float mx = -INFINITY, l = 0.0f, o[8] = {};
+  for (int bb = b0; bb <= b1; bb += U) {
+    float2 ml[U];
+    float4 v[U][2];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  float o[DPL] = {}, l = 0.0f;
-  constexpr int U = 8;  // pieces whose loads are in flight together
-  for (int bb = b0; bb <= b1; bb += 32) {
-    const int n = min(32, b1 + 1 - bb);
-    float2 ml = ml0;
-    if (bb > b0) {
-      ml = make_float2(-INFINITY, 0.0f);
-      if (lane < n) ml = __ldcg(a.part_ml + slot_of(bb + lane) * a.rows + r);
-    }
-    const float w = lane < n ? exp2f(ml.x - mx) : 0.0f;
-    for (int j0 = 0; j0 < n; j0 += U) {
-      float2 v[U][DPL / 2];
-#pragma unroll
-      for (int j = 0; j < U; j++)
-        if (j0 + j < n) {
-          const float2* src = reinterpret_cast<const float2*>(
-              a.part_o + (slot_of(bb + j0 + j) * a.rows + r) * HD + lane * DPL);
-#pragma unroll
-          for (int d = 0; d < DPL / 2; d++) v[j][d] = __ldcg(src + d);
-        }
-#pragma unroll
-      for (int j = 0; j < U; j++) {
-        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-        const float lj = __shfl_sync(0xffffffffu, ml.y, (j0 + j) & 31);
-        if (j0 + j < n) {
-          l = fmaf(lj, wj, l);
-#pragma unroll
-          for (int d = 0; d < DPL / 2; d++) {
-            o[2 * d] = fmaf(v[j][d].x, wj, o[2 * d]);
-            o[2 * d + 1] = fmaf(v[j][d].y, wj, o[2 * d + 1]);
-          }
-        }
+    for (int j = 0; j < U; j++) {
+      ml[j] = make_float2(-INFINITY, 0.0f);
+      v[j][0] = v[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (bb + j <= b1 && live) {
+        // piece of CTA b: its first, unless it began in front of the unit
+        const size_t slot = (size_t)(bb + j) * 2 + (share * (bb + j) < u0 ? 1 : 0);
+        ml[j] = __ldcg(a.part_ml + slot * a.rows + r);
+        v[j][0] = __ldcg(po + slot * piece);
+        v[j][1] = __ldcg(po + slot * piece + a.rows);
       }
+    }
+    float m2 = mx;
+#pragma unroll
+    for (int j = 0; j < U; j++) m2 = fmaxf(m2, ml[j].x);
+    const float ref = m2 == -INFINITY ? 0.0f : m2, alpha = exp2_fast(mx - ref);
+    mx = m2;
+    l *= alpha;
+#pragma unroll
+    for (int d = 0; d < 8; d++) o[d] *= alpha;
+#pragma unroll
+    for (int j = 0; j < U; j++) {
+      const float w = exp2_fast(ml[j].x - ref);
+      l = fmaf(ml[j].y, w, l);
+      const float* f = reinterpret_cast<const float*>(v[j]);
+#pragma unroll
+      for (int d = 0; d < 8; d++) o[d] = fmaf(f[d], w, o[d]);
     }
   }
   const float inv = 1.0f / l;
-#pragma unroll
-  for (int d = 0; d < DPL; d += 2)
-    *reinterpret_cast<__half2*>(dst + d) = __floats2half2_rn(o[d] * inv, o[d + 1] * inv);
+  if (live)
+    *dst = make_uint4(pack_f16(o[0] * inv, o[1] * inv), pack_f16(o[2] * inv, o[3] * inv),
+                      pack_f16(o[4] * inv, o[5] * inv), pack_f16(o[6] * inv, o[7] * inv));
 }
 
 // Query rows of a unit.  Up to 32 rows run on the mma.sync kernel, more on
@@ -567,7 +562,7 @@ int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
                   : a.rows == 16 ? launch_shape<HD, 1, 1>(a, n_cta, st)
                                  : launch_shape<HD, 2, 1>(a, n_cta, st);
   if (e == cudaSuccess) {
-    const int blocks = (a.nt * a.nq + TJ_ROWS - 1) / TJ_ROWS;
+    const int blocks = (a.nt * a.G + TJ_ROWS - 1) / TJ_ROWS;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -575,7 +570,7 @@ int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = programmatic_launch() ? 1 : 0;
-    cfg.gridDim = dim3((unsigned)(a.n_seq * blocks));
+    cfg.gridDim = dim3((unsigned)(a.n_seq * blocks * a.nkv * (HD / TJ_DIMS)));
     cfg.blockDim = dim3(TJ_THREADS);
     e = cudaLaunchKernelEx(&cfg, tree_join_kernel<HD>, a, n_cta, blocks);
   }

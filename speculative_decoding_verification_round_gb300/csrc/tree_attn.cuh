@@ -25,7 +25,7 @@ struct TreeArgs {
   __half* out;
   int rows;        // query rows of a unit (16 to 256, a power of two)
   int tile_shift;  // log2 of the positions of a tile
-  float* part_o;    // [N][2][rows][HD]
+  float* part_o;    // [N][2][HD / 4][rows][4]: a lane a row, its stores side by side
   float2* part_ml;  // [N][2][rows]
   uint32_t* part_err;  // [N]: 1 if the CTA gave up on a wait
   int32_t* status;

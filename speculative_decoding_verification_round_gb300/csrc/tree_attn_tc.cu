@@ -629,42 +629,62 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       }
       const bool whole = t0 == 0 && n == q.tiles;
       const size_t slot = (size_t)blockIdx.x * 2 + (w > w0 ? 1 : 0);
-      __half* dst = a.out + (((int64_t)s * a.nt + node) * a.nq + head) * HD;
-      float* po = a.part_o + (slot * ROWS + rr) * HD;
-      // 32 dimensions of the row, as they are, or times 1 / sum as fp16
-      auto put = [&](int d, const uint32_t (&o)[32], float inv) {
-        if (!live) return;
-        if (whole) {
+      // this warp's part of the q tiles, free now, turns rows of lanes into
+      // rows of memory: 32 rows x D dimensions of fp16, 16-byte chunks swizzled
+      const uint32_t turn = sm0 + warp * 32 * HD * 2;
+      auto put_whole = [&](auto&& chunk, int D, int dim0) {  // chunk(c): 8 dimensions of this lane's row
+        const int cr = D / 8, sw = cr >= 8 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
-          for (int x = 0; x < 4; x++) {
-            uint4 y;
-            auto f = [&](int e) { return __uint_as_float(o[8 * x + e]) * inv; };
-            y.x = pack_f16(f(0), f(1));
-            y.y = pack_f16(f(2), f(3));
-            y.z = pack_f16(f(4), f(5));
-            y.w = pack_f16(f(6), f(7));
-            *reinterpret_cast<uint4*>(dst + 32 * d + 8 * x) = y;
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 8; x++)
-            *reinterpret_cast<uint4*>(po + 32 * d + 4 * x) =
-                make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        for (int c = 0; c < cr; c++) {
+          const uint4 y = chunk(c);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(turn + lane * D * 2 + ((c ^ sw) << 4)),
+                       "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
         }
+        __syncwarp();
+        const int row_e = live ? node * a.nq + head : -1;  // this lane's row of the sequence's output
+#pragma unroll
+        for (int p = 0; p < cr; p++) {
+          const int row = p * (32 / cr) + lane / cr, c = lane % cr;
+          const int e = __shfl_sync(0xffffffffu, row_e, row), sw2 = cr >= 8 ? row & 7 : (row >> 1) & 3;
+          uint4 y;
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                       : "r"(turn + row * D * 2 + ((c ^ sw2) << 4)));
+          if (e >= 0)
+            *reinterpret_cast<uint4*>(a.out + ((int64_t)s * a.nt * a.nq + e) * HD + dim0 + 8 * c) = y;
+        }
+      };
+      auto put_piece = [&](int d, const uint32_t (&o)[32]) {  // dimensions 32 d .. 32 d + 31
+        if (!live) return;
+        uint4* po = reinterpret_cast<uint4*>(a.part_o) + (slot * (HD / 4) + 8 * d) * ROWS + rr;
+#pragma unroll
+        for (int x = 0; x < 8; x++)
+          po[x * ROWS] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+      };
+      auto chunk_of = [](const uint32_t (&o)[32], int c, float inv) {
+        auto f = [&](int e) { return __uint_as_float(o[8 * (c & 3) + e]) * inv; };
+        return make_uint4(pack_f16(f(0), f(1)), pack_f16(f(2), f(3)), pack_f16(f(4), f(5)), pack_f16(f(6), f(7)));
       };
       if (TWO || n == 1) {  // the row's one stream
         if (warp_live && nj > 0) {
           const float inv = 1.0f / sum;
+          uint32_t o[CH][32];
 #pragma unroll
-          for (int d = 0; d < CH; d++) {
-            uint32_t o[32];
-            tm_ld32(tO + 32 * d, o);
-            tm_wait_ld(o);
-            put(d, o, inv);
+          for (int d = 0; d < CH; d++) tm_ld32(tO + 32 * d, o[d]);
+#pragma unroll
+          for (int d = 0; d < CH; d++) tm_wait_ld(o[d]);
+          if (whole) {
+            put_whole([&](int c) { return chunk_of(o[c >> 2], c, inv); }, HD, 0);
+          } else {
+#pragma unroll
+            for (int d = 0; d < CH; d++) put_piece(d, o[d]);
+            if (live) a.part_ml[slot * ROWS + rr] = make_float2(mx, sum);
           }
-          if (live && !whole) a.part_ml[slot * ROWS + rr] = make_float2(mx, sum);
         }
-        if (!TWO) asm volatile("bar.sync 3, 256;" ::: "memory");  // both groups write the next q tile
+        // before the next q tile: its loaders have read what they turned
+        if (TWO)
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + j) : "memory");
+        else
+          asm volatile("bar.sync 3, 256;" ::: "memory");
       } else {
         // the streams exchange halves: stream j finishes dimensions
         // [j HD / 2, (j + 1) HD / 2) of every row and hands the others over
@@ -672,15 +692,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         float* x_out = reinterpret_cast<float*>(smem + j * Sh::TILE);
         const float* x_in = reinterpret_cast<const float*>(smem + (1 - j) * Sh::TILE);
         constexpr int XR = ROWS == 64 ? 64 : 128;
+        uint32_t o[CH / 2][32];
         if (warp_live) {
           sh.x_ml[j][rr] = make_float2(mx, sum);
 #pragma unroll
           for (int d = 0; d < CH / 2; d++) {
-            uint32_t o[32];
-            tm_ld32(tO + 32 * ((1 - j) * (CH / 2) + d), o);
-            tm_wait_ld(o);
+            tm_ld32(tO + 32 * ((1 - j) * (CH / 2) + d), o[d]);
+            tm_wait_ld(o[d]);
 #pragma unroll
-            for (int e = 0; e < 32; e++) x_out[(32 * d + e) * XR + rr] = __uint_as_float(o[e]);
+            for (int e = 0; e < 32; e++) x_out[(32 * d + e) * XR + rr] = __uint_as_float(o[d][e]);
           }
         }
         asm volatile("bar.sync 3, 256;" ::: "memory");
@@ -690,19 +710,24 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           const float w_own = exp2_fast(mx - ref), w_other = exp2_fast(other.x - ref);
           sum = sum * w_own + other.y * w_other;
           if (live && !whole && j == 0) a.part_ml[slot * ROWS + rr] = make_float2(m2, sum);
-          const float inv = 1.0f / sum;
 #pragma unroll
           for (int d = 0; d < CH / 2; d++) {
-            uint32_t o[32];
-            tm_ld32(tO + 32 * (j * (CH / 2) + d), o);
-            tm_wait_ld(o);
+            tm_ld32(tO + 32 * (j * (CH / 2) + d), o[d]);
+            tm_wait_ld(o[d]);
 #pragma unroll
             for (int e = 0; e < 32; e++)
-              o[e] = __float_as_uint(fmaf(x_in[(32 * d + e) * XR + rr], w_other, __uint_as_float(o[e]) * w_own));
-            put(j * (CH / 2) + d, o, inv);
+              o[d][e] = __float_as_uint(fmaf(x_in[(32 * d + e) * XR + rr], w_other, __uint_as_float(o[d][e]) * w_own));
+            if (!whole) put_piece(j * (CH / 2) + d, o[d]);
           }
         }
-        asm volatile("bar.sync 3, 256;" ::: "memory");  // read, before the next q tile
+        asm volatile("bar.sync 3, 256;" ::: "memory");  // both halves have been read
+        if (whole) {
+          if (warp_live) {
+            const float inv = 1.0f / sum;
+            put_whole([&](int c) { return chunk_of(o[c >> 2], c, inv); }, HD / 2, j * (HD / 2));
+          }
+          asm volatile("bar.sync 3, 256;" ::: "memory");  // before the next q tile
+        }
       }
     }
   }
