@@ -17,6 +17,8 @@
 // of the positions.
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "tree_attn.cuh"
 
@@ -96,7 +98,12 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
   const int g = lane >> 2, t4 = lane & 3;
   const int kg = warp % KG, rw = warp / KG;  // this warp's key group and row block
 
-  const Range range = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, s_part, &s_at);
+  const int n_cta = gridDim.x - 1;
+  if ((int)blockIdx.x == n_cta) {
+    check_sequences<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part);
+    return;
+  }
+  const Range range = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part, &s_at);
   const long long w0 = range.w0, w1 = range.w1;
   if (w0 >= w1) return;
   int s = s_at.s;
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
         for (int e = tid; e < ROWS * UNITS; e += TT_THREADS) {
           const int r = e / UNITS, u = e % UNITS, m = row0 + r;
           const bool ok = m < M;
-          const int node = ok ? m / a.G : 0, h = kvh * a.G + (ok ? m % a.G : 0);
+          const int node = ok ? node_of(a, m) : 0, h = kvh * a.G + (ok ? m - node * a.G : 0);
           cp16(qs0 + tile_off<HD>(r, u), a.q + ((int64_t)s * a.nt + node) * a.q_stride + h * HD + u * 8, ok);
         }
       }
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         const int m = row0 + (rw * MT + i) * 16 + h * 8 + g;
-        const int node = m < M ? m / a.G : 0;
+        const int node = m < M ? node_of(a, m) : 0;
         pos[i][h] = q.len + s_tree.depth[node];
         anc[i][h] = m < M ? s_tree.anc[node] : 0ull;
         mx[i][h] = -INFINITY;
@@ -410,7 +417,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
         y.y = pack_f16(acc[2] * inv, acc[3] * inv);
         y.z = pack_f16(acc[4] * inv, acc[5] * inv);
         y.w = pack_f16(acc[6] * inv, acc[7] * inv);
-        const int node = m / a.G, hd = kvh * a.G + m % a.G;
+        const int node = node_of(a, m), hd = kvh * a.G + m - node * a.G;
         *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + hd) * HD + u * 8) =
             y;
       } else {
@@ -426,75 +433,50 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
 }
 
 // ---------------------------------------------------------------------------
-// the joining kernel: a CTA has 32 rows (node, head) of one kv head and 32 of
-// their dimensions, a lane a row and 8 dimensions.  Checks the sequence (slot,
-// length, pages, tree) while the main kernel runs; then joins the pieces of
-// the rows' unit in the order of the positions, eight pieces' loads in flight
-// together, or writes NaN for a sequence in error.
+// the joining kernel: a CTA has 32 rows (node, head) of one kv head, a lane a
+// row and 8 dimensions, eight pieces' loads in flight together.  Joins the
+// pieces of the rows' unit in the order of the positions, or writes NaN for a
+// sequence in error.  SPLIT: the CTA has 8 dimensions and its warps a quarter
+// of the pieces each (the kernel for few rows cuts a long context into dozens
+// of pieces: 8 nodes over 4096 positions, 33 pieces, 22 -> 18 us); otherwise
+// 32 dimensions and every warp all pieces (the tcgen05 kernel's few: 12 x 16
+// nodes 37 -> 29 us).
 // ---------------------------------------------------------------------------
-constexpr int TJ_THREADS = 128;
-constexpr int TJ_ROWS = 32, TJ_DIMS = 8 * TJ_THREADS / 32;
+constexpr int TJ_THREADS = 128, TJ_WARPS = TJ_THREADS / 32;
+constexpr int TJ_ROWS = 32;
 
-template <int HD>
+template <int HD, bool SPLIT>
 __global__ void __launch_bounds__(TJ_THREADS)
 tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
-  __shared__ TreeSmem s_tree;
-  __shared__ long long s_part[TJ_THREADS / 32];
-  constexpr int SLICES = HD / TJ_DIMS;
+  __shared__ float s_o[TJ_WARPS][8][TJ_ROWS];
+  __shared__ float2 s_ml[TJ_WARPS][TJ_ROWS];
+  constexpr int SLICES = HD / (SPLIT ? 8 : 8 * TJ_WARPS);
   const int slice = blockIdx.x % SLICES, kvh = blockIdx.x / SLICES % a.nkv;
   const int blk = blockIdx.x / (SLICES * a.nkv) % blocks, s = blockIdx.x / (SLICES * a.nkv) / blocks;
-  const bool first = slice == 0 && kvh == 0 && blk == 0;  // writes the status
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long total = 0, before = 0;
-  for (int base = 0; base < a.n_seq; base += TJ_THREADS) {
-    const long long mine = base + tid < a.n_seq ? seq_info(a, base + tid, a.rows, a.tile_shift).work() : 0;
-    long long chunk;
-    block_excl<TJ_THREADS>(mine, s_part, &chunk);
-    total += chunk;
-    if (s < base) continue;
-    block_excl<TJ_THREADS>(base + tid < s ? mine : 0, s_part, &chunk);
-    before += chunk;
-  }
-  const SeqInfo q = seq_info(a, s, a.rows, a.tile_shift);
-  int st = q.bad;
-  if (st == 0) {
-    if (!load_tree(a, s, q.m, s_tree)) st |= SPEC_ST_TREE;
-    const int held = q.m == 0 || q.len == 0 ? 0 : (q.len - 1) / a.page_size + 1;
-    // with a window, the pages between the sinks and the window may be gone
-    const int e1 = q.sinks > 0 ? (q.sinks - 1) / a.page_size + 1 : 0;
-    const int e0 = q.lo < q.len ? q.lo / a.page_size : held;
-    bool bad = false;
-    for (int e = tid; e < held; e += TJ_THREADS) {
-      if (e >= e1 && e < e0) continue;
-      const int p = a.table[(int64_t)q.slot * a.max_pages + e];
-      bad |= p < 0 || p >= a.n_pages;
-    }
-    if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
-  }
-  const int nodes = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
-  // the rows' unit (one for all of them: blocks do not cross units), its
-  // tiles and the CTAs that hold the first and last
-  const int m = blk * TJ_ROWS + lane, r = m & (a.rows - 1);
-  const long long share = max(share_of(total, n_cta), 1ll);
-  const long long u0 = before + (long long)(blk * TJ_ROWS / a.rows * a.nkv + kvh) * q.tiles, u1 = u0 + q.tiles;
-  const bool any = blk * TJ_ROWS < nodes * a.G, live = m < nodes * a.G;
-  const int b0 = st == 0 && any ? (int)div_ll(u0, share) : 0;
-  const int b1 = st == 0 && any ? (int)div_ll(u1 - 1, share) : 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int m = blk * TJ_ROWS + lane, r = m & (a.rows - 1), node = node_of(a, m);
   grid_dep_wait();
+  const longlong2 p0 = __ldcg(reinterpret_cast<const longlong2*>(a.plan + s));
+  const int4 p1 = __ldcg(reinterpret_cast<const int4*>(a.plan + s) + 1);
+  const long long before = p0.x, share = p0.y;
+  const int tiles = p1.x, nodes = p1.y;
+  int st = p1.z;
+  if (blk * TJ_ROWS >= nodes * a.G) return;
+  const bool live = m < nodes * a.G;
+  // the rows' unit (one for all of them: blocks do not cross units), and the
+  // CTAs that hold its first and last tile
+  const long long u0 = before + (long long)(blk * TJ_ROWS / a.rows * a.nkv + kvh) * tiles, u1 = u0 + tiles;
+  const int b0 = st == 0 ? (int)div_ll(u0, share) : 0, b1 = st == 0 ? (int)div_ll(u1 - 1, share) : 0;
   if (a.part_err != nullptr && st == 0) {  // CTAs that gave up on a wait
     bool gave_up = false;
-    if (any)
-      for (int b = b0 + tid; b <= b1; b += TJ_THREADS) gave_up |= __ldcg(a.part_err + b) != 0u;
-    if (first && q.work() > 0) {  // the status speaks for every row
-      const long long f1 = div_ll(before + q.work() - 1, share);
-      for (long long b = div_ll(before, share) + tid; b <= f1; b += TJ_THREADS)
-        gave_up |= __ldcg(a.part_err + b) != 0u;
+    for (int b = b0 + (int)threadIdx.x; b <= b1; b += TJ_THREADS) gave_up |= __ldcg(a.part_err + b) != 0u;
+    if (__syncthreads_or(gave_up)) {
+      st |= SPEC_ST_TIMEOUT;
+      if (threadIdx.x == 0) atomicOr(a.status + s, SPEC_ST_TIMEOUT);
     }
-    if (__syncthreads_or(gave_up)) st |= SPEC_ST_TIMEOUT;
   }
-  if (first && tid == 0) a.status[s] = st;
-  if (!any || (st == 0 && b0 == b1)) return;  // no rows, or whole: written by its CTA
-  const int node = live ? m / a.G : 0, d0 = slice * TJ_DIMS + warp * 8;
+  if (st == 0 && b0 == b1) return;  // whole: written by its CTA
+  const int d0 = 8 * (SPLIT ? slice : slice * TJ_WARPS + warp);
   uint4* dst = reinterpret_cast<uint4*>(
       a.out + (((int64_t)s * a.nt + node) * a.nq + kvh * a.G + (m - node * a.G)) * HD + d0);
   if (st != 0) {
@@ -504,15 +486,17 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
   const float4* po = reinterpret_cast<const float4*>(a.part_o) + (size_t)(d0 / 4) * a.rows + r;
   const size_t piece = (size_t)a.rows * (HD / 4);
   constexpr int U = 8;
+  const int per = SPLIT ? (b1 - b0 + TJ_WARPS) / TJ_WARPS : b1 + 1 - b0;  // pieces of a warp
+  const int w0 = SPLIT ? b0 + warp * per : b0, w1 = min(b1 + 1, w0 + per);
   float mx = -INFINITY, l = 0.0f, o[8] = {};
-  for (int bb = b0; bb <= b1; bb += U) {
+  for (int bb = w0; bb < w1; bb += U) {
     float2 ml[U];
     float4 v[U][2];
 #pragma unroll
     for (int j = 0; j < U; j++) {
       ml[j] = make_float2(-INFINITY, 0.0f);
       v[j][0] = v[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (bb + j <= b1 && live) {
+      if (bb + j < w1 && live) {
         // piece of CTA b: its first, unless it began in front of the unit
         const size_t slot = (size_t)(bb + j) * 2 + (share * (bb + j) < u0 ? 1 : 0);
         ml[j] = __ldcg(a.part_ml + slot * a.rows + r);
@@ -532,9 +516,34 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
     for (int j = 0; j < U; j++) {
       const float w = exp2_fast(ml[j].x - ref);
       l = fmaf(ml[j].y, w, l);
-      const float* f = reinterpret_cast<const float*>(v[j]);
+      o[0] = fmaf(v[j][0].x, w, o[0]);
+      o[1] = fmaf(v[j][0].y, w, o[1]);
+      o[2] = fmaf(v[j][0].z, w, o[2]);
+      o[3] = fmaf(v[j][0].w, w, o[3]);
+      o[4] = fmaf(v[j][1].x, w, o[4]);
+      o[5] = fmaf(v[j][1].y, w, o[5]);
+      o[6] = fmaf(v[j][1].z, w, o[6]);
+      o[7] = fmaf(v[j][1].w, w, o[7]);
+    }
+  }
+  if (SPLIT) {
 #pragma unroll
-      for (int d = 0; d < 8; d++) o[d] = fmaf(f[d], w, o[d]);
+    for (int d = 0; d < 8; d++) s_o[warp][d][lane] = o[d];
+    s_ml[warp][lane] = make_float2(mx, l);
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < TJ_WARPS; w++) mx = fmaxf(mx, s_ml[w][lane].x);
+    l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < 8; d++) o[d] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < TJ_WARPS; w++) {
+      const float2 ml = s_ml[w][lane];
+      const float f = exp2_fast(ml.x - mx);  // mx is finite: every row sees itself
+      l = fmaf(ml.y, f, l);
+#pragma unroll
+      for (int d = 0; d < 8; d++) o[d] = fmaf(s_o[w][d][lane], f, o[d]);
     }
   }
   const float inv = 1.0f / l;
@@ -552,7 +561,7 @@ bool on_tc(int rows) { return rows >= 64; }
 
 template <int HD, int MT, int RTW>
 cudaError_t launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  tree_attn_kernel<HD, MT, RTW><<<n_cta, TT_THREADS, Shape<HD, MT, RTW>::SMEM, st>>>(a);
+  tree_attn_kernel<HD, MT, RTW><<<n_cta + 1, TT_THREADS, Shape<HD, MT, RTW>::SMEM, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -570,9 +579,10 @@ int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = programmatic_launch() ? 1 : 0;
-    cfg.gridDim = dim3((unsigned)(a.n_seq * blocks * a.nkv * (HD / TJ_DIMS)));
+    cfg.gridDim = dim3((unsigned)(a.n_seq * blocks * a.nkv * (HD / (on_tc(a.rows) ? 8 * TJ_WARPS : 8))));
     cfg.blockDim = dim3(TJ_THREADS);
-    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<HD>, a, n_cta, blocks);
+    e = cudaLaunchKernelEx(&cfg, on_tc(a.rows) ? tree_join_kernel<HD, false> : tree_join_kernel<HD, true>, a,
+                           n_cta, blocks);
   }
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("tree attention: ") + cudaGetErrorString(e));
   return SPEC_OK;
@@ -591,8 +601,9 @@ int device_sms() {
   return n > 0 ? n : 1;
 }
 
-// The resident CTAs: two an SM, or one.
-int tree_ctas(int rows) { return (on_tc(rows) ? 1 : 2) * device_sms(); }
+// The CTAs with tiles: what is resident, two an SM or one, but for the one
+// that checks.
+int tree_ctas(int rows) { return std::max(1, (on_tc(rows) ? 1 : 2) * device_sms() - 1); }
 
 int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
   int rc = check_pages(kv, true);
@@ -605,7 +616,9 @@ int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
     return fail(SPEC_E_SHAPE, "n_q_heads must be a positive multiple of n_kv_heads");
   if ((int64_t)kv->max_pages * kv->page_size > INT32_MAX - 2 * TT_KEYS)
     return fail(SPEC_E_SHAPE, "max_pages * page_size must stay below 2^31 - 128 positions");
-  if ((double)n_seq * nt * n_q_heads > INT32_MAX) return fail(SPEC_E_SHAPE, "n_seq * nt * n_q_heads too large");
+  if (n_q_heads / kv->n_kv_heads > 4096)
+    return fail(SPEC_E_SHAPE, "more than 4096 query heads a kv head");
+  if ((double)n_seq * nt * n_q_heads * (kv->head_dim / 8) > INT32_MAX) return fail(SPEC_E_SHAPE, "n_seq * nt * n_q_heads too large");
   return SPEC_OK;
 }
 
@@ -624,7 +637,8 @@ int tree_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads, size_
   if (rc != SPEC_OK) return rc;
   const size_t rows = rows_of(nt * (n_q_heads / kv->n_kv_heads));
   const size_t n = tree_ctas((int)rows);
-  *bytes = n * 2 * rows * (sizeof(float) * kv->head_dim + sizeof(float2)) + n * sizeof(uint32_t);
+  *bytes = n * 2 * rows * (sizeof(float) * kv->head_dim + sizeof(float2)) +
+           (n * sizeof(uint32_t) + 15) / 16 * 16 + (size_t)n_seq * sizeof(TreePlan);
   return SPEC_OK;
 }
 
@@ -651,6 +665,7 @@ int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint1
   a.nt = t->nt;
   a.nq = t->n_q_heads;
   a.G = t->n_q_heads / kv->n_kv_heads;
+  a.g_inv = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
   a.window = t->window;
   a.sinks = t->sinks;
   a.scale_log2 = (t->scale != 0.0f ? t->scale : 1.0f / sqrtf((float)kv->head_dim)) * 1.4426950408889634f;
@@ -666,6 +681,8 @@ int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint1
   a.tile_shift = on_tc(a.rows) ? TREE_TC_SHIFT : TT_SHIFT;
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)n_cta * 2 * rows * kv->head_dim);
-  a.part_err = on_tc(a.rows) ? reinterpret_cast<uint32_t*>(a.part_ml + (size_t)n_cta * 2 * rows) : nullptr;
+  uint32_t* err = reinterpret_cast<uint32_t*>(a.part_ml + (size_t)n_cta * 2 * rows);
+  a.part_err = on_tc(a.rows) ? err : nullptr;
+  a.plan = reinterpret_cast<TreePlan*>(err + ((size_t)n_cta + 3) / 4 * 4);
   return kv->head_dim == 128 ? launch_hd<128>(a, n_cta, st) : launch_hd<64>(a, n_cta, st);
 }

@@ -23,12 +23,24 @@ struct TreeArgs {
   const __half* v_new;
   int64_t kv_stride;
   __half* out;
+  uint32_t g_inv;  // ceil(2^32 / G): m / G = umulhi(m, g_inv) for m G < 2^32 and G > 1
   int rows;        // query rows of a unit (16 to 256, a power of two)
   int tile_shift;  // log2 of the positions of a tile
   float* part_o;    // [N][2][HD / 4][rows][4]: a lane a row, its stores side by side
   float2* part_ml;  // [N][2][rows]
   uint32_t* part_err;  // [N]: 1 if the CTA gave up on a wait
+  struct TreePlan* plan;  // [n_seq]
   int32_t* status;
+};
+
+// One sequence's part of the cut, for the joining kernel.
+struct TreePlan {
+  long long before;  // tiles of the sequences in front of it
+  long long share;   // tiles of a CTA
+  int tiles;         // of each of its units
+  int nodes;         // rows of the output that are the call's to write
+  int status;
+  int pad;
 };
 
 namespace {
@@ -110,6 +122,71 @@ __device__ __forceinline__ long long share_of(long long total, int n) {
   return div_ll(total + n - 1, n);
 }
 
+__device__ __forceinline__ int node_of(const TreeArgs& a, int m) {  // m / G
+  return a.G == 1 ? m : (int)__umulhi((unsigned)m, a.g_inv);
+}
+
+// The last CTA of a grid has no tiles: it checks the sequences (tree and
+// pages; slot, length and count come from seq_info) and writes their plans
+// and status, while the others work.  One warp per sequence.
+template <int THREADS>
+__device__ __forceinline__ void check_sequences(const TreeArgs& a, int rows, int tile_shift, int n_cta,
+                                                long long* s_part) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long total = 0, chunk = 0;
+  for (int base = 0; base < a.n_seq; base += THREADS) {
+    block_excl<THREADS>(base + tid < a.n_seq ? seq_info(a, base + tid, rows, tile_shift).work() : 0, s_part,
+                        &chunk);
+    total += chunk;
+  }
+  const long long share = max(share_of(total, n_cta), 1ll);
+  long long first = 0;
+  for (int base = 0; base < a.n_seq; base += THREADS) {
+    SeqInfo q;
+    if (base + tid < a.n_seq) q = seq_info(a, base + tid, rows, tile_shift);
+    const long long excl = block_excl<THREADS>(base + tid < a.n_seq ? q.work() : 0, s_part, &chunk);
+    if (base + tid < a.n_seq) {
+      TreePlan p;
+      p.before = first + excl;
+      p.share = share;
+      p.tiles = q.tiles;
+      p.nodes = p.status = p.pad = 0;  // by the warp that checks
+      a.plan[base + tid] = p;
+    }
+    first += chunk;
+  }
+  __syncthreads();
+  for (int s = warp; s < a.n_seq; s += THREADS / 32) {
+    const SeqInfo q = seq_info(a, s, rows, tile_shift);
+    int st = q.bad;
+    if (st == 0) {
+      bool bad = false;
+      if (a.parents != nullptr)
+        for (int i = lane; i < q.m; i += 32) {
+          const int p = a.parents[(int64_t)s * a.nt + i];
+          bad |= p < -1 || p >= i;
+        }
+      if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_TREE;
+      const int held = q.m == 0 || q.len == 0 ? 0 : (q.len - 1) / a.page_size + 1;
+      // with a window, the pages between the sinks and the window may be gone
+      const int e1 = q.sinks > 0 ? (q.sinks - 1) / a.page_size + 1 : 0;
+      const int e0 = q.lo < q.len ? q.lo / a.page_size : held;
+      bad = false;
+      for (int e = lane; e < held; e += 32) {
+        if (e >= e1 && e < e0) continue;
+        const int p = a.table[(int64_t)q.slot * a.max_pages + e];
+        bad |= p < 0 || p >= a.n_pages;
+      }
+      if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_PAGE;
+    }
+    if (lane == 0) {
+      a.plan[s].nodes = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
+      a.plan[s].status = st;
+      a.status[s] = st;
+    }
+  }
+}
+
 // Finds this CTA's first tile: the sequence that holds tile b * share (and
 // how far into its work) goes to *at; returns its tiles' range, empty if it
 // has none.
@@ -122,7 +199,7 @@ struct Start {
   int s;
 };
 template <int THREADS>
-__device__ __forceinline__ Range find_range(const TreeArgs& a, int rows, int tile_shift,
+__device__ __forceinline__ Range find_range(const TreeArgs& a, int rows, int tile_shift, int n_cta,
                                             long long* s_part, Start* at) {
   long long total = 0, mine = 0, excl = 0, chunk = 0;
   const int tid = threadIdx.x;
@@ -136,7 +213,7 @@ __device__ __forceinline__ Range find_range(const TreeArgs& a, int rows, int til
     excl = block_excl<THREADS>(mine, s_part, &chunk);
     total += chunk;
   }
-  const long long share = share_of(total, gridDim.x);
+  const long long share = share_of(total, n_cta);
   Range r;
   r.w0 = share * blockIdx.x;
   r.w1 = min(total, r.w0 + share);

@@ -206,7 +206,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   TcSmall& sh = *reinterpret_cast<TcSmall*>(smem + Sh::END);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   grid_dep_launch();  // the joining kernel may get ready
-  const Range range = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, sh.part, &sh.at);
+  const int n_cta = gridDim.x - 1;
+  if ((int)blockIdx.x == n_cta) {
+    check_sequences<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part);
+    return;
+  }
+  const Range range = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part, &sh.at);
   const long long w0 = range.w0, w1 = range.w1;
   if (w0 >= w1 || (sm0 & 1023u) != 0u) {  // no tiles (a base off the swizzle's atoms never happens)
     if (tid == 0) a.part_err[blockIdx.x] = w0 < w1;
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       const int wr = 32 * (warp & 3);  // the warp's first lane
       const bool warp_live = ROWS == 64 ? (wr >> 6) == j && row0 + (wr & 63) < M
                                         : row0 + (TWO ? 128 * j : 0) + wr < M;
-      const int node = in ? m / a.G : 0, head = kvh * a.G + (in ? m - node * a.G : 0);
+      const int node = in ? node_of(a, m) : 0, head = kvh * a.G + (in ? m - node * a.G : 0);
       {
         const __half* src = a.q + ((int64_t)s * a.nt + node) * a.q_stride + head * HD;
         constexpr int MINE = TWO ? UNITS : UNITS / 2;  // both groups share a tile of one stream's rows
@@ -741,7 +746,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
 
 template <int HD, int ROWS>
 cudaError_t launch(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  tree_attn_tc_kernel<HD, ROWS><<<n_cta, TC_THREADS, tc_smem<HD>(), st>>>(a);
+  tree_attn_tc_kernel<HD, ROWS><<<n_cta + 1, TC_THREADS, tc_smem<HD>(), st>>>(a);
   return cudaGetLastError();
 }
 
