@@ -628,7 +628,7 @@ int spec_accept_tree(const int32_t* argmax, const int32_t* tokens, const int32_t
  *      the running sum of the kept weights exceeds floor(u * total / 2^32).
  * All of it is integer arithmetic: results are bit-identical to any correct
  * implementation of these rules.
- *   logits  fp32 [R][V], ld elements from row to row (0: V)
+ *   logits  fp32 [R][V], V <= 1048512, ld elements from row to row (0: V)
  *   u       32-bit random words [R]
  *   temperature, top_k, top_p, min_p  per row, fp32 / int32 [R]; each may be
  *           NULL (1, 0 = off, 1 = off, 0 = off).  T >= 0 finite, top_k >= 0,
@@ -641,8 +641,8 @@ int spec_accept_tree(const int32_t* argmax, const int32_t* tokens, const int32_t
  *           spec_accept_stochastic as p_logits / q_logits, filtered rows
  *           make its rejection sampling lossless for the filtered
  *           distributions
- * A row with a NaN or +infinity, without any finite logit, or with a setting
- * out of range gets token -1, n_kept 0 and a filtered row of NaN (which
+ * A row with a NaN or +infinity, without any finite logit, whose largest
+ * l / T overflows, or with a setting out of range gets token -1, n_kept 0 and a filtered row of NaN (which
  * spec_accept_stochastic refuses). */
 int spec_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u,
                 const float* temperature, const int32_t* top_k, const float* top_p,

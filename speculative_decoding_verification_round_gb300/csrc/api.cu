@@ -1210,8 +1210,8 @@ extern "C" int spec_sample(const float* logits, int R, int V, int64_t ld, const 
                            int64_t ld_filtered, void* stream) {
   if (logits == nullptr || u == nullptr || token == nullptr)
     return fail(SPEC_E_INVALID, "null argument");
-  if (R < 1 || V < 1 || R > (1 << 27) || V > (1 << 30))
-    return fail(SPEC_E_SHAPE, "R in [1, 2^27] and V in [1, 2^30] required");
+  if (R < 1 || V < 1 || R > (1 << 26) || V > 1048512)
+    return fail(SPEC_E_SHAPE, "R in [1, 2^26] and V in [1, 1048512] required");
   if (ld == 0) ld = V;
   if (ld_filtered == 0) ld_filtered = V;
   if (ld < V || ld_filtered < V || ld > (1ll << 40) || ld_filtered > (1ll << 40))
