@@ -11,11 +11,12 @@
 // One cluster of CTAs per row keeps the row in shared memory: the logits are
 // read from HBM once, whatever the filters.  A cut is found without sorting
 // the row:
-//  - top-k: every thread knows the largest of the logits that it loaded; the
-//    k-th largest of these is a bound that at least k tokens, and typically
-//    few more, reach.  Those are collected and ranked against one another.
+//  - top-k: every four threads know the largest of the logits that they loaded;
+//    the k-th largest of these is a bound that at least k tokens, and
+//    typically few more, reach.  Those are collected in every
+//    CTA, which all sort them: from there on nobody has to be asked.
 //  - top-p alone: a histogram of masses over equal steps of z gives the step
-//    that holds the cut; its tokens are collected and ranked.
+//    that holds the cut; its tokens are collected and sorted.
 //  - a step with too many tokens (or a top-k whose bound is reached by too
 //    many) is refined by the bits of the order key, down to tokens of equal
 //    logits, whose cut is the n-th lowest id.
@@ -37,9 +38,10 @@ typedef unsigned long long u64;
 constexpr int SM_THREADS = 512;
 constexpr int SM_WARPS = SM_THREADS / 32;
 constexpr int SM_BINS = 1024;
-constexpr int SM_CAND = 2048;   // tokens that are ranked against one another
+constexpr int SM_CAND = 2048;   // tokens that are collected and sorted
 constexpr int SM_LOCAL = 1024;  // of one CTA
 constexpr int SM_MAX_CL = 16;
+constexpr int SM_GROUPS = SM_THREADS / 4;  // of a CTA: four threads each
 constexpr float SM_SPAN = 23.0f;  // z steps cover [max - 23, max]: W is 0 from 22.2 below it
 // a CTA's logits: the 16-bit halves of as many weights (each below 2^17) sum
 // to less than 2^32
@@ -62,6 +64,11 @@ struct SampleArgs {
   int cap;  // of them in shared memory
 };
 
+struct Cut {
+  u64 key;   // composite key of the last token that stays
+  u64 mass;  // of the tokens up to it
+};
+
 struct alignas(16) Shared {  // the row's logits (16-byte stores) follow it
   union {
     struct {
@@ -72,22 +79,33 @@ struct alignas(16) Shared {  // the row's logits (16-byte stores) follow it
       uint32_t own_w[SM_LOCAL];
     };
   };
-  u64 key[SM_CAND];  // the row's collected tokens: order key, then lower ids first
-  uint32_t w[SM_CAND];  // their weights, 2^32 as 2^32 - 1 (which no other weight is)
-  u64 slice_w[SM_BINS];       // this rank's share of the combined bins: inclusive sums
-  uint32_t slice_c[SM_BINS];
+  union {
+    struct {  // until the tokens are collected
+      u64 slice_w[SM_BINS];  // this rank's share of the combined bins: inclusive sums
+      uint32_t slice_c[SM_BINS];
+    };
+    struct {
+      u64 key[SM_CAND];     // the row's collected tokens
+      uint32_t w[SM_CAND];  // their weights, 2^32 as 2^32 - 1 (which no other weight is)
+    };
+  };
   u64 part[SM_WARPS];
-  uint32_t part32[SM_WARPS];
-  u64 pub_w;  // this rank's published totals
+  float warp_max[SM_WARPS];  // published at the start
+  uint32_t own_group[SM_GROUPS];
+  uint32_t part32[2 * SM_WARPS];
+  u64 pub_w;  // this rank's published totals of the bins, and of the draw
   uint32_t pub_c;
-  uint32_t pub_key;
-  int pub_bad;
-  uint32_t n_own, theta;
-  // published by the rank that finds it
-  int f_bin;
-  u64 f_before_w;
-  uint32_t f_before_c, f_bin_c;
-  u64 cut_key, cut_w;
+  u64 draw_w;
+  uint32_t draw_c;
+  uint32_t n_own;
+  // published by the rank that finds it: two, in turn, so that one may be
+  // written while the other is read
+  struct {
+    int bin;
+    u64 before_w;
+    uint32_t before_c, bin_c;
+  } found[2];
+  Cut cut;
   int pick;
 };
 static_assert(sizeof(Shared) % 16 == 0, "the logits behind it are 16-byte aligned");
@@ -153,11 +171,14 @@ __device__ __forceinline__ u64 widen(uint32_t w) { return (u64)w + (w == 0xFFFFF
 struct Row {
   float T, inv_T, zmax;
   bool plain;  // divide by the division: T is 1 or far from it
-  u64 cut;     // tokens whose composite key is at least this stay
-  u64 min_w;
-  // Order key and id as one number: larger stands first (ties: the lower id).
-  static __device__ __forceinline__ u64 composite(float l, int id) {
-    return ((u64)max_key(l) << 32) | (uint32_t)~id;
+  float least;  // tokens above it stay; those equal to it with ids up to last_id
+  int last_id;
+  uint32_t min_w;  // of those, the ones of at least this weight (2^32 as 2^32 - 1)
+  // Order key and id as one number, larger for what stands first (of equal
+  // logits the lower id): ids have 20 bits, and the lowest 12 are free for a
+  // place in a list.
+  static __device__ __forceinline__ u64 composite(uint32_t key, int id) {
+    return ((u64)key << 32) | ((uint32_t)(0xFFFFF - id) << 12);
   }
   // x = z - max z of two logits.  z = l / T, correctly rounded: from the
   // correctly rounded reciprocal y of T, q0 = l y; q <- q + (l - q T) y twice.
@@ -209,64 +230,90 @@ struct Row {
     return b < (float)(SM_BINS - 1) ? (int)b : SM_BINS - 1;
   }
   __device__ __forceinline__ int bin(float l) const { return bin_of(x2(make_float2(l, l)).x); }
-  __device__ __forceinline__ bool inside(float l, int id) const { return composite(l, id) >= cut; }
+  __device__ __forceinline__ void set_cut(u64 key) {
+    least = key_value((uint32_t)(key >> 32));
+    last_id = 0xFFFFF - (int)((uint32_t)key >> 12);
+    if (!(least > -INFINITY)) no_cut();  // a top-k beyond the finite logits
+  }
+  __device__ __forceinline__ void no_cut() {
+    least = -FLT_MAX;
+    last_id = 0x7FFFFFFF;
+  }
+  __device__ __forceinline__ bool inside(float l, int id) const {
+    return l > least || (l == least && id <= last_id);
+  }
 };
 
 // The first id, in the order of ids over the whole row, at which the running
-// sum of the two measures of measure(logits, id of the first) reaches
+// sum of the weights of measure(two logits, id of the first, count) reaches
 // target(total); every thread of the cluster gets it, and the total.  -1 if
-// it is never reached.
+// it is never reached.  `count` is summed up as well, for rank 0's *counted.
 template <class M, class Tg>
 __device__ int ordered_pick(cg::cluster_group& cl, Shared& sh, const Segment& seg, M&& measure,
-                            Tg&& target, u64* total) {
+                            Tg&& target, uint32_t* counted) {
   const int rank = (int)cl.block_rank(), n = (int)cl.num_blocks();
   // a thread owns a run of ids; an odd number of pairs keeps its strided
   // reads of shared memory at two wavefronts
   const int c = 2 * (((seg.len + 2 * SM_THREADS - 1) / (2 * SM_THREADS)) | 1);
   const int i0 = min(seg.len, (int)threadIdx.x * c), i1 = min(seg.len, i0 + c);
   auto pair = [&](int i) {  // the second of the last pair may be past the end
-    return make_float2(seg.at(i), i + 1 < i1 ? seg.at(i + 1) : -INFINITY);
+    if (i + 1 < i1) return i + 1 < seg.cap ? *reinterpret_cast<const float2*>(seg.s + i) : make_float2(seg.at(i), seg.at(i + 1));
+    return make_float2(seg.at(i), -INFINITY);
   };
   u64 mine = 0;
+  uint32_t cnt = 0;
   for (int i = i0; i < i1; i += 2) {
-    const ulonglong2 w = measure(pair(i), seg.id0 + i);
-    mine += w.x + w.y;
+    const uint2 w = measure(pair(i), seg.id0 + i, cnt);
+    mine += w.x;
+    mine += w.y;
+    mine += (w.x == 0xFFFFFFFFu) + (w.y == 0xFFFFFFFFu);
   }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
+  if ((threadIdx.x & 31) == 0) sh.part32[threadIdx.x >> 5] = cnt;
   u64 cta;
   const u64 incl = block_prefix(mine, sh, &cta);
   if (threadIdx.x == 0) {
-    sh.pub_w = cta;
+    uint32_t all = 0;
+    for (int w = 0; w < SM_WARPS; w++) all += sh.part32[w];
+    sh.draw_w = cta;
+    sh.draw_c = all;
     sh.pick = -1;
   }
   cl.sync();
   u64 before = 0, all = 0;
   for (int r = 0; r < n; r++) {
-    const u64 w = *cl.map_shared_rank(&sh.pub_w, r);
+    const u64 w = *cl.map_shared_rank(&sh.draw_w, r);
     if (r < rank) before += w;
     all += w;
+  }
+  if (counted != nullptr && rank == 0 && threadIdx.x == 0) {
+    uint32_t sum = 0;
+    for (int r = 0; r < n; r++) sum += *cl.map_shared_rank(&sh.draw_c, r);
+    *counted = sum;
   }
   const u64 t = target(all);
   const u64 hi = before + incl, lo = hi - mine;
   if (mine > 0 && lo < t && t <= hi) {  // this thread's run holds it: at most one thread does
     u64 run = lo;
     for (int i = i0; i < i1; i += 2) {
-      const ulonglong2 w = measure(pair(i), seg.id0 + i);
-      if (run + w.x + w.y >= t) {
-        const int id = seg.id0 + i + (run + w.x >= t ? 0 : 1);
+      const uint2 w = measure(pair(i), seg.id0 + i, cnt);
+      const u64 wx = widen(w.x), wy = widen(w.y);
+      if (run + wx + wy >= t) {
+        const int id = seg.id0 + i + (run + wx >= t ? 0 : 1);
         for (int r = 0; r < n; r++) *cl.map_shared_rank(&sh.pick, r) = id;
         break;
       }
-      run += w.x + w.y;
+      run += wx + wy;
     }
   }
   cl.sync();
-  *total = all;
   return sh.pick;
 }
 
 // The combined bins of the cluster from every CTA's: every rank holds its
 // share of them as inclusive sums.
-template <bool MASS>
+template <bool COUNT, bool MASS>
 __device__ void combine(cg::cluster_group& cl, Shared& sh) {
   const int rank = (int)cl.block_rank(), n = (int)cl.num_blocks();
   cl.sync();
@@ -281,7 +328,7 @@ __device__ void combine(cg::cluster_group& cl, Shared& sh) {
     cc[k] = 0;
     if (b < share)
       for (int r = 0; r < n; r++) {
-        cc[k] += cl.map_shared_rank(sh.cnt, r)[b0 + b];
+        if (COUNT) cc[k] += cl.map_shared_rank(sh.cnt, r)[b0 + b];
         if (MASS)
           w[k] += ((u64)cl.map_shared_rank(sh.hi, r)[b0 + b] << 16) + cl.map_shared_rank(sh.lo, r)[b0 + b];
       }
@@ -290,7 +337,7 @@ __device__ void combine(cg::cluster_group& cl, Shared& sh) {
   }
   u64 all_w = 0, all_c = 0;
   u64 run_w = MASS ? block_prefix(wt, sh, &all_w) - wt : 0;
-  u64 run_c = block_prefix(ct, sh, &all_c) - ct;
+  u64 run_c = COUNT ? block_prefix(ct, sh, &all_c) - ct : 0;
 #pragma unroll
   for (int k = 0; k < PER; k++) {
     const int b = (int)threadIdx.x * PER + k;
@@ -319,7 +366,9 @@ __device__ __forceinline__ void add_mass(Shared& sh, int b, uint32_t w) {
 }
 
 // Histogram of all tokens over the steps of z (two 32-bit additions a mass:
-// 64-bit ones in shared memory are compare-and-swap loops, four times slower).
+// 64-bit ones in shared memory are compare-and-swap loops, 24 us for a CTA's
+// 30720 logits where these take 3).
+template <bool COUNT>
 __device__ void histogram(cg::cluster_group& cl, Shared& sh, const Segment& seg, const Row& row) {
   clear_bins(sh);
   for (int i = 2 * threadIdx.x; i < seg.len; i += 2 * SM_THREADS) {
@@ -327,14 +376,12 @@ __device__ void histogram(cg::cluster_group& cl, Shared& sh, const Segment& seg,
     const float2 x = row.x2(make_float2(seg.at(i), two ? seg.at(i + 1) : -INFINITY));
     const uint2 w = Row::w2(x);
     const int b0 = Row::bin_of(x.x), b1 = Row::bin_of(x.y);
-    atomicAdd(&sh.cnt[b0], 1u);
+    if (COUNT) atomicAdd(&sh.cnt[b0], 1u);
+    if (COUNT && two) atomicAdd(&sh.cnt[b1], 1u);
     if (w.x != 0) add_mass(sh, b0, w.x);
-    if (two) {
-      atomicAdd(&sh.cnt[b1], 1u);
-      if (w.y != 0) add_mass(sh, b1, w.y);
-    }
+    if (w.y != 0) add_mass(sh, b1, w.y);
   }
-  combine<true>(cl, sh);
+  combine<COUNT, true>(cl, sh);
 }
 
 // What a search for a target in the combined bins gives.
@@ -347,7 +394,7 @@ struct Found {
 // The bin at which the running sum of counts (BY_COUNT) or masses reaches
 // `target` (1 <= target <= the total).
 template <bool BY_COUNT>
-__device__ Found find_bin(cg::cluster_group& cl, Shared& sh, u64 target) {
+__device__ Found find_bin(cg::cluster_group& cl, Shared& sh, u64 target, int& turn) {
   const int rank = (int)cl.block_rank(), n = (int)cl.num_blocks();
   const int share = SM_BINS / n;
   u64 bw = 0, bc = 0;
@@ -363,28 +410,23 @@ __device__ Found find_bin(cg::cluster_group& cl, Shared& sh, u64 target) {
       const u64 pw = b == 0 ? 0ull : sh.slice_w[b - 1];
       const uint32_t pc = b == 0 ? 0u : sh.slice_c[b - 1];
       for (int r = 0; r < n; r++) {
-        Shared& o = *cl.map_shared_rank(&sh, r);
-        o.f_bin = rank * share + b;
-        o.f_before_w = bw + pw;
-        o.f_before_c = (uint32_t)bc + pc;
-        o.f_bin_c = sh.slice_c[b] - pc;
+        auto& o = cl.map_shared_rank(&sh, r)->found[turn];
+        o.bin = rank * share + b;
+        o.before_w = bw + pw;
+        o.before_c = (uint32_t)bc + pc;
+        o.bin_c = sh.slice_c[b] - pc;
       }
     }
   }
   cl.sync();
   Found f;
-  f.bin = sh.f_bin;
-  f.before_w = sh.f_before_w;
-  f.before_c = sh.f_before_c;
-  f.bin_c = sh.f_bin_c;
-  cl.sync();  // read before the next search writes
+  f.bin = sh.found[turn].bin;
+  f.before_w = sh.found[turn].before_w;
+  f.before_c = sh.found[turn].before_c;
+  f.bin_c = sh.found[turn].bin_c;
+  turn ^= 1;
   return f;
 }
-
-struct Cut {
-  u64 key;   // composite key of the last token that stays
-  u64 mass;  // of the tokens up to it
-};
 
 // The tokens that take(logit) accepts, collected into every CTA's sh.key and
 // sh.w; returns their number, or more than SM_CAND if they are too many.
@@ -399,12 +441,12 @@ __device__ int collect(cg::cluster_group& cl, Shared& sh, const Segment& seg, co
     if (take(l)) {
       const uint32_t at = atomicAdd(&sh.n_own, 1u);
       if (at < SM_LOCAL) {
-        sh.own_key[at] = Row::composite(l, seg.id0 + i);
+        sh.own_key[at] = Row::composite(max_key(l), seg.id0 + i);
         sh.own_w[at] = mass ? row.weight(l) : 0u;
       }
     }
   }
-  cl.sync();
+  cl.sync();  // (and the combined bins have been read, which the tokens now overwrite)
   uint32_t before = 0, all = 0;
   bool over = false;
   for (int r = 0; r < n; r++) {
@@ -418,7 +460,7 @@ __device__ int collect(cg::cluster_group& cl, Shared& sh, const Segment& seg, co
     for (int e = threadIdx.x; e < own * n; e += SM_THREADS) {
       const int r = e / own, c = e - r * own;
       Shared& o = *cl.map_shared_rank(&sh, r);
-      o.key[before + c] = sh.own_key[c];
+      o.key[before + c] = sh.own_key[c] | (before + c);
       o.w[before + c] = sh.own_w[c];
     }
   }
@@ -426,45 +468,86 @@ __device__ int collect(cg::cluster_group& cl, Shared& sh, const Segment& seg, co
   return over ? SM_CAND + 1 : (int)all;
 }
 
-// Ranks the m collected tokens against one another, each by up to 32 threads
-// of the CTAs in turn, and calls f(composite key, count and mass in front of
-// it, weight) once for each, on some thread of the cluster.
-template <class F>
-__device__ void rank_all(cg::cluster_group& cl, Shared& sh, int m, bool mass, F&& f) {
-  const int rank = (int)cl.block_rank(), n = (int)cl.num_blocks();
-  const int per = (m + n - 1) / n, c0 = rank * per, mine = max(0, min(m - c0, per));
-  int grp = 1;  // threads of a token
-  while (grp < 32 && mine * grp * 2 <= SM_THREADS) grp *= 2;
-  const int step = SM_THREADS / grp;
-  for (int base = 0; base < mine; base += step) {  // uniform over the CTA
-    const int c = base + (int)threadIdx.x / grp;
-    const bool ok = c < mine;
-    const u64 me = ok ? sh.key[c0 + c] : ~0ull;
-    uint32_t cnt = 0;
-    u64 sum = 0;
-    if (mass) {
-      for (int j = threadIdx.x % grp; j < m; j += grp)
-        if (sh.key[j] > me) {
-          cnt++;
-          sum += widen(sh.w[j]);
-        }
-    } else {
-      for (int j = threadIdx.x % grp; j < m; j += grp) cnt += sh.key[j] > me;
+// Sorts sh.key[0, SM_THREADS E) from the largest down: a bitonic network on
+// registers, E numbers a thread; partners in other warps meet in shared memory.
+template <int E>
+__device__ void sort_keys(Shared& sh) {
+  const int tid = threadIdx.x;
+  u64 v[E];
+#pragma unroll
+  for (int e = 0; e < E; e++) v[e] = sh.key[tid * E + e];
+#pragma unroll 1
+  for (int k = 2; k <= SM_THREADS * E; k *= 2) {
+#pragma unroll 1
+    for (int d = k >> 1; d >= E; d >>= 1) {
+      if (d >= 32 * E) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; e++) sh.key[tid * E + e] = v[e];
+        __syncthreads();
+      }
+#pragma unroll
+      for (int e = 0; e < E; e++) {
+        const int i = tid * E + e;
+        const u64 o = d >= 32 * E ? sh.key[i ^ d] : __shfl_xor_sync(0xffffffffu, v[e], d / E);
+        const bool larger = ((i & d) == 0) == ((i & k) == 0);  // of the two, this place gets
+        v[e] = (o > v[e]) == larger ? o : v[e];
+      }
     }
-    for (int off = grp >> 1; off > 0; off >>= 1) {
-      cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
-      sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    }
-    if (ok && threadIdx.x % grp == 0) f(me, cnt, sum, widen(sh.w[c0 + c]));
+#pragma unroll
+    for (int d = E / 2; d > 0; d >>= 1)
+      if (d < k)
+#pragma unroll
+        for (int e = 0; e < E; e++)
+          if ((e & d) == 0) {
+            const bool down = ((tid * E + e) & k) == 0;
+            const u64 x = v[e], y = v[e | d];
+            if ((x < y) == down) v[e] = y, v[e | d] = x;
+          }
   }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; e++) sh.key[tid * E + e] = v[e];
+  __syncthreads();
 }
 
-__device__ __forceinline__ void publish(cg::cluster_group& cl, Shared& sh, u64 key, u64 mass) {
-  for (int r = 0; r < (int)cl.num_blocks(); r++) {
-    Shared& o = *cl.map_shared_rank(&sh, r);
-    o.cut_key = key;
-    o.cut_w = mass;
+// Sorts the m collected tokens, the first in the order first.
+__device__ void sort_list(Shared& sh, int m) {
+  const int size = m <= SM_THREADS ? SM_THREADS : SM_CAND;
+  for (int i = m + (int)threadIdx.x; i < size; i += SM_THREADS) sh.key[i] = 0;  // behind every token
+  __syncthreads();
+  if (size == SM_THREADS)
+    sort_keys<1>(sh);
+  else
+    sort_keys<SM_CAND / SM_THREADS>(sh);
+}
+
+// Of the sorted list: the cut of a count (by_count) or of a mass.  `mass`
+// gets the sum up to it.
+__device__ Cut cut_list(Shared& sh, int m, bool by_count, u64 target) {
+  constexpr int PER = SM_CAND / SM_THREADS;
+  u64 w[PER], mine = 0;
+#pragma unroll
+  for (int e = 0; e < PER; e++) {
+    const int i = (int)threadIdx.x * PER + e;
+    w[e] = i < m ? widen(sh.w[sh.key[i] & 0xFFFu]) : 0;
+    mine += w[e];
   }
+  u64 all, run = block_prefix(mine, sh, &all) - mine;
+#pragma unroll
+  for (int e = 0; e < PER; e++) {
+    const int i = (int)threadIdx.x * PER + e;
+    const u64 before = run;
+    run += w[e];
+    if (i < m && (by_count ? (u64)i + 1 == target : before < target && target <= run)) {
+      sh.cut.key = sh.key[i];
+      sh.cut.mass = run;
+    }
+  }
+  __syncthreads();
+  const Cut c = sh.cut;
+  __syncthreads();
+  return c;
 }
 
 // The token at which the running sum of counts (BY_COUNT) or masses, in the
@@ -472,12 +555,11 @@ __device__ __forceinline__ void publish(cg::cluster_group& cl, Shared& sh, u64 k
 // all tokens over the steps of z is combined; the search overwrites it.
 template <bool BY_COUNT>
 __device__ Cut find_cut(cg::cluster_group& cl, Shared& sh, const Segment& seg, const Row& row,
-                        u64 target) {
-  Found f = find_bin<BY_COUNT>(cl, sh, target);
+                        u64 target, int& turn) {
+  Found f = find_bin<BY_COUNT>(cl, sh, target, turn);
   const int zbin = f.bin;
   u64 before_w = f.before_w;
   u64 left = target - (BY_COUNT ? (u64)f.before_c : f.before_w);  // to reach inside the bin
-  uint32_t members = f.bin_c;
   // refinement by the bits of the order key: 10, 10, 10, 2 from the top,
   // larger keys in lower bins
   int known = 32;  // bits still unknown
@@ -487,7 +569,8 @@ __device__ Cut find_cut(cg::cluster_group& cl, Shared& sh, const Segment& seg, c
   };
   int m = SM_CAND + 1;
   for (;;) {
-    if (members <= SM_CAND) m = collect(cl, sh, seg, row, true, [&](float l) { return member(l, max_key(l)); });
+    if (!BY_COUNT || f.bin_c <= SM_CAND)
+      m = collect(cl, sh, seg, row, true, [&](float l) { return member(l, max_key(l)); });
     if (m <= SM_CAND || known == 0) break;
     const int bits = min(10, known), down = known - bits;
     clear_bins(sh);
@@ -500,36 +583,29 @@ __device__ Cut find_cut(cg::cluster_group& cl, Shared& sh, const Segment& seg, c
         add_mass(sh, b, row.weight(l));
       }
     }
-    combine<true>(cl, sh);
-    f = find_bin<BY_COUNT>(cl, sh, left);
+    combine<true, true>(cl, sh);
+    f = find_bin<BY_COUNT>(cl, sh, left, turn);
     before_w += f.before_w;
     left -= BY_COUNT ? (u64)f.before_c : f.before_w;
     prefix = (known < 32 ? prefix << bits : 0u) | (uint32_t)((SM_BINS - 1) - f.bin);
     known = down;
-    members = f.bin_c;
   }
   Cut cut;
   if (m > SM_CAND) {  // all of one logit: the n-th lowest id of them
     const uint32_t key = prefix;
     const u64 w = widen(row.weight(key_value(key)));
     const u64 nth = BY_COUNT ? left : (left + w - 1) / w;
-    u64 all;
     const int id = ordered_pick(
         cl, sh, seg,
-        [&](float2 l, int) { return make_ulonglong2(max_key(l.x) == key, max_key(l.y) == key); },
-        [&](u64) { return nth; }, &all);
-    cut.key = ((u64)key << 32) | (uint32_t)~id;
+        [&](float2 l, int, uint32_t&) { return make_uint2(max_key(l.x) == key, max_key(l.y) == key); },
+        [&](u64) { return nth; }, nullptr);
+    cut.key = Row::composite(key, id);
     cut.mass = before_w + nth * w;
     return cut;
   }
-  rank_all(cl, sh, m, true, [&](u64 key, uint32_t cnt, u64 sum, u64 w) {
-    const u64 lo = BY_COUNT ? (u64)cnt : sum, step = BY_COUNT ? 1ull : w;
-    if (lo < left && left <= lo + step) publish(cl, sh, key, before_w + sum + w);
-  });
-  cl.sync();
-  cut.key = sh.cut_key;
-  cut.mass = sh.cut_w;
-  cl.sync();  // read before the next search writes
+  sort_list(sh, m);
+  cut = cut_list(sh, m, BY_COUNT, left);
+  cut.mass += before_w;
   return cut;
 }
 
@@ -569,15 +645,9 @@ sample_kernel(const SampleArgs a) {
   row.inv_T = __frcp_rn(row.T);
   row.plain = row.T == 1.0f || !(row.T > 0x1p-60f && row.T < 0x1p60f);
 
-  // ---- the segment into shared memory; its largest logit, NaN and +inf
+  // ---- the segment into shared memory; its largest logit (NaN if there is one)
   float mx = -INFINITY;  // of this thread's
-  bool nan = false;
-  int finite = 0;  // logits above -inf
-  auto see = [&](float l) {
-    nan |= !(l < INFINITY);
-    finite += l > -INFINITY;
-    mx = fmaxf(mx, l);
-  };
+  auto see = [&](float l) { asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(l)); };
   if ((reinterpret_cast<uintptr_t>(seg.g) & 15u) == 0) {
     const int n4 = seg.cap / 4;
     const float4* g4 = reinterpret_cast<const float4*>(seg.g);
@@ -600,37 +670,32 @@ sample_kernel(const SampleArgs a) {
     for (int i = threadIdx.x; i < seg.cap; i += SM_THREADS) see(buf[i] = seg.g[i]);
   }
   for (int i = seg.cap + threadIdx.x; i < seg.len; i += SM_THREADS) see(__ldcg(seg.g + i));
-  float cmx = mx;
+  float gmx = mx, wmx;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const float o = __shfl_xor_sync(0xffffffffu, off == 4 ? gmx : off > 4 ? wmx : gmx, off);
+    if (off < 4) {
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(gmx) : "f"(o));
+    } else {
+      if (off == 4) wmx = gmx;
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(wmx) : "f"(o));
+    }
+  }
+  if ((threadIdx.x & 3) == 0) sh.own_group[threadIdx.x >> 2] = max_key(gmx);
+  if ((threadIdx.x & 31) == 0) sh.warp_max[threadIdx.x >> 5] = wmx;
+  cl.sync();
+  float top = -INFINITY;
+  for (int e = threadIdx.x & 31; e < n * SM_WARPS; e += 32) {
+    const float o = cl.map_shared_rank(sh.warp_max, e / SM_WARPS)[e % SM_WARPS];
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(o));
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    cmx = fmaxf(cmx, __shfl_xor_sync(0xffffffffu, cmx, off));
-    finite += __shfl_xor_sync(0xffffffffu, finite, off);
+    const float o = __shfl_xor_sync(0xffffffffu, top, off);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(o));
   }
-  if ((threadIdx.x & 31) == 0) {
-    sh.part32[threadIdx.x >> 5] = max_key(cmx);
-    sh.part[threadIdx.x >> 5] = finite;
-  }
-  const int any_nan = __syncthreads_or(nan);
-  if (threadIdx.x == 0) {
-    uint32_t key = 0, fin = 0;
-    for (int w = 0; w < SM_WARPS; w++) {
-      key = max(key, sh.part32[w]);
-      fin += (uint32_t)sh.part[w];
-    }
-    sh.pub_key = key;
-    sh.pub_bad = any_nan;
-    sh.pub_c = fin;
-  }
-  cl.sync();
-  uint32_t key = 0, n_fin = 0;
-  for (int q = 0; q < n; q++) {
-    key = max(key, *cl.map_shared_rank(&sh.pub_key, q));
-    bad |= *cl.map_shared_rank(&sh.pub_bad, q) != 0;
-    n_fin += *cl.map_shared_rank(&sh.pub_c, q);
-  }
-  cl.sync();  // read before the next totals are published
-  row.zmax = row_zmax(key, row.T);
-  bad |= n_fin == 0 || !(fabsf(row.zmax) < INFINITY);
+  row.zmax = row_zmax(max_key(top), row.T);
+  bad |= !(fabsf(top) < INFINITY) || !(fabsf(row.zmax) < INFINITY);  // NaN, +inf, nothing but -inf
   float* frow = a.filtered != nullptr ? a.filtered + (int64_t)r * a.ldf + seg.id0 : nullptr;
   if (bad) {  // the whole cluster
     if (frow != nullptr)
@@ -639,143 +704,134 @@ sample_kernel(const SampleArgs a) {
       a.token[r] = -1;
       if (a.n_kept != nullptr) a.n_kept[r] = 0;
     }
+    cl.sync();  // shared memory stays until everybody has read it
     return;
   }
 
   // ---- the cuts.  Everything above -inf is inside at first.
-  row.cut = (u64)0x00800000u << 32;  // the key of -FLT_MAX, any id
-  row.min_w = (u64)floor((double)min_p * 4294967296.0);
+  row.no_cut();
+  const u64 M = (u64)floor((double)min_p * 4294967296.0);
+  row.min_w = (uint32_t)min(M, 0xFFFFFFFFull);
   const u64 P = (u64)floor((double)top_p * 4294967296.0);
-  const bool by_k = k > 0 && (uint32_t)k < n_fin, by_p = P < (1ull << 32);
+  const bool by_k = k > 0 && k < a.V, by_p = P < (1ull << 32);
+  int turn = 0;
   bool done = false;
-  if (by_k && k <= n * SM_THREADS) {
-    // the k-th largest of the threads' largest logits, to a step of z: no
-    // token below it is among the first k
-    clear_bins(sh);
-    if (mx > -INFINITY) atomicAdd(&sh.cnt[row.bin(mx)], 1u);
-    if (threadIdx.x == 0) sh.theta = ~0u;
-    combine<false>(cl, sh);
-    uint32_t threads = 0;  // with a finite logit
-    for (int q = 0; q < n; q++) threads += *cl.map_shared_rank(&sh.pub_c, q);
-    if ((uint32_t)k <= threads) {
-      const Found f = find_bin<true>(cl, sh, (u64)k);
-      if (mx > -INFINITY && row.bin(mx) <= f.bin) atomicMin(&sh.theta, max_key(mx));
-      cl.sync();
-      uint32_t theta = ~0u;
-      for (int q = 0; q < n; q++) theta = min(theta, *cl.map_shared_rank(&sh.theta, q));
-      const float bound = key_value(theta);
-      const int m = collect(cl, sh, seg, row, by_p, [&](float l) { return l >= bound; });
-      if (m <= SM_CAND) {
-        // a thread ranks at most SM_CAND / SM_THREADS tokens; the cut of the
-        // mass needs the total up to the k-th first
-        u64 keys[SM_CAND / SM_THREADS], sums[SM_CAND / SM_THREADS], ws[SM_CAND / SM_THREADS];
-        int held = 0;
+  if (by_k) {
+    // a bound that at least k tokens reach, and hardly more than SM_CAND
+    const int groups = n * SM_GROUPS;
+    float bound = -INFINITY;
+    int bin = -1;
+    if (k <= groups * 3 / 4) {
+      // the k-th largest of the groups' largest, bit by bit (its order key's
+      // first 20: a bound may be a little low)
+      constexpr int PER = SM_MAX_CL * SM_GROUPS / SM_THREADS;
+      uint32_t mine[PER];
 #pragma unroll
-        for (int e = 0; e < SM_CAND / SM_THREADS; e++) keys[e] = sums[e] = ws[e] = 0;
-        rank_all(cl, sh, m, by_p, [&](u64 ck, uint32_t cnt, u64 sum, u64 w) {
-#pragma unroll
-          for (int e = 0; e < SM_CAND / SM_THREADS; e++)
-            if (e == held) keys[e] = ck, sums[e] = sum, ws[e] = w;
-          held++;
-          if (cnt == (uint32_t)k - 1) publish(cl, sh, ck, sum + w);
-        });
-        cl.sync();
-        row.cut = sh.cut_key;
-        const u64 S = sh.cut_w;
-        cl.sync();
-        if (by_p) {
-          const u64 need = mass_needed(P, S);
-#pragma unroll
-          for (int e = 0; e < SM_CAND / SM_THREADS; e++)
-            if (e < held && sums[e] < need && need <= sums[e] + ws[e]) publish(cl, sh, keys[e], 0);
-          cl.sync();
-          row.cut = sh.cut_key;
-        }
-        done = true;
+      for (int e = 0; e < PER; e++) {
+        const int g = (int)threadIdx.x + e * SM_THREADS;
+        mine[e] = g < groups ? cl.map_shared_rank(sh.own_group, g / SM_GROUPS)[g % SM_GROUPS] : 0u;
       }
+      uint32_t low = 0u;
+      for (int bit = 31; bit >= 12; bit--) {
+        const uint32_t at = low | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int e = 0; e < PER; e++) c += mine[e] >= at;
+        c = __reduce_add_sync(0xffffffffu, c);
+        uint32_t* part = sh.part32 + (bit & 1) * SM_WARPS;  // two, in turn: one barrier a bit
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = (uint32_t)c;
+        __syncthreads();
+        uint32_t all = 0;
+#pragma unroll
+        for (int w = 0; w < SM_WARPS; w++) all += part[w];
+        if (all >= (uint32_t)k) low = at;
+      }
+      // -inf or below: fewer than k groups have a finite logit
+      if (low > 0x007FFFFFu) bound = key_value(low);
+    } else if (k <= SM_CAND) {  // to a step of z: the k-th largest of all tokens
+      clear_bins(sh);
+      for (int i = 2 * threadIdx.x; i < seg.len; i += 2 * SM_THREADS) {
+        const bool two = i + 1 < seg.len;
+        const float2 x = row.x2(make_float2(seg.at(i), two ? seg.at(i + 1) : -INFINITY));
+        atomicAdd(&sh.cnt[Row::bin_of(x.x)], 1u);
+        if (two) atomicAdd(&sh.cnt[Row::bin_of(x.y)], 1u);
+      }
+      combine<true, false>(cl, sh);
+      bin = find_bin<true>(cl, sh, (u64)k, turn).bin;
+    }
+    int m = SM_CAND + 1;
+    if (bound > -INFINITY)
+      m = collect(cl, sh, seg, row, by_p, [&](float l) { return l >= bound; });
+    else if (bin >= 0)
+      m = collect(cl, sh, seg, row, by_p, [&](float l) { return row.bin(l) <= bin; });
+    if (m <= SM_CAND) {
+      sort_list(sh, m);
+      Cut c = cut_list(sh, m, true, (u64)k);
+      if (by_p) c = cut_list(sh, m, false, mass_needed(P, c.mass));
+      row.set_cut(c.key);
+      done = true;
     }
   }
   if (!done && (by_k || by_p)) {
     u64 S = 0;
-    histogram(cl, sh, seg, row);
-    if (by_p && !by_k)
-      for (int q = 0; q < n; q++) S += *cl.map_shared_rank(&sh.pub_w, q);
     if (by_k) {
-      const Cut c = find_cut<true>(cl, sh, seg, row, (u64)k);
-      row.cut = c.key;
+      histogram<true>(cl, sh, seg, row);
+      const Cut c = find_cut<true>(cl, sh, seg, row, (u64)k, turn);
+      row.set_cut(c.key);
       S = c.mass;
-      if (by_p) histogram(cl, sh, seg, row);
     }
-    if (by_p) row.cut = find_cut<false>(cl, sh, seg, row, mass_needed(P, S)).key;
+    if (by_p) {
+      histogram<false>(cl, sh, seg, row);
+      if (!by_k)
+        for (int q = 0; q < n; q++) S += *cl.map_shared_rank(&sh.pub_w, q);
+      row.set_cut(find_cut<false>(cl, sh, seg, row, mass_needed(P, S), turn).key);
+    }
   }
 
   // ---- the draw, in the order of ids
   const uint32_t u = a.u[r];
-  u64 total;
-  const float least = key_value((uint32_t)(row.cut >> 32));  // logits below it are outside
+  uint32_t kept = 0;
   const int tok = ordered_pick(
       cl, sh, seg,
-      [&](float2 l, int id) {
-        ulonglong2 w = make_ulonglong2(0, 0);
-        if (l.x >= least || l.y >= least) {
-          const uint2 v = row.weight2(l);
-          if (row.inside(l.x, id) && widen(v.x) >= row.min_w) w.x = widen(v.x);
-          if (row.inside(l.y, id + 1) && widen(v.y) >= row.min_w) w.y = widen(v.y);
+      [&](float2 l, int id, uint32_t& cnt) {
+        uint2 w = make_uint2(0u, 0u);
+        if (l.x >= row.least || l.y >= row.least) {
+          w = row.weight2(l);
+          const bool in_x = row.inside(l.x, id) && w.x >= row.min_w;
+          const bool in_y = row.inside(l.y, id + 1) && w.y >= row.min_w;
+          cnt += in_x;
+          cnt += in_y;
+          w.x = in_x ? w.x : 0u;
+          w.y = in_y ? w.y : 0u;
         }
         return w;
       },
-      [&](u64 all) { return (u64)scaled_threshold(u, all) + 1; }, &total);
-  if (rank == 0 && threadIdx.x == 0) a.token[r] = tok;
-  if (a.n_kept == nullptr && frow == nullptr) return;
-  int kept = 0;
-  auto stays = [&](float l, int id) {
-    return l >= least && row.inside(l, id) && (row.min_w == 0 || widen(row.weight(l)) >= row.min_w);
+      [&](u64 all) { return (u64)scaled_threshold(u, all) + 1; }, &kept);
+  if (rank == 0 && threadIdx.x == 0) {
+    a.token[r] = tok;
+    if (a.n_kept != nullptr) a.n_kept[r] = (int)kept;
+  }
+  if (frow == nullptr) return;
+  auto out = [&](float l, int id) {
+    const bool in = row.inside(l, id) && (row.min_w == 0u || row.weight(l) >= row.min_w);
+    return in ? l : SPEC_FILTERED;
   };
-  if (frow != nullptr && (reinterpret_cast<uintptr_t>(frow) & 15u) == 0 && seg.cap == seg.len) {
+  if ((reinterpret_cast<uintptr_t>(frow) & 15u) == 0 && seg.cap == seg.len) {
     const int n4 = seg.len / 4;
     for (int i = threadIdx.x; i < n4; i += SM_THREADS) {
-      float4 l = reinterpret_cast<const float4*>(buf)[i];
+      const float4 l = reinterpret_cast<const float4*>(buf)[i];
       const int id = seg.id0 + 4 * i;
-      const bool s0 = stays(l.x, id), s1 = stays(l.y, id + 1), s2 = stays(l.z, id + 2), s3 = stays(l.w, id + 3);
-      kept += s0 + s1 + s2 + s3;
-      l = make_float4(s0 ? l.x : SPEC_FILTERED, s1 ? l.y : SPEC_FILTERED, s2 ? l.z : SPEC_FILTERED,
-                      s3 ? l.w : SPEC_FILTERED);
-      __stcs(reinterpret_cast<float4*>(frow) + i, l);
+      __stcs(reinterpret_cast<float4*>(frow) + i,
+             make_float4(out(l.x, id), out(l.y, id + 1), out(l.z, id + 2), out(l.w, id + 3)));
     }
-    for (int i = 4 * n4 + threadIdx.x; i < seg.len; i += SM_THREADS) {
-      const bool s0 = stays(buf[i], seg.id0 + i);
-      kept += s0;
-      frow[i] = s0 ? buf[i] : SPEC_FILTERED;
-    }
+    for (int i = 4 * n4 + threadIdx.x; i < seg.len; i += SM_THREADS) frow[i] = out(buf[i], seg.id0 + i);
   } else {
-    for (int i = threadIdx.x; i < seg.len; i += SM_THREADS) {
-      const float l = seg.at(i);
-      const bool s0 = stays(l, seg.id0 + i);
-      kept += s0;
-      if (frow != nullptr) frow[i] = s0 ? l : SPEC_FILTERED;
-    }
-  }
-  if (a.n_kept != nullptr) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) kept += __shfl_xor_sync(0xffffffffu, kept, off);
-    if ((threadIdx.x & 31) == 0) sh.part32[threadIdx.x >> 5] = (uint32_t)kept;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      uint32_t all = 0;
-      for (int w = 0; w < SM_WARPS; w++) all += sh.part32[w];
-      sh.pub_c = all;
-    }
-    cl.sync();
-    if (rank == 0 && threadIdx.x == 0) {
-      uint32_t all = 0;
-      for (int q = 0; q < n; q++) all += *cl.map_shared_rank(&sh.pub_c, q);
-      a.n_kept[r] = (int)all;
-    }
-    cl.sync();  // shared memory stays until rank 0 has read it
+    for (int i = threadIdx.x; i < seg.len; i += SM_THREADS) frow[i] = out(seg.at(i), seg.id0 + i);
   }
 }
 
 }  // namespace
+
 void sample_init_attrs() {
   int dev = 0, optin = 0;
   cudaGetDevice(&dev);
