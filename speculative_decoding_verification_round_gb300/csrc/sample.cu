@@ -13,10 +13,10 @@
 // the row:
 //  - top-k: every four threads know the largest of the logits that they loaded;
 //    the k-th largest of these is a bound that at least k tokens, and
-//    typically few more, reach.  Those are collected in every
-//    CTA, which all sort them: from there on nobody has to be asked.
+//    typically few more, reach.  Those are collected in every CTA, which all
+//    find the cut among them: nobody has to be asked.
 //  - top-p alone: a histogram of masses over equal steps of z gives the step
-//    that holds the cut; its tokens are collected and sorted.
+//    that holds the cut; its tokens are collected.
 //  - a step with too many tokens (or a top-k whose bound is reached by too
 //    many) is refined by the bits of the order key, down to tokens of equal
 //    logits, whose cut is the n-th lowest id.
@@ -38,7 +38,7 @@ typedef unsigned long long u64;
 constexpr int SM_THREADS = 512;
 constexpr int SM_WARPS = SM_THREADS / 32;
 constexpr int SM_BINS = 1024;
-constexpr int SM_CAND = 2048;   // tokens that are collected and sorted
+constexpr int SM_CAND = 2048;   // tokens that are collected
 constexpr int SM_LOCAL = 1024;  // of one CTA
 constexpr int SM_MAX_CL = 16;
 constexpr int SM_GROUPS = SM_THREADS / 4;  // of a CTA: four threads each
@@ -74,10 +74,7 @@ struct alignas(16) Shared {  // the row's logits (16-byte stores) follow it
     struct {
       uint32_t cnt[SM_BINS], lo[SM_BINS], hi[SM_BINS];  // counts; masses' low 16 bits, and the rest
     };
-    struct {
-      u64 own_key[SM_LOCAL];  // this CTA's collected tokens
-      uint32_t own_w[SM_LOCAL];
-    };
+    u64 own_key[SM_LOCAL];  // this CTA's collected tokens
   };
   union {
     struct {  // until the tokens are collected
@@ -90,9 +87,10 @@ struct alignas(16) Shared {  // the row's logits (16-byte stores) follow it
     };
   };
   u64 part[SM_WARPS];
-  float warp_max[SM_WARPS];  // published at the start
+  float warp_max[SM_WARPS];
+  float cta_max;  // published at the start, with the groups'
   uint32_t own_group[SM_GROUPS];
-  uint32_t part32[2 * SM_WARPS];
+  uint32_t part32[4 * SM_WARPS];
   u64 pub_w;  // this rank's published totals of the bins, and of the draw
   uint32_t pub_c;
   u64 draw_w;
@@ -106,6 +104,9 @@ struct alignas(16) Shared {  // the row's logits (16-byte stores) follow it
     uint32_t before_c, bin_c;
   } found[2];
   Cut cut;
+  u64 list_lo, list_w;
+  uint32_t list_c;
+  int list_bin;
   int pick;
 };
 static_assert(sizeof(Shared) % 16 == 0, "the logits behind it are 16-byte aligned");
@@ -122,15 +123,31 @@ __device__ __forceinline__ u64 block_prefix(u64 v, Shared& sh, u64* total) {
   __syncthreads();
   if (lane == 31) sh.part[warp] = x;
   __syncthreads();
-  u64 before = 0, all = 0;
+  // every warp adds the warps' sums up, a lane one of them
+  u64 p = lane < SM_WARPS ? sh.part[lane] : 0;
+  const u64 own = p;
 #pragma unroll
-  for (int w = 0; w < SM_WARPS; w++) {
-    const u64 p = sh.part[w];
-    if (w < warp) before += p;
-    all += p;
+  for (int off = 1; off < SM_WARPS; off <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, p, off);
+    if (lane >= off) p += y;
   }
-  *total = all;
-  return before + x;
+  *total = __shfl_sync(0xffffffffu, p, SM_WARPS - 1);
+  return __shfl_sync(0xffffffffu, p - own, warp) + x;
+}
+
+// The ranks' values at *p: their sum, and the sum of those in front of this
+// rank; a lane reads a rank's, so that the remote loads are in flight together.
+template <class T>
+__device__ __forceinline__ T over_ranks(cg::cluster_group& cl, T* p, T* before) {
+  const int lane = threadIdx.x & 31, rank = (int)cl.block_rank();
+  T v = lane < (int)cl.num_blocks() ? *cl.map_shared_rank(p, lane) : T(0), front = lane < rank ? v : T(0);
+#pragma unroll
+  for (int off = SM_MAX_CL / 2; off > 0; off >>= 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, off);
+    front += __shfl_xor_sync(0xffffffffu, front, off);
+  }
+  *before = __shfl_sync(0xffffffffu, front, 0);
+  return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // The row's segment of this CTA.
@@ -174,11 +191,10 @@ struct Row {
   float least;  // tokens above it stay; those equal to it with ids up to last_id
   int last_id;
   uint32_t min_w;  // of those, the ones of at least this weight (2^32 as 2^32 - 1)
-  // Order key and id as one number, larger for what stands first (of equal
-  // logits the lower id): ids have 20 bits, and the lowest 12 are free for a
-  // place in a list.
+  // Order key and id (20 bits) as one number, larger for what stands first
+  // (of equal logits the lower id).
   static __device__ __forceinline__ u64 composite(uint32_t key, int id) {
-    return ((u64)key << 32) | ((uint32_t)(0xFFFFF - id) << 12);
+    return ((u64)key << 20) | (uint32_t)(0xFFFFF - id);
   }
   // x = z - max z of two logits.  z = l / T, correctly rounded: from the
   // correctly rounded reciprocal y of T, q0 = l y; q <- q + (l - q T) y twice.
@@ -231,8 +247,8 @@ struct Row {
   }
   __device__ __forceinline__ int bin(float l) const { return bin_of(x2(make_float2(l, l)).x); }
   __device__ __forceinline__ void set_cut(u64 key) {
-    least = key_value((uint32_t)(key >> 32));
-    last_id = 0xFFFFF - (int)((uint32_t)key >> 12);
+    least = key_value((uint32_t)(key >> 20));
+    last_id = 0xFFFFF - (int)(key & 0xFFFFFu);
     if (!(least > -INFINITY)) no_cut();  // a top-k beyond the finite logits
   }
   __device__ __forceinline__ void no_cut() {
@@ -281,30 +297,39 @@ __device__ int ordered_pick(cg::cluster_group& cl, Shared& sh, const Segment& se
     sh.pick = -1;
   }
   cl.sync();
-  u64 before = 0, all = 0;
-  for (int r = 0; r < n; r++) {
-    const u64 w = *cl.map_shared_rank(&sh.draw_w, r);
-    if (r < rank) before += w;
-    all += w;
-  }
-  if (counted != nullptr && rank == 0 && threadIdx.x == 0) {
-    uint32_t sum = 0;
-    for (int r = 0; r < n; r++) sum += *cl.map_shared_rank(&sh.draw_c, r);
-    *counted = sum;
+  u64 before;
+  const u64 all = over_ranks(cl, &sh.draw_w, &before);
+  if (counted != nullptr && rank == 0 && threadIdx.x < 32) {
+    uint32_t front;
+    *counted = over_ranks(cl, &sh.draw_c, &front);
   }
   const u64 t = target(all);
   const u64 hi = before + incl, lo = hi - mine;
-  if (mine > 0 && lo < t && t <= hi) {  // this thread's run holds it: at most one thread does
-    u64 run = lo;
-    for (int i = i0; i < i1; i += 2) {
-      const uint2 w = measure(pair(i), seg.id0 + i, cnt);
-      const u64 wx = widen(w.x), wy = widen(w.y);
-      if (run + wx + wy >= t) {
-        const int id = seg.id0 + i + (run + wx >= t ? 0 : 1);
-        for (int r = 0; r < n; r++) *cl.map_shared_rank(&sh.pick, r) = id;
+  // at most one thread's run holds it; its warp goes through the run, a lane a pair
+  const unsigned owner = __ballot_sync(0xffffffffu, mine > 0 && lo < t && t <= hi);
+  if (owner != 0u) {
+    const int lane = threadIdx.x & 31, who = __ffs(owner) - 1;
+    const int j0 = __shfl_sync(0xffffffffu, i0, who), j1 = __shfl_sync(0xffffffffu, i1, who);
+    u64 run = __shfl_sync(0xffffffffu, lo, who);
+    for (int base = j0; base < j1; base += 64) {
+      const int i = base + 2 * lane;
+      uint2 w = make_uint2(0u, 0u);
+      if (i < j1) w = measure(make_float2(seg.at(i), i + 1 < j1 ? seg.at(i + 1) : -INFINITY), seg.id0 + i, cnt);
+      const u64 wx = widen(w.x), both = wx + widen(w.y);
+      u64 upto = both;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, run + upto >= t);
+      if (hit != 0u) {
+        const int first = __ffs(hit) - 1;
+        const int id = __shfl_sync(0xffffffffu, seg.id0 + i + (run + upto - both + wx >= t ? 0 : 1), first);
+        if (lane < n) *cl.map_shared_rank(&sh.pick, lane) = id;
         break;
       }
-      run += wx + wy;
+      run += __shfl_sync(0xffffffffu, upto, 31);
     }
   }
   cl.sync();
@@ -327,6 +352,7 @@ __device__ void combine(cg::cluster_group& cl, Shared& sh) {
     w[k] = 0;
     cc[k] = 0;
     if (b < share)
+#pragma unroll 8
       for (int r = 0; r < n; r++) {
         if (COUNT) cc[k] += cl.map_shared_rank(sh.cnt, r)[b0 + b];
         if (MASS)
@@ -397,11 +423,10 @@ template <bool BY_COUNT>
 __device__ Found find_bin(cg::cluster_group& cl, Shared& sh, u64 target, int& turn) {
   const int rank = (int)cl.block_rank(), n = (int)cl.num_blocks();
   const int share = SM_BINS / n;
-  u64 bw = 0, bc = 0;
-  for (int r = 0; r < rank; r++) {
-    bw += *cl.map_shared_rank(&sh.pub_w, r);
-    bc += *cl.map_shared_rank(&sh.pub_c, r);
-  }
+  u64 bw;
+  uint32_t bc;
+  over_ranks(cl, &sh.pub_w, &bw);
+  over_ranks(cl, &sh.pub_c, &bc);
   const u64 base = BY_COUNT ? bc : bw;
   for (int b = threadIdx.x; b < share; b += SM_THREADS) {
     const u64 hi = base + (BY_COUNT ? (u64)sh.slice_c[b] : sh.slice_w[b]);
@@ -413,7 +438,7 @@ __device__ Found find_bin(cg::cluster_group& cl, Shared& sh, u64 target, int& tu
         auto& o = cl.map_shared_rank(&sh, r)->found[turn];
         o.bin = rank * share + b;
         o.before_w = bw + pw;
-        o.before_c = (uint32_t)bc + pc;
+        o.before_c = bc + pc;
         o.bin_c = sh.slice_c[b] - pc;
       }
     }
@@ -433,7 +458,7 @@ __device__ Found find_bin(cg::cluster_group& cl, Shared& sh, u64 target, int& tu
 template <class P>
 __device__ int collect(cg::cluster_group& cl, Shared& sh, const Segment& seg, const Row& row, bool mass,
                        P&& take) {
-  const int rank = (int)cl.block_rank(), n = (int)cl.num_blocks();
+  const int n = (int)cl.num_blocks();
   if (threadIdx.x == 0) sh.n_own = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < seg.len; i += SM_THREADS) {
@@ -442,108 +467,104 @@ __device__ int collect(cg::cluster_group& cl, Shared& sh, const Segment& seg, co
       const uint32_t at = atomicAdd(&sh.n_own, 1u);
       if (at < SM_LOCAL) {
         sh.own_key[at] = Row::composite(max_key(l), seg.id0 + i);
-        sh.own_w[at] = mass ? row.weight(l) : 0u;
       }
     }
   }
   cl.sync();  // (and the combined bins have been read, which the tokens now overwrite)
-  uint32_t before = 0, all = 0;
-  bool over = false;
-  for (int r = 0; r < n; r++) {
-    const uint32_t c = *cl.map_shared_rank(&sh.n_own, r);
-    over |= c > SM_LOCAL;
-    if (r < rank) before += c;
-    all += c;
-  }
+  uint32_t before;
+  const uint32_t all = over_ranks(cl, &sh.n_own, &before);
+  const int lane = threadIdx.x & 31;
+  const bool over = __any_sync(0xffffffffu, lane < n && *cl.map_shared_rank(&sh.n_own, min(lane, n - 1)) > SM_LOCAL);
   if (!over && all <= SM_CAND) {
+    // a thread has a token and a part of the ranks
     const int own = (int)sh.n_own;
-    for (int e = threadIdx.x; e < own * n; e += SM_THREADS) {
-      const int r = e / own, c = e - r * own;
-      Shared& o = *cl.map_shared_rank(&sh, r);
-      o.key[before + c] = sh.own_key[c] | (before + c);
-      o.w[before + c] = sh.own_w[c];
+    int parts = 1;
+    while (parts < n && own * parts * 2 <= SM_THREADS) parts *= 2;
+    for (int e = threadIdx.x; e < own * parts; e += SM_THREADS) {
+      const int c = e / parts;
+      const u64 key = sh.own_key[c];
+      const uint32_t w = mass ? row.weight(key_value((uint32_t)(key >> 20))) : 0u;
+      for (int r = e % parts; r < n; r += parts) {
+        Shared& o = *cl.map_shared_rank(&sh, r);
+        o.key[before + c] = key;
+        o.w[before + c] = w;
+      }
     }
   }
   cl.sync();
   return over ? SM_CAND + 1 : (int)all;
 }
 
-// Sorts sh.key[0, SM_THREADS E) from the largest down: a bitonic network on
-// registers, E numbers a thread; partners in other warps meet in shared memory.
-template <int E>
-__device__ void sort_keys(Shared& sh) {
-  const int tid = threadIdx.x;
-  u64 v[E];
-#pragma unroll
-  for (int e = 0; e < E; e++) v[e] = sh.key[tid * E + e];
-#pragma unroll 1
-  for (int k = 2; k <= SM_THREADS * E; k *= 2) {
-#pragma unroll 1
-    for (int d = k >> 1; d >= E; d >>= 1) {
-      if (d >= 32 * E) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < E; e++) sh.key[tid * E + e] = v[e];
-        __syncthreads();
-      }
-#pragma unroll
-      for (int e = 0; e < E; e++) {
-        const int i = tid * E + e;
-        const u64 o = d >= 32 * E ? sh.key[i ^ d] : __shfl_xor_sync(0xffffffffu, v[e], d / E);
-        const bool larger = ((i & d) == 0) == ((i & k) == 0);  // of the two, this place gets
-        v[e] = (o > v[e]) == larger ? o : v[e];
+// Of the m collected tokens, the one at which the running count or mass, in
+// the order of their composite keys, reaches `target`; `mass` gets the sum of
+// the masses up to it.  Radix selection, nine bits a step, from the first of
+// the `open` low bits in which the keys may differ (prefix: those above);
+// ends at the first step that leaves one token.
+constexpr int LIST_BITS = 9, LIST_BINS = 1 << LIST_BITS;
+static_assert(LIST_BINS == SM_THREADS, "a bin a thread");
+__device__ Cut cut_list(Shared& sh, int m, bool by_count, bool masses, u64 target, int open, u64 prefix) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  u64 left = target, before = 0;
+  while (open > 0) {
+    const int down = max(0, open - LIST_BITS), bits = open - down;
+    sh.cnt[tid] = 0u;
+    if (masses) sh.lo[tid] = sh.hi[tid] = 0u;
+    __syncthreads();
+    for (int i = tid; i < m; i += SM_THREADS) {
+      const u64 key = sh.key[i];
+      if ((key >> open) == prefix) {
+        const int b = LIST_BINS - 1 - (int)((key >> down) & ((1u << bits) - 1u));
+        atomicAdd(&sh.cnt[b], 1u);
+        if (masses) add_mass(sh, b, sh.w[i]);
       }
     }
+    __syncthreads();
+    const uint32_t c = sh.cnt[tid];
+    const u64 w = masses ? ((u64)sh.hi[tid] << 16) + sh.lo[tid] : 0;
+    uint32_t rc = c;
+    u64 rw = w;
 #pragma unroll
-    for (int d = E / 2; d > 0; d >>= 1)
-      if (d < k)
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, rc, off);
+      if (lane >= off) rc += x;
+    }
+    if (masses)
 #pragma unroll
-        for (int e = 0; e < E; e++)
-          if ((e & d) == 0) {
-            const bool down = ((tid * E + e) & k) == 0;
-            const u64 x = v[e], y = v[e | d];
-            if ((x < y) == down) v[e] = y, v[e | d] = x;
-          }
+      for (int off = 1; off < 32; off <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, rw, off);
+        if (lane >= off) rw += y;
+      }
+    if (lane == 31) {
+      sh.part32[warp] = rc;
+      sh.part[warp] = rw;
+    }
+    __syncthreads();
+    rc += __reduce_add_sync(0xffffffffu, lane < warp ? sh.part32[lane] : 0u);
+    if (masses) {
+      u64 front = lane < warp ? sh.part[lane] : 0;
+#pragma unroll
+      for (int off = SM_WARPS / 2; off > 0; off >>= 1) front += __shfl_xor_sync(0xffffffffu, front, off);
+      rw += __shfl_sync(0xffffffffu, front, 0);
+    }
+    const u64 hi = by_count ? rc : rw, lo = hi - (by_count ? c : w);
+    if (lo < left && left <= hi) {
+      sh.list_bin = tid;
+      sh.list_lo = lo;
+      sh.list_w = rw - w;
+      sh.list_c = c;
+    }
+    __syncthreads();
+    prefix = (prefix << bits) | (u64)(LIST_BINS - 1 - sh.list_bin);
+    left -= sh.list_lo;
+    before += sh.list_w;
+    open = down;
+    if (sh.list_c == 1) break;
   }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < E; e++) sh.key[tid * E + e] = v[e];
-  __syncthreads();
-}
-
-// Sorts the m collected tokens, the first in the order first.
-__device__ void sort_list(Shared& sh, int m) {
-  const int size = m <= SM_THREADS ? SM_THREADS : SM_CAND;
-  for (int i = m + (int)threadIdx.x; i < size; i += SM_THREADS) sh.key[i] = 0;  // behind every token
-  __syncthreads();
-  if (size == SM_THREADS)
-    sort_keys<1>(sh);
-  else
-    sort_keys<SM_CAND / SM_THREADS>(sh);
-}
-
-// Of the sorted list: the cut of a count (by_count) or of a mass.  `mass`
-// gets the sum up to it.
-__device__ Cut cut_list(Shared& sh, int m, bool by_count, u64 target) {
-  constexpr int PER = SM_CAND / SM_THREADS;
-  u64 w[PER], mine = 0;
-#pragma unroll
-  for (int e = 0; e < PER; e++) {
-    const int i = (int)threadIdx.x * PER + e;
-    w[e] = i < m ? widen(sh.w[sh.key[i] & 0xFFFu]) : 0;
-    mine += w[e];
-  }
-  u64 all, run = block_prefix(mine, sh, &all) - mine;
-#pragma unroll
-  for (int e = 0; e < PER; e++) {
-    const int i = (int)threadIdx.x * PER + e;
-    const u64 before = run;
-    run += w[e];
-    if (i < m && (by_count ? (u64)i + 1 == target : before < target && target <= run)) {
+  for (int i = tid; i < m; i += SM_THREADS)
+    if ((sh.key[i] >> open) == prefix) {  // one token
       sh.cut.key = sh.key[i];
-      sh.cut.mass = run;
+      sh.cut.mass = before + (masses ? widen(sh.w[i]) : 0);
     }
-  }
   __syncthreads();
   const Cut c = sh.cut;
   __syncthreads();
@@ -603,8 +624,7 @@ __device__ Cut find_cut(cg::cluster_group& cl, Shared& sh, const Segment& seg, c
     cut.mass = before_w + nth * w;
     return cut;
   }
-  sort_list(sh, m);
-  cut = cut_list(sh, m, BY_COUNT, left);
+  cut = cut_list(sh, m, BY_COUNT, true, left, 20 + known, known >= 32 ? 0u : prefix);
   cut.mass += before_w;
   return cut;
 }
@@ -683,17 +703,24 @@ sample_kernel(const SampleArgs a) {
   }
   if ((threadIdx.x & 3) == 0) sh.own_group[threadIdx.x >> 2] = max_key(gmx);
   if ((threadIdx.x & 31) == 0) sh.warp_max[threadIdx.x >> 5] = wmx;
-  cl.sync();
-  float top = -INFINITY;
-  for (int e = threadIdx.x & 31; e < n * SM_WARPS; e += 32) {
-    const float o = cl.map_shared_rank(sh.warp_max, e / SM_WARPS)[e % SM_WARPS];
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(o));
-  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    wmx = threadIdx.x < SM_WARPS ? sh.warp_max[threadIdx.x] : -INFINITY;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
+    for (int off = SM_WARPS / 2; off > 0; off >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, wmx, off);
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(wmx) : "f"(o));
+    }
+    if (threadIdx.x == 0) sh.cta_max = wmx;
+  }
+  cl.sync();
+  float top = (int)(threadIdx.x & 31) < n ? *cl.map_shared_rank(&sh.cta_max, threadIdx.x & 31) : -INFINITY;
+#pragma unroll
+  for (int off = SM_MAX_CL / 2; off > 0; off >>= 1) {
     const float o = __shfl_xor_sync(0xffffffffu, top, off);
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(o));
   }
+  top = __shfl_sync(0xffffffffu, top, 0);
   row.zmax = row_zmax(max_key(top), row.T);
   bad |= !(fabsf(top) < INFINITY) || !(fabsf(row.zmax) < INFINITY);  // NaN, +inf, nothing but -inf
   float* frow = a.filtered != nullptr ? a.filtered + (int64_t)r * a.ldf + seg.id0 : nullptr;
@@ -732,19 +759,27 @@ sample_kernel(const SampleArgs a) {
         mine[e] = g < groups ? cl.map_shared_rank(sh.own_group, g / SM_GROUPS)[g % SM_GROUPS] : 0u;
       }
       uint32_t low = 0u;
-      for (int bit = 31; bit >= 12; bit--) {
-        const uint32_t at = low | (1u << bit);
-        int c = 0;
+      for (int bit = 30; bit >= 12; bit -= 2) {
+        uint32_t c12 = 0, c3 = 0;  // at least low + 1, 2, 3 steps
 #pragma unroll
-        for (int e = 0; e < PER; e++) c += mine[e] >= at;
-        c = __reduce_add_sync(0xffffffffu, c);
-        uint32_t* part = sh.part32 + (bit & 1) * SM_WARPS;  // two, in turn: one barrier a bit
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = (uint32_t)c;
+        for (int e = 0; e < PER; e++) {
+          c12 += mine[e] >= (low | (1u << bit)) ? 1u : 0u;
+          c12 += mine[e] >= (low | (2u << bit)) ? 1u << 16 : 0u;
+          c3 += mine[e] >= (low | (3u << bit)) ? 1u : 0u;
+        }
+        c12 = __reduce_add_sync(0xffffffffu, c12);
+        c3 = __reduce_add_sync(0xffffffffu, c3);
+        uint32_t* part = sh.part32 + (bit & 2) * SM_WARPS;  // two, in turn: one barrier a step
+        if ((threadIdx.x & 31) == 0) {
+          part[threadIdx.x >> 5] = c12;
+          part[SM_WARPS + (threadIdx.x >> 5)] = c3;
+        }
         __syncthreads();
-        uint32_t all = 0;
-#pragma unroll
-        for (int w = 0; w < SM_WARPS; w++) all += part[w];
-        if (all >= (uint32_t)k) low = at;
+        const int lane = threadIdx.x & 31;
+        c12 = __reduce_add_sync(0xffffffffu, lane < SM_WARPS ? part[lane] : 0u);
+        c3 = __reduce_add_sync(0xffffffffu, lane < SM_WARPS ? part[SM_WARPS + lane] : 0u);
+        const uint32_t step = c3 >= (uint32_t)k ? 3u : (c12 >> 16) >= (uint32_t)k ? 2u : (c12 & 0xFFFFu) >= (uint32_t)k ? 1u : 0u;
+        low |= step << bit;
       }
       // -inf or below: fewer than k groups have a finite logit
       if (low > 0x007FFFFFu) bound = key_value(low);
@@ -765,9 +800,16 @@ sample_kernel(const SampleArgs a) {
     else if (bin >= 0)
       m = collect(cl, sh, seg, row, by_p, [&](float l) { return row.bin(l) <= bin; });
     if (m <= SM_CAND) {
-      sort_list(sh, m);
-      Cut c = cut_list(sh, m, true, (u64)k);
-      if (by_p) c = cut_list(sh, m, false, mass_needed(P, c.mass));
+      // the keys agree above the first bit in which the bound and the largest differ
+      int open = 32;
+      u64 prefix = 0;
+      if (bound > -INFINITY) {
+        const uint32_t hi = max_key(top), lo = max_key(bound);
+        open = 32 - __clz(hi ^ lo);
+        prefix = open < 32 ? hi >> open : 0u;
+      }
+      Cut c = cut_list(sh, m, true, by_p, (u64)k, 20 + open, prefix);
+      if (by_p) c = cut_list(sh, m, false, true, mass_needed(P, c.mass), 20 + open, prefix);
       row.set_cut(c.key);
       done = true;
     }
@@ -782,8 +824,8 @@ sample_kernel(const SampleArgs a) {
     }
     if (by_p) {
       histogram<false>(cl, sh, seg, row);
-      if (!by_k)
-        for (int q = 0; q < n; q++) S += *cl.map_shared_rank(&sh.pub_w, q);
+      u64 front;
+      if (!by_k) S = over_ranks(cl, &sh.pub_w, &front);
       row.set_cut(find_cut<false>(cl, sh, seg, row, mass_needed(P, S), turn).key);
     }
   }
