@@ -106,6 +106,8 @@ _lock = threading.Lock()
 def lib():
     """The loaded C library.  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -187,16 +189,27 @@ def _check(rc: int):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_current_raw_stream = None  # torch's current stream as an address
 
 
 def _stream(stream):
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    """A stream as an address (None: torch's current one)."""
+    if stream is not None:
+        return stream.cuda_stream
+    global _current_raw_stream
+    if _current_raw_stream is None:
+        import torch
+        c = torch._C
+        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+            torch.cuda.current_stream()  # (initialises CUDA)
+            raw, device = c._cuda_getCurrentRawStream, c._cuda_getDevice
+            _current_raw_stream = lambda: raw(device())  # noqa: E731
+        else:
+            _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_raw_stream()
 
 
 def _qweight(w: dict) -> spec_qweight:
