@@ -641,13 +641,19 @@ int spec_accept_tree(const int32_t* argmax, const int32_t* tokens, const int32_t
  *           spec_accept_stochastic as p_logits / q_logits, filtered rows
  *           make its rejection sampling lossless for the filtered
  *           distributions
+ *   workspace  spec_sample_workspace bytes, 16-byte aligned (NULL if that is
+ *           0: few or short rows); its contents do not matter before and
+ *           after the call
  * A row with a NaN or +infinity, without any finite logit, whose largest
  * l / T overflows, or with a setting out of range gets token -1, n_kept 0 and a filtered row of NaN (which
  * spec_accept_stochastic refuses). */
 int spec_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u,
                 const float* temperature, const int32_t* top_k, const float* top_p,
                 const float* min_p, int32_t* token, int32_t* n_kept, float* filtered,
-                int64_t ld_filtered, void* stream);
+                int64_t ld_filtered, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for spec_sample of R rows of V logits. */
+int spec_sample_workspace(int R, int V, size_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -46,7 +46,8 @@ EXPORTED = ["spec_last_error", "spec_qmat_create", "spec_qmat_destroy", "spec_li
             "spec_depth_ctl_destroy", "spec_depth_ctl_next", "spec_depth_ctl_observe",
             "spec_depth_ctl_estimates", "spec_model_pages", "spec_pages_copy", "spec_pages_fork",
             "spec_pages_extend", "spec_pages_commit", "spec_pages_free", "spec_tree_attn",
-            "spec_tree_attn_workspace", "spec_accept_tree", "spec_sample"]
+            "spec_tree_attn_workspace", "spec_accept_tree", "spec_sample",
+            "spec_sample_workspace"]
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
@@ -167,7 +168,8 @@ def lib():
                 "spec_tree_attn": (I32, [P, I32, P, P, I64, P, P, I64, P, P, SZ, P, P]),
                 "spec_tree_attn_workspace": (I32, [P, I32, I32, I32, P]),
                 "spec_accept_tree": (I32, [P, P, P, P, I32, I32, P, P, P, P]),
-                "spec_sample": (I32, [P, I32, I32, I64, P, P, P, P, P, P, P, P, I64, P]),
+                "spec_sample": (I32, [P, I32, I32, I64, P, P, P, P, P, P, P, P, I64, P, SZ, P]),
+                "spec_sample_workspace": (I32, [I32, I32, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -625,11 +627,30 @@ def spec_accept_tree(argmax, tokens, parents, n_nodes, n_seq: int, nt: int, path
                                   _stream(stream)))
 
 
+def spec_sample_workspace(R: int, V: int) -> int:
+    """Bytes of workspace that spec_sample needs for R rows of V logits (0: none)."""
+    b = SZ()
+    _check(lib().spec_sample_workspace(int(R), int(V), ctypes.byref(b)))
+    return b.value
+
+
 def spec_sample(logits, R: int, V: int, u, token, temperature=None, top_k=None, top_p=None,
                 min_p=None, n_kept=None, filtered=None, ld: int = 0, ld_filtered: int = 0,
-                stream=None):
+                workspace=None, stream=None):
     """One token per row from the random words u after temperature, top-k,
-    top-p and min-p; filtered: the logits that stayed (SPEC_FILTERED elsewhere)."""
+    top-p and min-p; filtered: the logits that stayed (SPEC_FILTERED elsewhere).
+    workspace: a tensor of spec_sample_workspace bytes (None: taken from
+    torch's allocator for the call where one is needed)."""
+    n = 0
+    if workspace is not None:
+        n = workspace.numel() * workspace.element_size()
+    elif R * V > 4000000:  # (below, no call needs one)
+        n = spec_sample_workspace(R, V)
+        if n > 0:
+            import torch
+            workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
+            if stream is not None:
+                workspace.record_stream(stream)
     _check(lib().spec_sample(_ptr(logits), int(R), int(V), int(ld), _ptr(u), _ptr(temperature),
                              _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(n_kept),
-                             _ptr(filtered), int(ld_filtered), _stream(stream)))
+                             _ptr(filtered), int(ld_filtered), _ptr(workspace), n, _stream(stream)))

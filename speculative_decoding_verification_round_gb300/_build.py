@@ -16,11 +16,13 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libspecverify.so")
 SOURCES = ["api.cu", "linear.cu", "tcgemm.cu", "attn.cu", "ops.cu", "accept.cu", "depth.cu",
-           "pages.cu", "tree_attn.cu", "tree_attn_tc.cu", "sample.cu"]
+           "pages.cu", "tree_attn.cu", "tree_attn_tc.cu", "sample.cu",
+           "sample_rows.cu"]
 # host code whose doubles must be rounded operation by operation
 FILE_FLAGS = {"depth.cu": ["-Xcompiler", "-ffp-contract=off"]}
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "tc_ops.cuh"),
            os.path.join(CSRC, "sampler.cuh"), os.path.join(CSRC, "tree_attn.cuh"),
+           os.path.join(CSRC, "sample.cuh"),
            os.path.join(os.path.dirname(HERE), "include", "spec_verify.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")

@@ -1204,10 +1204,18 @@ extern "C" int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* 
                      as_stream(stream));
 }
 
+extern "C" int spec_sample_workspace(int R, int V, size_t* bytes) {
+  if (bytes == nullptr) return fail(SPEC_E_INVALID, "null argument");
+  if (R < 1 || V < 1 || R > (1 << 26) || V > 1048512)
+    return fail(SPEC_E_SHAPE, "R in [1, 2^26] and V in [1, 1048512] required");
+  *bytes = sample_bytes(R, V);
+  return SPEC_OK;
+}
+
 extern "C" int spec_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u,
                            const float* temperature, const int32_t* top_k, const float* top_p,
                            const float* min_p, int32_t* token, int32_t* n_kept, float* filtered,
-                           int64_t ld_filtered, void* stream) {
+                           int64_t ld_filtered, void* workspace, size_t workspace_bytes, void* stream) {
   if (logits == nullptr || u == nullptr || token == nullptr)
     return fail(SPEC_E_INVALID, "null argument");
   if (R < 1 || V < 1 || R > (1 << 26) || V > 1048512)
@@ -1224,7 +1232,10 @@ extern "C" int spec_sample(const float* logits, int R, int V, int64_t ld, const 
     if (overlaps(filtered, outb, logits, in))
       return fail(SPEC_E_INVALID, "filtered overlaps logits without being logits");
   }
+  const size_t need = sample_bytes(R, V);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
+    return fail(SPEC_E_SHAPE, "16-byte aligned workspace of " + std::to_string(need) + " bytes required");
   init_attrs_once();
   return launch_sample(logits, R, V, ld, u, temperature, top_k, top_p, min_p, token, n_kept, filtered,
-                       ld_filtered, as_stream(stream));
+                       ld_filtered, workspace, as_stream(stream));
 }

@@ -266,7 +266,8 @@ int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint1
 int launch_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u,
                   const float* temperature, const int32_t* top_k, const float* top_p,
                   const float* min_p, int32_t* token, int32_t* n_kept, float* filtered, int64_t ldf,
-                  cudaStream_t st);
+                  void* workspace, cudaStream_t st);
+size_t sample_bytes(int R, int V);
 
 // Whether kernels that can overlap their predecessor's tail are launched as
 // programmatic dependents (default on; SPEC_VERIFY_PDL=0 in the environment

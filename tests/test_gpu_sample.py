@@ -175,6 +175,101 @@ def test_rows_beyond_shared_memory(orc, dev):
     check(orc, dev, logits, u, T, k, p, m, in_place=True, off=1)
 
 
+def many(g, R, V, scale=2.0):
+    logits = (g.standard_normal((R, V)) * scale).astype(np.float32)
+    return logits, g.integers(0, 2 ** 32, R, dtype=np.uint64)
+
+
+@pytest.mark.parametrize("R,V,ld,off,in_place", [(100, 40003, 0, 0, False), (244, 16500, 16501, 1, True),
+                                                 (5, 1000001, 0, 2, True), (126, 32000, 32004, 0, True)])
+def test_many_long_rows(orc, dev, R, V, ld, off, in_place):
+    """Enough logits for passes over all rows: kinds mixed, strides and
+    alignments, the last segment and the last group of 128 cut short."""
+    import speculative_decoding_verification_round_gb300 as sv
+    assert sv.spec_sample_workspace(R, V) > 0
+    g = np.random.default_rng([20, V])
+    logits, u = many(g, R, V)
+    logits *= g.choice([0.1, 1.0, 3.0], (R, 1)).astype(np.float32)  # flat rows, too: long lists
+    T, k, p, m = settings(g, R, V)
+    T[:2], k[:2], p[:2], m[:2] = 1, [0, 2000], [0.9999, 1.0], 0
+    check(orc, dev, logits, u, T, k, p, m, ld=ld, off=off, in_place=in_place)
+
+
+def test_many_long_rows_of_equal_masked_and_bad_logits(orc, dev):
+    """Rows whose tokens do not fit the list (all of them equal, or of two
+    values, or with all large ones in one place), rows with one token left,
+    and refused ones between."""
+    g = np.random.default_rng(21)
+    R, V = 112, 36000
+    logits, u = many(g, R, V)
+    T, k, p, m = settings(g, R, V)
+    T = np.where(T == 0, np.float32(0), np.maximum(T, np.float32(1.0)))
+    for r in range(0, R, 2):
+        if r % 14 == 0:
+            logits[r] = 1.5
+        elif r % 14 == 2:
+            logits[r] = g.integers(0, 2, V)
+        elif r % 14 == 4:
+            logits[r].sort()
+        elif r % 14 == 6:
+            logits[r, g.permutation(V)[:V - 1]] = [-np.inf, LOW][r // 14 % 2]
+        elif r % 14 == 8:
+            logits[r, :V - 5000] = -np.inf
+        elif r % 14 == 10:
+            logits[r, g.permutation(V)[:200]] = [0.0, -0.0] * 100
+            logits[r] = np.minimum(logits[r], 0)
+    check(orc, dev, logits, u, T, k, p, m)
+    good = run(dev, logits, u, T, k, p, m)
+    bad = [1, 17, 39, 61, 83, 111]
+    logits[1, V - 1], logits[17, 0], logits[39] = np.nan, np.inf, -np.inf
+    T[61], k[83], p[111] = -1, -1, np.nan
+    tok, kept, filt = run(dev, logits, u, T, k, p, m)
+    assert (tok[bad] == -1).all() and (kept[bad] == 0).all() and np.isnan(filt[bad]).all()
+    rest = np.setdiff1d(np.arange(R), bad)
+    assert np.array_equal(tok[rest], good[0][rest]) and np.array_equal(kept[rest], good[1][rest])
+    assert np.array_equal(filt[rest], good[2][rest])
+
+
+def test_many_long_rows_replayed_and_on_two_streams(orc, dev):
+    """Two graphs with a workspace each, replayed at once on two streams; and
+    calls without one, whose workspace is the allocator's."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(22)
+    R, V = 130, 31999
+    sides = []
+    for s in range(2):
+        logits, u = many(g, R, V)
+        T, k, p, m = settings(g, R, V)
+        want = [tree.sample_row(logits[r], orc.row_weights, u[r], float(T[r]), int(k[r]), p[r], m[r])[0] for r in range(R)]
+        c = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+        x = (c(logits), R, V, c(u.astype(np.uint32).view(np.int32)), torch.zeros(R, dtype=torch.int32, device=dev),
+             c(T), c(k), c(p), c(m))
+        ws = torch.empty(sv.spec_sample_workspace(R, V), dtype=torch.uint8, device=dev)
+        st = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=st):
+            sv.spec_sample(*x, workspace=ws)
+        sides.append((x, ws, st, graph, want))
+    for _ in range(5):
+        for x, _, st, graph, _ in sides:
+            with torch.cuda.stream(st):
+                x[4].zero_()
+                graph.replay()
+    torch.cuda.synchronize()
+    assert all(x[4].tolist() == want for x, _, _, _, want in sides)
+    for x, _, st, _, _ in sides:
+        with torch.cuda.stream(st):
+            x[4].zero_()
+            sv.spec_sample(*x)
+    for x, _, st, _, _ in sides:  # the stream as an argument
+        x[4].record_stream(st)
+        sv.spec_sample(*x, stream=st)
+    torch.cuda.synchronize()
+    assert all(x[4].tolist() == want for x, _, _, _, want in sides)
+
+
 def test_filtered_logits_feed_the_rejection_sampler(orc, dev):
     """Drafts sampled under filters, target rows filtered alike: the accept of
     the filtered rows is the oracle's, and no emitted token was filtered out."""

@@ -232,10 +232,12 @@ def test_sample_refuses_bad_arguments(sv):
     L = sv.lib()
 
     def call(logits=A, R=2, V=100, ld=0, u=A, token=A, filtered=None, ldf=0):
-        return L.spec_sample(logits, R, V, ld, u, None, None, None, None, token, None, filtered, ldf, None)
+        return L.spec_sample(logits, R, V, ld, u, None, None, None, None, token, None, filtered, ldf, None, 0, None)
     for kw in (dict(logits=None), dict(u=None), dict(token=None)):
         assert call(**kw) == sv.SPEC_E_INVALID
     for kw in (dict(R=0), dict(V=0), dict(V=1048513, ld=1 << 21), dict(ld=99), dict(filtered=A + (1 << 16), ldf=50), dict(logits=A + 2)):
         assert call(**kw) == sv.SPEC_E_SHAPE, kw
+    assert call(R=192, V=248320) == sv.SPEC_E_SHAPE and "workspace" in sv.last_error()
+    assert sv.spec_sample_workspace(1, 151936) == 0 and sv.spec_sample_workspace(192, 248320) > 0
     assert call(filtered=A + 4) == sv.SPEC_E_INVALID  # half over the logits
     assert call(filtered=A, ld=100, ldf=104) == sv.SPEC_E_INVALID  # the logits with another stride
