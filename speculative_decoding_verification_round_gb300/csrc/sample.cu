@@ -31,6 +31,16 @@ namespace cg = cooperative_groups;
 namespace {
 
 struct alignas(16) Shared : ListSmem {  // the row's logits (16-byte stores) follow it
+  union {
+    struct {  // until the tokens are collected
+      u64 slice_w[SM_BINS];  // this rank's share of the combined bins: inclusive sums
+      uint32_t slice_c[SM_BINS];
+    };
+    struct {
+      u64 key[SM_CAND];     // the row's collected tokens
+      uint32_t w[SM_CAND];  // their weights, 2^32 as 2^32 - 1 (which no other weight is)
+    };
+  };
   float warp_max[SM_WARPS];
   float cta_max;  // published at the start, with the groups'
   uint32_t own_group[SM_GROUPS];

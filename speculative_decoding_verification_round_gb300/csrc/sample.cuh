@@ -64,16 +64,6 @@ struct ListSmem {
     };
     u64 own_key[SM_LOCAL];  // this CTA's collected tokens
   };
-  union {
-    struct {  // until the tokens are collected
-      u64 slice_w[SM_BINS];  // this rank's share of the combined bins: inclusive sums
-      uint32_t slice_c[SM_BINS];
-    };
-    struct {
-      u64 key[SM_CAND];     // the row's collected tokens
-      uint32_t w[SM_CAND];  // their weights, 2^32 as 2^32 - 1 (which no other weight is)
-    };
-  };
   u64 part[SM_WARPS];
   uint32_t part32[4 * SM_WARPS];
   Cut cut;

@@ -7,52 +7,64 @@
 // other filters), top-p alone, or neither.  Streaming passes have a CTA per
 // 8192 logits of a row, a warp per 1024 of them; between them a CTA per row
 // decides.
-//   maxima   stream: the largest logit of every 128
+//   maxima   stream: the largest logit of every 128, and of every 16
 //   bound    row: the largest, the settings, and for a top-k a bound that at
-//            least k of the groups of 128 reach
-//   pass     stream: top-k rows collect the tokens at the bound; top-p rows
-//            add their masses up over steps of z; the others over 1024 ids
+//            least k of these groups reach
+//   pass     stream: top-k rows collect the tokens at the bound (only blocks
+//            of 128 that reach it are read); top-p rows add their masses up
+//            over steps of z; the others over 1024 ids
 //   cut      row: top-k rows find their cut among the collected tokens and
 //            draw from them; rows without filters draw; top-p rows find the
 //            step that holds their cut
 //   step     stream, top-p rows: the masses above that step over 1024 ids,
 //            its tokens collected
 //   draw     row, top-p rows: the cut, and the draw
-//   filter   stream, where filtered logits are wanted
+//   filter   stream, where filtered logits are wanted: blocks below the cut
+//            are written without being read
 // A row that collects too many tokens goes to the clusters of sample.cu as a
-// whole.  Each kernel is a programmatic dependent of the one in front of it.
+// whole.  Each kernel is a programmatic dependent of the one in front of it,
+// and every other stream runs from the last row to the first, to find in L2
+// what the one before read last.
 #include <algorithm>
 
 #include "sample.cuh"
 
 namespace {
 
-constexpr int SR_GROUP = 128;   // logits whose largest is kept
+constexpr int SR_BLOCK = 128;   // logits of a warp's load
+// Groups whose largest bound a top-k: blocks, or up to SR_FEW logits (where
+// blocks are too few for a k of some hundreds) the 16 of four lanes.
+constexpr int SR_FEW = 131072;
+constexpr int SR_MAX_GROUPS = 8192;
 constexpr int SR_RANGE = 1024;  // logits of a warp, and ids whose mass is kept
 constexpr int SR_WARPS = 8;
 constexpr int SR_THREADS = 32 * SR_WARPS;
 constexpr int SR_SEG = SR_RANGE * SR_WARPS;
-constexpr int SR_LIST = 8192;   // tokens that are collected of a row
+constexpr int SR_LIST = 4096;   // tokens that are collected of a row
 constexpr int SR_MAX_K = 2048;  // of a top-k by a bound, so that these are enough mostly
 constexpr int SR_MAX_RANGES = 1024;
+constexpr int SR_BOUND_BITS = 9, SR_BOUND_BINS = 1 << SR_BOUND_BITS;
+static_assert(SR_BOUND_BINS == SM_THREADS, "a bin a thread");
 constexpr int SR_HARD_CLUSTERS = 16;
 
 enum RowKind : int { ROW_BAD, ROW_PLAIN, ROW_TOP_K, ROW_TOP_P, ROW_HARD };
 
 struct RowState {
   Row row;  // least, last_id: the cut, once `done`
-  float top, bound;
+  float top;
+  float bound;   // top-k: tokens from here on are collected; top-p: from here on up to
+  float summed;  // here, and from here on their masses are summed up
   int kind, k;
   u64 P;
   u64 left;  // top-p: the mass to reach inside the step
-  int bin;
   uint32_t listed;
 };
 
 // One row's workspace.
 struct RowSpace {
   RowState* state;
-  uint32_t* group;  // order keys
+  uint32_t* block;  // order keys of the largest of SR_BLOCK logits
+  uint32_t* group;  // and of each group (the same where a block is one)
   u64* mass;        // top-p: over SM_BINS steps of z
   u64* key;         // collected tokens
   uint32_t* w;
@@ -64,7 +76,8 @@ struct Spaces {
   char* base;
   int32_t* hard;  // rows for the clusters, and their number in front
   size_t stride;  // bytes of a row
-  int groups, ranges;
+  int blocks, groups, ranges;
+  int per;  // groups of a block: 1 or 8
   __host__ __device__ static size_t up(size_t b) { return (b + 127) / 128 * 128; }
   __host__ __device__ RowSpace row(int r) const {
     RowSpace s;
@@ -81,49 +94,79 @@ struct Spaces {
     p += up(sizeof(u64) * ranges);
     s.range_c = reinterpret_cast<uint32_t*>(p);
     p += up(sizeof(uint32_t) * ranges);
-    s.group = reinterpret_cast<uint32_t*>(p);
+    s.block = reinterpret_cast<uint32_t*>(p);
+    s.group = per == 1 ? s.block : s.block + blocks;
     return s;
   }
 };
 
 Spaces spaces(void* workspace, int R, int V) {
   Spaces s;
-  s.groups = (V + SR_GROUP - 1) / SR_GROUP;
+  s.per = V > SR_FEW ? 1 : 8;
+  s.blocks = (V + SR_BLOCK - 1) / SR_BLOCK;
+  s.groups = s.blocks * s.per;
   s.ranges = (V + SR_RANGE - 1) / SR_RANGE;
   s.stride = Spaces::up(sizeof(RowState)) + Spaces::up(sizeof(u64) * SM_BINS) + Spaces::up(sizeof(u64) * SR_LIST) +
              Spaces::up(sizeof(uint32_t) * SR_LIST) + Spaces::up(sizeof(u64) * s.ranges) +
-             Spaces::up(sizeof(uint32_t) * s.ranges) + Spaces::up(sizeof(uint32_t) * s.groups);
+             Spaces::up(sizeof(uint32_t) * s.ranges) + Spaces::up(sizeof(uint32_t) * (s.blocks + s.groups));
   s.hard = reinterpret_cast<int32_t*>(workspace);
   s.base = reinterpret_cast<char*>(workspace) + Spaces::up(sizeof(int32_t) * ((size_t)R + 1));
   return s;
 }
 
-// Up to four logits of the 128 from id g0 on, for this lane: ids g0 + 4 lane
-// .. (16-byte loads) where the row is aligned, else g0 + lane + 32 e.
-struct Quad {
-  float l[4];
-  int id[4];
-};
-__device__ __forceinline__ Quad load_quad(const float* row, bool aligned, int g0, int V, int lane) {
-  Quad q;
-  if (aligned && g0 + SR_GROUP <= V) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(row + g0) + lane);
-    q.l[0] = v.x, q.l[1] = v.y, q.l[2] = v.z, q.l[3] = v.w;
+// A lane's four logits of each of the warp's blocks, from id v0 on: ids
+// 4 lane .. of a block (16-byte loads) where the rows are aligned and the block
+// is whole, else lane + 32 e.
+constexpr int SR_BLOCKS = SR_RANGE / SR_BLOCK;  // of a warp
+struct Logits {
+  float4 l[SR_BLOCKS];
+  int v0, V, lane;
+  bool aligned;
+  __device__ __forceinline__ Logits(const void* row, int v0_, int V_)
+      : v0(v0_), V(V_), lane(threadIdx.x & 31), aligned((reinterpret_cast<uintptr_t>(row) & 15u) == 0) {}
+  __device__ __forceinline__ bool whole(int g) const { return aligned && v0 + (g + 1) * SR_BLOCK <= V; }
+  __device__ __forceinline__ int id(int g, int e) const {
+    return v0 + g * SR_BLOCK + (whole(g) ? 4 * lane + e : lane + 32 * e);
+  }
+  // the blocks of `which` (a bit each)
+  __device__ __forceinline__ void load(const float* row, uint32_t which) {
+    if (which == (1u << SR_BLOCKS) - 1u && whole(SR_BLOCKS - 1)) {
 #pragma unroll
-    for (int e = 0; e < 4; e++) q.id[e] = g0 + 4 * lane + e;
-  } else {
+      for (int g = 0; g < SR_BLOCKS; g++) l[g] = reinterpret_cast<const float4*>(row + v0 + g * SR_BLOCK)[lane];
+      return;
+    }
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-      q.id[e] = g0 + lane + 32 * e;
-      q.l[e] = q.id[e] < V ? __ldcs(row + q.id[e]) : -INFINITY;
+    for (int g = 0; g < SR_BLOCKS; g++) {
+      l[g] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (which >> g & 1u) {
+        if (whole(g)) {
+          l[g] = reinterpret_cast<const float4*>(row + v0 + g * SR_BLOCK)[lane];
+        } else {
+          const int at = v0 + g * SR_BLOCK + lane;
+          if (at < V) l[g].x = row[at];
+          if (at + 32 < V) l[g].y = row[at + 32];
+          if (at + 64 < V) l[g].z = row[at + 64];
+          if (at + 96 < V) l[g].w = row[at + 96];
+        }
+      }
     }
   }
-  return q;
+};
+// The warp's blocks whose largest logit is at least `least`.
+__device__ __forceinline__ uint32_t blocks_from(const Spaces& sp, const RowSpace& s, int v0, float least) {
+  const int lane = threadIdx.x & 31, at = v0 / SR_BLOCK + lane;
+  const uint32_t key = lane < SR_BLOCKS && at < sp.blocks ? __ldcg(s.block + at) : 0u;
+  return __ballot_sync(0xffffffffu, key >= max_key(least));
 }
 
 // ---------------------------------------------------------------------------
 // maxima
 // ---------------------------------------------------------------------------
+constexpr uint32_t NAN_KEY = 0xFFFFFFFFu;  // above every key
+__device__ __forceinline__ float nan_max(float x, float y) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(y));
+  return x;
+}
 __global__ void __launch_bounds__(SR_THREADS)
 sr_maxima_kernel(const SampleArgs a, const Spaces sp, int segs) {
   grid_dep_launch();
@@ -138,39 +181,45 @@ sr_maxima_kernel(const SampleArgs a, const Spaces sp, int segs) {
     }
   }
   const float* row = a.logits + (int64_t)r * a.ld;
-  const bool aligned = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
   const int v0 = seg * SR_SEG + warp * SR_RANGE;
-  constexpr int G = SR_RANGE / SR_GROUP;
-  float mx[G];
+  Logits q(row, v0, a.V);
+  q.load(row, (1u << SR_BLOCKS) - 1u);
+  uint32_t mx[SR_BLOCKS];  // order keys, NAN_KEY for a NaN (of which the bits of a sum say nothing)
 #pragma unroll
-  for (int g = 0; g < G; g++) {
-    const Quad q = load_quad(row, aligned, v0 + g * SR_GROUP, a.V, lane);
-    float m = q.l[0];
-#pragma unroll
-    for (int e = 1; e < 4; e++) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(q.l[e]));
-    mx[g] = m;
+  for (int g = 0; g < SR_BLOCKS; g++) {
+    float m = nan_max(nan_max(q.l[g].x, q.l[g].y), nan_max(q.l[g].z, q.l[g].w));
+    m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    mx[g] = m != m ? NAN_KEY : max_key(m);
   }
+  static_assert(SR_BLOCKS == 8, "two blocks a lane of four");
+  const int b0 = v0 / SR_BLOCK;
+  if (sp.per == 8) {  // lane 4 j + i: group j of blocks i and i + 4
+    uint32_t lo = mx[0], hi = mx[4];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-    for (int g = 0; g < G; g++) {
-      const float o = __shfl_xor_sync(0xffffffffu, mx[g], off);
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx[g]) : "f"(o));
+    for (int i = 1; i < 4; i++) {
+      lo = (lane & 3) == i ? mx[i] : lo;
+      hi = (lane & 3) == i ? mx[4 + i] : hi;
     }
-  float mine = mx[0];
+    const int at = b0 + (lane & 3);
+    if (at < sp.blocks) s.group[at * 8 + (lane >> 2)] = lo;
+    if (at + 4 < sp.blocks) s.group[(at + 4) * 8 + (lane >> 2)] = hi;
+  }
+  uint32_t mine = 0u;
 #pragma unroll
-  for (int g = 1; g < G; g++) mine = lane == g ? mx[g] : mine;
-  const int at = v0 / SR_GROUP + lane;
-  if (lane < G && at < sp.groups) s.group[at] = max_key(mine);  // NaN is above every key
+  for (int g = 0; g < SR_BLOCKS; g++) {
+    const uint32_t all = __reduce_max_sync(0xffffffffu, mx[g]);
+    mine = lane == g ? all : mine;
+  }
+  if (lane < SR_BLOCKS && b0 + lane < sp.blocks) s.block[b0 + lane] = mine;
 }
 
 // ---------------------------------------------------------------------------
 // bound
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(SR_THREADS)
+__global__ void __launch_bounds__(SM_THREADS)
 sr_bound_kernel(const SampleArgs a, const Spaces sp) {
-  extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_part[4][SR_WARPS];
+  __shared__ uint32_t s_top[SM_WARPS], s_low[SM_WARPS], s_cnt[SR_BOUND_BINS], s_from;
   grid_dep_launch();
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const RowSpace s = sp.row(r);
@@ -193,18 +242,27 @@ sr_bound_kernel(const SampleArgs a, const Spaces sp) {
   row.min_w = (uint32_t)min((u64)floor((double)min_p * 4294967296.0), 0xFFFFFFFFull);
   st.P = (u64)floor((double)top_p * 4294967296.0);
   grid_dep_wait();
-  uint32_t top = 0;
-  for (int g = tid; g < sp.groups; g += SR_THREADS) {
-    const uint32_t k = __ldcg(s.group + g);
-    s_key[g] = k;
-    top = max(top, k);
+  // the groups' keys, of finite logits (0 for the others), and their range
+  constexpr uint32_t NONE = 0x007FFFFFu;  // key of -infinity
+  uint32_t key[SR_MAX_GROUPS / SM_THREADS], top = 0, least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int i = 0; i < SR_MAX_GROUPS / SM_THREADS; i++) {
+    const int g = i * SM_THREADS + tid;
+    key[i] = g < sp.groups ? __ldcg(s.group + g) : 0u;
+    if (key[i] <= NONE) key[i] = 0u;
+    top = max(top, key[i]);
+    least = min(least, key[i] - 1u);  // (0 is the largest)
   }
   top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_part[0][warp] = top;
+  least = __reduce_min_sync(0xffffffffu, least);
+  if (lane == 0) {
+    s_top[warp] = top;
+    s_low[warp] = least;
+  }
   __syncthreads();
-  for (int w = 0; w < SR_WARPS; w++) top = max(top, s_part[0][w]);
-  __syncthreads();
-  const bool finite = top > 0x007FFFFFu && top < 0xFF800000u;  // above -inf, below +inf and NaN
+  top = __reduce_max_sync(0xffffffffu, s_top[lane % SM_WARPS]);
+  least = __reduce_min_sync(0xffffffffu, s_low[lane % SM_WARPS]) + 1u;
+  const bool finite = top > NONE && top < 0xFF800000u;  // below +infinity and NaN
   st.top = finite ? key_value(top) : 0.0f;
   row.zmax = row_zmax(max_key(st.top), row.T);
   bad |= !finite || !(fabsf(row.zmax) < INFINITY);
@@ -212,33 +270,47 @@ sr_bound_kernel(const SampleArgs a, const Spaces sp) {
   st.bound = -INFINITY;
   st.kind = bad ? ROW_BAD : by_k ? ROW_HARD : st.P < (1ull << 32) ? ROW_TOP_P : ROW_PLAIN;
   if (!bad && by_k && st.k <= SR_MAX_K && st.k <= sp.groups * 3 / 4) {
-    // the k-th largest of the groups' largest, two bits a step (the order
-    // key's first 20: a bound may be a little low)
-    uint32_t low = 0u;
-    int turn = 0;
-    for (int bit = 30; bit >= 12; bit -= 2) {
-      uint32_t c12 = 0, c3 = 0;  // at least low + 1, 2, 3 steps
-      for (int g = tid; g < sp.groups; g += SR_THREADS) {
-        const uint32_t k = s_key[g];
-        c12 += k >= (low | (1u << bit)) ? 1u : 0u;
-        c12 += k >= (low | (2u << bit)) ? 1u << 16 : 0u;
-        c3 += k >= (low | (3u << bit)) ? 1u : 0u;
+    // the k-th largest of the keys, nine bits a step from the first that
+    // differs; after two steps what is left of the bits is taken as 0
+    const int open = 32 - __clz(top ^ least);
+    int down = open;
+    uint32_t from = open < 32 ? top >> open : 0u, left = (uint32_t)st.k;
+    bool enough = true;
+    for (int step = 0; step < 2 && down > 0 && enough; step++) {
+      const int above = down;
+      down = max(0, down - SR_BOUND_BITS);
+      const uint32_t mask = (1u << (above - down)) - 1u;
+      s_cnt[tid] = 0u;
+      if (tid == 0) s_from = 0xFFFFFFFFu;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < SR_MAX_GROUPS / SM_THREADS; i++)
+        if (key[i] != 0u && (above == 32 || key[i] >> above == from))
+          atomicAdd(&s_cnt[SR_BOUND_BINS - 1 - (key[i] >> down & mask)], 1u);
+      __syncthreads();
+      const uint32_t c = s_cnt[tid];
+      uint32_t run = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, run, off);
+        if (lane >= off) run += y;
       }
-      c12 = __reduce_add_sync(0xffffffffu, c12);
-      c3 = __reduce_add_sync(0xffffffffu, c3);
-      if (lane == 0) {
-        s_part[2 * turn][warp] = c12;
-        s_part[2 * turn + 1][warp] = c3;
+      if (lane == 31) s_top[warp] = run;
+      __syncthreads();
+      run += __reduce_add_sync(0xffffffffu, lane < warp ? s_top[lane] : 0u);
+      if (run - c < left && left <= run) {
+        s_from = from << (above - down) | (uint32_t)(SR_BOUND_BINS - 1 - tid);
+        s_low[0] = left - (run - c);
       }
       __syncthreads();
-      c12 = __reduce_add_sync(0xffffffffu, lane < SR_WARPS ? s_part[2 * turn][lane] : 0u);
-      c3 = __reduce_add_sync(0xffffffffu, lane < SR_WARPS ? s_part[2 * turn + 1][lane] : 0u);
-      const uint32_t k = (uint32_t)st.k;
-      low |= (c3 >= k ? 3u : (c12 >> 16) >= k ? 2u : (c12 & 0xFFFFu) >= k ? 1u : 0u) << bit;
-      turn ^= 1;
+      enough = s_from != 0xFFFFFFFFu;  // at least k groups have a finite logit
+      from = s_from;
+      left = s_low[0];
+      __syncthreads();
     }
-    if (low > 0x007FFFFFu) {  // at least k groups have a finite logit
-      st.bound = key_value(low);
+    if (open == 0) enough = false;  // (all alike: more than a list of them)
+    if (enough) {
+      st.bound = key_value(from << down);
       st.kind = ROW_TOP_K;
     }
   }
@@ -281,18 +353,24 @@ struct Sum {
   u64 w = 0;
   uint32_t c = 0;
   __device__ __forceinline__ void add(uint32_t x, bool in) {
-    w += in ? x : 0u;
-    w += in && x == 0xFFFFFFFFu;
-    c += in;
+    if (in) {
+      w += x;
+      w += x == 0xFFFFFFFFu;
+      c++;
+    }
   }
-  __device__ __forceinline__ void over_warp() {
+  __device__ __forceinline__ void store(const RowSpace& s, int v0, int V) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
     c = __reduce_add_sync(0xffffffffu, c);
+    if ((threadIdx.x & 31) == 0 && v0 < V) {
+      s.range_w[v0 / SR_RANGE] = w;
+      s.range_c[v0 / SR_RANGE] = c;
+    }
   }
 };
 
-__global__ void __launch_bounds__(SR_THREADS)
+__global__ void __launch_bounds__(SR_THREADS, 4)
 sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
   __shared__ union {
     struct {
@@ -301,13 +379,12 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
     OwnList own;
   } sh;
   grid_dep_launch();
-  const int r = blockIdx.x / segs, seg = blockIdx.x % segs;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int at = (int)(gridDim.x - 1 - blockIdx.x), r = at / segs, seg = at % segs;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
-  const bool aligned = (reinterpret_cast<uintptr_t>(lrow) & 15u) == 0;
   const int v0 = seg * SR_SEG + warp * SR_RANGE;
-  constexpr int G = SR_RANGE / SR_GROUP;
+  Logits q(lrow, v0, a.V);
   grid_dep_wait();
   const int kind = s.state->kind;
   const Row row = s.state->row;
@@ -315,23 +392,28 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
     const float bound = s.state->bound;
     if (tid == 0) sh.own.n = 0;
     __syncthreads();
+    const uint32_t which = blocks_from(sp, s, v0, bound);
+    if (which != 0u) {
+      q.load(lrow, which);
 #pragma unroll
-    for (int g = 0; g < G; g++) {
-      const Quad q = load_quad(lrow, aligned, v0 + g * SR_GROUP, a.V, lane);
+      for (int g = 0; g < SR_BLOCKS; g++) {
+        const float l[4] = {q.l[g].x, q.l[g].y, q.l[g].z, q.l[g].w};
 #pragma unroll
-      for (int e = 0; e < 4; e++)
-        if (q.l[e] >= bound) own_add(sh.own, q.l[e], q.id[e]);
+        for (int e = 0; e < 4; e++)
+          if (l[e] >= bound) own_add(sh.own, l[e], q.id(g, e));
+      }
     }
     own_flush(sh.own, s, row);
   } else if (kind == ROW_TOP_P) {
     for (int b = tid; b < SM_BINS; b += SR_THREADS) sh.lo[b] = sh.hi[b] = 0;
+    q.load(lrow, (1u << SR_BLOCKS) - 1u);
     __syncthreads();
-#pragma unroll 2
-    for (int g = 0; g < G; g++) {
-      const Quad q = load_quad(lrow, aligned, v0 + g * SR_GROUP, a.V, lane);
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const float2 x = row.x2(make_float2(q.l[e], q.l[e + 1]));
+    for (int g = 0; g < SR_BLOCKS; g++) {
+      const float2 l[2] = {make_float2(q.l[g].x, q.l[g].y), make_float2(q.l[g].z, q.l[g].w)};
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const float2 x = row.x2(l[e]);
         const uint2 w = Row::w2(x);
         const uint32_t ww[2] = {w.x, w.y};
         const int bb[2] = {Row::bin_of(x.x), Row::bin_of(x.y)};
@@ -351,21 +433,18 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
     }
   } else if (kind == ROW_PLAIN) {
     Sum sum;
-#pragma unroll 2
-    for (int g = 0; g < G; g++) {
-      const Quad q = load_quad(lrow, aligned, v0 + g * SR_GROUP, a.V, lane);
+    q.load(lrow, (1u << SR_BLOCKS) - 1u);
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const uint2 w = row.weight2(make_float2(q.l[e], q.l[e + 1]));
-        sum.add(w.x, q.l[e] > -INFINITY && w.x >= row.min_w);
-        sum.add(w.y, q.l[e + 1] > -INFINITY && w.y >= row.min_w);
+    for (int g = 0; g < SR_BLOCKS; g++) {
+      const float2 l[2] = {make_float2(q.l[g].x, q.l[g].y), make_float2(q.l[g].z, q.l[g].w)};
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const uint2 w = row.weight2(l[e]);
+        sum.add(w.x, l[e].x > -INFINITY && w.x >= row.min_w);
+        sum.add(w.y, l[e].y > -INFINITY && w.y >= row.min_w);
       }
     }
-    sum.over_warp();
-    if (lane == 0 && v0 < a.V) {
-      s.range_w[v0 / SR_RANGE] = sum.w;
-      s.range_c[v0 / SR_RANGE] = sum.c;
-    }
+    sum.store(s, v0, a.V);
   }
 }
 
@@ -386,6 +465,25 @@ __device__ __forceinline__ void make_hard(const Spaces& sp, RowState* st, int r)
     st->kind = ROW_HARD;
     sp.hard[1 + atomicAdd(sp.hard, 1)] = r;
   }
+}
+
+// The least float whose step of z is at most `target`, by a warp: five bits a
+// turn of the largest order key with a later step (a step never rises with the
+// logit, as each rounding keeps the order).
+__device__ __forceinline__ float first_of_step(const Row& row, float top, int target) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t last = max_key(top);
+  uint32_t base = 0u;
+  for (int shift = 27;; shift = max(0, shift - 5)) {
+    const uint32_t key = base + ((uint32_t)lane << shift);
+    bool later = key < 0x00800000u;  // -infinity and what is below it
+    if (!later && key <= last) later = row.bin(key_value(key)) > target;
+    // (in the last turn lanes 4 .. 31 lie past a key that is known not to be later)
+    const uint32_t yes = __ballot_sync(0xffffffffu, later && key >= base);
+    base += (uint32_t)(31 - __clz(yes)) << shift;
+    if (shift == 0) break;
+  }
+  return key_value(base + 1u);
 }
 
 // The draw from the masses over SR_RANGE ids in sh.range_w: the range that
@@ -462,13 +560,21 @@ sr_cut_kernel(const SampleArgs a, const Spaces sp) {
     }
     u64 run = block_prefix(mine, sh, &S) - mine;
     const u64 need = mass_needed(st->P, S);
+    if (tid == 0) sh.range = SM_BINS - 1;
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < PER; e++) {
       if (run < need && need <= run + w[e]) {
-        st->bin = tid * PER + e;
+        sh.range = tid * PER + e;
         st->left = need - run;
       }
       run += w[e];
+    }
+    __syncthreads();
+    if (tid < 64) {
+      const float first = first_of_step(row, st->top, sh.range - (tid >> 5));
+      if (tid == 0) st->bound = first;
+      if (tid == 32) st->summed = sh.range == 0 ? INFINITY : first;
     }
   } else if (kind == ROW_TOP_K) {
     const uint32_t m = st->listed;
@@ -514,44 +620,43 @@ sr_cut_kernel(const SampleArgs a, const Spaces sp) {
 // ---------------------------------------------------------------------------
 // step and draw of the top-p rows
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(SR_THREADS)
+__global__ void __launch_bounds__(SR_THREADS, 4)
 sr_step_kernel(const SampleArgs a, const Spaces sp, int segs) {
   __shared__ OwnList own;
   grid_dep_launch();
   const int r = blockIdx.x / segs, seg = blockIdx.x % segs;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
-  const bool aligned = (reinterpret_cast<uintptr_t>(lrow) & 15u) == 0;
   const int v0 = seg * SR_SEG + warp * SR_RANGE;
+  Logits q(lrow, v0, a.V);
   if (tid == 0) own.n = 0;
   __syncthreads();
   grid_dep_wait();
   if (s.state->kind != ROW_TOP_P) return;
   const Row row = s.state->row;
-  const int bin = s.state->bin;
+  const float bound = s.state->bound, summed = s.state->summed;
   Sum sum;
-#pragma unroll 2
-  for (int g = 0; g < SR_RANGE / SR_GROUP; g++) {
-    const Quad q = load_quad(lrow, aligned, v0 + g * SR_GROUP, a.V, lane);
+  const uint32_t which = blocks_from(sp, s, v0, bound);
+  if (which != 0u) {
+    q.load(lrow, which);
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      const float2 x = row.x2(make_float2(q.l[e], q.l[e + 1]));
-      const int b0 = Row::bin_of(x.x), b1 = Row::bin_of(x.y);
-      if (b0 < bin || b1 < bin) {
-        const uint2 w = Row::w2(x);
-        sum.add(w.x, b0 < bin && w.x >= row.min_w);
-        sum.add(w.y, b1 < bin && w.y >= row.min_w);
+    for (int g = 0; g < SR_BLOCKS; g++) {
+      const float l[4] = {q.l[g].x, q.l[g].y, q.l[g].z, q.l[g].w};
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        if (l[e] >= summed || l[e + 1] >= summed) {
+          const uint2 w = row.weight2(make_float2(l[e], l[e + 1]));
+          sum.add(w.x, l[e] >= summed && w.x >= row.min_w);
+          sum.add(w.y, l[e + 1] >= summed && w.y >= row.min_w);
+        }
+#pragma unroll
+        for (int h = e; h < e + 2; h++)
+          if (l[h] >= bound && l[h] < summed) own_add(own, l[h], q.id(g, h));
       }
-      if (b0 == bin && q.l[e] > -INFINITY) own_add(own, q.l[e], q.id[e]);
-      if (b1 == bin && q.l[e + 1] > -INFINITY) own_add(own, q.l[e + 1], q.id[e + 1]);
     }
   }
-  sum.over_warp();
-  if (lane == 0 && v0 < a.V) {
-    s.range_w[v0 / SR_RANGE] = sum.w;
-    s.range_c[v0 / SR_RANGE] = sum.c;
-  }
+  sum.store(s, v0, a.V);
   own_flush(own, s, row);
 }
 
@@ -596,37 +701,37 @@ sr_draw_kernel(const SampleArgs a, const Spaces sp) {
 // ---------------------------------------------------------------------------
 // filter
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(SR_THREADS)
+__global__ void __launch_bounds__(SR_THREADS, 4)
 sr_filter_kernel(const SampleArgs a, const Spaces sp, int segs) {
-  const int r = blockIdx.x / segs, seg = blockIdx.x % segs;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const RowState* st = sp.row(r).state;
+  const int at = (int)(gridDim.x - 1 - blockIdx.x), r = at / segs, seg = at % segs;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
   float* frow = a.filtered + (int64_t)r * a.ldf;
-  const bool aligned =
-      ((reinterpret_cast<uintptr_t>(lrow) | reinterpret_cast<uintptr_t>(frow)) & 15u) == 0;
   const int v0 = seg * SR_SEG + warp * SR_RANGE;
+  Logits q(lrow, v0, a.V);
+  q.aligned = q.aligned && (reinterpret_cast<uintptr_t>(frow) & 15u) == 0;
   grid_dep_wait();
-  const int kind = st->kind;
+  const int kind = s.state->kind;
   if (kind == ROW_HARD) return;  // written by its cluster
-  const Row row = st->row;
-#pragma unroll 4
-  for (int g = 0; g < SR_RANGE / SR_GROUP; g++) {
-    const int g0 = v0 + g * SR_GROUP;
-    const Quad q = load_quad(lrow, aligned, g0, a.V, lane);
-    float o[4];
+  const Row row = s.state->row;
+  const float out = kind == ROW_BAD ? __int_as_float(0x7FFFFFFF) : SPEC_FILTERED;
+  q.load(lrow, kind == ROW_BAD ? 0u : blocks_from(sp, s, v0, row.least));
+#pragma unroll
+  for (int g = 0; g < SR_BLOCKS; g++) {
+    float o[4] = {q.l[g].x, q.l[g].y, q.l[g].z, q.l[g].w};
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-      bool in = row.inside(q.l[e], q.id[e]);
-      if (in && row.min_w != 0u) in = row.weight(q.l[e]) >= row.min_w;
-      o[e] = kind == ROW_BAD ? __int_as_float(0x7FFFFFFF) : in ? q.l[e] : SPEC_FILTERED;
+      bool in = row.inside(o[e], q.id(g, e));
+      if (in && row.min_w != 0u) in = row.weight(o[e]) >= row.min_w;
+      o[e] = in ? o[e] : out;
     }
-    if (aligned && g0 + SR_GROUP <= a.V) {
-      __stcs(reinterpret_cast<float4*>(frow + g0) + lane, make_float4(o[0], o[1], o[2], o[3]));
+    if (q.whole(g)) {
+      __stcs(reinterpret_cast<float4*>(frow + v0 + g * SR_BLOCK) + lane, make_float4(o[0], o[1], o[2], o[3]));
     } else {
 #pragma unroll
       for (int e = 0; e < 4; e++)
-        if (q.id[e] < a.V) frow[q.id[e]] = o[e];
+        if (q.id(g, e) < a.V) frow[q.id(g, e)] = o[e];
     }
   }
 }
@@ -669,7 +774,7 @@ int sample_rows_launch(SampleArgs a, void* workspace, cudaStream_t st) {
   if (grid > INT32_MAX) return fail(SPEC_E_SHAPE, "sample: R * V too large");
   cudaError_t e = launch(sr_maxima_kernel, grid, SR_THREADS, 0, st, false, a, sp, segs);
   if (e == cudaSuccess)
-    e = launch(sr_bound_kernel, a.R, SR_THREADS, sizeof(uint32_t) * sp.groups, st, true, a, sp);
+    e = launch(sr_bound_kernel, a.R, SM_THREADS, 0, st, true, a, sp);
   if (e == cudaSuccess) e = launch(sr_pass_kernel, grid, SR_THREADS, 0, st, true, a, sp, segs);
   if (e == cudaSuccess) e = launch(sr_cut_kernel, a.R, SM_THREADS, sizeof(RowSmem), st, true, a, sp);
   if (e == cudaSuccess && a.top_p != nullptr) {
