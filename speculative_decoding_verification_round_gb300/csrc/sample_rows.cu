@@ -5,8 +5,8 @@
 //
 // A row is one of three kinds, by its settings: top-k (with or without the
 // other filters), top-p alone, or neither.  Streaming passes have a CTA per
-// 8192 logits of a row, a warp per 1024 of them; between them a CTA per row
-// decides.
+// 8192 or 16384 logits of a row, a warp per 1024 of them at a time; between
+// them a CTA per row decides.
 //   maxima   stream: the largest logit of every 128, and of every 16
 //   bound    row: the largest, the settings, and for a top-k a bound that at
 //            least k of these groups reach
@@ -152,10 +152,12 @@ struct Logits {
     }
   }
 };
-// The warp's blocks whose largest logit is at least `least`.
+// The blocks of the warp's turns whose largest logit is at least
+// `least`: eight bits a turn.
+constexpr int SR_TURNS = 2;  // at most: segments of a CTA
 __device__ __forceinline__ uint32_t blocks_from(const Spaces& sp, const RowSpace& s, int v0, float least) {
-  const int lane = threadIdx.x & 31, at = v0 / SR_BLOCK + lane;
-  const uint32_t key = lane < SR_BLOCKS && at < sp.blocks ? __ldcg(s.block + at) : 0u;
+  const int lane = threadIdx.x & 31, at = (v0 + (lane >> 3) * SR_SEG) / SR_BLOCK + (lane & 7);
+  const uint32_t key = at < sp.blocks ? __ldcg(s.block + at) : 0u;
   return __ballot_sync(0xffffffffu, key >= max_key(least));
 }
 
@@ -329,19 +331,19 @@ sr_bound_kernel(const SampleArgs a, const Spaces sp) {
 // ---------------------------------------------------------------------------
 // A CTA's collected tokens (ids of its segment), to the row's list.
 struct OwnList {
-  u64 key[SM_LOCAL];
+  u64 key[SR_LIST];
   uint32_t n, at;
 };
 __device__ __forceinline__ void own_add(OwnList& o, float l, int id) {
   const uint32_t at = atomicAdd(&o.n, 1u);
-  if (at < SM_LOCAL) o.key[at] = Row::composite(max_key(l), id);
+  if (at < SR_LIST) o.key[at] = Row::composite(max_key(l), id);
 }
 __device__ __forceinline__ void own_flush(OwnList& o, const RowSpace& s, const Row& row) {
   __syncthreads();
   const uint32_t n = o.n;
-  if (threadIdx.x == 0 && n > 0) o.at = atomicAdd(&s.state->listed, n > SM_LOCAL ? SR_LIST + 1 : n);
+  if (threadIdx.x == 0 && n > 0) o.at = atomicAdd(&s.state->listed, min(n, SR_LIST + 1u));
   __syncthreads();
-  for (uint32_t c = threadIdx.x; c < min(n, (uint32_t)SM_LOCAL); c += SR_THREADS)
+  for (uint32_t c = threadIdx.x; c < min(n, (uint32_t)SR_LIST); c += SR_THREADS)
     if (o.at + c < SR_LIST) {
       s.key[o.at + c] = o.key[c];
       s.w[o.at + c] = row.weight(key_value((uint32_t)(o.key[c] >> 20)));
@@ -371,7 +373,7 @@ struct Sum {
 };
 
 __global__ void __launch_bounds__(SR_THREADS, 4)
-sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
+sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
   __shared__ union {
     struct {
       uint32_t lo[SM_BINS], hi[SM_BINS];
@@ -383,8 +385,7 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
-  const int v0 = seg * SR_SEG + warp * SR_RANGE;
-  Logits q(lrow, v0, a.V);
+  Logits q(lrow, (seg * turns * SR_WARPS + warp) * SR_RANGE, a.V);
   grid_dep_wait();
   const int kind = s.state->kind;
   const Row row = s.state->row;
@@ -392,8 +393,10 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
     const float bound = s.state->bound;
     if (tid == 0) sh.own.n = 0;
     __syncthreads();
-    const uint32_t which = blocks_from(sp, s, v0, bound);
-    if (which != 0u) {
+    uint32_t blocks = blocks_from(sp, s, q.v0, bound);
+    for (int turn = 0; turn < turns; turn++, q.v0 += SR_SEG, blocks >>= SR_BLOCKS) {
+      const uint32_t which = blocks & ((1u << SR_BLOCKS) - 1u);
+      if (which == 0u) continue;
       q.load(lrow, which);
 #pragma unroll
       for (int g = 0; g < SR_BLOCKS; g++) {
@@ -406,24 +409,26 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
     own_flush(sh.own, s, row);
   } else if (kind == ROW_TOP_P) {
     for (int b = tid; b < SM_BINS; b += SR_THREADS) sh.lo[b] = sh.hi[b] = 0;
-    q.load(lrow, (1u << SR_BLOCKS) - 1u);
     __syncthreads();
+    for (int turn = 0; turn < turns; turn++, q.v0 += SR_SEG) {
+      q.load(lrow, (1u << SR_BLOCKS) - 1u);
 #pragma unroll
-    for (int g = 0; g < SR_BLOCKS; g++) {
-      const float2 l[2] = {make_float2(q.l[g].x, q.l[g].y), make_float2(q.l[g].z, q.l[g].w)};
+      for (int g = 0; g < SR_BLOCKS; g++) {
+        const float2 l[2] = {make_float2(q.l[g].x, q.l[g].y), make_float2(q.l[g].z, q.l[g].w)};
 #pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const float2 x = row.x2(l[e]);
-        const uint2 w = Row::w2(x);
-        const uint32_t ww[2] = {w.x, w.y};
-        const int bb[2] = {Row::bin_of(x.x), Row::bin_of(x.y)};
+        for (int e = 0; e < 2; e++) {
+          const float2 x = row.x2(l[e]);
+          const uint2 w = Row::w2(x);
+          const uint32_t ww[2] = {w.x, w.y};
+          const int bb[2] = {Row::bin_of(x.x), Row::bin_of(x.y)};
 #pragma unroll
-        for (int h = 0; h < 2; h++)
-          if (ww[h] != 0u) {
-            const u64 v = widen(ww[h]);
-            atomicAdd(&sh.lo[bb[h]], (uint32_t)v & 0xFFFFu);
-            atomicAdd(&sh.hi[bb[h]], (uint32_t)(v >> 16));
-          }
+          for (int h = 0; h < 2; h++)
+            if (ww[h] != 0u) {
+              const u64 v = widen(ww[h]);
+              atomicAdd(&sh.lo[bb[h]], (uint32_t)v & 0xFFFFu);
+              atomicAdd(&sh.hi[bb[h]], (uint32_t)(v >> 16));
+            }
+        }
       }
     }
     __syncthreads();
@@ -432,19 +437,21 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs) {
       if (v != 0) atomicAdd(&s.mass[b], v);
     }
   } else if (kind == ROW_PLAIN) {
-    Sum sum;
-    q.load(lrow, (1u << SR_BLOCKS) - 1u);
+    for (int turn = 0; turn < turns; turn++, q.v0 += SR_SEG) {
+      Sum sum;
+      q.load(lrow, (1u << SR_BLOCKS) - 1u);
 #pragma unroll
-    for (int g = 0; g < SR_BLOCKS; g++) {
-      const float2 l[2] = {make_float2(q.l[g].x, q.l[g].y), make_float2(q.l[g].z, q.l[g].w)};
+      for (int g = 0; g < SR_BLOCKS; g++) {
+        const float2 l[2] = {make_float2(q.l[g].x, q.l[g].y), make_float2(q.l[g].z, q.l[g].w)};
 #pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const uint2 w = row.weight2(l[e]);
-        sum.add(w.x, l[e].x > -INFINITY && w.x >= row.min_w);
-        sum.add(w.y, l[e].y > -INFINITY && w.y >= row.min_w);
+        for (int e = 0; e < 2; e++) {
+          const uint2 w = row.weight2(l[e]);
+          sum.add(w.x, l[e].x > -INFINITY && w.x >= row.min_w);
+          sum.add(w.y, l[e].y > -INFINITY && w.y >= row.min_w);
+        }
       }
+      sum.store(s, q.v0, a.V);
     }
-    sum.store(s, v0, a.V);
   }
 }
 
@@ -621,42 +628,59 @@ sr_cut_kernel(const SampleArgs a, const Spaces sp) {
 // step and draw of the top-p rows
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(SR_THREADS, 4)
-sr_step_kernel(const SampleArgs a, const Spaces sp, int segs) {
+sr_step_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
   __shared__ OwnList own;
   grid_dep_launch();
   const int r = blockIdx.x / segs, seg = blockIdx.x % segs;
   const int tid = threadIdx.x, warp = tid >> 5;
   const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
-  const int v0 = seg * SR_SEG + warp * SR_RANGE;
-  Logits q(lrow, v0, a.V);
+  Logits q(lrow, (seg * turns * SR_WARPS + warp) * SR_RANGE, a.V);
   if (tid == 0) own.n = 0;
   __syncthreads();
   grid_dep_wait();
   if (s.state->kind != ROW_TOP_P) return;
   const Row row = s.state->row;
   const float bound = s.state->bound, summed = s.state->summed;
-  Sum sum;
-  const uint32_t which = blocks_from(sp, s, v0, bound);
-  if (which != 0u) {
-    q.load(lrow, which);
+  uint32_t blocks = blocks_from(sp, s, q.v0, bound);
+  for (int turn = 0; turn < turns; turn++, q.v0 += SR_SEG, blocks >>= SR_BLOCKS) {
+    Sum sum;
+    const uint32_t which = blocks & ((1u << SR_BLOCKS) - 1u);
+    if (which != 0u) {
+      q.load(lrow, which);
+      // a bit for each of the lane's logits; few of a row are above its cut,
+      // so that a lane weighs its own, read again, rather than all in turn
+      uint32_t above = 0u, within = 0u;
 #pragma unroll
-    for (int g = 0; g < SR_BLOCKS; g++) {
-      const float l[4] = {q.l[g].x, q.l[g].y, q.l[g].z, q.l[g].w};
+      for (int g = 0; g < SR_BLOCKS; g++) {
+        const float l[4] = {q.l[g].x, q.l[g].y, q.l[g].z, q.l[g].w};
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        if (l[e] >= summed || l[e + 1] >= summed) {
-          const uint2 w = row.weight2(make_float2(l[e], l[e + 1]));
-          sum.add(w.x, l[e] >= summed && w.x >= row.min_w);
-          sum.add(w.y, l[e + 1] >= summed && w.y >= row.min_w);
+        for (int e = 0; e < 4; e++) {
+          if (l[e] >= summed) above |= 1u << (4 * g + e);
+          if (l[e] >= bound) within |= 1u << (4 * g + e);
         }
-#pragma unroll
-        for (int h = e; h < e + 2; h++)
-          if (l[h] >= bound && l[h] < summed) own_add(own, l[h], q.id(g, h));
+      }
+      within &= ~above;
+      while (above != 0u) {
+        const int i = __ffs(above) - 1;
+        above &= above - 1u;
+        const bool two = above != 0u;
+        const int j = two ? __ffs(above) - 1 : i;
+        above &= above - 1u;
+        const uint2 w = row.weight2(make_float2(lrow[q.id(i >> 2, i & 3)], lrow[q.id(j >> 2, j & 3)]));
+        sum.add(w.x, w.x >= row.min_w);
+        sum.add(w.y, two && w.y >= row.min_w);
+      }
+      while (within != 0u) {
+        const int i = __ffs(within) - 1;
+        within &= within - 1u;
+        const int id = q.id(i >> 2, i & 3);
+        own_add(own, lrow[id], id);
       }
     }
+    __syncwarp();
+    sum.store(s, q.v0, a.V);
   }
-  sum.store(s, v0, a.V);
   own_flush(own, s, row);
 }
 
@@ -701,37 +725,42 @@ sr_draw_kernel(const SampleArgs a, const Spaces sp) {
 // ---------------------------------------------------------------------------
 // filter
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(SR_THREADS, 4)
-sr_filter_kernel(const SampleArgs a, const Spaces sp, int segs) {
+__global__ void __launch_bounds__(SR_THREADS, 6)
+sr_filter_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
   const int at = (int)(gridDim.x - 1 - blockIdx.x), r = at / segs, seg = at % segs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
   float* frow = a.filtered + (int64_t)r * a.ldf;
-  const int v0 = seg * SR_SEG + warp * SR_RANGE;
-  Logits q(lrow, v0, a.V);
-  q.aligned = q.aligned && (reinterpret_cast<uintptr_t>(frow) & 15u) == 0;
+  const bool aligned = ((reinterpret_cast<uintptr_t>(lrow) | reinterpret_cast<uintptr_t>(frow)) & 15u) == 0;
+  int v0 = (seg * turns * SR_WARPS + warp) * SR_RANGE;
   grid_dep_wait();
   const int kind = s.state->kind;
   if (kind == ROW_HARD) return;  // written by its cluster
   const Row row = s.state->row;
   const float out = kind == ROW_BAD ? __int_as_float(0x7FFFFFFF) : SPEC_FILTERED;
-  q.load(lrow, kind == ROW_BAD ? 0u : blocks_from(sp, s, v0, row.least));
-#pragma unroll
-  for (int g = 0; g < SR_BLOCKS; g++) {
-    float o[4] = {q.l[g].x, q.l[g].y, q.l[g].z, q.l[g].w};
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      bool in = row.inside(o[e], q.id(g, e));
-      if (in && row.min_w != 0u) in = row.weight(o[e]) >= row.min_w;
-      o[e] = in ? o[e] : out;
-    }
-    if (q.whole(g)) {
-      __stcs(reinterpret_cast<float4*>(frow + v0 + g * SR_BLOCK) + lane, make_float4(o[0], o[1], o[2], o[3]));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; e++)
-        if (q.id(g, e) < a.V) frow[q.id(g, e)] = o[e];
+  uint32_t blocks = kind == ROW_BAD ? 0u : blocks_from(sp, s, v0, row.least);
+  auto put = [&](float l, int id) {
+    bool in = row.inside(l, id);
+    if (in && row.min_w != 0u) in = row.weight(l) >= row.min_w;
+    return in ? l : out;
+  };
+  for (int turn = 0; turn < turns; turn++, v0 += SR_SEG) {
+#pragma unroll 2
+    for (int g = 0; g < SR_BLOCKS; g++, blocks >>= 1) {
+      const int g0 = v0 + g * SR_BLOCK;
+      if (aligned && g0 + SR_BLOCK <= a.V) {
+        float4 l = make_float4(out, out, out, out);
+        if (blocks & 1u) {
+          l = reinterpret_cast<const float4*>(lrow + g0)[lane];
+          const int id = g0 + 4 * lane;
+          l = make_float4(put(l.x, id), put(l.y, id + 1), put(l.z, id + 2), put(l.w, id + 3));
+        }
+        reinterpret_cast<float4*>(frow + g0)[lane] = l;
+      } else {
+        for (int id = g0 + lane; id < min(a.V, g0 + SR_BLOCK); id += 32)
+          frow[id] = blocks & 1u ? put(lrow[id], id) : out;
+      }
     }
   }
 }
@@ -772,17 +801,23 @@ int sample_rows_launch(SampleArgs a, void* workspace, cudaStream_t st) {
   const int segs = (a.V + SR_SEG - 1) / SR_SEG;
   const size_t grid = (size_t)a.R * segs;
   if (grid > INT32_MAX) return fail(SPEC_E_SHAPE, "sample: R * V too large");
+  // two segments a CTA where CTAs are many (192 rows of 248320 logits, a top-k:
+  // 86 us with one, 78 with two, 76 with four, which then end unevenly where
+  // rows are of different kinds: 129 us with two, 132 with four)
+  const int turns = (int)std::max<size_t>(1, std::min<size_t>(SR_TURNS, grid / 1216));
+  const int long_segs = (segs + turns - 1) / turns;
+  const size_t long_grid = (size_t)a.R * long_segs;
   cudaError_t e = launch(sr_maxima_kernel, grid, SR_THREADS, 0, st, false, a, sp, segs);
   if (e == cudaSuccess)
     e = launch(sr_bound_kernel, a.R, SM_THREADS, 0, st, true, a, sp);
-  if (e == cudaSuccess) e = launch(sr_pass_kernel, grid, SR_THREADS, 0, st, true, a, sp, segs);
+  if (e == cudaSuccess) e = launch(sr_pass_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
   if (e == cudaSuccess) e = launch(sr_cut_kernel, a.R, SM_THREADS, sizeof(RowSmem), st, true, a, sp);
   if (e == cudaSuccess && a.top_p != nullptr) {
-    e = launch(sr_step_kernel, grid, SR_THREADS, 0, st, true, a, sp, segs);
+    e = launch(sr_step_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
     if (e == cudaSuccess) e = launch(sr_draw_kernel, a.R, SM_THREADS, sizeof(RowSmem), st, true, a, sp);
   }
   if (e == cudaSuccess && a.filtered != nullptr)
-    e = launch(sr_filter_kernel, grid, SR_THREADS, 0, st, true, a, sp, segs);
+    e = launch(sr_filter_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("sample: ") + cudaGetErrorString(e));
   // (an ordinary launch: behind everything in front of it)
   a.rows = sp.hard + 1;
