@@ -644,7 +644,7 @@ def spec_sample(logits, R: int, V: int, u, token, temperature=None, top_k=None, 
     n = 0
     if workspace is not None:
         n = workspace.numel() * workspace.element_size()
-    elif R * V > 4000000:  # (below, no call needs one)
+    elif R * V > 2000000:  # (below, no call needs one)
         n = spec_sample_workspace(R, V)
         if n > 0:
             import torch

@@ -662,8 +662,13 @@ int sample_clusters_launch(SampleArgs a, int clusters, cudaStream_t st) {
   return SPEC_OK;
 }
 
-// Many long rows go through the passes of sample_rows.cu.
-static bool by_passes(int R, int V) { return V > 16384 && (long long)R * V > 4000000; }
+// Many long rows go through the passes of sample_rows.cu: 8 rows of 248320
+// logits take 35 us in clusters and 37 in passes (of mixed settings; a top-k
+// alone 26 and 22), 32 rows 86 and 51; 128 rows of 32000 38 and 47, 256 rows 64
+// and 56.
+static bool by_passes(int R, int V) {
+  return V > 16384 && (long long)R * V > (V > 65536 ? 2000000 : 5000000);
+}
 
 size_t sample_bytes(int R, int V) { return by_passes(R, V) ? sample_rows_bytes(R, V) : 0; }
 

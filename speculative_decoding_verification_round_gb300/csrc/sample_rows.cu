@@ -7,7 +7,7 @@
 // other filters), top-p alone, or neither.  Streaming passes have a CTA per
 // 8192 or 16384 logits of a row, a warp per 1024 of them at a time; between
 // them a CTA per row decides.
-//   maxima   stream: the largest logit of every 128, and of every 16
+//   maxima   stream: the largest logit of every 128, and of groups of 16 .. 128
 //   bound    row: the largest, the settings, and for a top-k a bound that at
 //            least k of these groups reach
 //   pass     stream: top-k rows collect the tokens at the bound (only blocks
@@ -31,17 +31,15 @@
 
 namespace {
 
-constexpr int SR_BLOCK = 128;   // logits of a warp's load
-// Groups whose largest bound a top-k: blocks, or up to SR_FEW logits (where
-// blocks are too few for a k of some hundreds) the 16 of four lanes.
-constexpr int SR_FEW = 131072;
+constexpr int SR_BLOCK = 128;  // logits of a warp's load
+// Groups whose largest bound a top-k: 1, 2, 4 or 8 of a block, as many as make
+// no more than SR_MAX_GROUPS.
 constexpr int SR_MAX_GROUPS = 8192;
 constexpr int SR_RANGE = 1024;  // logits of a warp, and ids whose mass is kept
 constexpr int SR_WARPS = 8;
 constexpr int SR_THREADS = 32 * SR_WARPS;
 constexpr int SR_SEG = SR_RANGE * SR_WARPS;
-constexpr int SR_LIST = 4096;   // tokens that are collected of a row
-constexpr int SR_MAX_K = 2048;  // of a top-k by a bound, so that these are enough mostly
+constexpr int SR_LIST = 4096;  // tokens that are collected of a row
 constexpr int SR_MAX_RANGES = 1024;
 constexpr int SR_BOUND_BITS = 9, SR_BOUND_BINS = 1 << SR_BOUND_BITS;
 static_assert(SR_BOUND_BINS == SM_THREADS, "a bin a thread");
@@ -77,7 +75,7 @@ struct Spaces {
   int32_t* hard;  // rows for the clusters, and their number in front
   size_t stride;  // bytes of a row
   int blocks, groups, ranges;
-  int per;  // groups of a block: 1 or 8
+  int per;  // groups of a block
   __host__ __device__ static size_t up(size_t b) { return (b + 127) / 128 * 128; }
   __host__ __device__ RowSpace row(int r) const {
     RowSpace s;
@@ -102,8 +100,9 @@ struct Spaces {
 
 Spaces spaces(void* workspace, int R, int V) {
   Spaces s;
-  s.per = V > SR_FEW ? 1 : 8;
   s.blocks = (V + SR_BLOCK - 1) / SR_BLOCK;
+  s.per = 8;
+  while (s.blocks * s.per > SR_MAX_GROUPS) s.per /= 2;
   s.groups = s.blocks * s.per;
   s.ranges = (V + SR_RANGE - 1) / SR_RANGE;
   s.stride = Spaces::up(sizeof(RowState)) + Spaces::up(sizeof(u64) * SM_BINS) + Spaces::up(sizeof(u64) * SR_LIST) +
@@ -196,16 +195,23 @@ sr_maxima_kernel(const SampleArgs a, const Spaces sp, int segs) {
   }
   static_assert(SR_BLOCKS == 8, "two blocks a lane of four");
   const int b0 = v0 / SR_BLOCK;
-  if (sp.per == 8) {  // lane 4 j + i: group j of blocks i and i + 4
+  if (sp.per > 1) {
+    int each = 4;  // lanes of a group
+    for (; each * sp.per < 32; each *= 2)
+#pragma unroll
+      for (int g = 0; g < SR_BLOCKS; g++) mx[g] = max(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], each));
+    // the group's lanes 0 .. 3: blocks i and i + 4
     uint32_t lo = mx[0], hi = mx[4];
 #pragma unroll
     for (int i = 1; i < 4; i++) {
       lo = (lane & 3) == i ? mx[i] : lo;
       hi = (lane & 3) == i ? mx[4 + i] : hi;
     }
-    const int at = b0 + (lane & 3);
-    if (at < sp.blocks) s.group[at * 8 + (lane >> 2)] = lo;
-    if (at + 4 < sp.blocks) s.group[(at + 4) * 8 + (lane >> 2)] = hi;
+    const int at = b0 + (lane & 3), group = lane / each;
+    if (lane % each < 4) {
+      if (at < sp.blocks) s.group[at * sp.per + group] = lo;
+      if (at + 4 < sp.blocks) s.group[(at + 4) * sp.per + group] = hi;
+    }
   }
   uint32_t mine = 0u;
 #pragma unroll
@@ -271,7 +277,10 @@ sr_bound_kernel(const SampleArgs a, const Spaces sp) {
   const bool by_k = st.k > 0 && st.k < a.V;
   st.bound = -INFINITY;
   st.kind = bad ? ROW_BAD : by_k ? ROW_HARD : st.P < (1ull << 32) ? ROW_TOP_P : ROW_PLAIN;
-  if (!bad && by_k && st.k <= SR_MAX_K && st.k <= sp.groups * 3 / 4) {
+  // how many tokens would be collected, were logits independent: groups of n
+  // are below the bound with the chance 1 - k / groups
+  const float n = (float)(SR_BLOCK / sp.per), part = (float)st.k / (float)sp.groups;
+  if (!bad && by_k && part < 1.0f && n * sp.groups * (1.0f - powf(1.0f - part, 1.0f / n)) < 0.9f * SR_LIST) {
     // the k-th largest of the keys, nine bits a step from the first that
     // differs; after two steps what is left of the bits is taken as 0
     const int open = 32 - __clz(top ^ least);

@@ -180,8 +180,9 @@ def many(g, R, V, scale=2.0):
     return logits, g.integers(0, 2 ** 32, R, dtype=np.uint64)
 
 
-@pytest.mark.parametrize("R,V,ld,off,in_place", [(100, 40003, 0, 0, False), (244, 16500, 16501, 1, True),
-                                                 (5, 1000001, 0, 2, True), (126, 32000, 32004, 0, True)])
+@pytest.mark.parametrize("R,V,ld,off,in_place", [(126, 40003, 0, 0, False), (304, 16500, 16501, 1, True),
+                                                 (3, 1000001, 0, 2, True), (158, 32000, 32004, 0, True),
+                                                 (16, 151936, 0, 0, False), (5, 500002, 0, 0, True)])
 def test_many_long_rows(orc, dev, R, V, ld, off, in_place):
     """Enough logits for passes over all rows: kinds mixed, strides and
     alignments, the last segment and the last group of 128 cut short."""
@@ -200,7 +201,7 @@ def test_many_long_rows_of_equal_masked_and_bad_logits(orc, dev):
     values, or with all large ones in one place), rows with one token left,
     and refused ones between."""
     g = np.random.default_rng(21)
-    R, V = 112, 36000
+    R, V = 140, 36000
     logits, u = many(g, R, V)
     T, k, p, m = settings(g, R, V)
     T = np.where(T == 0, np.float32(0), np.maximum(T, np.float32(1.0)))
@@ -236,7 +237,7 @@ def test_many_long_rows_replayed_and_on_two_streams(orc, dev):
     import torch
     import speculative_decoding_verification_round_gb300 as sv
     g = np.random.default_rng(22)
-    R, V = 130, 31999
+    R, V = 158, 31999
     sides = []
     for s in range(2):
         logits, u = many(g, R, V)
