@@ -8,13 +8,12 @@
 // nodes are the last tile, masked by each node's set of ancestors.
 //
 // Work is cut evenly whatever the lengths are: the (sequence, kv head, row
-// block) units, each of its own number of tiles, are laid end to end, and CTA
-// b of N takes tiles [b T / N, (b + 1) T / N).  The lengths are only known on
-// the device, so every CTA derives the cut from them.  A unit that one CTA
-// holds whole is written by it; the pieces of a cut unit (at most two a CTA)
-// go to the workspace as (max, sum, unnormalised O) and a second kernel, which
-// also checks the sequences and writes their status, joins them in the order
-// of the positions.
+// block) units, each of its own number of tiles, are laid end to end, and every
+// CTA takes as many tiles of them.  The lengths are only known on the device,
+// so every CTA derives the cut from them.  A unit that one CTA holds whole is
+// written by it; the pieces of a cut unit (at most two a CTA) go to the
+// workspace as (max, sum, unnormalised O) and a second kernel joins them in the
+// order of the positions.
 #include <math.h>
 
 #include <algorithm>
@@ -100,21 +99,24 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
 
   const int n_cta = gridDim.x - 1;
   if ((int)blockIdx.x == n_cta) {
-    check_sequences<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part);
+    plan_sequences<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part, smem);
     return;
   }
-  const Range range = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part, &s_at);
-  const long long w0 = range.w0, w1 = range.w1;
-  if (w0 >= w1) return;
+  long long left = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part, smem, &s_at);
+  if (left <= 0) {
+    check_others<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, TT_THREADS / 32);
+    return;
+  }
   int s = s_at.s;
   long long off = s_at.off;
   SeqInfo q = s_at.q;
+  bool first = true;  // piece of this CTA
   load_tree(a, s, q.m, s_tree);
 
   const uint32_t sm0 = smem_u32(smem), qs0 = sm0 + (uint32_t)Sh::Q_OFF;
   const int lu = tid % UNITS, lr = tid / UNITS;  // this thread's unit and first row of a tile
   constexpr int LR = TT_THREADS / UNITS;         // rows of a pass
-  for (long long w = w0; w < w1;) {
+  while (left > 0) {
     if (off >= q.work()) {  // the next sequence with work
       s++;
       off = 0;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
       continue;
     }
     const int unit = (int)div_ll(off, q.tiles), t0 = (int)(off - (long long)unit * q.tiles);
-    const int t1 = (int)min((long long)q.tiles, t0 + (w1 - w));
+    const int t1 = (int)min((long long)q.tiles, t0 + left);
     const int kvh = unit % a.nkv, row0 = unit / a.nkv * ROWS, M = q.m * a.G;
 
     // positions of tile t (context tiles only)
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
       }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == q.tiles;
-    const size_t slot = (size_t)blockIdx.x * 2 + (w > w0 ? 1 : 0);
+    const size_t slot = (size_t)blockIdx.x * 2 + (first ? 0 : 1);
     for (int e = tid; e < ROWS * UNITS; e += TT_THREADS) {
       // rows of the output are contiguous, rows of a piece are neighbours
       const int r = whole ? e / UNITS : e % ROWS, u = whole ? e % UNITS : e / ROWS, m = row0 + r;
@@ -427,9 +429,11 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
         if (u == 0) a.part_ml[slot * ROWS + r] = make_float2(m2, l);
       }
     }
-    w += t1 - t0;
+    left -= t1 - t0;
     off += t1 - t0;
+    first = false;
   }
+  check_others<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, TT_THREADS / 32);
 }
 
 // ---------------------------------------------------------------------------
@@ -459,13 +463,13 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
   const longlong2 p0 = __ldcg(reinterpret_cast<const longlong2*>(a.plan + s));
   const int4 p1 = __ldcg(reinterpret_cast<const int4*>(a.plan + s) + 1);
   const long long before = p0.x, share = p0.y;
-  const int tiles = p1.x, nodes = p1.y;
-  int st = p1.z;
+  const int tiles = p1.x, padded = p1.y, nodes = p1.z;
+  int st = p1.w;
   if (blk * TJ_ROWS >= nodes * a.G) return;
   const bool live = m < nodes * a.G;
   // the rows' unit (one for all of them: blocks do not cross units), and the
   // CTAs that hold its first and last tile
-  const long long u0 = before + (long long)(blk * TJ_ROWS / a.rows * a.nkv + kvh) * tiles, u1 = u0 + tiles;
+  const long long u0 = before + (long long)(blk * TJ_ROWS / a.rows * a.nkv + kvh) * padded, u1 = u0 + tiles;
   const int b0 = st == 0 ? (int)div_ll(u0, share) : 0, b1 = st == 0 ? (int)div_ll(u1 - 1, share) : 0;
   if (a.part_err != nullptr && st == 0) {  // CTAs that gave up on a wait
     bool gave_up = false;

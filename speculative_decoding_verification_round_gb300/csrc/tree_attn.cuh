@@ -38,9 +38,9 @@ struct TreePlan {
   long long before;  // tiles of the sequences in front of it
   long long share;   // tiles of a CTA
   int tiles;         // of each of its units
+  int padded;        // and with the rest of its last piece
   int nodes;         // rows of the output that are the call's to write
   int status;
-  int pad;
 };
 
 namespace {
@@ -117,126 +117,181 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return a / b;
 }
 
-// Tiles of a CTA: CTA b takes [b * share, (b + 1) * share) of the total.
-__device__ __forceinline__ long long share_of(long long total, int n) {
-  return div_ll(total + n - 1, n);
+// The cut: CTA b takes tiles [b * share, (b + 1) * share) of the units laid
+// end to end.  An even share of the total gives many CTAs the end of one unit
+// and the start of the next: two pieces, each with its own first loads and its
+// own end, which cost as much as about three tiles.  Where a share of up to
+// three tiles more lets every CTA have one piece of one unit (the last piece
+// of a unit shorter), that is taken: units count as padded to whole shares.
+struct Cut {
+  long long share;
+  bool pieces;
+  // tiles of a unit of q's, and with a cut into pieces the rest of its last
+  __device__ __forceinline__ int padded(const SeqInfo& q) const {
+    return pieces ? (int)(((unsigned)q.tiles + (unsigned)share - 1) / (unsigned)share * (unsigned)share) : q.tiles;
+  }
+  __device__ __forceinline__ long long work(const SeqInfo& q) const { return (long long)q.units * padded(q); }
+};
+constexpr int CUT_MORE = 4;     // shares that are tried: the even one, and up to three tiles more
+constexpr int CUT_LONG = 64;    // from here on no share is tried
+// q: this thread's sequence (with a cut into pieces there are no more of them
+// than threads).  scratch: 40 bytes a thread.
+template <int THREADS>
+__device__ __forceinline__ Cut cut_work(const TreeArgs& a, int rows, int tile_shift, int n_cta, long long* s_part,
+                                        void* scratch, SeqInfo& q) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long total = 0, chunk = 0;
+  for (int base = 0; base < a.n_seq; base += THREADS) {
+    long long mine = 0;
+    if (base + tid < a.n_seq) {
+      q = seq_info(a, base + tid, rows, tile_shift);
+      mine = q.work();
+    }
+    block_excl<THREADS>(mine, s_part, &chunk);
+    total += chunk;
+  }
+  Cut c;
+  c.share = max(div_ll(total + n_cta - 1, n_cta), 1ll);
+  c.pieces = false;
+  if (a.n_seq > THREADS || c.share >= CUT_LONG) return c;
+  int2* seq = reinterpret_cast<int2*>(scratch);
+  unsigned long long* sums = reinterpret_cast<unsigned long long*>(seq + THREADS);
+  if (tid < a.n_seq) seq[tid] = make_int2(q.units, q.tiles);
+  __syncthreads();
+  const unsigned share = (unsigned)c.share + tid % CUT_MORE;
+  unsigned long long n = 0;
+  for (int s = tid / CUT_MORE; s < a.n_seq; s += THREADS / CUT_MORE)
+    n += (unsigned long long)seq[s].x * (((unsigned)seq[s].y + share - 1) / share);
+#pragma unroll
+  for (int off = CUT_MORE; off < 32; off *= 2) n += __shfl_xor_sync(0xffffffffu, n, off);
+  if (lane < CUT_MORE) sums[warp * CUT_MORE + lane] = n;
+  __syncthreads();
+#pragma unroll
+  for (int more = CUT_MORE - 1; more >= 0; more--) {
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; w++) n += sums[w * CUT_MORE + more];
+    if (n <= (unsigned long long)n_cta) {
+      c.pieces = true;
+      c.share = share - tid % CUT_MORE + more;
+    }
+  }
+  return c;
 }
 
 __device__ __forceinline__ int node_of(const TreeArgs& a, int m) {  // m / G
   return a.G == 1 ? m : (int)__umulhi((unsigned)m, a.g_inv);
 }
 
-// The last CTA of a grid has no tiles: it checks the sequences (tree and
-// pages; slot, length and count come from seq_info) and writes their plans
-// and status, while the others work.  One warp per sequence.
-template <int THREADS>
-__device__ __forceinline__ void check_sequences(const TreeArgs& a, int rows, int tile_shift, int n_cta,
-                                                long long* s_part) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long total = 0, chunk = 0;
-  for (int base = 0; base < a.n_seq; base += THREADS) {
-    block_excl<THREADS>(base + tid < a.n_seq ? seq_info(a, base + tid, rows, tile_shift).work() : 0, s_part,
-                        &chunk);
-    total += chunk;
-  }
-  const long long share = max(share_of(total, n_cta), 1ll);
-  long long first = 0;
-  for (int base = 0; base < a.n_seq; base += THREADS) {
-    SeqInfo q;
-    if (base + tid < a.n_seq) q = seq_info(a, base + tid, rows, tile_shift);
-    const long long excl = block_excl<THREADS>(base + tid < a.n_seq ? q.work() : 0, s_part, &chunk);
-    if (base + tid < a.n_seq) {
-      TreePlan p;
-      p.before = first + excl;
-      p.share = share;
-      p.tiles = q.tiles;
-      p.nodes = p.status = p.pad = 0;  // by the warp that checks
-      a.plan[base + tid] = p;
-    }
-    first += chunk;
-  }
-  __syncthreads();
-  for (int s = warp; s < a.n_seq; s += THREADS / 32) {
-    const SeqInfo q = seq_info(a, s, rows, tile_shift);
-    int st = q.bad;
-    if (st == 0) {
-      bool bad = false;
-      if (a.parents != nullptr)
-        for (int i = lane; i < q.m; i += 32) {
-          const int p = a.parents[(int64_t)s * a.nt + i];
-          bad |= p < -1 || p >= i;
-        }
-      if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_TREE;
-      const int held = q.m == 0 || q.len == 0 ? 0 : (q.len - 1) / a.page_size + 1;
-      // with a window, the pages between the sinks and the window may be gone
-      const int e1 = q.sinks > 0 ? (q.sinks - 1) / a.page_size + 1 : 0;
-      const int e0 = q.lo < q.len ? q.lo / a.page_size : held;
-      bad = false;
-      for (int e = lane; e < held; e += 32) {
-        if (e >= e1 && e < e0) continue;
-        const int p = a.table[(int64_t)q.slot * a.max_pages + e];
-        bad |= p < 0 || p >= a.n_pages;
+// Checks a sequence (tree and pages; slot, length and count come from
+// seq_info) and writes its status.  A warp.
+__device__ __forceinline__ void check_sequence(const TreeArgs& a, int s, int rows, int tile_shift) {
+  const int lane = threadIdx.x & 31;
+  const SeqInfo q = seq_info(a, s, rows, tile_shift);
+  int st = q.bad;
+  if (st == 0) {
+    bool bad = false;
+    if (a.parents != nullptr)
+      for (int i = lane; i < q.m; i += 32) {
+        const int p = a.parents[(int64_t)s * a.nt + i];
+        bad |= p < -1 || p >= i;
       }
-      if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_PAGE;
-    }
-    if (lane == 0) {
-      a.plan[s].nodes = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
-      a.plan[s].status = st;
-      a.status[s] = st;
-    }
+    if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_TREE;
+    const int held = q.m == 0 || q.len == 0 ? 0 : (q.len - 1) / a.page_size + 1;
+    // with a window, the pages between the sinks and the window may be gone
+    const int e1 = q.sinks > 0 ? min(held, (q.sinks - 1) / a.page_size + 1) : 0;
+    const int e0 = q.lo < q.len ? q.lo / a.page_size : held;
+    const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
+    bad = false;
+    auto look = [&](int e) {
+      const int p = row[e];
+      bad |= p < 0 || p >= a.n_pages;
+    };
+#pragma unroll 4
+    for (int e = lane; e < e1; e += 32) look(e);
+#pragma unroll 4
+    for (int e = max(e0, e1) + lane; e < held; e += 32) look(e);
+    if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_PAGE;
+  }
+  if (lane == 0) {
+    a.plan[s].nodes = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
+    a.plan[s].status = st;
+    a.status[s] = st;
   }
 }
 
-// Finds this CTA's first tile: the sequence that holds tile b * share (and
-// how far into its work) goes to *at; returns its tiles' range, empty if it
-// has none.
-struct Range {
-  long long w0, w1;
-};
-struct Start {
-  SeqInfo q;
-  long long off;
-  int s;
-};
+// The last CTA of a grid has no tiles: it writes the sequences' plans, while
+// the others work, and checks the first of them, four a warp; those behind
+// them are checked by warps of the others.
+constexpr int CHECKS_A_WARP = 4;
 template <int THREADS>
-__device__ __forceinline__ Range find_range(const TreeArgs& a, int rows, int tile_shift, int n_cta,
-                                            long long* s_part, Start* at) {
-  long long total = 0, mine = 0, excl = 0, chunk = 0;
-  const int tid = threadIdx.x;
+__device__ __forceinline__ void plan_sequences(const TreeArgs& a, int rows, int tile_shift, int n_cta,
+                                               long long* s_part, void* scratch) {
+  const int tid = threadIdx.x, warp = tid >> 5;
+  constexpr int FIRST = CHECKS_A_WARP * (THREADS / 32);
   SeqInfo q;
+  const Cut c = cut_work<THREADS>(a, rows, tile_shift, n_cta, s_part, scratch, q);
+  long long first = 0, chunk = 0;
   for (int base = 0; base < a.n_seq; base += THREADS) {
-    mine = 0;
+    if (a.n_seq > THREADS && base + tid < a.n_seq) q = seq_info(a, base + tid, rows, tile_shift);
+    const long long excl = block_excl<THREADS>(base + tid < a.n_seq ? c.work(q) : 0, s_part, &chunk);
     if (base + tid < a.n_seq) {
-      q = seq_info(a, base + tid, rows, tile_shift);
-      mine = q.work();
-    }
-    excl = block_excl<THREADS>(mine, s_part, &chunk);
-    total += chunk;
-  }
-  const long long share = share_of(total, n_cta);
-  Range r;
-  r.w0 = share * blockIdx.x;
-  r.w1 = min(total, r.w0 + share);
-  if (r.w0 >= r.w1) return r;
-  long long first = 0;
-  for (int base = 0; base < a.n_seq; base += THREADS) {
-    if (a.n_seq > THREADS) {
-      mine = 0;
-      if (base + tid < a.n_seq) {
-        q = seq_info(a, base + tid, rows, tile_shift);
-        mine = q.work();
-      }
-      excl = block_excl<THREADS>(mine, s_part, &chunk);
-    }
-    if (first + excl <= r.w0 && r.w0 < first + excl + mine) {
-      at->q = q;
-      at->off = r.w0 - first - excl;
-      at->s = base + tid;
+      TreePlan* p = a.plan + base + tid;
+      p->before = first + excl;
+      p->share = c.share;
+      p->tiles = q.tiles;
+      p->padded = c.padded(q);
     }
     first += chunk;
   }
+  for (int s = warp; s < min(a.n_seq, FIRST); s += THREADS / 32) check_sequence(a, s, rows, tile_shift);
+}
+// The other CTAs' share of the checks, over `warps` of each.
+template <int THREADS>
+__device__ __forceinline__ void check_others(const TreeArgs& a, int rows, int tile_shift, int n_cta, int warps) {
+  constexpr int FIRST = CHECKS_A_WARP * (THREADS / 32);
+  for (long long s = FIRST + (long long)blockIdx.x * warps + (threadIdx.x >> 5); s < a.n_seq;
+       s += (long long)n_cta * warps)
+    check_sequence(a, (int)s, rows, tile_shift);
+}
+
+// Finds this CTA's first tile: the sequence that holds tile b * share (and
+// how far into its work) goes to *at; returns how many it
+// takes (0 or less: none).  (What pads a unit stands behind its last piece, which ends there.)
+struct Start {
+  SeqInfo q;
+  long long off;
+  int s, left;  // with a cut into pieces: tiles of the unit from here on
+};
+template <int THREADS>
+__device__ __forceinline__ long long find_range(const TreeArgs& a, int rows, int tile_shift, int n_cta,
+                                            long long* s_part, void* scratch, Start* at) {
+  const int tid = threadIdx.x;
+  SeqInfo q;
+  const Cut c = cut_work<THREADS>(a, rows, tile_shift, n_cta, s_part, scratch, q);
+  const long long w0 = c.share * blockIdx.x;
+  long long first = 0, chunk = 0;
+  for (int base = 0; base < a.n_seq; base += THREADS) {
+    if (a.n_seq > THREADS && base + tid < a.n_seq) q = seq_info(a, base + tid, rows, tile_shift);
+    const long long mine = base + tid < a.n_seq ? c.work(q) : 0;
+    const long long excl = block_excl<THREADS>(mine, s_part, &chunk);
+    if (first + excl <= w0 && w0 < first + excl + mine) {
+      const long long off = w0 - first - excl;
+      at->q = q;
+      at->off = off;
+      at->s = base + tid;
+      if (c.pieces) {  // (of at most CUT_LONG tiles a CTA: 32 bits)
+        const unsigned padded = (unsigned)c.padded(q), unit = (unsigned)off / padded, t0 = (unsigned)off % padded;
+        at->off = unit * q.tiles + t0;
+        at->left = q.tiles - (int)t0;
+      }
+    }
+    first += chunk;
+  }
+  long long n = min(first, w0 + c.share) - w0;
   __syncthreads();
-  return r;
+  if (c.pieces && n > 0) n = min(n, (long long)at->left);  // one piece, without what pads it
+  return n;
 }
 
 // ---------------------------------------------------------------------------

@@ -208,13 +208,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   grid_dep_launch();  // the joining kernel may get ready
   const int n_cta = gridDim.x - 1;
   if ((int)blockIdx.x == n_cta) {
-    check_sequences<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part);
+    plan_sequences<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part, smem);
     return;
   }
-  const Range range = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part, &sh.at);
-  const long long w0 = range.w0, w1 = range.w1;
-  if (w0 >= w1 || (sm0 & 1023u) != 0u) {  // no tiles (a base off the swizzle's atoms never happens)
-    if (tid == 0) a.part_err[blockIdx.x] = w0 < w1;
+  const long long my_tiles = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part, smem, &sh.at);
+  if (my_tiles <= 0 || (sm0 & 1023u) != 0u) {  // no tiles (a base off the swizzle's atoms never happens)
+    if (tid == 0) a.part_err[blockIdx.x] = my_tiles > 0;
+    if (warp < 8) check_others<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, 8);
     return;
   }
   auto bar = [&](unsigned long long& b) { return smem_u32(&b); };
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   uint32_t item0 = 0, seg = 0;  // ring items and pieces before this one
   // what a piece is
   int t0 = 0, n = 0, kvh = 0, row0 = 0, M = 0;
-  auto next_piece = [&](long long w) {
+  auto next_piece = [&](long long left) {
     while (off >= q.work()) {
       s++;
       off = 0;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
     }
     const int unit = (int)div_ll(off, q.tiles);
     t0 = (int)(off - (long long)unit * q.tiles);
-    n = (int)min((long long)(q.tiles - t0), w1 - w);
+    n = (int)min((long long)(q.tiles - t0), left);
     kvh = unit % a.nkv;
     row0 = unit / a.nkv * ROWS;
     M = q.m * a.G;
@@ -314,8 +314,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       }
       return x;
     };
-    for (long long w = w0; w < w1; w += n, off += n, item0 += 2 * n, seg++) {
-      next_piece(w);
+    for (long long left = my_tiles; left > 0; left -= n, off += n, item0 += 2 * n, seg++) {
+      next_piece(left);
       // the rows of the next tile are looked up while this one waits for its buffer
       Rows next = lookup(t0);
       for (int i = 0; i < n; i++) {
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         }
         __syncwarp();
       };
-      for (long long w = w0; w < w1; w += n, off += n, item0 += 2 * n, seg++) {
-        next_piece(w);
+      for (long long left = my_tiles; left > 0; left -= n, off += n, item0 += 2 * n, seg++) {
+        next_piece(left);
         const int step = TWO ? 1 : 2;
         int i = TWO ? 0 : j;
         if (i >= n) continue;
@@ -439,14 +439,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
     __syncwarp();
   } else {
     // ======================================================= the softmax
+    check_others<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, 8);  // (here, as the first keys are on their way)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     const int j = warp >> 2, r = tid & 127;  // stream, lane of tensor memory
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + j * 128, tO = tmem + lanes + 256 + j * 128;
     const float scale = fabsf(a.scale_log2);
     uint32_t n_s = 0, n_o = 0;  // tiles and pieces of this stream so far
-    for (long long w = w0; w < w1; w += n, off += n, item0 += 2 * n, seg++) {
-      next_piece(w);
+    for (long long left = my_tiles; left > 0; left -= n, off += n, item0 += 2 * n, seg++) {
+      next_piece(left);
       const int nj = TWO ? n : (n - j + 1) / 2;
       // this thread's row of the unit; its chunks of the q tile
       const int rr = ROWS == 64 ? r & 63 : ROWS == 128 ? r : 128 * j + r;
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         tc_fence_after();
       }
       const bool whole = t0 == 0 && n == q.tiles;
-      const size_t slot = (size_t)blockIdx.x * 2 + (w > w0 ? 1 : 0);
+      const size_t slot = (size_t)blockIdx.x * 2 + (seg > 0 ? 1 : 0);
       // this warp's part of the q tiles, free now, turns rows of lanes into
       // rows of memory: 32 rows x D dimensions of fp16, 16-byte chunks swizzled
       const uint32_t turn = sm0 + warp * 32 * HD * 2;
