@@ -110,18 +110,19 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
   int s = s_at.s;
   long long off = s_at.off;
   SeqInfo q = s_at.q;
-  bool first = true;  // piece of this CTA
-  load_tree(a, s, q.m, s_tree);
+  bool first = true, new_tree = true;  // piece of this CTA; of its sequence
 
   const uint32_t sm0 = smem_u32(smem), qs0 = sm0 + (uint32_t)Sh::Q_OFF;
   const int lu = tid % UNITS, lr = tid / UNITS;  // this thread's unit and first row of a tile
-  constexpr int LR = TT_THREADS / UNITS;         // rows of a pass
+  constexpr int LR = TT_THREADS / UNITS, WR = 32 / UNITS;  // rows of a pass, and of a warp in it
+  // the row of a tile that this lane looks up for its warp
+  const int my_row = (lane % 16) / WR * LR + warp * WR + lane % WR;
   while (left > 0) {
     if (off >= q.work()) {  // the next sequence with work
       s++;
       off = 0;
       q = seq_info(a, s, ROWS, TT_SHIFT);
-      if (q.work() > 0) load_tree(a, s, q.m, s_tree);
+      new_tree = true;
       continue;
     }
     const int unit = (int)div_ll(off, q.tiles), t0 = (int)(off - (long long)unit * q.tiles);
@@ -131,45 +132,50 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
     // positions of tile t (context tiles only)
     const int n_sink = q.n_sink, w_tile = q.w_tile, last = q.tiles - 1;
     auto tile_base = [&](int t) { return (t < n_sink ? t : w_tile + t - n_sink) * TT_KEYS; };
-    auto load_tile = [&](int t) {
-      const uint32_t ks = sm0 + (uint32_t)(t % TT_STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
-      if (t == last) {  // the tree's nodes
-#pragma unroll
-        for (int i = 0; i < TT_KEYS / LR; i++) {
-          const int r = lr + i * LR;
-          const bool ok = r < q.m;
-          const int64_t at = ((int64_t)s * a.nt + (ok ? r : 0)) * a.kv_stride + kvh * HD + lu * 8;
-          cp16(ks + tile_off<HD>(r, lu), a.k_new + at, ok);
-          cp16(vs + tile_off<HD>(r, lu), a.v_new + at, ok);
-        }
-      } else {
-        const int base = tile_base(t);
-        const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
-        int pages[TT_KEYS / LR], ats[TT_KEYS / LR];
-#pragma unroll
-        for (int i = 0; i < TT_KEYS / LR; i++) {
-          const int pos = min(base + lr + i * LR, q.len - 1);
+    // The cache row (or the tree's node) of this lane's row of tile t, ~0 for
+    // zeros: looked up a tile ahead of its load, as the table is memory, too.
+    // (2^32 rows would be 550 GB.)
+    auto lookup = [&](int t) {
+      uint32_t x = ~0u;
+      if (t == last) {
+        if (my_row < q.m) x = (uint32_t)my_row;
+      } else if (t < t1) {
+        const int pos = tile_base(t) + my_row;
+        if (pos < q.len) {
           const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
-          ats[i] = pos - e * a.page_size;
-          pages[i] = __ldg(row + e);
+          const int pg = __ldg(a.table + (int64_t)q.slot * a.max_pages + e);
+          if (pg >= 0 && pg < a.n_pages)
+            x = ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
         }
+      }
+      return x;
+    };
+    auto load_tile = [&](int t, uint32_t at) {
+      const uint32_t ks = sm0 + (uint32_t)(t % TT_STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
+      const bool tree = t == last;
+      const int64_t row = tree ? a.kv_stride : HD, from = tree ? (int64_t)s * a.nt * a.kv_stride + kvh * HD : 0;
+      const __half* kp = (tree ? a.k_new : a.k) + from + lu * 8;
+      const __half* vp = (tree ? a.v_new : a.v) + from + lu * 8;
 #pragma unroll
-        for (int i = 0; i < TT_KEYS / LR; i++) {
-          const int r = lr + i * LR;
-          const bool ok = base + r < q.len && pages[i] >= 0 && pages[i] < a.n_pages;
-          const int64_t at =
-              (((int64_t)(ok ? pages[i] : 0) * a.nkv + kvh) * a.page_size + (ok ? ats[i] : 0)) * HD + lu * 8;
-          cp16(ks + tile_off<HD>(r, lu), a.k + at, ok);
-          cp16(vs + tile_off<HD>(r, lu), a.v + at, ok);
-        }
+      for (int i = 0; i < TT_KEYS / LR; i++) {
+        const uint32_t x = __shfl_sync(0xffffffffu, at, i * WR + lane / UNITS);
+        const bool ok = x != ~0u;
+        const int64_t off = (int64_t)(ok ? x : 0u) * row;
+        cp16(ks + tile_off<HD>(lr + i * LR, lu), kp + off, ok);
+        cp16(vs + tile_off<HD>(lr + i * LR, lu), vp + off, ok);
       }
     };
 
     // ---- the piece's first tiles, and its q rows
+    uint32_t ahead[TT_STAGES];
+#pragma unroll
+    for (int i = 0; i < TT_STAGES; i++) ahead[i] = lookup(t0 + i);
+    if (new_tree) load_tree(a, s, q.m, s_tree);
+    new_tree = false;
     __syncthreads();  // the last piece's exchange and q rows have been read
 #pragma unroll
     for (int i = 0; i < TT_STAGES - 1; i++) {
-      if (t0 + i < t1) load_tile(t0 + i);
+      if (t0 + i < t1) load_tile(t0 + i, ahead[i]);
       if (i == 0) {
         for (int e = tid; e < ROWS * UNITS; e += TT_THREADS) {
           const int r = e / UNITS, u = e % UNITS, m = row0 + r;
@@ -205,8 +211,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
     for (int t = t0; t < t1; t++) {
       asm volatile("cp.async.wait_group %0;" ::"n"(TT_STAGES - 2) : "memory");
       __syncthreads();
-      if (t + TT_STAGES - 1 < t1) load_tile(t + TT_STAGES - 1);
+      if (t + TT_STAGES - 1 < t1) load_tile(t + TT_STAGES - 1, ahead[TT_STAGES - 1]);
       asm volatile("cp.async.commit_group;");
+      ahead[TT_STAGES - 1] = lookup(t + TT_STAGES);
       const uint32_t ks = sm0 + (uint32_t)(t % TT_STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
       const int key0 = kg * KEYS;
 
@@ -408,9 +415,11 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
         const float2 ml = s_ml[rb * KG + k][rl];
         const float wk = exp2f(ml.x - ref);
         l = fmaf(ml.y, wk, l);
-        const float* src = x + ((size_t)k * ROWS + r) * Sh::XROW + u * 8;
+        const float4* src = reinterpret_cast<const float4*>(x + ((size_t)k * ROWS + r) * Sh::XROW + u * 8);
+        const float4 s0 = src[0], s1 = src[1];
+        const float v[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-        for (int d = 0; d < 8; d++) acc[d] = fmaf(src[d], wk, acc[d]);
+        for (int d = 0; d < 8; d++) acc[d] = fmaf(v[d], wk, acc[d]);
       }
       if (whole) {
         const float inv = 1.0f / l;
