@@ -25,7 +25,6 @@ namespace {
 
 constexpr int TT_SHIFT = 6, TT_KEYS = 1 << TT_SHIFT;  // positions per tile
 constexpr int TT_THREADS = 128;
-constexpr int TT_STAGES = 3;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -72,22 +71,29 @@ __device__ __forceinline__ uint32_t tile_off(int r, int u) {
 // MT m16 tiles of rows against 64 / KG keys of every tile, with its own
 // running (max, sum, O), joined over the key groups at the end of a piece.
 // ---------------------------------------------------------------------------
+// CTAs of an SM: two of 128 dimensions (three with two stages each: no gain,
+// 64 sequences of one node over 512 positions 74 -> 78 us), four of 64
+// dimensions and 16 rows (16 sequences of 32768 positions 56 us with three, 54
+// with four; with a window of 4096 17.2 us with two, 15.6 with four).
+constexpr int resident(int hd, int rows) { return hd == 64 && rows == 16 ? 4 : 2; }
+
 template <int HD, int MT, int RTW>
 struct Shape {
   static constexpr int ROWS = 16 * MT * RTW;
+  static constexpr int RESIDENT = resident(HD, ROWS), STAGES = 3;
   static constexpr int KG = 4 / RTW;
   static constexpr int KEYS = TT_KEYS / KG;
   static constexpr int TILE = TT_KEYS * HD * 2;  // bytes of a K (or V) tile
   static constexpr int XROW = HD + 8;            // floats of an exchange row (padded)
-  static constexpr size_t Q_OFF = (size_t)TT_STAGES * 2 * TILE;
+  static constexpr size_t Q_OFF = (size_t)STAGES * 2 * TILE;
   static constexpr size_t SMEM = Q_OFF + (size_t)ROWS * HD * 2;
   static_assert((size_t)KG * ROWS * (XROW * 4 + 8) <= Q_OFF, "the exchange fits over the tiles");
 };
 
 template <int HD, int MT, int RTW>
-__global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree_attn_kernel(const TreeArgs a) {
   using Sh = Shape<HD, MT, RTW>;
-  constexpr int ROWS = Sh::ROWS, KG = Sh::KG, KEYS = Sh::KEYS, NB = KEYS / 8, UNITS = HD / 8;
+  constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, KG = Sh::KG, KEYS = Sh::KEYS, NB = KEYS / 8, UNITS = HD / 8;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ TreeSmem s_tree;
   __shared__ long long s_part[TT_THREADS / 32];
@@ -151,7 +157,7 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
       return x;
     };
     auto load_tile = [&](int t, uint32_t at) {
-      const uint32_t ks = sm0 + (uint32_t)(t % TT_STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
+      const uint32_t ks = sm0 + (uint32_t)(t % STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
       const bool tree = t == last;
       const int64_t row = tree ? a.kv_stride : HD, from = tree ? (int64_t)s * a.nt * a.kv_stride + kvh * HD : 0;
       const __half* kp = (tree ? a.k_new : a.k) + from + lu * 8;
@@ -167,14 +173,14 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
     };
 
     // ---- the piece's first tiles, and its q rows
-    uint32_t ahead[TT_STAGES];
+    uint32_t ahead[STAGES];
 #pragma unroll
-    for (int i = 0; i < TT_STAGES; i++) ahead[i] = lookup(t0 + i);
+    for (int i = 0; i < STAGES; i++) ahead[i] = lookup(t0 + i);
     if (new_tree) load_tree(a, s, q.m, s_tree);
     new_tree = false;
     __syncthreads();  // the last piece's exchange and q rows have been read
 #pragma unroll
-    for (int i = 0; i < TT_STAGES - 1; i++) {
+    for (int i = 0; i < STAGES - 1; i++) {
       if (t0 + i < t1) load_tile(t0 + i, ahead[i]);
       if (i == 0) {
         for (int e = tid; e < ROWS * UNITS; e += TT_THREADS) {
@@ -209,12 +215,12 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
     const int q_row = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix row of a q fragment
 
     for (int t = t0; t < t1; t++) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(TT_STAGES - 2) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
       __syncthreads();
-      if (t + TT_STAGES - 1 < t1) load_tile(t + TT_STAGES - 1, ahead[TT_STAGES - 1]);
+      if (t + STAGES - 1 < t1) load_tile(t + STAGES - 1, ahead[STAGES - 1]);
       asm volatile("cp.async.commit_group;");
-      ahead[TT_STAGES - 1] = lookup(t + TT_STAGES);
-      const uint32_t ks = sm0 + (uint32_t)(t % TT_STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
+      ahead[STAGES - 1] = lookup(t + STAGES);
+      const uint32_t ks = sm0 + (uint32_t)(t % STAGES) * 2 * Sh::TILE, vs = ks + Sh::TILE;
       const int key0 = kg * KEYS;
 
       // ---- S = Q K^T
@@ -400,7 +406,9 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
     __syncthreads();
     const bool whole = t0 == 0 && t1 == q.tiles;
     const size_t slot = (size_t)blockIdx.x * 2 + (first ? 0 : 1);
-    for (int e = tid; e < ROWS * UNITS; e += TT_THREADS) {
+#pragma unroll
+    for (int e0 = 0; e0 < ROWS * UNITS; e0 += TT_THREADS) {
+      const int e = e0 + tid;
       // rows of the output are contiguous, rows of a piece are neighbours
       const int r = whole ? e / UNITS : e % ROWS, u = whole ? e % UNITS : e / ROWS, m = row0 + r;
       if (m >= M) continue;
@@ -449,23 +457,23 @@ __global__ void __launch_bounds__(TT_THREADS, 2) tree_attn_kernel(const TreeArgs
 // the joining kernel: a CTA has 32 rows (node, head) of one kv head, a lane a
 // row and 8 dimensions, eight pieces' loads in flight together.  Joins the
 // pieces of the rows' unit in the order of the positions, or writes NaN for a
-// sequence in error.  SPLIT: the CTA has 8 dimensions and its warps a quarter
+// sequence in error.  SPLIT: the CTA has 8 dimensions and its warps an eighth
 // of the pieces each (the kernel for few rows cuts a long context into dozens
 // of pieces: 8 nodes over 4096 positions, 33 pieces, 22 -> 18 us); otherwise
 // 32 dimensions and every warp all pieces (the tcgen05 kernel's few: 12 x 16
 // nodes 37 -> 29 us).
 // ---------------------------------------------------------------------------
-constexpr int TJ_THREADS = 128, TJ_WARPS = TJ_THREADS / 32;
 constexpr int TJ_ROWS = 32;
+constexpr int join_warps(bool split) { return split ? 8 : 4; }
 
 template <int HD, bool SPLIT>
-__global__ void __launch_bounds__(TJ_THREADS)
-tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
+__global__ void __launch_bounds__(32 * join_warps(SPLIT))
+tree_join_kernel(const TreeArgs a, int blocks, int slices) {
+  constexpr int TJ_WARPS = join_warps(SPLIT), TJ_THREADS = 32 * TJ_WARPS;
   __shared__ float s_o[TJ_WARPS][8][TJ_ROWS];
   __shared__ float2 s_ml[TJ_WARPS][TJ_ROWS];
-  constexpr int SLICES = HD / (SPLIT ? 8 : 8 * TJ_WARPS);
-  const int slice = blockIdx.x % SLICES, kvh = blockIdx.x / SLICES % a.nkv;
-  const int blk = blockIdx.x / (SLICES * a.nkv) % blocks, s = blockIdx.x / (SLICES * a.nkv) / blocks;
+  const int slice = blockIdx.x % slices, kvh = blockIdx.x / slices % a.nkv;
+  const int blk = blockIdx.x / (slices * a.nkv) % blocks, s = blockIdx.x / (slices * a.nkv) / blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int m = blk * TJ_ROWS + lane, r = m & (a.rows - 1), node = node_of(a, m);
   grid_dep_wait();
@@ -489,80 +497,81 @@ tree_join_kernel(const TreeArgs a, int n_cta, int blocks) {
     }
   }
   if (st == 0 && b0 == b1) return;  // whole: written by its CTA
-  const int d0 = 8 * (SPLIT ? slice : slice * TJ_WARPS + warp);
-  uint4* dst = reinterpret_cast<uint4*>(
-      a.out + (((int64_t)s * a.nt + node) * a.nq + kvh * a.G + (m - node * a.G)) * HD + d0);
-  if (st != 0) {
-    if (live) *dst = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
-    return;
-  }
-  const float4* po = reinterpret_cast<const float4*>(a.part_o) + (size_t)(d0 / 4) * a.rows + r;
-  const size_t piece = (size_t)a.rows * (HD / 4);
-  constexpr int U = 8;
-  const int per = SPLIT ? (b1 - b0 + TJ_WARPS) / TJ_WARPS : b1 + 1 - b0;  // pieces of a warp
-  const int w0 = SPLIT ? b0 + warp * per : b0, w1 = min(b1 + 1, w0 + per);
-  float mx = -INFINITY, l = 0.0f, o[8] = {};
-  for (int bb = w0; bb < w1; bb += U) {
-    float2 ml[U];
-    float4 v[U][2];
+  for (int d0 = 8 * (SPLIT ? slice : slice * TJ_WARPS + warp); d0 < HD; d0 += 8 * (SPLIT ? slices : slices * TJ_WARPS)) {
+    uint4* dst = reinterpret_cast<uint4*>(
+        a.out + (((int64_t)s * a.nt + node) * a.nq + kvh * a.G + (m - node * a.G)) * HD + d0);
+    if (st != 0) {
+      if (live) *dst = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+      continue;
+    }
+    const float4* po = reinterpret_cast<const float4*>(a.part_o) + (size_t)(d0 / 4) * a.rows + r;
+    const size_t piece = (size_t)a.rows * (HD / 4);
+    constexpr int U = 8;
+    const int per = SPLIT ? (b1 - b0 + TJ_WARPS) / TJ_WARPS : b1 + 1 - b0;  // pieces of a warp
+    const int w0 = SPLIT ? b0 + warp * per : b0, w1 = min(b1 + 1, w0 + per);
+    float mx = -INFINITY, l = 0.0f, o[8] = {};
+    for (int bb = w0; bb < w1; bb += U) {
+      float2 ml[U];
+      float4 v[U][2];
 #pragma unroll
-    for (int j = 0; j < U; j++) {
-      ml[j] = make_float2(-INFINITY, 0.0f);
-      v[j][0] = v[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (bb + j < w1 && live) {
-        // piece of CTA b: its first, unless it began in front of the unit
-        const size_t slot = (size_t)(bb + j) * 2 + (share * (bb + j) < u0 ? 1 : 0);
-        ml[j] = __ldcg(a.part_ml + slot * a.rows + r);
-        v[j][0] = __ldcg(po + slot * piece);
-        v[j][1] = __ldcg(po + slot * piece + a.rows);
+      for (int j = 0; j < U; j++) {
+        ml[j] = make_float2(-INFINITY, 0.0f);
+        v[j][0] = v[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (bb + j < w1 && live) {
+          // piece of CTA b: its first, unless it began in front of the unit
+          const size_t slot = (size_t)(bb + j) * 2 + (share * (bb + j) < u0 ? 1 : 0);
+          ml[j] = __ldcg(a.part_ml + slot * a.rows + r);
+          v[j][0] = __ldcg(po + slot * piece);
+          v[j][1] = __ldcg(po + slot * piece + a.rows);
+        }
+      }
+      float m2 = mx;
+#pragma unroll
+      for (int j = 0; j < U; j++) m2 = fmaxf(m2, ml[j].x);
+      const float ref = m2 == -INFINITY ? 0.0f : m2, alpha = exp2_fast(mx - ref);
+      mx = m2;
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < 8; d++) o[d] *= alpha;
+#pragma unroll
+      for (int j = 0; j < U; j++) {
+        const float w = exp2_fast(ml[j].x - ref);
+        l = fmaf(ml[j].y, w, l);
+        o[0] = fmaf(v[j][0].x, w, o[0]);
+        o[1] = fmaf(v[j][0].y, w, o[1]);
+        o[2] = fmaf(v[j][0].z, w, o[2]);
+        o[3] = fmaf(v[j][0].w, w, o[3]);
+        o[4] = fmaf(v[j][1].x, w, o[4]);
+        o[5] = fmaf(v[j][1].y, w, o[5]);
+        o[6] = fmaf(v[j][1].z, w, o[6]);
+        o[7] = fmaf(v[j][1].w, w, o[7]);
       }
     }
-    float m2 = mx;
+    if (SPLIT) {
 #pragma unroll
-    for (int j = 0; j < U; j++) m2 = fmaxf(m2, ml[j].x);
-    const float ref = m2 == -INFINITY ? 0.0f : m2, alpha = exp2_fast(mx - ref);
-    mx = m2;
-    l *= alpha;
+      for (int d = 0; d < 8; d++) s_o[warp][d][lane] = o[d];
+      s_ml[warp][lane] = make_float2(mx, l);
+      __syncthreads();
+      if (warp != 0) return;
 #pragma unroll
-    for (int d = 0; d < 8; d++) o[d] *= alpha;
+      for (int w = 1; w < TJ_WARPS; w++) mx = fmaxf(mx, s_ml[w][lane].x);
+      l = 0.0f;
 #pragma unroll
-    for (int j = 0; j < U; j++) {
-      const float w = exp2_fast(ml[j].x - ref);
-      l = fmaf(ml[j].y, w, l);
-      o[0] = fmaf(v[j][0].x, w, o[0]);
-      o[1] = fmaf(v[j][0].y, w, o[1]);
-      o[2] = fmaf(v[j][0].z, w, o[2]);
-      o[3] = fmaf(v[j][0].w, w, o[3]);
-      o[4] = fmaf(v[j][1].x, w, o[4]);
-      o[5] = fmaf(v[j][1].y, w, o[5]);
-      o[6] = fmaf(v[j][1].z, w, o[6]);
-      o[7] = fmaf(v[j][1].w, w, o[7]);
+      for (int d = 0; d < 8; d++) o[d] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < TJ_WARPS; w++) {
+        const float2 ml = s_ml[w][lane];
+        const float f = exp2_fast(ml.x - mx);  // mx is finite: every row sees itself
+        l = fmaf(ml.y, f, l);
+#pragma unroll
+        for (int d = 0; d < 8; d++) o[d] = fmaf(s_o[w][d][lane], f, o[d]);
+      }
     }
+    const float inv = 1.0f / l;
+    if (live)
+      *dst = make_uint4(pack_f16(o[0] * inv, o[1] * inv), pack_f16(o[2] * inv, o[3] * inv),
+                        pack_f16(o[4] * inv, o[5] * inv), pack_f16(o[6] * inv, o[7] * inv));
   }
-  if (SPLIT) {
-#pragma unroll
-    for (int d = 0; d < 8; d++) s_o[warp][d][lane] = o[d];
-    s_ml[warp][lane] = make_float2(mx, l);
-    __syncthreads();
-    if (warp != 0) return;
-#pragma unroll
-    for (int w = 1; w < TJ_WARPS; w++) mx = fmaxf(mx, s_ml[w][lane].x);
-    l = 0.0f;
-#pragma unroll
-    for (int d = 0; d < 8; d++) o[d] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < TJ_WARPS; w++) {
-      const float2 ml = s_ml[w][lane];
-      const float f = exp2_fast(ml.x - mx);  // mx is finite: every row sees itself
-      l = fmaf(ml.y, f, l);
-#pragma unroll
-      for (int d = 0; d < 8; d++) o[d] = fmaf(s_o[w][d][lane], f, o[d]);
-    }
-  }
-  const float inv = 1.0f / l;
-  if (live)
-    *dst = make_uint4(pack_f16(o[0] * inv, o[1] * inv), pack_f16(o[2] * inv, o[3] * inv),
-                      pack_f16(o[4] * inv, o[5] * inv), pack_f16(o[6] * inv, o[7] * inv));
 }
 
 // Query rows of a unit.  Up to 32 rows run on the mma.sync kernel, more on
@@ -592,10 +601,12 @@ int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = programmatic_launch() ? 1 : 0;
-    cfg.gridDim = dim3((unsigned)(a.n_seq * blocks * a.nkv * (HD / (on_tc(a.rows) ? 8 * TJ_WARPS : 8))));
-    cfg.blockDim = dim3(TJ_THREADS);
-    e = cudaLaunchKernelEx(&cfg, on_tc(a.rows) ? tree_join_kernel<HD, false> : tree_join_kernel<HD, true>, a,
-                           n_cta, blocks);
+    const long long units = (long long)a.n_seq * blocks * a.nkv;
+    const bool split = units * 8 <= n_cta;
+    const int slices = split ? HD / 8 : units * (HD / 32) <= 1216 ? HD / 32 : 1;
+    cfg.gridDim = dim3((unsigned)(units * slices));
+    cfg.blockDim = dim3(32 * join_warps(split));
+    e = cudaLaunchKernelEx(&cfg, split ? tree_join_kernel<HD, true> : tree_join_kernel<HD, false>, a, blocks, slices);
   }
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("tree attention: ") + cudaGetErrorString(e));
   return SPEC_OK;
@@ -614,9 +625,8 @@ int device_sms() {
   return n > 0 ? n : 1;
 }
 
-// The CTAs with tiles: what is resident, two an SM or one, but for the one
-// that checks.
-int tree_ctas(int rows) { return std::max(1, (on_tc(rows) ? 1 : 2) * device_sms() - 1); }
+// The CTAs with tiles: what is resident, but for the one that plans.
+int tree_ctas(int hd, int rows) { return std::max(1, (on_tc(rows) ? 1 : resident(hd, rows)) * device_sms() - 1); }
 
 int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
   int rc = check_pages(kv, true);
@@ -649,7 +659,7 @@ int tree_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads, size_
   const int rc = check_tree(kv, n_seq, nt, n_q_heads);
   if (rc != SPEC_OK) return rc;
   const size_t rows = rows_of(nt * (n_q_heads / kv->n_kv_heads));
-  const size_t n = tree_ctas((int)rows);
+  const size_t n = tree_ctas(kv->head_dim, (int)rows);
   *bytes = n * 2 * rows * (sizeof(float) * kv->head_dim + sizeof(float2)) +
            (n * sizeof(uint32_t) + 15) / 16 * 16 + (size_t)n_seq * sizeof(TreePlan);
   return SPEC_OK;
@@ -690,7 +700,7 @@ int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint1
   a.out = reinterpret_cast<__half*>(out);
   a.status = status;
   const size_t rows = a.rows = rows_of(a.nt * a.G);
-  const int n_cta = tree_ctas(a.rows);
+  const int n_cta = tree_ctas(kv->head_dim, a.rows);
   a.tile_shift = on_tc(a.rows) ? TREE_TC_SHIFT : TT_SHIFT;
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)n_cta * 2 * rows * kv->head_dim);
