@@ -108,14 +108,15 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree
     plan_sequences<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part, smem);
     return;
   }
-  long long left = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part, smem, &s_at);
+  Start start;
+  long long left = find_range<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, s_part, smem, &s_at, start);
   if (left <= 0) {
     check_others<TT_THREADS>(a, ROWS, TT_SHIFT, n_cta, TT_THREADS / 32);
     return;
   }
-  int s = s_at.s;
-  long long off = s_at.off;
-  SeqInfo q = s_at.q;
+  int s = start.s;
+  long long off = start.off;
+  SeqInfo q = start.q;
   bool first = true, new_tree = true;  // piece of this CTA; of its sequence
 
   const uint32_t sm0 = smem_u32(smem), qs0 = sm0 + (uint32_t)Sh::Q_OFF;

@@ -132,14 +132,63 @@ struct Cut {
   }
   __device__ __forceinline__ long long work(const SeqInfo& q) const { return (long long)q.units * padded(q); }
 };
-constexpr int CUT_MORE = 4;     // shares that are tried: the even one, and up to three tiles more
-constexpr int CUT_LONG = 64;    // from here on no share is tried
+constexpr int CUT_MORE = 4;   // shares that are tried: the even one, and up to three tiles more
+constexpr int CUT_LONG = 64;  // from here on no share is tried
+// The share, from the number of pieces that each one tried makes.
+__device__ __forceinline__ Cut cut_of(long long even, const unsigned (&pieces)[CUT_MORE], int n_cta) {
+  Cut c;
+  c.share = even;
+  c.pieces = false;
+#pragma unroll
+  for (int more = CUT_MORE - 1; more >= 0; more--)
+    if (pieces[more] <= (unsigned)n_cta) {
+      c.pieces = true;
+      c.share = even + more;
+    }
+  return c;
+}
+__device__ __forceinline__ unsigned pieces_of(const SeqInfo& q, unsigned share) {
+  return min((unsigned long long)q.units * (((unsigned)q.tiles + share - 1) / share), 1ull << 20);
+}
+__device__ __forceinline__ long long even_share(long long total, int n_cta) {
+  return max(div_ll(total + n_cta - 1, n_cta), 1ll);
+}
+
+// Inclusive sum over a warp.
+__device__ __forceinline__ long long warp_incl(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += y;
+  }
+  return v;
+}
+
+// Up to 32 sequences: every warp by itself, a lane a sequence (q: this
+// lane's), without a barrier (12 x 16 nodes: 25.5 us with the barriers of the
+// general form, 24.0 without).
+__device__ __forceinline__ Cut cut_work_few(const TreeArgs& a, int rows, int tile_shift, int n_cta, SeqInfo& q) {
+  const int lane = threadIdx.x & 31;
+  q.units = 0;
+  q.tiles = 1;
+  if (lane < a.n_seq) q = seq_info(a, lane, rows, tile_shift);
+  const long long even = even_share(__shfl_sync(0xffffffffu, warp_incl(q.work()), 31), n_cta);
+  unsigned pieces[CUT_MORE];
+#pragma unroll
+  for (int more = 0; more < CUT_MORE; more++)
+    pieces[more] = even < CUT_LONG ? __reduce_add_sync(0xffffffffu, pieces_of(q, (unsigned)even + more)) : ~0u;
+  return cut_of(even, pieces, n_cta);
+}
+
 // q: this thread's sequence (with a cut into pieces there are no more of them
-// than threads).  scratch: 40 bytes a thread.
+// than threads).  scratch: 16 bytes.
 template <int THREADS>
 __device__ __forceinline__ Cut cut_work(const TreeArgs& a, int rows, int tile_shift, int n_cta, long long* s_part,
                                         void* scratch, SeqInfo& q) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  unsigned* sums = reinterpret_cast<unsigned*>(scratch);
+  if (tid < CUT_MORE) sums[tid] = 0u;
   long long total = 0, chunk = 0;
   for (int base = 0; base < a.n_seq; base += THREADS) {
     long long mine = 0;
@@ -150,33 +199,20 @@ __device__ __forceinline__ Cut cut_work(const TreeArgs& a, int rows, int tile_sh
     block_excl<THREADS>(mine, s_part, &chunk);
     total += chunk;
   }
-  Cut c;
-  c.share = max(div_ll(total + n_cta - 1, n_cta), 1ll);
-  c.pieces = false;
-  if (a.n_seq > THREADS || c.share >= CUT_LONG) return c;
-  int2* seq = reinterpret_cast<int2*>(scratch);
-  unsigned long long* sums = reinterpret_cast<unsigned long long*>(seq + THREADS);
-  if (tid < a.n_seq) seq[tid] = make_int2(q.units, q.tiles);
-  __syncthreads();
-  const unsigned share = (unsigned)c.share + tid % CUT_MORE;
-  unsigned long long n = 0;
-  for (int s = tid / CUT_MORE; s < a.n_seq; s += THREADS / CUT_MORE)
-    n += (unsigned long long)seq[s].x * (((unsigned)seq[s].y + share - 1) / share);
+  const long long even = even_share(total, n_cta);
+  unsigned pieces[CUT_MORE] = {~0u, ~0u, ~0u, ~0u};
+  if (a.n_seq <= THREADS && even < CUT_LONG) {
 #pragma unroll
-  for (int off = CUT_MORE; off < 32; off *= 2) n += __shfl_xor_sync(0xffffffffu, n, off);
-  if (lane < CUT_MORE) sums[warp * CUT_MORE + lane] = n;
-  __syncthreads();
-#pragma unroll
-  for (int more = CUT_MORE - 1; more >= 0; more--) {
-    n = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; w++) n += sums[w * CUT_MORE + more];
-    if (n <= (unsigned long long)n_cta) {
-      c.pieces = true;
-      c.share = share - tid % CUT_MORE + more;
+    for (int more = 0; more < CUT_MORE; more++) {
+      const unsigned n =
+          __reduce_add_sync(0xffffffffu, tid < a.n_seq ? pieces_of(q, (unsigned)even + more) : 0u);
+      if (lane == 0 && n > 0u) atomicAdd(&sums[more], n);
     }
+    __syncthreads();
+#pragma unroll
+    for (int more = 0; more < CUT_MORE; more++) pieces[more] = sums[more];
   }
-  return c;
+  return cut_of(even, pieces, n_cta);
 }
 
 __device__ __forceinline__ int node_of(const TreeArgs& a, int m) {  // m / G
@@ -255,19 +291,48 @@ __device__ __forceinline__ void check_others(const TreeArgs& a, int rows, int ti
     check_sequence(a, (int)s, rows, tile_shift);
 }
 
-// Finds this CTA's first tile: the sequence that holds tile b * share (and
-// how far into its work) goes to *at; returns how many it
-// takes (0 or less: none).  (What pads a unit stands behind its last piece, which ends there.)
+// Finds this CTA's first tile, of the sequence that holds tile b * share:
+// which, and how far into its work (*at: shared memory on the way).  Returns
+// how many tiles the CTA takes (0 or less: none).  What pads a unit stands
+// behind its last piece, which ends there.
 struct Start {
   SeqInfo q;
   long long off;
   int s, left;  // with a cut into pieces: tiles of the unit from here on
 };
+__device__ __forceinline__ Start start_in(const Cut& c, const SeqInfo& q, int s, long long off) {
+  Start at;
+  at.q = q;
+  at.off = off;
+  at.s = s;
+  at.left = 0;
+  if (c.pieces) {  // (of less than CUT_LONG + CUT_MORE tiles a CTA: 32 bits)
+    const unsigned padded = (unsigned)c.padded(q), unit = (unsigned)off / padded, t0 = (unsigned)off % padded;
+    at.off = unit * q.tiles + t0;
+    at.left = q.tiles - (int)t0;
+  }
+  return at;
+}
 template <int THREADS>
 __device__ __forceinline__ long long find_range(const TreeArgs& a, int rows, int tile_shift, int n_cta,
-                                            long long* s_part, void* scratch, Start* at) {
+                                                long long* s_part, void* scratch, Start* at, Start& start) {
   const int tid = threadIdx.x;
   SeqInfo q;
+  if (a.n_seq <= 32) {
+    const Cut c = cut_work_few(a, rows, tile_shift, n_cta, q);
+    const long long w0 = c.share * blockIdx.x, mine = c.work(q), incl = warp_incl(mine);
+    const long long all = __shfl_sync(0xffffffffu, incl, 31);
+    const unsigned here = __ballot_sync(0xffffffffu, incl - mine <= w0 && w0 < incl);
+    if (here == 0u) return 0;
+    const int src = __ffs(here) - 1;
+    static_assert(sizeof(SeqInfo) % 4 == 0, "words");
+    int* words = reinterpret_cast<int*>(&q);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(SeqInfo) / 4); i++) words[i] = __shfl_sync(0xffffffffu, words[i], src);
+    start = start_in(c, q, src, w0 - __shfl_sync(0xffffffffu, incl - mine, src));
+    const long long n = min(all, w0 + c.share) - w0;
+    return c.pieces ? min(n, (long long)start.left) : n;
+  }
   const Cut c = cut_work<THREADS>(a, rows, tile_shift, n_cta, s_part, scratch, q);
   const long long w0 = c.share * blockIdx.x;
   long long first = 0, chunk = 0;
@@ -275,23 +340,14 @@ __device__ __forceinline__ long long find_range(const TreeArgs& a, int rows, int
     if (a.n_seq > THREADS && base + tid < a.n_seq) q = seq_info(a, base + tid, rows, tile_shift);
     const long long mine = base + tid < a.n_seq ? c.work(q) : 0;
     const long long excl = block_excl<THREADS>(mine, s_part, &chunk);
-    if (first + excl <= w0 && w0 < first + excl + mine) {
-      const long long off = w0 - first - excl;
-      at->q = q;
-      at->off = off;
-      at->s = base + tid;
-      if (c.pieces) {  // (of at most CUT_LONG tiles a CTA: 32 bits)
-        const unsigned padded = (unsigned)c.padded(q), unit = (unsigned)off / padded, t0 = (unsigned)off % padded;
-        at->off = unit * q.tiles + t0;
-        at->left = q.tiles - (int)t0;
-      }
-    }
+    if (first + excl <= w0 && w0 < first + excl + mine) *at = start_in(c, q, base + tid, w0 - first - excl);
     first += chunk;
   }
-  long long n = min(first, w0 + c.share) - w0;
+  const long long n = min(first, w0 + c.share) - w0;
   __syncthreads();
-  if (c.pieces && n > 0) n = min(n, (long long)at->left);  // one piece, without what pads it
-  return n;
+  if (n <= 0) return 0;
+  start = *at;
+  return c.pieces ? min(n, (long long)start.left) : n;  // one piece, without what pads it
 }
 
 // ---------------------------------------------------------------------------

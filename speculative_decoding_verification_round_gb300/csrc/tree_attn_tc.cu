@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
     plan_sequences<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part, smem);
     return;
   }
-  const long long my_tiles = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part, smem, &sh.at);
+  Start start;
+  const long long my_tiles = find_range<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part, smem, &sh.at, start);
   if (my_tiles <= 0 || (sm0 & 1023u) != 0u) {  // no tiles (a base off the swizzle's atoms never happens)
     if (tid == 0) a.part_err[blockIdx.x] = my_tiles > 0;
     if (warp < 8) check_others<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, 8);
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   }
   auto bar = [&](unsigned long long& b) { return smem_u32(&b); };
   if (tid == 0) {
+    sh.at = start;
     for (int i = 0; i < TC_RING; i++) {
       mbar_init(bar(sh.full[i]), PROD_THREADS);
       mbar_init(bar(sh.empty[i]), TWO ? 2 : 1);  // the streams that read it
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   auto item_k = [](int i) { return TWO ? 2 * i : (i == 0 ? 0 : 2 * i - 1); };
   auto item_v = [](int i, int n) { return TWO ? 2 * i + 1 : min(2 * i + 2, 2 * n - 1); };
 
+  // (out of shared memory: nothing is known about them, and kept in registers, here)
   int s = sh.at.s;
   long long off = sh.at.off;
   SeqInfo q = sh.at.q;
