@@ -7,8 +7,8 @@
 // One CTA per SM holds 128 or 256 rows against tiles of 128 positions, in
 // roles that only meet at mbarriers:
 //   warps 8-11   gather the positions' rows through the page table, two
-//                warps K's and two V's, into a ring of five 128-position
-//                buffers (16-byte cp.async, written in the MMA's
+//                warps K's and two V's, into rings of two and three
+//                128-position buffers (16-byte cp.async, written in the MMA's
 //                128-byte-swizzled layout; K as a K-major operand, V as an
 //                MN-major one, so that neither is transposed)
 //   warps 12, 13 issue S_j = Q_j K^T and O_j += P_j V, one stream each
@@ -41,7 +41,7 @@
 namespace {
 
 constexpr int TC_SHIFT = TREE_TC_SHIFT, TC_KEYS = 1 << TC_SHIFT;
-constexpr int TC_RING = 5;
+constexpr int K_RING = 2, V_RING = 3, TC_RING = K_RING + V_RING;
 constexpr int TC_THREADS = 512;
 constexpr int PROD_WARP = 8, MMA_WARP = 12, ALLOC_WARP = 14;
 constexpr int PROD_THREADS = 64;  // of K's loads, and of V's
@@ -250,15 +250,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   auto wait = [&](unsigned long long& b, uint32_t parity) {
     if (!mbar_wait(smem_u32(&b), parity & 1u, LIN_WAIT_TRIES, abort_flag)) *abort_flag = 1;
   };
-  // The ring's order: K runs one tile ahead of V, two where the streams alternate.
-  auto item_k = [](int i) { return TWO ? 2 * i : (i == 0 ? 0 : 2 * i - 1); };
-  auto item_v = [](int i, int n) { return TWO ? 2 * i + 1 : min(2 * i + 2, 2 * n - 1); };
+  // Buffers and turns of K and V of the CTA's tile x.  Each has a ring of its
+  // own: a barrier tells a phase from the next one only, and as the streams
+  // run freely against each other, a loader may not leave out a phase of a
+  // buffer.  V's are held longer than K's.
+  struct Item {
+    uint32_t slot, turn;
+  };
+  auto item_k = [](uint32_t x) { return Item{x % K_RING, x / K_RING}; };
+  auto item_v = [](uint32_t x) { return Item{K_RING + x % V_RING, x / V_RING}; };
 
   // (out of shared memory: nothing is known about them, and kept in registers, here)
   int s = sh.at.s;
   long long off = sh.at.off;
   SeqInfo q = sh.at.q;
-  uint32_t item0 = 0, seg = 0;  // ring items and pieces before this one
+  uint32_t tile0 = 0, seg = 0;  // tiles and pieces before this one
   // what a piece is
   int t0 = 0, n = 0, kvh = 0, row0 = 0, M = 0;
   auto next_piece = [&](long long left) {
@@ -317,17 +323,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       }
       return x;
     };
-    for (long long left = my_tiles; left > 0; left -= n, off += n, item0 += 2 * n, seg++) {
+    for (long long left = my_tiles; left > 0; left -= n, off += n, tile0 += n, seg++) {
       next_piece(left);
       // the rows of the next tile are looked up while this one waits for its buffer
       Rows next = lookup(t0);
       for (int i = 0; i < n; i++) {
         const int t = t0 + i;
-        const uint32_t item = item0 + (is_k ? item_k(i) : item_v(i, n));
-        const uint32_t slot = item % TC_RING, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
+        const Item item = is_k ? item_k(tile0 + i) : item_v(tile0 + i);
+        const uint32_t slot = item.slot, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
         const Rows x = next;
         if (i + 1 < n) next = lookup(t + 1);
-        wait(sh.empty[slot], (item / TC_RING) + 1);
+        wait(sh.empty[slot], item.turn + 1);
         if (t == q.tiles - 1) {
           const __half* src = fresh + (int64_t)s * a.nt * a.kv_stride + kvh * HD;
 #pragma unroll 4
@@ -388,13 +394,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       const uint64_t d_k = smem_desc_sw128(sm0 + Sh::RING_OFF), d_v = smem_desc_mn(sm0 + Sh::RING_OFF, Sh::SUB);
       const uint32_t tS = tmem + j * 128, tO = tmem + 256 + j * 128;
       uint32_t n_p = 0;  // the stream's tiles so far
-      auto wait_item = [&](uint32_t item) {
-        wait(sh.full[item % TC_RING], item / TC_RING);
+      auto wait_item = [&](const Item& item) {
+        wait(sh.full[item.slot], item.turn);
         __syncwarp();
         fence_proxy_async();  // the copies, to the tensor core's proxy
       };
-      auto scores = [&](uint32_t item) {
-        const uint64_t dk = d_k + item % TC_RING * (uint32_t)(Sh::TILE >> 4);
+      auto scores = [&](const Item& item) {
+        wait_item(item);
+        const uint64_t dk = d_k + item.slot * (uint32_t)(Sh::TILE >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < HD / 16; kk++) {
@@ -402,21 +409,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
             tc_mma(tS, d_q + o, dk + o, id_s, kk > 0);
           }
           tc_commit(bar(sh.s_full[j]));
-          tc_commit(bar(sh.empty[item % TC_RING]));
+          tc_commit(bar(sh.empty[item.slot]));
         }
         __syncwarp();
       };
-      for (long long left = my_tiles; left > 0; left -= n, off += n, item0 += 2 * n, seg++) {
+      for (long long left = my_tiles; left > 0; left -= n, off += n, tile0 += n, seg++) {
         next_piece(left);
         const int step = TWO ? 1 : 2;
         int i = TWO ? 0 : j;
+        wait(sh.q_full, seg);  // (without a tile, too: a phase each piece)
         if (i >= n) continue;
-        wait(sh.q_full, seg);
-        wait_item(item0 + item_k(i));
-        scores(item0 + item_k(i));
+        scores(item_k(tile0 + i));
         for (; i < n; i += step) {
-          const uint32_t vi = item0 + item_v(i, n);
-          const uint64_t dv = d_v + vi % TC_RING * (uint32_t)(Sh::TILE >> 4);
+          const Item vi = item_v(tile0 + i);
+          const uint64_t dv = d_v + vi.slot * (uint32_t)(Sh::TILE >> 4);
           wait_item(vi);
           wait(sh.p_ready[j], n_p++);
           __syncwarp();
@@ -425,14 +431,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
 #pragma unroll
             for (int kk = 0; kk < TC_KEYS / 16; kk++)
               tc_mma_ta(tO, tS + 8 * kk, dv + ((kk * 2048) >> 4), id_o, 1u);
-            tc_commit(bar(sh.empty[vi % TC_RING]));
+            tc_commit(bar(sh.empty[vi.slot]));
             if (i + step >= n) tc_commit(bar(sh.o_done[j]));  // the stream's last tile
           }
           __syncwarp();
-          if (i + step < n) {
-            wait_item(item0 + item_k(i + step));
-            scores(item0 + item_k(i + step));
-          }
+          if (i + step < n) scores(item_k(tile0 + i + step));
         }
       }
       if (elect_one()) tc_commit(bar(sh.drain[j]));
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
     const uint32_t tS = tmem + lanes + j * 128, tO = tmem + lanes + 256 + j * 128;
     const float scale = fabsf(a.scale_log2);
     uint32_t n_s = 0, n_o = 0;  // tiles and pieces of this stream so far
-    for (long long left = my_tiles; left > 0; left -= n, off += n, item0 += 2 * n, seg++) {
+    for (long long left = my_tiles; left > 0; left -= n, off += n, tile0 += n, seg++) {
       next_piece(left);
       const int nj = TWO ? n : (n - j + 1) / 2;
       // this thread's row of the unit; its chunks of the q tile
@@ -585,8 +588,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           sum += l[0].x + l[0].y;
           tm_wait_st();
           if (masked) {
-            const uint32_t item = item0 + item_v(i, n), slot = item % TC_RING;
-            wait(sh.full[slot], item / TC_RING);
+            const Item item = item_v(tile0 + i);
+            const uint32_t slot = item.slot;
+            wait(sh.full[slot], item.turn);
             __syncwarp();
             if ((sh.bad[slot][0] | sh.bad[slot][1]) != 0ull) {
               const bool tree = t == q.tiles - 1;
@@ -697,7 +701,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       } else {
         // the streams exchange halves: stream j finishes dimensions
         // [j HD / 2, (j + 1) HD / 2) of every row and hands the others over
-        // through the q tiles (every S is done): x[dimension][row]
+        // through the q tiles: x[dimension][row].  The other stream may be a
+        // tile behind, with an S to come
+        asm volatile("bar.sync 3, 256;" ::: "memory");
         float* x_out = reinterpret_cast<float*>(smem + j * Sh::TILE);
         const float* x_in = reinterpret_cast<const float*>(smem + (1 - j) * Sh::TILE);
         constexpr int XR = ROWS == 64 ? 64 : 128;

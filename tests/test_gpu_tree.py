@@ -157,6 +157,70 @@ def test_many_ragged_sequences(dev):
     c.check(got)
 
 
+@pytest.mark.parametrize("nq,nkv,hd,n,longest,nt", [(32, 8, 128, 2, 9001, 16), (16, 8, 64, 3, 7000, 40),
+                                                    (32, 8, 128, 500, 290, 16), (40, 8, 128, 300, 140, 16),
+                                                    (8, 2, 64, 700, 200, 64)])
+def test_repeated_calls_agree(dev, nq, nkv, hd, n, longest, nt):
+    """No result depends on how the streams of a CTA run against each other:
+    pieces of one tile and of many, sequences that begin in the middle of a
+    CTA, the same call forty times, bit by bit."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng([31, nq, n])
+    lens = g.integers(0, longest + 1, n)
+    lens[:2] = longest
+    c = Case(sv, dev, g, nq, nkv, hd, lens.tolist(), nt, 64, layers=1)
+    first = c.call()
+    c.check(first, range(0, n, max(1, n // 12)))
+    out, kv, slots, parents, counts = c.out, c.pool(), c.T(c.slots), c.T(c.parents), c.T(c.counts)
+    q, kn, vn, want = c.T(c.q), c.T(c.kn), c.T(c.vn), c.out.clone()
+    ws = torch.empty(sv.spec_tree_attn_workspace(kv, n, nt, nq), dtype=torch.uint8, device=dev)
+    for _ in range(40):
+        out.fill_(7.0)
+        sv.spec_tree_attn(kv, 0, n, slots, nt, nq, q, kn, vn, out, ws, c.status, parents=parents, n_nodes=counts)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("nt", [16, 32])
+def test_repeated_calls_over_a_long_context_agree(dev, nt):
+    """Two sequences of 131071 positions: the streams of a CTA get far apart
+    on the way, and the second sequence begins in the middle of one."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(nt)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=dev, dtype=torch.float16)  # noqa: E731
+    nq, nkv, hd, page, ctx, n = 32, 8, 128, 256, 131071, 2
+    pages = -(-ctx // page)
+    k, v = rnd(1, n * pages, nkv, page, hd), rnd(1, n * pages, nkv, page, hd)
+    i32 = dict(dtype=torch.int32, device=dev)
+    table = torch.arange(n * pages, **i32).view(n, pages)
+    lens, slots = torch.full((n,), ctx, **i32), torch.arange(n, **i32)
+    q, kn, vn = rnd(n, nt, nq, hd), rnd(n, nt, nkv, hd), rnd(n, nt, nkv, hd)
+    out, status = torch.empty((n, nt, nq, hd), dtype=torch.float16, device=dev), torch.full((n,), 9, **i32)
+    pool = sv.KVPages(k, v, table, lens)
+    ws = torch.empty(sv.spec_tree_attn_workspace(pool, n, nt, nq), dtype=torch.uint8, device=dev)
+    want = None
+    for _ in range(60):  # a chain, with no parents given
+        sv.spec_tree_attn(pool, 0, n, slots, nt, nq, q, kn, vn, out, ws, status)
+        want = out.clone() if want is None else want
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    assert status.tolist() == [0, 0]
+    g = nq // nkv
+    for b, h in ((0, 0), (0, 7), (1, 0), (1, 3)):
+        kk = torch.cat([k[0, b * pages:(b + 1) * pages, h].reshape(-1, hd)[:ctx], kn[b, :, h]]).double()
+        vv = torch.cat([v[0, b * pages:(b + 1) * pages, h].reshape(-1, hd)[:ctx], vn[b, :, h]]).double()
+        s = torch.einsum("ngd,kd->ngk", q[b, :, h * g:(h + 1) * g].double(), kk) * hd ** -0.5
+        s[:, :, ctx:].masked_fill_(torch.ones(nt, nt, device=dev).triu(1).bool()[:, None], -float("inf"))
+        w = torch.softmax(s, -1)
+        ref, mag = torch.einsum("ngk,kd->ngd", w, vv), torch.einsum("ngk,kd->ngd", w, vv.abs())
+        # (the bound of Case.check; |q . k| sums are below 2 hd here)
+        rel = np.expm1(2 * (hd + 4) * 2.0 ** -23 * hd ** -0.5 * 2 * hd) + 2.0 ** -20 + (
+            (ctx + nt) / 8 + 64) * 2.0 ** -23 + 2.0 ** -11 + (ctx + nt) * 2.0 ** -31
+        err = (out[b, :, h * g:(h + 1) * g].double() - ref).abs()
+        assert (err <= 2.0 ** -11 * ref.abs() + 2.0 ** -25 + 1.01 * rel * mag).all()
+
+
 def test_large_scores_and_a_given_scale(dev):
     """Scores far apart (weights underflow, the running maximum moves) and a
     scale of the caller's, negative too."""
