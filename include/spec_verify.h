@@ -580,7 +580,9 @@ typedef struct {
  *          are NaN (for its first n_nodes rows, all nt if that is bad too)
  *   workspace  spec_tree_attn_workspace bytes, 16-byte aligned; its contents
  *          do not matter before and after the call
- *   status int32 [n_seq]: SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_TREE
+ *   status int32 [n_seq]: SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_TREE,
+ *          SPEC_ST_TIMEOUT
+ * out and workspace overlap none of the inputs, nor each other.
  * The scores' statistics and sums are fp32.  The same call gives the same
  * bits; which bits may depend on the other sequences of the call (the work
  * is cut evenly over the SMs), unlike spec_verify_attn, whose rows do not
@@ -645,14 +647,16 @@ int spec_accept_tree(const int32_t* argmax, const int32_t* tokens, const int32_t
  *           0: few or short rows); its contents do not matter before and
  *           after the call
  * A row with a NaN or +infinity, without any finite logit, whose largest
- * l / T overflows, or with a setting out of range gets token -1, n_kept 0 and a filtered row of NaN (which
- * spec_accept_stochastic refuses). */
+ * l / T overflows, or with a setting out of range gets token -1, n_kept 0 and
+ * a filtered row of NaN (which spec_accept_stochastic refuses). */
 int spec_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u,
                 const float* temperature, const int32_t* top_k, const float* top_p,
                 const float* min_p, int32_t* token, int32_t* n_kept, float* filtered,
                 int64_t ld_filtered, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace for spec_sample of R rows of V logits. */
+/* Bytes of workspace for spec_sample of R rows of V logits (0: none needed;
+ * many long rows are sampled in passes over all of them, few in one kernel:
+ * the same results). */
 int spec_sample_workspace(int R, int V, size_t* bytes);
 
 #ifdef __cplusplus

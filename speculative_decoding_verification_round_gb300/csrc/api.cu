@@ -1199,6 +1199,15 @@ extern "C" int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* 
     return fail(SPEC_E_SHAPE, "row strides are too large");
   if (workspace_bytes < need)
     return fail(SPEC_E_SHAPE, "workspace of " + std::to_string(need) + " bytes required");
+  // a unit's rows may be written while another CTA reads its inputs
+  const size_t nodes = (size_t)t->n_seq * t->nt, qd = (size_t)t->n_q_heads * kv->head_dim,
+               kd = (size_t)kv->n_kv_heads * kv->head_dim;
+  const size_t out_b = 2 * nodes * qd, q_b = 2 * ((nodes - 1) * (q_stride != 0 ? (size_t)q_stride : qd) + qd),
+               new_b = 2 * ((nodes - 1) * (kv_stride != 0 ? (size_t)kv_stride : kd) + kd);
+  if (overlaps(out, out_b, q, q_b) || overlaps(out, out_b, k_new, new_b) || overlaps(out, out_b, v_new, new_b) ||
+      overlaps(out, out_b, workspace, need) || overlaps(workspace, need, q, q_b) ||
+      overlaps(workspace, need, k_new, new_b) || overlaps(workspace, need, v_new, new_b))
+    return fail(SPEC_E_INVALID, "out and workspace must not overlap q, k_new, v_new or each other");
   init_attrs_once();
   return launch_tree(kv, layer, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status,
                      as_stream(stream));

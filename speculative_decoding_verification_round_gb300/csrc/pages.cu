@@ -8,6 +8,14 @@
 // arrays alone.  Every entry of a call is checked by every CTA that works on
 // it from arrays that the kernel does not write (or writes only for other
 // entries), so an entry is done whole or not at all.
+//
+// Bound by the bytes moved, or by the launch: 96 pages of 64 positions copied
+// in 40 layers (8 heads of 128; 2.01 GB read and written) 296 us, the copy
+// bandwidth; 12 prompts of 550 positions freed, forked into four branches each
+// and extended by 16 positions, the filled part of 36 last pages copied (0.37
+// GB, 55 us of the copy bandwidth) 70 us in four launches; accepted paths of
+// 12 x 16 nodes committed in 40 layers (31 MB, 4.6 us) 8.4 us; acceptance
+// along one tree 1.7 us, 512 trees of 63 nodes 3.0 us.
 #include <climits>
 
 #include "common.cuh"

@@ -25,6 +25,15 @@
 // whole.  Each kernel is a programmatic dependent of the one in front of it,
 // and every other stream runs from the last row to the first, to find in L2
 // what the one before read last.
+//
+// Measured, 192 rows of 248320 logits (191 MB, 28 us at the copy bandwidth):
+// without filters 84 us, with a top-k 78, with all filters 84, with a top-p
+// alone 171, a quarter of the rows each of four settings 129 (in clusters
+// 380); 44 to 80 more where filtered logits are written (another 191 MB).
+// maxima 28 us: the memory.  pass 51 (no filter: ~17 instructions a weight),
+// 32 (top-k: the blocks that hold a token above the bound), 63 (top-p: two
+// 32-bit additions in shared memory a logit).  step 58, draw 14 (top-p).
+// bound 5 to 7, cut 6 to 15: a CTA a row, latency.
 #include <algorithm>
 
 #include "sample.cuh"

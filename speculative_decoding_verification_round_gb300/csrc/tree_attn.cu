@@ -67,9 +67,18 @@ __device__ __forceinline__ uint32_t tile_off(int r, int u) {
 }
 
 // ---------------------------------------------------------------------------
-// the main kernel.  Four warps = RTW row blocks x KG key groups; a warp holds
-// MT m16 tiles of rows against 64 / KG keys of every tile, with its own
-// running (max, sum, O), joined over the key groups at the end of a piece.
+// the main kernel.  Each of four warps has all rows (MT m16 tiles) against 16
+// keys of every tile, with its own running (max, sum, O), joined at the end of
+// a piece: few rows have to share the keys among the warps.
+//
+// 2 x rows flops per byte of K (twice that for P V, whose weights are a pair)
+// keep mma.sync within the memory's time up to 32 rows.  Long contexts are
+// bound by the memory: 64 sequences of 32768 positions, one node each, 14
+// query heads over 2 of 64 dimensions (1.0 GB), take 170 us, 5.9 TB/s, 87% of
+// the copy bandwidth.  Short ones are bound by their chain of latencies: 8
+// nodes over 4096 positions, 32 heads over 8 of 128 (17 MB) 15 us, of which 2
+// the cut, 2.5 the tree, the page lookups and the first loads, 4 two tiles, 2
+// the piece's end and 3 the joining kernel.
 // ---------------------------------------------------------------------------
 // CTAs of an SM: two of 128 dimensions (three with two stages each: no gain,
 // 64 sequences of one node over 512 positions 74 -> 78 us), four of 64
@@ -77,11 +86,11 @@ __device__ __forceinline__ uint32_t tile_off(int r, int u) {
 // with four; with a window of 4096 17.2 us with two, 15.6 with four).
 constexpr int resident(int hd, int rows) { return hd == 64 && rows == 16 ? 4 : 2; }
 
-template <int HD, int MT, int RTW>
+template <int HD, int MT>
 struct Shape {
-  static constexpr int ROWS = 16 * MT * RTW;
+  static constexpr int ROWS = 16 * MT;
   static constexpr int RESIDENT = resident(HD, ROWS), STAGES = 3;
-  static constexpr int KG = 4 / RTW;
+  static constexpr int KG = TT_THREADS / 32;
   static constexpr int KEYS = TT_KEYS / KG;
   static constexpr int TILE = TT_KEYS * HD * 2;  // bytes of a K (or V) tile
   static constexpr int XROW = HD + 8;            // floats of an exchange row (padded)
@@ -90,9 +99,9 @@ struct Shape {
   static_assert((size_t)KG * ROWS * (XROW * 4 + 8) <= Q_OFF, "the exchange fits over the tiles");
 };
 
-template <int HD, int MT, int RTW>
-__global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree_attn_kernel(const TreeArgs a) {
-  using Sh = Shape<HD, MT, RTW>;
+template <int HD, int MT>
+__global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT>::RESIDENT) tree_attn_kernel(const TreeArgs a) {
+  using Sh = Shape<HD, MT>;
   constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, KG = Sh::KG, KEYS = Sh::KEYS, NB = KEYS / 8, UNITS = HD / 8;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ TreeSmem s_tree;
@@ -101,7 +110,7 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree
   grid_dep_launch();  // the joining kernel may get ready
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const int kg = warp % KG, rw = warp / KG;  // this warp's key group and row block
+  const int kg = warp;  // this warp's key group
 
   const int n_cta = gridDim.x - 1;
   if ((int)blockIdx.x == n_cta) {
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree
     for (int i = 0; i < MT; i++) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const int m = row0 + (rw * MT + i) * 16 + h * 8 + g;
+        const int m = row0 + i * 16 + h * 8 + g;
         const int node = m < M ? node_of(a, m) : 0;
         pos[i][h] = q.len + s_tree.depth[node];
         anc[i][h] = m < M ? s_tree.anc[node] : 0ull;
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree
         for (int i = 0; i < MT; i++)
 #pragma unroll
           for (int j = 0; j < 2; j++)
-            ldsm_x4(qs0 + tile_off<HD>((rw * MT + i) * 16 + q_row, 2 * (kk + j) + (lane >> 4)), qa[i][j]);
+            ldsm_x4(qs0 + tile_off<HD>(i * 16 + q_row, 2 * (kk + j) + (lane >> 4)), qa[i][j]);
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
           uint32_t b[4];
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         const int r = i * 16 + h * 8 + g;
         if (t4 == 0) s_ml[warp][r] = make_float2(mx[i][h], l);
-        float* dst = x + ((size_t)kg * ROWS + rw * MT * 16 + r) * Sh::XROW + 2 * t4;
+        float* dst = x + ((size_t)kg * ROWS + r) * Sh::XROW + 2 * t4;
 #pragma unroll
         for (int d = 0; d < HD / 8; d++)
           *reinterpret_cast<float2*>(dst + 8 * d) = make_float2(o[i][d][2 * h], o[i][d][2 * h + 1]);
@@ -413,15 +422,14 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree
       // rows of the output are contiguous, rows of a piece are neighbours
       const int r = whole ? e / UNITS : e % ROWS, u = whole ? e % UNITS : e / ROWS, m = row0 + r;
       if (m >= M) continue;
-      const int rb = r / (16 * MT), rl = r % (16 * MT);
       float m2 = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < KG; k++) m2 = fmaxf(m2, s_ml[rb * KG + k][rl].x);
+      for (int k = 0; k < KG; k++) m2 = fmaxf(m2, s_ml[k][r].x);
       const float ref = m2 == -INFINITY ? 0.0f : m2;
       float acc[8] = {}, l = 0.0f;
 #pragma unroll
       for (int k = 0; k < KG; k++) {
-        const float2 ml = s_ml[rb * KG + k][rl];
+        const float2 ml = s_ml[k][r];
         const float wk = exp2f(ml.x - ref);
         l = fmaf(ml.y, wk, l);
         const float4* src = reinterpret_cast<const float4*>(x + ((size_t)k * ROWS + r) * Sh::XROW + u * 8);
@@ -460,9 +468,12 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT, RTW>::RESIDENT) tree
 // pieces of the rows' unit in the order of the positions, or writes NaN for a
 // sequence in error.  SPLIT: the CTA has 8 dimensions and its warps an eighth
 // of the pieces each (the kernel for few rows cuts a long context into dozens
-// of pieces: 8 nodes over 4096 positions, 33 pieces, 22 -> 18 us); otherwise
-// 32 dimensions and every warp all pieces (the tcgen05 kernel's few: 12 x 16
-// nodes 37 -> 29 us).
+// of pieces: 8 nodes over 4096 positions, 33 pieces, 22 us without, 18 with
+// four warps, 16.3 -> 15.1 with eight); otherwise every warp has all pieces of
+// its dimensions (12 x 16 nodes 37 -> 29 us), the CTA 32 of them a turn, so
+// that many units, most of them whole, take no more CTAs than fit at once
+// (64 sequences of one node over 512 positions: 44 of 74 us were spent here
+// with a CTA per 8 dimensions, now 38 in all).
 // ---------------------------------------------------------------------------
 constexpr int TJ_ROWS = 32;
 constexpr int join_warps(bool split) { return split ? 8 : 4; }
@@ -582,17 +593,17 @@ int rows_of(int M) {
 }
 bool on_tc(int rows) { return rows >= 64; }
 
-template <int HD, int MT, int RTW>
+template <int HD, int MT>
 cudaError_t launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  tree_attn_kernel<HD, MT, RTW><<<n_cta + 1, TT_THREADS, Shape<HD, MT, RTW>::SMEM, st>>>(a);
+  tree_attn_kernel<HD, MT><<<n_cta + 1, TT_THREADS, Shape<HD, MT>::SMEM, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int HD>
 int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
   cudaError_t e = on_tc(a.rows)  ? tree_tc_launch(a, HD, n_cta, st)
-                  : a.rows == 16 ? launch_shape<HD, 1, 1>(a, n_cta, st)
-                                 : launch_shape<HD, 2, 1>(a, n_cta, st);
+                  : a.rows == 16 ? launch_shape<HD, 1>(a, n_cta, st)
+                                 : launch_shape<HD, 2>(a, n_cta, st);
   if (e == cudaSuccess) {
     const int blocks = (a.nt * a.G + TJ_ROWS - 1) / TJ_ROWS;
     cudaLaunchAttribute at[1];
@@ -613,10 +624,10 @@ int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
   return SPEC_OK;
 }
 
-template <int HD, int MT, int RTW>
+template <int HD, int MT>
 void init_shape() {
-  cudaFuncSetAttribute(tree_attn_kernel<HD, MT, RTW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)Shape<HD, MT, RTW>::SMEM);
+  cudaFuncSetAttribute(tree_attn_kernel<HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)Shape<HD, MT>::SMEM);
 }
 
 int device_sms() {
@@ -649,10 +660,10 @@ int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
 }  // namespace
 
 void tree_init_attrs() {
-  init_shape<64, 1, 1>();
-  init_shape<64, 2, 1>();
-  init_shape<128, 1, 1>();
-  init_shape<128, 2, 1>();
+  init_shape<64, 1>();
+  init_shape<64, 2>();
+  init_shape<128, 1>();
+  init_shape<128, 2>();
   tree_tc_init_attrs();
 }
 

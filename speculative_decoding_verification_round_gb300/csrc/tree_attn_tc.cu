@@ -32,6 +32,14 @@
 // rows does, which waits for the cache anyway) would make the tensor core the
 // bound.  2^6 is multiplied into weights and sum alike, so that those of 2^-20
 // are still normal numbers.
+//
+// Measured: 2 x 16 nodes over 131071 positions (32 heads over 8 of 128, 1.07
+// GB) 180 us, 5.9 TB/s, 88% of the copy bandwidth: the memory.  4 x 63 nodes
+// over 8191 positions 53 us, of which about 8 are the start (cut, tensor
+// memory, page lookups, first tiles), 8 the end and the joining kernel, and
+// 2.1 a tile of 128 positions x 256 rows: a stream's own chain of S, softmax
+// and P V (the products of both streams alone take 1.3).  12 x 16 nodes over
+// 512 positions, five tiles a unit and a unit a CTA, 24 us: start and end.
 #include <math.h>
 
 #include "common.cuh"

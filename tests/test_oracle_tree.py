@@ -221,6 +221,10 @@ def test_tree_attention_refuses_bad_arguments(sv):
                dict(q=A + 8), dict(out=A + 2), dict(qs=4 * 128 + 4), dict(qs=128), dict(kvs=8), dict(qs=-512),
                dict(nbytes=16), dict(ws=A + 8)):
         assert call(**kw) == sv.SPEC_E_SHAPE, kw
+    # out over q (A is k_new and v_new, too), workspace over them, workspace over out
+    far, farther = A + (1 << 30), A + (1 << 34)
+    for kw in (dict(ws=farther), dict(ws=farther, out=A + 2048), dict(out=far, q=farther), dict(ws=far, out=far, nbytes=1 << 24)):
+        assert call(**kw) == sv.SPEC_E_INVALID and "overlap" in sv.last_error(), kw
     odd = pages(sv, head_dim=96, layer_stride=8 * 2 * 64 * 96)
     assert call(kv=odd) == sv.SPEC_E_UNSUPPORTED
     assert L.spec_accept_tree(A, A, A, None, 1, 65, A, A, A, None) == sv.SPEC_E_SHAPE
