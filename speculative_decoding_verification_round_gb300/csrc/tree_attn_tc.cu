@@ -421,13 +421,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         }
         __syncwarp();
       };
+      // The streams take turns, each with its P V and its next S in one go: were
+      // both streams' products mixed, both would wait for theirs, and then
+      // both be in their softmax, with the tensor core idle.
+      auto hand_over = [](int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); };
+      auto take_over = [](int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); };
+      constexpr int TURN_0_1 = 4, TURN_1_0 = 5, START_0_1 = 6;
       for (long long left = my_tiles; left > 0; left -= n, off += n, tile0 += n, seg++) {
         next_piece(left);
         const int step = TWO ? 1 : 2;
         int i = TWO ? 0 : j;
         wait(sh.q_full, seg);  // (without a tile, too: a phase each piece)
         if (i >= n) continue;
+        if (j == 1) take_over(START_0_1);
         scores(item_k(tile0 + i));
+        if (j == 0 && (TWO || n > 1)) hand_over(START_0_1);
         for (; i < n; i += step) {
           const Item vi = item_v(tile0 + i);
           const uint64_t dv = d_v + vi.slot * (uint32_t)(Sh::TILE >> 4);
@@ -435,6 +443,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           wait(sh.p_ready[j], n_p++);
           __syncwarp();
           tc_fence_after();
+          if (j == 1 || i > 0) take_over(j == 1 ? TURN_0_1 : TURN_1_0);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < TC_KEYS / 16; kk++)
@@ -444,6 +453,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           }
           __syncwarp();
           if (i + step < n) scores(item_k(tile0 + i + step));
+          if (TWO ? j == 0 || i + 1 < n : i + 1 < n) hand_over(j == 0 ? TURN_0_1 : TURN_1_0);
         }
       }
       if (elect_one()) tc_commit(bar(sh.drain[j]));
