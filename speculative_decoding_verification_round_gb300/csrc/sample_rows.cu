@@ -13,12 +13,11 @@
 //   pass     stream: top-k rows collect the tokens at the bound (only blocks
 //            of 128 that reach it are read); top-p rows add their masses up
 //            over steps of z; the others over 1024 ids
-//   cut      row: top-k rows find their cut among the collected tokens and
-//            draw from them; rows without filters draw; top-p rows find the
-//            step that holds their cut
+//   cut      row, top-p rows: the step that holds the cut
 //   step     stream, top-p rows: the masses above that step over 1024 ids,
 //            its tokens collected
-//   draw     row, top-p rows: the cut, and the draw
+//   draw     row: the cut among the collected tokens, and the draw from these
+//            (top-k), from the masses over ids (no filter) or both (top-p)
 //   filter   stream, where filtered logits are wanted: blocks below the cut
 //            are written without being read
 // A row that collects too many tokens goes to the clusters of sample.cu as a
@@ -557,93 +556,91 @@ __device__ void draw_from_ranges(const SampleArgs& a, RowSmem& sh, const Row& ro
   }
 }
 
+// A top-p row's step that holds its cut.
 __global__ void __launch_bounds__(SM_THREADS)
 sr_cut_kernel(const SampleArgs a, const Spaces sp) {
-  extern __shared__ __align__(16) unsigned char dyn[];
-  RowSmem& sh = *reinterpret_cast<RowSmem*>(dyn);
+  __shared__ ListSmem sh;
+  __shared__ int s_step;
   grid_dep_launch();
-  const int r = blockIdx.x, tid = threadIdx.x;
-  const RowSpace s = sp.row(r);
+  const int tid = threadIdx.x;
+  const RowSpace s = sp.row(blockIdx.x);
   grid_dep_wait();
   RowState* st = s.state;
-  const int kind = st->kind;
+  if (st->kind != ROW_TOP_P) return;
+  const Row row = st->row;
+  constexpr int PER = SM_BINS / SM_THREADS;
+  u64 w[PER], mine = 0, S;
+#pragma unroll
+  for (int e = 0; e < PER; e++) {
+    w[e] = __ldcg(s.mass + tid * PER + e);
+    mine += w[e];
+  }
+  u64 run = block_prefix(mine, sh, &S) - mine;
+  const u64 need = mass_needed(st->P, S);
+  if (tid == 0) s_step = SM_BINS - 1;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < PER; e++) {
+    if (run < need && need <= run + w[e]) {
+      s_step = tid * PER + e;
+      st->left = need - run;
+    }
+    run += w[e];
+  }
+  __syncthreads();
+  if (tid < 64) {
+    const float first = first_of_step(row, st->top, s_step - (tid >> 5));
+    if (tid == 0) st->bound = first;
+    if (tid == 32) st->summed = s_step == 0 ? INFINITY : first;
+  }
+}
+
+// The cut of a top-k row among its collected tokens, and the draw from them.
+__device__ void cut_and_draw(const SampleArgs& a, const Spaces& sp, const RowSpace& s, RowSmem& sh, int r) {
+  const int tid = threadIdx.x;
+  RowState* st = s.state;
   Row row = st->row;
-  if (kind == ROW_PLAIN) {
-    for (int i = tid; i < sp.ranges; i += SM_THREADS) {
-      sh.range_w[i] = __ldcg(s.range_w + i);
-      sh.range_c[i] = __ldcg(s.range_c + i);
-    }
-    __syncthreads();
-    draw_from_ranges(a, sh, row, sp.ranges, r);
-  } else if (kind == ROW_TOP_P) {
-    constexpr int PER = SM_BINS / SM_THREADS;
-    u64 w[PER], mine = 0, S;
-#pragma unroll
-    for (int e = 0; e < PER; e++) {
-      w[e] = __ldcg(s.mass + tid * PER + e);
-      mine += w[e];
-    }
-    u64 run = block_prefix(mine, sh, &S) - mine;
-    const u64 need = mass_needed(st->P, S);
-    if (tid == 0) sh.range = SM_BINS - 1;
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < PER; e++) {
-      if (run < need && need <= run + w[e]) {
-        sh.range = tid * PER + e;
-        st->left = need - run;
-      }
-      run += w[e];
-    }
-    __syncthreads();
-    if (tid < 64) {
-      const float first = first_of_step(row, st->top, sh.range - (tid >> 5));
-      if (tid == 0) st->bound = first;
-      if (tid == 32) st->summed = sh.range == 0 ? INFINITY : first;
-    }
-  } else if (kind == ROW_TOP_K) {
-    const uint32_t m = st->listed;
-    if (m > SR_LIST) {
-      make_hard(sp, st, r);
-      return;
-    }
-    for (int i = tid; i < (int)m; i += SM_THREADS) {
-      sh.keys[i] = __ldcg(s.key + i);
-      sh.ws[i] = __ldcg(s.w + i);
-    }
-    __syncthreads();
-    // the keys agree above the first bit in which the bound and the largest differ
-    const uint32_t hi = max_key(st->top), lo = max_key(st->bound);
-    const int open = 32 - __clz(hi ^ lo);
-    const u64 prefix = open < 32 ? hi >> open : 0u;
-    const bool by_p = st->P < (1ull << 32);
-    Cut c = cut_list(sh, sh.keys, sh.ws, (int)m, true, by_p, (u64)st->k, 20 + open, prefix);
-    if (by_p) c = cut_list(sh, sh.keys, sh.ws, (int)m, false, true, mass_needed(st->P, c.mass), 20 + open, prefix);
-    row.set_cut(c.key);
-    // the draw: in the order of ids, among the tokens that stay
-    u64 mine = 0, S, counted;
-    uint32_t cnt = 0;
-    for (int i = tid; i < (int)m; i += SM_THREADS) {
-      const bool in = sh.keys[i] >= c.key && sh.ws[i] >= row.min_w;
-      if (!in) sh.ws[i] = 0u;
-      sh.keys[i] &= 0xFFFFFu;  // the lower ids first
-      mine += widen(sh.ws[i]);
-      cnt += in;
-    }
-    block_prefix(cnt, sh, &counted);
-    block_prefix(mine, sh, &S);
-    const u64 t = (u64)scaled_threshold(a.u[r], S) + 1;
-    const Cut d = cut_list(sh, sh.keys, sh.ws, (int)m, false, true, t, 20, 0);
-    if (tid == 0) {
-      a.token[r] = 0xFFFFF - (int)d.key;
-      if (a.n_kept != nullptr) a.n_kept[r] = (int)counted;
-      st->row = row;
-    }
+  const uint32_t m = st->listed;
+  if (m > SR_LIST) {
+    make_hard(sp, st, r);
+    return;
+  }
+  for (int i = tid; i < (int)m; i += SM_THREADS) {
+    sh.keys[i] = __ldcg(s.key + i);
+    sh.ws[i] = __ldcg(s.w + i);
+  }
+  __syncthreads();
+  // the keys agree above the first bit in which the bound and the largest differ
+  const uint32_t hi = max_key(st->top), lo = max_key(st->bound);
+  const int open = 32 - __clz(hi ^ lo);
+  const u64 prefix = open < 32 ? hi >> open : 0u;
+  const bool by_p = st->P < (1ull << 32);
+  Cut c = cut_list(sh, sh.keys, sh.ws, (int)m, true, by_p, (u64)st->k, 20 + open, prefix);
+  if (by_p) c = cut_list(sh, sh.keys, sh.ws, (int)m, false, true, mass_needed(st->P, c.mass), 20 + open, prefix);
+  row.set_cut(c.key);
+  // the draw: in the order of ids, among the tokens that stay
+  u64 mine = 0, S, counted;
+  uint32_t cnt = 0;
+  for (int i = tid; i < (int)m; i += SM_THREADS) {
+    const bool in = sh.keys[i] >= c.key && sh.ws[i] >= row.min_w;
+    if (!in) sh.ws[i] = 0u;
+    sh.keys[i] &= 0xFFFFFu;  // the lower ids first
+    mine += widen(sh.ws[i]);
+    cnt += in;
+  }
+  block_prefix(cnt, sh, &counted);
+  block_prefix(mine, sh, &S);
+  const u64 t = (u64)scaled_threshold(a.u[r], S) + 1;
+  const Cut d = cut_list(sh, sh.keys, sh.ws, (int)m, false, true, t, 20, 0);
+  if (tid == 0) {
+    a.token[r] = 0xFFFFF - (int)d.key;
+    if (a.n_kept != nullptr) a.n_kept[r] = (int)counted;
+    st->row = row;
   }
 }
 
 // ---------------------------------------------------------------------------
-// step and draw of the top-p rows
+// the step of the top-p rows, and the draw
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(SR_THREADS, 4)
 sr_step_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
@@ -711,15 +708,22 @@ sr_draw_kernel(const SampleArgs a, const Spaces sp) {
   const RowSpace s = sp.row(r);
   grid_dep_wait();
   RowState* st = s.state;
-  if (st->kind != ROW_TOP_P) return;
+  const int kind = st->kind;
+  if (kind == ROW_TOP_K) cut_and_draw(a, sp, s, sh, r);
+  if (kind != ROW_PLAIN && kind != ROW_TOP_P) return;
+  for (int i = tid; i < sp.ranges; i += SM_THREADS) {
+    sh.range_w[i] = __ldcg(s.range_w + i);
+    sh.range_c[i] = __ldcg(s.range_c + i);
+  }
+  if (kind == ROW_PLAIN) {
+    __syncthreads();
+    draw_from_ranges(a, sh, st->row, sp.ranges, r);
+    return;
+  }
   const uint32_t m = st->listed;
   if (m > SR_LIST) {
     make_hard(sp, st, r);
     return;
-  }
-  for (int i = tid; i < sp.ranges; i += SM_THREADS) {
-    sh.range_w[i] = __ldcg(s.range_w + i);
-    sh.range_c[i] = __ldcg(s.range_c + i);
   }
   for (int i = tid; i < (int)m; i += SM_THREADS) {
     sh.keys[i] = __ldcg(s.key + i);
@@ -810,7 +814,6 @@ void sample_rows_init_attrs() {
   int dev = 0, optin = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-  cudaFuncSetAttribute(sr_cut_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
   cudaFuncSetAttribute(sr_draw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
 }
 
@@ -829,11 +832,11 @@ int sample_rows_launch(SampleArgs a, void* workspace, cudaStream_t st) {
   if (e == cudaSuccess)
     e = launch(sr_bound_kernel, a.R, SM_THREADS, 0, st, true, a, sp);
   if (e == cudaSuccess) e = launch(sr_pass_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
-  if (e == cudaSuccess) e = launch(sr_cut_kernel, a.R, SM_THREADS, sizeof(RowSmem), st, true, a, sp);
   if (e == cudaSuccess && a.top_p != nullptr) {
-    e = launch(sr_step_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
-    if (e == cudaSuccess) e = launch(sr_draw_kernel, a.R, SM_THREADS, sizeof(RowSmem), st, true, a, sp);
+    e = launch(sr_cut_kernel, a.R, SM_THREADS, 0, st, true, a, sp);
+    if (e == cudaSuccess) e = launch(sr_step_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
   }
+  if (e == cudaSuccess) e = launch(sr_draw_kernel, a.R, SM_THREADS, sizeof(RowSmem), st, true, a, sp);
   if (e == cudaSuccess && a.filtered != nullptr)
     e = launch(sr_filter_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("sample: ") + cudaGetErrorString(e));
