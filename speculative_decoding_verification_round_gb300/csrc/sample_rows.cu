@@ -26,13 +26,13 @@
 // what the one before read last.
 //
 // Measured, 192 rows of 248320 logits (191 MB, 28 us at the copy bandwidth):
-// without filters 84 us, with a top-k 78, with all filters 84, with a top-p
-// alone 171, a quarter of the rows each of four settings 129 (in clusters
-// 380); 44 to 80 more where filtered logits are written (another 191 MB).
-// maxima 28 us: the memory.  pass 51 (no filter: ~17 instructions a weight),
-// 32 (top-k: the blocks that hold a token above the bound), 63 (top-p: two
-// 32-bit additions in shared memory a logit).  step 58, draw 14 (top-p).
-// bound 5 to 7, cut 6 to 15: a CTA a row, latency.
+// without filters 90 us, with a top-k 79, with all filters 82, with a top-p
+// alone 174, rows of mixed settings 117 (in clusters 380); 48 to 77 more where
+// filtered logits are written (another 191 MB).  maxima 30 us: the memory.
+// pass 51 (no filter: 17 instructions a weight and the sums), 30 (top-k: the
+// blocks that reach the bound), 63 (top-p: two 32-bit additions in shared
+// memory a logit).  step 61 (top-p).  filter 38 to 64.  bound 5 to 9, cut 5,
+// draw 6 to 14: a CTA a row, latency.
 #include <algorithm>
 
 #include "sample.cuh"
@@ -125,8 +125,9 @@ Spaces spaces(void* workspace, int R, int V) {
 // 4 lane .. of a block (16-byte loads) where the rows are aligned and the block
 // is whole, else lane + 32 e.
 constexpr int SR_BLOCKS = SR_RANGE / SR_BLOCK;  // of a warp
+template <int N>
 struct Logits {
-  float4 l[SR_BLOCKS];
+  float4 l[N];
   int v0, V, lane;
   bool aligned;
   __device__ __forceinline__ Logits(const void* row, int v0_, int V_)
@@ -137,13 +138,13 @@ struct Logits {
   }
   // the blocks of `which` (a bit each)
   __device__ __forceinline__ void load(const float* row, uint32_t which) {
-    if (which == (1u << SR_BLOCKS) - 1u && whole(SR_BLOCKS - 1)) {
+    if (which == (1u << N) - 1u && whole(N - 1)) {
 #pragma unroll
-      for (int g = 0; g < SR_BLOCKS; g++) l[g] = reinterpret_cast<const float4*>(row + v0 + g * SR_BLOCK)[lane];
+      for (int g = 0; g < N; g++) l[g] = reinterpret_cast<const float4*>(row + v0 + g * SR_BLOCK)[lane];
       return;
     }
 #pragma unroll
-    for (int g = 0; g < SR_BLOCKS; g++) {
+    for (int g = 0; g < N; g++) {
       l[g] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       if (which >> g & 1u) {
         if (whole(g)) {
@@ -166,6 +167,26 @@ __device__ __forceinline__ uint32_t blocks_from(const Spaces& sp, const RowSpace
   const int lane = threadIdx.x & 31, at = (v0 + (lane >> 3) * SR_SEG) / SR_BLOCK + (lane & 7);
   const uint32_t key = at < sp.blocks ? __ldcg(s.block + at) : 0u;
   return __ballot_sync(0xffffffffu, key >= max_key(least));
+}
+
+// The warp's turns by halves: each(half, its blocks of `blocks`), and after each
+// turn done(its first id).  Half the registers, so that five or six CTAs are
+// resident: mixed rows with filtered logits 191 us with whole turns and four,
+// 177 by halves; 215 with a half's loads in front of the other's work.
+constexpr int SR_HALF = SR_BLOCKS / 2;
+typedef Logits<SR_HALF> Half;
+template <class Each, class Done>
+__device__ __forceinline__ void by_halves(const float* row, Half& a, int turns, uint32_t blocks, Each&& each,
+                                          Done&& done) {
+  constexpr uint32_t ALL = (1u << SR_HALF) - 1u;
+  for (int turn = 0; turn < turns; turn++, a.v0 += SR_SEG - SR_RANGE) {
+#pragma unroll 1
+    for (int half = 0; half < 2; half++, a.v0 += SR_RANGE / 2, blocks >>= SR_HALF) {
+      a.load(row, blocks & ALL);
+      each(a, blocks & ALL);
+    }
+    done(a.v0 - SR_RANGE);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -191,7 +212,7 @@ sr_maxima_kernel(const SampleArgs a, const Spaces sp, int segs) {
   }
   const float* row = a.logits + (int64_t)r * a.ld;
   const int v0 = seg * SR_SEG + warp * SR_RANGE;
-  Logits q(row, v0, a.V);
+  Logits<SR_BLOCKS> q(row, v0, a.V);
   q.load(row, (1u << SR_BLOCKS) - 1u);
   uint32_t mx[SR_BLOCKS];  // order keys, NAN_KEY for a NaN (of which the bits of a sum say nothing)
 #pragma unroll
@@ -386,10 +407,12 @@ struct Sum {
       s.range_w[v0 / SR_RANGE] = w;
       s.range_c[v0 / SR_RANGE] = c;
     }
+    w = 0;
+    c = 0;
   }
 };
 
-__global__ void __launch_bounds__(SR_THREADS, 4)
+__global__ void __launch_bounds__(SR_THREADS, 5)
 sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
   __shared__ union {
     struct {
@@ -402,7 +425,7 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
-  Logits q(lrow, (seg * turns * SR_WARPS + warp) * SR_RANGE, a.V);
+  Half q(lrow, (seg * turns * SR_WARPS + warp) * SR_RANGE, a.V);
   grid_dep_wait();
   const int kind = s.state->kind;
   const Row row = s.state->row;
@@ -410,65 +433,65 @@ sr_pass_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
     const float bound = s.state->bound;
     if (tid == 0) sh.own.n = 0;
     __syncthreads();
-    uint32_t blocks = blocks_from(sp, s, q.v0, bound);
-    for (int turn = 0; turn < turns; turn++, q.v0 += SR_SEG, blocks >>= SR_BLOCKS) {
-      const uint32_t which = blocks & ((1u << SR_BLOCKS) - 1u);
-      if (which == 0u) continue;
-      q.load(lrow, which);
+    by_halves(lrow, q, turns, blocks_from(sp, s, q.v0, bound),
+              [&](const Half& h, uint32_t which) {
+                if (which == 0u) return;
 #pragma unroll
-      for (int g = 0; g < SR_BLOCKS; g++) {
-        const float l[4] = {q.l[g].x, q.l[g].y, q.l[g].z, q.l[g].w};
+                for (int g = 0; g < SR_HALF; g++) {
+                  const float l[4] = {h.l[g].x, h.l[g].y, h.l[g].z, h.l[g].w};
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (l[e] >= bound) own_add(sh.own, l[e], q.id(g, e));
-      }
-    }
+                  for (int e = 0; e < 4; e++)
+                    if (l[e] >= bound) own_add(sh.own, l[e], h.id(g, e));
+                }
+              },
+              [](int) {});
     own_flush(sh.own, s, row);
   } else if (kind == ROW_TOP_P) {
     for (int b = tid; b < SM_BINS; b += SR_THREADS) sh.lo[b] = sh.hi[b] = 0;
     __syncthreads();
-    for (int turn = 0; turn < turns; turn++, q.v0 += SR_SEG) {
-      q.load(lrow, (1u << SR_BLOCKS) - 1u);
+    by_halves(lrow, q, turns, ~0u,
+              [&](const Half& h, uint32_t) {
 #pragma unroll
-      for (int g = 0; g < SR_BLOCKS; g++) {
-        const float2 l[2] = {make_float2(q.l[g].x, q.l[g].y), make_float2(q.l[g].z, q.l[g].w)};
+                for (int g = 0; g < SR_HALF; g++) {
+                  const float2 l[2] = {make_float2(h.l[g].x, h.l[g].y), make_float2(h.l[g].z, h.l[g].w)};
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-          const float2 x = row.x2(l[e]);
-          const uint2 w = Row::w2(x);
-          const uint32_t ww[2] = {w.x, w.y};
-          const int bb[2] = {Row::bin_of(x.x), Row::bin_of(x.y)};
+                  for (int e = 0; e < 2; e++) {
+                    const float2 x = row.x2(l[e]);
+                    const uint2 w = Row::w2(x);
+                    const uint32_t ww[2] = {w.x, w.y};
+                    const int bb[2] = {Row::bin_of(x.x), Row::bin_of(x.y)};
 #pragma unroll
-          for (int h = 0; h < 2; h++)
-            if (ww[h] != 0u) {
-              const u64 v = widen(ww[h]);
-              atomicAdd(&sh.lo[bb[h]], (uint32_t)v & 0xFFFFu);
-              atomicAdd(&sh.hi[bb[h]], (uint32_t)(v >> 16));
-            }
-        }
-      }
-    }
+                    for (int k = 0; k < 2; k++)
+                      if (ww[k] != 0u) {
+                        const u64 v = widen(ww[k]);
+                        atomicAdd(&sh.lo[bb[k]], (uint32_t)v & 0xFFFFu);
+                        atomicAdd(&sh.hi[bb[k]], (uint32_t)(v >> 16));
+                      }
+                  }
+                }
+              },
+              [](int) {});
     __syncthreads();
     for (int b = tid; b < SM_BINS; b += SR_THREADS) {
       const u64 v = ((u64)sh.hi[b] << 16) + sh.lo[b];
       if (v != 0) atomicAdd(&s.mass[b], v);
     }
   } else if (kind == ROW_PLAIN) {
-    for (int turn = 0; turn < turns; turn++, q.v0 += SR_SEG) {
-      Sum sum;
-      q.load(lrow, (1u << SR_BLOCKS) - 1u);
+    Sum sum;
+    by_halves(lrow, q, turns, ~0u,
+              [&](const Half& h, uint32_t) {
 #pragma unroll
-      for (int g = 0; g < SR_BLOCKS; g++) {
-        const float2 l[2] = {make_float2(q.l[g].x, q.l[g].y), make_float2(q.l[g].z, q.l[g].w)};
+                for (int g = 0; g < SR_HALF; g++) {
+                  const float2 l[2] = {make_float2(h.l[g].x, h.l[g].y), make_float2(h.l[g].z, h.l[g].w)};
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-          const uint2 w = row.weight2(l[e]);
-          sum.add(w.x, l[e].x > -INFINITY && w.x >= row.min_w);
-          sum.add(w.y, l[e].y > -INFINITY && w.y >= row.min_w);
-        }
-      }
-      sum.store(s, q.v0, a.V);
-    }
+                  for (int e = 0; e < 2; e++) {
+                    const uint2 w = row.weight2(l[e]);
+                    sum.add(w.x, l[e].x > -INFINITY && w.x >= row.min_w);
+                    sum.add(w.y, l[e].y > -INFINITY && w.y >= row.min_w);
+                  }
+                }
+              },
+              [&](int v0) { sum.store(s, v0, a.V); });
   }
 }
 
@@ -642,7 +665,7 @@ __device__ void cut_and_draw(const SampleArgs& a, const Spaces& sp, const RowSpa
 // ---------------------------------------------------------------------------
 // the step of the top-p rows, and the draw
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(SR_THREADS, 4)
+__global__ void __launch_bounds__(SR_THREADS, 5)
 sr_step_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
   __shared__ OwnList own;
   grid_dep_launch();
@@ -650,52 +673,52 @@ sr_step_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
-  Logits q(lrow, (seg * turns * SR_WARPS + warp) * SR_RANGE, a.V);
+  Half q(lrow, (seg * turns * SR_WARPS + warp) * SR_RANGE, a.V);
   if (tid == 0) own.n = 0;
   __syncthreads();
   grid_dep_wait();
   if (s.state->kind != ROW_TOP_P) return;
   const Row row = s.state->row;
   const float bound = s.state->bound, summed = s.state->summed;
-  uint32_t blocks = blocks_from(sp, s, q.v0, bound);
-  for (int turn = 0; turn < turns; turn++, q.v0 += SR_SEG, blocks >>= SR_BLOCKS) {
-    Sum sum;
-    const uint32_t which = blocks & ((1u << SR_BLOCKS) - 1u);
-    if (which != 0u) {
-      q.load(lrow, which);
-      // a bit for each of the lane's logits; few of a row are above its cut,
-      // so that a lane weighs its own, read again, rather than all in turn
-      uint32_t above = 0u, within = 0u;
+  Sum sum;
+  by_halves(lrow, q, turns, blocks_from(sp, s, q.v0, bound),
+            [&](const Half& h, uint32_t which) {
+              if (which == 0u) return;
+              // a bit for each of the lane's logits; few of a row are above its
+              // cut, so that a lane weighs its own, read again, rather than all
+              // in turn
+              uint32_t above = 0u, within = 0u;
 #pragma unroll
-      for (int g = 0; g < SR_BLOCKS; g++) {
-        const float l[4] = {q.l[g].x, q.l[g].y, q.l[g].z, q.l[g].w};
+              for (int g = 0; g < SR_HALF; g++) {
+                const float l[4] = {h.l[g].x, h.l[g].y, h.l[g].z, h.l[g].w};
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          if (l[e] >= summed) above |= 1u << (4 * g + e);
-          if (l[e] >= bound) within |= 1u << (4 * g + e);
-        }
-      }
-      within &= ~above;
-      while (above != 0u) {
-        const int i = __ffs(above) - 1;
-        above &= above - 1u;
-        const bool two = above != 0u;
-        const int j = two ? __ffs(above) - 1 : i;
-        above &= above - 1u;
-        const uint2 w = row.weight2(make_float2(lrow[q.id(i >> 2, i & 3)], lrow[q.id(j >> 2, j & 3)]));
-        sum.add(w.x, w.x >= row.min_w);
-        sum.add(w.y, two && w.y >= row.min_w);
-      }
-      while (within != 0u) {
-        const int i = __ffs(within) - 1;
-        within &= within - 1u;
-        const int id = q.id(i >> 2, i & 3);
-        own_add(own, lrow[id], id);
-      }
-    }
-    __syncwarp();
-    sum.store(s, q.v0, a.V);
-  }
+                for (int e = 0; e < 4; e++) {
+                  if (l[e] >= summed) above |= 1u << (4 * g + e);
+                  if (l[e] >= bound) within |= 1u << (4 * g + e);
+                }
+              }
+              within &= ~above;
+              while (above != 0u) {
+                const int i = __ffs(above) - 1;
+                above &= above - 1u;
+                const bool two = above != 0u;
+                const int j = two ? __ffs(above) - 1 : i;
+                above &= above - 1u;
+                const uint2 w = row.weight2(make_float2(lrow[h.id(i >> 2, i & 3)], lrow[h.id(j >> 2, j & 3)]));
+                sum.add(w.x, w.x >= row.min_w);
+                sum.add(w.y, two && w.y >= row.min_w);
+              }
+              while (within != 0u) {
+                const int i = __ffs(within) - 1;
+                within &= within - 1u;
+                const int id = h.id(i >> 2, i & 3);
+                own_add(own, lrow[id], id);
+              }
+            },
+            [&](int v0) {
+              __syncwarp();
+              sum.store(s, v0, a.V);
+            });
   own_flush(own, s, row);
 }
 
@@ -750,41 +773,41 @@ sr_draw_kernel(const SampleArgs a, const Spaces sp) {
 __global__ void __launch_bounds__(SR_THREADS, 6)
 sr_filter_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
   const int at = (int)(gridDim.x - 1 - blockIdx.x), r = at / segs, seg = at % segs;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const RowSpace s = sp.row(r);
   const float* lrow = a.logits + (int64_t)r * a.ld;
   float* frow = a.filtered + (int64_t)r * a.ldf;
-  const bool aligned = ((reinterpret_cast<uintptr_t>(lrow) | reinterpret_cast<uintptr_t>(frow)) & 15u) == 0;
-  int v0 = (seg * turns * SR_WARPS + warp) * SR_RANGE;
+  Half q(lrow, (seg * turns * SR_WARPS + warp) * SR_RANGE, a.V);
+  q.aligned = q.aligned && (reinterpret_cast<uintptr_t>(frow) & 15u) == 0;
   grid_dep_wait();
   const int kind = s.state->kind;
   if (kind == ROW_HARD) return;  // written by its cluster
   const Row row = s.state->row;
   const float out = kind == ROW_BAD ? __int_as_float(0x7FFFFFFF) : SPEC_FILTERED;
-  uint32_t blocks = kind == ROW_BAD ? 0u : blocks_from(sp, s, v0, row.least);
   auto put = [&](float l, int id) {
     bool in = row.inside(l, id);
     if (in && row.min_w != 0u) in = row.weight(l) >= row.min_w;
     return in ? l : out;
   };
-  for (int turn = 0; turn < turns; turn++, v0 += SR_SEG) {
-#pragma unroll 2
-    for (int g = 0; g < SR_BLOCKS; g++, blocks >>= 1) {
-      const int g0 = v0 + g * SR_BLOCK;
-      if (aligned && g0 + SR_BLOCK <= a.V) {
-        float4 l = make_float4(out, out, out, out);
-        if (blocks & 1u) {
-          l = reinterpret_cast<const float4*>(lrow + g0)[lane];
-          const int id = g0 + 4 * lane;
-          l = make_float4(put(l.x, id), put(l.y, id + 1), put(l.z, id + 2), put(l.w, id + 3));
-        }
-        reinterpret_cast<float4*>(frow + g0)[lane] = l;
-      } else {
-        for (int id = g0 + lane; id < min(a.V, g0 + SR_BLOCK); id += 32)
-          frow[id] = blocks & 1u ? put(lrow[id], id) : out;
-      }
-    }
-  }
+  by_halves(lrow, q, turns, kind == ROW_BAD ? 0u : blocks_from(sp, s, q.v0, row.least),
+            [&](const Half& h, uint32_t which) {
+#pragma unroll
+              for (int g = 0; g < SR_HALF; g++) {
+                float4 l = make_float4(out, out, out, out);
+                if (which >> g & 1u)
+                  l = make_float4(put(h.l[g].x, h.id(g, 0)), put(h.l[g].y, h.id(g, 1)), put(h.l[g].z, h.id(g, 2)),
+                                  put(h.l[g].w, h.id(g, 3)));
+                if (h.whole(g)) {
+                  reinterpret_cast<float4*>(frow + h.v0 + g * SR_BLOCK)[h.lane] = l;
+                } else {
+                  const float e[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                  for (int k = 0; k < 4; k++)
+                    if (h.id(g, k) < a.V) frow[h.id(g, k)] = e[k];
+                }
+              }
+            },
+            [](int) {});
 }
 
 template <class... P, class... A>
@@ -823,8 +846,8 @@ int sample_rows_launch(SampleArgs a, void* workspace, cudaStream_t st) {
   const size_t grid = (size_t)a.R * segs;
   if (grid > INT32_MAX) return fail(SPEC_E_SHAPE, "sample: R * V too large");
   // two segments a CTA where CTAs are many (192 rows of 248320 logits, a top-k:
-  // 86 us with one, 78 with two, 76 with four, which then end unevenly where
-  // rows are of different kinds: 129 us with two, 132 with four)
+  // 86 us with one, 78 with two, 76 with four, which end unevenly, though,
+  // where rows are of different kinds)
   const int turns = (int)std::max<size_t>(1, std::min<size_t>(SR_TURNS, grid / 1216));
   const int long_segs = (segs + turns - 1) / turns;
   const size_t long_grid = (size_t)a.R * long_segs;
