@@ -647,10 +647,11 @@ def spec_sample(logits, R: int, V: int, u, token, temperature=None, top_k=None, 
     elif R * V > 2000000:  # (below, no call needs one)
         n = spec_sample_workspace(R, V)
         if n > 0:
+            import contextlib
             import torch
-            workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            # (of the allocator's pool of the call's stream: behind that stream's work only)
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
     _check(lib().spec_sample(_ptr(logits), int(R), int(V), int(ld), _ptr(u), _ptr(temperature),
                              _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(n_kept),
                              _ptr(filtered), int(ld_filtered), _ptr(workspace), n, _stream(stream)))

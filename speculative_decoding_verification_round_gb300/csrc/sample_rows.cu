@@ -56,7 +56,7 @@ constexpr int SR_HARD_CLUSTERS = 16;
 enum RowKind : int { ROW_BAD, ROW_PLAIN, ROW_TOP_K, ROW_TOP_P, ROW_HARD };
 
 struct RowState {
-  Row row;  // least, last_id: the cut, once `done`
+  Row row;  // (the cut in it where there is one: from the kernel that finds it on)
   float top;
   float bound;   // top-k: tokens from here on are collected; top-p: from here on up to
   float summed;  // here, and from here on their masses are summed up
