@@ -274,10 +274,28 @@ size_t sample_bytes(int R, int V);
 // turns it off).
 bool programmatic_launch();
 
+#ifdef __CUDACC__
+// A launch as a programmatic dependent of the stream's kernel in front of it
+// (the kernel's first step is grid_dep_wait).
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), size_t grid, int threads, size_t smem, cudaStream_t st,
+                                    A... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = programmatic_launch() ? 1 : 0;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------------------
 // device helpers
 // ---------------------------------------------------------------------------
-#ifdef __CUDACC__
 __device__ __forceinline__ uint32_t lop3_and_or(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;  // (a & b) | c
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
@@ -319,6 +337,12 @@ __device__ __forceinline__ void mma_16816_zero(float (&d)[4], const uint32_t (&a
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Both, in this order: a dependent that reads a call's arguments in front of
+// its own wait finds them written.
+__device__ __forceinline__ void grid_dep_begin() {
+  grid_dep_wait();
+  grid_dep_launch();
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const uint4* p) {

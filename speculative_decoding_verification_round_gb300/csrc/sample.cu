@@ -615,6 +615,7 @@ sample_kernel(const SampleArgs a) {
   Shared& sh = *reinterpret_cast<Shared*>(dyn);
   float* buf = reinterpret_cast<float*>(dyn + sizeof(Shared));
   cg::cluster_group cl = cg::this_cluster();
+  grid_dep_begin();
   if constexpr (LIST) {
     const int n = (int)cl.num_blocks(), count = *a.n_rows;
     for (int at = blockIdx.x / n; at < count; at += gridDim.x / n) {
@@ -650,15 +651,17 @@ int sample_clusters_launch(SampleArgs a, int clusters, cudaStream_t st) {
   if (a.seg > SM_SEG) return fail(SPEC_E_SHAPE, "V above 1048512 is not supported");
   const int room = (int)((227 * 1024 - sizeof(Shared)) / sizeof(float)) / 4 * 4;
   a.cap = std::min(a.seg, room);
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = cl;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = programmatic_launch() ? 2 : 1;
   cfg.gridDim = dim3((unsigned)clusters * cl);
   cfg.blockDim = dim3(SM_THREADS);
   cfg.dynamicSmemBytes = sizeof(Shared) + sizeof(float) * (size_t)a.cap;

@@ -199,7 +199,7 @@ __device__ __forceinline__ float nan_max(float x, float y) {
 }
 __global__ void __launch_bounds__(SR_THREADS)
 sr_maxima_kernel(const SampleArgs a, const Spaces sp, int segs) {
-  grid_dep_launch();
+  grid_dep_begin();  // (what comes next reads the settings in front of its wait)
   const int r = blockIdx.x / segs, seg = blockIdx.x % segs;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const RowSpace s = sp.row(r);
@@ -810,22 +810,6 @@ sr_filter_kernel(const SampleArgs a, const Spaces sp, int segs, int turns) {
             [](int) {});
 }
 
-template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), size_t grid, int threads, size_t smem, cudaStream_t st, bool dependent,
-                   A... args) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = dependent && programmatic_launch() ? 1 : 0;
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
 
 size_t sample_rows_bytes(int R, int V) {
@@ -851,19 +835,18 @@ int sample_rows_launch(SampleArgs a, void* workspace, cudaStream_t st) {
   const int turns = (int)std::max<size_t>(1, std::min<size_t>(SR_TURNS, grid / 1216));
   const int long_segs = (segs + turns - 1) / turns;
   const size_t long_grid = (size_t)a.R * long_segs;
-  cudaError_t e = launch(sr_maxima_kernel, grid, SR_THREADS, 0, st, false, a, sp, segs);
+  cudaError_t e = launch_dependent(sr_maxima_kernel, grid, SR_THREADS, 0, st, a, sp, segs);
   if (e == cudaSuccess)
-    e = launch(sr_bound_kernel, a.R, SM_THREADS, 0, st, true, a, sp);
-  if (e == cudaSuccess) e = launch(sr_pass_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
+    e = launch_dependent(sr_bound_kernel, a.R, SM_THREADS, 0, st, a, sp);
+  if (e == cudaSuccess) e = launch_dependent(sr_pass_kernel, long_grid, SR_THREADS, 0, st, a, sp, long_segs, turns);
   if (e == cudaSuccess && a.top_p != nullptr) {
-    e = launch(sr_cut_kernel, a.R, SM_THREADS, 0, st, true, a, sp);
-    if (e == cudaSuccess) e = launch(sr_step_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
+    e = launch_dependent(sr_cut_kernel, a.R, SM_THREADS, 0, st, a, sp);
+    if (e == cudaSuccess) e = launch_dependent(sr_step_kernel, long_grid, SR_THREADS, 0, st, a, sp, long_segs, turns);
   }
-  if (e == cudaSuccess) e = launch(sr_draw_kernel, a.R, SM_THREADS, sizeof(RowSmem), st, true, a, sp);
+  if (e == cudaSuccess) e = launch_dependent(sr_draw_kernel, a.R, SM_THREADS, sizeof(RowSmem), st, a, sp);
   if (e == cudaSuccess && a.filtered != nullptr)
-    e = launch(sr_filter_kernel, long_grid, SR_THREADS, 0, st, true, a, sp, long_segs, turns);
+    e = launch_dependent(sr_filter_kernel, long_grid, SR_THREADS, 0, st, a, sp, long_segs, turns);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("sample: ") + cudaGetErrorString(e));
-  // (an ordinary launch: behind everything in front of it)
   a.rows = sp.hard + 1;
   a.n_rows = sp.hard;
   return sample_clusters_launch(a, std::min(a.R, SR_HARD_CLUSTERS), st);

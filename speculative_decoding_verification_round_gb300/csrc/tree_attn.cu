@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT>::RESIDENT) tree_attn
   __shared__ TreeSmem s_tree;
   __shared__ long long s_part[TT_THREADS / 32];
   __shared__ Start s_at;
-  grid_dep_launch();  // the joining kernel may get ready
+  grid_dep_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int kg = warp;  // this warp's key group
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT>::RESIDENT) tree_attn
         const int pos = tile_base(t) + my_row;
         if (pos < q.len) {
           const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
-          const int pg = __ldg(a.table + (int64_t)q.slot * a.max_pages + e);
+          const int pg = a.table[(int64_t)q.slot * a.max_pages + e];
           if (pg >= 0 && pg < a.n_pages)
             x = ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
         }
@@ -488,7 +488,7 @@ tree_join_kernel(const TreeArgs a, int blocks, int slices) {
   const int blk = blockIdx.x / (slices * a.nkv) % blocks, s = blockIdx.x / (slices * a.nkv) / blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int m = blk * TJ_ROWS + lane, r = m & (a.rows - 1), node = node_of(a, m);
-  grid_dep_wait();
+  grid_dep_begin();
   const longlong2 p0 = __ldcg(reinterpret_cast<const longlong2*>(a.plan + s));
   const int4 p1 = __ldcg(reinterpret_cast<const int4*>(a.plan + s) + 1);
   const long long before = p0.x, share = p0.y;
@@ -595,8 +595,7 @@ bool on_tc(int rows) { return rows >= 64; }
 
 template <int HD, int MT>
 cudaError_t launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  tree_attn_kernel<HD, MT><<<n_cta + 1, TT_THREADS, Shape<HD, MT>::SMEM, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(tree_attn_kernel<HD, MT>, n_cta + 1, TT_THREADS, Shape<HD, MT>::SMEM, st, a);
 }
 
 template <int HD>
@@ -606,19 +605,11 @@ int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
                                  : launch_shape<HD, 2>(a, n_cta, st);
   if (e == cudaSuccess) {
     const int blocks = (a.nt * a.G + TJ_ROWS - 1) / TJ_ROWS;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = programmatic_launch() ? 1 : 0;
     const long long units = (long long)a.n_seq * blocks * a.nkv;
     const bool split = units * 8 <= n_cta;
     const int slices = split ? HD / 8 : units * (HD / 32) <= 1216 ? HD / 32 : 1;
-    cfg.gridDim = dim3((unsigned)(units * slices));
-    cfg.blockDim = dim3(32 * join_warps(split));
-    e = cudaLaunchKernelEx(&cfg, split ? tree_join_kernel<HD, true> : tree_join_kernel<HD, false>, a, blocks, slices);
+    e = launch_dependent(split ? tree_join_kernel<HD, true> : tree_join_kernel<HD, false>, (size_t)(units * slices),
+                         32 * join_warps(split), 0, st, a, blocks, slices);
   }
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("tree attention: ") + cudaGetErrorString(e));
   return SPEC_OK;

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   const uint32_t sm0 = smem_u32(smem);
   TcSmall& sh = *reinterpret_cast<TcSmall*>(smem + Sh::END);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  grid_dep_launch();  // the joining kernel may get ready
+  grid_dep_begin();
   const int n_cta = gridDim.x - 1;
   if ((int)blockIdx.x == n_cta) {
     plan_sequences<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, sh.part, smem);
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         const int pos = base + 32 * h;
         if (pos < q.len) {
           const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
-          const int pg = __ldg(row + e);
+          const int pg = row[e];
           if (pg >= 0 && pg < a.n_pages)
             x.at[h] = ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
         }
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       }
       // the row's node's ancestors and position
       auto parent = [&](int i) {
-        const int p = a.parents != nullptr ? __ldg(a.parents + (int64_t)s * a.nt + i) : i - 1;
+        const int p = a.parents != nullptr ? a.parents[(int64_t)s * a.nt + i] : i - 1;
         return p < i ? p : -1;  // (a tree that is none is refused by the joining kernel)
       };
       unsigned long long anc = 1ull << node;
@@ -777,8 +777,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
 
 template <int HD, int ROWS>
 cudaError_t launch(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  tree_attn_tc_kernel<HD, ROWS><<<n_cta + 1, TC_THREADS, tc_smem<HD>(), st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(tree_attn_tc_kernel<HD, ROWS>, n_cta + 1, TC_THREADS, tc_smem<HD>(), st, a);
 }
 
 template <int HD>
