@@ -35,11 +35,11 @@
 //
 // Measured: 2 x 16 nodes over 131071 positions (32 heads over 8 of 128, 1.07
 // GB) 182 us, 5.9 TB/s, 87% of the copy bandwidth: the memory.  4 x 63 nodes
-// over 8191 positions 49 us, of which about 8 are the start (cut, tensor
+// over 8191 positions 48 us, of which about 8 are the start (cut, tensor
 // memory, page lookups, first tiles), 8 the end and the joining kernel, and
 // 1.9 a tile of 128 positions x 256 rows: a stream's own chain of S, softmax
 // and P V (the products of both streams alone take 1.3).  12 x 16 nodes over
-// 512 positions, five tiles a unit and a unit a CTA, 24 us: start and end.
+// 512 positions, five tiles a unit and a unit a CTA, 23.5 us: start and end.
 // Not kept: the weights handed over in halves (52.8 -> 53.4 us), the maximum
 // taken beside the weights (49.0 -> 50.4), rings of three K and two V buffers
 // (48.8 -> 50.5; 4 x 63 nodes each).
