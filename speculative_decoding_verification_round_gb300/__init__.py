@@ -531,8 +531,9 @@ class KVPages:
     def __init__(self, k, v, table=None, lens=None, refs=None):
         n_layers, n_pages, n_kv_heads, page_size, head_dim = k.shape
         for t, name in ((k, "k"), (v, "v")):
-            if tuple(t.shape) != tuple(k.shape) or t.element_size() != 2 or not t[0].is_contiguous():
-                raise ValueError(f"{name}: a 16-bit tensor [n_layers][n_pages][n_kv_heads][page_size]"
+            if tuple(t.shape) != tuple(k.shape) or t.element_size() != 2 or not t[0].is_contiguous() or (
+                    t.is_floating_point() and str(t.dtype) != "torch.float16"):
+                raise ValueError(f"{name}: an fp16 tensor [n_layers][n_pages][n_kv_heads][page_size]"
                                  "[head_dim] with contiguous layers is required")
         if k.stride(0) != v.stride(0):
             raise ValueError("k and v must have the same layer stride")

@@ -245,3 +245,19 @@ def test_sample_refuses_bad_arguments(sv):
     assert sv.spec_sample_workspace(1, 151936) == 0 and sv.spec_sample_workspace(192, 248320) > 0
     assert call(filtered=A + 4) == sv.SPEC_E_INVALID  # half over the logits
     assert call(filtered=A, ld=100, ldf=104) == sv.SPEC_E_INVALID  # the logits with another stride
+
+
+def test_pages_of_other_tensors_are_refused():
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    ok = torch.zeros((2, 4, 2, 8, 64), dtype=torch.float16)
+    sv.KVPages(ok, ok.clone(), torch.zeros((3, 2), dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+    for k, v in ((ok.bfloat16(), ok.bfloat16()), (ok.float(), ok.float()), (ok, ok[:1]), (ok, ok.bfloat16()),
+                 (ok.transpose(2, 3), ok.transpose(2, 3))):
+        with pytest.raises(ValueError):
+            sv.KVPages(k, v)
+    for kw in (dict(table=torch.zeros((3, 2), dtype=torch.int64)), dict(lens=torch.zeros(2, dtype=torch.int32)),
+               dict(refs=torch.zeros(3, dtype=torch.int32))):
+        args = dict(table=torch.zeros((3, 2), dtype=torch.int32), lens=torch.zeros(3, dtype=torch.int32))
+        with pytest.raises(ValueError):
+            sv.KVPages(ok, ok.clone(), **{**args, **kw})
