@@ -271,6 +271,40 @@ def test_many_long_rows_replayed_and_on_two_streams(orc, dev):
     assert all(x[4].tolist() == want for x, _, _, _, want in sides)
 
 
+@pytest.mark.parametrize("R,V,step", [(2, 1048512, 1), (300, 20000, 100), (1000, 65536, 20), (45, 131073, 15),
+                                      (12, 524289, 3)])
+def test_many_rows_and_few_agree(dev, R, V, step):
+    """All rows at once (in passes) and a few at a time (in clusters): the
+    same tokens, counts and filtered logits, with ties and settings of all
+    kinds, up to the longest row."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    assert sv.spec_sample_workspace(R, V) > 0 == sv.spec_sample_workspace(step, V)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(V)
+    rnd = lambda: torch.rand((R,), generator=gen, device=dev)  # noqa: E731
+    x = torch.randn((R, V), generator=gen, device=dev) * torch.rand((R, 1), generator=gen, device=dev) * 4
+    x[::7] = (x[::7] * 2).round() / 2
+    u = torch.randint(-2 ** 31, 2 ** 31, (R,), generator=gen, device=dev).to(torch.int32)
+    one, none = torch.ones(R, device=dev), torch.zeros(R, device=dev)
+    T = torch.where(rnd() < 0.3, one, rnd() * 1.5 + 0.1)
+    k = torch.where(rnd() < 0.5, none, 10 ** (rnd() * 5)).to(torch.int32)
+    p, m = torch.where(rnd() < 0.5, one, rnd()), torch.where(rnd() < 0.7, none, rnd() * 0.1)
+
+    def call(s):
+        n = x[s].shape[0]
+        token, kept = torch.zeros(n, dtype=torch.int32, device=dev), torch.zeros(n, dtype=torch.int32, device=dev)
+        out = torch.empty_like(x[s])
+        sv.spec_sample(x[s], n, V, u[s], token, temperature=T[s], top_k=k[s], top_p=p[s], min_p=m[s], n_kept=kept,
+                       filtered=out)
+        return token, kept, out
+    all_rows = call(slice(0, R))
+    assert (all_rows[0] >= 0).all()
+    for i in range(0, R, step):
+        s = slice(i, min(R, i + step))
+        assert all(torch.equal(a[s], b) for a, b in zip(all_rows, call(s))), i
+
+
 def test_filtered_logits_feed_the_rejection_sampler(orc, dev):
     """Drafts sampled under filters, target rows filtered alike: the accept of
     the filtered rows is the oracle's, and no emitted token was filtered out."""
