@@ -122,7 +122,9 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 // and the start of the next: two pieces, each with its own first loads and its
 // own end, which cost as much as about three tiles.  Where a share of up to
 // three tiles more lets every CTA have one piece of one unit (the last piece
-// of a unit shorter), that is taken: units count as padded to whole shares.
+// of a unit shorter), that is taken: units count as padded to whole shares (12
+// x 16 nodes over 512 positions 26.6 -> 24.8 us, 16 sequences of one node with
+// a window of 4096 19.3 -> 17.8 us).
 struct Cut {
   long long share;
   bool pieces;
@@ -389,7 +391,7 @@ __device__ __forceinline__ bool load_tree(const TreeArgs& a, int s, int m, TreeS
 
 }  // namespace
 
-// The kernel for many query rows a kv head (tree_attn_tc.cu): a.rows 128 or
+// The kernel for many query rows a kv head (tree_attn_tc.cu): a.rows 64, 128 or
 // 256, tiles of 128 positions, one CTA an SM.
 constexpr int TREE_TC_SHIFT = 7;
 cudaError_t tree_tc_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st);
