@@ -583,8 +583,9 @@ typedef struct {
  *   status int32 [n_seq]: SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_TREE,
  *          SPEC_ST_TIMEOUT
  * out and workspace overlap none of the inputs, nor each other.
- * The scores' statistics and sums are fp32.  The same call gives the same
- * bits; which bits may depend on the other sequences of the call (the work
+ * The scores' statistics and sums are fp32, and the weights are multiplied as
+ * pairs of fp16 numbers (2^-21 of a weight, 2^-36 of the row's largest), for any
+ * number of rows.  The same call gives the same bits; which bits may depend on the other sequences of the call (the work
  * is cut evenly over the SMs), unlike spec_verify_attn, whose rows do not
  * depend on the batch. */
 int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,

@@ -14,8 +14,9 @@
 //   warps 12, 13 issue S_j = Q_j K^T and O_j += P_j V, one stream each
 //   warps 0-3, 4-7  two streams j = 0, 1: a thread owns a row; it reads its
 //                scores from tensor memory, keeps the running maximum and sum
-//                in fp32 (log2 domain) and writes P back as fp16, over the
-//                scores, where the MMA takes it as its A operand
+//                in fp32 (log2 domain) and writes P back over the scores as a
+//                pair of fp16 numbers, hi and lo, which the MMA takes as its A
+//                operands one after the other
 // The streams keep the tensor core busy while the other one is in its
 // softmax: with 256 rows they are the two row halves of every tile, with up
 // to 128 they take the even and the odd tiles of the same rows, each with its
@@ -23,26 +24,25 @@
 // Q tile twice, stream 0 has those of lanes 0-63 and stream 1 those of lanes
 // 64-127, so that the four SM sub-partitions share the softmax evenly.
 //
-// O is only rescaled when a row's maximum has grown by more than 2^8 since
-// the last time (the weights may exceed 1 until then, by less than fp16's
-// range), so the accumulator in tensor memory is hardly ever touched by the
-// softmax.  The weights are rounded once, to fp16, which costs an output half
-// an fp16 step of its average |v|: 2^-11 relative, as the rounding of the
-// output itself; a second MMA with the rounding errors (as the kernel for few
-// rows does, which waits for the cache anyway) would make the tensor core the
-// bound.  2^6 is multiplied into weights and sum alike, so that those of 2^-20
-// are still normal numbers.
+// O is only rescaled when a row's maximum has grown by more than 2^3 since
+// the last time (the weights may exceed 1 until then), so the accumulator in
+// tensor memory is hardly ever touched by the softmax.  2^12 is multiplied into
+// weights and sum alike, which keeps them below 2^15 and, with it, inside
+// fp16's range: of a weight w the pair holds all but 2^-21 w + 2^-36, so that
+// keys far below a row's largest are there, too (of n keys 20 nats below it, a
+// sum n e^-20 in front of the rounding of the output).  One fp16 number would
+// leave out 2^-11 w, as much again as the rounding of the output.
 //
 // Measured: 2 x 16 nodes over 131071 positions (32 heads over 8 of 128, 1.07
-// GB) 182 us, 5.9 TB/s, 87% of the copy bandwidth: the memory.  4 x 63 nodes
-// over 8191 positions 48 us, of which about 8 are the start (cut, tensor
+// GB) 181 us, 5.9 TB/s, 87% of the copy bandwidth: the memory.  4 x 63 nodes
+// over 8191 positions 57 us, of which about 8 are the start (cut, tensor
 // memory, page lookups, first tiles), 8 the end and the joining kernel, and
-// 1.9 a tile of 128 positions x 256 rows: a stream's own chain of S, softmax
-// and P V (the products of both streams alone take 1.3).  12 x 16 nodes over
-// 512 positions, five tiles a unit and a unit a CTA, 23.5 us: start and end.
-// Not kept: the weights handed over in halves (52.8 -> 53.4 us), the maximum
-// taken beside the weights (49.0 -> 50.4), rings of three K and two V buffers
-// (48.8 -> 50.5; 4 x 63 nodes each).
+// 2.4 a tile of 128 positions x 256 rows: a stream's own chain of S, softmax
+// and P V (the products of both streams alone take 1.9).  12 x 16 nodes over
+// 512 positions, five tiles a unit and a unit a CTA, 24.6 us: start and end.
+// With weights of one fp16 number these were 181, 48 and 24.  Not kept: the high
+// parts' product under the forming of the low ones (57 -> 56 us), rings of three
+// K and two V buffers (57 -> 59; 4 x 63 nodes each).
 #include <math.h>
 
 #include "common.cuh"
@@ -59,8 +59,9 @@ constexpr int PROD_THREADS = 64;  // of K's loads, and of V's
 // Registers a thread: the softmax keeps a row's 128 scores.  Both pairs of
 // warpgroups together hold the 512 x 128 of the launch.
 constexpr int REGS_SOFTMAX = 200, REGS_OTHER = 56;
-constexpr float P_BIAS = 6.0f;   // log2 of the factor of weights and sum
-constexpr float P_SLACK = 8.0f;  // growth of the maximum before O is rescaled
+constexpr float P_BIAS = 12.0f;  // log2 of the factor of weights and sum
+constexpr float P_SLACK = 3.0f;  // growth of the maximum before O is rescaled
+constexpr int P_LO = 64;         // columns from the weights' high parts to their low ones
 
 template <int HD>
 struct TcShape {
@@ -153,13 +154,10 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&v)[32])
       "r"(v[30]), "r"(v[31])
       : "memory");
 }
-__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+__device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tm_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -448,9 +446,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           tc_fence_after();
           if (j == 1 || i > 0) take_over(j == 1 ? TURN_0_1 : TURN_1_0);
           if (elect_one()) {
+#pragma unroll 1  // (sixteen in a row take registers that this warp does not have)
+            for (int lo = 0; lo <= P_LO; lo += P_LO)
 #pragma unroll
-            for (int kk = 0; kk < TC_KEYS / 16; kk++)
-              tc_mma_ta(tO, tS + 8 * kk, dv + ((kk * 2048) >> 4), id_o, 1u);
+              for (int kk = 0; kk < TC_KEYS / 16; kk++)
+                tc_mma_ta(tO, tS + lo + 8 * kk, dv + ((kk * 2048) >> 4), id_o, 1u);
             tc_commit(bar(sh.empty[vi.slot]));
             if (i + step >= n) tc_commit(bar(sh.o_done[j]));  // the stream's last tile
           }
@@ -589,21 +589,30 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
               }
             }
           }
-          // ---- the weights, as fp16 over the scores
+          // ---- the weights over the scores, as pairs of fp16: hi is the
+          // ---- weight cut off behind its 11th bit, lo the rest
           const float shift = P_BIAS - (mx == -INFINITY ? 0.0f : mx);
           const float2 sc2 = make_float2(scale, scale), sh2 = make_float2(shift, shift);
           float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
           for (int b = 0; b < 4; b++) {
-            uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 y = fma2(make_float2(__uint_as_float(v[b][e]), __uint_as_float(v[b][e + 1])), sc2, sh2);
-              const float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-              l[(e >> 1) & 1] = add2(l[(e >> 1) & 1], p);
-              pk[e >> 1] = pack_f16(p.x, p.y);
+            for (int e0 = 0; e0 < 32; e0 += 16) {
+              uint32_t hi[8], lo[8];
+#pragma unroll
+              for (int e = e0; e < e0 + 16; e += 2) {
+                const float2 y = fma2(make_float2(__uint_as_float(v[b][e]), __uint_as_float(v[b][e + 1])), sc2, sh2);
+                const float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                l[(e >> 1) & 1] = add2(l[(e >> 1) & 1], p);
+                const float2 cut = make_float2(__uint_as_float(__float_as_uint(p.x) & 0xFFFFE000u),
+                                               __uint_as_float(__float_as_uint(p.y) & 0xFFFFE000u));
+                const float2 rest = fma2(cut, make_float2(-1.0f, -1.0f), p);
+                hi[(e - e0) >> 1] = pack_f16(cut.x, cut.y);
+                lo[(e - e0) >> 1] = pack_f16(rest.x, rest.y);
+              }
+              tm_st8(tS + 16 * b + (e0 >> 1), hi);
+              tm_st8(tS + P_LO + 16 * b + (e0 >> 1), lo);
             }
-            tm_st16(tS + 16 * b, pk);
           }
           l[0] = add2(l[0], l[1]);
           sum += l[0].x + l[0].y;
@@ -620,7 +629,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
 #pragma unroll 1
                 for (unsigned long long left = sh.bad[slot][b]; left != 0ull; left &= left - 1ull) {
                   const int key = 64 * b + __ffsll((long long)left) - 1;
-                  const float p = half_of(tm_ld1(tS + (key >> 1)), key & 1);
+                  const float p = half_of(tm_ld1(tS + (key >> 1)), key & 1) + half_of(tm_ld1(tS + P_LO + (key >> 1)), key & 1);
                   const __half* src = a.v;
                   if (tree) {
                     src = a.v_new + ((int64_t)s * a.nt + key) * a.kv_stride + kvh * HD;
@@ -728,15 +737,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         float* x_out = reinterpret_cast<float*>(smem + j * Sh::TILE);
         const float* x_in = reinterpret_cast<const float*>(smem + (1 - j) * Sh::TILE);
         constexpr int XR = ROWS == 64 ? 64 : 128;
-        uint32_t o[CH / 2][32];
+        uint4 y[CH * 2];
         if (warp_live) {
           sh.x_ml[j][rr] = make_float2(mx, sum);
 #pragma unroll
           for (int d = 0; d < CH / 2; d++) {
-            tm_ld32(tO + 32 * ((1 - j) * (CH / 2) + d), o[d]);
-            tm_wait_ld(o[d]);
+            uint32_t o[32];
+            tm_ld32(tO + 32 * ((1 - j) * (CH / 2) + d), o);
+            tm_wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 32; e++) x_out[(32 * d + e) * XR + rr] = __uint_as_float(o[d][e]);
+            for (int e = 0; e < 32; e++) x_out[(32 * d + e) * XR + rr] = __uint_as_float(o[e]);
           }
         }
         asm volatile("bar.sync 3, 256;" ::: "memory");
@@ -745,23 +755,27 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           const float m2 = fmaxf(mx, other.x), ref = m2 == -INFINITY ? 0.0f : m2;
           const float w_own = exp2_fast(mx - ref), w_other = exp2_fast(other.x - ref);
           sum = sum * w_own + other.y * w_other;
+          const float inv = 1.0f / sum;
           if (live && !whole && j == 0) a.part_ml[slot * ROWS + rr] = make_float2(m2, sum);
 #pragma unroll
           for (int d = 0; d < CH / 2; d++) {
-            tm_ld32(tO + 32 * (j * (CH / 2) + d), o[d]);
-            tm_wait_ld(o[d]);
+            uint32_t o[32];
+            tm_ld32(tO + 32 * (j * (CH / 2) + d), o);
+            tm_wait_ld(o);
 #pragma unroll
             for (int e = 0; e < 32; e++)
-              o[d][e] = __float_as_uint(fmaf(x_in[(32 * d + e) * XR + rr], w_other, __uint_as_float(o[d][e]) * w_own));
-            if (!whole) put_piece(j * (CH / 2) + d, o[d]);
+              o[e] = __float_as_uint(fmaf(x_in[(32 * d + e) * XR + rr], w_other, __uint_as_float(o[e]) * w_own));
+            if (!whole) {
+              put_piece(j * (CH / 2) + d, o);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; c++) y[4 * d + c] = chunk_of(o, c, inv);
+            }
           }
         }
         asm volatile("bar.sync 3, 256;" ::: "memory");  // both halves have been read
         if (whole) {
-          if (warp_live) {
-            const float inv = 1.0f / sum;
-            put_whole([&](int c) { return chunk_of(o[c >> 2], c, inv); }, HD / 2, j * (HD / 2));
-          }
+          if (warp_live) put_whole([&](int c) { return y[c]; }, HD / 2, j * (HD / 2));
           asm volatile("bar.sync 3, 256;" ::: "memory");  // before the next q tile
         }
       }

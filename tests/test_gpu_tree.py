@@ -558,3 +558,44 @@ def test_rounds_of_a_tree_drafting_decoder(orc, dev):
         for p, t in enumerate(texts[s][:-1]):
             pg = table[s, p // page].item()
             assert torch.equal(kc[:, pg, :, p % page], Wkd[:, t]) and torch.equal(vc[:, pg, :, p % page], Wvd[:, t])
+
+
+# ---------------------------------------------------------------------------
+# the weights' precision
+# ---------------------------------------------------------------------------
+def check_tight(c, got, floor):
+    """As Case.check, without a rounding of the weights to fp16 for any number
+    of rows.  Weights, relative to themselves: the split into two fp16 numbers
+    2^-21 (hi cut off behind 11 bits, lo rounded to half a step of its own),
+    exp2 2^-22, the rounding of its argument, up to 16 in magnitude where a
+    weight counts, 2^-21: together less than 2^-19.  Relative to the row's
+    largest weight, 1: `floor`, where hi and lo leave fp16's normal numbers.
+    Plus the scores' error and fp32 sums as there."""
+    for b in range(c.n):
+        m = int(c.counts[b])
+        if m == 0:
+            continue
+        k, v = c.cached(0, b), c.cached(1, b)
+        ref, mag, dots = tree.tree_attention(c.q[b, :m], k, v, c.kn[b, :m], c.vn[b, :m], c.parents[b, :m].tolist(),
+                                             c.window, c.sinks, c.scale)
+        scale = c.scale or c.hd ** -0.5
+        ds = (c.hd + 4) * 2.0 ** -23 * abs(scale) * dots
+        rel = np.expm1(2 * ds) + 2.0 ** -19 + ((c.lens[b] + m) / 8 + 64) * 2.0 ** -23
+        g = c.nq // c.nkv
+        v_sum = np.abs(v.astype(np.float64)).sum(0) + np.abs(c.vn[b, :m].astype(np.float64)).sum(0)  # [nkv][hd]
+        bound = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 1.01 * (rel[..., None] * mag + floor * np.repeat(v_sum, g, 0))
+        err = np.abs(got[b, :m].astype(np.float64) - ref)
+        assert np.isfinite(got[b, :m]).all() and (err <= bound).all(), (b, float(np.max(err - bound)))
+
+
+WEIGHT_FLOOR = 2.0 ** -36  # of the kernel for many rows: 2^-25 twice over a factor of 2^12
+
+
+@pytest.mark.parametrize("nq,nkv,hd,lens,nt", [(32, 8, 128, [300, 77], 16), (40, 8, 128, [512, 260], 16),
+                                               (8, 2, 64, [900, 130], 32), (8, 1, 128, [700], 63), (16, 2, 64, [128], 64)])
+def test_weights_of_many_rows_are_not_rounded_to_fp16(dev, nq, nkv, hd, lens, nt):
+    """More than 32 query rows a kv head are as exact as fewer."""
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng([41, nq, nt])
+    c = Case(sv, dev, g, nq, nkv, hd, lens, nt, 64)
+    check_tight(c, c.call(), WEIGHT_FLOOR)
