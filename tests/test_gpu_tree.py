@@ -599,3 +599,24 @@ def test_weights_of_many_rows_are_not_rounded_to_fp16(dev, nq, nkv, hd, lens, nt
     g = np.random.default_rng([41, nq, nt])
     c = Case(sv, dev, g, nq, nkv, hd, lens, nt, 64)
     check_tight(c, c.call(), WEIGHT_FLOOR)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2000, 4)])
+@pytest.mark.parametrize("nt", [4, 8, 16, 32, 64])
+def test_keys_far_below_a_dominant_one(dev, nt, window, sinks):
+    """A first position whose score stands 8 to 18 nats above thousands of
+    nearly equal ones and whose value is 0: the output is what those add up
+    to.  16, 32, 64, 128 and 256 rows a kv head."""
+    import speculative_decoding_verification_round_gb300 as sv
+    hd, n = 64, 3000
+    for nats in (8.0, 14.0, 16.0, 18.0):
+        g = np.random.default_rng([43, nt, int(nats)])
+        c = Case(sv, dev, g, 4, 1, hd, [n], nt, 64, window, sinks, layers=1)
+        c.q[:] = 1.0 + 0.01 * g.standard_normal(c.q.shape)
+        for a in (c.k, c.kn):
+            a[:] = 0.01 * g.standard_normal(a.shape)
+        for a in (c.v, c.vn):
+            a[:] = g.uniform(0.5, 1.5, a.shape)
+        first = c.table[c.slots[0], 0]
+        c.k[0, first, 0, 0], c.v[0, first, 0, 0] = nats / np.sqrt(hd), 0.0
+        check_tight(c, c.call(), WEIGHT_FLOOR)
