@@ -591,13 +591,23 @@ def check_tight(c, got, floor):
 WEIGHT_FLOOR = 2.0 ** -36  # of the kernel for many rows: 2^-25 twice over a factor of 2^12
 
 
-@pytest.mark.parametrize("nq,nkv,hd,lens,nt", [(32, 8, 128, [300, 77], 16), (40, 8, 128, [512, 260], 16),
+@pytest.mark.parametrize("nq,nkv,hd,lens,nt", [(8, 2, 64, [500, 90], 3), (8, 2, 128, [500, 90], 8),
+                                               (32, 8, 128, [300, 77], 16), (40, 8, 128, [512, 260], 16),
                                                (8, 2, 64, [900, 130], 32), (8, 1, 128, [700], 63), (16, 2, 64, [128], 64)])
-def test_weights_of_many_rows_are_not_rounded_to_fp16(dev, nq, nkv, hd, lens, nt):
-    """More than 32 query rows a kv head are as exact as fewer."""
+def test_weights_are_not_rounded_to_fp16(dev, nq, nkv, hd, lens, nt):
+    """Keys of score 0 and value 1 against as many of a score a little below
+    and value -1: the output is half the difference of the two weights, a few
+    roundings of one fp16 number, and the scores are too small to be off.  With
+    any number of rows."""
     import speculative_decoding_verification_round_gb300 as sv
     g = np.random.default_rng([41, nq, nt])
-    c = Case(sv, dev, g, nq, nkv, hd, lens, nt, 64)
+    c = Case(sv, dev, g, nq, nkv, hd, lens, nt, 64, scale=1.0)
+    c.q[:] = 0
+    c.q[..., 0] = g.uniform(0.5, 2.0, c.q.shape[:3])
+    for k, v in ((c.k, c.v), (c.kn, c.vn)):
+        low = g.integers(0, 2, k.shape[:-1]).astype(bool)
+        k[:], v[:] = 0, np.where(low, -1.0, 1.0)[..., None]
+        k[..., 0] = np.where(low, -0.0011, 0.0)
     check_tight(c, c.call(), WEIGHT_FLOOR)
 
 
