@@ -140,22 +140,23 @@ constexpr int EX_THREADS = 1024;  // one thread per entry
 constexpr int EX_PER = 4;         // reference counts a thread looks at per step
 
 // Inclusive sum over the CTA's threads; *total gets the whole (every thread).
-__device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
+// In 64 bits: each of 1024 entries may want 2^31 pages.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  int64_t x = v;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
     if (lane >= off) x += y;
   }
   __syncthreads();  // s_warp of the last call has been read
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int w = s_warp[lane];
+    int64_t w = s_warp[lane];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, off);
+      const int64_t y = __shfl_up_sync(0xffffffffu, w, off);
       if (lane >= off) w += y;
     }
     s_warp[lane] = w;
@@ -169,16 +170,17 @@ __global__ void __launch_bounds__(EX_THREADS)
 pages_extend_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slots,
                     const int32_t* __restrict__ n_new, int32_t* __restrict__ copies,
                     int32_t* __restrict__ status) {
-  __shared__ int s_slot[EX_THREADS], s_tail[EX_THREADS], s_first[EX_THREADS + 1];
+  __shared__ int s_slot[EX_THREADS], s_tail[EX_THREADS];
+  __shared__ int64_t s_first[EX_THREADS + 1], s_warp[32];
   __shared__ int s_entry[EX_THREADS];  // first table entry that the entry's fresh pages fill
   __shared__ unsigned char s_copy[EX_THREADS];
-  __shared__ int s_warp[32];
   const int i = threadIdx.x;
   const bool mine = i < n;
   const int slot = mine ? slots[i] : -1;
   s_slot[i] = slot;
   __syncthreads();
-  int st = 0, tail = -1, need = 0, j0 = 0;
+  int st = 0, tail = -1, j0 = 0;
+  int64_t need = 0;
   bool partial = false;
   if (mine) {
     if (slot < 0 || slot >= kv.n_slots) st |= SPEC_ST_SLOT;
@@ -213,7 +215,7 @@ pages_extend_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slot
         }
         for (int j = j0; j < want; j++)
           if (row[j] >= 0) st |= SPEC_ST_PAGE;
-        need = (int)(want > j0 ? want - j0 : 0);
+        need = want > j0 ? want - j0 : 0;
         if (add == 0) tail = -1, partial = false;  // nothing will be written
       }
     }
@@ -232,8 +234,8 @@ pages_extend_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slot
   }
   if (st != 0) need = 0;
   need += copy;
-  int total;
-  const int incl = block_scan(need, s_warp, &total);
+  int64_t total;
+  const int64_t incl = block_scan(need, s_warp, &total);
   s_first[i + 1] = incl;
   if (i == 0) s_first[0] = 0;
   s_entry[i] = j0;
@@ -241,16 +243,17 @@ pages_extend_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slot
   __syncthreads();
   // the k-th free page (in page order) belongs to the entry whose range of
   // the prefix sum holds k: first its copy, then its entries j0, j0 + 1, ...
-  int found = 0;
-  for (int base = 0; base < kv.n_pages && found < total; base += EX_THREADS * EX_PER) {
+  int64_t found = 0;
+  const int most = total <= kv.n_pages ? kv.n_pages : 0;  // (more than the pool has: none is given out)
+  for (int base = 0; base < most && found < total; base += EX_THREADS * EX_PER) {
     const int p0 = base + i * EX_PER;
     int free_mask = 0;
 #pragma unroll
     for (int u = 0; u < EX_PER; u++)
       if (p0 + u < kv.n_pages && kv.refs[p0 + u] == 0) free_mask |= 1 << u;
-    int here;
-    const int upto = block_scan(__popc(free_mask), s_warp, &here);
-    int k = found + upto - __popc(free_mask);
+    int64_t here;
+    const int64_t upto = block_scan(__popc(free_mask), s_warp, &here);
+    int64_t k = found + upto - __popc(free_mask);
     for (int m = free_mask; m != 0 && k < total; m &= m - 1, k++) {
       const int p = p0 + __ffs(m) - 1;
       int lo = 0, hi = EX_THREADS - 1;  // the last entry with s_first <= k
@@ -258,7 +261,7 @@ pages_extend_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slot
         const int mid = (lo + hi + 1) >> 1;
         if (s_first[mid] <= k) lo = mid; else hi = mid - 1;
       }
-      const int idx = k - s_first[lo];
+      const int64_t idx = k - s_first[lo];
       if (s_copy[lo] && idx == 0)
         copies[2 * lo + 1] = p;
       else
@@ -275,12 +278,12 @@ pages_extend_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slot
     if (st == 0) {
       if (full) {  // take back what was given out
         st |= SPEC_ST_FULL;
-        const int k0 = s_first[i];
-        for (int idx = 0; idx < need && k0 + idx < found; idx++) {
+        const int64_t k0 = s_first[i];
+        for (int64_t idx = 0; idx < need && k0 + idx < found; idx++) {
           if (copy && idx == 0) {
             kv.refs[copies[2 * i + 1]] = 0;
           } else {
-            const int e = s_entry[i] + idx - (copy ? 1 : 0);
+            const int64_t e = s_entry[i] + idx - (copy ? 1 : 0);
             kv.refs[row[e]] = 0;
             row[e] = -1;
           }

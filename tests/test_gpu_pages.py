@@ -174,6 +174,27 @@ def test_many_entries_and_a_large_pool(dev):
     p.check()
 
 
+def test_wanted_pages_that_sum_up_past_32_bits(dev):
+    """1024 entries, each of which its table has room for: the sum of the pages
+    that they want is 2^32, and 2^31 and a little; none gets any."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    n, n_pages, i32 = 1024, 1500, dict(dtype=torch.int32, device=dev)
+    table = torch.full((n, 2 ** 22), -1, **i32)
+    lens, refs = torch.zeros(n, **i32), torch.zeros(n_pages, **i32)
+    k = torch.zeros((1, n_pages, 1, 1, 8), dtype=torch.int16, device=dev)
+    kv = sv.KVPages(k, k.clone(), table, lens, refs)
+    slots = torch.arange(n, **i32)
+    for want in (2 ** 22, 2 ** 21 + 1):
+        st, cp = torch.full((n,), 77, **i32), torch.full((n, 2), 7, **i32)
+        sv.spec_pages_extend(kv, n, slots, torch.full((n,), want, **i32), cp, st)
+        assert (st == tree.ST_FULL).all() and (cp == -1).all()
+        assert not refs.any() and (table == -1).all()
+    sv.spec_pages_extend(kv, n, slots, torch.ones(n, **i32), cp, st)
+    assert not st.any() and (refs[:n] == 1).all() and not refs[n:].any()
+    assert torch.equal(table[:, 0], slots) and (table[:, 1] == -1).all()
+
+
 def test_a_long_prompt_is_appended_in_place(dev):
     """path NULL, more rows than a CTA's share, several pages, an odd start;
     then new_len apart from len."""
