@@ -244,9 +244,9 @@ pages_extend_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slot
   // the k-th free page (in page order) belongs to the entry whose range of
   // the prefix sum holds k: first its copy, then its entries j0, j0 + 1, ...
   int64_t found = 0;
-  const int most = total <= kv.n_pages ? kv.n_pages : 0;  // (more than the pool has: none is given out)
-  for (int base = 0; base < most && found < total; base += EX_THREADS * EX_PER) {
-    const int p0 = base + i * EX_PER;
+  const int64_t most = total <= kv.n_pages ? kv.n_pages : 0;  // (more than the pool has: none is given out)
+  for (int64_t base = 0; base < most && found < total; base += EX_THREADS * EX_PER) {
+    const int64_t p0 = base + i * EX_PER;
     int free_mask = 0;
 #pragma unroll
     for (int u = 0; u < EX_PER; u++)
@@ -255,7 +255,7 @@ pages_extend_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slot
     const int64_t upto = block_scan(__popc(free_mask), s_warp, &here);
     int64_t k = found + upto - __popc(free_mask);
     for (int m = free_mask; m != 0 && k < total; m &= m - 1, k++) {
-      const int p = p0 + __ffs(m) - 1;
+      const int p = (int)p0 + __ffs(m) - 1;
       int lo = 0, hi = EX_THREADS - 1;  // the last entry with s_first <= k
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;

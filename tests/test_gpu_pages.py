@@ -195,6 +195,23 @@ def test_wanted_pages_that_sum_up_past_32_bits(dev):
     assert torch.equal(table[:, 0], slots) and (table[:, 1] == -1).all()
 
 
+def test_the_largest_pool(dev):
+    """2^31 - 1 pages: the last one is found, and when it is taken the call ends."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    n_pages, i32 = 2 ** 31 - 1, dict(dtype=torch.int32, device=dev)
+    k = torch.empty((1, n_pages, 1, 1, 8), dtype=torch.int16, device=dev)
+    refs = torch.ones(n_pages, **i32)
+    refs[-1] = 0
+    table, lens = torch.full((1, 4), -1, **i32), torch.zeros(1, **i32)
+    kv = sv.KVPages(k, k, table, lens, refs)
+    one, st, cp = torch.ones(1, **i32), torch.full((1,), 77, **i32), torch.full((1, 2), 7, **i32)
+    sv.spec_pages_extend(kv, 1, torch.zeros(1, **i32), one, cp, st)
+    assert st.item() == 0 and table.tolist() == [[n_pages - 1, -1, -1, -1]] and refs[-1].item() == 1
+    sv.spec_pages_extend(kv, 1, torch.zeros(1, **i32), one * 2, cp, st)
+    assert st.item() == tree.ST_FULL and table.tolist() == [[n_pages - 1, -1, -1, -1]] and cp.tolist() == [[-1, -1]]
+
+
 def test_a_long_prompt_is_appended_in_place(dev):
     """path NULL, more rows than a CTA's share, several pages, an odd start;
     then new_len apart from len."""
