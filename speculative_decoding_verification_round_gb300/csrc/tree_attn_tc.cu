@@ -622,21 +622,28 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
             const uint32_t slot = item.slot;
             wait(sh.full[slot], item.turn);
             __syncwarp();
-            if ((sh.bad[slot][0] | sh.bad[slot][1]) != 0ull) {
+            // (one lane's reading for the whole warp, and a row's place checked:
+            // after a wait that has given up the marks may be another tile's)
+            const unsigned long long bad[2] = {__shfl_sync(0xffffffffu, sh.bad[slot][0], 0),
+                                               __shfl_sync(0xffffffffu, sh.bad[slot][1], 0)};
+            if ((bad[0] | bad[1]) != 0ull) {
               const bool tree = t == q.tiles - 1;
 #pragma unroll 1
               for (int b = 0; b < 2; b++)
 #pragma unroll 1
-                for (unsigned long long left = sh.bad[slot][b]; left != 0ull; left &= left - 1ull) {
+                for (unsigned long long left = b == 0 ? bad[0] : bad[1]; left != 0ull; left &= left - 1ull) {
                   const int key = 64 * b + __ffsll((long long)left) - 1;
                   const float p = half_of(tm_ld1(tS + (key >> 1)), key & 1) + half_of(tm_ld1(tS + P_LO + (key >> 1)), key & 1);
                   const __half* src = a.v;
                   if (tree) {
+                    if (key >= q.m) continue;
                     src = a.v_new + ((int64_t)s * a.nt + key) * a.kv_stride + kvh * HD;
                   } else {
                     const int at = tile_base(t) + key, e = at / a.page_size;
-                    src += (((int64_t)a.table[(int64_t)q.slot * a.max_pages + e] * a.nkv + kvh) * a.page_size +
-                            (at - e * a.page_size)) * HD;
+                    if (at >= q.len) continue;
+                    const int pg = a.table[(int64_t)q.slot * a.max_pages + e];
+                    if (pg < 0 || pg >= a.n_pages) continue;
+                    src += (((int64_t)pg * a.nkv + kvh) * a.page_size + (at - e * a.page_size)) * HD;
                   }
 #pragma unroll 1
                   for (int d = 0; d < CH; d++) {
