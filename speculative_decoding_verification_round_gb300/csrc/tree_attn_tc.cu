@@ -424,14 +424,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       };
       // The streams take turns, each with its P V and its next S in one go: were
       // both streams' products mixed, both would wait for theirs, and then
-      // both be in their softmax, with the tensor core idle.
+      // both be in their softmax, with the tensor core idle.  These barriers
+      // have no limit of their own, and need none: both warps go through the
+      // same pieces and tiles whatever their bounded waits say, and meet
+      // between two pieces, so that no barrier is arrived at twice.
       auto hand_over = [](int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); };
       auto take_over = [](int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); };
-      constexpr int TURN_0_1 = 4, TURN_1_0 = 5, START_0_1 = 6;
+      constexpr int TURN_0_1 = 4, TURN_1_0 = 5, START_0_1 = 6, PIECE = 7;
       for (long long left = my_tiles; left > 0; left -= n, off += n, tile0 += n, seg++) {
         next_piece(left);
         const int step = TWO ? 1 : 2;
         int i = TWO ? 0 : j;
+        if (seg > 0) take_over(PIECE);
         wait(sh.q_full, seg);  // (without a tile, too: a phase each piece)
         if (i >= n) continue;
         if (j == 1) take_over(START_0_1);
