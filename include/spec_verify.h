@@ -598,6 +598,16 @@ int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* t, const ui
 int spec_tree_attn_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads,
                              size_t* bytes);
 
+/* Test hook for the fail-closed path of spec_tree_attn's bounded waits (of the
+ * kernel for more than 32 query rows a kv head).  A wait that gives up (131072
+ * suspended tries of about 10 us) ends its CTA's loads and products; the CTA
+ * lets those in flight end, and the sequences that it works on get
+ * SPEC_ST_TIMEOUT and NaN.  This call sets the budget of the first wait of
+ * each CTA's softmax for the calling thread's later calls (a captured call
+ * keeps the one it was captured with); 0 makes that wait give up at once.
+ * 0 <= tries <= 131072. */
+int spec_tree_set_wait_budget(int tries);
+
 /* Greedy acceptance along the trees: from node 0 (the anchor, parent -1), the
  * target's argmax at the current node selects the child that carries that
  * token (the lowest numbered of several), until none does.

@@ -47,7 +47,7 @@ EXPORTED = ["spec_last_error", "spec_qmat_create", "spec_qmat_destroy", "spec_li
             "spec_depth_ctl_estimates", "spec_model_pages", "spec_pages_copy", "spec_pages_fork",
             "spec_pages_extend", "spec_pages_commit", "spec_pages_free", "spec_tree_attn",
             "spec_tree_attn_workspace", "spec_accept_tree", "spec_sample",
-            "spec_sample_workspace"]
+            "spec_sample_workspace", "spec_tree_set_wait_budget"]
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
@@ -170,6 +170,7 @@ def lib():
                 "spec_accept_tree": (I32, [P, P, P, P, I32, I32, P, P, P, P]),
                 "spec_sample": (I32, [P, I32, I32, I64, P, P, P, P, P, P, P, P, I64, P, SZ, P]),
                 "spec_sample_workspace": (I32, [I32, I32, P]),
+                "spec_tree_set_wait_budget": (I32, [I32]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -618,6 +619,12 @@ def spec_tree_attn(kv: KVPages, layer: int, n_seq: int, slots, nt: int, n_q_head
                                 _ptr(k_new), _ptr(v_new), int(kv_stride), _ptr(out),
                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
                                 _ptr(status), _stream(stream)))
+
+
+def spec_tree_set_wait_budget(tries: int):
+    """Test hook: the budget of each CTA's first wait in this thread's later
+    spec_tree_attn calls (0: it gives up at once; normally 131072)."""
+    _check(lib().spec_tree_set_wait_budget(int(tries)))
 
 
 def spec_accept_tree(argmax, tokens, parents, n_nodes, n_seq: int, nt: int, path, n_path, emitted,

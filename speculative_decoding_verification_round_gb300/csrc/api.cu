@@ -1213,6 +1213,12 @@ extern "C" int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* 
                      as_stream(stream));
 }
 
+extern "C" int spec_tree_set_wait_budget(int tries) {
+  if (tries < 0 || tries > LIN_WAIT_TRIES) return fail(SPEC_E_INVALID, "tries outside [0, 131072]");
+  tree_set_wait_budget(tries);
+  return SPEC_OK;
+}
+
 extern "C" int spec_sample_workspace(int R, int V, size_t* bytes) {
   if (bytes == nullptr) return fail(SPEC_E_INVALID, "null argument");
   if (R < 1 || V < 1 || R > (1 << 26) || V > 1048512)

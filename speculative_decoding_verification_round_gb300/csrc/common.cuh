@@ -268,6 +268,7 @@ int launch_sample(const float* logits, int R, int V, int64_t ld, const uint32_t*
                   const float* min_p, int32_t* token, int32_t* n_kept, float* filtered, int64_t ldf,
                   void* workspace, cudaStream_t st);
 size_t sample_bytes(int R, int V);
+void tree_set_wait_budget(int tries);
 
 // Whether kernels that can overlap their predecessor's tail are launched as
 // programmatic dependents (default on; SPEC_VERIFY_PDL=0 in the environment

@@ -653,7 +653,12 @@ int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
   return SPEC_OK;
 }
 
+// Budget of the calling thread's calls for the first wait of a CTA (tree_set_wait_budget).
+thread_local int t_wait_tries = LIN_WAIT_TRIES;
+
 }  // namespace
+
+void tree_set_wait_budget(int tries) { t_wait_tries = tries; }
 
 void tree_init_attrs() {
   init_shape<64, 1>();
@@ -714,6 +719,7 @@ int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint1
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)n_cta * 2 * rows * kv->head_dim);
   uint32_t* err = reinterpret_cast<uint32_t*>(a.part_ml + (size_t)n_cta * 2 * rows);
   a.part_err = on_tc(a.rows) ? err : nullptr;
+  a.wait_tries = t_wait_tries;
   a.plan = reinterpret_cast<TreePlan*>(err + ((size_t)n_cta + 3) / 4 * 4);
   return kv->head_dim == 128 ? launch_hd<128>(a, n_cta, st) : launch_hd<64>(a, n_cta, st);
 }

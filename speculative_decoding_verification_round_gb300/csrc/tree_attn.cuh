@@ -29,6 +29,7 @@ struct TreeArgs {
   float* part_o;    // [N][2][HD / 4][rows][4]: a lane a row, its stores side by side
   float2* part_ml;  // [N][2][rows]
   uint32_t* part_err;  // [N]: 1 if the CTA gave up on a wait
+  int wait_tries;      // budget of a CTA's first wait for scores (tree_set_wait_budget)
   struct TreePlan* plan;  // [n_seq]
   int32_t* status;
 };

@@ -254,10 +254,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   tc_fence_after();
   const uint32_t tmem = sh.tmem;  // columns: S_0, S_1 (128 each; P_j over S_j), O_0, O_1
   volatile int* abort_flag = &sh.abort;
-  // Every wait is bounded; once one has given up the others return at their
-  // first try, and all roles run to their ends with whatever is there.
+  // Every wait on another role is bounded; once one has given up the others
+  // return at their first try.  The loads and the products then end there, the
+  // softmax (whose warps meet at barriers of their own) runs to its end with
+  // whatever is there.
   auto wait = [&](unsigned long long& b, uint32_t parity) {
-    if (!mbar_wait(smem_u32(&b), parity & 1u, LIN_WAIT_TRIES, abort_flag)) *abort_flag = 1;
+    const bool ok = mbar_wait(smem_u32(&b), parity & 1u, LIN_WAIT_TRIES, abort_flag);
+    if (!ok) *abort_flag = 1;
+    return ok;
   };
   // Buffers and turns of K and V of the CTA's tile x.  Each has a ring of its
   // own: a barrier tells a phase from the next one only, and as the streams
@@ -332,7 +336,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       }
       return x;
     };
-    for (long long left = my_tiles; left > 0; left -= n, off += n, tile0 += n, seg++) {
+    bool go = true;
+    for (long long left = my_tiles; left > 0 && go; left -= n, off += n, tile0 += n, seg++) {
       next_piece(left);
       // the rows of the next tile are looked up while this one waits for its buffer
       Rows next = lookup(t0);
@@ -342,7 +347,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         const uint32_t slot = item.slot, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
         const Rows x = next;
         if (i + 1 < n) next = lookup(t + 1);
-        wait(sh.empty[slot], item.turn + 1);
+        go = __all_sync(0xffffffffu, wait(sh.empty[slot], item.turn + 1));
+        if (!go) break;
         if (t == q.tiles - 1) {
           const __half* src = fresh + (int64_t)s * a.nt * a.kv_stride + kvh * HD;
 #pragma unroll 4
@@ -403,15 +409,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       const uint64_t d_k = smem_desc_sw128(sm0 + Sh::RING_OFF), d_v = smem_desc_mn(sm0 + Sh::RING_OFF, Sh::SUB);
       const uint32_t tS = tmem + j * 128, tO = tmem + 256 + j * 128;
       uint32_t n_p = 0;  // the stream's tiles so far
+      // Whether the products go on, by what this lane has waited for: once a
+      // wait has given up nothing is issued any more, while the turns below are
+      // still handed over.
+      bool go = true;
       auto wait_item = [&](const Item& item) {
-        wait(sh.full[item.slot], item.turn);
+        go = wait(sh.full[item.slot], item.turn) && go;
         __syncwarp();
         fence_proxy_async();  // the copies, to the tensor core's proxy
       };
       auto scores = [&](const Item& item) {
         wait_item(item);
         const uint64_t dk = d_k + item.slot * (uint32_t)(Sh::TILE >> 4);
-        if (elect_one()) {
+        if (elect_one() && go) {
 #pragma unroll
           for (int kk = 0; kk < HD / 16; kk++) {
             const uint32_t o = ((kk >> 2) * Sh::SUB + (kk & 3) * 32) >> 4;
@@ -436,7 +446,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         const int step = TWO ? 1 : 2;
         int i = TWO ? 0 : j;
         if (seg > 0) take_over(PIECE);
-        wait(sh.q_full, seg);  // (without a tile, too: a phase each piece)
+        go = wait(sh.q_full, seg) && go;  // (without a tile, too: a phase each piece)
+        __syncwarp();
         if (i >= n) continue;
         if (j == 1) take_over(START_0_1);
         scores(item_k(tile0 + i));
@@ -445,11 +456,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           const Item vi = item_v(tile0 + i);
           const uint64_t dv = d_v + vi.slot * (uint32_t)(Sh::TILE >> 4);
           wait_item(vi);
-          wait(sh.p_ready[j], n_p++);
+          go = wait(sh.p_ready[j], n_p++) && go;
           __syncwarp();
           tc_fence_after();
           if (j == 1 || i > 0) take_over(j == 1 ? TURN_0_1 : TURN_1_0);
-          if (elect_one()) {
+          if (elect_one() && go) {
 #pragma unroll 1  // (sixteen in a row take registers that this warp does not have)
             for (int lo = 0; lo <= P_LO; lo += P_LO)
 #pragma unroll
@@ -463,9 +474,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           if (TWO ? j == 0 || i + 1 < n : i + 1 < n) hand_over(j == 0 ? TURN_0_1 : TURN_1_0);
         }
       }
+      // the products that were issued have ended before this CTA's memory is
+      // another's: with the full budget, whether a wait has given up or not
       if (elect_one()) tc_commit(bar(sh.drain[j]));
       __syncwarp();
-      wait(sh.drain[j], 0);
+      if (!mbar_wait(bar(sh.drain[j]), 0u, LIN_WAIT_TRIES)) *abort_flag = 1;
     }
     __syncwarp();
   } else {
@@ -539,7 +552,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       float mx = -INFINITY, sum = 0.0f;
       for (int c = 0; c < nj; c++) {
         const int i = TWO ? c : 2 * c + j, t = t0 + i;
-        wait(sh.s_full[j], n_s++);
+        if (!mbar_wait(bar(sh.s_full[j]), n_s & 1u, n_s == 0 ? a.wait_tries : LIN_WAIT_TRIES, abort_flag)) *abort_flag = 1;
+        n_s++;
         __syncwarp();
         tc_fence_after();
         if (warp_live) {
@@ -791,6 +805,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
         }
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();

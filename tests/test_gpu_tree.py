@@ -630,3 +630,40 @@ def test_keys_far_below_a_dominant_one(dev, nt, window, sinks):
         first = c.table[c.slots[0], 0]
         c.k[0, first, 0, 0], c.v[0, first, 0, 0] = nats / np.sqrt(hd), 0.0
         check_tight(c, c.call(), WEIGHT_FLOOR)
+
+
+# ---------------------------------------------------------------------------
+# waits that give up
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("nq,nkv,hd,lens,nt", [(32, 8, 128, [900, 0, 37, 400, 5], 16), (40, 8, 128, [600, 0, 1, 200, 9], 16),
+                                               (8, 2, 64, [700, 0, 130, 65, 20000], 63), (16, 2, 64, [40, 0, 300, 9, 128], 12),
+                                               (6, 1, 128, [30000, 0, 2, 70, 7], 64)])
+def test_a_wait_that_gives_up_fails_closed(dev, nq, nkv, hd, lens, nt):
+    """Every CTA's first wait given up at once: the call ends, the sequences
+    with nodes are NaN with SPEC_ST_TIMEOUT beside a status of their own, rows
+    of no node stay; with the budget restored the next calls are right, bit by
+    bit as before."""
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng([47, nq, nt])
+    c = Case(sv, dev, g, nq, nkv, hd, lens, nt, 32, window=0, sinks=0, counts=[nt, nt, nt - 1, 0, 5])
+    c.slots[2] = 77
+    c.v[c.layer, c.table[c.slots[0], 0]] = np.inf  # (behind a masked tile's marks, too: a window)
+    good = c.call()
+    assert c.status.tolist() == [0, 0, tree.ST_SLOT, 0, 0]
+    try:
+        for window in (0, 20, 0):
+            sv.spec_tree_set_wait_budget(0)
+            c.window, c.sinks = window, window // 5
+            got = c.call()
+            assert c.status.tolist() == [sv.SPEC_ST_TIMEOUT] * 2 + [tree.ST_SLOT, 0, sv.SPEC_ST_TIMEOUT]
+            for b, m in enumerate(c.counts):
+                assert np.isnan(got[b, :m]).all() and (got[b, m:] == 7.0).all(), b
+            c.window = c.sinks = 0
+            sv.spec_tree_set_wait_budget(131072)
+            assert np.array_equal(c.call().view(np.uint16), good.view(np.uint16))
+            assert c.status.tolist() == [0, 0, tree.ST_SLOT, 0, 0]
+        for bad in (-1, 131073):
+            with pytest.raises(sv.SpecError):
+                sv.spec_tree_set_wait_budget(bad)
+    finally:
+        sv.spec_tree_set_wait_budget(131072)
