@@ -253,7 +253,8 @@ __device__ __forceinline__ void check_sequence(const TreeArgs& a, int s, int row
     if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_PAGE;
   }
   if (lane == 0) {
-    a.plan[s].nodes = (st & SPEC_ST_TREE) || a.n_nodes == nullptr ? a.nt : a.n_nodes[s];
+    const int m = a.n_nodes != nullptr ? a.n_nodes[s] : a.nt;
+    a.plan[s].nodes = m < 0 || m > a.nt ? a.nt : m;  // (q.m is 0 for a sequence in error)
     a.plan[s].status = st;
     a.status[s] = st;
   }

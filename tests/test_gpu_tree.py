@@ -320,6 +320,25 @@ def test_refused_sequences(dev):
     assert c.status.tolist()[3] == tree.ST_PAGE and np.isnan(got[3]).all()
 
 
+@pytest.mark.parametrize("nq,nkv,nt", [(8, 2, 6), (8, 1, 12)])
+def test_rows_behind_a_refused_sequence_stay(dev, nq, nkv, nt):
+    """Whatever a sequence is refused for, only its first n_nodes rows are NaN;
+    all of them if the count is what is wrong."""
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(12)
+    c = Case(sv, dev, g, nq, nkv, 64, [100, 90, 80, 70, 60, 50, 0], nt, 16, counts=[4, 3, 4, 4, nt + 1, -1, 2])
+    c.parents[0, 3] = 3              # a node that is its own parent
+    c.slots[1] = -1
+    c.table[c.slots[2], 1] = -3
+    c.parents[3, 2], c.table[c.slots[3], 0] = -2, 10 ** 6
+    c.parents[6, 1] = 1
+    got = c.call()
+    assert c.status.tolist() == [tree.ST_TREE, tree.ST_SLOT, tree.ST_PAGE, tree.ST_TREE | tree.ST_PAGE, tree.ST_TREE,
+                                 tree.ST_TREE, tree.ST_TREE]
+    for b, m in enumerate([4, 3, 4, 4, nt, nt, 2]):
+        assert np.isnan(got[b, :m]).all() and (got[b, m:] == 7.0).all(), b
+
+
 def test_graph_replay_and_two_streams(dev):
     """A captured call replayed over new lengths, trees and rows; and two calls
     at once on two streams, each with a workspace of its own."""
