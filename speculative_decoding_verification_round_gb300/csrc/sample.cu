@@ -458,6 +458,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, cg::cluster_grou
   }
   top = __shfl_sync(0xffffffffu, top, 0);
   row.zmax = row_zmax(max_key(top), row.T);
+  row.plain |= Row::far(row.zmax);
   bad |= !(fabsf(top) < INFINITY) || !(fabsf(row.zmax) < INFINITY);  // NaN, +inf, nothing but -inf
   float* frow = a.filtered != nullptr ? a.filtered + (int64_t)r * a.ldf + seg.id0 : nullptr;
   if (bad) {  // the whole cluster

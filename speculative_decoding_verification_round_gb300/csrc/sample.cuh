@@ -125,7 +125,7 @@ __device__ __forceinline__ u64 widen(uint32_t w) { return (u64)w + (w == 0xFFFFF
 // One row's state in registers of every thread.
 struct Row {
   float T, inv_T, zmax;
-  bool plain;  // divide by the division: T is 1 or far from it
+  bool plain;  // divide by the division: T is 1 or far from it, or a quotient may be at the end of the range
   float least;  // tokens above it stay; those equal to it with ids up to last_id
   int last_id;
   uint32_t min_w;  // of those, the ones of at least this weight (2^32 as 2^32 - 1)
@@ -140,7 +140,11 @@ struct Row {
   // is then the correctly rounded quotient (Markstein, "Computation of
   // elementary functions on the IBM RISC System/6000 processor", 1990).  Five
   // packed operations for two logits.  Where l / T overflows below, x is NaN,
-  // which is taken as a weight of 0 and the last step.
+  // which is taken as a weight of 0 and the last step.  l y may overflow where
+  // l / T is within two units of the largest float, so rows whose largest z is
+  // far are divided by the division; in the others such a z lies so far below
+  // the largest that its weight is 0 and its step the last all the same.
+  static __device__ __forceinline__ bool far(float z) { return fabsf(z) > 0x1p126f; }
   __device__ __forceinline__ float2 x2(float2 l) const {
     float2 z;
     if (plain) {

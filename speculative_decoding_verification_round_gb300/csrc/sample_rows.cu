@@ -302,6 +302,7 @@ sr_bound_kernel(const SampleArgs a, const Spaces sp) {
   const bool finite = top > NONE && top < 0xFF800000u;  // below +infinity and NaN
   st.top = finite ? key_value(top) : 0.0f;
   row.zmax = row_zmax(max_key(st.top), row.T);
+  row.plain |= Row::far(row.zmax);
   bad |= !finite || !(fabsf(row.zmax) < INFINITY);
   const bool by_k = st.k > 0 && st.k < a.V;
   st.bound = -INFINITY;

@@ -135,6 +135,36 @@ def test_refused_rows(orc, dev):
         assert (tok[r], kept[r]) == (ref, len(ids)) and np.isfinite(filt[r]).all()
 
 
+def test_quotients_at_the_end_of_the_range(orc, dev):
+    """Largest logits whose l / T is finite by a unit or two in the last place
+    while l (1 / T) overflows; few rows and many."""
+    g = np.random.default_rng(15)
+    ends = []
+    with np.errstate(over="ignore"):
+        for T in g.uniform(0.05, 0.999, 400).astype(np.float32):
+            l = np.float32(np.finfo(np.float32).max * T)
+            for _ in range(6):
+                if np.isfinite(l / T) and not np.isfinite(l * (np.float32(1) / T)):
+                    ends.append((T, l))
+                l = np.nextafter(l, np.float32(0))
+    ends = ends[:24]
+    assert len(ends) == 24
+    for V, R in ((500, 24), (100003, 24)):
+        logits = g.standard_normal((R, V)).astype(np.float32)
+        for r, (T, l) in enumerate(ends):
+            at = g.permutation(V)[:9]
+            logits[r, at[:5]] = l
+            logits[r, at[5]] = np.nextafter(l, np.float32(0))
+            logits[r, at[6:]] = -l
+            if r % 6 == 5:  # everything at the other end
+                logits[r] = -l
+        T = np.array([t for t, _ in ends])
+        kinds = np.arange(R) % 4
+        check(orc, dev, logits, g.integers(0, 2 ** 32, R, dtype=np.uint64), T,
+              np.where(kinds == 1, 3, 0).astype(np.int32), np.where(kinds >= 2, 0.6, 1.0).astype(np.float32),
+              np.where(kinds == 3, 0.01, 0.0).astype(np.float32))
+
+
 def test_in_place_without_outputs_on_a_stream_and_replayed(orc, dev):
     import torch
     import speculative_decoding_verification_round_gb300 as sv
