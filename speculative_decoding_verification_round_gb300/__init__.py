@@ -195,24 +195,38 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-_current_raw_stream = None  # torch's current stream as an address
+_cuda_device = _cuda_raw_stream = None  # torch's current device, and its stream there as an address
+
+
+def _init_cuda():
+    global _cuda_device, _cuda_raw_stream
+    import torch
+    torch.cuda.current_stream()  # (initialises CUDA)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _cuda_raw_stream = raw or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(stream):
+    """The current device, and a stream as an address (None: torch's current one)."""
+    if _cuda_device is None:
+        _init_cuda()
+    d = _cuda_device()
+    return d, _cuda_raw_stream(d) if stream is None else stream.cuda_stream
 
 
 def _stream(stream):
-    """A stream as an address (None: torch's current one)."""
-    if stream is not None:
-        return stream.cuda_stream
-    global _current_raw_stream
-    if _current_raw_stream is None:
-        import torch
-        c = torch._C
-        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
-            torch.cuda.current_stream()  # (initialises CUDA)
-            raw, device = c._cuda_getCurrentRawStream, c._cuda_getDevice
-            _current_raw_stream = lambda: raw(device())  # noqa: E731
-        else:
-            _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-    return _current_raw_stream()
+    return _here(None)[1] if stream is None else stream.cuda_stream
+
+
+def _dev(t, device: int):
+    """A tensor's address for a kernel on `device`: it has to be there, or in
+    pinned host memory."""
+    if t is None:
+        return None
+    if t.get_device() != device and (t.is_cuda or not t.is_pinned()):
+        raise ValueError(f"a tensor on {t.device}: the current device's (or pinned host memory) is required")
+    return t.data_ptr()
 
 
 def _qweight(w: dict) -> spec_qweight:
@@ -531,6 +545,12 @@ class KVPages:
 
     def __init__(self, k, v, table=None, lens=None, refs=None):
         n_layers, n_pages, n_kv_heads, page_size, head_dim = k.shape
+        self.device = k.get_device()  # of a call; -1: any
+        for t, name in ((v, "v"), (table, "table"), (lens, "lens"), (refs, "refs")):
+            if t is not None and t.get_device() != self.device:
+                raise ValueError(f"{name}: a tensor on {t.device} beside a cache on {k.device}")
+        if not all(t is None or t.is_cuda or t.is_pinned() for t in (k, v, table, lens, refs)):
+            self.device = -2  # no kernel can read them
         for t, name in ((k, "k"), (v, "v")):
             if tuple(t.shape) != tuple(k.shape) or t.element_size() != 2 or not t[0].is_contiguous() or (
                     t.is_floating_point() and str(t.dtype) != "torch.float16"):
@@ -552,11 +572,19 @@ class KVPages:
                                 None if lens is None else lens.data_ptr())
         self.ref = ctypes.byref(self.pages)
 
+    def at(self, device: int):
+        """The struct for a call on `device`."""
+        if self.device != device and self.device != -1:
+            raise ValueError("pages on another device than the current one" if self.device >= 0 else
+                             "pages in host memory that is not pinned")
+        return self.ref
+
     @classmethod
     def of_model(cls, m: Model) -> "KVPages":
         """The model's own slot cache (spec_model_pages): page id = slot."""
         self = cls.__new__(cls)
         self._keep = (m,)
+        self.device = -1  # (the model's; not known here)
         self.pages = spec_pages()
         self.ref = ctypes.byref(self.pages)
         _check(lib().spec_model_pages(m.handle, self.ref))
@@ -569,33 +597,38 @@ def spec_model_pages(m: Model) -> KVPages:
 
 def spec_pages_copy(kv: KVPages, n: int, src, dst, status, n_pos=None, stream=None):
     """Page src[i] to page dst[i], all layers; n_pos: only its first positions."""
-    _check(lib().spec_pages_copy(kv.ref, int(n), _ptr(src), _ptr(dst), _ptr(n_pos), _ptr(status),
-                                 _stream(stream)))
+    d, st = _here(stream)
+    _check(lib().spec_pages_copy(kv.at(d), int(n), _dev(src, d), _dev(dst, d), _dev(n_pos, d), _dev(status, d),
+                                 st))
 
 
 def spec_pages_fork(kv: KVPages, n: int, src, dst, status, stream=None):
     """Slot dst[i] becomes a branch of slot src[i], sharing its pages."""
-    _check(lib().spec_pages_fork(kv.ref, int(n), _ptr(src), _ptr(dst), _ptr(status), _stream(stream)))
+    d, st = _here(stream)
+    _check(lib().spec_pages_fork(kv.at(d), int(n), _dev(src, d), _dev(dst, d), _dev(status, d), st))
 
 
 def spec_pages_extend(kv: KVPages, n: int, slots, n_new, copies, status, stream=None):
     """Room for n_new[i] more positions of slot slots[i] (copy on write)."""
-    _check(lib().spec_pages_extend(kv.ref, int(n), _ptr(slots), _ptr(n_new), _ptr(copies),
-                                   _ptr(status), _stream(stream)))
+    d, st = _here(stream)
+    _check(lib().spec_pages_extend(kv.at(d), int(n), _dev(slots, d), _dev(n_new, d), _dev(copies, d),
+                                   _dev(status, d), st))
 
 
 def spec_pages_commit(kv: KVPages, n: int, slots, nt: int, k_new, v_new, path, n_path, status,
                       new_len=None, new_layer_stride: int = 0, stream=None):
     """Rows path[i][:n_path[i]] of k_new / v_new [n_layers][n][nt][n_kv_heads]
     [head_dim] behind the committed positions of slot slots[i], all layers."""
-    _check(lib().spec_pages_commit(kv.ref, int(n), _ptr(slots), int(nt), _ptr(k_new), _ptr(v_new),
-                                   int(new_layer_stride), _ptr(path), _ptr(n_path), _ptr(new_len),
-                                   _ptr(status), _stream(stream)))
+    d, st = _here(stream)
+    _check(lib().spec_pages_commit(kv.at(d), int(n), _dev(slots, d), int(nt), _dev(k_new, d), _dev(v_new, d),
+                                   int(new_layer_stride), _dev(path, d), _dev(n_path, d), _dev(new_len, d),
+                                   _dev(status, d), st))
 
 
 def spec_pages_free(kv: KVPages, n: int, slots, status, stream=None):
     """Gives back every page of the slots."""
-    _check(lib().spec_pages_free(kv.ref, int(n), _ptr(slots), _ptr(status), _stream(stream)))
+    d, st = _here(stream)
+    _check(lib().spec_pages_free(kv.at(d), int(n), _dev(slots, d), _dev(status, d), st))
 
 
 def spec_tree_attn_workspace(kv: KVPages, n_seq: int, nt: int, n_q_heads: int) -> int:
@@ -612,13 +645,12 @@ def spec_tree_attn(kv: KVPages, layer: int, n_seq: int, slots, nt: int, n_q_head
                    stream=None):
     """Attention of n_seq trees of up to nt nodes over the pages of `layer`
     and over their own nodes (rules in include/spec_verify.h)."""
-    t = spec_tree(n_seq, nt, n_q_heads, window, sinks, scale, slots.data_ptr(),
-                  None if parents is None else parents.data_ptr(),
-                  None if n_nodes is None else n_nodes.data_ptr())
-    _check(lib().spec_tree_attn(kv.ref, int(layer), ctypes.byref(t), _ptr(q), int(q_stride),
-                                _ptr(k_new), _ptr(v_new), int(kv_stride), _ptr(out),
-                                _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                _ptr(status), _stream(stream)))
+    d, st = _here(stream)
+    t = spec_tree(n_seq, nt, n_q_heads, window, sinks, scale, _dev(slots, d), _dev(parents, d), _dev(n_nodes, d))
+    _check(lib().spec_tree_attn(kv.at(d), int(layer), ctypes.byref(t), _dev(q, d), int(q_stride),
+                                _dev(k_new, d), _dev(v_new, d), int(kv_stride), _dev(out, d),
+                                _dev(workspace, d), workspace.numel() * workspace.element_size(),
+                                _dev(status, d), st))
 
 
 def spec_tree_set_wait_budget(tries: int):
@@ -630,9 +662,10 @@ def spec_tree_set_wait_budget(tries: int):
 def spec_accept_tree(argmax, tokens, parents, n_nodes, n_seq: int, nt: int, path, n_path, emitted,
                      stream=None):
     """Greedy acceptance along the trees; n_nodes None: nt each."""
-    _check(lib().spec_accept_tree(_ptr(argmax), _ptr(tokens), _ptr(parents), _ptr(n_nodes),
-                                  int(n_seq), int(nt), _ptr(path), _ptr(n_path), _ptr(emitted),
-                                  _stream(stream)))
+    d, st = _here(stream)
+    _check(lib().spec_accept_tree(_dev(argmax, d), _dev(tokens, d), _dev(parents, d), _dev(n_nodes, d),
+                                  int(n_seq), int(nt), _dev(path, d), _dev(n_path, d), _dev(emitted, d),
+                                  st))
 
 
 def spec_sample_workspace(R: int, V: int) -> int:
@@ -649,6 +682,8 @@ def spec_sample(logits, R: int, V: int, u, token, temperature=None, top_k=None, 
     top-p and min-p; filtered: the logits that stayed (SPEC_FILTERED elsewhere).
     workspace: a tensor of spec_sample_workspace bytes (None: taken from
     torch's allocator for the call where one is needed)."""
+    d, st = _here(stream)
+    at = _dev(logits, d)
     n = 0
     if workspace is not None:
         n = workspace.numel() * workspace.element_size()
@@ -659,7 +694,7 @@ def spec_sample(logits, R: int, V: int, u, token, temperature=None, top_k=None, 
             import torch
             # (of the allocator's pool of the call's stream: behind that stream's work only)
             with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-                workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
-    _check(lib().spec_sample(_ptr(logits), int(R), int(V), int(ld), _ptr(u), _ptr(temperature),
-                             _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(n_kept),
-                             _ptr(filtered), int(ld_filtered), _ptr(workspace), n, _stream(stream)))
+                workspace = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", d))
+    _check(lib().spec_sample(at, int(R), int(V), int(ld), _dev(u, d), _dev(temperature, d),
+                             _dev(top_k, d), _dev(top_p, d), _dev(min_p, d), _dev(token, d), _dev(n_kept, d),
+                             _dev(filtered, d), int(ld_filtered), _dev(workspace, d), n, st))

@@ -261,3 +261,72 @@ def test_pages_of_other_tensors_are_refused():
         args = dict(table=torch.zeros((3, 2), dtype=torch.int32), lens=torch.zeros(3, dtype=torch.int32))
         with pytest.raises(ValueError):
             sv.KVPages(ok, ok.clone(), **{**args, **kw})
+
+
+def test_tensors_that_a_kernel_cannot_read_are_refused(sv, monkeypatch):
+    """Host tensors, and tensors of another device than the current one, in
+    every call of the drafted-tree operators and in KVPages: refused in front
+    of the library."""
+    import torch
+    host = lambda *shape: torch.zeros(shape, dtype=torch.int32)  # noqa: E731
+    cache = torch.zeros((1, 4, 1, 8, 64), dtype=torch.float16)
+    on_host = sv.KVPages(cache, cache, host(3, 2), host(3), host(4))
+
+    class Device:  # a tensor of device 0, as far as the binding looks
+        is_cuda = True
+        device = "cuda:0"
+
+        def __init__(self, t, index=0):
+            self.t, self.index, self.shape, self.dtype = t, index, t.shape, t.dtype
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def __getitem__(self, i):
+            return self.t[i]
+
+        def get_device(self):
+            return self.index
+
+        def data_ptr(self):
+            return A
+    on0 = lambda *shape: Device(host(*shape))  # noqa: E731
+    kv = sv.KVPages(Device(cache), Device(cache), on0(3, 2), on0(3), on0(4))
+    for other in (host(3), Device(host(3), 1)):
+        with pytest.raises(ValueError):
+            sv.KVPages(Device(cache), Device(cache), on0(3, 2), other, on0(4))
+    half = Device(torch.zeros(4096, dtype=torch.float16))
+    n = on0(1)
+    calls = {  # the arguments that are tensors, by name
+        sv.spec_pages_copy: (dict(kv=kv, n=1), dict(src=n, dst=n, status=n, n_pos=n)),
+        sv.spec_pages_fork: (dict(kv=kv, n=1), dict(src=n, dst=n, status=n)),
+        sv.spec_pages_extend: (dict(kv=kv, n=1), dict(slots=n, n_new=n, copies=n, status=n)),
+        sv.spec_pages_commit: (dict(kv=kv, n=1, nt=1), dict(slots=n, k_new=half, v_new=half, path=n, n_path=n, status=n,
+                                                         new_len=n)),
+        sv.spec_pages_free: (dict(kv=kv, n=1), dict(slots=n, status=n)),
+        sv.spec_tree_attn: (dict(kv=kv, layer=0, n_seq=1, nt=1, n_q_heads=1),
+                            dict(slots=n, q=half, k_new=half, v_new=half, out=half, workspace=half, status=n, parents=n,
+                                 n_nodes=n)),
+        sv.spec_accept_tree: (dict(n_seq=1, nt=1), dict(argmax=n, tokens=n, parents=n, n_nodes=n, path=n, n_path=n,
+                                                        emitted=n)),
+        sv.spec_sample: (dict(R=1, V=8), dict(logits=half, u=n, token=n, temperature=half, top_k=n, top_p=half, min_p=half,
+                                              n_kept=n, filtered=half, workspace=half)),
+    }
+    here = lambda d: monkeypatch.setattr(sv, "_here", lambda stream: (d, None))  # noqa: E731
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: pytest.fail("a refused call reached the library")
+    monkeypatch.setattr(sv, "lib", Library)
+    for call, (plain, tensors) in calls.items():
+        for name, good in tensors.items():
+            for bad in (good.t, Device(good.t, 1)):
+                here(0)
+                with pytest.raises(ValueError):
+                    call(**plain, **{**tensors, name: bad})
+        if "kv" in plain:
+            with pytest.raises(ValueError):
+                call(**{**plain, "kv": on_host}, **tensors)
+        here(1)  # everything on device 0, device 1 current
+        with pytest.raises(ValueError):
+            call(**plain, **tensors)
