@@ -584,7 +584,7 @@ typedef struct {
  *          SPEC_ST_TIMEOUT
  * out and workspace overlap none of the inputs, nor each other.
  * The scores' statistics and sums are fp32, and the weights are multiplied as
- * pairs of fp16 numbers (2^-21 of a weight, 2^-36 of the row's largest), for any
+ * pairs of fp16 numbers (2^-20 of a weight, 2^-36 of the row's largest), for any
  * number of rows.  The same call gives the same bits; which bits may depend on the other sequences of the call (the work
  * is cut evenly over the SMs), unlike spec_verify_attn, whose rows do not
  * depend on the batch. */

@@ -87,8 +87,8 @@ __device__ __forceinline__ uint32_t tile_off(int r, int u) {
 constexpr int resident(int hd, int rows) { return hd == 64 && rows == 16 ? 4 : 2; }
 
 // Factor of weights and sums: a weight w, at most 1, goes to the MMA as a pair
-// of fp16 numbers, which holds all of it but 2^-22 w + 2^-40 with the factor and
-// all but 2^-22 w + 2^-25 without (16 nats below a row's largest, 6% off).
+// of fp16 numbers, which holds all of it but 2^-20 w + 2^-39 with the factor and
+// all but 2^-20 w + 2^-24 without (16 nats below a row's largest, 6% off).
 constexpr float P_FACTOR = 32768.0f;
 
 template <int HD, int MT>
@@ -380,9 +380,9 @@ __global__ void __launch_bounds__(TT_THREADS, Shape<HD, MT>::RESIDENT) tree_attn
 #pragma unroll
             for (int h = 0; h < 2; h++) {
               const float p0 = sc[i][2 * kk + n][2 * h], p1 = sc[i][2 * kk + n][2 * h + 1];
-              hi[i][2 * n + h] = pack_f16(p0, p1);
-              const float2 f = unpack_f16(hi[i][2 * n + h]);
-              lo[i][2 * n + h] = pack_f16(p0 - f.x, p1 - f.y);
+              const float c0 = __uint_as_float(__float_as_uint(p0) & P_CUT), c1 = __uint_as_float(__float_as_uint(p1) & P_CUT);
+              hi[i][2 * n + h] = pack_f16(c0, c1);
+              lo[i][2 * n + h] = pack_f16(fmaf(c0, -P_REST, p0), fmaf(c1, -P_REST, p1));
             }
 #pragma unroll
         for (int d = 0; d < HD / 8; d += 2) {

@@ -363,6 +363,14 @@ struct TreeSmem {
   signed char par[SPEC_MAX_TREE];
 };
 
+// A weight goes to the MMA as hi + lo: hi is the weight cut off behind its 11th
+// bit (w & P_CUT), lo = w - P_REST hi the rest and 2^-22 of hi more, so that neither is
+// ever negative, and lo not 0 beside a hi that is not (down to 2^-3, where fp16
+// ends): a value that is infinite stays so, where inf * 0 or inf - inf would be
+// a NaN.
+constexpr uint32_t P_CUT = 0xFFFFE000u;
+constexpr float P_REST = 1.0f - 0x1p-22f;
+
 // Every thread of the CTA; returns whether the parents make a tree.
 __device__ __forceinline__ bool load_tree(const TreeArgs& a, int s, int m, TreeSmem& t) {
   const int i = threadIdx.x;

@@ -28,7 +28,7 @@
 // the last time (the weights may exceed 1 until then), so the accumulator in
 // tensor memory is hardly ever touched by the softmax.  2^12 is multiplied into
 // weights and sum alike, which keeps them below 2^15 and, with it, inside
-// fp16's range: of a weight w the pair holds all but 2^-21 w + 2^-36, so that
+// fp16's range: of a weight w the pair holds all but 2^-20 w + 2^-36, so that
 // keys far below a row's largest are there, too (of n keys 20 nats below it, a
 // sum n e^-20 in front of the rounding of the output).  One fp16 number would
 // leave out 2^-11 w, as much again as the rounding of the output.
@@ -622,9 +622,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
                 const float2 y = fma2(make_float2(__uint_as_float(v[b][e]), __uint_as_float(v[b][e + 1])), sc2, sh2);
                 const float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
                 l[(e >> 1) & 1] = add2(l[(e >> 1) & 1], p);
-                const float2 cut = make_float2(__uint_as_float(__float_as_uint(p.x) & 0xFFFFE000u),
-                                               __uint_as_float(__float_as_uint(p.y) & 0xFFFFE000u));
-                const float2 rest = fma2(cut, make_float2(-1.0f, -1.0f), p);
+                const float2 cut = make_float2(__uint_as_float(__float_as_uint(p.x) & P_CUT),
+                                               __uint_as_float(__float_as_uint(p.y) & P_CUT));
+                const float2 rest = fma2(cut, make_float2(-P_REST, -P_REST), p);
                 hi[(e - e0) >> 1] = pack_f16(cut.x, cut.y);
                 lo[(e - e0) >> 1] = pack_f16(rest.x, rest.y);
               }

@@ -585,9 +585,10 @@ def test_rounds_of_a_tree_drafting_decoder(orc, dev):
 def check_tight(c, got, floor):
     """As Case.check, without a rounding of the weights to fp16 for any number
     of rows.  Weights, relative to themselves: the split into two fp16 numbers
-    2^-21 (hi cut off behind 11 bits, lo rounded to half a step of its own),
-    exp2 2^-22, the rounding of its argument, up to 16 in magnitude where a
-    weight counts, 2^-21: together less than 2^-19.  Relative to the row's
+    2^-21 (hi cut off behind 11 bits, lo rounded to half a step of its own) and
+    2^-22 (that much of hi more in lo), exp2 2^-22, the rounding of its
+    argument, up to 16 in magnitude where a weight counts, 2^-21: together less
+    than 2^-19.  Relative to the row's
     largest weight, 1: `floor`, where hi and lo leave fp16's normal numbers.
     Plus the scores' error and fp32 sums as there."""
     for b in range(c.n):
@@ -649,6 +650,23 @@ def test_keys_far_below_a_dominant_one(dev, nt, window, sinks):
         first = c.table[c.slots[0], 0]
         c.k[0, first, 0, 0], c.v[0, first, 0, 0] = nats / np.sqrt(hd), 0.0
         check_tight(c, c.call(), WEIGHT_FLOOR)
+
+
+@pytest.mark.parametrize("nq,nkv,hd,nt", [(4, 2, 64, 3), (8, 1, 128, 4), (8, 2, 128, 16), (8, 2, 64, 32), (4, 1, 128, 64)])
+def test_infinite_values_that_are_seen(dev, nq, nkv, hd, nt):
+    """Infinities in V at positions that every row sees: infinite outputs of
+    their sign, NaN where both signs meet or a NaN is, and nothing elsewhere."""
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng([53, nt])
+    c = Case(sv, dev, g, nq, nkv, hd, [600, 140], nt, 32)
+    clean = c.call()
+    for b in range(2):
+        for p, d, x in ((3, 0, np.inf), (100, 1, -np.inf), (40, 2, np.inf), (90, 2, -np.inf), (7, 3, np.nan), (20, 4, np.inf),
+                        (127, 4, np.inf)):
+            c.v[c.layer, c.table[c.slots[b], p // 32], :, p % 32, d] = x
+    got = c.call()
+    assert (got[..., [0, 4]] == np.inf).all() and (got[..., 1] == -np.inf).all() and np.isnan(got[..., 2:4]).all()
+    assert np.array_equal(got[..., 5:].view(np.uint16), clean[..., 5:].view(np.uint16))
 
 
 # ---------------------------------------------------------------------------
