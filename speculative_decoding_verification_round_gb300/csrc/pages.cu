@@ -409,10 +409,10 @@ pages_free_kernel(const spec_pages kv, int n, const int32_t* __restrict__ slots,
     bool bad = false;
     for (int j = threadIdx.x; j < kv.max_pages; j += PG_THREADS) {
       const int p = row[j];
-      if (p >= kv.n_pages)
-        bad = true;
-      else if (p >= 0)
+      if (p >= 0 && p < kv.n_pages)
         atomicSub(kv.refs + p, 1);
+      else if (p != -1)
+        bad = true;
       if (p != -1) row[j] = -1;
     }
     if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;

@@ -264,6 +264,21 @@ def test_refused_entries_change_nothing(dev):
     assert torch.equal(p.table[3].cpu(), torch.full((4,), -1, dtype=torch.int32))
 
 
+def test_ids_below_minus_one_are_out_of_range_too(dev):
+    """A slot whose row holds one is emptied, and told."""
+    import speculative_decoding_verification_round_gb300 as sv
+    p = Pool(sv, dev, 3, 4, 16, 4)
+    p.extend([0, 1], [9, 9])
+    p.commit([0, 1], [[0] * 9] * 2, [9, 9], 9)
+    held = p.book.table[1][1]
+    p.table[1, 1] = -2
+    st = p.i32([77, 77, 77])
+    sv.spec_pages_free(p.kv, 3, p.i32([0, 1, 2]), st)
+    assert st.tolist() == [0, tree.ST_PAGE, 0]
+    assert (p.table == -1).all() and not p.lens.any()
+    assert p.refs.tolist() == [int(i == held) for i in range(16)]  # the page whose id was lost stays taken
+
+
 @pytest.mark.parametrize("page,hd,nkv,layers", [(4, 64, 2, 3), (300, 128, 8, 2), (1, 8, 1, 1)])
 def test_copies(dev, page, hd, nkv, layers):
     """Whole pages and prefixes of them (of zero positions too), a page larger
