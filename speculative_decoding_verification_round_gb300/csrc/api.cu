@@ -73,7 +73,7 @@ bool programmatic_launch() {
   return on;
 }
 
-static int sm_count() {
+int device_sms() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
@@ -187,7 +187,7 @@ extern "C" int spec_qmat_create(const spec_qweight* w, int max_rows, void* strea
   init_attrs_once();
   cudaStream_t st = as_stream(stream);
   spec_qmat* m = new spec_qmat();
-  int rc = qmat_pack(w, PERM_IDENTITY, 0, sm_count(), st, &m->w);
+  int rc = qmat_pack(w, PERM_IDENTITY, 0, device_sms(), st, &m->w);
   if (rc != SPEC_OK) {
     delete m;
     return rc;
@@ -410,7 +410,7 @@ extern "C" int spec_model_create(const spec_model_desc* desc, const spec_model_w
   spec_model* m = new spec_model();
   m->d = *desc;
   cudaGetDevice(&m->device);
-  m->sms = sm_count();
+  m->sms = device_sms();
   const spec_model_desc& D = m->d;
   const int L = D.n_layers, H = D.hidden, V = D.vocab, hd = D.head_dim, nq = D.n_q_heads,
             nkv = D.n_kv_heads, F = D.ffn;

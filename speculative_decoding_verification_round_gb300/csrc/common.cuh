@@ -270,6 +270,9 @@ int launch_sample(const float* logits, int R, int V, int64_t ld, const uint32_t*
 size_t sample_bytes(int R, int V);
 void tree_set_wait_budget(int tries);
 
+// SMs of the current device.
+int device_sms();
+
 // Whether kernels that can overlap their predecessor's tail are launched as
 // programmatic dependents (default on; SPEC_VERIFY_PDL=0 in the environment
 // turns it off).

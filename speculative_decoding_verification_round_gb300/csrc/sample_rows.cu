@@ -830,10 +830,10 @@ int sample_rows_launch(SampleArgs a, void* workspace, cudaStream_t st) {
   const int segs = (a.V + SR_SEG - 1) / SR_SEG;
   const size_t grid = (size_t)a.R * segs;
   if (grid > INT32_MAX) return fail(SPEC_E_SHAPE, "sample: R * V too large");
-  // two segments a CTA where CTAs are many (192 rows of 248320 logits, a top-k:
-  // 86 us with one, 78 with two, 76 with four, which end unevenly, though,
-  // where rows are of different kinds)
-  const int turns = (int)std::max<size_t>(1, std::min<size_t>(SR_TURNS, grid / 1216));
+  // two segments a CTA where CTAs are many, eight an SM and more of them (192
+  // rows of 248320 logits, a top-k: 86 us with one, 78 with two, 76 with four,
+  // which end unevenly, though, where rows are of different kinds)
+  const int turns = (int)std::max<size_t>(1, std::min<size_t>(SR_TURNS, grid / (8 * device_sms())));
   const int long_segs = (segs + turns - 1) / turns;
   const size_t long_grid = (size_t)a.R * long_segs;
   cudaError_t e = launch_dependent(sr_maxima_kernel, grid, SR_THREADS, 0, st, a, sp, segs);

@@ -612,7 +612,8 @@ int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
     const int blocks = (a.nt * a.G + TJ_ROWS - 1) / TJ_ROWS;
     const long long units = (long long)a.n_seq * blocks * a.nkv;
     const bool split = units * 8 <= n_cta;
-    const int slices = split ? HD / 8 : units * (HD / 32) <= 1216 ? HD / 32 : 1;
+    // (a slice of 32 dimensions a CTA as long as those are resident at once, eight an SM)
+    const int slices = split ? HD / 8 : units * (HD / 32) <= 8 * device_sms() ? HD / 32 : 1;
     e = launch_dependent(split ? tree_join_kernel<HD, true> : tree_join_kernel<HD, false>, (size_t)(units * slices),
                          32 * join_warps(split), 0, st, a, blocks, slices);
   }
@@ -624,13 +625,6 @@ template <int HD, int MT>
 void init_shape() {
   cudaFuncSetAttribute(tree_attn_kernel<HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)Shape<HD, MT>::SMEM);
-}
-
-int device_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
 }
 
 // The CTAs with tiles: what is resident, but for the one that plans.
