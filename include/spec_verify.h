@@ -495,7 +495,10 @@ typedef struct {
  * (page id = slot), table, and len = the model's n_past; refs is NULL, so
  * fork, extend and free refuse it (SPEC_E_UNSUPPORTED), and its pages are
  * copied from slot to slot by spec_pages_copy.  What spec_pages_commit
- * writes is what the model's later rounds read. */
+ * writes is what the model's later rounds read; of the slot's state it advances
+ * n_past alone, so that a program that goes on with spec_verify_round there
+ * sets anchor (the last emitted token, whose key and value are not in the cache
+ * yet) and emit_idx with spec_state_set first. */
 int spec_model_pages(spec_model* m, spec_pages* out);
 
 /* Copies page src[i] to page dst[i] in every layer, i < n (device int32 [n]):

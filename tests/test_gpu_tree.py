@@ -467,6 +467,20 @@ def test_the_models_cache_as_pages(dev):
         assert e.value.code == sv.SPEC_E_UNSUPPORTED
 
 
+def test_a_commit_into_the_models_cache_advances_n_past_alone(dev):
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(16)
+    m = attn_model(sv, dev, g, 4, 2, 128, 100, 7, 3)
+    kv = sv.spec_model_pages(m)
+    sv.spec_state_set(m, [0, 1, 2], n_past=[5, 6, 7], emit_idx=[8, 9, 10], anchor=[1, 2, 3])
+    kn = torch.ones((1, 4, 2, 128), dtype=torch.float16, device=dev)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    st = i32([9])
+    sv.spec_pages_commit(kv, 1, i32([1]), 4, kn, kn, None, i32([3]), st)
+    assert st.item() == 0 and sv.spec_state_get(m, [0, 1, 2]) == ([5, 9, 7], [8, 9, 10], [1, 2, 3])
+
+
 def test_rounds_of_a_tree_drafting_decoder(orc, dev):
     """The operators as a tree-drafting program uses them, over a small
     attention model whose logits are a fixed projection of the attention
