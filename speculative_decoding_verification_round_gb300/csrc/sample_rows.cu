@@ -51,6 +51,11 @@ constexpr int SR_LIST = 4096;  // tokens that are collected of a row
 constexpr int SR_MAX_RANGES = 1024;
 constexpr int SR_BOUND_BITS = 9, SR_BOUND_BINS = 1 << SR_BOUND_BITS;
 static_assert(SR_BOUND_BINS == SM_THREADS, "a bin a thread");
+// Clusters for the rows that do not fit the list, in turns.  Flat rows are such:
+// top-p rows of 248320 logits whose deviation is below about 0.4 T have more
+// than SR_LIST tokens in the step that holds their cut.  A cluster's refinement
+// adds to few bins then, so that a row takes about 180 us of it: 192 of them 2.4
+// ms (deviation 0.3 T), 0.23 at 0.5 T and 0.17 at 2 T.
 constexpr int SR_HARD_CLUSTERS = 16;
 
 enum RowKind : int { ROW_BAD, ROW_PLAIN, ROW_TOP_K, ROW_TOP_P, ROW_HARD };

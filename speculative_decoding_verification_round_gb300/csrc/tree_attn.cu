@@ -3,9 +3,10 @@
 //
 // Every query row of one (sequence, kv head) -- nodes x GQA group -- reads the
 // same keys, so the rows are the M of an MMA tile and the cache is streamed
-// once per 64 rows: S = Q K^T, a softmax with a running maximum and sum in
+// once for all of them: S = Q K^T, a softmax with a running maximum and sum in
 // fp32 (log2 domain), O = P V, over tiles of 64 positions.  The tree's own
-// nodes are the last tile, masked by each node's set of ancestors.
+// nodes are the last tile, masked by each node's set of ancestors.  The kernel
+// here has 16 or 32 rows; more go to tree_attn_tc.cu.
 //
 // Work is cut evenly whatever the lengths are: the (sequence, kv head, row
 // block) units, each of its own number of tiles, are laid end to end, and every
