@@ -13,9 +13,9 @@
 // in 40 layers (8 heads of 128; 2.01 GB read and written) 296 us, the copy
 // bandwidth; 12 prompts of 550 positions freed, forked into four branches each
 // and extended by 16 positions, the filled part of 36 last pages copied (0.37
-// GB, 55 us of the copy bandwidth) 70 us in four launches; accepted paths of
-// 12 x 16 nodes committed in 40 layers (31 MB, 4.6 us) 8.4 us; acceptance
-// along one tree 1.7 us, 512 trees of 63 nodes 3.0 us.
+// GB, 55 us of the copy bandwidth) 73 us in four launches; accepted paths of
+// 12 x 16 nodes committed in 40 layers (31 MB, 4.6 us) 8.9 us; acceptance
+// along one tree 1.9 us, 512 trees of 63 nodes 2.8 us.
 #include <climits>
 
 #include "common.cuh"
