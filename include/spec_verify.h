@@ -673,6 +673,87 @@ int spec_sample(const float* logits, int R, int V, int64_t ld, const uint32_t* u
  * the same results). */
 int spec_sample_workspace(int R, int V, size_t* bytes);
 
+/* ===========================================================================
+ * Long contexts: a cache held in 4 bits, and attention over the blocks of a
+ * cache that a cheap score selects for each query.  As the operators above,
+ * these allocate nothing and keep nothing between calls, report errors seen on
+ * the device in the caller's `status`, and may run at the same time on several
+ * streams, or be captured, as long as the arrays that they write are not shared.
+ * ======================================================================== */
+
+/* A KV cache in pages whose rows are held in 4 bits: each 32 neighbouring
+ * elements of a row are 16 bytes of codes and one fp16 scale, laid out as in
+ * SPEC_Q4 (byte j: element j in the low nibble, element j + 16 in the high one;
+ * u = q + 8), and an element's value is scale * q, q in [-8, 7].
+ * spec_pages_q4_commit makes scales of at most eight significant bits, with
+ * which every value is exact in fp16; other scales are taken, too, their
+ * values then being rounded to fp16 where rows are attended to or read.  An
+ * infinite or NaN scale makes its elements infinite or NaN. */
+typedef struct {
+  uint8_t* k_qs; /* [n_layers][n_pages][n_kv_heads][page_size][head_dim / 32][16] */
+  uint8_t* v_qs;
+  uint16_t* k_scales; /* fp16 [n_layers][n_pages][n_kv_heads][page_size][head_dim / 32] */
+  uint16_t* v_scales; /* all four 16-byte aligned */
+  int64_t layer_stride; /* rows (of head_dim / 32 blocks) from one layer to the next (>= a layer's) */
+  int32_t n_layers, n_pages, n_kv_heads, page_size;
+  int32_t head_dim;     /* a multiple of 32 (attention: 64 or 128) */
+  int32_t n_slots, max_pages;
+  int32_t* table; /* these as in spec_pages */
+  int32_t* refs;
+  int32_t* len;
+} spec_pages_q4;
+
+/* spec_pages_copy, _fork, _extend and _free for a cache in 4 bits: the same
+ * arguments, rules and status bits. */
+int spec_pages_q4_copy(const spec_pages_q4* kv, int n, const int32_t* src, const int32_t* dst,
+                       const int32_t* n_pos, int32_t* status, void* stream);
+int spec_pages_q4_fork(const spec_pages_q4* kv, int n, const int32_t* src, const int32_t* dst,
+                       int32_t* status, void* stream);
+int spec_pages_q4_extend(const spec_pages_q4* kv, int n, const int32_t* slots, const int32_t* n_new,
+                         int32_t* copies, int32_t* status, void* stream);
+int spec_pages_q4_free(const spec_pages_q4* kv, int n, const int32_t* slots, int32_t* status,
+                       void* stream);
+
+/* spec_pages_commit into a cache in 4 bits: the same arguments, rules and status
+ * bits; the fp16 rows are quantised on their way.  Of 32 elements x, m is the
+ * one of the largest magnitude (the first of several):
+ *   scale = -m / 8, rounded to eight significant bits (to even) and then to fp16,
+ *           its magnitude at most 8160;
+ *   q     = x / scale (fp32), rounded to a whole number (to even), kept in [-8, 7];
+ *           0 where the scale is 0.
+ * Elements that are not all finite get a NaN for their scale (and q = 0): whoever
+ * sees them gets a NaN. */
+int spec_pages_q4_commit(const spec_pages_q4* kv, int n, const int32_t* slots, int nt,
+                         const uint16_t* k_new, const uint16_t* v_new, int64_t new_layer_stride,
+                         const int32_t* path, const int32_t* n_path, int32_t* new_len,
+                         int32_t* status, void* stream);
+
+/* The reverse: position pos0[i] + j of slot slots[i], j < n_pos[i], as fp16 into
+ * row j of entry i, every layer (device int32 [n]; 0 <= n_pos <= nt; a slot may
+ * be named more than once).
+ *   k, v  fp16 [n_layers][n][nt][n_kv_heads][head_dim], 16-byte aligned;
+ *         rows j >= n_pos, and those of an entry whose status is not 0, are left
+ *         as they were.  layer_stride elements from one layer to the next (0:
+ *         contiguous; a multiple of 8)
+ * The pages have to be there (SPEC_ST_PAGE); len is not looked at.  SPEC_ST_SLOT:
+ * a slot out of range; SPEC_ST_TREE: n_pos outside [0, nt]; SPEC_ST_FULL: positions
+ * below 0 or past what max_pages hold. */
+int spec_pages_q4_read(const spec_pages_q4* kv, int n, const int32_t* slots, int nt,
+                       const int32_t* pos0, const int32_t* n_pos, uint16_t* k, uint16_t* v,
+                       int64_t layer_stride, int32_t* status, void* stream);
+
+/* spec_tree_attn over a cache in 4 bits: the same arguments and rules.  The
+ * trees' own keys and values, q and out are fp16.  Keys are multiplied as they
+ * are, code by code, with the scale in fp32; values as fp16. */
+int spec_tree_attn_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, const uint16_t* q,
+                      int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new,
+                      int64_t kv_stride, uint16_t* out, void* workspace, size_t workspace_bytes,
+                      int32_t* status, void* stream);
+
+/* Bytes of workspace for spec_tree_attn_q4 on the current device. */
+int spec_tree_attn_q4_workspace(const spec_pages_q4* kv, int n_seq, int nt, int n_q_heads,
+                                size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

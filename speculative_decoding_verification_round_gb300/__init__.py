@@ -47,7 +47,9 @@ EXPORTED = ["spec_last_error", "spec_qmat_create", "spec_qmat_destroy", "spec_li
             "spec_depth_ctl_estimates", "spec_model_pages", "spec_pages_copy", "spec_pages_fork",
             "spec_pages_extend", "spec_pages_commit", "spec_pages_free", "spec_tree_attn",
             "spec_tree_attn_workspace", "spec_accept_tree", "spec_sample",
-            "spec_sample_workspace", "spec_tree_set_wait_budget"]
+            "spec_sample_workspace", "spec_tree_set_wait_budget", "spec_pages_q4_copy",
+            "spec_pages_q4_fork", "spec_pages_q4_extend", "spec_pages_q4_free", "spec_pages_q4_commit",
+            "spec_pages_q4_read", "spec_tree_attn_q4", "spec_tree_attn_q4_workspace"]
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
@@ -89,6 +91,12 @@ class spec_pages(ctypes.Structure):
     _fields_ = [("k", P), ("v", P), ("layer_stride", I64), ("n_layers", I32), ("n_pages", I32),
                 ("n_kv_heads", I32), ("page_size", I32), ("head_dim", I32), ("n_slots", I32),
                 ("max_pages", I32), ("table", P), ("refs", P), ("len", P)]
+
+
+class spec_pages_q4(ctypes.Structure):
+    _fields_ = [("k_qs", P), ("v_qs", P), ("k_scales", P), ("v_scales", P), ("layer_stride", I64),
+                ("n_layers", I32), ("n_pages", I32), ("n_kv_heads", I32), ("page_size", I32),
+                ("head_dim", I32), ("n_slots", I32), ("max_pages", I32), ("table", P), ("refs", P), ("len", P)]
 
 
 class spec_tree(ctypes.Structure):
@@ -171,6 +179,14 @@ def lib():
                 "spec_sample": (I32, [P, I32, I32, I64, P, P, P, P, P, P, P, P, I64, P, SZ, P]),
                 "spec_sample_workspace": (I32, [I32, I32, P]),
                 "spec_tree_set_wait_budget": (I32, [I32]),
+                "spec_pages_q4_copy": (I32, [P, I32, P, P, P, P, P]),
+                "spec_pages_q4_fork": (I32, [P, I32, P, P, P, P]),
+                "spec_pages_q4_extend": (I32, [P, I32, P, P, P, P, P]),
+                "spec_pages_q4_free": (I32, [P, I32, P, P, P]),
+                "spec_pages_q4_commit": (I32, [P, I32, P, I32, P, P, I64, P, P, P, P, P]),
+                "spec_pages_q4_read": (I32, [P, I32, P, I32, P, P, P, P, I64, P, P]),
+                "spec_tree_attn_q4": (I32, [P, I32, P, P, I64, P, P, I64, P, P, SZ, P, P]),
+                "spec_tree_attn_q4_workspace": (I32, [P, I32, I32, I32, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -698,3 +714,121 @@ def spec_sample(logits, R: int, V: int, u, token, temperature=None, top_k=None, 
     _check(lib().spec_sample(at, int(R), int(V), int(ld), _dev(u, d), _dev(temperature, d),
                              _dev(top_k, d), _dev(top_p, d), _dev(min_p, d), _dev(token, d), _dev(n_kept, d),
                              _dev(filtered, d), int(ld_filtered), _dev(workspace, d), n, st))
+
+
+# ---------------------------------------------------------------------------
+# long contexts: a cache in 4 bits
+# ---------------------------------------------------------------------------
+def _check_book(table, lens, refs, n_pages):
+    """(n_slots, max_pages) of a cache's bookkeeping."""
+    n_slots, max_pages = (0, 0) if table is None else table.shape
+    for t, n, name in ((table, n_slots * max_pages, "table"), (lens, n_slots, "lens"), (refs, n_pages, "refs")):
+        if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()
+                              or t.numel() != n):
+            raise ValueError(f"{name}: a contiguous int32 tensor of {n} values is required")
+    return n_slots, max_pages
+
+
+def _one_device(first, others):
+    """The device of tensors that belong together (-2: no kernel can read them)."""
+    device = first.get_device()
+    for t, name in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name}: a tensor on {t.device} beside one on {first.device}")
+    return device if all(t is None or t.is_cuda or t.is_pinned() for t in (first, *(t for t, _ in others))) else -2
+
+
+class KVPagesQ4:
+    """A paged KV cache in 4 bits (spec_pages_q4) over the caller's tensors,
+    which it keeps alive: codes uint8 [n_layers][n_pages][n_kv_heads][page_size]
+    [head_dim / 32][16] and scales fp16 [n_layers][n_pages][n_kv_heads]
+    [page_size][head_dim / 32] (a layer's pages contiguous), table, lens and
+    refs as in KVPages."""
+
+    def __init__(self, k_qs, v_qs, k_scales, v_scales, table=None, lens=None, refs=None):
+        n_layers, n_pages, n_kv_heads, page_size, blocks = k_scales.shape
+        self.device = _one_device(k_qs, ((v_qs, "v_qs"), (k_scales, "k_scales"), (v_scales, "v_scales"),
+                                         (table, "table"), (lens, "lens"), (refs, "refs")))
+        rows = n_pages * n_kv_heads * page_size
+        for t, name, bytes_, shape in ((k_qs, "k_qs", 1, (*k_scales.shape, 16)), (v_qs, "v_qs", 1, (*k_scales.shape, 16)),
+                                       (k_scales, "k_scales", 2, k_scales.shape), (v_scales, "v_scales", 2, k_scales.shape)):
+            if tuple(t.shape) != tuple(shape) or t.element_size() != bytes_ or not t[0].is_contiguous() or (
+                    t.is_floating_point() and str(t.dtype) != "torch.float16"):
+                raise ValueError(f"{name}: a tensor {tuple(shape)} of {bytes_}-byte values with contiguous layers is "
+                                 "required")
+        strides = {k_qs.stride(0) / (16 * blocks), v_qs.stride(0) / (16 * blocks), k_scales.stride(0) / blocks,
+                   v_scales.stride(0) / blocks} if n_layers > 1 else {float(rows)}
+        if len(strides) != 1 or not next(iter(strides)).is_integer():
+            raise ValueError("codes and scales must have the same layer stride, in rows")
+        n_slots, max_pages = _check_book(table, lens, refs, n_pages)
+        self._keep = (k_qs, v_qs, k_scales, v_scales, table, lens, refs)
+        self.pages = spec_pages_q4(k_qs.data_ptr(), v_qs.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                                   int(strides.pop()), n_layers, n_pages, n_kv_heads, page_size, 32 * blocks,
+                                   n_slots, max_pages, _ptr(table), _ptr(refs), _ptr(lens))
+        self.ref = ctypes.byref(self.pages)
+
+    at = KVPages.at
+
+
+def spec_pages_q4_copy(kv: KVPagesQ4, n: int, src, dst, status, n_pos=None, stream=None):
+    """spec_pages_copy for a cache in 4 bits."""
+    d, st = _here(stream)
+    _check(lib().spec_pages_q4_copy(kv.at(d), int(n), _dev(src, d), _dev(dst, d), _dev(n_pos, d), _dev(status, d),
+                                    st))
+
+
+def spec_pages_q4_fork(kv: KVPagesQ4, n: int, src, dst, status, stream=None):
+    """spec_pages_fork for a cache in 4 bits."""
+    d, st = _here(stream)
+    _check(lib().spec_pages_q4_fork(kv.at(d), int(n), _dev(src, d), _dev(dst, d), _dev(status, d), st))
+
+
+def spec_pages_q4_extend(kv: KVPagesQ4, n: int, slots, n_new, copies, status, stream=None):
+    """spec_pages_extend for a cache in 4 bits."""
+    d, st = _here(stream)
+    _check(lib().spec_pages_q4_extend(kv.at(d), int(n), _dev(slots, d), _dev(n_new, d), _dev(copies, d),
+                                      _dev(status, d), st))
+
+
+def spec_pages_q4_free(kv: KVPagesQ4, n: int, slots, status, stream=None):
+    """spec_pages_free for a cache in 4 bits."""
+    d, st = _here(stream)
+    _check(lib().spec_pages_q4_free(kv.at(d), int(n), _dev(slots, d), _dev(status, d), st))
+
+
+def spec_pages_q4_commit(kv: KVPagesQ4, n: int, slots, nt: int, k_new, v_new, path, n_path, status,
+                         new_len=None, new_layer_stride: int = 0, stream=None):
+    """spec_pages_commit into a cache in 4 bits: fp16 rows are quantised on their way."""
+    d, st = _here(stream)
+    _check(lib().spec_pages_q4_commit(kv.at(d), int(n), _dev(slots, d), int(nt), _dev(k_new, d), _dev(v_new, d),
+                                      int(new_layer_stride), _dev(path, d), _dev(n_path, d), _dev(new_len, d),
+                                      _dev(status, d), st))
+
+
+def spec_pages_q4_read(kv: KVPagesQ4, n: int, slots, nt: int, pos0, n_pos, k, v, status,
+                       layer_stride: int = 0, stream=None):
+    """Positions pos0[i] + j, j < n_pos[i], of slot slots[i] as fp16 into row j of
+    entry i of k and v [n_layers][n][nt][n_kv_heads][head_dim]."""
+    d, st = _here(stream)
+    _check(lib().spec_pages_q4_read(kv.at(d), int(n), _dev(slots, d), int(nt), _dev(pos0, d), _dev(n_pos, d),
+                                    _dev(k, d), _dev(v, d), int(layer_stride), _dev(status, d), st))
+
+
+def spec_tree_attn_q4_workspace(kv: KVPagesQ4, n_seq: int, nt: int, n_q_heads: int) -> int:
+    """Bytes of workspace that spec_tree_attn_q4 needs for trees of this size."""
+    b = SZ()
+    _check(lib().spec_tree_attn_q4_workspace(kv.ref, int(n_seq), int(nt), int(n_q_heads), ctypes.byref(b)))
+    return b.value
+
+
+def spec_tree_attn_q4(kv: KVPagesQ4, layer: int, n_seq: int, slots, nt: int, n_q_heads: int, q, k_new,
+                      v_new, out, workspace, status, parents=None, n_nodes=None, window: int = 0,
+                      sinks: int = 0, scale: float = 0.0, q_stride: int = 0, kv_stride: int = 0,
+                      stream=None):
+    """spec_tree_attn over a cache in 4 bits."""
+    d, st = _here(stream)
+    t = spec_tree(n_seq, nt, n_q_heads, window, sinks, scale, _dev(slots, d), _dev(parents, d), _dev(n_nodes, d))
+    _check(lib().spec_tree_attn_q4(kv.at(d), int(layer), ctypes.byref(t), _dev(q, d), int(q_stride),
+                                   _dev(k_new, d), _dev(v_new, d), int(kv_stride), _dev(out, d),
+                                   _dev(workspace, d), workspace.numel() * workspace.element_size(),
+                                   _dev(status, d), st))

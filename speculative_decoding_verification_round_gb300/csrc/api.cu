@@ -49,6 +49,7 @@ void linear_init_attrs();
 void tc_init_attrs();
 void tree_init_attrs();
 void sample_init_attrs();
+void q4_init_attrs();
 static std::mutex g_attr_mu;
 static std::vector<int> g_attr_done;
 static void init_attrs_once() {
@@ -62,6 +63,7 @@ static void init_attrs_once() {
   tc_init_attrs();
   tree_init_attrs();
   sample_init_attrs();
+  q4_init_attrs();
   g_attr_done.push_back(dev);
 }
 
@@ -1175,6 +1177,36 @@ extern "C" int spec_tree_attn_workspace(const spec_pages* kv, int n_seq, int nt,
   return tree_workspace(kv, n_seq, nt, n_q_heads, bytes);
 }
 
+// The checks that tree attention's forms share (need: the workspace's bytes).
+static int check_tree_call(int n_layers, int n_kv_heads, int head_dim, int layer, const spec_tree* t, const void* q,
+                           int64_t q_stride, const void* k_new, const void* v_new, int64_t kv_stride, const void* out,
+                           const void* workspace, size_t workspace_bytes, size_t need) {
+  if (layer < 0 || layer >= n_layers) return fail(SPEC_E_SHAPE, "layer out of range");
+  if (t->window < 0 || t->sinks < 0) return fail(SPEC_E_INVALID, "window and sinks must be >= 0");
+  if (!std::isfinite(t->scale)) return fail(SPEC_E_INVALID, "scale must be finite");
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) ||
+      !aligned16(workspace))
+    return fail(SPEC_E_SHAPE, "q, k_new, v_new, out and workspace must be 16-byte aligned");
+  if (q_stride % 8 != 0 || kv_stride % 8 != 0 || q_stride < 0 || kv_stride < 0 ||
+      (q_stride != 0 && q_stride < (int64_t)t->n_q_heads * head_dim) ||
+      (kv_stride != 0 && kv_stride < (int64_t)n_kv_heads * head_dim))
+    return fail(SPEC_E_SHAPE, "row strides must be multiples of 8 that hold a row's heads");
+  if ((double)std::max(q_stride, kv_stride) * t->n_seq * t->nt > 4.0e15)
+    return fail(SPEC_E_SHAPE, "row strides are too large");
+  if (workspace_bytes < need)
+    return fail(SPEC_E_SHAPE, "workspace of " + std::to_string(need) + " bytes required");
+  // a unit's rows may be written while another CTA reads its inputs
+  const size_t nodes = (size_t)t->n_seq * t->nt, qd = (size_t)t->n_q_heads * head_dim,
+               kd = (size_t)n_kv_heads * head_dim;
+  const size_t out_b = 2 * nodes * qd, q_b = 2 * ((nodes - 1) * (q_stride != 0 ? (size_t)q_stride : qd) + qd),
+               new_b = 2 * ((nodes - 1) * (kv_stride != 0 ? (size_t)kv_stride : kd) + kd);
+  if (overlaps(out, out_b, q, q_b) || overlaps(out, out_b, k_new, new_b) || overlaps(out, out_b, v_new, new_b) ||
+      overlaps(out, out_b, workspace, need) || overlaps(workspace, need, q, q_b) ||
+      overlaps(workspace, need, k_new, new_b) || overlaps(workspace, need, v_new, new_b))
+    return fail(SPEC_E_INVALID, "out and workspace must not overlap q, k_new, v_new or each other");
+  return SPEC_OK;
+}
+
 extern "C" int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,
                               int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new,
                               int64_t kv_stride, uint16_t* out, void* workspace,
@@ -1183,34 +1215,38 @@ extern "C" int spec_tree_attn(const spec_pages* kv, int layer, const spec_tree* 
       v_new == nullptr || out == nullptr || workspace == nullptr || status == nullptr)
     return fail(SPEC_E_INVALID, "null argument");
   size_t need = 0;
-  const int rc = tree_workspace(kv, t->n_seq, t->nt, t->n_q_heads, &need);
+  int rc = tree_workspace(kv, t->n_seq, t->nt, t->n_q_heads, &need);
+  if (rc == SPEC_OK)
+    rc = check_tree_call(kv->n_layers, kv->n_kv_heads, kv->head_dim, layer, t, q, q_stride, k_new, v_new, kv_stride,
+                         out, workspace, workspace_bytes, need);
   if (rc != SPEC_OK) return rc;
-  if (layer < 0 || layer >= kv->n_layers) return fail(SPEC_E_SHAPE, "layer out of range");
-  if (t->window < 0 || t->sinks < 0) return fail(SPEC_E_INVALID, "window and sinks must be >= 0");
-  if (!std::isfinite(t->scale)) return fail(SPEC_E_INVALID, "scale must be finite");
-  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) ||
-      !aligned16(workspace))
-    return fail(SPEC_E_SHAPE, "q, k_new, v_new, out and workspace must be 16-byte aligned");
-  if (q_stride % 8 != 0 || kv_stride % 8 != 0 || q_stride < 0 || kv_stride < 0 ||
-      (q_stride != 0 && q_stride < (int64_t)t->n_q_heads * kv->head_dim) ||
-      (kv_stride != 0 && kv_stride < (int64_t)kv->n_kv_heads * kv->head_dim))
-    return fail(SPEC_E_SHAPE, "row strides must be multiples of 8 that hold a row's heads");
-  if ((double)std::max(q_stride, kv_stride) * t->n_seq * t->nt > 4.0e15)
-    return fail(SPEC_E_SHAPE, "row strides are too large");
-  if (workspace_bytes < need)
-    return fail(SPEC_E_SHAPE, "workspace of " + std::to_string(need) + " bytes required");
-  // a unit's rows may be written while another CTA reads its inputs
-  const size_t nodes = (size_t)t->n_seq * t->nt, qd = (size_t)t->n_q_heads * kv->head_dim,
-               kd = (size_t)kv->n_kv_heads * kv->head_dim;
-  const size_t out_b = 2 * nodes * qd, q_b = 2 * ((nodes - 1) * (q_stride != 0 ? (size_t)q_stride : qd) + qd),
-               new_b = 2 * ((nodes - 1) * (kv_stride != 0 ? (size_t)kv_stride : kd) + kd);
-  if (overlaps(out, out_b, q, q_b) || overlaps(out, out_b, k_new, new_b) || overlaps(out, out_b, v_new, new_b) ||
-      overlaps(out, out_b, workspace, need) || overlaps(workspace, need, q, q_b) ||
-      overlaps(workspace, need, k_new, new_b) || overlaps(workspace, need, v_new, new_b))
-    return fail(SPEC_E_INVALID, "out and workspace must not overlap q, k_new, v_new or each other");
   init_attrs_once();
   return launch_tree(kv, layer, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status,
                      as_stream(stream));
+}
+
+extern "C" int spec_tree_attn_q4_workspace(const spec_pages_q4* kv, int n_seq, int nt, int n_q_heads,
+                                           size_t* bytes) {
+  if (bytes == nullptr) return fail(SPEC_E_INVALID, "null argument");
+  return q4_workspace(kv, n_seq, nt, n_q_heads, bytes);
+}
+
+extern "C" int spec_tree_attn_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, const uint16_t* q,
+                                 int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new,
+                                 int64_t kv_stride, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                 int32_t* status, void* stream) {
+  if (kv == nullptr || t == nullptr || t->slots == nullptr || q == nullptr || k_new == nullptr ||
+      v_new == nullptr || out == nullptr || workspace == nullptr || status == nullptr)
+    return fail(SPEC_E_INVALID, "null argument");
+  size_t need = 0;
+  int rc = q4_workspace(kv, t->n_seq, t->nt, t->n_q_heads, &need);
+  if (rc == SPEC_OK)
+    rc = check_tree_call(kv->n_layers, kv->n_kv_heads, kv->head_dim, layer, t, q, q_stride, k_new, v_new, kv_stride,
+                         out, workspace, workspace_bytes, need);
+  if (rc != SPEC_OK) return rc;
+  init_attrs_once();
+  return launch_tree_q4(kv, layer, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status,
+                        as_stream(stream));
 }
 
 extern "C" int spec_tree_set_wait_budget(int tries) {

@@ -258,6 +258,18 @@ cudaError_t accept_commit_node_retarget(cudaGraphExec_t ex, cudaGraphNode_t node
 // lengths are used too.
 int check_pages(const spec_pages* kv, bool book);
 
+// The bookkeeping of an extension (pages.cu): checks, pages taken, copies named.
+int launch_extend_book(const spec_pages* kv, int n, const int32_t* slots, const int32_t* n_new, int32_t* copies,
+                       int32_t* status, cudaStream_t st);
+// A cache in 4 bits (pages_q4.cu): its checks, its bookkeeping as spec_pages.
+int check_pages_q4(const spec_pages_q4* kv, bool book);
+spec_pages book_of(const spec_pages_q4* kv);
+// Tree attention over it (q4_attn.cu).
+int q4_workspace(const spec_pages_q4* kv, int n_seq, int nt, int n_q_heads, size_t* bytes);
+int launch_tree_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, const uint16_t* q, int64_t q_stride,
+                   const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride, uint16_t* out, void* workspace,
+                   int32_t* status, cudaStream_t st);
+
 // Tree attention (tree_attn.cu) and filtered sampling (sample.cu).
 int tree_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads, size_t* bytes);
 int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,

@@ -1,0 +1,512 @@
+// key_warp.cuh -- one warp's attention of 8 NT query rows to keys in shared
+// memory, 16 at a time, with mma.sync: rows of fp16 or of 4-bit codes.  Internal.
+//
+// The keys are the M of the products and the query rows the N, S^T = K Q^T and
+// O^T += V^T P^T, so that the few rows of a decode step (a GQA group, 4 to 8)
+// fill a tile of 8 instead of half of one of 16.  What the layout of the
+// fragments asks of K, V and Q is met by choosing the order of the dimensions
+// and keys, which no sum depends on:
+//   4-bit K  lane (g, t) takes the word t of each block of 32 elements of its
+//            keys: a nibble by itself is a (subnormal) fp16 number u 2^-24, so
+//            that four masks and three shifts give eight elements of the
+//            operand.  u = q + 8: the accumulator starts at -8 2^-24 sum q of the
+//            block, and the block's scale multiplies it in fp32.
+//   4-bit V  lane (g, t) takes the 16 (64 dimensions: 8) elements g of the keys t,
+//            t + 4, t + 8, t + 12, pairs of keys in one register: the number
+//            1024 + u by its bits, minus 1032, times the pair's scales, both
+//            exact in fp16 (a scale has eight significant bits, u - 8 three).
+// A row's elements so belong to the accumulator tiles in another order than in
+// fp16 (dim_of).
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace {
+
+// The running maximum lags behind by up to 2^KW_SLACK, which saves the
+// reductions over the lanes, and 2^KW_BIAS multiplies weights and sums, which
+// keeps what lies far below the maximum inside fp16's range: a pair of fp16
+// numbers holds all of a weight w but 2^-20 w + 2^-36.
+constexpr float KW_SLACK = 3.0f, KW_BIAS = 12.0f;
+// hi is the weight cut off behind its 11th bit, lo the rest and 2^-22 of hi
+// more: both are non-negative, and an infinite value stays infinite.
+constexpr uint32_t KW_CUT = 0xFFFFE000u;
+constexpr float KW_REST = 1.0f - 0x1p-22f;
+
+__device__ __forceinline__ uint32_t kw_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t kw_lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t kw_lds16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 kw_lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint4 kw_lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void kw_sts64(uint32_t at, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void kw_sts64f(uint32_t at, float a, float b) {
+  kw_sts64(at, __float_as_uint(a), __float_as_uint(b));
+}
+// BYTES to shared memory; zeros if !valid (src is then any readable address).
+template <int BYTES>
+__device__ __forceinline__ void kw_copy(uint32_t dst, const void* src, bool valid) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0));
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+                 "r"(valid ? BYTES : 0));
+}
+__device__ __forceinline__ uint32_t kw_pack(float a, float b) {  // a in the low half
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float kw_half(uint32_t v, int hi) {
+  return __half2float(__ushort_as_half((unsigned short)(hi ? v >> 16 : v & 0xFFFFu)));
+}
+__device__ __forceinline__ float kw_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t kw_transpose(uint32_t v) {  // 8 x 8 of 16 bits
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t kw_hadd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t kw_hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t kw_hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// u - 8 of two nibbles: those at bits 0-3 and 16-19, and those at bits 4-7 and 20-23.
+__device__ __forceinline__ uint32_t q4_low(uint32_t x) {  // (1024 + u) - 1032
+  return kw_hadd2(lop3_and_or(x, 0x000F000Fu, 0x64006400u), 0xE408E408u);
+}
+__device__ __forceinline__ uint32_t q4_high(uint32_t x) {  // (1024 + 16 u) / 16 - 72
+  return kw_hfma2(lop3_and_or(x, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u);
+}
+__device__ __forceinline__ bool odd_half(uint32_t v) { return (v & 0x7C00u) == 0x7C00u; }  // infinite or NaN
+__device__ __forceinline__ bool odd_pair(uint32_t v) { return odd_half(v) || odd_half(v >> 16); }
+
+// The row of a group of eight that holds the group's key k: its even keys in
+// front, so that the four of one load lie in different banks.
+__device__ __forceinline__ int key_row(int k) { return (k >> 1 & 3) | (k & 1) << 2; }
+
+// A row of codes: HD / 2 bytes, 16-byte chunk c of row r at c ^ q4_swz(r).
+template <int HD>
+__device__ __forceinline__ int q4_swz(int r) {
+  return HD == 128 ? (r & 2) | (r >> 2 & 1) : r >> 2 & 1;
+}
+// A row of fp16: HD * 2 bytes, 16-byte unit u of row r at u ^ (r & 7).
+template <int HD>
+__device__ __forceinline__ uint32_t f16_off(int r, int u) {
+  return (uint32_t)(r * (HD * 2) + ((u ^ (r & 7)) << 4));
+}
+
+// Q4: the order of the dimensions that the codes ask for.
+template <int HD, int NT, bool Q4>
+struct KeyWarp {
+  static constexpr int STEPS = HD / 16, BLOCKS = HD / 32, MTILES = HD / 16;
+  static constexpr int Q_BYTES = STEPS * NT * 32 * 8;     // query fragments of a CTA
+  static constexpr int SUM_BYTES = BLOCKS * NT * 4 * 8;   // and sums of their blocks (Q4)
+  int g, t;
+  float o[MTILES][NT][4];  // (dimension g of a tile; rows 2t, 2t + 1), (dimension g + 8; ...)
+  float mx[NT][2], sum[NT][2];  // of rows 2t, 2t + 1; sum: this lane's keys
+
+  __device__ __forceinline__ void begin() {
+    g = (threadIdx.x & 31) >> 2;
+    t = threadIdx.x & 3;
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+#pragma unroll
+      for (int m = 0; m < MTILES; m++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[m][n][e] = 0.0f;
+      mx[n][0] = mx[n][1] = -INFINITY;
+      sum[n][0] = sum[n][1] = 0.0f;
+    }
+  }
+
+  // The dimension of accumulator tile m's row `half` (0: g, 1: g + 8).
+  __device__ __forceinline__ int dim_of(int m, int half) const {
+    if (!Q4) return 16 * m + 8 * half + g;
+    if (HD == 128) return 32 * (g >> 1) + 8 * (g & 1) + m + 16 * half;
+    return 32 * (g >> 2) + 4 * (g & 3) + m + 16 * half;
+  }
+
+  // Query fragments: entry e of (step, n, lane), row(r): row r's data or null.
+  // Every thread of the CTA; `threads` of them.
+  template <class F>
+  static __device__ __forceinline__ void put_queries(uint32_t qs, uint32_t sums, int tid, int threads, F&& row) {
+    for (int e = tid; e < STEPS * NT * 32; e += threads) {
+      const int lane = e & 31, n = e / 32 % NT, step = e / 32 / NT;
+      const __half* p = row(8 * n + (lane >> 2));
+      uint32_t b0 = 0u, b1 = 0u;
+      if (p != nullptr) {
+        if (Q4) {  // elements 4t, 4t + 2 and 4t + 1, 4t + 3
+          const uint2 v = *reinterpret_cast<const uint2*>(p + 16 * step + 4 * (lane & 3));
+          b0 = __byte_perm(v.x, v.y, 0x5410);
+          b1 = __byte_perm(v.x, v.y, 0x7632);
+        } else {
+          b0 = *reinterpret_cast<const uint32_t*>(p + 16 * step + 2 * (lane & 3));
+          b1 = *reinterpret_cast<const uint32_t*>(p + 16 * step + 2 * (lane & 3) + 8);
+        }
+      }
+      kw_sts64(qs + e * 8, b0, b1);
+    }
+    if (Q4)
+      for (int e = tid; e < BLOCKS * NT * 4; e += threads) {
+        const int tt = e & 3, n = e / 4 % NT, b = e / 4 / NT;
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const __half* p = row(8 * n + 2 * tt + h);
+          if (p != nullptr)
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+              const uint4 v = *reinterpret_cast<const uint4*>(p + 32 * b + 8 * u);
+              s[h] += kw_half(v.x, 0) + kw_half(v.x, 1) + kw_half(v.y, 0) + kw_half(v.y, 1) + kw_half(v.z, 0) +
+                      kw_half(v.z, 1) + kw_half(v.w, 0) + kw_half(v.w, 1);
+            }
+        }
+        kw_sts64f(sums + e * 8, s[0] * -0x1p-21f, s[1] * -0x1p-21f);
+      }
+  }
+
+  // x = scale (K Q^T) of KT tiles of 16 rows of codes at `ks` (their scales at
+  // `ss`), scale in log2 units.  Lane (g, t): keys key_row(g) and 8 + of each tile, rows
+  // 2t, 2t + 1 of each n.
+  template <int KT>
+  __device__ __forceinline__ void scores_q4(uint32_t ks, uint32_t ss, uint32_t qs, uint32_t sums, float scale,
+                                            float (&x)[KT][NT][4]) const {
+    const int lane = g * 4 + t, kr = key_row(g);
+    const float f = scale * 0x1p24f;
+    uint32_t sc[KT][2][BLOCKS / 2];
+#pragma unroll
+    for (int i = 0; i < KT; i++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const uint32_t at = ss + (16 * i + 8 * h + kr) * (HD / 16);
+        if (BLOCKS == 4) {
+          const uint2 v = kw_lds64(at);
+          sc[i][h][0] = v.x;
+          sc[i][h][BLOCKS / 2 - 1] = v.y;
+        } else {
+          sc[i][h][0] = kw_lds32(at);
+        }
+      }
+#pragma unroll
+    for (int b = 0; b < BLOCKS; b++) {
+      uint32_t w[KT][2];
+#pragma unroll
+      for (int i = 0; i < KT; i++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int r = 16 * i + 8 * h + kr;
+          w[i][h] = kw_lds32(ks + r * (HD / 2) + ((b ^ q4_swz<HD>(r)) << 4) + 4 * t);
+        }
+      float acc[KT][NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        const uint2 c = kw_lds64(sums + ((b * NT + n) * 4 + t) * 8);
+#pragma unroll
+        for (int i = 0; i < KT; i++) {
+          acc[i][n][0] = acc[i][n][2] = __uint_as_float(c.x);
+          acc[i][n][1] = acc[i][n][3] = __uint_as_float(c.y);
+        }
+      }
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        uint32_t a[KT][4];
+#pragma unroll
+        for (int i = 0; i < KT; i++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const uint32_t v = half ? w[i][h] >> 4 : w[i][h];
+            a[i][h] = v & 0x000F000Fu;
+            a[i][2 + h] = (v >> 8) & 0x000F000Fu;
+          }
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          const uint2 q = kw_lds64(qs + (((2 * b + half) * NT + n) * 32 + lane) * 8);
+#pragma unroll
+          for (int i = 0; i < KT; i++) mma_16816(acc[i][n], a[i], q.x, q.y);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < KT; i++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const float s = kw_half(sc[i][h][b >> 1], b & 1) * f;
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 2 * h; e < 2 * h + 2; e++)
+              x[i][n][e] = b == 0 ? acc[i][n][e] * s : fmaf(acc[i][n][e], s, x[i][n][e]);
+        }
+    }
+  }
+
+  // The same of one tile of 16 fp16 rows.  Keys in the order of the rows (not
+  // Q4) or in the codes' (Q4).
+  __device__ __forceinline__ void scores_f16(uint32_t ks, uint32_t qs, float scale, float (&x)[NT][4]) const {
+    const int lane = g * 4 + t;
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) x[n][e] = 0.0f;
+#pragma unroll
+    for (int step = 0; step < STEPS; step++) {
+      uint32_t a[4];
+      if (Q4) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int r = 8 * h + key_row(g);
+          const uint2 v = kw_lds64(ks + f16_off<HD>(r, 2 * step + (t >> 1)) + 8 * (t & 1));
+          a[h] = __byte_perm(v.x, v.y, 0x5410);
+          a[2 + h] = __byte_perm(v.x, v.y, 0x7632);
+        }
+      } else {
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                     : "r"(ks + f16_off<HD>(lane & 15, 2 * step + (lane >> 4))));
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        const uint2 q = kw_lds64(qs + ((step * NT + n) * 32 + lane) * 8);
+        mma_16816(x[n], a, q.x, q.y);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) x[n][e] *= scale;
+  }
+
+  // Scores to weights (times 2^KW_BIAS); the running maximum and sum.
+  template <int KT>
+  __device__ __forceinline__ void weights(float (&x)[KT][NT][4]) {
+    bool grow = false;
+    float top[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        top[n][h] = fmaxf(x[0][n][h], x[0][n][2 + h]);
+#pragma unroll
+        for (int i = 1; i < KT; i++) top[n][h] = fmaxf(top[n][h], fmaxf(x[i][n][h], x[i][n][2 + h]));
+        grow |= top[n][h] > mx[n][h] + KW_SLACK;  // (-infinity + 3 at first)
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        float al[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          float m = fmaxf(mx[n][h], top[n][h]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          al[h] = m == -INFINITY ? 1.0f : kw_exp2(mx[n][h] - m);
+          mx[n][h] = m;
+          sum[n][h] *= al[h];
+        }
+#pragma unroll
+        for (int m = 0; m < MTILES; m++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) o[m][n][e] *= al[e & 1];
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const float shift = KW_BIAS - (mx[n][h] == -INFINITY ? 0.0f : mx[n][h]);
+#pragma unroll
+        for (int i = 0; i < KT; i++) {
+          x[i][n][h] = kw_exp2(x[i][n][h] + shift);
+          x[i][n][2 + h] = kw_exp2(x[i][n][2 + h] + shift);
+          sum[n][h] += x[i][n][h] + x[i][n][2 + h];
+        }
+      }
+  }
+
+  // A tile's weights as fragments: pairs of fp16 numbers hi + lo.
+  __device__ __forceinline__ void split(const float (&p)[NT][4], uint32_t (&hi)[NT][2], uint32_t (&lo)[NT][2]) const {
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const float a = p[n][2 * h], b = p[n][2 * h + 1];
+        const float ca = __uint_as_float(__float_as_uint(a) & KW_CUT), cb = __uint_as_float(__float_as_uint(b) & KW_CUT);
+        hi[n][h] = kw_transpose(kw_pack(ca, cb));
+        lo[n][h] = kw_transpose(kw_pack(fmaf(ca, -KW_REST, a), fmaf(cb, -KW_REST, b)));
+      }
+  }
+  __device__ __forceinline__ void add(int m, const uint32_t (&a)[4], const uint32_t (&hi)[NT][2],
+                                      const uint32_t (&lo)[NT][2]) {
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      mma_16816(o[m][n], a, hi[n][0], hi[n][1]);
+      mma_16816(o[m][n], a, lo[n][0], lo[n][1]);
+    }
+  }
+
+  // O += P V of one tile of 16 rows of codes at `vs`, scales at `ss`.
+  __device__ __forceinline__ void values_q4(uint32_t vs, uint32_t ss, const float (&p)[NT][4]) {
+    constexpr int WORDS = HD / 64;
+    uint32_t hi[NT][2], lo[NT][2];
+    split(p, hi, lo);
+    uint32_t w[4][WORDS], s[4];  // keys t, t + 4, t + 8, t + 12
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int r = t + 4 * k;
+      if (HD == 128) {
+        const uint2 v = kw_lds64(vs + r * (HD / 2) + (((g >> 1) ^ q4_swz<HD>(r)) << 4) + 8 * (g & 1));
+        w[k][0] = v.x;
+        w[k][WORDS - 1] = v.y;
+        s[k] = kw_lds16(ss + r * (HD / 16) + 2 * (g >> 1));
+      } else {
+        w[k][0] = kw_lds32(vs + r * (HD / 2) + (((g >> 2) ^ q4_swz<HD>(r)) << 4) + 4 * (g & 3));
+        s[k] = kw_lds16(ss + r * (HD / 16) + 2 * (g >> 2));
+      }
+    }
+    const uint32_t s0 = s[0] | s[1] << 16, s1 = s[2] | s[3] << 16;
+#pragma unroll
+    for (int j = 0; j < WORDS; j++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {  // a byte: elements i and 16 + i of the word's
+        const uint32_t sel = i | i << 4 | (4 + i) << 8 | (4 + i) << 12;
+        const uint32_t x0 = __byte_perm(w[0][j], w[1][j], sel), x1 = __byte_perm(w[2][j], w[3][j], sel);
+        const uint32_t a[4] = {kw_hmul2(q4_low(x0), s0), kw_hmul2(q4_high(x0), s0), kw_hmul2(q4_low(x1), s1),
+                               kw_hmul2(q4_high(x1), s1)};
+        add(4 * j + i, a, hi, lo);
+      }
+  }
+
+  // The same of 16 fp16 rows.
+  __device__ __forceinline__ void values_f16(uint32_t vs, const float (&p)[NT][4]) {
+    uint32_t hi[NT][2], lo[NT][2];
+    split(p, hi, lo);
+    if (!Q4) {
+      const int lane = g * 4 + t, r = (lane & 7) + (lane >> 4) * 8, u = lane >> 3 & 1;
+#pragma unroll
+      for (int m = 0; m < MTILES; m++) {
+        uint32_t a[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                     : "r"(vs + f16_off<HD>(r, 2 * m + u)));
+        add(m, a, hi, lo);
+      }
+    } else {
+      // this lane's dimensions: MTILES neighbours, and those 16 behind
+      const int d0 = dim_of(0, 0);
+      uint32_t v[4][2][MTILES / 2];
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const uint32_t at = vs + f16_off<HD>(t + 4 * k, (d0 + 16 * h) >> 3) + 2 * (d0 & 7);
+          if (HD == 128) {
+            const uint4 x = kw_lds128(at);
+            v[k][h][0] = x.x;
+            v[k][h][1] = x.y;
+            v[k][h][MTILES / 2 - 2] = x.z;
+            v[k][h][MTILES / 2 - 1] = x.w;
+          } else {
+            const uint2 x = kw_lds64(at);
+            v[k][h][0] = x.x;
+            v[k][h][1] = x.y;
+          }
+        }
+#pragma unroll
+      for (int m = 0; m < MTILES; m++) {
+        const uint32_t sel = m & 1 ? 0x7632 : 0x5410;
+        const uint32_t a[4] = {__byte_perm(v[0][0][m >> 1], v[1][0][m >> 1], sel),
+                               __byte_perm(v[0][1][m >> 1], v[1][1][m >> 1], sel),
+                               __byte_perm(v[2][0][m >> 1], v[3][0][m >> 1], sel),
+                               __byte_perm(v[2][1][m >> 1], v[3][1][m >> 1], sel)};
+        add(m, a, hi, lo);
+      }
+    }
+  }
+
+  // A tile's values added one key after the other where it holds infinities or NaN
+  // that some rows do not see (0 times them is NaN): value(row, dimension).
+  template <class F>
+  __device__ __forceinline__ void values_slow(const float (&p)[NT][4], F&& value) {
+#pragma unroll 1
+    for (int k = 0; k < 16; k++) {
+      const int src = (k & 7) << 2 | t, r = (k & 8) + key_row(k & 7);
+      float pr[NT][2];
+      bool any = false;
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const float a = __shfl_sync(0xffffffffu, p[n][h], src), b = __shfl_sync(0xffffffffu, p[n][2 + h], src);
+          pr[n][h] = k < 8 ? a : b;
+          any |= !(pr[n][h] == 0.0f);
+        }
+      if (!any) continue;
+#pragma unroll
+      for (int m = 0; m < MTILES; m++)
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          const float v = value(r, dim_of(m, half));
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+              if (!(pr[n][h] == 0.0f)) o[m][n][2 * half + h] = fmaf(pr[n][h], v, o[m][n][2 * half + h]);
+        }
+    }
+  }
+
+  // The warp's results: o as x[row][dimension] (rows XROW floats apart), and
+  // (maximum, sum) of its rows.
+  template <int XROW>
+  __device__ __forceinline__ void put(float* x, float2* ml) const {
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float l = sum[n][h];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        const int r = 8 * n + 2 * t + h;
+        if (g == 0) ml[r] = make_float2(mx[n][h], l);
+#pragma unroll
+        for (int m = 0; m < MTILES; m++)
+#pragma unroll
+          for (int half = 0; half < 2; half++) x[r * XROW + dim_of(m, half)] = o[m][n][2 * half + h];
+      }
+  }
+};
+
+}  // namespace

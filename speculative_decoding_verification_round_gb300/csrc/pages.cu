@@ -558,21 +558,26 @@ extern "C" int spec_pages_fork(const spec_pages* kv, int n, const int32_t* src, 
   return launched("page fork");
 }
 
-extern "C" int spec_pages_extend(const spec_pages* kv, int n, const int32_t* slots,
-                                 const int32_t* n_new, int32_t* copies, int32_t* status,
-                                 void* stream) {
+int launch_extend_book(const spec_pages* kv, int n, const int32_t* slots, const int32_t* n_new, int32_t* copies,
+                       int32_t* status, cudaStream_t st) {
   int rc = check_pages(kv, true);
   if (rc == SPEC_OK) rc = check_refs(kv);
   if (rc == SPEC_OK) rc = check_list(slots, status, n);
   if (rc == SPEC_OK && (n_new == nullptr || copies == nullptr)) rc = fail(SPEC_E_INVALID, "null argument");
   if (rc != SPEC_OK) return rc;
   if (n > EX_THREADS) return fail(SPEC_E_SHAPE, "n must be <= 1024");
-  const int64_t grid = (int64_t)n * kv->n_layers;
-  if (grid > INT32_MAX) return fail(SPEC_E_SHAPE, "n * n_layers too large");
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((int64_t)n * kv->n_layers > INT32_MAX) return fail(SPEC_E_SHAPE, "n * n_layers too large");
   pages_extend_kernel<<<1, EX_THREADS, 0, st>>>(*kv, n, slots, n_new, copies, status);
-  rc = launched("page extend");
+  return launched("page extend");
+}
+
+extern "C" int spec_pages_extend(const spec_pages* kv, int n, const int32_t* slots,
+                                 const int32_t* n_new, int32_t* copies, int32_t* status,
+                                 void* stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int rc = launch_extend_book(kv, n, slots, n_new, copies, status, st);
   if (rc != SPEC_OK) return rc;
+  const int64_t grid = (int64_t)n * kv->n_layers;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;

@@ -1,0 +1,434 @@
+// pages_q4.cu -- the pages of a KV cache held in 4 bits: rows quantised into
+// it (commit), read back, copied; fork, extend and free are the bookkeeping of
+// pages.cu.
+//
+// A lane has two neighbouring elements of fp16 (or codes of them), a block of
+// 32 so is half a warp: its largest element is found by four exchanges.  Codes of
+// elements j and j + 16 share a byte, which the lane of element j's pair makes
+// with its neighbour 8 lanes on.
+#include <algorithm>
+#include <climits>
+
+#include "common.cuh"
+
+namespace {
+
+constexpr int PQ_THREADS = 256;
+
+__device__ __forceinline__ float half_of(uint32_t v, int hi) {
+  return __half2float(__ushort_as_half((unsigned short)(hi ? v >> 16 : v & 0xFFFFu)));
+}
+
+// The scale of a block whose element of the largest magnitude is m (finite):
+// eight significant bits, exact in fp16, at most 8160 (255 * 32: 8 times it is
+// fp16's, too).
+__device__ __forceinline__ float block_scale(float m) {
+  const float d = -0.125f * m;  // exact
+  const uint32_t u = __float_as_uint(d);
+  // to eight bits, to even (|d| <= 8188: no overflow), then to fp16's grid
+  const float r = __uint_as_float((u + 0x7FFFu + ((u >> 16) & 1u)) & 0xFFFF0000u);
+  return fminf(fmaxf(__half2float(__float2half_rn(r)), -8160.0f), 8160.0f);
+}
+
+// One block of 32 (half a warp, two elements a lane: 2j, 2j + 1 of lane j) to
+// codes and scale.  bytes: codes of elements 2j and 2j + 16, ... of lanes j < 8.
+struct Block {
+  uint32_t bytes;  // two code bytes (lanes 0-7 of the half)
+  uint32_t scale;  // fp16 bits
+};
+__device__ __forceinline__ Block quantise(uint32_t x) {
+  const float a = half_of(x, 0), b = half_of(x, 1);
+  // magnitude bits, and where they are equal the lowest index: the half's
+  // absolute bits over the complement of the index
+  const int j = threadIdx.x & 15;
+  const uint32_t ka = (x & 0x7FFFu) << 16 | (uint32_t)(63 - 2 * j) << 1 | ((x >> 15) & 1u);
+  const uint32_t kb = (x >> 16 & 0x7FFFu) << 16 | (uint32_t)(62 - 2 * j) << 1 | (x >> 31);
+  uint32_t k = max(ka, kb);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, off));
+  const uint32_t top = (k >> 16) | (k & 1u) << 15;  // its bits
+  Block out;
+  uint32_t u = 0x0808u;  // codes of this lane's two elements
+  if ((top & 0x7C00u) == 0x7C00u) {
+    out.scale = 0x7E00u;
+  } else {
+    const float d = block_scale(half_of(top, 0));
+    out.scale = __half_as_ushort(__float2half_rn(d));
+    if (d != 0.0f) {
+      const int qa = (int)fminf(fmaxf(rintf(__fdiv_rn(a, d)), -8.0f), 7.0f) + 8;
+      const int qb = (int)fminf(fmaxf(rintf(__fdiv_rn(b, d)), -8.0f), 7.0f) + 8;
+      u = (uint32_t)qa | (uint32_t)qb << 8;
+    }
+  }
+  const uint32_t high = __shfl_down_sync(0xffffffffu, u, 8, 16);
+  out.bytes = u | high << 4;
+  return out;
+}
+
+constexpr int CQ_ROWS = 64;  // rows of a CTA
+
+// One CTA per (entry, layer, block of rows); a warp does 64 elements at a time.
+__global__ void __launch_bounds__(PQ_THREADS)
+q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slots, int nt,
+                 const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new, int64_t new_layer_stride,
+                 const int32_t* __restrict__ path, const int32_t* __restrict__ n_path,
+                 int32_t* __restrict__ new_len, int blocks, int32_t* __restrict__ status) {
+  const int i = blockIdx.x / (kv.n_layers * blocks);
+  const int layer = blockIdx.x / blocks % kv.n_layers, blk = blockIdx.x % blocks;
+  const int slot = slots[i], np = n_path[i];
+  const int32_t* pth = path != nullptr ? path + (int64_t)i * nt : nullptr;
+  int st = 0;
+  if (slot < 0 || slot >= kv.n_slots) st |= SPEC_ST_SLOT;
+  if (np < 0 || np > nt) st |= SPEC_ST_TREE;
+  int len = 0;
+  const int32_t* row = nullptr;
+  if (st == 0) {
+    row = kv.table + (int64_t)slot * kv.max_pages;
+    len = kv.len[slot];
+    if (len < 0 || (int64_t)len + np > (int64_t)kv.max_pages * kv.page_size) st |= SPEC_ST_FULL;
+  }
+  int bits = 0;
+  for (int j = threadIdx.x; j < n; j += PQ_THREADS)
+    if (j != i && slots[j] == slot) bits |= SPEC_ST_SLOT;
+  if (st == 0 && np > 0) {
+    if (pth != nullptr)
+      for (int j = threadIdx.x; j < np; j += PQ_THREADS)
+        if (pth[j] < 0 || pth[j] >= nt) bits |= SPEC_ST_TREE;
+    const int e1 = (int)(((int64_t)len + np - 1) / kv.page_size);
+    for (int e = len / kv.page_size + threadIdx.x; e <= e1; e += PQ_THREADS) {
+      const int p = row[e];
+      if (p < 0 || p >= kv.n_pages)
+        bits |= SPEC_ST_PAGE;
+      else if (kv.refs != nullptr && kv.refs[p] != 1)
+        bits |= SPEC_ST_SHARED;
+    }
+  }
+  if (__syncthreads_or(bits))
+    for (int b = 1; b <= SPEC_ST_TREE; b <<= 1)
+      if (__syncthreads_or(bits & b)) st |= b;
+  if (layer == 0 && blk == 0 && threadIdx.x == 0) {
+    status[i] = st;
+    if (st == 0 && new_len != nullptr) new_len[slot] = len + np;
+  }
+  if (st != 0) return;
+  const int hd = kv.head_dim, node = kv.n_kv_heads * hd;  // elements of a node's row
+  const int64_t src0 = (int64_t)layer * new_layer_stride + (int64_t)i * nt * node;
+  const int r0 = blk * CQ_ROWS, r1 = min(np, r0 + CQ_ROWS);
+  const int lane = threadIdx.x & 31, half = lane >> 4, j = lane & 15;
+  const int per = node / 32;  // blocks of a node's row
+  const int64_t count = (int64_t)max(0, r1 - r0) * per;
+  for (int64_t b0 = (threadIdx.x >> 5) * 2; b0 < count; b0 += PQ_THREADS / 16) {
+    const int64_t b = b0 + half;
+    const bool ok = b < count;
+    const int jr = r0 + (ok ? (int)(b / per) : 0), w = ok ? (int)(b % per) : 0, h = w / (hd / 32), u = w % (hd / 32);
+    const int64_t from = src0 + (int64_t)(pth != nullptr ? pth[jr] : jr) * node + w * 32 + 2 * j;
+    const Block k = quantise(ok ? __ldg(reinterpret_cast<const uint32_t*>(k_new + from)) : 0u);
+    const Block v = quantise(ok ? __ldg(reinterpret_cast<const uint32_t*>(v_new + from)) : 0u);
+    if (!ok) continue;
+    const int64_t pos = (int64_t)len + jr;
+    const int64_t at = (int64_t)layer * kv.layer_stride +
+                       ((int64_t)row[pos / kv.page_size] * kv.n_kv_heads + h) * kv.page_size + pos % kv.page_size;
+    const int64_t to = at * (hd / 32) + u;
+    if (j < 8) {
+      reinterpret_cast<uint16_t*>(kv.k_qs)[to * 8 + j] = (uint16_t)k.bytes;
+      reinterpret_cast<uint16_t*>(kv.v_qs)[to * 8 + j] = (uint16_t)v.bytes;
+    }
+    if (j == 0) {
+      kv.k_scales[to] = (uint16_t)k.scale;
+      kv.v_scales[to] = (uint16_t)v.scale;
+    }
+  }
+}
+
+// The lengths advanced in place, after every CTA of the commit has read them.
+__global__ void q4_advance_kernel(int n, const int32_t* __restrict__ slots, const int32_t* __restrict__ n_path,
+                                  int32_t* len, const int32_t* __restrict__ status) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < n && status[i] == 0) len[slots[i]] += n_path[i];
+}
+
+// Rows out of the cache: a lane has two elements.
+__global__ void __launch_bounds__(PQ_THREADS)
+q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt, const int32_t* __restrict__ pos0,
+               const int32_t* __restrict__ n_pos, uint16_t* __restrict__ k, uint16_t* __restrict__ v, int n,
+               int64_t layer_stride, int blocks, int32_t* __restrict__ status) {
+  const int i = blockIdx.x / (kv.n_layers * blocks);
+  const int layer = blockIdx.x / blocks % kv.n_layers, blk = blockIdx.x % blocks;
+  const int slot = slots[i], np = n_pos[i], p0 = pos0[i];
+  int st = 0;
+  if (slot < 0 || slot >= kv.n_slots) st |= SPEC_ST_SLOT;
+  if (np < 0 || np > nt) st |= SPEC_ST_TREE;
+  if (p0 < 0 || (int64_t)p0 + max(np, 0) > (int64_t)kv.max_pages * kv.page_size) st |= SPEC_ST_FULL;
+  const int32_t* row = kv.table + (int64_t)(st == 0 ? slot : 0) * kv.max_pages;
+  bool bad = false;
+  if (st == 0 && np > 0) {
+    const int e1 = (int)(((int64_t)p0 + np - 1) / kv.page_size);
+    for (int e = p0 / kv.page_size + threadIdx.x; e <= e1; e += PQ_THREADS) bad |= row[e] < 0 || row[e] >= kv.n_pages;
+  }
+  if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
+  if (layer == 0 && blk == 0 && threadIdx.x == 0) status[i] = st;
+  if (st != 0) return;
+  const int hd = kv.head_dim, node = kv.n_kv_heads * hd;
+  const int64_t dst0 = (int64_t)layer * layer_stride + (int64_t)i * nt * node;
+  const int r0 = blk * CQ_ROWS, r1 = min(np, r0 + CQ_ROWS);
+  const int per = node / 32;
+  const int64_t count = (int64_t)max(0, r1 - r0) * per * 16;
+  for (int64_t e = threadIdx.x; e < count; e += PQ_THREADS) {
+    const int j = (int)(e & 15);
+    const int64_t b = e >> 4;
+    const int jr = r0 + (int)(b / per), w = (int)(b % per), h = w / (hd / 32), u = w % (hd / 32);
+    const int64_t pos = (int64_t)p0 + jr;
+    const int64_t at = (int64_t)layer * kv.layer_stride +
+                       ((int64_t)row[pos / kv.page_size] * kv.n_kv_heads + h) * kv.page_size + pos % kv.page_size;
+    const int64_t from = at * (hd / 32) + u, to = dst0 + (int64_t)jr * node + w * 32 + 2 * j;
+    auto pair = [&](const uint8_t* qs, const uint16_t* sc) {
+      const uint32_t c = reinterpret_cast<const uint16_t*>(qs)[from * 8 + (j & 7)] >> (j >= 8 ? 4 : 0);
+      const float s = half_of(sc[from], 0);
+      const __half2 x = __floats2half2_rn(s * (float)((int)(c & 15u) - 8), s * (float)((int)(c >> 8 & 15u) - 8));
+      return *reinterpret_cast<const uint32_t*>(&x);
+    };
+    *reinterpret_cast<uint32_t*>(k + to) = pair(kv.k_qs, kv.k_scales);
+    *reinterpret_cast<uint32_t*>(v + to) = pair(kv.v_qs, kv.v_scales);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// copies of pages: the four planes of the first positions of a page
+// ---------------------------------------------------------------------------
+// Units [e0, e1) of plane `which` of one layer: a head's positions are `unit`
+// bytes each (codes: head_dim / 2, scales: head_dim / 16), moved WORD bytes at a
+// time.
+template <class WORD>
+__device__ __forceinline__ void copy_plane(const uint8_t* s, uint8_t* d, uint32_t head, uint32_t run, uint32_t e0,
+                                           uint32_t e1) {
+  constexpr int U = 8;
+  const WORD* src = reinterpret_cast<const WORD*>(s);
+  WORD* dst = reinterpret_cast<WORD*>(d);
+  const bool whole = run == head;
+  for (uint32_t b = e0 + threadIdx.x; b < e1; b += PQ_THREADS * U) {
+    WORD t[U];
+    uint32_t at[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const uint32_t e = b + u * PQ_THREADS;
+      at[u] = whole ? e : e / run * head + e % run;
+      if (e < e1) t[u] = __ldcs(src + at[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (b + u * PQ_THREADS < e1) __stcs(dst + at[u], t[u]);
+  }
+}
+
+constexpr uint32_t CPQ_WORDS = 8192;  // words of one CTA
+
+// Part `part` of the copy of one page: (layer, K or V, codes or scales' words).
+struct CopyShape {
+  int code_blocks, scale_blocks;  // CTAs of a plane of a whole page
+  __host__ __device__ int per_layer() const { return 2 * (code_blocks + scale_blocks); }
+};
+__host__ __device__ inline CopyShape copy_shape(int nkv, int page, int hd) {
+  const int64_t rows = (int64_t)nkv * page;
+  CopyShape c;
+  c.code_blocks = (int)((rows * (hd / 32) + CPQ_WORDS - 1) / CPQ_WORDS);   // 16 bytes a word
+  c.scale_blocks = (int)((rows * (hd / 32) + CPQ_WORDS - 1) / CPQ_WORDS);  // 2 bytes a word
+  return c;
+}
+__device__ __forceinline__ void copy_part(const spec_pages_q4& kv, const CopyShape& c, int part, int src, int dst,
+                                          int n_pos) {
+  const int layer = part / c.per_layer(), x = part % c.per_layer();
+  const int which = x / (c.code_blocks + c.scale_blocks), y = x % (c.code_blocks + c.scale_blocks);
+  const int nb = kv.head_dim / 32;
+  const int64_t page = (int64_t)kv.n_kv_heads * kv.page_size * nb, base = (int64_t)layer * kv.layer_stride * nb;
+  const uint32_t head = kv.page_size * nb, run = n_pos * nb, words = run * kv.n_kv_heads;
+  if (y < c.code_blocks) {
+    uint8_t* p = which ? kv.v_qs : kv.k_qs;
+    const uint32_t e0 = y * CPQ_WORDS;
+    copy_plane<uint4>(p + (base + src * page) * 16, p + (base + dst * page) * 16, head, run, e0,
+                      min(words, e0 + CPQ_WORDS));
+  } else {
+    uint8_t* p = reinterpret_cast<uint8_t*>(which ? kv.v_scales : kv.k_scales);
+    const uint32_t e0 = (y - c.code_blocks) * CPQ_WORDS;
+    copy_plane<unsigned short>(p + (base + src * page) * 2, p + (base + dst * page) * 2, head, run, e0,
+                               min(words, e0 + CPQ_WORDS));
+  }
+}
+
+__global__ void __launch_bounds__(PQ_THREADS)
+q4_copy_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
+               const int32_t* __restrict__ n_pos, const CopyShape c, int32_t* __restrict__ status) {
+  const int per = kv.n_layers * c.per_layer();
+  const int i = blockIdx.x / per, part = blockIdx.x % per;
+  const int a = src[i], b = dst[i];
+  const int np = n_pos != nullptr ? n_pos[i] : kv.page_size;
+  int st = 0;
+  if (a < 0 || a >= kv.n_pages || b < 0 || b >= kv.n_pages) st |= SPEC_ST_SLOT;
+  if (np < 0 || np > kv.page_size) st |= SPEC_ST_PAGE;
+  bool hit = a == b;  // what another entry writes or reads, or reads what one writes
+  for (int j = threadIdx.x; j < n; j += PQ_THREADS) {
+    const int s = src[j], d = dst[j];
+    hit |= (j != i && d == b) || s == b || d == a;
+  }
+  if (__syncthreads_or(hit)) st |= SPEC_ST_SLOT;
+  if (part == 0 && threadIdx.x == 0) status[i] = st;
+  if (st == 0 && np > 0) copy_part(kv, c, part, a, b, np);
+}
+
+// The filled positions of the pages that an extension has replaced: one CTA per
+// (entry, layer, part of the page).
+__global__ void __launch_bounds__(PQ_THREADS)
+q4_cow_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, const int32_t* __restrict__ copies,
+              const CopyShape c) {
+  const int per = kv.n_layers * c.per_layer(), i = blockIdx.x / per;
+  grid_dep_wait();
+  const int a = copies[2 * i], b = copies[2 * i + 1];
+  if (a < 0) return;
+  copy_part(kv, c, blockIdx.x % per, a, b, kv.len[slots[i]] % kv.page_size);
+}
+
+int check_list(const void* a, const void* status, int n) {
+  if (a == nullptr || status == nullptr) return fail(SPEC_E_INVALID, "null argument");
+  if (n < 1) return fail(SPEC_E_SHAPE, "n >= 1 required");
+  return SPEC_OK;
+}
+int launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+// Rows of fp16 in or out beside the cache.
+int check_rows(const spec_pages_q4* kv, int n, int nt, const void* k, const void* v, int64_t* stride) {
+  if (k == nullptr || v == nullptr) return fail(SPEC_E_INVALID, "null argument");
+  if (nt < 1) return fail(SPEC_E_SHAPE, "nt >= 1 required");
+  if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15u) != 0)
+    return fail(SPEC_E_SHAPE, "k and v rows must be 16-byte aligned");
+  const double rows = (double)n * nt * kv->n_kv_heads * kv->head_dim;
+  if (rows > 4.0e15 || (double)*stride * kv->n_layers > 4.0e15) return fail(SPEC_E_SHAPE, "the rows are too large");
+  const int64_t layer = (int64_t)n * nt * kv->n_kv_heads * kv->head_dim;
+  if (*stride == 0) *stride = layer;
+  if (*stride % 8 != 0 || (kv->n_layers > 1 && *stride < layer))
+    return fail(SPEC_E_SHAPE, "the rows' layer stride must be a multiple of 8 and hold a layer's rows");
+  if ((double)n * kv->n_layers * ((nt + CQ_ROWS - 1) / CQ_ROWS) > INT32_MAX)
+    return fail(SPEC_E_SHAPE, "n * n_layers * nt too large");
+  return SPEC_OK;
+}
+
+}  // namespace
+
+// The bookkeeping of a cache in 4 bits as spec_pages (k and v are not to be
+// read: they stand for the codes).
+spec_pages book_of(const spec_pages_q4* kv) {
+  spec_pages p;
+  p.k = reinterpret_cast<uint16_t*>(kv->k_qs);
+  p.v = reinterpret_cast<uint16_t*>(kv->v_qs);
+  p.layer_stride = kv->layer_stride * kv->head_dim;
+  p.n_layers = kv->n_layers;
+  p.n_pages = kv->n_pages;
+  p.n_kv_heads = kv->n_kv_heads;
+  p.page_size = kv->page_size;
+  p.head_dim = kv->head_dim;
+  p.n_slots = kv->n_slots;
+  p.max_pages = kv->max_pages;
+  p.table = kv->table;
+  p.refs = kv->refs;
+  p.len = kv->len;
+  return p;
+}
+
+int check_pages_q4(const spec_pages_q4* kv, bool book) {
+  if (kv == nullptr || kv->k_qs == nullptr || kv->v_qs == nullptr || kv->k_scales == nullptr || kv->v_scales == nullptr)
+    return fail(SPEC_E_INVALID, "null pages or cache");
+  if (kv->head_dim < 32 || kv->head_dim % 32 != 0)
+    return fail(SPEC_E_SHAPE, "bad page dimensions (head_dim must be a multiple of 32)");
+  if (((reinterpret_cast<uintptr_t>(kv->k_qs) | reinterpret_cast<uintptr_t>(kv->v_qs) |
+        reinterpret_cast<uintptr_t>(kv->k_scales) | reinterpret_cast<uintptr_t>(kv->v_scales)) & 15u) != 0)
+    return fail(SPEC_E_SHAPE, "codes and scales must be 16-byte aligned");
+  if (kv->layer_stride < 0 || (double)kv->layer_stride * kv->head_dim > 4.0e15)
+    return fail(SPEC_E_SHAPE, "bad layer_stride");
+  const spec_pages p = book_of(kv);
+  return check_pages(&p, book);
+}
+
+extern "C" int spec_pages_q4_copy(const spec_pages_q4* kv, int n, const int32_t* src, const int32_t* dst,
+                                  const int32_t* n_pos, int32_t* status, void* stream) {
+  int rc = check_pages_q4(kv, false);
+  if (rc == SPEC_OK) rc = check_list(src, status, n);
+  if (rc == SPEC_OK) rc = check_list(dst, status, n);
+  if (rc != SPEC_OK) return rc;
+  const CopyShape c = copy_shape(kv->n_kv_heads, kv->page_size, kv->head_dim);
+  const double grid = (double)n * kv->n_layers * c.per_layer();
+  if (grid > INT32_MAX) return fail(SPEC_E_SHAPE, "n * n_layers * page too large");
+  q4_copy_kernel<<<(unsigned)grid, PQ_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(*kv, n, src, dst, n_pos, c,
+                                                                                          status);
+  return launched("4-bit page copy");
+}
+
+extern "C" int spec_pages_q4_fork(const spec_pages_q4* kv, int n, const int32_t* src, const int32_t* dst,
+                                  int32_t* status, void* stream) {
+  const int rc = check_pages_q4(kv, true);
+  if (rc != SPEC_OK) return rc;
+  const spec_pages p = book_of(kv);
+  return spec_pages_fork(&p, n, src, dst, status, stream);
+}
+
+extern "C" int spec_pages_q4_free(const spec_pages_q4* kv, int n, const int32_t* slots, int32_t* status,
+                                  void* stream) {
+  const int rc = check_pages_q4(kv, true);
+  if (rc != SPEC_OK) return rc;
+  const spec_pages p = book_of(kv);
+  return spec_pages_free(&p, n, slots, status, stream);
+}
+
+extern "C" int spec_pages_q4_extend(const spec_pages_q4* kv, int n, const int32_t* slots, const int32_t* n_new,
+                                    int32_t* copies, int32_t* status, void* stream) {
+  int rc = check_pages_q4(kv, true);
+  if (rc != SPEC_OK) return rc;
+  const spec_pages p = book_of(kv);
+  const CopyShape c = copy_shape(kv->n_kv_heads, kv->page_size, kv->head_dim);
+  if ((double)std::max(n, 1) * kv->n_layers * c.per_layer() > INT32_MAX)
+    return fail(SPEC_E_SHAPE, "n * n_layers * page too large");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  rc = launch_extend_book(&p, n, slots, n_new, copies, status, st);
+  if (rc != SPEC_OK) return rc;
+  const cudaError_t e = launch_dependent(q4_cow_kernel, (size_t)n * kv->n_layers * c.per_layer(), PQ_THREADS, 0, st,
+                                         *kv, slots, (const int32_t*)copies, c);
+  if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("4-bit page extend: ") + cudaGetErrorString(e));
+  return SPEC_OK;
+}
+
+extern "C" int spec_pages_q4_commit(const spec_pages_q4* kv, int n, const int32_t* slots, int nt,
+                                    const uint16_t* k_new, const uint16_t* v_new, int64_t new_layer_stride,
+                                    const int32_t* path, const int32_t* n_path, int32_t* new_len, int32_t* status,
+                                    void* stream) {
+  int rc = check_pages_q4(kv, true);
+  if (rc == SPEC_OK) rc = check_list(slots, status, n);
+  if (rc == SPEC_OK && n_path == nullptr) rc = fail(SPEC_E_INVALID, "null argument");
+  if (rc == SPEC_OK) rc = check_rows(kv, n, nt, k_new, v_new, &new_layer_stride);
+  if (rc != SPEC_OK) return rc;
+  const int blocks = (nt + CQ_ROWS - 1) / CQ_ROWS;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // lengths written where they are read from go up in a kernel behind
+  const uintptr_t a = reinterpret_cast<uintptr_t>(kv->len), b = reinterpret_cast<uintptr_t>(new_len);
+  const uintptr_t bytes = (uintptr_t)kv->n_slots * sizeof(int32_t);
+  const bool in_place = new_len == nullptr || a == b;
+  if (!in_place && a < b + bytes && b < a + bytes)
+    return fail(SPEC_E_INVALID, "new_len overlaps len without being len");
+  q4_commit_kernel<<<(unsigned)(n * kv->n_layers * blocks), PQ_THREADS, 0, st>>>(
+      *kv, n, slots, nt, k_new, v_new, new_layer_stride, path, n_path, in_place ? nullptr : new_len, blocks, status);
+  if (in_place)
+    q4_advance_kernel<<<(n + 127) / 128, 128, 0, st>>>(n, slots, n_path, kv->len, status);
+  return launched("4-bit page commit");
+}
+
+extern "C" int spec_pages_q4_read(const spec_pages_q4* kv, int n, const int32_t* slots, int nt, const int32_t* pos0,
+                                  const int32_t* n_pos, uint16_t* k, uint16_t* v, int64_t layer_stride,
+                                  int32_t* status, void* stream) {
+  int rc = check_pages_q4(kv, true);
+  if (rc == SPEC_OK) rc = check_list(slots, status, n);
+  if (rc == SPEC_OK && (pos0 == nullptr || n_pos == nullptr)) rc = fail(SPEC_E_INVALID, "null argument");
+  if (rc == SPEC_OK) rc = check_rows(kv, n, nt, k, v, &layer_stride);
+  if (rc != SPEC_OK) return rc;
+  const int blocks = (nt + CQ_ROWS - 1) / CQ_ROWS;
+  q4_read_kernel<<<(unsigned)(n * kv->n_layers * blocks), PQ_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      *kv, slots, nt, pos0, n_pos, k, v, n, layer_stride, blocks, status);
+  return launched("4-bit page read");
+}

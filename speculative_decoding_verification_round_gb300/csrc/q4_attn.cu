@@ -1,0 +1,376 @@
+// q4_attn.cu -- tree attention over a cache held in 4 bits (spec_tree_attn_q4).
+//
+// The units, their cut over the CTAs, the trees and the joining kernel are
+// those of the cache in fp16 (tree_attn.cuh, tree_attn.cu); the tree's own
+// nodes are fp16 here, too.  The kernel streams the codes and scales as they
+// are, 0.28 of the bytes of fp16, and makes the operands of the products
+// in registers (key_warp.cuh): a tile of fp16 in shared memory between would
+// be written and read once, 8 cycles of the SM's shared memory a position of
+// 128 dimensions where the HBM delivers one in 6.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "key_warp.cuh"
+#include "tree_attn.cuh"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Every warp has 32 positions of a tile of 128 and a ring of its own for them,
+// so that no barrier stands between the tiles; the four warps' results are
+// joined at the end of a piece.
+// ---------------------------------------------------------------------------
+constexpr int QA_SHIFT = 7, QA_KEYS = 1 << QA_SHIFT, QA_THREADS = 128, QA_WARPS = 4, WARP_KEYS = 32;
+
+template <int HD, int NT>
+struct QShape {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int STAGES = 3;
+  static constexpr int KT = NT == 4 ? 1 : 2;  // tiles of 16 keys a step
+  static constexpr int CODES = WARP_KEYS * HD / 2, SCALES = WARP_KEYS * HD / 16;
+  static constexpr int STAGE = 2 * (CODES + SCALES);  // bytes: K's and V's codes, K's and V's scales
+  static constexpr int RING = STAGES * STAGE;         // of a warp
+  static constexpr int XROW = HD + 4;                 // floats of an exchange row (padded)
+  static constexpr int EXCHANGE = QA_WARPS * ROWS * (XROW * 4 + 8);
+  static constexpr int NODES = NT == 4 ? 64 : 16;     // rows of the tree's own tile
+  static constexpr int TREE_OFF = QA_WARPS * RING > EXCHANGE ? QA_WARPS * RING : (EXCHANGE + 127) / 128 * 128;
+  static constexpr int Q_OFF = TREE_OFF + 2 * NODES * HD * 2;
+  static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, true>::Q_BYTES;
+  static constexpr size_t SMEM = SUM_OFF + KeyWarp<HD, NT, true>::SUM_BYTES;
+  static constexpr int RESIDENT = NT == 4 ? 2 : HD == 128 ? 3 : 5;
+};
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_kernel(const TreeArgs a) {
+  using Sh = QShape<HD, NT>;
+  using KW = KeyWarp<HD, NT, true>;
+  constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, KT = Sh::KT, UNITS = HD / 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ TreeSmem s_tree;
+  __shared__ long long s_part[QA_WARPS];
+  __shared__ Start s_at;
+  grid_dep_begin();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_cta = gridDim.x - 1;
+  if ((int)blockIdx.x == n_cta) {
+    plan_sequences<QA_THREADS>(a, ROWS, QA_SHIFT, n_cta, s_part, smem);
+    return;
+  }
+  Start start;
+  long long left = find_range<QA_THREADS>(a, ROWS, QA_SHIFT, n_cta, s_part, smem, &s_at, start);
+  if (left <= 0) {
+    check_others<QA_THREADS>(a, ROWS, QA_SHIFT, n_cta, QA_WARPS);
+    return;
+  }
+  int s = start.s;
+  long long off = start.off;
+  SeqInfo q = start.q;
+  bool first = true, new_tree = true;
+
+  const uint32_t sm0 = kw_smem(smem), ring = sm0 + warp * Sh::RING;
+  const uint32_t kn0 = sm0 + Sh::TREE_OFF, vn0 = kn0 + Sh::NODES * HD * 2;
+  const uint32_t qs = sm0 + Sh::Q_OFF, sums = sm0 + Sh::SUM_OFF;
+  KW kw;
+  while (left > 0) {
+    if (off >= q.work()) {  // the next sequence with work
+      s++;
+      off = 0;
+      q = seq_info(a, s, ROWS, QA_SHIFT);
+      new_tree = true;
+      continue;
+    }
+    const int unit = (int)div_ll(off, q.tiles), t0 = (int)(off - (long long)unit * q.tiles);
+    const int t1 = (int)min((long long)q.tiles, t0 + left);
+    const int kvh = unit % a.nkv, row0 = unit / a.nkv * ROWS, M = q.m * a.G;
+    const int n_sink = q.n_sink, w_tile = q.w_tile, last = q.tiles - 1;
+    auto tile_base = [&](int t) { return (t < n_sink ? t : w_tile + t - n_sink) * QA_KEYS; };
+    // the cache row of this lane's position of tile t, ~0 for zeros: looked up a
+    // tile ahead of its load (2^32 rows of 64 dimensions would be 300 GB)
+    auto lookup = [&](int t) {
+      uint32_t x = ~0u;
+      if (t < t1 && t != last) {
+        const int pos = tile_base(t) + warp * WARP_KEYS + lane;
+        if (pos < q.len) {
+          const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+          const int pg = a.table[(int64_t)q.slot * a.max_pages + e];
+          if (pg >= 0 && pg < a.n_pages)
+            x = ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
+        }
+      }
+      return x;
+    };
+    auto load_tile = [&](int t, uint32_t at) {
+      if (t != last) {
+        const uint32_t st = ring + (t % STAGES) * Sh::STAGE, ss = st + 2 * Sh::CODES;
+        constexpr int CH = HD / 32, PER = 32 / CH;  // 16-byte chunks of a row, rows a pass
+        const int c = lane % CH;
+#pragma unroll
+        for (int i = 0; i < CH; i++) {
+          const int r = i * PER + lane / CH;
+          const uint32_t x = __shfl_sync(0xffffffffu, at, r);
+          const bool ok = x != ~0u;
+          const uint64_t from = (uint64_t)(ok ? x : 0u) * (HD / 2) + c * 16;
+          const uint32_t to = st + r * (HD / 2) + ((c ^ q4_swz<HD>(r)) << 4);
+          kw_copy<16>(to, a.k_qs + from, ok);
+          kw_copy<16>(to + Sh::CODES, a.v_qs + from, ok);
+        }
+        const bool ok = at != ~0u;
+        const uint64_t from = (uint64_t)(ok ? at : 0u) * (HD / 32);
+        kw_copy<HD / 16>(ss + lane * (HD / 16), a.k_scales + from, ok);
+        kw_copy<HD / 16>(ss + Sh::SCALES + lane * (HD / 16), a.v_scales + from, ok);
+      } else if (16 * warp < q.m) {  // this warp's sixteen nodes
+        const int64_t from = (int64_t)s * a.nt * a.kv_stride + kvh * HD;
+#pragma unroll
+        for (int e = lane; e < 16 * UNITS; e += 32) {
+          const int r = 16 * warp + e / UNITS, u = e % UNITS;
+          const bool ok = r < q.m;
+          const int64_t at_r = from + (ok ? r : 0) * a.kv_stride + u * 8;
+          kw_copy<16>(kn0 + f16_off<HD>(r, u), a.k_new + at_r, ok);
+          kw_copy<16>(vn0 + f16_off<HD>(r, u), a.v_new + at_r, ok);
+        }
+      }
+    };
+
+    // ---- the piece's first tiles, and its q rows
+    uint32_t ahead[STAGES];
+#pragma unroll
+    for (int i = 0; i < STAGES; i++) ahead[i] = lookup(t0 + i);
+    if (new_tree) load_tree(a, s, q.m, s_tree);
+    new_tree = false;
+    __syncthreads();  // the last piece's exchange and q rows have been read
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; i++) {
+      if (t0 + i < t1) load_tile(t0 + i, ahead[i]);
+      asm volatile("cp.async.commit_group;");
+    }
+    KW::put_queries(qs, sums, tid, QA_THREADS, [&](int r) -> const __half* {
+      const int m = row0 + r;
+      if (m >= M) return nullptr;
+      const int node = node_of(a, m);
+      return a.q + ((int64_t)s * a.nt + node) * a.q_stride + (kvh * a.G + m - node * a.G) * HD;
+    });
+    __syncthreads();
+    kw.begin();
+    const int gk = key_row(kw.g);
+    // bits of the keys (gk, 8 + gk, ...; two a tile of 16) that row 8 n + 2 t + h sees
+    // of a tile at `base`, or of the tree's
+    auto visible = [&](int t, int base, int n, int h) {
+      const int m = row0 + 8 * n + 2 * kw.t + h, node = m < M ? node_of(a, m) : 0;
+      const int pos = q.len + s_tree.depth[node];
+      const unsigned long long anc = m < M ? s_tree.anc[node] : 0ull;
+      uint32_t bits = 0u;
+      const int count = t == last ? 2 : WARP_KEYS / 8;
+#pragma unroll
+      for (int i = 0; i < WARP_KEYS / 8; i++) {
+        if (i >= count) break;
+        bool see;
+        int p;
+        if (t == last) {
+          const int key = 16 * warp + 8 * i + gk;
+          see = (anc >> key) & 1;
+          p = q.len + (see ? s_tree.depth[key] : 0);
+        } else {
+          p = base + 8 * i + gk;
+          see = p < q.len;
+        }
+        if (a.window > 0) see = see && (p < a.sinks || p > pos - a.window);
+        bits |= (uint32_t)see << i;
+      }
+      return bits;
+    };
+
+    for (int t = t0; t < t1; t++) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+      __syncwarp();
+      if (t + STAGES - 1 < t1) load_tile(t + STAGES - 1, ahead[STAGES - 1]);
+      asm volatile("cp.async.commit_group;");
+      ahead[STAGES - 1] = lookup(t + STAGES);
+      if (t == last) {
+        if (16 * warp >= q.m) continue;
+        const uint32_t ks = kn0 + f16_off<HD>(16 * warp, 0), vs = vn0 + f16_off<HD>(16 * warp, 0);
+        float x[1][NT][4];
+        kw.scores_f16(ks, qs, a.scale_log2, x[0]);
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const uint32_t bits = visible(t, 0, n, h);
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+              if (!(bits >> i & 1)) x[0][n][2 * i + h] = -INFINITY;
+          }
+        kw.template weights<1>(x);
+        bool odd = false;
+#pragma unroll
+        for (int e = lane; e < 16 * UNITS; e += 32) {
+          const uint4 v = kw_lds128(vs + e * 16);
+          odd |= odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w);
+        }
+        if (__any_sync(0xffffffffu, odd))
+          kw.values_slow(x[0], [&](int r, int d) {
+            return kw_half(kw_lds16(vs + f16_off<HD>(r, d >> 3) + 2 * (d & 7)), 0);
+          });
+        else
+          kw.values_f16(vs, x[0]);
+        continue;
+      }
+      const uint32_t ks = ring + (t % STAGES) * Sh::STAGE, vs = ks + Sh::CODES, kss = vs + Sh::CODES,
+                     vss = kss + Sh::SCALES;
+      const int base = tile_base(t) + warp * WARP_KEYS;
+      const bool masked = base + WARP_KEYS > q.len ||
+                          (a.window > 0 && base + WARP_KEYS > q.sinks && base < q.lo + SPEC_MAX_TREE);
+      bool odd = false;
+      if (masked)  // this lane's position's scales
+#pragma unroll
+        for (int b = 0; b < HD / 32; b++) odd |= odd_half(kw_lds16(vss + lane * (HD / 16) + 2 * b));
+      odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+      for (int i0 = 0; i0 < WARP_KEYS / 16; i0 += KT) {
+        float x[KT][NT][4];
+        const uint32_t kt = i0 * 16;
+        kw.template scores_q4<KT>(ks + kt * (HD / 2), kss + kt * (HD / 16), qs, sums, a.scale_log2, x);
+        if (masked) {
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const uint32_t bits = visible(t, base, n, h) >> (2 * i0);
+#pragma unroll
+              for (int i = 0; i < 2 * KT; i++)
+                if (!(bits >> i & 1)) x[i >> 1][n][2 * (i & 1) + h] = -INFINITY;
+            }
+        }
+        kw.template weights<KT>(x);
+#pragma unroll
+        for (int i = 0; i < KT; i++) {
+          const uint32_t vt = vs + (kt + 16 * i) * (HD / 2), st = vss + (kt + 16 * i) * (HD / 16);
+          if (odd)
+            kw.values_slow(x[i], [&](int r, int d) {
+              const int b = d >> 5, j = d & 31;
+              const uint32_t w = kw_lds32(vt + r * (HD / 2) + ((b ^ q4_swz<HD>(r)) << 4) + (j & 12));
+              const int u = (w >> (8 * (j & 3) + (j >> 4) * 4)) & 15;
+              return (float)(u - 8) * kw_half(kw_lds16(st + r * (HD / 16) + 2 * b), 0);
+            });
+          else
+            kw.values_q4(vt, st, x[i]);
+        }
+      }
+    }
+    // ---- the end of the piece: the warps' results through shared memory
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the rings have been read
+    float* x = reinterpret_cast<float*>(smem);
+    float2(*s_ml)[ROWS] = reinterpret_cast<float2(*)[ROWS]>(x + (size_t)QA_WARPS * ROWS * Sh::XROW);
+    kw.template put<Sh::XROW>(x + (size_t)warp * ROWS * Sh::XROW, s_ml[warp]);
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == q.tiles;
+    const size_t slot = (size_t)blockIdx.x * 2 + (first ? 0 : 1);
+#pragma unroll
+    for (int e0 = 0; e0 < ROWS * UNITS; e0 += QA_THREADS) {
+      const int e = e0 + tid;
+      if (ROWS * UNITS % QA_THREADS != 0 && e >= ROWS * UNITS) break;
+      // rows of the output are contiguous, rows of a piece are neighbours
+      const int r = whole ? e / UNITS : e % ROWS, u = whole ? e % UNITS : e / ROWS, m = row0 + r;
+      if (m >= M) continue;
+      float m2 = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < QA_WARPS; k++) m2 = fmaxf(m2, s_ml[k][r].x);
+      const float ref = m2 == -INFINITY ? 0.0f : m2;
+      float acc[8] = {}, l = 0.0f;
+#pragma unroll
+      for (int k = 0; k < QA_WARPS; k++) {
+        const float2 ml = s_ml[k][r];
+        const float wk = kw_exp2(ml.x - ref);
+        l = fmaf(ml.y, wk, l);
+        const float4* src = reinterpret_cast<const float4*>(x + ((size_t)k * ROWS + r) * Sh::XROW + u * 8);
+        const float4 s0 = src[0], s1 = src[1];
+        const float v[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+        for (int d = 0; d < 8; d++) acc[d] = fmaf(v[d], wk, acc[d]);
+      }
+      if (whole) {
+        const float inv = 1.0f / l;
+        const int node = node_of(a, m), hd = kvh * a.G + m - node * a.G;
+        *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + hd) * HD + u * 8) =
+            make_uint4(kw_pack(acc[0] * inv, acc[1] * inv), kw_pack(acc[2] * inv, acc[3] * inv),
+                       kw_pack(acc[4] * inv, acc[5] * inv), kw_pack(acc[6] * inv, acc[7] * inv));
+      } else {
+        float4* po = reinterpret_cast<float4*>(a.part_o) + (slot * (HD / 4) + 2 * u) * ROWS + r;
+        po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        po[ROWS] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (u == 0) a.part_ml[slot * ROWS + r] = make_float2(m2, l);
+      }
+    }
+    left -= t1 - t0;
+    off += t1 - t0;
+    first = false;
+  }
+  check_others<QA_THREADS>(a, ROWS, QA_SHIFT, n_cta, QA_WARPS);
+}
+
+// Query rows of a unit.
+int q4_rows(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : 32; }
+
+int q4_resident(int hd, int rows) {
+  return rows == 32 ? QShape<128, 4>::RESIDENT : hd == 128 ? QShape<128, 1>::RESIDENT : QShape<64, 1>::RESIDENT;
+}
+// The CTAs with tiles: what is resident, but for the one that plans.
+int q4_ctas(int hd, int rows) { return std::max(1, q4_resident(hd, rows) * device_sms() - 1); }
+
+template <int HD, int NT>
+cudaError_t launch_q4(const TreeArgs& a, int n_cta, cudaStream_t st) {
+  return launch_dependent(q4_attn_kernel<HD, NT>, n_cta + 1, QA_THREADS, QShape<HD, NT>::SMEM, st, a);
+}
+template <int HD>
+cudaError_t launch_q4_rows(const TreeArgs& a, int n_cta, cudaStream_t st) {
+  return a.rows == 8    ? launch_q4<HD, 1>(a, n_cta, st)
+         : a.rows == 16 ? launch_q4<HD, 2>(a, n_cta, st)
+                        : launch_q4<HD, 4>(a, n_cta, st);
+}
+template <int HD, int NT>
+void init_q4() {
+  cudaFuncSetAttribute(q4_attn_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)QShape<HD, NT>::SMEM);
+}
+
+}  // namespace
+
+void q4_init_attrs() {
+  init_q4<64, 1>();
+  init_q4<64, 2>();
+  init_q4<64, 4>();
+  init_q4<128, 1>();
+  init_q4<128, 2>();
+  init_q4<128, 4>();
+}
+
+int q4_workspace(const spec_pages_q4* kv, int n_seq, int nt, int n_q_heads, size_t* bytes) {
+  const int rc = check_pages_q4(kv, true);
+  if (rc != SPEC_OK) return rc;
+  const spec_pages book = book_of(kv);
+  const int rc2 = tree_check(&book, n_seq, nt, n_q_heads);
+  if (rc2 != SPEC_OK) return rc2;
+  const int rows = q4_rows(nt * (n_q_heads / kv->n_kv_heads));
+  *bytes = tree_scratch(kv->head_dim, rows, q4_ctas(kv->head_dim, rows), n_seq);
+  return SPEC_OK;
+}
+
+int launch_tree_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, const uint16_t* q, int64_t q_stride,
+                   const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride, uint16_t* out, void* workspace,
+                   int32_t* status, cudaStream_t st) {
+  TreeArgs a;
+  const spec_pages book = book_of(kv);
+  const int hd = kv->head_dim, rows = q4_rows(t->nt * (t->n_q_heads / kv->n_kv_heads)), n_cta = q4_ctas(hd, rows);
+  tree_fill(a, &book, 0, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status, rows, QA_SHIFT, n_cta, false);
+  const int64_t row = (int64_t)layer * kv->layer_stride;
+  a.k_qs = kv->k_qs + row * (hd / 2);
+  a.v_qs = kv->v_qs + row * (hd / 2);
+  a.k_scales = reinterpret_cast<const __half*>(kv->k_scales) + row * (hd / 32);
+  a.v_scales = reinterpret_cast<const __half*>(kv->v_scales) + row * (hd / 32);
+  cudaError_t e = hd == 128 ? launch_q4_rows<128>(a, n_cta, st) : launch_q4_rows<64>(a, n_cta, st);
+  if (e == cudaSuccess) e = tree_join_launch(a, hd, n_cta, st);
+  if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("4-bit tree attention: ") + cudaGetErrorString(e));
+  return SPEC_OK;
+}

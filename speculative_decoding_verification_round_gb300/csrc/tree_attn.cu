@@ -605,19 +605,22 @@ cudaError_t launch_shape(const TreeArgs& a, int n_cta, cudaStream_t st) {
 }
 
 template <int HD>
+cudaError_t launch_join(const TreeArgs& a, int n_cta, cudaStream_t st) {
+  const int blocks = (a.nt * a.G + TJ_ROWS - 1) / TJ_ROWS;
+  const long long units = (long long)a.n_seq * blocks * a.nkv;
+  const bool split = units * 8 <= n_cta;
+  // (a slice of 32 dimensions a CTA as long as those are resident at once, eight an SM)
+  const int slices = split ? HD / 8 : units * (HD / 32) <= 8 * device_sms() ? HD / 32 : 1;
+  return launch_dependent(split ? tree_join_kernel<HD, true> : tree_join_kernel<HD, false>, (size_t)(units * slices),
+                          32 * join_warps(split), 0, st, a, blocks, slices);
+}
+
+template <int HD>
 int launch_hd(const TreeArgs& a, int n_cta, cudaStream_t st) {
   cudaError_t e = on_tc(a.rows)  ? tree_tc_launch(a, HD, n_cta, st)
                   : a.rows == 16 ? launch_shape<HD, 1>(a, n_cta, st)
                                  : launch_shape<HD, 2>(a, n_cta, st);
-  if (e == cudaSuccess) {
-    const int blocks = (a.nt * a.G + TJ_ROWS - 1) / TJ_ROWS;
-    const long long units = (long long)a.n_seq * blocks * a.nkv;
-    const bool split = units * 8 <= n_cta;
-    // (a slice of 32 dimensions a CTA as long as those are resident at once, eight an SM)
-    const int slices = split ? HD / 8 : units * (HD / 32) <= 8 * device_sms() ? HD / 32 : 1;
-    e = launch_dependent(split ? tree_join_kernel<HD, true> : tree_join_kernel<HD, false>, (size_t)(units * slices),
-                         32 * join_warps(split), 0, st, a, blocks, slices);
-  }
+  if (e == cudaSuccess) e = launch_join<HD>(a, n_cta, st);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("tree attention: ") + cudaGetErrorString(e));
   return SPEC_OK;
 }
@@ -631,7 +634,12 @@ void init_shape() {
 // The CTAs with tiles: what is resident, but for the one that plans.
 int tree_ctas(int hd, int rows) { return std::max(1, (on_tc(rows) ? 1 : resident(hd, rows)) * device_sms() - 1); }
 
-int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
+// Budget of the calling thread's calls for the first wait of a CTA (tree_set_wait_budget).
+thread_local int t_wait_tries = LIN_WAIT_TRIES;
+
+}  // namespace
+
+int tree_check(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
   int rc = check_pages(kv, true);
   if (rc != SPEC_OK) return rc;
   if (kv->head_dim != 64 && kv->head_dim != 128)
@@ -648,10 +656,9 @@ int check_tree(const spec_pages* kv, int n_seq, int nt, int n_q_heads) {
   return SPEC_OK;
 }
 
-// Budget of the calling thread's calls for the first wait of a CTA (tree_set_wait_budget).
-thread_local int t_wait_tries = LIN_WAIT_TRIES;
-
-}  // namespace
+cudaError_t tree_join_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st) {
+  return hd == 128 ? launch_join<128>(a, n_cta, st) : launch_join<64>(a, n_cta, st);
+}
 
 void tree_set_wait_budget(int tries) { t_wait_tries = tries; }
 
@@ -664,19 +671,22 @@ void tree_init_attrs() {
 }
 
 int tree_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads, size_t* bytes) {
-  const int rc = check_tree(kv, n_seq, nt, n_q_heads);
+  const int rc = tree_check(kv, n_seq, nt, n_q_heads);
   if (rc != SPEC_OK) return rc;
-  const size_t rows = rows_of(nt * (n_q_heads / kv->n_kv_heads));
-  const size_t n = tree_ctas(kv->head_dim, (int)rows);
-  *bytes = n * 2 * rows * (sizeof(float) * kv->head_dim + sizeof(float2)) +
-           (n * sizeof(uint32_t) + 15) / 16 * 16 + (size_t)n_seq * sizeof(TreePlan);
+  const int rows = rows_of(nt * (n_q_heads / kv->n_kv_heads));
+  *bytes = tree_scratch(kv->head_dim, rows, tree_ctas(kv->head_dim, rows), n_seq);
   return SPEC_OK;
 }
 
-int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,
-                int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride,
-                uint16_t* out, void* workspace, int32_t* status, cudaStream_t st) {
-  TreeArgs a;
+size_t tree_scratch(int hd, int rows, int n_cta, int n_seq) {
+  const size_t n = n_cta, r = rows;
+  return n * 2 * r * (sizeof(float) * hd + sizeof(float2)) + (n * sizeof(uint32_t) + 15) / 16 * 16 +
+         (size_t)n_seq * sizeof(TreePlan);
+}
+
+void tree_fill(TreeArgs& a, const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q, int64_t q_stride,
+               const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride, uint16_t* out, void* workspace,
+               int32_t* status, int rows, int tile_shift, int n_cta, bool bounded_waits) {
   a.k = reinterpret_cast<const __half*>(kv->k) + (int64_t)layer * kv->layer_stride;
   a.v = reinterpret_cast<const __half*>(kv->v) + (int64_t)layer * kv->layer_stride;
   a.table = kv->table;
@@ -707,14 +717,22 @@ int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint1
   a.kv_stride = kv_stride != 0 ? kv_stride : (int64_t)a.nkv * kv->head_dim;
   a.out = reinterpret_cast<__half*>(out);
   a.status = status;
-  const size_t rows = a.rows = rows_of(a.nt * a.G);
-  const int n_cta = tree_ctas(kv->head_dim, a.rows);
-  a.tile_shift = on_tc(a.rows) ? TREE_TC_SHIFT : TT_SHIFT;
+  a.rows = rows;
+  a.tile_shift = tile_shift;
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)n_cta * 2 * rows * kv->head_dim);
   uint32_t* err = reinterpret_cast<uint32_t*>(a.part_ml + (size_t)n_cta * 2 * rows);
-  a.part_err = on_tc(a.rows) ? err : nullptr;
+  a.part_err = bounded_waits ? err : nullptr;
   a.wait_tries = t_wait_tries;
   a.plan = reinterpret_cast<TreePlan*>(err + ((size_t)n_cta + 3) / 4 * 4);
+}
+
+int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,
+                int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride,
+                uint16_t* out, void* workspace, int32_t* status, cudaStream_t st) {
+  TreeArgs a;
+  const int rows = rows_of(t->nt * (t->n_q_heads / kv->n_kv_heads)), n_cta = tree_ctas(kv->head_dim, rows);
+  tree_fill(a, kv, layer, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status, rows,
+            on_tc(rows) ? TREE_TC_SHIFT : TT_SHIFT, n_cta, on_tc(rows));
   return kv->head_dim == 128 ? launch_hd<128>(a, n_cta, st) : launch_hd<64>(a, n_cta, st);
 }

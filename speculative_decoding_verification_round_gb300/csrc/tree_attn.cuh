@@ -32,6 +32,11 @@ struct TreeArgs {
   int wait_tries;      // budget of a CTA's first wait for scores (tree_set_wait_budget)
   struct TreePlan* plan;  // [n_seq]
   int32_t* status;
+  // a cache in 4 bits: the layer's codes and scales, in place of k and v
+  const uint8_t* k_qs;
+  const uint8_t* v_qs;
+  const __half* k_scales;
+  const __half* v_scales;
 };
 
 // One sequence's part of the cut, for the joining kernel.
@@ -406,3 +411,12 @@ __device__ __forceinline__ bool load_tree(const TreeArgs& a, int s, int m, TreeS
 constexpr int TREE_TC_SHIFT = 7;
 cudaError_t tree_tc_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st);
 void tree_tc_init_attrs();
+
+// What the kernels for the cache in fp16 and in 4 bits share (tree_attn.cu):
+// argument checks, a workspace's bytes, the arguments, the joining kernel.
+int tree_check(const spec_pages* kv, int n_seq, int nt, int n_q_heads);
+size_t tree_scratch(int hd, int rows, int n_cta, int n_seq);
+void tree_fill(TreeArgs& a, const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q, int64_t q_stride,
+               const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride, uint16_t* out, void* workspace,
+               int32_t* status, int rows, int tile_shift, int n_cta, bool bounded_waits);
+cudaError_t tree_join_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st);
