@@ -488,6 +488,7 @@ typedef struct {
 #define SPEC_ST_FULL 8   /* not enough free pages, or more positions than max_pages hold */
 #define SPEC_ST_TREE 16  /* bad parents, node count or path */
 #define SPEC_ST_TIMEOUT 32 /* a bounded device wait ran out */
+#define SPEC_ST_BLOCK 64   /* a block that the sequence does not have */
 
 #define SPEC_MAX_TREE 64 /* nodes of a tree */
 
@@ -753,6 +754,89 @@ int spec_tree_attn_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, co
 /* Bytes of workspace for spec_tree_attn_q4 on the current device. */
 int spec_tree_attn_q4_workspace(const spec_pages_q4* kv, int n_seq, int nt, int n_q_heads,
                                 size_t* bytes);
+
+/* The digests of a cache's blocks: `block` neighbouring positions of a page (16,
+ * 32, 64 or 128, a divisor of page_size) have the least and the largest value of
+ * every channel of their keys, in every layer and kv head.  Beside the cache, and
+ * addressed by its table: a page that several slots share has one digest. */
+typedef struct {
+  uint16_t* data; /* fp16 [n_layers][n_pages][n_kv_heads][page_size / block][2][head_dim], 16-byte
+                     aligned: the least values, then the largest */
+  int64_t layer_stride; /* elements from one layer to the next (>= a layer's, a multiple of 8) */
+  int32_t n_layers, n_pages, n_kv_heads, page_size; /* the cache's */
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t block;
+  int32_t n_slots, max_pages;
+  const int32_t* table; /* the cache's */
+  const int32_t* len;
+} spec_digest;
+
+/* Digests of the blocks that hold positions [pos0[i], len) of slot slots[i], in
+ * every layer, from all committed positions of these blocks (device int32 [n];
+ * pos0 NULL: from 0 on; the last block may be filled partly).  After a commit pos0 is the length in
+ * front of it; after an extension with a copy of a page it is the start of that
+ * page.  A NaN among a channel's keys makes both of its values NaN.  `kv` has the digest's sizes
+ * (its table and len are not looked at).  Slots may be named more than once.
+ * status: SPEC_ST_SLOT (slot out of range), SPEC_ST_FULL (pos0 below 0, or a length that the table cannot
+ * have), SPEC_ST_PAGE (no valid page for some block; the others are done). */
+int spec_block_digest(const spec_digest* dg, const spec_pages* kv, int n, const int32_t* slots,
+                      const int32_t* pos0, int32_t* status, void* stream);
+int spec_block_digest_q4(const spec_digest* dg, const spec_pages_q4* kv, int n, const int32_t* slots,
+                         const int32_t* pos0, int32_t* status, void* stream);
+
+/* Scores of every block of `layer` for each node's query: the largest logit that
+ * any key between the block's least and largest values could have with any of the
+ * kv head's query heads,
+ *   scores[s][i][h][j] = max over the heads g of h: sum_d max(q_gd lo_jd, q_gd hi_jd)
+ * (without the softmax's scale; fp32 sums), for the blocks j that hold positions
+ * [0, len).
+ *   slots, n_nodes  as in spec_tree; at most 64 query heads a kv head
+ *   q       fp16 as in spec_tree_attn
+ *   scores  fp32 [n_seq][nt][n_kv_heads][ld]; what no block stands for, and rows of nodes >=
+ *           n_nodes, is left as it was
+ *   status  int32 [n_seq]: SPEC_ST_SLOT, SPEC_ST_TREE (node count), SPEC_ST_FULL (a length that
+ *           the table cannot have, or more blocks than ld): no scores are written;
+ *           SPEC_ST_PAGE (no valid page for some block, whose scores are -infinity) */
+int spec_block_scores(const spec_digest* dg, int layer, int n_seq, const int32_t* slots, int nt,
+                      const int32_t* n_nodes, int n_q_heads, const uint16_t* q, int64_t q_stride,
+                      float* scores, int64_t ld, int32_t* status, void* stream);
+
+/* The blocks that each row of scores selects: the first n_first and the last n_last
+ * of the blocks that hold positions [0, len), and of the others those with the
+ * largest scores, n_keep in all (all blocks if there are no more).  Equal scores:
+ * the lowest block; a NaN counts as +infinity, -0 as 0.
+ *   len     int32 [n_slots], slots and n_nodes as above, scores fp32 [n_seq][nt][n_kv_heads][ld]
+ *   blocks  int32 [n_seq][nt][n_kv_heads][n_keep]: ascending, -1 behind; rows of nodes >=
+ *           n_nodes are left as they were
+ *   status  int32 [n_seq]: SPEC_ST_SLOT, SPEC_ST_TREE (node count), SPEC_ST_FULL (a length
+ *           below 0, or more blocks than ld): the rows are -1 then
+ * 1 <= n_keep <= 4096, n_first + n_last <= n_keep. */
+int spec_block_select(const int32_t* len, int n_slots, int block, int n_seq, const int32_t* slots,
+                      int nt, const int32_t* n_nodes, int n_kv_heads, const float* scores, int64_t ld,
+                      int n_keep, int n_first, int n_last, int32_t* blocks, int32_t* status,
+                      void* stream);
+
+/* Attention of the trees' nodes over the committed positions of selected blocks, a
+ * list for each node and kv head, and over themselves (a node sees itself and its
+ * ancestors), otherwise as spec_tree_attn.
+ *   t       window has to be 0 (SPEC_E_UNSUPPORTED: the lists take its place)
+ *   blocks  int32 [n_seq][nt][n_kv_heads][n_keep], n_keep <= 4096: blocks of `block` positions
+ *           (16, 32, 64 or 128, a divisor of page_size), -1: none.  A block that is named twice
+ *           counts twice
+ *   status  int32 [n_seq][nt][n_kv_heads]: SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_TREE, and
+ *           SPEC_ST_BLOCK for a block outside [0, len); the query heads of such a row are NaN.
+ *           Rows of nodes >= n_nodes of status and out are left as they were (bad counts: all
+ *           nt rows are NaN with SPEC_ST_TREE)
+ * out overlaps none of the inputs.  A row's bits do not depend on the call's other rows, but
+ * they may on how many there are. */
+int spec_block_attn(const spec_pages* kv, int layer, const spec_tree* t, int block, int n_keep,
+                    const int32_t* blocks, const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                    const uint16_t* v_new, int64_t kv_stride, uint16_t* out, int32_t* status,
+                    void* stream);
+int spec_block_attn_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, int block, int n_keep,
+                       const int32_t* blocks, const uint16_t* q, int64_t q_stride,
+                       const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride,
+                       uint16_t* out, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -59,3 +59,33 @@ def values(codes, scales):
     with np.errstate(invalid="ignore"):
         v = u * np.asarray(scales, np.float64)[..., None]
     return v.reshape(v.shape[:-2] + (-1,))
+
+
+# ---------------------------------------------------------------------------
+# blocks
+# ---------------------------------------------------------------------------
+def digest(k):
+    """[2][hd]: the least and the largest value of every channel of keys [n][hd]."""
+    k = np.asarray(k, np.float64)
+    return np.stack([k.min(0), k.max(0)])  # (a NaN spreads)
+
+
+def score(q, d):
+    """q [heads][hd] of one kv head, a block's digest [2][hd]: the largest bound of a
+    head's logits, and the sum of magnitudes behind it."""
+    q, d = np.asarray(q, np.float64), np.asarray(d, np.float64)
+    with np.errstate(invalid="ignore"):
+        x = np.maximum(q * d[0], q * d[1])
+    return x.sum(-1).max(), np.abs(x).sum(-1).max()
+
+
+def select(scores, nb, keep, first, last):
+    """Ascending ids of nb blocks: the first, the last, and the largest-scored of the
+    others (the lowest of equal ones; NaN as infinity)."""
+    if nb <= keep:
+        return list(range(nb))
+    forced = [j for j in range(nb) if j < first or j >= nb - last]
+    rest = [j for j in range(nb) if first <= j < nb - last]
+    value = lambda j: math.inf if math.isnan(scores[j]) else float(scores[j])  # noqa: E731
+    rest.sort(key=lambda j: (-value(j), j))
+    return sorted(forced + rest[:keep - len(forced)])

@@ -29,8 +29,8 @@ SPEC_Q4, SPEC_Q6, SPEC_Q8 = 4, 6, 8
 SPEC_MAX_NT = 16
 SPEC_MAX_TREE = 64
 SPEC_FILTERED = -3.4028234663852886e38
-SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_SHARED, SPEC_ST_FULL, SPEC_ST_TREE, SPEC_ST_TIMEOUT = (
-    1, 2, 4, 8, 16, 32)
+SPEC_ST_SLOT, SPEC_ST_PAGE, SPEC_ST_SHARED, SPEC_ST_FULL, SPEC_ST_TREE, SPEC_ST_TIMEOUT, SPEC_ST_BLOCK = (
+    1, 2, 4, 8, 16, 32, 64)
 SPEC_PROF_QKV, SPEC_PROF_O, SPEC_PROF_GATE_UP, SPEC_PROF_DOWN = 0, 1, 2, 3
 SPEC_PROF_LM_HEAD, SPEC_PROF_ALL_GEMMS, SPEC_PROF_ATTN = 4, 5, 6
 
@@ -49,7 +49,9 @@ EXPORTED = ["spec_last_error", "spec_qmat_create", "spec_qmat_destroy", "spec_li
             "spec_tree_attn_workspace", "spec_accept_tree", "spec_sample",
             "spec_sample_workspace", "spec_tree_set_wait_budget", "spec_pages_q4_copy",
             "spec_pages_q4_fork", "spec_pages_q4_extend", "spec_pages_q4_free", "spec_pages_q4_commit",
-            "spec_pages_q4_read", "spec_tree_attn_q4", "spec_tree_attn_q4_workspace"]
+            "spec_pages_q4_read", "spec_tree_attn_q4", "spec_tree_attn_q4_workspace",
+            "spec_block_digest", "spec_block_digest_q4", "spec_block_scores", "spec_block_select",
+            "spec_block_attn", "spec_block_attn_q4"]
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
@@ -97,6 +99,12 @@ class spec_pages_q4(ctypes.Structure):
     _fields_ = [("k_qs", P), ("v_qs", P), ("k_scales", P), ("v_scales", P), ("layer_stride", I64),
                 ("n_layers", I32), ("n_pages", I32), ("n_kv_heads", I32), ("page_size", I32),
                 ("head_dim", I32), ("n_slots", I32), ("max_pages", I32), ("table", P), ("refs", P), ("len", P)]
+
+
+class spec_digest(ctypes.Structure):
+    _fields_ = [("data", P), ("layer_stride", I64), ("n_layers", I32), ("n_pages", I32), ("n_kv_heads", I32),
+                ("page_size", I32), ("head_dim", I32), ("block", I32), ("n_slots", I32), ("max_pages", I32),
+                ("table", P), ("len", P)]
 
 
 class spec_tree(ctypes.Structure):
@@ -187,6 +195,12 @@ def lib():
                 "spec_pages_q4_read": (I32, [P, I32, P, I32, P, P, P, P, I64, P, P]),
                 "spec_tree_attn_q4": (I32, [P, I32, P, P, I64, P, P, I64, P, P, SZ, P, P]),
                 "spec_tree_attn_q4_workspace": (I32, [P, I32, I32, I32, P]),
+                "spec_block_digest": (I32, [P, P, I32, P, P, P, P]),
+                "spec_block_digest_q4": (I32, [P, P, I32, P, P, P, P]),
+                "spec_block_scores": (I32, [P, I32, I32, P, I32, P, I32, P, I64, P, I64, P, P]),
+                "spec_block_select": (I32, [P, I32, I32, I32, P, I32, P, I32, P, I64, I32, I32, I32, P, P, P]),
+                "spec_block_attn": (I32, [P, I32, P, I32, I32, P, P, I64, P, P, I64, P, P, P]),
+                "spec_block_attn_q4": (I32, [P, I32, P, I32, I32, P, P, I64, P, P, I64, P, P, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -832,3 +846,84 @@ def spec_tree_attn_q4(kv: KVPagesQ4, layer: int, n_seq: int, slots, nt: int, n_q
                                    _dev(k_new, d), _dev(v_new, d), int(kv_stride), _dev(out, d),
                                    _dev(workspace, d), workspace.numel() * workspace.element_size(),
                                    _dev(status, d), st))
+
+
+# ---------------------------------------------------------------------------
+# long contexts: attention over selected blocks
+# ---------------------------------------------------------------------------
+class KVDigest:
+    """The digests of a cache's blocks (spec_digest) over the caller's tensors,
+    which it keeps alive: data fp16 [n_layers][n_pages][n_kv_heads]
+    [page_size / block][2][head_dim] (a layer's contiguous), the cache's table
+    and lens."""
+
+    def __init__(self, data, block: int, table, lens):
+        n_layers, n_pages, n_kv_heads, per, two, head_dim = data.shape
+        self.device = _one_device(data, ((table, "table"), (lens, "lens")))
+        if two != 2 or data.element_size() != 2 or not data[0].is_contiguous() or (
+                data.is_floating_point() and str(data.dtype) != "torch.float16"):
+            raise ValueError("data: an fp16 tensor [n_layers][n_pages][n_kv_heads][page_size / block][2][head_dim] "
+                             "with contiguous layers is required")
+        n_slots, max_pages = _check_book(table, lens, None, n_pages)
+        self._keep = (data, table, lens)
+        self.pages = spec_digest(data.data_ptr(), data.stride(0), n_layers, n_pages, n_kv_heads, per * int(block),
+                                 head_dim, int(block), n_slots, max_pages, _ptr(table), _ptr(lens))
+        self.ref = ctypes.byref(self.pages)
+
+    at = KVPages.at
+
+
+def spec_block_digest(dg: KVDigest, kv, n: int, slots, status, pos0=None, stream=None):
+    """Digests of the blocks that hold positions [pos0[i], len) of slot slots[i],
+    every layer; kv: a KVPages or KVPagesQ4 (spec_block_digest_q4)."""
+    d, st = _here(stream)
+    call = lib().spec_block_digest_q4 if isinstance(kv, KVPagesQ4) else lib().spec_block_digest
+    _check(call(dg.at(d), kv.at(d), int(n), _dev(slots, d), _dev(pos0, d), _dev(status, d), st))
+
+
+def spec_block_digest_q4(dg: KVDigest, kv: KVPagesQ4, n: int, slots, status, pos0=None, stream=None):
+    """spec_block_digest of a cache in 4 bits."""
+    spec_block_digest(dg, kv, n, slots, status, pos0, stream)
+
+
+def _rows_of_scores(scores):
+    if scores.element_size() != 4 or not scores.is_floating_point() or not scores.is_contiguous():
+        raise ValueError("scores: a contiguous fp32 tensor [n_seq][nt][n_kv_heads][blocks] is required")
+    return scores.shape[-1]
+
+
+def spec_block_scores(dg: KVDigest, layer: int, n_seq: int, slots, nt: int, n_q_heads: int, q, scores,
+                      status, n_nodes=None, q_stride: int = 0, stream=None):
+    """Every block's score for each node's query: scores fp32 [n_seq][nt][n_kv_heads][ld]."""
+    d, st = _here(stream)
+    _check(lib().spec_block_scores(dg.at(d), int(layer), int(n_seq), _dev(slots, d), int(nt), _dev(n_nodes, d),
+                                   int(n_q_heads), _dev(q, d), int(q_stride), _dev(scores, d),
+                                   _rows_of_scores(scores), _dev(status, d), st))
+
+
+def spec_block_select(lens, block: int, n_seq: int, slots, nt: int, n_kv_heads: int, scores, n_keep: int,
+                      blocks, status, n_nodes=None, n_first: int = 1, n_last: int = 1, stream=None):
+    """The first n_first, the last n_last and the largest-scored others of a row's
+    blocks, ascending, -1 behind: blocks int32 [n_seq][nt][n_kv_heads][n_keep]."""
+    d, st = _here(stream)
+    _check(lib().spec_block_select(_dev(lens, d), lens.numel(), int(block), int(n_seq), _dev(slots, d), int(nt),
+                                   _dev(n_nodes, d), int(n_kv_heads), _dev(scores, d), _rows_of_scores(scores),
+                                   int(n_keep), int(n_first), int(n_last), _dev(blocks, d), _dev(status, d), st))
+
+
+def spec_block_attn(kv, layer: int, n_seq: int, slots, nt: int, n_q_heads: int, block: int, n_keep: int,
+                    blocks, q, k_new, v_new, out, status, parents=None, n_nodes=None, scale: float = 0.0,
+                    q_stride: int = 0, kv_stride: int = 0, stream=None):
+    """Attention of the trees' nodes over the blocks of each node's and kv head's
+    list and over themselves; kv: a KVPages or KVPagesQ4 (spec_block_attn_q4);
+    status int32 [n_seq][nt][n_kv_heads]."""
+    d, st = _here(stream)
+    t = spec_tree(n_seq, nt, n_q_heads, 0, 0, scale, _dev(slots, d), _dev(parents, d), _dev(n_nodes, d))
+    call = lib().spec_block_attn_q4 if isinstance(kv, KVPagesQ4) else lib().spec_block_attn
+    _check(call(kv.at(d), int(layer), ctypes.byref(t), int(block), int(n_keep), _dev(blocks, d), _dev(q, d),
+                int(q_stride), _dev(k_new, d), _dev(v_new, d), int(kv_stride), _dev(out, d), _dev(status, d), st))
+
+
+def spec_block_attn_q4(kv: KVPagesQ4, *args, **kw):
+    """spec_block_attn over a cache in 4 bits."""
+    spec_block_attn(kv, *args, **kw)

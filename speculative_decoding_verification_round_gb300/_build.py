@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libspecverify.so")
 SOURCES = ["api.cu", "linear.cu", "tcgemm.cu", "attn.cu", "ops.cu", "accept.cu", "depth.cu",
-           "pages.cu", "pages_q4.cu", "tree_attn.cu", "q4_attn.cu", "tree_attn_tc.cu", "sample.cu",
+           "pages.cu", "pages_q4.cu", "tree_attn.cu", "q4_attn.cu", "blocks.cu", "block_attn.cu", "tree_attn_tc.cu", "sample.cu",
            "sample_rows.cu"]
 # host code whose doubles must be rounded operation by operation
 FILE_FLAGS = {"depth.cu": ["-Xcompiler", "-ffp-contract=off"]}

@@ -50,9 +50,11 @@ void tc_init_attrs();
 void tree_init_attrs();
 void sample_init_attrs();
 void q4_init_attrs();
+void blocks_init_attrs();
+void block_attn_init_attrs();
 static std::mutex g_attr_mu;
 static std::vector<int> g_attr_done;
-static void init_attrs_once() {
+void init_attrs_once() {
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lk(g_attr_mu);
@@ -64,6 +66,8 @@ static void init_attrs_once() {
   tree_init_attrs();
   sample_init_attrs();
   q4_init_attrs();
+  blocks_init_attrs();
+  block_attn_init_attrs();
   g_attr_done.push_back(dev);
 }
 
@@ -1247,6 +1251,58 @@ extern "C" int spec_tree_attn_q4(const spec_pages_q4* kv, int layer, const spec_
   init_attrs_once();
   return launch_tree_q4(kv, layer, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status,
                         as_stream(stream));
+}
+
+static int check_block_call(const spec_pages* book, int layer, const spec_tree* t, int block, int n_keep,
+                            const int32_t* blocks, const void* q, int64_t q_stride, const void* k_new,
+                            const void* v_new, int64_t kv_stride, const void* out, const int32_t* status) {
+  if (t == nullptr || t->slots == nullptr || blocks == nullptr || q == nullptr || k_new == nullptr ||
+      v_new == nullptr || out == nullptr || status == nullptr)
+    return fail(SPEC_E_INVALID, "null argument");
+  int rc = tree_check(book, t->n_seq, t->nt, t->n_q_heads);
+  if (rc == SPEC_OK)
+    rc = check_tree_call(book->n_layers, book->n_kv_heads, book->head_dim, layer, t, q, q_stride, k_new, v_new,
+                         kv_stride, out, nullptr, 0, 0);
+  if (rc != SPEC_OK) return rc;
+  if (t->window != 0) return fail(SPEC_E_UNSUPPORTED, "attention over selected blocks has no window");
+  if (!block_fits(block, book->page_size))
+    return fail(SPEC_E_SHAPE, "block must be 16, 32, 64 or 128 and divide page_size");
+  if (n_keep < 1 || n_keep > SPEC_MAX_KEEP) return fail(SPEC_E_SHAPE, "n_keep in [1, 4096] required");
+  const size_t lists = sizeof(int32_t) * (size_t)t->n_seq * t->nt * book->n_kv_heads * n_keep,
+               out_b = 2 * (size_t)t->n_seq * t->nt * t->n_q_heads * book->head_dim;
+  if (overlaps(out, out_b, blocks, lists)) return fail(SPEC_E_INVALID, "out must not overlap blocks");
+  return SPEC_OK;
+}
+
+extern "C" int spec_block_attn(const spec_pages* kv, int layer, const spec_tree* t, int block, int n_keep,
+                               const int32_t* blocks, const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                               const uint16_t* v_new, int64_t kv_stride, uint16_t* out, int32_t* status,
+                               void* stream) {
+  const int rc = check_block_call(kv, layer, t, block, n_keep, blocks, q, q_stride, k_new, v_new, kv_stride, out, status);
+  if (rc != SPEC_OK) return rc;
+  init_attrs_once();
+  const int64_t at = (int64_t)layer * kv->layer_stride;
+  const BlockPlanes p = {reinterpret_cast<const uint8_t*>(kv->k + at), reinterpret_cast<const uint8_t*>(kv->v + at),
+                         nullptr, nullptr};
+  return launch_block_attn(kv, p, t, block, n_keep, blocks, q, q_stride, k_new, v_new, kv_stride, out, status,
+                           as_stream(stream));
+}
+
+extern "C" int spec_block_attn_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, int block, int n_keep,
+                                  const int32_t* blocks, const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                                  const uint16_t* v_new, int64_t kv_stride, uint16_t* out, int32_t* status,
+                                  void* stream) {
+  int rc = check_pages_q4(kv, true);
+  if (rc != SPEC_OK) return rc;
+  const spec_pages book = book_of(kv);
+  rc = check_block_call(&book, layer, t, block, n_keep, blocks, q, q_stride, k_new, v_new, kv_stride, out, status);
+  if (rc != SPEC_OK) return rc;
+  init_attrs_once();
+  const int64_t row = (int64_t)layer * kv->layer_stride, nb = kv->head_dim / 32;
+  const BlockPlanes p = {kv->k_qs + row * nb * 16, kv->v_qs + row * nb * 16, kv->k_scales + row * nb,
+                         kv->v_scales + row * nb};
+  return launch_block_attn(&book, p, t, block, n_keep, blocks, q, q_stride, k_new, v_new, kv_stride, out, status,
+                           as_stream(stream));
 }
 
 extern "C" int spec_tree_set_wait_budget(int tries) {

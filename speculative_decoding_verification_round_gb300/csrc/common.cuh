@@ -270,6 +270,22 @@ int launch_tree_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, const
                    const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride, uint16_t* out, void* workspace,
                    int32_t* status, cudaStream_t st);
 
+// Attention over selected blocks (block_attn.cu): one layer's rows of fp16, or
+// codes with scales; block sizes (blocks.cu); the library's kernel attributes.
+constexpr int SPEC_MAX_KEEP = 4096;  // blocks of a list
+struct BlockPlanes {
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint16_t* k_scales;
+  const uint16_t* v_scales;
+};
+int launch_block_attn(const spec_pages* book, const BlockPlanes& planes, const spec_tree* t, int block, int n_keep,
+                      const int32_t* blocks, const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                      const uint16_t* v_new, int64_t kv_stride, uint16_t* out, int32_t* status, cudaStream_t st);
+bool block_fits(int block, int page_size);
+int tree_check(const spec_pages* kv, int n_seq, int nt, int n_q_heads);
+void init_attrs_once();
+
 // Tree attention (tree_attn.cu) and filtered sampling (sample.cu).
 int tree_workspace(const spec_pages* kv, int n_seq, int nt, int n_q_heads, size_t* bytes);
 int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,

@@ -413,8 +413,7 @@ cudaError_t tree_tc_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st
 void tree_tc_init_attrs();
 
 // What the kernels for the cache in fp16 and in 4 bits share (tree_attn.cu):
-// argument checks, a workspace's bytes, the arguments, the joining kernel.
-int tree_check(const spec_pages* kv, int n_seq, int nt, int n_q_heads);
+// a workspace's bytes, the arguments, the joining kernel.
 size_t tree_scratch(int hd, int rows, int n_cta, int n_seq);
 void tree_fill(TreeArgs& a, const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q, int64_t q_stride,
                const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride, uint16_t* out, void* workspace,

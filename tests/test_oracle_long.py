@@ -44,3 +44,22 @@ def test_codes():
     t = np.zeros(32, np.float16)
     t[4], t[9] = 2, -2
     assert lc.quantise(t)[1][0] == -0.25 and lc.quantise(-t)[1][0] == 0.25
+
+
+def test_scores_bound_every_key_of_a_block():
+    g = np.random.default_rng(2)
+    k, q = g.standard_normal((16, 64)), g.standard_normal((4, 64))
+    d = lc.digest(k)
+    top, mag = lc.score(q, d)
+    assert top >= (q @ k.T).max() and mag >= abs(top)
+    assert lc.score(q, lc.digest(k[3:4]))[0] == (q @ k[3]).max() or math.isclose(
+        lc.score(q, lc.digest(k[3:4]))[0], (q @ k[3]).max())
+
+
+def test_selection():
+    x = [5.0, 1.0, 7.0, 7.0, float("nan"), -1.0, 7.0, 0.0]
+    assert lc.select(x, 8, 4, 1, 1) == [0, 2, 4, 7]
+    assert lc.select(x, 8, 5, 1, 1) == [0, 2, 3, 4, 7]
+    assert lc.select(x, 8, 3, 0, 0) == [2, 3, 4]
+    assert lc.select(x, 5, 5, 1, 1) == [0, 1, 2, 3, 4] and lc.select(x, 0, 3, 1, 1) == []
+    assert lc.select(x, 8, 2, 2, 0) == [0, 1]
