@@ -50,7 +50,6 @@ void tc_init_attrs();
 void tree_init_attrs();
 void sample_init_attrs();
 void q4_init_attrs();
-void blocks_init_attrs();
 void block_attn_init_attrs();
 static std::mutex g_attr_mu;
 static std::vector<int> g_attr_done;
@@ -66,7 +65,6 @@ void init_attrs_once() {
   tree_init_attrs();
   sample_init_attrs();
   q4_init_attrs();
-  blocks_init_attrs();
   block_attn_init_attrs();
   g_attr_done.push_back(dev);
 }

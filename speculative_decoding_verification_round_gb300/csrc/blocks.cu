@@ -13,7 +13,8 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // digests: a warp per block, 16 bytes a lane and load, several rows of the block a
-// load; the lanes that hold the same channels are joined at the end
+// load, up to 16 loads in flight; the lanes that hold the same channels are joined
+// at the end, each keeping the half of the registers that the other one gives away
 // ---------------------------------------------------------------------------
 constexpr int DG_THREADS = 128, DG_WARPS = DG_THREADS / 32;
 
@@ -35,12 +36,38 @@ struct Keys {
   int64_t layer_stride;  // rows
 };
 
+// REGS registers of both bounds, joined over the lanes that differ in bits [BIT, 5) of
+// their number.  Afterwards a lane has REGS >> (5 - BIT) of them, from the returned
+// one on: the highest lane bit chooses between the halves.
+template <int REGS, int BIT>
+__device__ __forceinline__ int join_lanes(uint32_t (&lo)[REGS], uint32_t (&hi)[REGS]) {
+  static_assert(REGS >> (5 - BIT) > 0, "one register at least");
+  const int lane = threadIdx.x & 31;
+  int reg0 = 0;
+#pragma unroll
+  for (int bit = 4, left = REGS / 2; bit >= BIT; bit--, left /= 2) {
+    const bool upper = lane >> bit & 1;
+#pragma unroll
+    for (int x = 0; x < REGS / 2; x++) {
+      if (x >= left) break;
+      const uint32_t gl = upper ? lo[x] : lo[x + left], gh = upper ? hi[x] : hi[x + left];
+      const uint32_t ol = upper ? lo[x + left] : lo[x], oh = upper ? hi[x + left] : hi[x];
+      lo[x] = min2(ol, __shfl_xor_sync(0xffffffffu, gl, 1 << bit));
+      hi[x] = max2(oh, __shfl_xor_sync(0xffffffffu, gh, 1 << bit));
+    }
+    if (upper) reg0 += left;
+  }
+  return reg0;
+}
+
 template <int HD, bool Q4>
 __global__ void __launch_bounds__(DG_THREADS)
 digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __restrict__ slots,
               const int32_t* __restrict__ pos0, int split, int32_t* __restrict__ status) {
   constexpr int ROW = Q4 ? HD / 2 : HD * 2, LANES = ROW / 16, PER = 32 / LANES;  // bytes; lanes and rows of a load
-  constexpr int REGS = Q4 ? 16 : 4, U = Q4 ? 4 : 8;
+  constexpr int REGS = Q4 ? 16 : 4, U = Q4 ? 4 : 16;
+  constexpr int BIT = LANES == 16 ? 4 : LANES == 8 ? 3 : LANES == 4 ? 2 : 1;
+  constexpr int KEPT = REGS >> (5 - BIT);
   grid_dep_begin();
   const int lane = threadIdx.x & 31;
   const long long w = (long long)blockIdx.x * DG_WARPS + (threadIdx.x >> 5);
@@ -66,10 +93,10 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
     if (lane == 0) status[i] = st;
   }
   for (int64_t b = (int64_t)p0 / block + y; b < nb; b += split) {
-    const int pg = row[b / per];
+    const int in_page = (int)b % per, pg = row[(int)b / per];
     if (pg < 0 || pg >= dg.n_pages) continue;
     const int64_t head = (int64_t)pg * dg.n_kv_heads + h;
-    const int64_t r0 = (int64_t)layer * keys.layer_stride + head * dg.page_size + (b % per) * block;
+    const int64_t r0 = (int64_t)layer * keys.layer_stride + head * dg.page_size + in_page * block;
     const int rows = (int)min((int64_t)block, len - b * block);
     uint32_t lo[REGS], hi[REGS];
 #pragma unroll
@@ -79,17 +106,19 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
     }
     const uint8_t* src = keys.rows + r0 * ROW + (lane % LANES) * 16;
     const __half* sc = Q4 ? keys.scales + r0 * (HD / 32) + lane % LANES : nullptr;
-    for (int r = lane / LANES; r < rows; r += PER * U) {
+    for (int r = 0; r < rows; r += PER * U) {
       uint4 v[U];
       uint32_t s[U];
 #pragma unroll
       for (int u = 0; u < U; u++) {
-        const int at = min(r + u * PER, rows - 1);  // (a row again changes nothing)
-        v[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)at * ROW));
-        if (Q4) s[u] = __half_as_ushort(__ldg(sc + (int64_t)at * (HD / 32))) * 0x10001u;
+        if (u > 0 && r + u * PER >= rows) break;
+        const int at = min(r + u * PER + lane / LANES, rows - 1);  // (a row again changes nothing)
+        v[u] = __ldg(reinterpret_cast<const uint4*>(src + at * ROW));
+        if (Q4) s[u] = __half_as_ushort(__ldg(sc + at * (HD / 32))) * 0x10001u;
       }
 #pragma unroll
       for (int u = 0; u < U; u++) {
+        if (u > 0 && r + u * PER >= rows) break;
         const uint32_t q[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
         for (int x = 0; x < REGS; x++) {
@@ -102,53 +131,46 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
         }
       }
     }
+    const int reg0 = join_lanes<REGS, BIT>(lo, hi), l = lane % LANES;
+    uint16_t* to = dg.data + (int64_t)layer * dg.layer_stride + (head * per + in_page) * (2 * HD);
+    if (!Q4) {  // word l * 4 + reg of the row
 #pragma unroll
-    for (int x = 0; x < REGS; x++)
-#pragma unroll
-      for (int off = LANES; off < 32; off <<= 1) {
-        lo[x] = min2(lo[x], __shfl_xor_sync(0xffffffffu, lo[x], off));
-        hi[x] = max2(hi[x], __shfl_xor_sync(0xffffffffu, hi[x], off));
+      for (int x = 0; x < KEPT; x++) {
+        reinterpret_cast<uint32_t*>(to)[l * 4 + reg0 + x] = lo[x];
+        reinterpret_cast<uint32_t*>(to + HD)[l * 4 + reg0 + x] = hi[x];
       }
-    uint16_t* to = dg.data + (int64_t)layer * dg.layer_stride + (head * per + b % per) * (2 * HD);
-    if (lane < LANES) {
-      uint4* d[2] = {reinterpret_cast<uint4*>(to), reinterpret_cast<uint4*>(to + HD)};
+    } else if (KEPT >= 2) {  // neighbours: elements 0, 2 and 1, 3 of a word's four, or 16 + ...
 #pragma unroll
-      for (int which = 0; which < 2; which++) {
-        const uint32_t(&z)[REGS] = which ? hi : lo;
-        if (!Q4) {
-          d[which][lane] = make_uint4(z[0], z[1], z[2], z[3]);
-        } else {
-#pragma unroll
-          for (int half = 0; half < 2; half++)
-#pragma unroll
-            for (int p = 0; p < 2; p++) {  // elements 16 half + 8 p ...: words 2 p, 2 p + 1
-              uint32_t e[4];
-#pragma unroll
-              for (int x = 0; x < 2; x++) {
-                const uint32_t even = z[4 * (2 * p + x) + 2 * half], odd = z[4 * (2 * p + x) + 2 * half + 1];
-                e[2 * x] = __byte_perm(even, odd, 0x5410);
-                e[2 * x + 1] = __byte_perm(even, odd, 0x7632);
-              }
-              d[which][4 * lane + 2 * half + p] = make_uint4(e[0], e[1], e[2], e[3]);
-            }
-        }
+      for (int x = 0; x < KEPT; x += 2) {
+        const int reg = reg0 + x, word = (32 * l + 16 * (reg >> 1 & 1) + 4 * (reg >> 2)) / 2;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint32_t*>(to) + word) =
+            make_uint2(__byte_perm(lo[x], lo[x + 1], 0x5410), __byte_perm(lo[x], lo[x + 1], 0x7632));
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint32_t*>(to + HD) + word) =
+            make_uint2(__byte_perm(hi[x], hi[x + 1], 0x5410), __byte_perm(hi[x], hi[x + 1], 0x7632));
       }
+    } else {  // one register: elements reg & 1, + 2
+      const int reg = reg0, e = 32 * l + 16 * (reg >> 1 & 1) + 4 * (reg >> 2) + (reg & 1);
+      to[e] = (uint16_t)lo[0];
+      to[e + 2] = (uint16_t)(lo[0] >> 16);
+      to[HD + e] = (uint16_t)hi[0];
+      to[HD + e + 2] = (uint16_t)(hi[0] >> 16);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// scores: sum_d max(q lo, q hi) = min(q, 0) . lo + max(q, 0) . hi, a product over 2 hd
-// channels with the digest as it lies in memory: a tile of 16 blocks a warp
-// (its digests straight into the A fragments, whose order of channels the queries
-// follow), 8 query rows a product, and the maximum over the group's heads
-// through shared memory
+// scores: sum_d max(q lo, q hi) = min(q, 0) . lo + max(q, 0) . hi, two products with the
+// digest as it lies in memory: a tile of 16 blocks a warp (its digests straight into
+// the A fragments, whose order of channels the queries follow) against 8 query
+// rows at a time.  A node's heads are neighbouring rows, as many as the next power of
+// two (the first head again in the places behind), so that the maximum over them is taken in
+// registers and by exchanges.
 // ---------------------------------------------------------------------------
-constexpr int SC_THREADS = 128, SC_WARPS = 4, SC_ROWS = 64;
+constexpr int SC_THREADS = 256, SC_WARPS = SC_THREADS / 32, SC_ROWS = 64;
 
 struct ScoreArgs {
   spec_digest dg;
-  int layer, n_seq, nt, nq, G;
+  int layer, n_seq, nt, nq, G, GP;  // GP: G to the next power of two
   const int32_t* slots;
   const int32_t* n_nodes;
   const __half* q;
@@ -163,6 +185,12 @@ struct ScoreArgs {
 template <int HD>
 __host__ __device__ constexpr int score_q_bytes(int tiles) {
   return tiles * (2 * HD / 16) * 32 * 8;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 template <int HD>
@@ -182,7 +210,7 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
     len = dg.len[slot];
   if (m < 0 || m > a.nt) st |= SPEC_ST_TREE;
   const int block = dg.block, per = dg.page_size / block;
-  const int64_t nb = ((int64_t)max(len, 0) + block - 1) / block;
+  const int nb = (int)(((int64_t)max(len, 0) + block - 1) / block);
   if (len < 0 || len > dg.max_pages * dg.page_size || nb > a.ld) st |= SPEC_ST_FULL;
   const int32_t* row = dg.table + (int64_t)(st == 0 ? slot : 0) * dg.max_pages;
   if (chunk == 0 && grp == 0 && h == 0) {
@@ -193,76 +221,105 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
     if (tid == 0) a.status[s] = st;
     st &= ~SPEC_ST_PAGE;
   }
-  const int node0 = grp * a.nodes, nodes = min(a.nodes, m - node0), rows = nodes * a.G;
-  if (st != 0 || nodes <= 0 || (int64_t)chunk * 16 * SC_WARPS >= nb) return;
+  const int node0 = grp * a.nodes, nodes = min(a.nodes, m - node0), rows = nodes * a.GP;
+  const int first = chunk * SC_WARPS * 16;
+  if (st != 0 || nodes <= 0 || first >= nb) return;
   const int tiles = (rows + 7) / 8;
   const uint32_t qs = kw_smem(smem);
-  for (int e = tid; e < tiles * STEPS * 32; e += SC_THREADS) {
-    const int el = e & 31, step = e / 32 % STEPS, n = e / 32 / STEPS;
-    const int r = 8 * n + (el >> 2), c = 8 * (4 * (step >> 1) + (el & 3)) + 4 * (step & 1);  // of 2 hd channels
-    uint32_t b0 = 0u, b1 = 0u;
-    if (r < rows) {
-      const int node = node0 + r / a.G, head = h * a.G + r % a.G;
-      const uint2 v =
-          *reinterpret_cast<const uint2*>(a.q + ((int64_t)s * a.nt + node) * a.q_stride + head * HD + c % HD);
-      b0 = c < HD ? min2(v.x, 0u) : max2(v.x, 0u);
-      b1 = c < HD ? min2(v.y, 0u) : max2(v.y, 0u);
-    }
-    kw_sts64(qs + e * 8, b0, b1);
-  }
-  __syncthreads();
-  // [block of the tile][row], a row more to keep the banks apart
-  float* x = reinterpret_cast<float*>(smem + score_q_bytes<HD>((a.nodes * a.G + 7) / 8)) + warp * 16 * (SC_ROWS + 1);
-  for (int64_t b0 = ((int64_t)chunk * SC_WARPS + warp) * 16; b0 < nb; b0 += (int64_t)a.chunks * SC_WARPS * 16) {
-    uint4 v[2][LOADS];
-    bool there[2];
+  // the digests of a tile of 16 blocks: lane (g, t) has units t, t + 4, ... of blocks g, 8 + g
+  uint4 v[2][LOADS];
+  bool there[2];
+  auto load = [&](int b0) {
 #pragma unroll
     for (int half = 0; half < 2; half++) {
-      const int64_t b = b0 + 8 * half + g;
-      const int pg = b < nb ? row[b / per] : -1;
+      const int b = b0 + 8 * half + g, e = b / per, pg = b < nb ? row[e] : -1;
       there[half] = pg >= 0 && pg < dg.n_pages;
       const uint4* src = reinterpret_cast<const uint4*>(
           dg.data + (int64_t)a.layer * dg.layer_stride +
-          (((int64_t)(there[half] ? pg : 0) * dg.n_kv_heads + h) * per + (there[half] ? b % per : 0)) * (2 * HD));
+          (((int64_t)(there[half] ? pg : 0) * dg.n_kv_heads + h) * per + (there[half] ? b - e * per : 0)) * (2 * HD));
 #pragma unroll
       for (int i = 0; i < LOADS; i++) v[half][i] = __ldg(src + 4 * i + t);
     }
+  };
+  const int mine = first + warp * 16;
+  if (mine < nb) load(mine);
+  // the queries' fragments: 16 bytes of a row are two steps' of lo and two of hi
+  for (int e = tid; e < tiles * 8 * (HD / 8); e += SC_THREADS) {
+    const int u = e % (HD / 8), r = e / (HD / 8), i = u >> 2, col = r & 7, n = r >> 3;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows) {
+      const int node = node0 + r / a.GP, k = r & (a.GP - 1), head = h * a.G + (k < a.G ? k : 0);
+      x = *reinterpret_cast<const uint4*>(a.q + ((int64_t)s * a.nt + node) * a.q_stride + head * HD + 8 * u);
+    }
+    const uint32_t to = qs + ((n * STEPS + 2 * i) * 32 + col * 4 + (u & 3)) * 8;
+    kw_sts64(to, min2(x.x, 0u), min2(x.y, 0u));
+    kw_sts64(to + 256, min2(x.z, 0u), min2(x.w, 0u));
+    kw_sts64(to + STEPS * 128, max2(x.x, 0u), max2(x.y, 0u));
+    kw_sts64(to + STEPS * 128 + 256, max2(x.z, 0u), max2(x.w, 0u));
+  }
+  __syncthreads();
+  const int64_t out0 = (((int64_t)s * a.nt + node0) * dg.n_kv_heads + h) * a.ld, node_ld = (int64_t)dg.n_kv_heads * a.ld;
+  for (int b0 = mine; b0 < nb; b0 += a.chunks * SC_WARPS * 16) {
+    if (b0 != mine) load(b0);
+    float top[4];  // of a node with more than 8 heads
     for (int n = 0; n < tiles; n++) {
-      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float lo[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < LOADS; i++) {
-        const uint2 q0 = kw_lds64(qs + ((n * STEPS + 2 * i) * 32 + lane) * 8);
-        const uint2 q1 = kw_lds64(qs + ((n * STEPS + 2 * i + 1) * 32 + lane) * 8);
-        const uint32_t a0[4] = {v[0][i].x, v[1][i].x, v[0][i].y, v[1][i].y};
-        const uint32_t a1[4] = {v[0][i].z, v[1][i].z, v[0][i].w, v[1][i].w};
-        mma_16816(acc, a0, q0.x, q0.y);
-        mma_16816(acc, a1, q1.x, q1.y);
-      }
+      for (int i = 0; i < LOADS / 2; i++) {
 #pragma unroll
-      for (int e = 0; e < 4; e++)
-        x[(g + 8 * (e >> 1)) * (SC_ROWS + 1) + 8 * n + 2 * t + (e & 1)] = there[e >> 1] ? acc[e] : -INFINITY;
-    }
-    __syncwarp();
-    const int64_t b = b0 + (lane & 15);
-    for (int i = lane >> 4; i < nodes; i += 2) {
-      const float* p = x + (lane & 15) * (SC_ROWS + 1) + i * a.G;
-      float top = p[0];
-      bool nan = top != top;
-      for (int k = 1; k < a.G; k++) {
-        nan |= p[k] != p[k];
-        top = fmaxf(top, p[k]);
+        for (int k = 0; k < 2; k++) {
+          const uint32_t at = qs + ((n * STEPS + 2 * i + k) * 32 + lane) * 8;
+          const uint2 ql = kw_lds64(at), qh = kw_lds64(at + STEPS * 128);
+          const uint4 &l0 = v[0][i], &l1 = v[1][i], &h0 = v[0][i + LOADS / 2], &h1 = v[1][i + LOADS / 2];
+          const uint32_t al[4] = {k ? l0.z : l0.x, k ? l1.z : l1.x, k ? l0.w : l0.y, k ? l1.w : l1.y};
+          const uint32_t ah[4] = {k ? h0.z : h0.x, k ? h1.z : h1.x, k ? h0.w : h0.y, k ? h1.w : h1.y};
+          mma_16816(lo, al, ql.x, ql.y);
+          mma_16816(hi, ah, qh.x, qh.y);
+        }
       }
-      if (nan) top = __int_as_float(0x7FFFFFFF);
-      if (b < nb) a.scores[(((int64_t)s * a.nt + node0 + i) * dg.n_kv_heads + h) * a.ld + b] = top;
+      // (block g, rows 2t, 2t + 1), (block 8 + g, ...)
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) x[e] = there[e >> 1] ? lo[e] + hi[e] : -INFINITY;
+      auto put = [&](int node, int half, float value) {
+        const int b = b0 + 8 * half + g;
+        if (b < nb && node < nodes) a.scores[out0 + node * node_ld + b] = value;
+      };
+      if (a.GP == 1) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) put(8 * n + 2 * t + (e & 1), e >> 1, x[e]);
+      } else {
+        float y[2] = {max_nan(x[0], x[1]), max_nan(x[2], x[3])};
+        if (a.GP >= 4)
+#pragma unroll
+          for (int e = 0; e < 2; e++) y[e] = max_nan(y[e], __shfl_xor_sync(0xffffffffu, y[e], 1));
+        if (a.GP >= 8)
+#pragma unroll
+          for (int e = 0; e < 2; e++) y[e] = max_nan(y[e], __shfl_xor_sync(0xffffffffu, y[e], 2));
+        if (a.GP <= 8) {
+          const int shift = a.GP == 2 ? 0 : a.GP == 4 ? 1 : 2;  // lanes t of a node
+          if ((t & ((1 << shift) - 1)) == 0)
+#pragma unroll
+            for (int e = 0; e < 2; e++) put((8 >> (shift + 1)) * n + (t >> shift), e, y[e]);
+        } else {
+          const int part = n & (a.GP / 8 - 1);
+#pragma unroll
+          for (int e = 0; e < 2; e++) top[e] = part == 0 ? y[e] : max_nan(top[e], y[e]);
+          if (part == a.GP / 8 - 1 && t == 0)
+#pragma unroll
+            for (int e = 0; e < 2; e++) put(n / (a.GP / 8), e, top[e]);
+        }
+      }
     }
-    __syncwarp();
   }
 }
 
 // ---------------------------------------------------------------------------
-// selection: a CTA per row.  The k-th largest score's bits are found from the
-// highest on, by counting the scores that reach each candidate (they stay in
-// registers, PER a thread); the rows end early once exactly k scores do.
+// selection: a CTA per row, a row's keys (its scores as whole numbers in the same
+// order) in registers, four neighbours and THREADS * 4 behind the next four.  The
+// bits of the k-th largest key are found from the highest in which the row's keys
+// differ, by counting the keys that reach each candidate, until exactly k do; the
+// chosen blocks are marked in a bit map, whose words then are written out in order.
 // ---------------------------------------------------------------------------
 struct SelectArgs {
   const int32_t* len;
@@ -278,7 +335,9 @@ struct SelectArgs {
 
 template <int THREADS, int PER>
 __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
-  __shared__ int s_warp[2][THREADS / 32];
+  constexpr int WARPS = THREADS / 32, SPAN = THREADS * PER;
+  __shared__ int s_sum[2][WARPS];
+  __shared__ uint32_t s_bits[SPAN / 32], s_mm[2][WARPS];
   grid_dep_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r = blockIdx.x;
@@ -301,101 +360,175 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
     for (int j = tid; j < k; j += THREADS) out[j] = j;
     return;
   }
+  // Of the blocks [a.first, nb - a.last) `need` are chosen, the others are.  A key is
+  // never 0, which stands for no block.
   const float* x = a.scores + r * a.ld;
-  auto key_of = [&](int j) -> uint32_t {
-    if (j >= nb) return 0u;
-    if (j < a.first || j >= nb - a.last) return 0xFFFFFFFFu;
-    const float f = x[j];
-    return f != f ? 0xFF800000u : logit_key(f);
-  };
-  // this thread's scores: PER neighbours, chunk after chunk of THREADS * PER
+  const int end = nb - a.last, need = k - a.first - a.last;
+  auto to_key = [&](float f) -> uint32_t { return f != f ? 0xFF800000u : logit_key(f); };
+  auto key_of = [&](int j) -> uint32_t { return j >= a.first && j < end ? to_key(x[j]) : 0u; };
+  const bool one = nb <= SPAN, vec = ((reinterpret_cast<uintptr_t>(x) & 15u) == 0);
   uint32_t key[PER];
-  const bool one = nb <= THREADS * PER;
+  // block of key i of this thread, in the span from c0 on
+  auto block_of = [&](int c0, int i) { return c0 + (i >> 2) * (THREADS * 4) + tid * 4 + (i & 3); };
+  auto load = [&](int c0) {
 #pragma unroll
-  for (int i = 0; i < PER; i++) key[i] = one ? key_of(tid * PER + i) : 0u;
+    for (int i = 0; i < PER; i += 4) {
+      const int j = block_of(c0, i);
+      if (vec && j >= a.first && j + 3 < end) {
+        const float4 f = *reinterpret_cast<const float4*>(x + j);
+        key[i] = to_key(f.x);
+        key[i + 1] = to_key(f.y);
+        key[i + 2] = to_key(f.z);
+        key[i + 3] = to_key(f.w);
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; y++) key[i + y] = key_of(j + y);
+      }
+    }
+  };
   int which = 0;
-  auto count = [&](uint32_t t) {
+  auto count = [&](uint32_t t) {  // keys >= t
     int c = 0;
     if (one) {
 #pragma unroll
       for (int i = 0; i < PER; i++) c += key[i] >= t;
     } else {
-      for (int j = tid; j < nb; j += THREADS) c += key_of(j) >= t;
+      for (int j = a.first + tid; j < end; j += THREADS) c += key_of(j) >= t;
     }
     c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) s_warp[which][warp] = c;
-    __syncthreads();
-    c = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; w++) c += s_warp[which][w];
-    which ^= 1;
+    if (WARPS > 1) {
+      if (lane == 0) s_sum[which][warp] = c;
+      __syncthreads();
+      c = lane < WARPS ? s_sum[which][lane] : 0;
+      c = __reduce_add_sync(0xffffffffu, c);
+      which ^= 1;
+    }
     return c;
   };
-  uint32_t t = 0u;
-  int reach = nb;
-  for (uint32_t bit = 0x80000000u; bit != 0u && reach != k; bit >>= 1) {
-    const int c = count(t | bit);
-    if (c >= k) {
-      t |= bit;
-      reach = c;
+  load(0);
+  // the bits that all keys have in common
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+  if (one) {
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      hi = max(hi, key[i]);
+      lo = min(lo, key[i] - 1u);  // (no block: the largest)
+    }
+  } else {
+    for (int j = a.first + tid; j < end; j += THREADS) {
+      const uint32_t y = key_of(j);
+      hi = max(hi, y);
+      lo = min(lo, y - 1u);
     }
   }
-  // where more reach it than there is room for, they end in equal scores: the
-  // lowest blocks of these
-  const int over = reach - k;  // equal ones that stay out, the last ones
-  const int equal_in = over == 0 ? INT_MAX : (count(t) - count(t + 1u)) - over;
-  // (t is no forced block's key: of those there are at most k)
-  int base_gt = 0, base_eq = 0;
-  for (int c0 = 0; c0 < nb; c0 += THREADS * PER) {
-    int gt = 0, eq = 0;
-#pragma unroll
-    for (int i = 0; i < PER; i++) {
-      if (!one) key[i] = key_of(c0 + tid * PER + i);
-      const bool in = key[i] >= t && c0 + tid * PER + i < nb;
-      eq += in && over > 0 && key[i] == t;
-      gt += in && !(over > 0 && key[i] == t);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (WARPS > 1) {
+    if (lane == 0) {
+      s_mm[0][warp] = hi;
+      s_mm[1][warp] = lo;
     }
-    // exclusive sums over the CTA
-    int g0 = gt, e0 = eq;
+    __syncthreads();
+    hi = __reduce_max_sync(0xffffffffu, lane < WARPS ? s_mm[0][lane] : 0u);
+    lo = __reduce_min_sync(0xffffffffu, lane < WARPS ? s_mm[1][lane] : 0xFFFFFFFFu);
+  }
+  lo += 1u;
+  // t: the largest number that `need` keys reach (above all keys if none is needed)
+  uint32_t t = need > 0 ? lo : 0xFFFFFFFFu;
+  int reach = need > 0 ? end - a.first : 0;
+  if (reach != need && hi != lo) {
+    const int top = 31 - __clz((int)(hi ^ lo));
+    t = hi & ~((2u << top) - 1u);  // the bits in common
+    for (uint32_t bit = 1u << top; bit != 0u && reach != need; bit >>= 1) {
+      const int c = count(t | bit);
+      if (c >= need) {
+        t |= bit;
+        reach = c;
+      }
+    }
+  }
+  // Where more reach it than are needed, the search has come to its end: t is a key, and
+  // of the equal ones the lowest blocks are taken.
+  const int ties = reach > need ? need - count(t + 1u) : INT_MAX;
+  int base = 0, ties_before = 0;
+  for (int c0 = 0; c0 < nb; c0 += SPAN) {
+    if (c0 > 0) {
+      load(c0);
+      __syncthreads();  // the bit map has been read
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < PER; i0 += 4) {
+      // ties in order: those of the threads in front, of the fours of a chunk
+      uint32_t mine = 0u;
+      int eq = 0;
+#pragma unroll
+      for (int y = 0; y < 4; y++) {
+        const int j = block_of(c0, i0 + y);
+        const uint32_t kk = key[i0 + y];
+        const bool in = j < nb && (j < a.first || j >= end || (need > 0 && kk >= t));
+        const bool tie = in && ties != INT_MAX && kk == t;
+        if (in && !tie) mine |= 1u << y;
+        if (tie) {
+          mine |= 16u << y;
+          eq++;
+        }
+      }
+      if (ties != INT_MAX) {
+        int before = eq;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int z = __shfl_up_sync(0xffffffffu, before, off);
+          if (lane >= off) before += z;
+        }
+        __syncthreads();
+        if (lane == 31) s_sum[0][warp] = before;
+        __syncthreads();
+        int all = 0;
+        before += ties_before - eq;
+        for (int w = 0; w < WARPS; w++) {
+          if (w < warp) before += s_sum[0][w];
+          all += s_sum[0][w];
+        }
+        ties_before += all;
+#pragma unroll
+        for (int y = 0; y < 4; y++)
+          if (mine >> (4 + y) & 1) {
+            if (before < ties) mine |= 1u << y;
+            before++;
+          }
+      }
+      // eight threads make a word of the map
+      uint32_t bits = (mine & 15u) << (4 * (lane & 7));
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, off);
+      if ((lane & 7) == 0) s_bits[(i0 * THREADS + tid * 4) / 32] = bits;
+    }
+    __syncthreads();
+    // the words in order, a thread one (SPAN / 32 <= THREADS)
+    static_assert(SPAN / 32 <= THREADS, "a word a thread");
+    uint32_t w = tid < SPAN / 32 ? s_bits[tid] : 0u;
+    const int c = __popc(w);
+    int at = c;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int yg = __shfl_up_sync(0xffffffffu, g0, off), ye = __shfl_up_sync(0xffffffffu, e0, off);
-      if (lane >= off) {
-        g0 += yg;
-        e0 += ye;
+      const int z = __shfl_up_sync(0xffffffffu, at, off);
+      if (lane >= off) at += z;
+    }
+    if (WARPS > 1) {
+      if (lane == 31) s_sum[1][warp] = at;
+      __syncthreads();
+    }
+    int all = at;
+    if (WARPS > 1) {
+      all = 0;
+      for (int x2 = 0; x2 < WARPS; x2++) {
+        if (x2 < warp) at += s_sum[1][x2];
+        all += s_sum[1][x2];
       }
     }
-    __syncthreads();
-    if (lane == 31) {
-      s_warp[0][warp] = g0;
-      s_warp[1][warp] = e0;
-    }
-    __syncthreads();
-    int all_g = 0, all_e = 0;
-    g0 += base_gt - gt;
-    e0 += base_eq - eq;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; w++) {
-      if (w < warp) {
-        g0 += s_warp[0][w];
-        e0 += s_warp[1][w];
-      }
-      all_g += s_warp[0][w];
-      all_e += s_warp[1][w];
-    }
-#pragma unroll
-    for (int i = 0; i < PER; i++) {
-      const int j = c0 + tid * PER + i;
-      if (key[i] < t || j >= nb) continue;
-      const bool tie = over > 0 && key[i] == t;
-      if (!tie || e0 < equal_in) out[g0 + min(e0, equal_in)] = j;
-      if (tie)
-        e0++;
-      else
-        g0++;
-    }
-    base_gt += all_g;
-    base_eq += all_e;
+    at += base - c;
+    base += all;
+    for (; w != 0u; w &= w - 1u) out[at++] = c0 + tid * 32 + __ffs(w) - 1;
   }
 }
 
@@ -445,13 +578,7 @@ bool block_fits(int block, int page_size) {
   return (block == 16 || block == 32 || block == 64 || block == 128) && page_size % block == 0;
 }
 
-void blocks_init_attrs() {
-  const int most = SC_WARPS * 16 * (SC_ROWS + 1) * 4;
-  cudaFuncSetAttribute(scores_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       score_q_bytes<64>(SC_ROWS / 8) + most);
-  cudaFuncSetAttribute(scores_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       score_q_bytes<128>(SC_ROWS / 8) + most);
-}
+static_assert(score_q_bytes<128>(SC_ROWS / 8) <= 48 * 1024, "without an attribute of the kernel's");
 
 static bool same_sizes(const spec_digest* dg, int n_layers, int n_pages, int nkv, int page, int hd) {
   return dg->n_layers == n_layers && dg->n_pages == n_pages && dg->n_kv_heads == nkv && dg->page_size == page &&
@@ -515,18 +642,18 @@ extern "C" int spec_block_scores(const spec_digest* dg, int layer, int n_seq, co
   a.scores = scores;
   a.ld = ld;
   a.status = status;
-  a.nodes = std::min(nt, SC_ROWS / a.G);
+  a.GP = 1;
+  while (a.GP < a.G) a.GP *= 2;
+  a.nodes = std::min(nt, SC_ROWS / a.GP);
   a.groups = (nt + a.nodes - 1) / a.nodes;
-  // a tile of 16 blocks a warp, until there are CTAs for eight an SM
+  // a tile of 16 blocks a warp, until there are CTAs for four an SM
   const int64_t most = std::min<int64_t>(ld, (int64_t)dg->max_pages * (dg->page_size / dg->block));
   const double units = (double)n_seq * dg->n_kv_heads * a.groups;
-  const int64_t fill = std::max<int64_t>(1, (int64_t)(8 * device_sms() / units));
+  const int64_t fill = std::max<int64_t>(1, (int64_t)(4 * device_sms() / units));
   a.chunks = (int)std::min<int64_t>((most + 16 * SC_WARPS - 1) / (16 * SC_WARPS), fill);
   if (units * a.chunks > INT32_MAX) return fail(SPEC_E_SHAPE, "n_seq * nt * n_kv_heads too large");
-  const int tiles = (a.nodes * a.G + 7) / 8;
-  const size_t smem = (dg->head_dim == 128 ? score_q_bytes<128>(tiles) : score_q_bytes<64>(tiles)) +
-                      SC_WARPS * 16 * (SC_ROWS + 1) * sizeof(float);
-  init_attrs_once();
+  const int tiles = (a.nodes * a.GP + 7) / 8;
+  const size_t smem = dg->head_dim == 128 ? score_q_bytes<128>(tiles) : score_q_bytes<64>(tiles);
   const cudaError_t e =
       launch_dependent(dg->head_dim == 128 ? scores_kernel<128> : scores_kernel<64>, (size_t)(units * a.chunks),
                        SC_THREADS, smem, reinterpret_cast<cudaStream_t>(stream), a);
@@ -553,9 +680,14 @@ extern "C" int spec_block_select(const int32_t* len, int n_slots, int block, int
                         n_last, blocks, status};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t grid = (size_t)rows;
-  const cudaError_t e = ld <= 1024   ? launch_dependent(select_kernel<128, 8>, grid, 128, 0, st, a)
+  // 16 keys a thread, up to 16384 a row (longer ones are read again for every bit); scores
+  // past a row's last block cost threads without keys, so the class goes by ld
+  const cudaError_t e = ld <= 512    ? launch_dependent(select_kernel<32, 16>, grid, 32, 0, st, a)
+                        : ld <= 1024 ? launch_dependent(select_kernel<64, 16>, grid, 64, 0, st, a)
+                        : ld <= 2048 ? launch_dependent(select_kernel<128, 16>, grid, 128, 0, st, a)
                         : ld <= 4096 ? launch_dependent(select_kernel<256, 16>, grid, 256, 0, st, a)
-                                     : launch_dependent(select_kernel<512, 32>, grid, 512, 0, st, a);
+                        : ld <= 8192 ? launch_dependent(select_kernel<512, 16>, grid, 512, 0, st, a)
+                                     : launch_dependent(select_kernel<1024, 16>, grid, 1024, 0, st, a);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("block selection: ") + cudaGetErrorString(e));
   return SPEC_OK;
 }

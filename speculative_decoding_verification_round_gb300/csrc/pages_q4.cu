@@ -2,10 +2,8 @@
 // it (commit), read back, copied; fork, extend and free are the bookkeeping of
 // pages.cu.
 //
-// A lane has two neighbouring elements of fp16 (or codes of them), a block of
-// 32 so is half a warp: its largest element is found by four exchanges.  Codes of
-// elements j and j + 16 share a byte, which the lane of element j's pair makes
-// with its neighbour 8 lanes on.
+// A lane has eight neighbouring elements of fp16, 16 bytes, and four lanes a block
+// of 32: two exchanges find its largest element.
 #include <algorithm>
 #include <climits>
 
@@ -29,50 +27,139 @@ __device__ __forceinline__ float block_scale(float m) {
   const float r = __uint_as_float((u + 0x7FFFu + ((u >> 16) & 1u)) & 0xFFFF0000u);
   return fminf(fmaxf(__half2float(__float2half_rn(r)), -8160.0f), 8160.0f);
 }
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // a NaN stays one
+  uint32_t r;
+  asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two floats at a time.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2f(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
-// One block of 32 (half a warp, two elements a lane: 2j, 2j + 1 of lane j) to
-// codes and scale.  bytes: codes of elements 2j and 2j + 16, ... of lanes j < 8.
+// A block of 32 elements, eight a lane (lane l of four has 8 l ...), to its scale
+// (fp16 bits, every lane) and codes (lanes 0 and 1: 8 bytes each).
+//
+// x / d is not divided: y = x (1 / d) is within two units of it, and one step
+// y + (x - y d) (1 / d) then is exact wherever x / d is a half of an odd number.
+// Nothing else is near one: x has 11 bits and d 8, so that |x / d - (k + 1/2)| is 0
+// or at least 2^-13.
 struct Block {
-  uint32_t bytes;  // two code bytes (lanes 0-7 of the half)
-  uint32_t scale;  // fp16 bits
+  uint32_t scale;
+  uint2 codes;
 };
-__device__ __forceinline__ Block quantise(uint32_t x) {
-  const float a = half_of(x, 0), b = half_of(x, 1);
-  // magnitude bits, and where they are equal the lowest index: the half's
-  // absolute bits over the complement of the index
-  const int j = threadIdx.x & 15;
-  const uint32_t ka = (x & 0x7FFFu) << 16 | (uint32_t)(63 - 2 * j) << 1 | ((x >> 15) & 1u);
-  const uint32_t kb = (x >> 16 & 0x7FFFu) << 16 | (uint32_t)(62 - 2 * j) << 1 | (x >> 31);
-  uint32_t k = max(ka, kb);
+__device__ __forceinline__ Block quantise(const uint4& in) {
+  const uint32_t x[4] = {in.x, in.y, in.z, in.w};
+  uint32_t hi = max2(max2(x[0], x[1]), max2(x[2], x[3])), lo = min2(min2(x[0], x[1]), min2(x[2], x[3]));
+  hi = max2(hi, __byte_perm(hi, hi, 0x1032));
+  lo = min2(lo, __byte_perm(lo, lo, 0x1032));
+  uint32_t both = __byte_perm(hi, lo ^ 0x80008000u, 0x5410);  // the largest, and minus the least
+  both = max2(both, __shfl_xor_sync(0xffffffffu, both, 1));
+  both = max2(both, __shfl_xor_sync(0xffffffffu, both, 2));
+  const float up = half_of(both, 0), down = half_of(both, 1);
+  float m = up > down ? up : -down;
+  if (__any_sync(0xffffffffu, up == down && up != 0.0f)) {  // the first of both decides
+    int first = 32;
+    const uint32_t top = both & 0x7FFFu;
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, off));
-  const uint32_t top = (k >> 16) | (k & 1u) << 15;  // its bits
-  Block out;
-  uint32_t u = 0x0808u;  // codes of this lane's two elements
-  if ((top & 0x7C00u) == 0x7C00u) {
-    out.scale = 0x7E00u;
-  } else {
-    const float d = block_scale(half_of(top, 0));
-    out.scale = __half_as_ushort(__float2half_rn(d));
-    if (d != 0.0f) {
-      const int qa = (int)fminf(fmaxf(rintf(__fdiv_rn(a, d)), -8.0f), 7.0f) + 8;
-      const int qb = (int)fminf(fmaxf(rintf(__fdiv_rn(b, d)), -8.0f), 7.0f) + 8;
-      u = (uint32_t)qa | (uint32_t)qb << 8;
+    for (int e = 7; e >= 0; e--) {
+      const uint32_t v = x[e >> 1] >> (16 * (e & 1));
+      if ((v & 0x7FFFu) == top) first = 2 * (8 * (int)(threadIdx.x & 3) + e) + (int)(v >> 15 & 1u);
     }
+    if (first == 32) first = 64;
+    first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
+    first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
+    if (up == down) m = first & 1 ? -up : up;
   }
-  const uint32_t high = __shfl_down_sync(0xffffffffu, u, 8, 16);
-  out.bytes = u | high << 4;
+  Block out;
+  const bool fine = up < INFINITY && down < INFINITY;  // (a NaN is not)
+  const float d = fine ? block_scale(m) : 0.0f, inv = d != 0.0f ? __frcp_rn(d) : 0.0f;
+  out.scale = fine ? __half_as_ushort(__float2half_rn(d)) : 0x7E00u;
+  const uint64_t inv2 = pair_of(inv, inv), neg2 = pair_of(-d, -d), magic = pair_of(12582912.0f, 12582912.0f),
+                 back = pair_of(-12582912.0f, -12582912.0f);
+  uint32_t u[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    const uint32_t v = fine ? x[e] : 0u;  // (d = 0: everything 0)
+    const uint64_t f = pair_of(half_of(v, 0), half_of(v, 1));
+    uint64_t y = mul2f(f, inv2);
+    y = fma2f(fma2f(y, neg2, f), d != 0.0f ? inv2 : 0ull, y);
+    y = add2f(add2f(y, magic), back);  // to whole numbers, to even
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(y));
+    uint32_t q;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q) : "f"(b), "f"(a));
+    q = min2(max2(q, 0xC800C800u), 0x47004700u);  // [-8, 7]
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(u[e]) : "r"(q), "r"(0x64086408u));  // 1024 + q + 8
+  }
+  const uint32_t c0 = __byte_perm(u[0], u[1], 0x6420) & 0x0F0F0F0Fu, c1 = __byte_perm(u[2], u[3], 0x6420) & 0x0F0F0F0Fu;
+  // element j and j + 16 share a byte: lanes 0, 1 and lanes 2, 3
+  out.codes.x = c0 | __shfl_down_sync(0xffffffffu, c0, 2) << 4;
+  out.codes.y = c1 | __shfl_down_sync(0xffffffffu, c1, 2) << 4;
   return out;
 }
 
-constexpr int CQ_ROWS = 64;  // rows of a CTA
+// A CTA has up to CQ_ROWS rows (of a node, all heads) of one entry and layer: a
+// warp takes 256 neighbouring elements of a row, eight a lane, of every
+// CQ_PHASES-th row, so that what a lane's place in the row is, is found once.
+constexpr int CQ_ROWS = 64, CQ_PHASES = 8;
 
-// One CTA per (entry, layer, block of rows); a warp does 64 elements at a time.
+// Where the rows of a CTA lie in the cache (of head 0).
+struct RowPlace {
+  int64_t at[CQ_ROWS];
+};
+__device__ __forceinline__ void place_rows(const spec_pages_q4& kv, int layer, const int32_t* row, int64_t pos0, int r0,
+                                           int r1, RowPlace& p) {
+  for (int j = r0 + threadIdx.x; j < r1; j += PQ_THREADS) {
+    const int64_t pos = pos0 + j, e = pos / kv.page_size;
+    p.at[j - r0] = (int64_t)layer * kv.layer_stride + (int64_t)row[e] * kv.n_kv_heads * kv.page_size + pos - e * kv.page_size;
+  }
+}
+// The work of a CTA: f(r, e, block): row r0 <= r < r1, this lane's elements e ... e + 7 of it, and
+// how many blocks behind the row's place (of head 0) theirs is; `ok` false for lanes
+// past the row.  Whole warps.
+template <int U, class F>
+__device__ __forceinline__ void each_piece(const spec_pages_q4& kv, int r0, int r1, F&& f) {
+  const int node = kv.n_kv_heads * kv.head_dim, per = (node + 255) / 256, nb = kv.head_dim / 32;
+  const int lane = threadIdx.x & 31;
+  for (int item = threadIdx.x >> 5; item < per * CQ_PHASES; item += PQ_THREADS / 32) {
+    const int phase = item / per, e = (item - phase * per) * 256 + lane * 8;
+    const bool ok = e < node;
+    const int h = ok ? e / kv.head_dim : 0;
+    const int64_t block = (int64_t)h * kv.page_size * nb + (ok ? e - h * kv.head_dim : 0) / 32;
+    for (int r = r0 + phase; r < r1; r += CQ_PHASES * U) f(r, ok ? e : 0, block, ok);
+  }
+}
+
 __global__ void __launch_bounds__(PQ_THREADS)
 q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slots, int nt,
                  const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new, int64_t new_layer_stride,
                  const int32_t* __restrict__ path, const int32_t* __restrict__ n_path,
                  int32_t* __restrict__ new_len, int blocks, int32_t* __restrict__ status) {
+  __shared__ RowPlace place;
+  __shared__ int s_node[CQ_ROWS];
   const int i = blockIdx.x / (kv.n_layers * blocks);
   const int layer = blockIdx.x / blocks % kv.n_layers, blk = blockIdx.x % blocks;
   const int slot = slots[i], np = n_path[i];
@@ -90,6 +177,7 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
   int bits = 0;
   for (int j = threadIdx.x; j < n; j += PQ_THREADS)
     if (j != i && slots[j] == slot) bits |= SPEC_ST_SLOT;
+  const int r0 = blk * CQ_ROWS, r1 = min(np, r0 + CQ_ROWS);
   if (st == 0 && np > 0) {
     if (pth != nullptr)
       for (int j = threadIdx.x; j < np; j += PQ_THREADS)
@@ -102,6 +190,8 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
       else if (kv.refs != nullptr && kv.refs[p] != 1)
         bits |= SPEC_ST_SHARED;
     }
+    place_rows(kv, layer, row, len, r0, r1, place);
+    for (int j = r0 + threadIdx.x; j < r1; j += PQ_THREADS) s_node[j - r0] = pth != nullptr ? pth[j] : j;
   }
   if (__syncthreads_or(bits))
     for (int b = 1; b <= SPEC_ST_TREE; b <<= 1)
@@ -111,33 +201,34 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
     if (st == 0 && new_len != nullptr) new_len[slot] = len + np;
   }
   if (st != 0) return;
-  const int hd = kv.head_dim, node = kv.n_kv_heads * hd;  // elements of a node's row
+  const int hd = kv.head_dim, node = kv.n_kv_heads * hd, nb = hd / 32;
   const int64_t src0 = (int64_t)layer * new_layer_stride + (int64_t)i * nt * node;
-  const int r0 = blk * CQ_ROWS, r1 = min(np, r0 + CQ_ROWS);
-  const int lane = threadIdx.x & 31, half = lane >> 4, j = lane & 15;
-  const int per = node / 32;  // blocks of a node's row
-  const int64_t count = (int64_t)max(0, r1 - r0) * per;
-  for (int64_t b0 = (threadIdx.x >> 5) * 2; b0 < count; b0 += PQ_THREADS / 16) {
-    const int64_t b = b0 + half;
-    const bool ok = b < count;
-    const int jr = r0 + (ok ? (int)(b / per) : 0), w = ok ? (int)(b % per) : 0, h = w / (hd / 32), u = w % (hd / 32);
-    const int64_t from = src0 + (int64_t)(pth != nullptr ? pth[jr] : jr) * node + w * 32 + 2 * j;
-    const Block k = quantise(ok ? __ldg(reinterpret_cast<const uint32_t*>(k_new + from)) : 0u);
-    const Block v = quantise(ok ? __ldg(reinterpret_cast<const uint32_t*>(v_new + from)) : 0u);
-    if (!ok) continue;
-    const int64_t pos = (int64_t)len + jr;
-    const int64_t at = (int64_t)layer * kv.layer_stride +
-                       ((int64_t)row[pos / kv.page_size] * kv.n_kv_heads + h) * kv.page_size + pos % kv.page_size;
-    const int64_t to = at * (hd / 32) + u;
-    if (j < 8) {
-      reinterpret_cast<uint16_t*>(kv.k_qs)[to * 8 + j] = (uint16_t)k.bytes;
-      reinterpret_cast<uint16_t*>(kv.v_qs)[to * 8 + j] = (uint16_t)v.bytes;
+  const int l = threadIdx.x & 3;
+  constexpr int U = 2;  // rows in flight: four loads a lane
+  each_piece<U>(kv, r0, r1, [&](int r, int e, int64_t block, bool ok) {
+    uint4 k[U], v[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int rr = r + u * CQ_PHASES;
+      const bool there = ok && rr < r1;
+      const int64_t from = src0 + (int64_t)s_node[there ? rr - r0 : r - r0] * node + e;
+      k[u] = there ? __ldcs(reinterpret_cast<const uint4*>(k_new + from)) : make_uint4(0u, 0u, 0u, 0u);
+      v[u] = there ? __ldcs(reinterpret_cast<const uint4*>(v_new + from)) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (j == 0) {
-      kv.k_scales[to] = (uint16_t)k.scale;
-      kv.v_scales[to] = (uint16_t)v.scale;
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int rr = r + u * CQ_PHASES;
+      if (rr >= r1) break;  // (whole warps)
+      const Block kq = quantise(k[u]), vq = quantise(v[u]);
+      const int64_t to = place.at[rr - r0] * nb + block;
+      if (ok && l < 2) {
+        reinterpret_cast<uint2*>(kv.k_qs)[2 * to + l] = kq.codes;
+        reinterpret_cast<uint2*>(kv.v_qs)[2 * to + l] = vq.codes;
+      }
+      if (ok && l == 2) kv.k_scales[to] = (uint16_t)kq.scale;
+      if (ok && l == 3) kv.v_scales[to] = (uint16_t)vq.scale;
     }
-  }
+  });
 }
 
 // The lengths advanced in place, after every CTA of the commit has read them.
@@ -147,11 +238,25 @@ __global__ void q4_advance_kernel(int n, const int32_t* __restrict__ slots, cons
   if (i < n && status[i] == 0) len[slots[i]] += n_path[i];
 }
 
-// Rows out of the cache: a lane has two elements.
+// Eight values out of 8 bytes of codes (already shifted to their low nibbles).
+__device__ __forceinline__ uint4 eight_values(uint2 c, uint32_t s) {
+  const uint32_t s2 = s * 0x10001u;
+  auto two = [&](uint32_t w, uint32_t sel) {
+    uint32_t u, r;
+    const uint32_t x = lop3_and_or(__byte_perm(w, w, sel), 0x000F000Fu, 0x64006400u);
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(u) : "r"(x), "r"(0xE408E408u));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(s2));
+    return r;
+  };
+  return make_uint4(two(c.x, 0x1100), two(c.x, 0x3322), two(c.y, 0x1100), two(c.y, 0x3322));
+}
+
+// Rows out of the cache.
 __global__ void __launch_bounds__(PQ_THREADS)
 q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt, const int32_t* __restrict__ pos0,
-               const int32_t* __restrict__ n_pos, uint16_t* __restrict__ k, uint16_t* __restrict__ v, int n,
+               const int32_t* __restrict__ n_pos, uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                int64_t layer_stride, int blocks, int32_t* __restrict__ status) {
+  __shared__ RowPlace place;
   const int i = blockIdx.x / (kv.n_layers * blocks);
   const int layer = blockIdx.x / blocks % kv.n_layers, blk = blockIdx.x % blocks;
   const int slot = slots[i], np = n_pos[i], p0 = pos0[i];
@@ -160,36 +265,41 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
   if (np < 0 || np > nt) st |= SPEC_ST_TREE;
   if (p0 < 0 || (int64_t)p0 + max(np, 0) > (int64_t)kv.max_pages * kv.page_size) st |= SPEC_ST_FULL;
   const int32_t* row = kv.table + (int64_t)(st == 0 ? slot : 0) * kv.max_pages;
+  const int r0 = blk * CQ_ROWS, r1 = min(np, r0 + CQ_ROWS);
   bool bad = false;
   if (st == 0 && np > 0) {
     const int e1 = (int)(((int64_t)p0 + np - 1) / kv.page_size);
     for (int e = p0 / kv.page_size + threadIdx.x; e <= e1; e += PQ_THREADS) bad |= row[e] < 0 || row[e] >= kv.n_pages;
+    place_rows(kv, layer, row, p0, r0, r1, place);
   }
   if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
   if (layer == 0 && blk == 0 && threadIdx.x == 0) status[i] = st;
   if (st != 0) return;
-  const int hd = kv.head_dim, node = kv.n_kv_heads * hd;
+  const int hd = kv.head_dim, node = kv.n_kv_heads * hd, nb = hd / 32;
   const int64_t dst0 = (int64_t)layer * layer_stride + (int64_t)i * nt * node;
-  const int r0 = blk * CQ_ROWS, r1 = min(np, r0 + CQ_ROWS);
-  const int per = node / 32;
-  const int64_t count = (int64_t)max(0, r1 - r0) * per * 16;
-  for (int64_t e = threadIdx.x; e < count; e += PQ_THREADS) {
-    const int j = (int)(e & 15);
-    const int64_t b = e >> 4;
-    const int jr = r0 + (int)(b / per), w = (int)(b % per), h = w / (hd / 32), u = w % (hd / 32);
-    const int64_t pos = (int64_t)p0 + jr;
-    const int64_t at = (int64_t)layer * kv.layer_stride +
-                       ((int64_t)row[pos / kv.page_size] * kv.n_kv_heads + h) * kv.page_size + pos % kv.page_size;
-    const int64_t from = at * (hd / 32) + u, to = dst0 + (int64_t)jr * node + w * 32 + 2 * j;
-    auto pair = [&](const uint8_t* qs, const uint16_t* sc) {
-      const uint32_t c = reinterpret_cast<const uint16_t*>(qs)[from * 8 + (j & 7)] >> (j >= 8 ? 4 : 0);
-      const float s = half_of(sc[from], 0);
-      const __half2 x = __floats2half2_rn(s * (float)((int)(c & 15u) - 8), s * (float)((int)(c >> 8 & 15u) - 8));
-      return *reinterpret_cast<const uint32_t*>(&x);
-    };
-    *reinterpret_cast<uint32_t*>(k + to) = pair(kv.k_qs, kv.k_scales);
-    *reinterpret_cast<uint32_t*>(v + to) = pair(kv.v_qs, kv.v_scales);
-  }
+  const int l = threadIdx.x & 3, sh = l < 2 ? 0 : 4;
+  constexpr int U = 4;
+  each_piece<U>(kv, r0, r1, [&](int r, int e, int64_t block, bool ok) {
+    uint2 kc[U], vc[U];
+    uint32_t ks[U], vs[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int rr = r + u * CQ_PHASES;
+      const int64_t from = place.at[(rr < r1 ? rr : r) - r0] * nb + block;
+      kc[u] = __ldg(reinterpret_cast<const uint2*>(kv.k_qs) + 2 * from + (l & 1));
+      vc[u] = __ldg(reinterpret_cast<const uint2*>(kv.v_qs) + 2 * from + (l & 1));
+      ks[u] = __ldg(kv.k_scales + from);
+      vs[u] = __ldg(kv.v_scales + from);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int rr = r + u * CQ_PHASES;
+      if (!ok || rr >= r1) break;
+      const int64_t to = dst0 + (int64_t)rr * node + e;
+      __stcs(reinterpret_cast<uint4*>(k + to), eight_values(make_uint2(kc[u].x >> sh, kc[u].y >> sh), ks[u]));
+      __stcs(reinterpret_cast<uint4*>(v + to), eight_values(make_uint2(vc[u].x >> sh, vc[u].y >> sh), vs[u]));
+    }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -429,6 +539,6 @@ extern "C" int spec_pages_q4_read(const spec_pages_q4* kv, int n, const int32_t*
   if (rc != SPEC_OK) return rc;
   const int blocks = (nt + CQ_ROWS - 1) / CQ_ROWS;
   q4_read_kernel<<<(unsigned)(n * kv->n_layers * blocks), PQ_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      *kv, slots, nt, pos0, n_pos, k, v, n, layer_stride, blocks, status);
+      *kv, slots, nt, pos0, n_pos, k, v, layer_stride, blocks, status);
   return launched("4-bit page read");
 }
