@@ -122,9 +122,9 @@ __device__ __forceinline__ Block quantise(const uint4& in) {
 }
 
 // A CTA has up to CQ_ROWS rows (of a node, all heads) of one entry and layer: a
-// warp takes 256 neighbouring elements of a row, eight a lane, of every
+// warp takes 256 neighbouring elements of a row of K or V, eight a lane, of every
 // CQ_PHASES-th row, so that what a lane's place in the row is, is found once.
-constexpr int CQ_ROWS = 64, CQ_PHASES = 8;
+constexpr int CQ_ROWS = 32, CQ_PHASES = 8;
 
 // Where the rows of a CTA lie in the cache (of head 0).
 struct RowPlace {
@@ -137,19 +137,19 @@ __device__ __forceinline__ void place_rows(const spec_pages_q4& kv, int layer, c
     p.at[j - r0] = (int64_t)layer * kv.layer_stride + (int64_t)row[e] * kv.n_kv_heads * kv.page_size + pos - e * kv.page_size;
   }
 }
-// The work of a CTA: f(r, e, block): row r0 <= r < r1, this lane's elements e ... e + 7 of it, and
-// how many blocks behind the row's place (of head 0) theirs is; `ok` false for lanes
-// past the row.  Whole warps.
+// The work of a CTA: f(which, r, e, block, ok): K or V, rows r, r + CQ_PHASES, ... (U of
+// them, below r1), this lane's elements e ... e + 7 of a row, and how many blocks behind the
+// row's place (of head 0) theirs is; `ok` false for lanes past the row.  Whole warps.
 template <int U, class F>
 __device__ __forceinline__ void each_piece(const spec_pages_q4& kv, int r0, int r1, F&& f) {
   const int node = kv.n_kv_heads * kv.head_dim, per = (node + 255) / 256, nb = kv.head_dim / 32;
   const int lane = threadIdx.x & 31;
-  for (int item = threadIdx.x >> 5; item < per * CQ_PHASES; item += PQ_THREADS / 32) {
-    const int phase = item / per, e = (item - phase * per) * 256 + lane * 8;
+  for (int item = threadIdx.x >> 5; item < per * CQ_PHASES * 2; item += PQ_THREADS / 32) {
+    const int part = item >> 1, phase = part / per, e = (part - phase * per) * 256 + lane * 8;
     const bool ok = e < node;
     const int h = ok ? e / kv.head_dim : 0;
     const int64_t block = (int64_t)h * kv.page_size * nb + (ok ? e - h * kv.head_dim : 0) / 32;
-    for (int r = r0 + phase; r < r1; r += CQ_PHASES * U) f(r, ok ? e : 0, block, ok);
+    for (int r = r0 + phase; r < r1; r += CQ_PHASES * U) f(item & 1, r, ok ? e : 0, block, ok);
   }
 }
 
@@ -204,29 +204,26 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
   const int hd = kv.head_dim, node = kv.n_kv_heads * hd, nb = hd / 32;
   const int64_t src0 = (int64_t)layer * new_layer_stride + (int64_t)i * nt * node;
   const int l = threadIdx.x & 3;
-  constexpr int U = 2;  // rows in flight: four loads a lane
-  each_piece<U>(kv, r0, r1, [&](int r, int e, int64_t block, bool ok) {
-    uint4 k[U], v[U];
+  constexpr int U = CQ_ROWS / CQ_PHASES;  // rows in flight
+  each_piece<U>(kv, r0, r1, [&](int which, int r, int e, int64_t block, bool ok) {
+    const uint16_t* src = (which ? v_new : k_new) + src0 + e;
+    uint4 x[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int rr = r + u * CQ_PHASES;
-      const bool there = ok && rr < r1;
-      const int64_t from = src0 + (int64_t)s_node[there ? rr - r0 : r - r0] * node + e;
-      k[u] = there ? __ldcs(reinterpret_cast<const uint4*>(k_new + from)) : make_uint4(0u, 0u, 0u, 0u);
-      v[u] = there ? __ldcs(reinterpret_cast<const uint4*>(v_new + from)) : make_uint4(0u, 0u, 0u, 0u);
+      x[u] = ok && rr < r1 ? __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)s_node[rr - r0] * node))
+                           : make_uint4(0u, 0u, 0u, 0u);
     }
+    uint2* codes = reinterpret_cast<uint2*>(which ? kv.v_qs : kv.k_qs) + 2 * block + l;
+    uint16_t* scales = (which ? kv.v_scales : kv.k_scales) + block;
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int rr = r + u * CQ_PHASES;
       if (rr >= r1) break;  // (whole warps)
-      const Block kq = quantise(k[u]), vq = quantise(v[u]);
-      const int64_t to = place.at[rr - r0] * nb + block;
-      if (ok && l < 2) {
-        reinterpret_cast<uint2*>(kv.k_qs)[2 * to + l] = kq.codes;
-        reinterpret_cast<uint2*>(kv.v_qs)[2 * to + l] = vq.codes;
-      }
-      if (ok && l == 2) kv.k_scales[to] = (uint16_t)kq.scale;
-      if (ok && l == 3) kv.v_scales[to] = (uint16_t)vq.scale;
+      const Block q = quantise(x[u]);
+      const int64_t at = place.at[rr - r0] * nb;
+      if (ok && l < 2) codes[2 * at] = q.codes;
+      if (ok && l == 2) scales[at] = (uint16_t)q.scale;
     }
   });
 }
@@ -278,26 +275,26 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
   const int hd = kv.head_dim, node = kv.n_kv_heads * hd, nb = hd / 32;
   const int64_t dst0 = (int64_t)layer * layer_stride + (int64_t)i * nt * node;
   const int l = threadIdx.x & 3, sh = l < 2 ? 0 : 4;
-  constexpr int U = 4;
-  each_piece<U>(kv, r0, r1, [&](int r, int e, int64_t block, bool ok) {
-    uint2 kc[U], vc[U];
-    uint32_t ks[U], vs[U];
+  constexpr int U = CQ_ROWS / CQ_PHASES;
+  each_piece<U>(kv, r0, r1, [&](int which, int r, int e, int64_t block, bool ok) {
+    const uint2* codes = reinterpret_cast<const uint2*>(which ? kv.v_qs : kv.k_qs) + 2 * block + (l & 1);
+    const uint16_t* scales = (which ? kv.v_scales : kv.k_scales) + block;
+    uint2 c[U];
+    uint32_t sc[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int rr = r + u * CQ_PHASES;
-      const int64_t from = place.at[(rr < r1 ? rr : r) - r0] * nb + block;
-      kc[u] = __ldg(reinterpret_cast<const uint2*>(kv.k_qs) + 2 * from + (l & 1));
-      vc[u] = __ldg(reinterpret_cast<const uint2*>(kv.v_qs) + 2 * from + (l & 1));
-      ks[u] = __ldg(kv.k_scales + from);
-      vs[u] = __ldg(kv.v_scales + from);
+      const int64_t at = place.at[(rr < r1 ? rr : r) - r0] * nb;
+      c[u] = __ldg(codes + 2 * at);
+      sc[u] = __ldg(scales + at);
     }
+    uint16_t* dst = (which ? v : k) + dst0 + e;
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int rr = r + u * CQ_PHASES;
       if (!ok || rr >= r1) break;
-      const int64_t to = dst0 + (int64_t)rr * node + e;
-      __stcs(reinterpret_cast<uint4*>(k + to), eight_values(make_uint2(kc[u].x >> sh, kc[u].y >> sh), ks[u]));
-      __stcs(reinterpret_cast<uint4*>(v + to), eight_values(make_uint2(vc[u].x >> sh, vc[u].y >> sh), vs[u]));
+      __stcs(reinterpret_cast<uint4*>(dst + (int64_t)rr * node),
+             eight_values(make_uint2(c[u].x >> sh, c[u].y >> sh), sc[u]));
     }
   });
 }

@@ -34,7 +34,7 @@ struct QShape {
   static constexpr int RING = STAGES * STAGE;         // of a warp
   static constexpr int XROW = HD + 4;                 // floats of an exchange row (padded)
   static constexpr int EXCHANGE = QA_WARPS * ROWS * (XROW * 4 + 8);
-  static constexpr int NODES = NT == 4 ? 64 : 16;     // rows of the tree's own tile
+  static constexpr int NODES = NT == 4 ? 32 : 16;     // rows of the tree's own tile (no more nodes than rows)
   static constexpr int TREE_OFF = QA_WARPS * RING > EXCHANGE ? QA_WARPS * RING : (EXCHANGE + 127) / 128 * 128;
   static constexpr int Q_OFF = TREE_OFF + 2 * NODES * HD * 2;
   static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, true>::Q_BYTES;
@@ -310,11 +310,16 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
   check_others<QA_THREADS>(a, ROWS, QA_SHIFT, n_cta, QA_WARPS);
 }
 
-// Query rows of a unit.
-int q4_rows(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : 32; }
+// Query rows of a unit.  Up to 32 rows run here, more on the tcgen05 kernel with 64,
+// 128 or 256 that share one read of the cache (tree_attn_tc.cu).
+int q4_rows(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+bool q4_on_tc(int rows) { return rows >= 64; }
 
 int q4_resident(int hd, int rows) {
-  return rows == 32 ? QShape<128, 4>::RESIDENT : hd == 128 ? QShape<128, 1>::RESIDENT : QShape<64, 1>::RESIDENT;
+  return q4_on_tc(rows) ? 1
+         : rows == 32   ? QShape<128, 4>::RESIDENT
+         : hd == 128    ? QShape<128, 1>::RESIDENT
+                        : QShape<64, 1>::RESIDENT;
 }
 // The CTAs with tiles: what is resident, but for the one that plans.
 int q4_ctas(int hd, int rows) { return std::max(1, q4_resident(hd, rows) * device_sms() - 1); }
@@ -363,13 +368,16 @@ int launch_tree_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, const
   TreeArgs a;
   const spec_pages book = book_of(kv);
   const int hd = kv->head_dim, rows = q4_rows(t->nt * (t->n_q_heads / kv->n_kv_heads)), n_cta = q4_ctas(hd, rows);
-  tree_fill(a, &book, 0, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status, rows, QA_SHIFT, n_cta, false);
+  tree_fill(a, &book, 0, t, q, q_stride, k_new, v_new, kv_stride, out, workspace, status, rows,
+            q4_on_tc(rows) ? TREE_TC_SHIFT : QA_SHIFT, n_cta, q4_on_tc(rows));
   const int64_t row = (int64_t)layer * kv->layer_stride;
   a.k_qs = kv->k_qs + row * (hd / 2);
   a.v_qs = kv->v_qs + row * (hd / 2);
   a.k_scales = reinterpret_cast<const __half*>(kv->k_scales) + row * (hd / 32);
   a.v_scales = reinterpret_cast<const __half*>(kv->v_scales) + row * (hd / 32);
-  cudaError_t e = hd == 128 ? launch_q4_rows<128>(a, n_cta, st) : launch_q4_rows<64>(a, n_cta, st);
+  cudaError_t e = q4_on_tc(rows) ? tree_tc_launch(a, hd, n_cta, st)
+                  : hd == 128    ? launch_q4_rows<128>(a, n_cta, st)
+                                 : launch_q4_rows<64>(a, n_cta, st);
   if (e == cudaSuccess) e = tree_join_launch(a, hd, n_cta, st);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("4-bit tree attention: ") + cudaGetErrorString(e));
   return SPEC_OK;

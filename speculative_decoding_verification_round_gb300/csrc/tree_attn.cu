@@ -725,6 +725,8 @@ void tree_fill(TreeArgs& a, const spec_pages* kv, int layer, const spec_tree* t,
   a.part_err = bounded_waits ? err : nullptr;
   a.wait_tries = t_wait_tries;
   a.plan = reinterpret_cast<TreePlan*>(err + ((size_t)n_cta + 3) / 4 * 4);
+  a.k_qs = a.v_qs = nullptr;
+  a.k_scales = a.v_scales = nullptr;
 }
 
 int launch_tree(const spec_pages* kv, int layer, const spec_tree* t, const uint16_t* q,

@@ -46,6 +46,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "key_warp.cuh"
 #include "tc_ops.cuh"
 #include "tree_attn.cuh"
 
@@ -63,12 +64,17 @@ constexpr float P_BIAS = 12.0f;  // log2 of the factor of weights and sum
 constexpr float P_SLACK = 3.0f;  // growth of the maximum before O is rescaled
 constexpr int P_LO = 64;         // columns from the weights' high parts to their low ones
 
-template <int HD>
+// Q4: a cache in 4 bits.  V's ring is a buffer shorter then, and each loading warp
+// has a ring of three half tiles of codes (32 rows) behind the tiles.
+template <int HD, bool Q4>
 struct TcShape {
   static constexpr int TILE = TC_KEYS * HD * 2;  // bytes of a Q, K or V tile
   static constexpr int SUB = TC_KEYS * 128;      // bytes of its 64-dimension part
   static constexpr int RING_OFF = 2 * TILE;
-  static constexpr int END = RING_OFF + TC_RING * TILE;
+  static constexpr int VR = Q4 ? V_RING - 1 : V_RING;
+  static constexpr int CODES_OFF = RING_OFF + (K_RING + VR) * TILE;
+  static constexpr int CODES = 32 * (HD / 2 + HD / 16), CODE_SLOTS = 3;  // bytes of a half tile
+  static constexpr int END = CODES_OFF + (Q4 ? 4 * CODE_SLOTS * CODES : 0);
 };
 
 struct TcSmall {
@@ -85,9 +91,9 @@ struct TcSmall {
 };
 constexpr int SMALL_MAX = 3072;
 static_assert(sizeof(TcSmall) <= SMALL_MAX, "behind the tiles");
-template <int HD>
+template <int HD, bool Q4>
 constexpr size_t tc_smem() {
-  return (size_t)TcShape<HD>::END + SMALL_MAX;
+  return (size_t)TcShape<HD, Q4>::END + SMALL_MAX;
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
@@ -205,9 +211,9 @@ __device__ __forceinline__ uint32_t low_bits(long long n) {
   return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << (int)n) - 1u;
 }
 
-template <int HD, int ROWS>
+template <int HD, int ROWS, bool Q4>
 __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeArgs a) {
-  using Sh = TcShape<HD>;
+  using Sh = TcShape<HD, Q4>;
   constexpr bool TWO = ROWS == 256;
   constexpr int UNITS = HD / 8, CH = HD / 32;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -271,7 +277,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
     uint32_t slot, turn;
   };
   auto item_k = [](uint32_t x) { return Item{x % K_RING, x / K_RING}; };
-  auto item_v = [](uint32_t x) { return Item{K_RING + x % V_RING, x / V_RING}; };
+  auto item_v = [](uint32_t x) { return Item{K_RING + x % (uint32_t)Sh::VR, x / (uint32_t)Sh::VR}; };
 
   // (out of shared memory: nothing is known about them, and kept in registers, here)
   int s = sh.at.s;
@@ -336,59 +342,158 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
       }
       return x;
     };
+    // the tree's own rows to a tile
+    auto load_fresh = [&](uint32_t buf) {
+      const __half* src = fresh + (int64_t)s * a.nt * a.kv_stride + kvh * HD;
+#pragma unroll 4
+      for (int p = 0; p < PASSES; p++) {
+        const int r = 64 * pw + RPP * p + sub;
+        const bool ok = r < q.m;
+        cp16(buf + dst_off(p), src + (ok ? r : 0) * a.kv_stride, ok);
+      }
+    };
+    // a masked tile's V: chunks with infinities or NaN, which 0 * inf would spread to
+    // rows that do not see them, are taken out here and added by the rows that do
+    auto take_out = [&](uint32_t buf) {
+      unsigned long long bad = 0ull;
+#pragma unroll 4
+      for (int p = 0; p < PASSES; p++) {
+        const uint32_t at = buf + dst_off(p);
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+        if (odd_chunk(v)) {
+          bad |= 1ull << (RPP * p + sub);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+        }
+      }
+      return bad;
+    };
+    auto mark = [&](uint32_t slot, unsigned long long bad) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+      if (lane == 0) sh.bad[slot][pw] = bad;
+    };
     bool go = true;
     for (long long left = my_tiles; left > 0 && go; left -= n, off += n, tile0 += n, seg++) {
       next_piece(left);
       // the rows of the next tile are looked up while this one waits for its buffer
       Rows next = lookup(t0);
-      for (int i = 0; i < n; i++) {
-        const int t = t0 + i;
-        const Item item = is_k ? item_k(tile0 + i) : item_v(tile0 + i);
-        const uint32_t slot = item.slot, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
-        const Rows x = next;
-        if (i + 1 < n) next = lookup(t + 1);
-        go = __all_sync(0xffffffffu, wait(sh.empty[slot], item.turn + 1));
-        if (!go) break;
-        if (t == q.tiles - 1) {
-          const __half* src = fresh + (int64_t)s * a.nt * a.kv_stride + kvh * HD;
-#pragma unroll 4
-          for (int p = 0; p < PASSES; p++) {
-            const int r = 64 * pw + RPP * p + sub;
-            const bool ok = r < q.m;
-            cp16(buf + dst_off(p), src + (ok ? r : 0) * a.kv_stride, ok);
-          }
-        } else {
+      if constexpr (!Q4) {
+        for (int i = 0; i < n; i++) {
+          const int t = t0 + i;
+          const Item item = is_k ? item_k(tile0 + i) : item_v(tile0 + i);
+          const uint32_t slot = item.slot, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
+          const Rows x = next;
+          if (i + 1 < n) next = lookup(t + 1);
+          go = __all_sync(0xffffffffu, wait(sh.empty[slot], item.turn + 1));
+          if (!go) break;
+          if (t == q.tiles - 1) {
+            load_fresh(buf);
+          } else {
 #pragma unroll
-          for (int p = 0; p < PASSES; p++) {
-            const uint32_t at = __shfl_sync(0xffffffffu, x.at[p / (PASSES / 2)], (RPP * p + sub) & 31);
+            for (int p = 0; p < PASSES; p++) {
+              const uint32_t at = __shfl_sync(0xffffffffu, x.at[p / (PASSES / 2)], (RPP * p + sub) & 31);
+              const bool ok = at != ~0u;
+              cp16(buf + dst_off(p), pool + (uint64_t)(ok ? at : 0u) * HD, ok);
+            }
+          }
+          if (is_k || !tile_masked(t)) {
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(sh.full[slot])) : "memory");
+            continue;
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          mark(slot, take_out(buf));
+          fence_proxy_async();
+          mbar_arrive(bar(sh.full[slot]));
+        }
+      } else {
+        // codes and scales of half tiles, three of them on their way, become the tile's
+        // rows: a block of 32 elements a lane, eight rows a quarter of the warp (whose 16-byte
+        // stores so lie in different banks)
+        constexpr int CB = HD / 2, SB = HD / 16, CH4 = HD / 32, PER4 = 32 / CH4;
+        const uint32_t ring = sm0 + Sh::CODES_OFF + (warp - PROD_WARP) * (Sh::CODE_SLOTS * Sh::CODES);
+        const uint8_t* qs = is_k ? a.k_qs : a.v_qs;
+        const __half* scales = is_k ? a.k_scales : a.v_scales;
+        auto swz = [](int r) { return HD == 128 ? r >> 1 & 3 : r >> 2 & 1; };
+        auto stage = [&](int c) {  // half tile c of the piece
+          const int i = c >> 1, t = t0 + i;
+          if (i < n && t != q.tiles - 1) {
+            const uint32_t at = c & 1 ? next.at[1] : next.at[0], to = ring + (c % Sh::CODE_SLOTS) * Sh::CODES;
+            const int u4 = lane % CH4;
+#pragma unroll
+            for (int p = 0; p < CH4; p++) {
+              const int r = p * PER4 + lane / CH4;
+              const uint32_t x = __shfl_sync(0xffffffffu, at, r);
+              const bool ok = x != ~0u;
+              cp16(to + r * CB + ((u4 ^ swz(r)) << 4), qs + (uint64_t)(ok ? x : 0u) * CB + u4 * 16, ok);
+            }
             const bool ok = at != ~0u;
-            cp16(buf + dst_off(p), pool + (uint64_t)(ok ? at : 0u) * HD, ok);
+            kw_copy<SB>(to + 32 * CB + lane * SB, scales + (uint64_t)(ok ? at : 0u) * CH4, ok);
           }
-        }
-        if (is_k || !tile_masked(t)) {
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(sh.full[slot])) : "memory");
-          continue;
-        }
-        // a masked tile's V: chunks with infinities or NaN, which 0 * inf
-        // would spread to rows that do not see them, are taken out here and
-        // added by the rows that do
-        asm volatile("cp.async.wait_all;" ::: "memory");
+          asm volatile("cp.async.commit_group;");
+          if ((c & 1) && i + 1 < n) next = lookup(t + 1);
+        };
+        __syncwarp();  // the last piece's half tiles have been read
+        stage(0);
+        stage(1);
         unsigned long long bad = 0ull;
-#pragma unroll 4
-        for (int p = 0; p < PASSES; p++) {
-          const uint32_t at = buf + dst_off(p);
-          uint4 v;
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-          if (odd_chunk(v)) {
-            bad |= 1ull << (RPP * p + sub);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+        for (int c = 0; c < 2 * n; c++) {
+          const int t = t0 + (c >> 1), half = c & 1;
+          const Item item = is_k ? item_k(tile0 + (c >> 1)) : item_v(tile0 + (c >> 1));
+          const uint32_t slot = item.slot, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
+          __syncwarp();  // half tile c - 1 has been read
+          stage(c + 2);
+          if (half == 0) {
+            go = __all_sync(0xffffffffu, wait(sh.empty[slot], item.turn + 1));
+            if (!go) break;
+            bad = 0ull;
+          }
+          if (t == q.tiles - 1) {  // (both halves at once)
+            if (half == 1) continue;
+            load_fresh(buf);
+            if (is_k) {
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(sh.full[slot])) : "memory");
+              continue;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            mark(slot, take_out(buf));
+            fence_proxy_async();
+            mbar_arrive(bar(sh.full[slot]));
+            continue;
+          }
+          const bool masked = !is_k && tile_masked(t);
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+          __syncwarp();
+          const uint32_t from = ring + (c % Sh::CODE_SLOTS) * Sh::CODES;
+#pragma unroll 2
+          for (int it = 0; it < CH4; it++) {
+            const int r = HD == 128 ? (lane & 7) + 8 * it : (lane & 7) + 8 * ((lane >> 4) + 2 * it);
+            const int b = HD == 128 ? lane >> 3 : lane >> 3 & 1, row = 64 * pw + 32 * half + r;
+            const uint4 w = kw_lds128(from + r * CB + ((b ^ swz(r)) << 4));
+            uint32_t sc = kw_lds16(from + 32 * CB + r * SB + 2 * b);
+            if (masked && odd_half(sc)) {
+              bad |= 1ull << (32 * half + r);
+              sc = 0u;
+            }
+            const uint32_t s2 = sc * 0x10001u;
+            auto put = [&](int u, uint32_t wa, uint32_t wb, bool high) {
+              auto two = [&](uint32_t x) { return kw_hmul2(high ? q4_high(x) : q4_low(x), s2); };
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + (u >> 3) * Sh::SUB + sw128_off(row, u & 7)),
+                           "r"(two(__byte_perm(wa, wa, 0x1100))), "r"(two(__byte_perm(wa, wa, 0x3322))),
+                           "r"(two(__byte_perm(wb, wb, 0x1100))), "r"(two(__byte_perm(wb, wb, 0x3322)))
+                           : "memory");
+            };
+            put(4 * b, w.x, w.y, false);
+            put(4 * b + 1, w.z, w.w, false);
+            put(4 * b + 2, w.x, w.y, true);
+            put(4 * b + 3, w.z, w.w, true);
+          }
+          if (half == 1) {
+            if (masked) mark(slot, bad);
+            fence_proxy_async();
+            mbar_arrive(bar(sh.full[slot]));
           }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-        if (lane == 0) sh.bad[slot][pw] = bad;
-        fence_proxy_async();
-        mbar_arrive(bar(sh.full[slot]));
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -653,6 +758,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
                   const int key = 64 * b + __ffsll((long long)left) - 1;
                   const float p = half_of(tm_ld1(tS + (key >> 1)), key & 1) + half_of(tm_ld1(tS + P_LO + (key >> 1)), key & 1);
                   const __half* src = a.v;
+                  int64_t cached = 0;  // the cache's row
                   if (tree) {
                     if (key >= q.m) continue;
                     src = a.v_new + ((int64_t)s * a.nt + key) * a.kv_stride + kvh * HD;
@@ -661,7 +767,33 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
                     if (at >= q.len) continue;
                     const int pg = a.table[(int64_t)q.slot * a.max_pages + e];
                     if (pg < 0 || pg >= a.n_pages) continue;
-                    src += (((int64_t)pg * a.nkv + kvh) * a.page_size + (at - e * a.page_size)) * HD;
+                    cached = ((int64_t)pg * a.nkv + kvh) * a.page_size + (at - e * a.page_size);
+                    src += cached * HD;
+                  }
+                  if constexpr (Q4) {
+                    if (!tree) {  // blocks of 32 whose scale is infinite or NaN
+#pragma unroll 1
+                      for (int d = 0; d < CH; d++) {
+                        const uint32_t sc = __half_as_ushort(a.v_scales[cached * CH + d]);
+                        if (!odd_half(sc)) continue;  // (the warp's)
+                        uint32_t o[32];
+                        tm_ld32(tO + 32 * d, o);
+                        tm_wait_ld(o);
+                        const uint4 w = *reinterpret_cast<const uint4*>(a.v_qs + (cached * CH + d) * 16);
+                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                        if (p > 0.0f) {
+#pragma unroll
+                          for (int e = 0; e < 32; e++) {
+                            const int u = ww[(e & 15) >> 2] >> (8 * (e & 3) + (e >> 4) * 4) & 15;
+                            o[e] = __float_as_uint(fmaf(p, half_of(sc, 0) * (float)(u - 8), __uint_as_float(o[e])));
+                          }
+                        }
+                        __syncwarp();
+                        tm_st32(tO + 32 * d, o);
+                        tm_wait_st();
+                      }
+                      continue;
+                    }
                   }
 #pragma unroll 1
                   for (int d = 0; d < CH; d++) {
@@ -815,35 +947,40 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   if (tid == 0) a.part_err[blockIdx.x] = sh.abort != 0 ? 1u : 0u;
 }
 
-template <int HD, int ROWS>
+template <int HD, int ROWS, bool Q4>
 cudaError_t launch(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  return launch_dependent(tree_attn_tc_kernel<HD, ROWS>, n_cta + 1, TC_THREADS, tc_smem<HD>(), st, a);
+  return launch_dependent(tree_attn_tc_kernel<HD, ROWS, Q4>, n_cta + 1, TC_THREADS, tc_smem<HD, Q4>(), st, a);
 }
 
-template <int HD>
+template <int HD, bool Q4>
 cudaError_t launch_rows(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  return a.rows == 64    ? launch<HD, 64>(a, n_cta, st)
-         : a.rows == 128 ? launch<HD, 128>(a, n_cta, st)
-                         : launch<HD, 256>(a, n_cta, st);
+  return a.rows == 64    ? launch<HD, 64, Q4>(a, n_cta, st)
+         : a.rows == 128 ? launch<HD, 128, Q4>(a, n_cta, st)
+                         : launch<HD, 256, Q4>(a, n_cta, st);
 }
 
-template <int HD, int ROWS>
+template <int HD, int ROWS, bool Q4>
 void init() {
-  cudaFuncSetAttribute(tree_attn_tc_kernel<HD, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)tc_smem<HD>());
+  cudaFuncSetAttribute(tree_attn_tc_kernel<HD, ROWS, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)tc_smem<HD, Q4>());
+}
+template <int HD, bool Q4>
+void init_rows() {
+  init<HD, 64, Q4>();
+  init<HD, 128, Q4>();
+  init<HD, 256, Q4>();
 }
 
 }  // namespace
 
 cudaError_t tree_tc_launch(const TreeArgs& a, int hd, int n_cta, cudaStream_t st) {
-  return hd == 128 ? launch_rows<128>(a, n_cta, st) : launch_rows<64>(a, n_cta, st);
+  if (a.k_qs != nullptr) return hd == 128 ? launch_rows<128, true>(a, n_cta, st) : launch_rows<64, true>(a, n_cta, st);
+  return hd == 128 ? launch_rows<128, false>(a, n_cta, st) : launch_rows<64, false>(a, n_cta, st);
 }
 
 void tree_tc_init_attrs() {
-  init<64, 64>();
-  init<64, 128>();
-  init<64, 256>();
-  init<128, 64>();
-  init<128, 128>();
-  init<128, 256>();
+  init_rows<64, false>();
+  init_rows<128, false>();
+  init_rows<64, true>();
+  init_rows<128, true>();
 }

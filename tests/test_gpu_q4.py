@@ -149,7 +149,7 @@ def test_large_scores_and_a_given_scale(dev):
             c.check(c.call())
 
 
-@pytest.mark.parametrize("hd,nq,nt", [(64, 2, 1), (128, 8, 4), (128, 8, 8), (128, 40, 8)])
+@pytest.mark.parametrize("hd,nq,nt", [(64, 2, 1), (128, 8, 4), (128, 8, 8), (128, 40, 8), (64, 16, 8), (64, 16, 64)])
 def test_nothing_of_what_is_masked_gets_in(dev, hd, nq, nt):
     """Rows that a row does not see -- behind the length, in front of the window,
     in other branches, past the node count -- may hold NaN scales, infinities and NaN."""
@@ -199,11 +199,54 @@ def test_infinities_of_the_trees_own_rows(dev):
         c.check(c.call())
 
 
+@pytest.mark.parametrize("nq,nkv,hd,n,longest,nt", [(32, 8, 128, 2, 9001, 16), (16, 8, 64, 3, 7000, 40),
+                                                    (32, 8, 128, 500, 290, 16), (40, 8, 128, 300, 140, 16),
+                                                    (8, 2, 64, 700, 200, 64), (32, 8, 128, 40, 3000, 1), (16, 2, 64, 60, 2000, 2)])
+def test_repeated_calls_agree(dev, nq, nkv, hd, n, longest, nt):
+    """No result depends on how the warps of a CTA run against each other: the same
+    call forty times, bit by bit."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng([31, nq, n])
+    lens = g.integers(0, longest + 1, n)
+    lens[:2] = longest
+    c = Q4Case(sv, dev, g, nq, nkv, hd, lens.tolist(), nt, 64, layers=1)
+    first = c.call()
+    c.check(first, range(0, n, max(1, n // 12)))
+    out, kv, slots, parents, counts = c.out, c.pool(), c.T(c.slots), c.T(c.parents), c.T(c.counts)
+    q, kn, vn, want = c.T(c.q), c.T(c.kn), c.T(c.vn), c.out.clone()
+    ws = torch.empty(sv.spec_tree_attn_q4_workspace(kv, n, nt, nq), dtype=torch.uint8, device=dev)
+    for _ in range(40):
+        out.fill_(7.0)
+        sv.spec_tree_attn_q4(kv, 0, n, slots, nt, nq, q, kn, vn, out, ws, c.status, parents=parents, n_nodes=counts)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+def test_waits_that_give_up(dev):
+    """Every CTA's first wait for scores gives up at once: its sequences are NaN
+    with SPEC_ST_TIMEOUT, and the next call is served."""
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(16)
+    try:
+        for nq, hd, nt in ((8, 64, 16), (8, 128, 24), (16, 128, 40)):
+            c = Q4Case(sv, dev, g, nq, 2, hd, [900, 130, 0], nt, 32)
+            good = c.call()
+            c.check(good)
+            sv.spec_tree_set_wait_budget(0)
+            got = c.call()
+            assert c.status.tolist() == [sv.SPEC_ST_TIMEOUT] * 3 and np.isnan(got).all()
+            sv.spec_tree_set_wait_budget(131072)
+            assert np.array_equal(c.call().view(np.uint16), good.view(np.uint16))
+            assert c.status.tolist() == [0, 0, 0]
+    finally:
+        sv.spec_tree_set_wait_budget(131072)
+
+
 def test_scales_of_any_size(dev):
     """Values from fp16's smallest to near its largest."""
     import speculative_decoding_verification_round_gb300 as sv
     g = np.random.default_rng(15)
-    for e, nt in ((-24, 1), (-20, 4), (-16, 8), (-13, 1), (11, 4), (12, 12)):
+    for e, nt in ((-24, 1), (-20, 4), (-16, 8), (-13, 1), (11, 4), (12, 12), (-24, 16), (12, 40)):
         c = Q4Case(sv, dev, g, 8, 2, 64, [300, 90], nt, 32)
         c.vs[:] = np.sign(c.vs) * np.exp2(e) * (1 if e < -18 else 1.9921875)
         c.v = lc.values(c.vc, c.vs).astype(np.float16)
