@@ -62,10 +62,11 @@ __device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
 // A block of 32 elements, eight a lane (lane l of four has 8 l ...), to its scale
 // (fp16 bits, every lane) and codes (lanes 0 and 1: 8 bytes each).
 //
-// x / d is not divided: y = x (1 / d) is within two units of it, and one step
+// x / d is not divided: y = x (1 / d) is within a few units of it, and one step
 // y + (x - y d) (1 / d) then is exact wherever x / d is a half of an odd number.
 // Nothing else is near one: x has 11 bits and d 8, so that |x / d - (k + 1/2)| is 0
-// or at least 2^-13.
+// or at least 2^-13.  |x / d| is at most 8 (1 + 2^-8) unless d is subnormal in fp16, so
+// that only 8 has to be kept from the codes: by a saturated (q + 9) / 16.
 struct Block {
   uint32_t scale;
   uint2 codes;
@@ -95,36 +96,42 @@ __device__ __forceinline__ Block quantise(const uint4& in) {
   }
   Block out;
   const bool fine = up < INFINITY && down < INFINITY;  // (a NaN is not)
-  const float d = fine ? block_scale(m) : 0.0f, inv = d != 0.0f ? __frcp_rn(d) : 0.0f;
+  const float d = fine ? block_scale(m) : 0.0f;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
+  if (d == 0.0f) inv = 0.0f;
+  const bool small = __any_sync(0xffffffffu, fabsf(d) < 0x1p-13f);
   out.scale = fine ? __half_as_ushort(__float2half_rn(d)) : 0x7E00u;
   const uint64_t inv2 = pair_of(inv, inv), neg2 = pair_of(-d, -d), magic = pair_of(12582912.0f, 12582912.0f),
                  back = pair_of(-12582912.0f, -12582912.0f);
   uint32_t u[4];
 #pragma unroll
   for (int e = 0; e < 4; e++) {
-    const uint32_t v = fine ? x[e] : 0u;  // (d = 0: everything 0)
-    const uint64_t f = pair_of(half_of(v, 0), half_of(v, 1));
+    const uint64_t f = pair_of(half_of(x[e], 0), half_of(x[e], 1));
     uint64_t y = mul2f(f, inv2);
-    y = fma2f(fma2f(y, neg2, f), d != 0.0f ? inv2 : 0ull, y);
+    y = fma2f(fma2f(y, neg2, f), inv2, y);
     y = add2f(add2f(y, magic), back);  // to whole numbers, to even
     float a, b;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(y));
     uint32_t q;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q) : "f"(b), "f"(a));
-    q = min2(max2(q, 0xC800C800u), 0x47004700u);  // [-8, 7]
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(u[e]) : "r"(q), "r"(0x64086408u));  // 1024 + q + 8
+    if (small) q = max2(q, 0xC800C800u);  // -8
+    asm("fma.rn.sat.f16x2 %0, %1, %2, %3;" : "=r"(q) : "r"(q), "r"(0x2C002C00u), "r"(0x38803880u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(u[e]) : "r"(q), "r"(0x4C004C00u), "r"(0x63FE63FEu));  // 16 (...) + 1023
   }
-  const uint32_t c0 = __byte_perm(u[0], u[1], 0x6420) & 0x0F0F0F0Fu, c1 = __byte_perm(u[2], u[3], 0x6420) & 0x0F0F0F0Fu;
+  uint32_t c0 = __byte_perm(u[0], u[1], 0x6420) & 0x0F0F0F0Fu, c1 = __byte_perm(u[2], u[3], 0x6420) & 0x0F0F0F0Fu;
+  if (!fine) c0 = c1 = 0x08080808u;
   // element j and j + 16 share a byte: lanes 0, 1 and lanes 2, 3
-  out.codes.x = c0 | __shfl_down_sync(0xffffffffu, c0, 2) << 4;
-  out.codes.y = c1 | __shfl_down_sync(0xffffffffu, c1, 2) << 4;
+  out.codes.x = c0 + __shfl_down_sync(0xffffffffu, c0, 2) * 16u;
+  out.codes.y = c1 + __shfl_down_sync(0xffffffffu, c1, 2) * 16u;
   return out;
 }
 
 // A CTA has up to CQ_ROWS rows (of a node, all heads) of one entry and layer: a
-// warp takes 256 neighbouring elements of a row of K or V, eight a lane, of every
-// CQ_PHASES-th row, so that what a lane's place in the row is, is found once.
-constexpr int CQ_ROWS = 32, CQ_PHASES = 8;
+// warp takes 256 neighbouring elements of K or V, eight a lane, of every row (every
+// second, fourth or eighth one where a row is shorter than 1024 elements), so that what a
+// lane's place in the row is, is found once; CQ_FLIGHT rows are in flight.
+constexpr int CQ_ROWS = 32, CQ_FLIGHT = 4, PQ_WARPS = PQ_THREADS / 32;
 
 // Where the rows of a CTA lie in the cache (of head 0).
 struct RowPlace {
@@ -137,23 +144,23 @@ __device__ __forceinline__ void place_rows(const spec_pages_q4& kv, int layer, c
     p.at[j - r0] = (int64_t)layer * kv.layer_stride + (int64_t)row[e] * kv.n_kv_heads * kv.page_size + pos - e * kv.page_size;
   }
 }
-// The work of a CTA: f(which, r, e, block, ok): K or V, rows r, r + CQ_PHASES, ... (U of
+// The work of a CTA: f(which, r, step, e, block, ok): K or V, rows r, r + step, ... (CQ_FLIGHT of
 // them, below r1), this lane's elements e ... e + 7 of a row, and how many blocks behind the
 // row's place (of head 0) theirs is; `ok` false for lanes past the row.  Whole warps.
-template <int U, class F>
+template <class F>
 __device__ __forceinline__ void each_piece(const spec_pages_q4& kv, int r0, int r1, F&& f) {
   const int node = kv.n_kv_heads * kv.head_dim, per = (node + 255) / 256, nb = kv.head_dim / 32;
-  const int lane = threadIdx.x & 31;
-  for (int item = threadIdx.x >> 5; item < per * CQ_PHASES * 2; item += PQ_THREADS / 32) {
+  const int lane = threadIdx.x & 31, step = per >= PQ_WARPS / 2 ? 1 : PQ_WARPS / 2 / per;
+  for (int item = threadIdx.x >> 5; item < per * step * 2; item += PQ_WARPS) {
     const int part = item >> 1, phase = part / per, e = (part - phase * per) * 256 + lane * 8;
     const bool ok = e < node;
     const int h = ok ? e / kv.head_dim : 0;
     const int64_t block = (int64_t)h * kv.page_size * nb + (ok ? e - h * kv.head_dim : 0) / 32;
-    for (int r = r0 + phase; r < r1; r += CQ_PHASES * U) f(item & 1, r, ok ? e : 0, block, ok);
+    for (int r = r0 + phase; r < r1; r += step * CQ_FLIGHT) f(item & 1, r, step, ok ? e : 0, block, ok);
   }
 }
 
-__global__ void __launch_bounds__(PQ_THREADS)
+__global__ void __launch_bounds__(PQ_THREADS, 5)
 q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slots, int nt,
                  const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new, int64_t new_layer_stride,
                  const int32_t* __restrict__ path, const int32_t* __restrict__ n_path,
@@ -204,13 +211,13 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
   const int hd = kv.head_dim, node = kv.n_kv_heads * hd, nb = hd / 32;
   const int64_t src0 = (int64_t)layer * new_layer_stride + (int64_t)i * nt * node;
   const int l = threadIdx.x & 3;
-  constexpr int U = CQ_ROWS / CQ_PHASES;  // rows in flight
-  each_piece<U>(kv, r0, r1, [&](int which, int r, int e, int64_t block, bool ok) {
+  constexpr int U = CQ_FLIGHT;
+  each_piece(kv, r0, r1, [&](int which, int r, int step, int e, int64_t block, bool ok) {
     const uint16_t* src = (which ? v_new : k_new) + src0 + e;
     uint4 x[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int rr = r + u * CQ_PHASES;
+      const int rr = r + u * step;
       x[u] = ok && rr < r1 ? __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)s_node[rr - r0] * node))
                            : make_uint4(0u, 0u, 0u, 0u);
     }
@@ -218,7 +225,7 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
     uint16_t* scales = (which ? kv.v_scales : kv.k_scales) + block;
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int rr = r + u * CQ_PHASES;
+      const int rr = r + u * step;
       if (rr >= r1) break;  // (whole warps)
       const Block q = quantise(x[u]);
       const int64_t at = place.at[rr - r0] * nb;
@@ -249,7 +256,7 @@ __device__ __forceinline__ uint4 eight_values(uint2 c, uint32_t s) {
 }
 
 // Rows out of the cache.
-__global__ void __launch_bounds__(PQ_THREADS)
+__global__ void __launch_bounds__(PQ_THREADS, 6)
 q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt, const int32_t* __restrict__ pos0,
                const int32_t* __restrict__ n_pos, uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                int64_t layer_stride, int blocks, int32_t* __restrict__ status) {
@@ -275,15 +282,15 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
   const int hd = kv.head_dim, node = kv.n_kv_heads * hd, nb = hd / 32;
   const int64_t dst0 = (int64_t)layer * layer_stride + (int64_t)i * nt * node;
   const int l = threadIdx.x & 3, sh = l < 2 ? 0 : 4;
-  constexpr int U = CQ_ROWS / CQ_PHASES;
-  each_piece<U>(kv, r0, r1, [&](int which, int r, int e, int64_t block, bool ok) {
+  constexpr int U = CQ_FLIGHT;
+  each_piece(kv, r0, r1, [&](int which, int r, int step, int e, int64_t block, bool ok) {
     const uint2* codes = reinterpret_cast<const uint2*>(which ? kv.v_qs : kv.k_qs) + 2 * block + (l & 1);
     const uint16_t* scales = (which ? kv.v_scales : kv.k_scales) + block;
     uint2 c[U];
     uint32_t sc[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int rr = r + u * CQ_PHASES;
+      const int rr = r + u * step;
       const int64_t at = place.at[(rr < r1 ? rr : r) - r0] * nb;
       c[u] = __ldg(codes + 2 * at);
       sc[u] = __ldg(scales + at);
@@ -291,7 +298,7 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
     uint16_t* dst = (which ? v : k) + dst0 + e;
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int rr = r + u * CQ_PHASES;
+      const int rr = r + u * step;
       if (!ok || rr >= r1) break;
       __stcs(reinterpret_cast<uint4*>(dst + (int64_t)rr * node),
              eight_values(make_uint2(c[u].x >> sh, c[u].y >> sh), sc[u]));
