@@ -2,8 +2,8 @@
 // it (commit), read back, copied; fork, extend and free are the bookkeeping of
 // pages.cu.
 //
-// A lane has eight neighbouring elements of fp16, 16 bytes, and four lanes a block
-// of 32: two exchanges find its largest element.
+// Two lanes have a block of 32 elements, lane l of them elements 8 l ... 8 l + 7 and 16 +
+// 8 l ...: those that share its eight bytes of codes.
 #include <algorithm>
 #include <climits>
 
@@ -59,42 +59,39 @@ __device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
   return r;
 }
 
-// A block of 32 elements, eight a lane (lane l of four has 8 l ...), to its scale
-// (fp16 bits, every lane) and codes (lanes 0 and 1: 8 bytes each).
+// Half a block of 32 elements (see above; low: elements 8 l ..., high: 16 + 8 l ...) to the
+// block's scale (fp16 bits) and its codes' bytes 8 l ... 8 l + 7.
 //
 // x / d is not divided: y = x (1 / d) is within a few units of it, and one step
 // y + (x - y d) (1 / d) then is exact wherever x / d is a half of an odd number.
 // Nothing else is near one: x has 11 bits and d 8, so that |x / d - (k + 1/2)| is 0
 // or at least 2^-13.  |x / d| is at most 8 (1 + 2^-8) unless d is subnormal in fp16, so
 // that only 8 has to be kept from the codes: by a saturated (q + 9) / 16.
-struct Block {
+struct Half {
   uint32_t scale;
   uint2 codes;
 };
-__device__ __forceinline__ Block quantise(const uint4& in) {
-  const uint32_t x[4] = {in.x, in.y, in.z, in.w};
-  uint32_t hi = max2(max2(x[0], x[1]), max2(x[2], x[3])), lo = min2(min2(x[0], x[1]), min2(x[2], x[3]));
-  hi = max2(hi, __byte_perm(hi, hi, 0x1032));
-  lo = min2(lo, __byte_perm(lo, lo, 0x1032));
-  uint32_t both = __byte_perm(hi, lo ^ 0x80008000u, 0x5410);  // the largest, and minus the least
+__device__ __forceinline__ Half quantise(const uint4& low, const uint4& high) {
+  const uint32_t x[8] = {low.x, low.y, low.z, low.w, high.x, high.y, high.z, high.w};
+  uint32_t hi = max2(max2(max2(x[0], x[1]), max2(x[2], x[3])), max2(max2(x[4], x[5]), max2(x[6], x[7])));
+  uint32_t lo = min2(min2(min2(x[0], x[1]), min2(x[2], x[3])), min2(min2(x[4], x[5]), min2(x[6], x[7])));
+  // (the largest, minus the least)
+  uint32_t both = max2(__byte_perm(hi, lo, 0x5410) ^ 0x80000000u, __byte_perm(hi, lo, 0x7632) ^ 0x80000000u);
   both = max2(both, __shfl_xor_sync(0xffffffffu, both, 1));
-  both = max2(both, __shfl_xor_sync(0xffffffffu, both, 2));
   const float up = half_of(both, 0), down = half_of(both, 1);
   float m = up > down ? up : -down;
   if (__any_sync(0xffffffffu, up == down && up != 0.0f)) {  // the first of both decides
-    int first = 32;
+    int first = 128;
     const uint32_t top = both & 0x7FFFu;
 #pragma unroll
-    for (int e = 7; e >= 0; e--) {
+    for (int e = 15; e >= 0; e--) {
       const uint32_t v = x[e >> 1] >> (16 * (e & 1));
-      if ((v & 0x7FFFu) == top) first = 2 * (8 * (int)(threadIdx.x & 3) + e) + (int)(v >> 15 & 1u);
+      if ((v & 0x7FFFu) == top) first = 2 * ((e >> 3) * 16 + 8 * (int)(threadIdx.x & 1) + (e & 7)) + (int)(v >> 15 & 1u);
     }
-    if (first == 32) first = 64;
     first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
-    first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
     if (up == down) m = first & 1 ? -up : up;
   }
-  Block out;
+  Half out;
   const bool fine = up < INFINITY && down < INFINITY;  // (a NaN is not)
   const float d = fine ? block_scale(m) : 0.0f;
   float inv;
@@ -104,9 +101,9 @@ __device__ __forceinline__ Block quantise(const uint4& in) {
   out.scale = fine ? __half_as_ushort(__float2half_rn(d)) : 0x7E00u;
   const uint64_t inv2 = pair_of(inv, inv), neg2 = pair_of(-d, -d), magic = pair_of(12582912.0f, 12582912.0f),
                  back = pair_of(-12582912.0f, -12582912.0f);
-  uint32_t u[4];
+  uint32_t u[8];
 #pragma unroll
-  for (int e = 0; e < 4; e++) {
+  for (int e = 0; e < 8; e++) {
     const uint64_t f = pair_of(half_of(x[e], 0), half_of(x[e], 1));
     uint64_t y = mul2f(f, inv2);
     y = fma2f(fma2f(y, neg2, f), inv2, y);
@@ -117,23 +114,22 @@ __device__ __forceinline__ Block quantise(const uint4& in) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q) : "f"(b), "f"(a));
     if (small) q = max2(q, 0xC800C800u);  // -8
     asm("fma.rn.sat.f16x2 %0, %1, %2, %3;" : "=r"(q) : "r"(q), "r"(0x2C002C00u), "r"(0x38803880u));
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(u[e]) : "r"(q), "r"(0x4C004C00u), "r"(0x63FE63FEu));  // 16 (...) + 1023
+    // 16 (q + 9) / 16 + 1023 = 1024 + code
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(u[e]) : "r"(q), "r"(0x4C004C00u), "r"(0x63FE63FEu));
   }
-  uint32_t c0 = __byte_perm(u[0], u[1], 0x6420) & 0x0F0F0F0Fu, c1 = __byte_perm(u[2], u[3], 0x6420) & 0x0F0F0F0Fu;
-  if (!fine) c0 = c1 = 0x08080808u;
-  // element j and j + 16 share a byte: lanes 0, 1 and lanes 2, 3
-  out.codes.x = c0 + __shfl_down_sync(0xffffffffu, c0, 2) * 16u;
-  out.codes.y = c1 + __shfl_down_sync(0xffffffffu, c1, 2) * 16u;
+  out.codes.x = __byte_perm(u[0], u[1], 0x6420) + __byte_perm(u[4], u[5], 0x6420) * 16u;
+  out.codes.y = __byte_perm(u[2], u[3], 0x6420) + __byte_perm(u[6], u[7], 0x6420) * 16u;
+  if (!fine) out.codes.x = out.codes.y = 0x88888888u;
   return out;
 }
 
 // A CTA has up to CQ_ROWS rows (of a node, all heads) of one entry and layer: a
-// warp takes 256 neighbouring elements of K or V, eight a lane, of every row (every
-// second, fourth or eighth one where a row is shorter than 1024 elements), so that what a
+// warp takes 512 neighbouring elements of K or V, half a block a lane, of every row (every
+// second, fourth or eighth one where a row is shorter than 2048 elements), so that what a
 // lane's place in the row is, is found once; CQ_FLIGHT rows are in flight.
-constexpr int CQ_ROWS = 32, CQ_FLIGHT = 4, PQ_WARPS = PQ_THREADS / 32;
+constexpr int CQ_ROWS = 32, CQ_FLIGHT = 2, PQ_WARPS = PQ_THREADS / 32;
 
-// Where the rows of a CTA lie in the cache (of head 0).
+// Where the rows of a CTA lie in the cache (of head 0), in blocks.
 struct RowPlace {
   int64_t at[CQ_ROWS];
 };
@@ -141,22 +137,24 @@ __device__ __forceinline__ void place_rows(const spec_pages_q4& kv, int layer, c
                                            int r1, RowPlace& p) {
   for (int j = r0 + threadIdx.x; j < r1; j += PQ_THREADS) {
     const int64_t pos = pos0 + j, e = pos / kv.page_size;
-    p.at[j - r0] = (int64_t)layer * kv.layer_stride + (int64_t)row[e] * kv.n_kv_heads * kv.page_size + pos - e * kv.page_size;
+    p.at[j - r0] = ((int64_t)layer * kv.layer_stride + (int64_t)row[e] * kv.n_kv_heads * kv.page_size + pos -
+                    e * kv.page_size) * (kv.head_dim / 32);
   }
 }
 // The work of a CTA: f(which, r, step, e, block, ok): K or V, rows r, r + step, ... (CQ_FLIGHT of
-// them, below r1), this lane's elements e ... e + 7 of a row, and how many blocks behind the
-// row's place (of head 0) theirs is; `ok` false for lanes past the row.  Whole warps.
+// them, below r1), this lane's first element e of a row (and eight from e + 16 on), and how many
+// blocks behind the row's place (of head 0) its block is; `ok` false for lanes past the
+// row.  Whole warps.
 template <class F>
 __device__ __forceinline__ void each_piece(const spec_pages_q4& kv, int r0, int r1, F&& f) {
-  const int node = kv.n_kv_heads * kv.head_dim, per = (node + 255) / 256, nb = kv.head_dim / 32;
+  const int nb = kv.head_dim / 32, blocks = kv.n_kv_heads * nb, per = (blocks + 15) / 16;
   const int lane = threadIdx.x & 31, step = per >= PQ_WARPS / 2 ? 1 : PQ_WARPS / 2 / per;
   for (int item = threadIdx.x >> 5; item < per * step * 2; item += PQ_WARPS) {
-    const int part = item >> 1, phase = part / per, e = (part - phase * per) * 256 + lane * 8;
-    const bool ok = e < node;
-    const int h = ok ? e / kv.head_dim : 0;
-    const int64_t block = (int64_t)h * kv.page_size * nb + (ok ? e - h * kv.head_dim : 0) / 32;
-    for (int r = r0 + phase; r < r1; r += step * CQ_FLIGHT) f(item & 1, r, step, ok ? e : 0, block, ok);
+    const int part = item >> 1, phase = part / per, b = (part - phase * per) * 16 + (lane >> 1);
+    const bool ok = b < blocks;
+    const int h = ok ? b / nb : 0, e = ok ? 32 * b + 8 * (lane & 1) : 0;
+    const int64_t block = (int64_t)h * kv.page_size * nb + (ok ? b - h * nb : 0);
+    for (int r = r0 + phase; r < r1; r += step * CQ_FLIGHT) f(item & 1, r, step, e, block, ok);
   }
 }
 
@@ -208,18 +206,22 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
     if (st == 0 && new_len != nullptr) new_len[slot] = len + np;
   }
   if (st != 0) return;
-  const int hd = kv.head_dim, node = kv.n_kv_heads * hd, nb = hd / 32;
+  const int node = kv.n_kv_heads * kv.head_dim;
   const int64_t src0 = (int64_t)layer * new_layer_stride + (int64_t)i * nt * node;
-  const int l = threadIdx.x & 3;
+  const int l = threadIdx.x & 1;
   constexpr int U = CQ_FLIGHT;
   each_piece(kv, r0, r1, [&](int which, int r, int step, int e, int64_t block, bool ok) {
     const uint16_t* src = (which ? v_new : k_new) + src0 + e;
-    uint4 x[U];
+    uint4 x[U][2];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int rr = r + u * step;
-      x[u] = ok && rr < r1 ? __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)s_node[rr - r0] * node))
-                           : make_uint4(0u, 0u, 0u, 0u);
+      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (ok && rr < r1) {
+        const uint4* p = reinterpret_cast<const uint4*>(src + (int64_t)s_node[rr - r0] * node);
+        x[u][0] = __ldcs(p);
+        x[u][1] = __ldcs(p + 2);
+      }
     }
     uint2* codes = reinterpret_cast<uint2*>(which ? kv.v_qs : kv.k_qs) + 2 * block + l;
     uint16_t* scales = (which ? kv.v_scales : kv.k_scales) + block;
@@ -227,10 +229,12 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
     for (int u = 0; u < U; u++) {
       const int rr = r + u * step;
       if (rr >= r1) break;  // (whole warps)
-      const Block q = quantise(x[u]);
-      const int64_t at = place.at[rr - r0] * nb;
-      if (ok && l < 2) codes[2 * at] = q.codes;
-      if (ok && l == 2) scales[at] = (uint16_t)q.scale;
+      const Half q = quantise(x[u][0], x[u][1]);
+      const int64_t at = place.at[rr - r0];
+      if (ok) {
+        codes[2 * at] = q.codes;
+        if (l == 0) scales[at] = (uint16_t)q.scale;
+      }
     }
   });
 }
@@ -242,13 +246,18 @@ __global__ void q4_advance_kernel(int n, const int32_t* __restrict__ slots, cons
   if (i < n && status[i] == 0) len[slots[i]] += n_path[i];
 }
 
-// Eight values out of 8 bytes of codes (already shifted to their low nibbles).
+// The eight values of 8 bytes of codes' low nibbles, or of their high ones.
+template <bool HIGH>
 __device__ __forceinline__ uint4 eight_values(uint2 c, uint32_t s) {
   const uint32_t s2 = s * 0x10001u;
   auto two = [&](uint32_t w, uint32_t sel) {
     uint32_t u, r;
-    const uint32_t x = lop3_and_or(__byte_perm(w, w, sel), 0x000F000Fu, 0x64006400u);
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(u) : "r"(x), "r"(0xE408E408u));
+    const uint32_t b = __byte_perm(w, w, sel);
+    if (HIGH)  // (1024 + 16 u) / 16 - 72
+      asm("fma.rn.f16x2 %0, %1, %2, %3;"
+          : "=r"(u) : "r"(lop3_and_or(b, 0x00F000F0u, 0x64006400u)), "r"(0x2C002C00u), "r"(0xD480D480u));
+    else  // (1024 + u) - 1032
+      asm("add.rn.f16x2 %0, %1, %2;" : "=r"(u) : "r"(lop3_and_or(b, 0x000F000Fu, 0x64006400u)), "r"(0xE408E408u));
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(s2));
     return r;
   };
@@ -279,19 +288,19 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
   if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
   if (layer == 0 && blk == 0 && threadIdx.x == 0) status[i] = st;
   if (st != 0) return;
-  const int hd = kv.head_dim, node = kv.n_kv_heads * hd, nb = hd / 32;
+  const int node = kv.n_kv_heads * kv.head_dim;
   const int64_t dst0 = (int64_t)layer * layer_stride + (int64_t)i * nt * node;
-  const int l = threadIdx.x & 3, sh = l < 2 ? 0 : 4;
+  const int l = threadIdx.x & 1;
   constexpr int U = CQ_FLIGHT;
   each_piece(kv, r0, r1, [&](int which, int r, int step, int e, int64_t block, bool ok) {
-    const uint2* codes = reinterpret_cast<const uint2*>(which ? kv.v_qs : kv.k_qs) + 2 * block + (l & 1);
+    const uint2* codes = reinterpret_cast<const uint2*>(which ? kv.v_qs : kv.k_qs) + 2 * block + l;
     const uint16_t* scales = (which ? kv.v_scales : kv.k_scales) + block;
     uint2 c[U];
     uint32_t sc[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int rr = r + u * step;
-      const int64_t at = place.at[(rr < r1 ? rr : r) - r0] * nb;
+      const int64_t at = place.at[(rr < r1 ? rr : r) - r0];
       c[u] = __ldg(codes + 2 * at);
       sc[u] = __ldg(scales + at);
     }
@@ -300,8 +309,9 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
     for (int u = 0; u < U; u++) {
       const int rr = r + u * step;
       if (!ok || rr >= r1) break;
-      __stcs(reinterpret_cast<uint4*>(dst + (int64_t)rr * node),
-             eight_values(make_uint2(c[u].x >> sh, c[u].y >> sh), sc[u]));
+      uint4* p = reinterpret_cast<uint4*>(dst + (int64_t)rr * node);
+      __stcs(p, eight_values<false>(c[u], sc[u]));
+      __stcs(p + 2, eight_values<true>(c[u], sc[u]));
     }
   });
 }
