@@ -217,13 +217,14 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
     if (gw + i * warps < steps) load_step(i, now[i]);
     asm volatile("cp.async.commit_group;");
   }
-  KW::put_queries(qs, sums, tid, BA_THREADS, [&](int r) -> const __half* {
+  KW::put_queries(qs, sums, tid, BA_THREADS, a.scale_log2 < 0.0f, [&](int r) -> const __half* {
     return r < rows ? a.q + ((int64_t)s * a.nt + node) * a.q_stride + (h0 + r) * HD : nullptr;
   });
   __syncthreads();
   KW kw;
   kw.begin();
   const int gk = Q4 ? key_row(kw.g) : kw.g;
+  const float scale = fabsf(a.scale_log2);
   int stage = 0;
   for (int u = gw; u < steps; u += warps) {
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
@@ -236,9 +237,9 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
                    vss = kss + Sh::SCALES;
     float x[KT][NT][4];
     if constexpr (Q4)
-      kw.template scores_q4<KT>(ks, kss, qs, sums, a.scale_log2, x);
+      kw.template scores_q4<KT>(ks, kss, qs, sums, x);
     else
-      kw.scores_f16(ks, qs, a.scale_log2, x[0]);
+      kw.scores_f16(ks, qs, x[0]);
     const uint32_t there = __ballot_sync(0xffffffffu, now[0] != ~0u);
     if (there != 0xffffffffu) {
 #pragma unroll
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
 #pragma unroll
           for (int n = 0; n < NT; n++) x[i >> 1][n][2 * (i & 1)] = x[i >> 1][n][2 * (i & 1) + 1] = -INFINITY;
     }
-    kw.template weights<KT>(x);
+    kw.template weights<KT>(Q4 ? scale * KW::CODE_UNIT : scale, x);
 #pragma unroll
     for (int i = 0; i < KT; i++) {
       if constexpr (Q4)
@@ -263,13 +264,13 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
   __syncwarp();
   for (int p = my_path; p < path_steps && my_path < BA_WARPS; p += warps) {
     float x[1][NT][4];
-    kw.scores_f16(kn0 + f16_off<HD>(16 * p, 0), qs, a.scale_log2, x[0]);
+    kw.scores_f16(kn0 + f16_off<HD>(16 * p, 0), qs, x[0]);
 #pragma unroll
     for (int i = 0; i < 2; i++)
       if (16 * p + 8 * i + gk >= n_path)
 #pragma unroll
         for (int n = 0; n < NT; n++) x[0][n][2 * i] = x[0][n][2 * i + 1] = -INFINITY;
-    kw.template weights<1>(x);
+    kw.template weights<1>(scale, x);
     kw.values_f16(vn0 + f16_off<HD>(16 * p, 0), x[0]);
   }
   // ---- the warps' results, then the CTAs'

@@ -59,8 +59,8 @@ __device__ __forceinline__ uint4 kw_lds128(uint32_t at) {
 __device__ __forceinline__ void kw_sts64(uint32_t at, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(a), "r"(b) : "memory");
 }
-__device__ __forceinline__ void kw_sts64f(uint32_t at, float a, float b) {
-  kw_sts64(at, __float_as_uint(a), __float_as_uint(b));
+__device__ __forceinline__ void kw_sts128f(uint32_t at, float a, float b, float c, float d) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 // BYTES to shared memory; zeros if !valid (src is then any readable address).
 template <int BYTES>
@@ -83,6 +83,22 @@ __device__ __forceinline__ float kw_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// Two floats at a time: x y + z, x + y.
+__device__ __forceinline__ void kw_fma2(float& r0, float& r1, float x0, float x1, float y0, float y1, float z0, float z1) {
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r0), "=f"(r1) : "f"(x0), "f"(x1), "f"(y0), "f"(y1), "f"(z0), "f"(z1));
+}
+__device__ __forceinline__ void kw_mul2(float& r0, float& r1, float x0, float x1, float y0, float y1) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r0), "=f"(r1) : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+}
+__device__ __forceinline__ void kw_add2(float& r0, float& r1, float x0, float x1, float y0, float y1) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r0), "=f"(r1) : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
 }
 __device__ __forceinline__ uint32_t kw_transpose(uint32_t v) {  // 8 x 8 of 16 bits
   uint32_t r;
@@ -134,7 +150,7 @@ template <int HD, int NT, bool Q4>
 struct KeyWarp {
   static constexpr int STEPS = HD / 16, BLOCKS = HD / 32, MTILES = HD / 16;
   static constexpr int Q_BYTES = STEPS * NT * 32 * 8;     // query fragments of a CTA
-  static constexpr int SUM_BYTES = BLOCKS * NT * 4 * 8;   // and sums of their blocks (Q4)
+  static constexpr int SUM_BYTES = BLOCKS * NT * 4 * 16;  // and sums of their blocks (Q4), as accumulators begin
   int g, t;
   float o[MTILES][NT][4];  // (dimension g of a tile; rows 2t, 2t + 1), (dimension g + 8; ...)
   float mx[NT][2], sum[NT][2];  // of rows 2t, 2t + 1; sum: this lane's keys
@@ -161,9 +177,11 @@ struct KeyWarp {
   }
 
   // Query fragments: entry e of (step, n, lane), row(r): row r's data or null.
-  // Every thread of the CTA; `threads` of them.
+  // Every thread of the CTA; `threads` of them.  neg: the scores' scale is negative,
+  // which the queries take over, so that a row's largest score has its largest product.
   template <class F>
-  static __device__ __forceinline__ void put_queries(uint32_t qs, uint32_t sums, int tid, int threads, F&& row) {
+  static __device__ __forceinline__ void put_queries(uint32_t qs, uint32_t sums, int tid, int threads, bool neg, F&& row) {
+    const uint32_t sign = neg ? 0x80008000u : 0u;
     for (int e = tid; e < STEPS * NT * 32; e += threads) {
       const int lane = e & 31, n = e / 32 % NT, step = e / 32 / NT;
       const __half* p = row(8 * n + (lane >> 2));
@@ -178,7 +196,7 @@ struct KeyWarp {
           b1 = *reinterpret_cast<const uint32_t*>(p + 16 * step + 2 * (lane & 3) + 8);
         }
       }
-      kw_sts64(qs + e * 8, b0, b1);
+      kw_sts64(qs + e * 8, b0 ^ sign, b1 ^ sign);
     }
     if (Q4)
       for (int e = tid; e < BLOCKS * NT * 4; e += threads) {
@@ -195,18 +213,17 @@ struct KeyWarp {
                       kw_half(v.z, 1) + kw_half(v.w, 0) + kw_half(v.w, 1);
             }
         }
-        kw_sts64f(sums + e * 8, s[0] * -0x1p-21f, s[1] * -0x1p-21f);
+        const float f = neg ? 0x1p-21f : -0x1p-21f;
+        kw_sts128f(sums + e * 16, s[0] * f, s[1] * f, s[0] * f, s[1] * f);
       }
   }
 
-  // x = scale (K Q^T) of KT tiles of 16 rows of codes at `ks` (their scales at
-  // `ss`), scale in log2 units.  Lane (g, t): keys key_row(g) and 8 + of each tile, rows
-  // 2t, 2t + 1 of each n.
+  // x = 2^-24 K Q^T of KT tiles of 16 rows of codes at `ks` (their scales at `ss`).
+  // Lane (g, t): keys key_row(g) and 8 + of each tile, rows 2t, 2t + 1 of each n.
   template <int KT>
-  __device__ __forceinline__ void scores_q4(uint32_t ks, uint32_t ss, uint32_t qs, uint32_t sums, float scale,
+  __device__ __forceinline__ void scores_q4(uint32_t ks, uint32_t ss, uint32_t qs, uint32_t sums,
                                             float (&x)[KT][NT][4]) const {
     const int lane = g * 4 + t, kr = key_row(g);
-    const float f = scale * 0x1p24f;
     uint32_t sc[KT][2][BLOCKS / 2];
 #pragma unroll
     for (int i = 0; i < KT; i++)
@@ -233,15 +250,6 @@ struct KeyWarp {
         }
       float acc[KT][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; n++) {
-        const uint2 c = kw_lds64(sums + ((b * NT + n) * 4 + t) * 8);
-#pragma unroll
-        for (int i = 0; i < KT; i++) {
-          acc[i][n][0] = acc[i][n][2] = __uint_as_float(c.x);
-          acc[i][n][1] = acc[i][n][3] = __uint_as_float(c.y);
-        }
-      }
-#pragma unroll
       for (int half = 0; half < 2; half++) {
         uint32_t a[KT][4];
 #pragma unroll
@@ -255,32 +263,40 @@ struct KeyWarp {
 #pragma unroll
         for (int n = 0; n < NT; n++) {
           const uint2 q = kw_lds64(qs + (((2 * b + half) * NT + n) * 32 + lane) * 8);
+          if (half == 0) {
+            const uint4 cc = kw_lds128(sums + ((b * NT + n) * 4 + t) * 16);
+            const float c[4] = {__uint_as_float(cc.x), __uint_as_float(cc.y), __uint_as_float(cc.z), __uint_as_float(cc.w)};
 #pragma unroll
-          for (int i = 0; i < KT; i++) mma_16816(acc[i][n], a[i], q.x, q.y);
+            for (int i = 0; i < KT; i++) mma_16816_c(acc[i][n], a[i], q.x, q.y, c);
+          } else {
+#pragma unroll
+            for (int i = 0; i < KT; i++) mma_16816(acc[i][n], a[i], q.x, q.y);
+          }
         }
       }
 #pragma unroll
       for (int i = 0; i < KT; i++)
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          const float s = kw_half(sc[i][h][b >> 1], b & 1) * f;
+          const float s = kw_half(sc[i][h][b >> 1], b & 1);
 #pragma unroll
-          for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int e = 2 * h; e < 2 * h + 2; e++)
-              x[i][n][e] = b == 0 ? acc[i][n][e] * s : fmaf(acc[i][n][e], s, x[i][n][e]);
+          for (int n = 0; n < NT; n++) {
+            float* y = &x[i][n][2 * h];
+            const float* z = &acc[i][n][2 * h];
+            if (b == 0)
+              kw_mul2(y[0], y[1], z[0], z[1], s, s);
+            else
+              kw_fma2(y[0], y[1], z[0], z[1], s, s, y[0], y[1]);
+          }
         }
     }
   }
+  static constexpr float CODE_UNIT = 0x1p24f;  // of these scores
 
-  // The same of one tile of 16 fp16 rows.  Keys in the order of the rows (not
-  // Q4) or in the codes' (Q4).
-  __device__ __forceinline__ void scores_f16(uint32_t ks, uint32_t qs, float scale, float (&x)[NT][4]) const {
+  // K Q^T of one tile of 16 fp16 rows.  Keys in the order of the rows (not Q4) or
+  // in the codes' (Q4).
+  __device__ __forceinline__ void scores_f16(uint32_t ks, uint32_t qs, float (&x)[NT][4]) const {
     const int lane = g * 4 + t;
-#pragma unroll
-    for (int n = 0; n < NT; n++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) x[n][e] = 0.0f;
 #pragma unroll
     for (int step = 0; step < STEPS; step++) {
       uint32_t a[4];
@@ -300,18 +316,18 @@ struct KeyWarp {
 #pragma unroll
       for (int n = 0; n < NT; n++) {
         const uint2 q = kw_lds64(qs + ((step * NT + n) * 32 + lane) * 8);
-        mma_16816(x[n], a, q.x, q.y);
+        if (step == 0)
+          mma_16816_zero(x[n], a, q.x, q.y);
+        else
+          mma_16816(x[n], a, q.x, q.y);
       }
     }
-#pragma unroll
-    for (int n = 0; n < NT; n++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) x[n][e] *= scale;
   }
 
-  // Scores to weights (times 2^KW_BIAS); the running maximum and sum.
+  // Scores x, f > 0 times which are in log2 units, to weights (times 2^KW_BIAS); the
+  // running maximum and sum.
   template <int KT>
-  __device__ __forceinline__ void weights(float (&x)[KT][NT][4]) {
+  __device__ __forceinline__ void weights(float f, float (&x)[KT][NT][4]) {
     bool grow = false;
     float top[NT][2];
 #pragma unroll
@@ -321,6 +337,7 @@ struct KeyWarp {
         top[n][h] = fmaxf(x[0][n][h], x[0][n][2 + h]);
 #pragma unroll
         for (int i = 1; i < KT; i++) top[n][h] = fmaxf(top[n][h], fmaxf(x[i][n][h], x[i][n][2 + h]));
+        top[n][h] *= f;
         grow |= top[n][h] > mx[n][h] + KW_SLACK;  // (-infinity + 3 at first)
       }
     if (__any_sync(0xffffffffu, grow)) {
@@ -343,17 +360,20 @@ struct KeyWarp {
       }
     }
 #pragma unroll
-    for (int n = 0; n < NT; n++)
+    for (int n = 0; n < NT; n++) {
+      const float s0 = KW_BIAS - (mx[n][0] == -INFINITY ? 0.0f : mx[n][0]);
+      const float s1 = KW_BIAS - (mx[n][1] == -INFINITY ? 0.0f : mx[n][1]);
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const float shift = KW_BIAS - (mx[n][h] == -INFINITY ? 0.0f : mx[n][h]);
+      for (int i = 0; i < KT; i++)
 #pragma unroll
-        for (int i = 0; i < KT; i++) {
-          x[i][n][h] = kw_exp2(x[i][n][h] + shift);
-          x[i][n][2 + h] = kw_exp2(x[i][n][2 + h] + shift);
-          sum[n][h] += x[i][n][h] + x[i][n][2 + h];
+        for (int h = 0; h < 2; h++) {
+          float* y = &x[i][n][2 * h];
+          kw_fma2(y[0], y[1], y[0], y[1], f, f, s0, s1);
+          y[0] = kw_exp2(y[0]);
+          y[1] = kw_exp2(y[1]);
+          kw_add2(sum[n][0], sum[n][1], sum[n][0], sum[n][1], y[0], y[1]);
         }
-      }
+    }
   }
 
   // A tile's weights as fragments: pairs of fp16 numbers hi + lo.
@@ -364,8 +384,10 @@ struct KeyWarp {
       for (int h = 0; h < 2; h++) {
         const float a = p[n][2 * h], b = p[n][2 * h + 1];
         const float ca = __uint_as_float(__float_as_uint(a) & KW_CUT), cb = __uint_as_float(__float_as_uint(b) & KW_CUT);
+        float ra, rb;
+        kw_fma2(ra, rb, ca, cb, -KW_REST, -KW_REST, a, b);
         hi[n][h] = kw_transpose(kw_pack(ca, cb));
-        lo[n][h] = kw_transpose(kw_pack(fmaf(ca, -KW_REST, a), fmaf(cb, -KW_REST, b)));
+        lo[n][h] = kw_transpose(kw_pack(ra, rb));
       }
   }
   __device__ __forceinline__ void add(int m, const uint32_t (&a)[4], const uint32_t (&hi)[NT][2],

@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
   const uint32_t sm0 = kw_smem(smem), ring = sm0 + warp * Sh::RING;
   const uint32_t kn0 = sm0 + Sh::TREE_OFF, vn0 = kn0 + Sh::NODES * HD * 2;
   const uint32_t qs = sm0 + Sh::Q_OFF, sums = sm0 + Sh::SUM_OFF;
+  const float scale = fabsf(a.scale_log2);
   KW kw;
   while (left > 0) {
     if (off >= q.work()) {  // the next sequence with work
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
       if (t0 + i < t1) load_tile(t0 + i, ahead[i]);
       asm volatile("cp.async.commit_group;");
     }
-    KW::put_queries(qs, sums, tid, QA_THREADS, [&](int r) -> const __half* {
+    KW::put_queries(qs, sums, tid, QA_THREADS, a.scale_log2 < 0.0f, [&](int r) -> const __half* {
       const int m = row0 + r;
       if (m >= M) return nullptr;
       const int node = node_of(a, m);
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
         if (16 * warp >= q.m) continue;
         const uint32_t ks = kn0 + f16_off<HD>(16 * warp, 0), vs = vn0 + f16_off<HD>(16 * warp, 0);
         float x[1][NT][4];
-        kw.scores_f16(ks, qs, a.scale_log2, x[0]);
+        kw.scores_f16(ks, qs, x[0]);
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
             for (int i = 0; i < 2; i++)
               if (!(bits >> i & 1)) x[0][n][2 * i + h] = -INFINITY;
           }
-        kw.template weights<1>(x);
+        kw.template weights<1>(scale, x);
         bool odd = false;
 #pragma unroll
         for (int e = lane; e < 16 * UNITS; e += 32) {
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
       for (int i0 = 0; i0 < WARP_KEYS / 16; i0 += KT) {
         float x[KT][NT][4];
         const uint32_t kt = i0 * 16;
-        kw.template scores_q4<KT>(ks + kt * (HD / 2), kss + kt * (HD / 16), qs, sums, a.scale_log2, x);
+        kw.template scores_q4<KT>(ks + kt * (HD / 2), kss + kt * (HD / 16), qs, sums, x);
         if (masked) {
 #pragma unroll
           for (int n = 0; n < NT; n++)
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
                 if (!(bits >> i & 1)) x[i >> 1][n][2 * (i & 1) + h] = -INFINITY;
             }
         }
-        kw.template weights<KT>(x);
+        kw.template weights<KT>(scale * KW::CODE_UNIT, x);
 #pragma unroll
         for (int i = 0; i < KT; i++) {
           const uint32_t vt = vs + (kt + 16 * i) * (HD / 2), st = vss + (kt + 16 * i) * (HD / 16);
