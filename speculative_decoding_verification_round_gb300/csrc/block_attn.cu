@@ -179,24 +179,20 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
   };
   auto load_step = [&](int stage, uint32_t at) {
     const uint32_t to = ring + stage * Sh::STAGE;
-    constexpr int CH = Sh::ROW / 16, PER = 32 / CH;
-    const int c = lane % CH;
+    if constexpr (Q4) {
+      load_codes<HD>(to, at, a.shift >= 5, a.k, a.v, a.k_scales, a.v_scales);
+    } else {
+      constexpr int CH = Sh::ROW / 16, PER = 32 / CH;
+      const int c = lane % CH;
 #pragma unroll
-    for (int i = 0; i < KEYS / PER; i++) {
-      const int r = i * PER + lane / CH;
-      const uint32_t x = __shfl_sync(0xffffffffu, at, r);
-      const bool ok = x != ~0u;
-      const uint64_t from = (uint64_t)(ok ? x : 0u) * Sh::ROW + c * 16;
-      const uint32_t d = to + (Q4 ? r * Sh::ROW + ((c ^ q4_swz<HD>(r)) << 4) : f16_off<HD>(r, c));
-      kw_copy<16>(d, a.k + from, ok);
-      kw_copy<16>(d + KEYS * Sh::ROW, a.v + from, ok);
-    }
-    if (Q4) {
-      const bool ok = at != ~0u;
-      const uint64_t from = (uint64_t)(ok ? at : 0u) * (HD / 32);
-      const uint32_t d = to + 2 * KEYS * Sh::ROW + lane * (HD / 16);
-      kw_copy<HD / 16>(d, a.k_scales + from, ok);
-      kw_copy<HD / 16>(d + Sh::SCALES, a.v_scales + from, ok);
+      for (int i = 0; i < KEYS / PER; i++) {
+        const int r = i * PER + lane / CH;
+        const uint32_t x = __shfl_sync(0xffffffffu, at, r);
+        const bool ok = x != ~0u;
+        const uint64_t from = (uint64_t)(ok ? x : 0u) * Sh::ROW + c * 16;
+        kw_copy<16>(to + f16_off<HD>(r, c), a.k + from, ok);
+        kw_copy<16>(to + KEYS * Sh::ROW + f16_off<HD>(r, c), a.v + from, ok);
+      }
     }
   };
   // the path's rows first: they are few, and their step comes last

@@ -134,7 +134,8 @@ __device__ __forceinline__ bool odd_pair(uint32_t v) { return odd_half(v) || odd
 // front, so that the four of one load lie in different banks.
 __device__ __forceinline__ int key_row(int k) { return (k >> 1 & 3) | (k & 1) << 2; }
 
-// A row of codes: HD / 2 bytes, 16-byte chunk c of row r at c ^ q4_swz(r).
+// A row of codes: HD / 2 bytes, 16-byte chunk c of row r at c ^ q4_swz(r).  (Rows 8 on have
+// the same one, rows 4 on its lowest bit turned.)
 template <int HD>
 __device__ __forceinline__ int q4_swz(int r) {
   return HD == 128 ? (r & 2) | (r >> 2 & 1) : r >> 2 & 1;
@@ -224,12 +225,13 @@ struct KeyWarp {
   __device__ __forceinline__ void scores_q4(uint32_t ks, uint32_t ss, uint32_t qs, uint32_t sums,
                                             float (&x)[KT][NT][4]) const {
     const int lane = g * 4 + t, kr = key_row(g);
+    const uint32_t k0 = ks + kr * (HD / 2) + 4 * t + (q4_swz<HD>(kr) << 4), s0 = ss + kr * (HD / 16);
     uint32_t sc[KT][2][BLOCKS / 2];
 #pragma unroll
     for (int i = 0; i < KT; i++)
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const uint32_t at = ss + (16 * i + 8 * h + kr) * (HD / 16);
+        const uint32_t at = s0 + (16 * i + 8 * h) * (HD / 16);
         if (BLOCKS == 4) {
           const uint2 v = kw_lds64(at);
           sc[i][h][0] = v.x;
@@ -241,13 +243,11 @@ struct KeyWarp {
 #pragma unroll
     for (int b = 0; b < BLOCKS; b++) {
       uint32_t w[KT][2];
+      const uint32_t kb = k0 ^ (b << 4);
 #pragma unroll
       for (int i = 0; i < KT; i++)
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int r = 16 * i + 8 * h + kr;
-          w[i][h] = kw_lds32(ks + r * (HD / 2) + ((b ^ q4_swz<HD>(r)) << 4) + 4 * t);
-        }
+        for (int h = 0; h < 2; h++) w[i][h] = kw_lds32(kb + (16 * i + 8 * h) * (HD / 2));
       float acc[KT][NT][4];
 #pragma unroll
       for (int half = 0; half < 2; half++) {
@@ -405,18 +405,20 @@ struct KeyWarp {
     uint32_t hi[NT][2], lo[NT][2];
     split(p, hi, lo);
     uint32_t w[4][WORDS], s[4];  // keys t, t + 4, t + 8, t + 12
+    const int block = HD == 128 ? g >> 1 : g >> 2;
+    const uint32_t v0 = vs + t * (HD / 2) + ((block ^ q4_swz<HD>(t)) << 4) + (HD == 128 ? 8 * (g & 1) : 4 * (g & 3)),
+                   s00 = ss + t * (HD / 16) + 2 * block;
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-      const int r = t + 4 * k;
+      const uint32_t at = (k & 1 ? v0 ^ 16u : v0) + 4 * k * (HD / 2);
       if (HD == 128) {
-        const uint2 v = kw_lds64(vs + r * (HD / 2) + (((g >> 1) ^ q4_swz<HD>(r)) << 4) + 8 * (g & 1));
+        const uint2 v = kw_lds64(at);
         w[k][0] = v.x;
         w[k][WORDS - 1] = v.y;
-        s[k] = kw_lds16(ss + r * (HD / 16) + 2 * (g >> 1));
       } else {
-        w[k][0] = kw_lds32(vs + r * (HD / 2) + (((g >> 2) ^ q4_swz<HD>(r)) << 4) + 4 * (g & 3));
-        s[k] = kw_lds16(ss + r * (HD / 16) + 2 * (g >> 2));
+        w[k][0] = kw_lds32(at);
       }
+      s[k] = kw_lds16(s00 + 4 * k * (HD / 16));
     }
     const uint32_t s0 = s[0] | s[1] << 16, s1 = s[2] | s[3] << 16;
 #pragma unroll
@@ -530,5 +532,46 @@ struct KeyWarp {
       }
   }
 };
+
+// 32 rows of codes and scales of K and V on their way to a stage (K's codes, V's, K's
+// scales, V's) of a warp's ring: lane l has the cache's row `at` of row l, ~0 for zeros.  With
+// `runs` the rows of a page come in whole runs of 32: where none is missing they are
+// neighbours then.
+template <int HD>
+__device__ __forceinline__ void load_codes(uint32_t to, uint32_t at, bool runs, const uint8_t* __restrict__ k_qs,
+                                           const uint8_t* __restrict__ v_qs, const __half* __restrict__ k_scales,
+                                           const __half* __restrict__ v_scales) {
+  constexpr int CH = HD / 32, PER = 32 / CH, CODES = 32 * HD / 2, SCALES = 32 * HD / 16;  // chunks of a row, rows a pass
+  const int lane = threadIdx.x & 31, c = lane % CH, r = lane / CH;
+  const uint32_t ss = to + 2 * CODES + lane * (HD / 16);
+  if (runs && __all_sync(0xffffffffu, at != ~0u)) {
+    const uint32_t x0 = __shfl_sync(0xffffffffu, at, 0);
+    const uint8_t* k = k_qs + (uint64_t)x0 * (HD / 2) + lane * 16;
+    const uint8_t* v = v_qs + (uint64_t)x0 * (HD / 2) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      // (PER is 8 or 16 rows: the swizzle repeats)
+      const uint32_t d = to + r * (HD / 2) + ((c ^ q4_swz<HD>(r)) << 4) + i * PER * (HD / 2);
+      kw_copy<16>(d, k + i * PER * (HD / 2), true);
+      kw_copy<16>(d + CODES, v + i * PER * (HD / 2), true);
+    }
+    kw_copy<HD / 16>(ss, k_scales + (uint64_t)x0 * CH + lane * CH, true);
+    kw_copy<HD / 16>(ss + SCALES, v_scales + (uint64_t)x0 * CH + lane * CH, true);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < CH; i++) {
+    const uint32_t x = __shfl_sync(0xffffffffu, at, i * PER + r);
+    const bool ok = x != ~0u;
+    const uint64_t from = (uint64_t)(ok ? x : 0u) * (HD / 2) + c * 16;
+    const uint32_t d = to + r * (HD / 2) + ((c ^ q4_swz<HD>(r)) << 4) + i * PER * (HD / 2);
+    kw_copy<16>(d, k_qs + from, ok);
+    kw_copy<16>(d + CODES, v_qs + from, ok);
+  }
+  const bool ok = at != ~0u;
+  const uint64_t from = (uint64_t)(ok ? at : 0u) * CH;
+  kw_copy<HD / 16>(ss, k_scales + from, ok);
+  kw_copy<HD / 16>(ss + SCALES, v_scales + from, ok);
+}
 
 }  // namespace

@@ -27,7 +27,7 @@ constexpr int QA_SHIFT = 7, QA_KEYS = 1 << QA_SHIFT, QA_THREADS = 128, QA_WARPS 
 template <int HD, int NT>
 struct QShape {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = 2;
   static constexpr int KT = NT == 4 ? 1 : 2;  // tiles of 16 keys a step
   static constexpr int CODES = WARP_KEYS * HD / 2, SCALES = WARP_KEYS * HD / 16;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // bytes: K's and V's codes, K's and V's scales
@@ -39,7 +39,7 @@ struct QShape {
   static constexpr int Q_OFF = TREE_OFF + 2 * NODES * HD * 2;
   static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, true>::Q_BYTES;
   static constexpr size_t SMEM = SUM_OFF + KeyWarp<HD, NT, true>::SUM_BYTES;
-  static constexpr int RESIDENT = NT == 4 ? 2 : HD == 128 ? 3 : 5;
+  static constexpr int RESIDENT = NT == 4 ? 2 : HD == 64 ? 6 : NT == 2 ? 3 : 4;
 };
 
 template <int HD, int NT>
@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
   const uint32_t kn0 = sm0 + Sh::TREE_OFF, vn0 = kn0 + Sh::NODES * HD * 2;
   const uint32_t qs = sm0 + Sh::Q_OFF, sums = sm0 + Sh::SUM_OFF;
   const float scale = fabsf(a.scale_log2);
+  const bool runs = a.page_size % WARP_KEYS == 0;
   KW kw;
   while (left > 0) {
     if (off >= q.work()) {  // the next sequence with work
@@ -104,23 +105,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
     };
     auto load_tile = [&](int t, uint32_t at) {
       if (t != last) {
-        const uint32_t st = ring + (t % STAGES) * Sh::STAGE, ss = st + 2 * Sh::CODES;
-        constexpr int CH = HD / 32, PER = 32 / CH;  // 16-byte chunks of a row, rows a pass
-        const int c = lane % CH;
-#pragma unroll
-        for (int i = 0; i < CH; i++) {
-          const int r = i * PER + lane / CH;
-          const uint32_t x = __shfl_sync(0xffffffffu, at, r);
-          const bool ok = x != ~0u;
-          const uint64_t from = (uint64_t)(ok ? x : 0u) * (HD / 2) + c * 16;
-          const uint32_t to = st + r * (HD / 2) + ((c ^ q4_swz<HD>(r)) << 4);
-          kw_copy<16>(to, a.k_qs + from, ok);
-          kw_copy<16>(to + Sh::CODES, a.v_qs + from, ok);
-        }
-        const bool ok = at != ~0u;
-        const uint64_t from = (uint64_t)(ok ? at : 0u) * (HD / 32);
-        kw_copy<HD / 16>(ss + lane * (HD / 16), a.k_scales + from, ok);
-        kw_copy<HD / 16>(ss + Sh::SCALES + lane * (HD / 16), a.v_scales + from, ok);
+        load_codes<HD>(ring + (t % STAGES) * Sh::STAGE, at, runs, a.k_qs, a.v_qs, a.k_scales, a.v_scales);
       } else if (16 * warp < q.m) {  // this warp's sixteen nodes
         const int64_t from = (int64_t)s * a.nt * a.kv_stride + kvh * HD;
 #pragma unroll
@@ -319,8 +304,9 @@ bool q4_on_tc(int rows) { return rows >= 64; }
 int q4_resident(int hd, int rows) {
   return q4_on_tc(rows) ? 1
          : rows == 32   ? QShape<128, 4>::RESIDENT
-         : hd == 128    ? QShape<128, 1>::RESIDENT
-                        : QShape<64, 1>::RESIDENT;
+         : hd == 64     ? QShape<64, 1>::RESIDENT
+         : rows == 16   ? QShape<128, 2>::RESIDENT
+                        : QShape<128, 1>::RESIDENT;
 }
 // The CTAs with tiles: what is resident, but for the one that plans.
 int q4_ctas(int hd, int rows) { return std::max(1, q4_resident(hd, rows) * device_sms() - 1); }
