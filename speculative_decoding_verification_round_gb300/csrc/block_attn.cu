@@ -19,7 +19,7 @@
 
 namespace {
 
-constexpr int BA_THREADS = 128, BA_WARPS = 4;
+constexpr int BA_THREADS = KJ_THREADS, BA_WARPS = KJ_WARPS;
 
 struct BlockArgs {
   const uint8_t* k;  // the layer's rows of fp16, or codes
@@ -53,35 +53,14 @@ struct BShape {
   static constexpr int SCALES = Q4 ? KEYS * (HD / 16) : 0;
   static constexpr int STAGE = 2 * (KEYS * ROW + SCALES);
   static constexpr int RING = STAGES * STAGE;  // of a warp
-  static constexpr int XROW = HD + 4;
-  static constexpr int EXCHANGE = BA_WARPS * ROWS * (XROW * 4 + 8);
-  static constexpr int PART_OFF = ((BA_WARPS * RING > EXCHANGE ? BA_WARPS * RING : EXCHANGE) + 127) / 128 * 128;
-  static constexpr int PART = ROWS * (XROW * 4 + 8);  // the CTA's result
-  static constexpr int Q_OFF = (PART_OFF + PART + 127) / 128 * 128;
+  using Join = JoinShape<HD, ROWS>;
+  static constexpr int PART_OFF = ((BA_WARPS * RING > Join::EXCHANGE ? BA_WARPS * RING : Join::EXCHANGE) + 127) / 128 * 128;
+  static constexpr int Q_OFF = (PART_OFF + Join::PART + 127) / 128 * 128;
   static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, Q4>::Q_BYTES;
   static constexpr int PATH_OFF = (SUM_OFF + (Q4 ? KeyWarp<HD, NT, Q4>::SUM_BYTES : 0) + 127) / 128 * 128;
   // behind it path_rows rows of k_new and of v_new, then the list (8 bytes a block)
   static size_t smem(int path_rows, int keep) { return PATH_OFF + (size_t)path_rows * HD * 4 + (size_t)keep * 8; }
 };
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_at(uint32_t at, uint32_t rank) {  // the address in another CTA
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 cluster_ld4(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ float2 cluster_ld2(uint32_t at) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
-  return v;
-}
 
 template <int HD, int NT, bool Q4>
 __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs a) {
@@ -269,88 +248,16 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
     kw.template weights<1>(scale, x);
     kw.values_f16(vn0 + f16_off<HD>(16 * p, 0), x[0]);
   }
-  // ---- the warps' results, then the CTAs'
   __syncthreads();  // the rings have been read
-  float* x = reinterpret_cast<float*>(smem);
-  float2* ml = reinterpret_cast<float2*>(x + (size_t)BA_WARPS * ROWS * Sh::XROW);
-  float* part = reinterpret_cast<float*>(smem + Sh::PART_OFF);
-  float2* part_ml = reinterpret_cast<float2*>(part + ROWS * Sh::XROW);
-  kw.template put<Sh::XROW>(x + (size_t)warp * ROWS * Sh::XROW, ml + warp * ROWS);
-  __syncthreads();
-  auto finish = [&](int r, int u, const float (&acc)[8], float l) {
-    const float inv = 1.0f / l;
-    *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + h0 + r) * HD + u * 8) =
-        make_uint4(kw_pack(acc[0] * inv, acc[1] * inv), kw_pack(acc[2] * inv, acc[3] * inv),
-                   kw_pack(acc[4] * inv, acc[5] * inv), kw_pack(acc[6] * inv, acc[7] * inv));
-  };
-  for (int e = tid; e < rows * UNITS; e += BA_THREADS) {
-    const int r = e / UNITS, u = e % UNITS;
-    float m2 = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < BA_WARPS; w++) m2 = fmaxf(m2, ml[w * ROWS + r].x);
-    const float ref = m2 == -INFINITY ? 0.0f : m2;
-    float acc[8] = {}, l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < BA_WARPS; w++) {
-      const float2 y = ml[w * ROWS + r];
-      const float f = kw_exp2(y.x - ref);
-      l = fmaf(y.y, f, l);
-      const float* src = x + ((size_t)w * ROWS + r) * Sh::XROW + u * 8;
-#pragma unroll
-      for (int d = 0; d < 8; d++) acc[d] = fmaf(src[d], f, acc[d]);
-    }
-    if (a.ranks == 1) {
-      finish(r, u, acc, l);
-    } else {
-#pragma unroll
-      for (int d = 0; d < 8; d++) part[r * Sh::XROW + u * 8 + d] = acc[d];
-      if (u == 0) part_ml[r] = make_float2(m2, l);
-    }
-  }
-  if (a.ranks == 1) return;
-  cluster_sync();
-  // a lane a rank: lanes [0, ranks) of a group have one item (row, 8 dimensions)
-  const int R = a.ranks, j = tid & (R - 1);
-  for (int e0 = 0; e0 < rows * UNITS; e0 += BA_THREADS) {  // items of all ranks together: BA_THREADS a turn
-    const int e = e0 + rank * (BA_THREADS / R) + tid / R;
-    const bool ok = e < rows * UNITS;
-    const int r = ok ? e / UNITS : 0, u = ok ? e % UNITS : 0;
-    const uint32_t from = cluster_at(kw_smem(part + r * Sh::XROW + u * 8), j);
-    const float2 y = cluster_ld2(cluster_at(kw_smem(part_ml + r), j));
-    const float4 v0 = cluster_ld4(from), v1 = cluster_ld4(from + 16);
-    float acc[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    float m2 = y.x;
-    for (int off = 1; off < R; off <<= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, off));
-    const float f = kw_exp2(y.x - (m2 == -INFINITY ? 0.0f : m2));
-    float l = y.y * f;
-#pragma unroll
-    for (int d = 0; d < 8; d++) acc[d] *= f;
-    for (int off = 1; off < R; off <<= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, off);
-#pragma unroll
-      for (int d = 0; d < 8; d++) acc[d] += __shfl_xor_sync(0xffffffffu, acc[d], off);
-    }
-    if (ok && j == 0) finish(r, u, acc, l);
-  }
-  cluster_sync();  // no CTA ends while another one reads its result
+  __half* out = a.out + (((int64_t)s * a.nt + node) * a.nq + h0) * HD;
+  join_unit(kw, smem, Sh::PART_OFF, rank, a.ranks, rows,
+            [&](int r, int u, const float (&acc)[8], float l) { put_row(out + r * HD + u * 8, acc, l); });
 }
 
 template <int HD, int NT, bool Q4>
 cudaError_t launch_block(const BlockArgs& a, size_t units, cudaStream_t st) {
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = programmatic_launch() ? 1 : 0;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = a.ranks;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  cfg.gridDim = dim3((unsigned)(units * a.ranks));
-  cfg.blockDim = dim3(BA_THREADS);
-  cfg.dynamicSmemBytes = BShape<HD, NT, Q4>::smem(a.path_rows, a.keep);
-  return cudaLaunchKernelEx(&cfg, block_attn_kernel<HD, NT, Q4>, a);
+  return launch_clusters(block_attn_kernel<HD, NT, Q4>, a, units * a.ranks, a.ranks,
+                         BShape<HD, NT, Q4>::smem(a.path_rows, a.keep), st);
 }
 
 template <int HD, int NT, bool Q4>

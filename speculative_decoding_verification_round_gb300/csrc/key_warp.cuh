@@ -574,4 +574,135 @@ __device__ __forceinline__ void load_codes(uint32_t to, uint32_t at, bool runs, 
   kw_copy<HD / 16>(ss + SCALES, v_scales + from, ok);
 }
 
+// ---------------------------------------------------------------------------
+// the warps' results of a unit, of one CTA or of a cluster's, joined
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_at(uint32_t at, uint32_t rank) {  // the address in another CTA
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+
+constexpr int KJ_THREADS = 128, KJ_WARPS = 4;
+
+// The shared memory that a join needs: the warps' results over whatever has been read
+// (from 0 on), the CTA's behind it.
+template <int HD, int ROWS>
+struct JoinShape {
+  static constexpr int XROW = HD + 4;  // floats of a row (padded)
+  static constexpr int PART = ROWS * (XROW * 4 + 8), EXCHANGE = KJ_WARPS * PART;
+};
+
+// finish(row, unit of 8 dimensions, unnormalised result, sum) for each of `rows` rows of a unit
+// which `ranks` (1 to 16, a power of two) CTAs of a cluster have, this one being `rank`: in
+// the order of the warps, and of the CTAs by halves.  All threads of all of them; what the
+// kernel had in the first EXCHANGE bytes of smem has been read.
+template <int HD, int NT, bool Q4, class F>
+__device__ __forceinline__ void join_unit(const KeyWarp<HD, NT, Q4>& kw, unsigned char* smem, int part_off, int rank,
+                                          int ranks, int rows, F&& finish) {
+  constexpr int ROWS = 8 * NT, UNITS = HD / 8, XROW = JoinShape<HD, ROWS>::XROW;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  float* x = reinterpret_cast<float*>(smem);
+  float2* ml = reinterpret_cast<float2*>(x + (size_t)KJ_WARPS * ROWS * XROW);
+  float* part = reinterpret_cast<float*>(smem + part_off);
+  float2* part_ml = reinterpret_cast<float2*>(part + ROWS * XROW);
+  kw.template put<XROW>(x + (size_t)warp * ROWS * XROW, ml + warp * ROWS);
+  __syncthreads();
+  for (int e = tid; e < rows * UNITS; e += KJ_THREADS) {
+    const int r = e / UNITS, u = e % UNITS;
+    float m2 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < KJ_WARPS; w++) m2 = fmaxf(m2, ml[w * ROWS + r].x);
+    const float ref = m2 == -INFINITY ? 0.0f : m2;
+    float acc[8] = {}, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < KJ_WARPS; w++) {
+      const float2 y = ml[w * ROWS + r];
+      const float f = kw_exp2(y.x - ref);
+      l = fmaf(y.y, f, l);
+      const float4* src = reinterpret_cast<const float4*>(x + ((size_t)w * ROWS + r) * XROW + u * 8);
+      const float4 a = src[0], b = src[1];
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int d = 0; d < 8; d++) acc[d] = fmaf(v[d], f, acc[d]);
+    }
+    if (ranks == 1) {
+      finish(r, u, acc, l);
+    } else {
+      float4* dst = reinterpret_cast<float4*>(part + r * XROW + u * 8);
+      dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (u == 0) part_ml[r] = make_float2(m2, l);
+    }
+  }
+  if (ranks == 1) return;
+  cluster_sync();
+  // a lane a rank: lanes [0, ranks) of a group have one item (row, 8 dimensions)
+  const int j = tid & (ranks - 1);
+  for (int e0 = 0; e0 < rows * UNITS; e0 += KJ_THREADS) {  // items of all ranks together: KJ_THREADS a turn
+    const int e = e0 + rank * (KJ_THREADS / ranks) + tid / ranks;
+    const bool ok = e < rows * UNITS;
+    const int r = ok ? e / UNITS : 0, u = ok ? e % UNITS : 0;
+    const uint32_t from = cluster_at(kw_smem(part + r * XROW + u * 8), j);
+    const float2 y = cluster_ld2(cluster_at(kw_smem(part_ml + r), j));
+    const float4 v0 = cluster_ld4(from), v1 = cluster_ld4(from + 16);
+    float acc[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    float m2 = y.x;
+    for (int off = 1; off < ranks; off <<= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, off));
+    const float f = kw_exp2(y.x - (m2 == -INFINITY ? 0.0f : m2));
+    float l = y.y * f;
+#pragma unroll
+    for (int d = 0; d < 8; d++) acc[d] *= f;
+    for (int off = 1; off < ranks; off <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+      for (int d = 0; d < 8; d++) acc[d] += __shfl_xor_sync(0xffffffffu, acc[d], off);
+    }
+    if (ok && j == 0) finish(r, u, acc, l);
+  }
+  cluster_sync();  // no CTA ends while another one reads its result
+}
+
+// Eight dimensions of a finished row.
+__device__ __forceinline__ void put_row(__half* to, const float (&acc)[8], float l) {
+  const float inv = 1.0f / l;
+  *reinterpret_cast<uint4*>(to) =
+      make_uint4(kw_pack(acc[0] * inv, acc[1] * inv), kw_pack(acc[2] * inv, acc[3] * inv),
+                 kw_pack(acc[4] * inv, acc[5] * inv), kw_pack(acc[6] * inv, acc[7] * inv));
+}
+
+// A launch in clusters of `ranks` CTAs (of KJ_THREADS threads), as a programmatic
+// dependent.
+template <class A>
+inline cudaError_t launch_clusters(void (*kernel)(const A), const A& a, size_t ctas, int ranks, size_t smem,
+                                   cudaStream_t st) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = programmatic_launch() ? 1 : 0;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ranks;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(KJ_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 }  // namespace

@@ -28,25 +28,159 @@ template <int HD, int NT>
 struct QShape {
   static constexpr int ROWS = 8 * NT;
   static constexpr int STAGES = 2;
-  static constexpr int KT = NT == 4 ? 1 : 2;  // tiles of 16 keys a step
   static constexpr int CODES = WARP_KEYS * HD / 2, SCALES = WARP_KEYS * HD / 16;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // bytes: K's and V's codes, K's and V's scales
   static constexpr int RING = STAGES * STAGE;         // of a warp
-  static constexpr int XROW = HD + 4;                 // floats of an exchange row (padded)
-  static constexpr int EXCHANGE = QA_WARPS * ROWS * (XROW * 4 + 8);
+  using Join = JoinShape<HD, ROWS>;
+  static constexpr int XROW = Join::XROW;
   static constexpr int NODES = NT == 4 ? 32 : 16;     // rows of the tree's own tile (no more nodes than rows)
-  static constexpr int TREE_OFF = QA_WARPS * RING > EXCHANGE ? QA_WARPS * RING : (EXCHANGE + 127) / 128 * 128;
+  static constexpr int TREE_OFF = ((QA_WARPS * RING > Join::EXCHANGE ? QA_WARPS * RING : Join::EXCHANGE) + 127) / 128 * 128;
   static constexpr int Q_OFF = TREE_OFF + 2 * NODES * HD * 2;
   static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, true>::Q_BYTES;
-  static constexpr size_t SMEM = SUM_OFF + KeyWarp<HD, NT, true>::SUM_BYTES;
+  static constexpr int END = SUM_OFF + KeyWarp<HD, NT, true>::SUM_BYTES;
+  static constexpr size_t SMEM = END;                  // the cut's kernel
+  static constexpr int PART_OFF = (END + 127) / 128 * 128;
+  static constexpr size_t SMEM_UNIT = PART_OFF + Join::PART;  // the clusters'
   static constexpr int RESIDENT = NT == 4 ? 2 : HD == 64 ? 6 : NT == 2 ? 3 : 4;
 };
+
+// What a unit's rows see.
+template <int HD, int NT>
+struct UnitRows {
+  const TreeArgs& a;
+  const TreeSmem& tree;
+  int len, row0, M;
+  // bits of the keys (key_row(g), 8 + key_row(g), ...) of 32 positions from `base` on that row r
+  // sees, or of 16 nodes from `base` on
+  __device__ __forceinline__ uint32_t visible(bool nodes, int base, int r, int gk) const {
+    const int m = row0 + r, node = m < M ? node_of(a, m) : 0;
+    const int pos = len + tree.depth[node];
+    const unsigned long long anc = m < M ? tree.anc[node] : 0ull;
+    uint32_t bits = 0u;
+    const int count = nodes ? 2 : WARP_KEYS / 8;
+#pragma unroll
+    for (int i = 0; i < WARP_KEYS / 8; i++) {
+      if (i >= count) break;
+      const int key = base + 8 * i + gk;
+      bool see;
+      int p = key;
+      if (nodes) {
+        see = (anc >> key) & 1;
+        p = len + (see ? tree.depth[key] : 0);
+      } else {
+        see = key < len;
+      }
+      if (a.window > 0) see = see && (p < a.sinks || p > pos - a.window);
+      bits |= (uint32_t)see << i;
+    }
+    return bits;
+  }
+};
+
+// 32 positions from `base` on, in a stage of the warp's ring.
+template <int HD, int NT>
+__device__ __forceinline__ void step_codes(KeyWarp<HD, NT, true>& kw, const UnitRows<HD, NT>& rows, uint32_t ks,
+                                           uint32_t qs, uint32_t sums, float scale, int base, bool masked) {
+  using Sh = QShape<HD, NT>;
+  constexpr int KT = NT == 4 ? 1 : 2;  // tiles of 16 keys at a time
+  const uint32_t vs = ks + Sh::CODES, kss = vs + Sh::CODES, vss = kss + Sh::SCALES;
+  const int lane = threadIdx.x & 31, gk = key_row(kw.g);
+  bool odd = false;
+  if (masked)  // this lane's position's scales
+#pragma unroll
+    for (int b = 0; b < HD / 32; b++) odd |= odd_half(kw_lds16(vss + lane * (HD / 16) + 2 * b));
+  odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+  for (int i0 = 0; i0 < WARP_KEYS / 16; i0 += KT) {
+    float x[KT][NT][4];
+    const uint32_t kt = i0 * 16;
+    kw.template scores_q4<KT>(ks + kt * (HD / 2), kss + kt * (HD / 16), qs, sums, x);
+    if (masked) {
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const uint32_t bits = rows.visible(false, base, 8 * n + 2 * kw.t + h, gk) >> (2 * i0);
+#pragma unroll
+          for (int i = 0; i < 2 * KT; i++)
+            if (!(bits >> i & 1)) x[i >> 1][n][2 * (i & 1) + h] = -INFINITY;
+        }
+    }
+    kw.template weights<KT>(scale * KeyWarp<HD, NT, true>::CODE_UNIT, x);
+#pragma unroll
+    for (int i = 0; i < KT; i++) {
+      const uint32_t vt = vs + (kt + 16 * i) * (HD / 2), st = vss + (kt + 16 * i) * (HD / 16);
+      if (odd)
+        kw.values_slow(x[i], [&](int r, int d) {
+          const int b = d >> 5, j = d & 31;
+          const uint32_t w = kw_lds32(vt + r * (HD / 2) + ((b ^ q4_swz<HD>(r)) << 4) + (j & 12));
+          const int u = (w >> (8 * (j & 3) + (j >> 4) * 4)) & 15;
+          return (float)(u - 8) * kw_half(kw_lds16(st + r * (HD / 16) + 2 * b), 0);
+        });
+      else
+        kw.values_q4(vt, st, x[i]);
+    }
+  }
+}
+
+// Sixteen of the tree's own nodes, from `node0` on: fp16 rows at ks and vs.
+template <int HD, int NT>
+__device__ __forceinline__ void step_nodes(KeyWarp<HD, NT, true>& kw, const UnitRows<HD, NT>& rows, uint32_t ks,
+                                           uint32_t vs, uint32_t qs, float scale, int node0) {
+  const int lane = threadIdx.x & 31, gk = key_row(kw.g);
+  float x[1][NT][4];
+  kw.scores_f16(ks, qs, x[0]);
+#pragma unroll
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const uint32_t bits = rows.visible(true, node0, 8 * n + 2 * kw.t + h, gk);
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+        if (!(bits >> i & 1)) x[0][n][2 * i + h] = -INFINITY;
+    }
+  kw.template weights<1>(scale, x);
+  bool odd = false;
+#pragma unroll
+  for (int e = lane; e < 16 * (HD / 8); e += 32) {
+    const uint4 v = kw_lds128(vs + e * 16);
+    odd |= odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w);
+  }
+  if (__any_sync(0xffffffffu, odd))
+    kw.values_slow(x[0], [&](int r, int d) { return kw_half(kw_lds16(vs + f16_off<HD>(r, d >> 3) + 2 * (d & 7)), 0); });
+  else
+    kw.values_f16(vs, x[0]);
+}
+
+// Sixteen rows of k_new and v_new from node0 on to fp16 tiles; zeros from node m on.
+template <int HD>
+__device__ __forceinline__ void load_nodes(const TreeArgs& a, int s, int kvh, int m, int node0, uint32_t kn0, uint32_t vn0) {
+  constexpr int UNITS = HD / 8;
+  const int64_t from = (int64_t)s * a.nt * a.kv_stride + kvh * HD;
+#pragma unroll
+  for (int e = threadIdx.x & 31; e < 16 * UNITS; e += 32) {
+    const int r = node0 + e / UNITS, u = e % UNITS;
+    const bool ok = r < m;
+    const int64_t at = from + (ok ? r : 0) * a.kv_stride + u * 8;
+    kw_copy<16>(kn0 + f16_off<HD>(r, u), a.k_new + at, ok);
+    kw_copy<16>(vn0 + f16_off<HD>(r, u), a.v_new + at, ok);
+  }
+}
+
+// The cache row of a position of a slot, ~0 for none (2^32 rows of 64 dimensions would be 300 GB).
+__device__ __forceinline__ uint32_t row_of(const TreeArgs& a, int slot, int len, int kvh, int pos) {
+  if (pos >= len) return ~0u;
+  const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+  const int pg = a.table[(int64_t)slot * a.max_pages + e];
+  if (pg < 0 || pg >= a.n_pages) return ~0u;
+  return ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
+}
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_kernel(const TreeArgs a) {
   using Sh = QShape<HD, NT>;
   using KW = KeyWarp<HD, NT, true>;
-  constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, KT = Sh::KT, UNITS = HD / 8;
+  constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, UNITS = HD / 8;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ TreeSmem s_tree;
   __shared__ long long s_part[QA_WARPS];
@@ -88,34 +222,15 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
     const int kvh = unit % a.nkv, row0 = unit / a.nkv * ROWS, M = q.m * a.G;
     const int n_sink = q.n_sink, w_tile = q.w_tile, last = q.tiles - 1;
     auto tile_base = [&](int t) { return (t < n_sink ? t : w_tile + t - n_sink) * QA_KEYS; };
-    // the cache row of this lane's position of tile t, ~0 for zeros: looked up a
-    // tile ahead of its load (2^32 rows of 64 dimensions would be 300 GB)
+    // the cache row of this lane's position of tile t: looked up a tile ahead of its load
     auto lookup = [&](int t) {
-      uint32_t x = ~0u;
-      if (t < t1 && t != last) {
-        const int pos = tile_base(t) + warp * WARP_KEYS + lane;
-        if (pos < q.len) {
-          const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
-          const int pg = a.table[(int64_t)q.slot * a.max_pages + e];
-          if (pg >= 0 && pg < a.n_pages)
-            x = ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
-        }
-      }
-      return x;
+      return t < t1 && t != last ? row_of(a, q.slot, q.len, kvh, tile_base(t) + warp * WARP_KEYS + lane) : ~0u;
     };
     auto load_tile = [&](int t, uint32_t at) {
       if (t != last) {
         load_codes<HD>(ring + (t % STAGES) * Sh::STAGE, at, runs, a.k_qs, a.v_qs, a.k_scales, a.v_scales);
       } else if (16 * warp < q.m) {  // this warp's sixteen nodes
-        const int64_t from = (int64_t)s * a.nt * a.kv_stride + kvh * HD;
-#pragma unroll
-        for (int e = lane; e < 16 * UNITS; e += 32) {
-          const int r = 16 * warp + e / UNITS, u = e % UNITS;
-          const bool ok = r < q.m;
-          const int64_t at_r = from + (ok ? r : 0) * a.kv_stride + u * 8;
-          kw_copy<16>(kn0 + f16_off<HD>(r, u), a.k_new + at_r, ok);
-          kw_copy<16>(vn0 + f16_off<HD>(r, u), a.v_new + at_r, ok);
-        }
+        load_nodes<HD>(a, s, kvh, q.m, 16 * warp, kn0, vn0);
       }
     };
 
@@ -139,33 +254,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
     });
     __syncthreads();
     kw.begin();
-    const int gk = key_row(kw.g);
-    // bits of the keys (gk, 8 + gk, ...; two a tile of 16) that row 8 n + 2 t + h sees
-    // of a tile at `base`, or of the tree's
-    auto visible = [&](int t, int base, int n, int h) {
-      const int m = row0 + 8 * n + 2 * kw.t + h, node = m < M ? node_of(a, m) : 0;
-      const int pos = q.len + s_tree.depth[node];
-      const unsigned long long anc = m < M ? s_tree.anc[node] : 0ull;
-      uint32_t bits = 0u;
-      const int count = t == last ? 2 : WARP_KEYS / 8;
-#pragma unroll
-      for (int i = 0; i < WARP_KEYS / 8; i++) {
-        if (i >= count) break;
-        bool see;
-        int p;
-        if (t == last) {
-          const int key = 16 * warp + 8 * i + gk;
-          see = (anc >> key) & 1;
-          p = q.len + (see ? s_tree.depth[key] : 0);
-        } else {
-          p = base + 8 * i + gk;
-          see = p < q.len;
-        }
-        if (a.window > 0) see = see && (p < a.sinks || p > pos - a.window);
-        bits |= (uint32_t)see << i;
-      }
-      return bits;
-    };
+    const UnitRows<HD, NT> rows = {a, s_tree, q.len, row0, M};
 
     for (int t = t0; t < t1; t++) {
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
@@ -175,74 +264,13 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
       ahead[STAGES - 1] = lookup(t + STAGES);
       if (t == last) {
         if (16 * warp >= q.m) continue;
-        const uint32_t ks = kn0 + f16_off<HD>(16 * warp, 0), vs = vn0 + f16_off<HD>(16 * warp, 0);
-        float x[1][NT][4];
-        kw.scores_f16(ks, qs, x[0]);
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const uint32_t bits = visible(t, 0, n, h);
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-              if (!(bits >> i & 1)) x[0][n][2 * i + h] = -INFINITY;
-          }
-        kw.template weights<1>(scale, x);
-        bool odd = false;
-#pragma unroll
-        for (int e = lane; e < 16 * UNITS; e += 32) {
-          const uint4 v = kw_lds128(vs + e * 16);
-          odd |= odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w);
-        }
-        if (__any_sync(0xffffffffu, odd))
-          kw.values_slow(x[0], [&](int r, int d) {
-            return kw_half(kw_lds16(vs + f16_off<HD>(r, d >> 3) + 2 * (d & 7)), 0);
-          });
-        else
-          kw.values_f16(vs, x[0]);
+        step_nodes(kw, rows, kn0 + f16_off<HD>(16 * warp, 0), vn0 + f16_off<HD>(16 * warp, 0), qs, scale, 16 * warp);
         continue;
       }
-      const uint32_t ks = ring + (t % STAGES) * Sh::STAGE, vs = ks + Sh::CODES, kss = vs + Sh::CODES,
-                     vss = kss + Sh::SCALES;
       const int base = tile_base(t) + warp * WARP_KEYS;
       const bool masked = base + WARP_KEYS > q.len ||
                           (a.window > 0 && base + WARP_KEYS > q.sinks && base < q.lo + SPEC_MAX_TREE);
-      bool odd = false;
-      if (masked)  // this lane's position's scales
-#pragma unroll
-        for (int b = 0; b < HD / 32; b++) odd |= odd_half(kw_lds16(vss + lane * (HD / 16) + 2 * b));
-      odd = __any_sync(0xffffffffu, odd);
-#pragma unroll
-      for (int i0 = 0; i0 < WARP_KEYS / 16; i0 += KT) {
-        float x[KT][NT][4];
-        const uint32_t kt = i0 * 16;
-        kw.template scores_q4<KT>(ks + kt * (HD / 2), kss + kt * (HD / 16), qs, sums, x);
-        if (masked) {
-#pragma unroll
-          for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-              const uint32_t bits = visible(t, base, n, h) >> (2 * i0);
-#pragma unroll
-              for (int i = 0; i < 2 * KT; i++)
-                if (!(bits >> i & 1)) x[i >> 1][n][2 * (i & 1) + h] = -INFINITY;
-            }
-        }
-        kw.template weights<KT>(scale * KW::CODE_UNIT, x);
-#pragma unroll
-        for (int i = 0; i < KT; i++) {
-          const uint32_t vt = vs + (kt + 16 * i) * (HD / 2), st = vss + (kt + 16 * i) * (HD / 16);
-          if (odd)
-            kw.values_slow(x[i], [&](int r, int d) {
-              const int b = d >> 5, j = d & 31;
-              const uint32_t w = kw_lds32(vt + r * (HD / 2) + ((b ^ q4_swz<HD>(r)) << 4) + (j & 12));
-              const int u = (w >> (8 * (j & 3) + (j >> 4) * 4)) & 15;
-              return (float)(u - 8) * kw_half(kw_lds16(st + r * (HD / 16) + 2 * b), 0);
-            });
-          else
-            kw.values_q4(vt, st, x[i]);
-        }
-      }
+      step_codes(kw, rows, ring + (t % STAGES) * Sh::STAGE, qs, sums, scale, base, masked);
     }
     // ---- the end of the piece: the warps' results through shared memory
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -296,6 +324,113 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
   check_others<QA_THREADS>(a, ROWS, QA_SHIFT, n_cta, QA_WARPS);
 }
 
+// ---------------------------------------------------------------------------
+// Small calls: a cluster of CTAs has a unit (sequence, kv head), its positions are dealt to
+// their warps 32 at a time, and the results are joined through distributed shared
+// memory: no cut to be found, no second kernel.
+// ---------------------------------------------------------------------------
+struct UnitArgs {
+  TreeArgs t;
+  int ranks;
+};
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_unit_kernel(const UnitArgs u) {
+  using Sh = QShape<HD, NT>;
+  using KW = KeyWarp<HD, NT, true>;
+  constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, UNITS = HD / 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ TreeSmem s_tree;
+  grid_dep_begin();
+  const TreeArgs& a = u.t;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % u.ranks, unit = blockIdx.x / u.ranks, kvh = unit % a.nkv, s = unit / a.nkv;
+  const SeqInfo q = seq_info(a, s, ROWS, QA_SHIFT);
+  const uint32_t sm0 = kw_smem(smem), ring = sm0 + warp * Sh::RING;
+  const uint32_t kn0 = sm0 + Sh::TREE_OFF, vn0 = kn0 + Sh::NODES * HD * 2;
+  const uint32_t qs = sm0 + Sh::Q_OFF, sums = sm0 + Sh::SUM_OFF;
+  // steps of 32 positions: of the sinks, then from the window's first on
+  const int sink_steps = (q.sinks + WARP_KEYS - 1) / WARP_KEYS;
+  const int from = max(q.lo / WARP_KEYS, sink_steps);
+  const int steps = sink_steps + max(0, (q.len + WARP_KEYS - 1) / WARP_KEYS - from);
+  auto step_base = [&](int i) { return (i < sink_steps ? i : from + i - sink_steps) * WARP_KEYS; };
+  const int warps = u.ranks * QA_WARPS, gw = rank * QA_WARPS + warp;
+  const int nodes0 = 16 * (warps - 1 - gw);  // the tree's nodes of this warp: the last warps have few steps
+  const bool has_nodes = warps - 1 - gw < 2 && nodes0 < q.m;
+  const bool runs = a.page_size % WARP_KEYS == 0;
+  auto lookup = [&](int i) { return i < steps ? row_of(a, q.slot, q.len, kvh, step_base(i) + lane) : ~0u; };
+  auto load = [&](int stage, uint32_t at) {
+    load_codes<HD>(ring + stage * Sh::STAGE, at, runs, a.k_qs, a.v_qs, a.k_scales, a.v_scales);
+  };
+  uint32_t ahead = lookup(gw);
+  if (has_nodes) load_nodes<HD>(a, s, kvh, q.m, nodes0, kn0, vn0);
+  if (gw < steps) load(0, ahead);
+  asm volatile("cp.async.commit_group;");
+  ahead = lookup(gw + warps);
+  // the sequence's status: slot, length and count, pages that somebody sees, tree
+  int st = q.bad;
+  if (q.bad == 0) {
+    bool bad = false;
+    const int held = q.m == 0 || q.len == 0 ? 0 : (q.len - 1) / a.page_size + 1;
+    const int e1 = q.sinks > 0 ? min(held, (q.sinks - 1) / a.page_size + 1) : 0;
+    const int e0 = max(q.lo < q.len ? q.lo / a.page_size : held, e1);
+    const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
+    for (int e = tid; e < e1 + max(0, held - e0); e += QA_THREADS) {
+      const int p = row[e < e1 ? e : e0 + e - e1];
+      bad |= p < 0 || p >= a.n_pages;
+    }
+    if (!load_tree(a, s, q.m, s_tree)) st |= SPEC_ST_TREE;
+    if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
+  }
+  if (kvh == 0 && rank == 0 && tid == 0) a.status[s] = st;
+  const int M = q.m * a.G;
+  if (st != 0 || q.m == 0) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (st == 0 || rank != 0) return;
+    const int m = a.n_nodes != nullptr ? a.n_nodes[s] : a.nt, nodes = m < 0 || m > a.nt ? a.nt : m;
+    for (int e = tid; e < nodes * a.G * UNITS; e += QA_THREADS) {
+      const int r = e / UNITS, node = node_of(a, r);
+      *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + kvh * a.G + r - node * a.G) * HD +
+                                e % UNITS * 8) = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+    }
+    return;
+  }
+  KW::put_queries(qs, sums, tid, QA_THREADS, a.scale_log2 < 0.0f, [&](int r) -> const __half* {
+    if (r >= M) return nullptr;
+    const int node = node_of(a, r);
+    return a.q + ((int64_t)s * a.nt + node) * a.q_stride + (kvh * a.G + r - node * a.G) * HD;
+  });
+  __syncthreads();
+  const float scale = fabsf(a.scale_log2);
+  const UnitRows<HD, NT> rows = {a, s_tree, q.len, 0, M};
+  KW kw;
+  kw.begin();
+  int stage = 0;
+  for (int i = gw; i < steps; i += warps) {
+    __syncwarp();  // the last stage has been read
+    if (i + warps < steps) load(stage ^ 1, ahead);
+    asm volatile("cp.async.commit_group;");
+    ahead = lookup(i + 2 * warps);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    const int base = step_base(i);
+    const bool masked = base + WARP_KEYS > q.len ||
+                        (a.window > 0 && base + WARP_KEYS > q.sinks && base < q.lo + SPEC_MAX_TREE);
+    step_codes(kw, rows, ring + stage * Sh::STAGE, qs, sums, scale, base, masked);
+    stage ^= 1;
+  }
+  static_assert(STAGES == 2, "a stage in use, a stage on its way");
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+  if (has_nodes)
+    step_nodes(kw, rows, kn0 + f16_off<HD>(nodes0, 0), vn0 + f16_off<HD>(nodes0, 0), qs, scale, nodes0);
+  __syncthreads();  // the rings have been read
+  join_unit(kw, smem, Sh::PART_OFF, rank, u.ranks, M, [&](int r, int x, const float (&acc)[8], float l) {
+    const int node = node_of(a, r);
+    put_row(a.out + (((int64_t)s * a.nt + node) * a.nq + kvh * a.G + r - node * a.G) * HD + x * 8, acc, l);
+  });
+}
+
 // Query rows of a unit.  Up to 32 rows run here, more on the tcgen05 kernel with 64,
 // 128 or 256 that share one read of the cache (tree_attn_tc.cu).
 int q4_rows(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
@@ -321,10 +456,40 @@ cudaError_t launch_q4_rows(const TreeArgs& a, int n_cta, cudaStream_t st) {
          : a.rows == 16 ? launch_q4<HD, 2>(a, n_cta, st)
                         : launch_q4<HD, 4>(a, n_cta, st);
 }
+// CTAs of a unit in the clusters' form, or 0 for the cut's: by the most positions that a
+// sequence can have (its table's, the window's) for the CTAs that are resident, two an
+// SM: a warp has UNIT_STEPS steps of 32 positions at most.  Twice the CTAs are taken as long
+// as those fit and each warp keeps a step.
+constexpr int UNIT_STEPS = 4;
+int unit_ranks(const TreeArgs& a) {
+  const int64_t units = (int64_t)a.n_seq * a.nkv, all = (int64_t)a.max_pages * a.page_size;
+  const int64_t most = a.window > 0 ? std::min<int64_t>(all, (int64_t)a.window + a.sinks + 2 * WARP_KEYS) : all;
+  const int64_t steps = (most + WARP_KEYS - 1) / WARP_KEYS, ctas = 2 * device_sms();
+  if (units > ctas || units * steps > UNIT_STEPS * QA_WARPS * ctas) return 0;
+  int ranks = 1;
+  while (ranks < 16 && units * ranks * 2 <= ctas && steps >= (int64_t)QA_WARPS * ranks * 2) ranks *= 2;
+  return ranks;
+}
+
+template <int HD, int NT>
+cudaError_t launch_unit(const TreeArgs& a, int ranks, cudaStream_t st) {
+  const UnitArgs u = {a, ranks};
+  return launch_clusters(q4_unit_kernel<HD, NT>, u, (size_t)a.n_seq * a.nkv * ranks, ranks, QShape<HD, NT>::SMEM_UNIT, st);
+}
+template <int HD>
+cudaError_t launch_unit_rows(const TreeArgs& a, int ranks, cudaStream_t st) {
+  return a.rows == 8    ? launch_unit<HD, 1>(a, ranks, st)
+         : a.rows == 16 ? launch_unit<HD, 2>(a, ranks, st)
+                        : launch_unit<HD, 4>(a, ranks, st);
+}
+
 template <int HD, int NT>
 void init_q4() {
   cudaFuncSetAttribute(q4_attn_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)QShape<HD, NT>::SMEM);
+  cudaFuncSetAttribute(q4_unit_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)QShape<HD, NT>::SMEM_UNIT);
+  cudaFuncSetAttribute(q4_unit_kernel<HD, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 }  // namespace
@@ -362,6 +527,12 @@ int launch_tree_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, const
   a.v_qs = kv->v_qs + row * (hd / 2);
   a.k_scales = reinterpret_cast<const __half*>(kv->k_scales) + row * (hd / 32);
   a.v_scales = reinterpret_cast<const __half*>(kv->v_scales) + row * (hd / 32);
+  const int ranks = q4_on_tc(rows) ? 0 : unit_ranks(a);
+  if (ranks > 0) {
+    const cudaError_t e = hd == 128 ? launch_unit_rows<128>(a, ranks, st) : launch_unit_rows<64>(a, ranks, st);
+    return e == cudaSuccess ? SPEC_OK
+                            : fail(SPEC_E_CUDA, std::string("4-bit tree attention: ") + cudaGetErrorString(e));
+  }
   cudaError_t e = q4_on_tc(rows) ? tree_tc_launch(a, hd, n_cta, st)
                   : hd == 128    ? launch_q4_rows<128>(a, n_cta, st)
                                  : launch_q4_rows<64>(a, n_cta, st);
