@@ -19,7 +19,6 @@
 
 namespace {
 
-constexpr int BA_THREADS = KJ_THREADS, BA_WARPS = KJ_WARPS;
 
 struct BlockArgs {
   const uint8_t* k;  // the layer's rows of fp16, or codes
@@ -47,14 +46,16 @@ struct BlockArgs {
 
 template <int HD, int NT, bool Q4>
 struct BShape {
-  static constexpr int ROWS = 8 * NT, STAGES = 3;
+  static constexpr int ROWS = 8 * NT;
+  // a step of fp16 rows is 8 KB, of codes 4.6
+  static constexpr int WARPS = Q4 ? 8 : 4, THREADS = 32 * WARPS, STAGES = Q4 ? 2 : 3;
   static constexpr int KEYS = Q4 ? 32 : 16, KT = KEYS / 16;  // keys of a step
   static constexpr int ROW = Q4 ? HD / 2 : HD * 2;           // bytes
   static constexpr int SCALES = Q4 ? KEYS * (HD / 16) : 0;
   static constexpr int STAGE = 2 * (KEYS * ROW + SCALES);
   static constexpr int RING = STAGES * STAGE;  // of a warp
-  using Join = JoinShape<HD, ROWS>;
-  static constexpr int PART_OFF = ((BA_WARPS * RING > Join::EXCHANGE ? BA_WARPS * RING : Join::EXCHANGE) + 127) / 128 * 128;
+  using Join = JoinShape<HD, ROWS, WARPS>;
+  static constexpr int PART_OFF = ((WARPS * RING > Join::EXCHANGE ? WARPS * RING : Join::EXCHANGE) + 127) / 128 * 128;
   static constexpr int Q_OFF = (PART_OFF + Join::PART + 127) / 128 * 128;
   static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, Q4>::Q_BYTES;
   static constexpr int PATH_OFF = (SUM_OFF + (Q4 ? KeyWarp<HD, NT, Q4>::SUM_BYTES : 0) + 127) / 128 * 128;
@@ -63,7 +64,7 @@ struct BShape {
 };
 
 template <int HD, int NT, bool Q4>
-__global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs a) {
+__global__ void __launch_bounds__((BShape<HD, NT, Q4>::THREADS)) block_attn_kernel(const BlockArgs a) {
   using Sh = BShape<HD, NT, Q4>;
   using KW = KeyWarp<HD, NT, Q4>;
   constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, KEYS = Sh::KEYS, KT = Sh::KT, UNITS = HD / 8;
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
     }
     __syncthreads();
     int used = 0;
-    for (int e = tid; e < a.keep; e += BA_THREADS) {
+    for (int e = tid; e < a.keep; e += Sh::THREADS) {
       const int b = list[e];
       uint2 x = make_uint2(0u, 0u);
       if (b < -1 || (b >= 0 && ((int64_t)b << a.shift) >= len)) {
@@ -133,14 +134,14 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
   if (rank == 0 && rb == 0 && tid == 0) a.status[row_id] = st;
   if (st != 0) {
     if (rank == 0)
-      for (int e = tid; e < rows * UNITS; e += BA_THREADS)
+      for (int e = tid; e < rows * UNITS; e += Sh::THREADS)
         *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + h0 + e / UNITS) * HD + e % UNITS * 8) =
             make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
     return;
   }
   const int n_path = s_depth;
   const int steps = (int)((((int64_t)s_used << a.shift) + KEYS - 1) / KEYS);
-  const int warps = a.ranks * BA_WARPS, gw = rank * BA_WARPS + warp;
+  const int warps = a.ranks * Sh::WARPS, gw = rank * Sh::WARPS + warp;
   const int path_steps = (n_path + 15) / 16, my_path = warps - 1 - gw;  // this warp's sixteen of the path, and those behind
   const uint32_t ring = sm0 + warp * Sh::RING, qs = sm0 + Sh::Q_OFF, sums = sm0 + Sh::SUM_OFF;
   const uint32_t kn0 = sm0 + Sh::PATH_OFF, vn0 = kn0 + a.path_rows * HD * 2;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
     }
   };
   // the path's rows first: they are few, and their step comes last
-  for (int p = my_path; p < path_steps && my_path < BA_WARPS; p += warps) {
+  for (int p = my_path; p < path_steps && my_path < Sh::WARPS; p += warps) {
     const int64_t from = (int64_t)s * a.nt * a.kv_stride + kvh * HD;
     for (int e = lane; e < 16 * UNITS; e += 32) {
       const int i = 16 * p + e / UNITS, u = e % UNITS;
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
     if (gw + i * warps < steps) load_step(i, now[i]);
     asm volatile("cp.async.commit_group;");
   }
-  KW::put_queries(qs, sums, tid, BA_THREADS, a.scale_log2 < 0.0f, [&](int r) -> const __half* {
+  KW::put_queries(qs, sums, tid, Sh::THREADS, a.scale_log2 < 0.0f, [&](int r) -> const __half* {
     return r < rows ? a.q + ((int64_t)s * a.nt + node) * a.q_stride + (h0 + r) * HD : nullptr;
   });
   __syncthreads();
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncwarp();
-  for (int p = my_path; p < path_steps && my_path < BA_WARPS; p += warps) {
+  for (int p = my_path; p < path_steps && my_path < Sh::WARPS; p += warps) {
     float x[1][NT][4];
     kw.scores_f16(kn0 + f16_off<HD>(16 * p, 0), qs, x[0]);
 #pragma unroll
@@ -250,13 +251,13 @@ __global__ void __launch_bounds__(BA_THREADS) block_attn_kernel(const BlockArgs 
   }
   __syncthreads();  // the rings have been read
   __half* out = a.out + (((int64_t)s * a.nt + node) * a.nq + h0) * HD;
-  join_unit(kw, smem, Sh::PART_OFF, rank, a.ranks, rows,
+  join_unit<Sh::WARPS>(kw, smem, Sh::PART_OFF, rank, a.ranks, rows,
             [&](int r, int u, const float (&acc)[8], float l) { put_row(out + r * HD + u * 8, acc, l); });
 }
 
 template <int HD, int NT, bool Q4>
 cudaError_t launch_block(const BlockArgs& a, size_t units, cudaStream_t st) {
-  return launch_clusters(block_attn_kernel<HD, NT, Q4>, a, units * a.ranks, a.ranks,
+  return launch_clusters(block_attn_kernel<HD, NT, Q4>, a, units * a.ranks, BShape<HD, NT, Q4>::THREADS, a.ranks,
                          BShape<HD, NT, Q4>::smem(a.path_rows, a.keep), st);
 }
 
@@ -319,11 +320,14 @@ int launch_block_attn(const spec_pages* book, const BlockPlanes& planes, const s
   a.out = reinterpret_cast<__half*>(out);
   a.status = status;
   const double units = (double)t->n_seq * t->nt * a.nkv * a.row_blocks;
-  // CTAs of a unit: as many as are resident (two an SM), as long as every warp has
-  // two steps of the list
+  // CTAs of a unit, as long as every warp has two steps of the list: of fp16 as many as are
+  // resident, two an SM, up to 16 (one node over 64 blocks of 64: 8.9 us, with up to eight
+  // 9.9); of codes, with twice the warps, one an SM, up to eight (8 sequences of one node
+  // over 64 blocks of 64: 17.3 us, with half the warps 20.8)
   const int64_t steps = ((int64_t)n_keep * block + (q4 ? 31 : 15)) / (q4 ? 32 : 16);
+  const int most = q4 ? 8 : 16, fit = q4 ? 1 : 2, warps = q4 ? 8 : 4;
   a.ranks = 1;
-  while (a.ranks < 16 && units * a.ranks * 2 <= 2 * device_sms() && steps >= (int64_t)2 * BA_WARPS * a.ranks * 2)
+  while (a.ranks < most && units * a.ranks * 2 <= fit * device_sms() && steps >= (int64_t)2 * warps * a.ranks * 2)
     a.ranks *= 2;
   if (units * a.ranks > INT32_MAX) return fail(SPEC_E_SHAPE, "n_seq * nt * n_q_heads too large");
   const size_t n = (size_t)units;

@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "key_warp.cuh"
@@ -12,8 +13,8 @@
 namespace {
 
 // ---------------------------------------------------------------------------
-// digests: a warp per block, 16 bytes a lane and load, several rows of the block a
-// load, up to 16 loads in flight; the lanes that hold the same channels are joined
+// digests: a warp per block, 16 bytes (of codes 8) a lane and load, several rows of the
+// block a load, up to 16 loads in flight; the lanes that hold the same channels are joined
 // at the end, each keeping the half of the registers that the other one gives away
 // ---------------------------------------------------------------------------
 constexpr int DG_THREADS = 128, DG_WARPS = DG_THREADS / 32;
@@ -61,12 +62,13 @@ __device__ __forceinline__ int join_lanes(uint32_t (&lo)[REGS], uint32_t (&hi)[R
 }
 
 template <int HD, bool Q4>
-__global__ void __launch_bounds__(DG_THREADS)
+__global__ void __launch_bounds__(DG_THREADS, Q4 ? 6 : 4)
 digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __restrict__ slots,
               const int32_t* __restrict__ pos0, int split, int32_t* __restrict__ status) {
-  constexpr int ROW = Q4 ? HD / 2 : HD * 2, LANES = ROW / 16, PER = 32 / LANES;  // bytes; lanes and rows of a load
-  constexpr int REGS = Q4 ? 16 : 4, U = Q4 ? 4 : 16;
-  constexpr int BIT = LANES == 16 ? 4 : LANES == 8 ? 3 : LANES == 4 ? 2 : 1;
+  constexpr int ROW = Q4 ? HD / 2 : HD * 2, LANES = ROW / (Q4 ? 8 : 16), PER = 32 / LANES;  // bytes; lanes and rows of a load
+  constexpr int REGS = Q4 ? 8 : 4, U = Q4 ? 8 : 16;
+  constexpr int BIT = LANES == 16 ? 4 : LANES == 8 ? 3 : 2;
+  using Load = typename std::conditional<Q4, uint2, uint4>::type;
   constexpr int KEPT = REGS >> (5 - BIT);
   grid_dep_begin();
   const int lane = threadIdx.x & 31;
@@ -104,22 +106,26 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
       lo[x] = 0x7C007C00u;
       hi[x] = 0xFC00FC00u;
     }
-    const uint8_t* src = keys.rows + r0 * ROW + (lane % LANES) * 16;
-    const __half* sc = Q4 ? keys.scales + r0 * (HD / 32) + lane % LANES : nullptr;
+    const uint8_t* src = keys.rows + r0 * ROW + (lane % LANES) * (int)sizeof(Load);
+    const __half* sc = Q4 ? keys.scales + r0 * (HD / 32) + lane % LANES / 2 : nullptr;
     for (int r = 0; r < rows; r += PER * U) {
-      uint4 v[U];
+      Load v[U];
       uint32_t s[U];
 #pragma unroll
       for (int u = 0; u < U; u++) {
         if (u > 0 && r + u * PER >= rows) break;
         const int at = min(r + u * PER + lane / LANES, rows - 1);  // (a row again changes nothing)
-        v[u] = __ldg(reinterpret_cast<const uint4*>(src + at * ROW));
+        v[u] = __ldg(reinterpret_cast<const Load*>(src + at * ROW));
         if (Q4) s[u] = __half_as_ushort(__ldg(sc + at * (HD / 32))) * 0x10001u;
       }
 #pragma unroll
       for (int u = 0; u < U; u++) {
         if (u > 0 && r + u * PER >= rows) break;
-        const uint32_t q[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t q[4] = {v[u].x, v[u].y, 0u, 0u};
+        if constexpr (!Q4) {
+          q[2] = v[u].z;
+          q[3] = v[u].w;
+        }
 #pragma unroll
         for (int x = 0; x < REGS; x++) {
           // codes: word x / 4; elements 0, 2 | 1, 3 | 16, 18 | 17, 19 of its four
@@ -142,14 +148,14 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
     } else if (KEPT >= 2) {  // neighbours: elements 0, 2 and 1, 3 of a word's four, or 16 + ...
 #pragma unroll
       for (int x = 0; x < KEPT; x += 2) {
-        const int reg = reg0 + x, word = (32 * l + 16 * (reg >> 1 & 1) + 4 * (reg >> 2)) / 2;
+        const int reg = reg0 + x, word = (32 * (l >> 1) + 16 * (reg >> 1 & 1) + 8 * (l & 1) + 4 * (reg >> 2)) / 2;
         *reinterpret_cast<uint2*>(reinterpret_cast<uint32_t*>(to) + word) =
             make_uint2(__byte_perm(lo[x], lo[x + 1], 0x5410), __byte_perm(lo[x], lo[x + 1], 0x7632));
         *reinterpret_cast<uint2*>(reinterpret_cast<uint32_t*>(to + HD) + word) =
             make_uint2(__byte_perm(hi[x], hi[x + 1], 0x5410), __byte_perm(hi[x], hi[x + 1], 0x7632));
       }
     } else {  // one register: elements reg & 1, + 2
-      const int reg = reg0, e = 32 * l + 16 * (reg >> 1 & 1) + 4 * (reg >> 2) + (reg & 1);
+      const int reg = reg0, e = 32 * (l >> 1) + 16 * (reg >> 1 & 1) + 8 * (l & 1) + 4 * (reg >> 2) + (reg & 1);
       to[e] = (uint16_t)lo[0];
       to[e + 2] = (uint16_t)(lo[0] >> 16);
       to[HD + e] = (uint16_t)hi[0];
@@ -170,7 +176,7 @@ constexpr int SC_THREADS = 256, SC_WARPS = SC_THREADS / 32, SC_ROWS = 64;
 
 struct ScoreArgs {
   spec_digest dg;
-  int layer, n_seq, nt, nq, G, GP;  // GP: G to the next power of two
+  int layer, n_seq, nt, nq, G, GP, gp_shift;  // GP: G to the next power of two
   const int32_t* slots;
   const int32_t* n_nodes;
   const __half* q;
@@ -244,18 +250,26 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
   const int mine = first + warp * 16;
   if (mine < nb) load(mine);
   // the queries' fragments: 16 bytes of a row are two steps' of lo and two of hi
-  for (int e = tid; e < tiles * 8 * (HD / 8); e += SC_THREADS) {
-    const int u = e % (HD / 8), r = e / (HD / 8), i = u >> 2, col = r & 7, n = r >> 3;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  constexpr int UNITS = HD / 8, IN_FLIGHT = SC_ROWS * UNITS / SC_THREADS;
+  uint4 x[IN_FLIGHT];
+#pragma unroll
+  for (int y = 0; y < IN_FLIGHT; y++) {
+    const int e = tid + y * SC_THREADS, u = e % UNITS, r = e / UNITS;
+    x[y] = make_uint4(0u, 0u, 0u, 0u);
     if (r < rows) {
-      const int node = node0 + r / a.GP, k = r & (a.GP - 1), head = h * a.G + (k < a.G ? k : 0);
-      x = *reinterpret_cast<const uint4*>(a.q + ((int64_t)s * a.nt + node) * a.q_stride + head * HD + 8 * u);
+      const int node = node0 + (r >> a.gp_shift), k = r & (a.GP - 1), head = h * a.G + (k < a.G ? k : 0);
+      x[y] = *reinterpret_cast<const uint4*>(a.q + ((int64_t)s * a.nt + node) * a.q_stride + head * HD + 8 * u);
     }
+  }
+#pragma unroll
+  for (int y = 0; y < IN_FLIGHT; y++) {
+    const int e = tid + y * SC_THREADS, u = e % UNITS, r = e / UNITS, i = u >> 2, col = r & 7, n = r >> 3;
+    if (n >= tiles) break;
     const uint32_t to = qs + ((n * STEPS + 2 * i) * 32 + col * 4 + (u & 3)) * 8;
-    kw_sts64(to, min2(x.x, 0u), min2(x.y, 0u));
-    kw_sts64(to + 256, min2(x.z, 0u), min2(x.w, 0u));
-    kw_sts64(to + STEPS * 128, max2(x.x, 0u), max2(x.y, 0u));
-    kw_sts64(to + STEPS * 128 + 256, max2(x.z, 0u), max2(x.w, 0u));
+    kw_sts64(to, min2(x[y].x, 0u), min2(x[y].y, 0u));
+    kw_sts64(to + 256, min2(x[y].z, 0u), min2(x[y].w, 0u));
+    kw_sts64(to + STEPS * 128, max2(x[y].x, 0u), max2(x[y].y, 0u));
+    kw_sts64(to + STEPS * 128 + 256, max2(x[y].z, 0u), max2(x[y].w, 0u));
   }
   __syncthreads();
   const int64_t out0 = (((int64_t)s * a.nt + node0) * dg.n_kv_heads + h) * a.ld, node_ld = (int64_t)dg.n_kv_heads * a.ld;
@@ -317,9 +331,11 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
 // ---------------------------------------------------------------------------
 // selection: a CTA per row, a row's keys (its scores as whole numbers in the same
 // order) in registers, four neighbours and THREADS * 4 behind the next four.  The
-// bits of the k-th largest key are found from the highest in which the row's keys
-// differ, by counting the keys that reach each candidate, until exactly k do; the
-// chosen blocks are marked in a bit map, whose words then are written out in order.
+// k-th largest key lies in a bin of a histogram of the eight highest bits in which the
+// row's keys differ; of the bin's keys, mostly a few dozen, each is ranked against the
+// others (192 x 8 rows of 2048: 15 us with the k-th key's bits found one by one
+// by counts).  The chosen blocks are marked in a bit map, whose words then are written
+// out in order.
 // ---------------------------------------------------------------------------
 struct SelectArgs {
   const int32_t* len;
@@ -335,9 +351,10 @@ struct SelectArgs {
 
 template <int THREADS, int PER>
 __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
-  constexpr int WARPS = THREADS / 32, SPAN = THREADS * PER;
+  constexpr int WARPS = THREADS / 32, SPAN = THREADS * PER, CAND = 256;
   __shared__ int s_sum[2][WARPS];
-  __shared__ uint32_t s_bits[SPAN / 32], s_mm[2][WARPS];
+  __shared__ uint32_t s_bits[SPAN / 32], s_mm[2][WARPS], s_hist[256], s_cand[CAND], s_key;
+  __shared__ int s_n, s_found[3];
   grid_dep_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r = blockIdx.x;
@@ -405,45 +422,106 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
     }
     return c;
   };
+  // f of every key but 0
+  auto each_key = [&](auto&& f) {
+    if (one) {
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        if (key[i] != 0u) f(key[i]);
+    } else {
+      for (int j = a.first + tid; j < end; j += THREADS) f(key_of(j));
+    }
+  };
   load(0);
+  for (int b = tid; b < 256; b += THREADS) s_hist[b] = 0u;
+  if (tid == 0) s_n = 0;
   // the bits that all keys have in common
   uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-  if (one) {
-#pragma unroll
-    for (int i = 0; i < PER; i++) {
-      hi = max(hi, key[i]);
-      lo = min(lo, key[i] - 1u);  // (no block: the largest)
-    }
-  } else {
-    for (int j = a.first + tid; j < end; j += THREADS) {
-      const uint32_t y = key_of(j);
-      hi = max(hi, y);
-      lo = min(lo, y - 1u);
-    }
-  }
+  each_key([&](uint32_t y) {
+    hi = max(hi, y);
+    lo = min(lo, y);
+  });
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
+  if (lane == 0) {
+    s_mm[0][warp] = hi;
+    s_mm[1][warp] = lo;
+  }
+  __syncthreads();
   if (WARPS > 1) {
-    if (lane == 0) {
-      s_mm[0][warp] = hi;
-      s_mm[1][warp] = lo;
-    }
-    __syncthreads();
     hi = __reduce_max_sync(0xffffffffu, lane < WARPS ? s_mm[0][lane] : 0u);
     lo = __reduce_min_sync(0xffffffffu, lane < WARPS ? s_mm[1][lane] : 0xFFFFFFFFu);
   }
-  lo += 1u;
-  // t: the largest number that `need` keys reach (above all keys if none is needed)
+  // t: the largest number that `need` keys reach (above all keys if none is needed); reach: how
+  // many do
   uint32_t t = need > 0 ? lo : 0xFFFFFFFFu;
   int reach = need > 0 ? end - a.first : 0;
-  if (reach != need && hi != lo) {
-    const int top = 31 - __clz((int)(hi ^ lo));
-    t = hi & ~((2u << top) - 1u);  // the bits in common
-    for (uint32_t bit = 1u << top; bit != 0u && reach != need; bit >>= 1) {
-      const int c = count(t | bit);
-      if (c >= need) {
-        t |= bit;
-        reach = c;
+  if (need > 0 && hi != lo) {
+    const int top = 31 - __clz((int)(hi ^ lo)), shift = max(0, top - 7);
+    const uint32_t bins = 2u << (top - shift);
+    t = hi & ~((2u << top) - 1u);
+    each_key([&](uint32_t y) { atomicAdd(&s_hist[(y >> shift) & (bins - 1u)], 1u); });
+    __syncthreads();
+    if (warp == 0) {  // eight bins a lane, from the highest on
+      int c[8], mine = 0;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        c[i] = (int)s_hist[255 - 8 * lane - i];
+        mine += c[i];
+      }
+      int at = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, at, off);
+        if (lane >= off) at += z;
+      }
+      int above = at - mine;
+      if (above < need && need <= at) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          if (above < need && need <= above + c[i]) {
+            s_found[0] = 255 - 8 * lane - i;
+            s_found[1] = above;
+            s_found[2] = c[i];
+          }
+          above += c[i];
+        }
+      }
+    }
+    __syncthreads();
+    const uint32_t bin = (uint32_t)s_found[0];
+    const int above = s_found[1], in_bin = s_found[2], rest = need - above;
+    t |= bin << shift;
+    reach = above + in_bin;
+    if (reach != need && shift > 0) {
+      if (in_bin <= CAND) {
+        each_key([&](uint32_t y) {
+          if (((y >> shift) & (bins - 1u)) == bin) s_cand[atomicAdd(&s_n, 1)] = y;
+        });
+        __syncthreads();
+        for (int e = tid; e < in_bin; e += THREADS) {
+          const uint32_t y = s_cand[e];
+          int more = 0, same = 0;
+          for (int z = 0; z < in_bin; z++) {
+            more += s_cand[z] > y;
+            same += s_cand[z] == y;
+          }
+          if (more < rest && rest <= more + same) {  // (several of the same key)
+            s_key = y;
+            s_found[0] = above + more + same;
+          }
+        }
+        __syncthreads();
+        t = s_key;
+        reach = s_found[0];
+      } else {  // bit by bit
+        for (uint32_t bit = 1u << (shift - 1); bit != 0u && reach != need; bit >>= 1) {
+          const int c = count(t | bit);
+          if (c >= need) {
+            t |= bit;
+            reach = c;
+          }
+        }
       }
     }
   }
@@ -562,7 +640,9 @@ int launch_digest(const spec_digest* dg, const Keys& keys, bool q4, int n, const
   if (units > INT32_MAX) return fail(SPEC_E_SHAPE, "n * n_layers * n_kv_heads too large");
   // warps of a unit: as many as keep the SMs full, when the blocks are many
   const int64_t most = (int64_t)dg->max_pages * (dg->page_size / dg->block);
-  const int split = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)(device_sms() * 48 / units)));
+  const int64_t fit = std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)(device_sms() * 64 / units)));
+  const int64_t rounds = (most + fit - 1) / fit;
+  const int split = (int)((most + rounds - 1) / rounds);
   const size_t grid = (size_t)((units * split + DG_WARPS - 1) / DG_WARPS);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto kernel = dg->head_dim == 128 ? (q4 ? digest_kernel<128, true> : digest_kernel<128, false>)
@@ -642,8 +722,9 @@ extern "C" int spec_block_scores(const spec_digest* dg, int layer, int n_seq, co
   a.scores = scores;
   a.ld = ld;
   a.status = status;
-  a.GP = 1;
-  while (a.GP < a.G) a.GP *= 2;
+  a.gp_shift = 0;
+  while (1 << a.gp_shift < a.G) a.gp_shift++;
+  a.GP = 1 << a.gp_shift;
   a.nodes = std::min(nt, SC_ROWS / a.GP);
   a.groups = (nt + a.nodes - 1) / a.nodes;
   // a tile of 16 blocks a warp, until there are CTAs for four an SM

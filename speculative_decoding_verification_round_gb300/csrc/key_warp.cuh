@@ -596,40 +596,38 @@ __device__ __forceinline__ float2 cluster_ld2(uint32_t at) {
   return v;
 }
 
-constexpr int KJ_THREADS = 128, KJ_WARPS = 4;
-
-// The shared memory that a join needs: the warps' results over whatever has been read
-// (from 0 on), the CTA's behind it.
-template <int HD, int ROWS>
+// The shared memory that a join of WARPS warps a CTA needs: the warps' results over
+// whatever has been read (from 0 on), the CTA's behind it.
+template <int HD, int ROWS, int WARPS>
 struct JoinShape {
   static constexpr int XROW = HD + 4;  // floats of a row (padded)
-  static constexpr int PART = ROWS * (XROW * 4 + 8), EXCHANGE = KJ_WARPS * PART;
+  static constexpr int PART = ROWS * (XROW * 4 + 8), EXCHANGE = WARPS * PART;
 };
 
 // finish(row, unit of 8 dimensions, unnormalised result, sum) for each of `rows` rows of a unit
 // which `ranks` (1 to 16, a power of two) CTAs of a cluster have, this one being `rank`: in
 // the order of the warps, and of the CTAs by halves.  All threads of all of them; what the
 // kernel had in the first EXCHANGE bytes of smem has been read.
-template <int HD, int NT, bool Q4, class F>
+template <int WARPS, int HD, int NT, bool Q4, class F>
 __device__ __forceinline__ void join_unit(const KeyWarp<HD, NT, Q4>& kw, unsigned char* smem, int part_off, int rank,
                                           int ranks, int rows, F&& finish) {
-  constexpr int ROWS = 8 * NT, UNITS = HD / 8, XROW = JoinShape<HD, ROWS>::XROW;
+  constexpr int ROWS = 8 * NT, UNITS = HD / 8, XROW = JoinShape<HD, ROWS, WARPS>::XROW, THREADS = 32 * WARPS;
   const int tid = threadIdx.x, warp = tid >> 5;
   float* x = reinterpret_cast<float*>(smem);
-  float2* ml = reinterpret_cast<float2*>(x + (size_t)KJ_WARPS * ROWS * XROW);
+  float2* ml = reinterpret_cast<float2*>(x + (size_t)WARPS * ROWS * XROW);
   float* part = reinterpret_cast<float*>(smem + part_off);
   float2* part_ml = reinterpret_cast<float2*>(part + ROWS * XROW);
   kw.template put<XROW>(x + (size_t)warp * ROWS * XROW, ml + warp * ROWS);
   __syncthreads();
-  for (int e = tid; e < rows * UNITS; e += KJ_THREADS) {
+  for (int e = tid; e < rows * UNITS; e += THREADS) {
     const int r = e / UNITS, u = e % UNITS;
     float m2 = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < KJ_WARPS; w++) m2 = fmaxf(m2, ml[w * ROWS + r].x);
+    for (int w = 0; w < WARPS; w++) m2 = fmaxf(m2, ml[w * ROWS + r].x);
     const float ref = m2 == -INFINITY ? 0.0f : m2;
     float acc[8] = {}, l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < KJ_WARPS; w++) {
+    for (int w = 0; w < WARPS; w++) {
       const float2 y = ml[w * ROWS + r];
       const float f = kw_exp2(y.x - ref);
       l = fmaf(y.y, f, l);
@@ -652,8 +650,8 @@ __device__ __forceinline__ void join_unit(const KeyWarp<HD, NT, Q4>& kw, unsigne
   cluster_sync();
   // a lane a rank: lanes [0, ranks) of a group have one item (row, 8 dimensions)
   const int j = tid & (ranks - 1);
-  for (int e0 = 0; e0 < rows * UNITS; e0 += KJ_THREADS) {  // items of all ranks together: KJ_THREADS a turn
-    const int e = e0 + rank * (KJ_THREADS / ranks) + tid / ranks;
+  for (int e0 = 0; e0 < rows * UNITS; e0 += THREADS) {  // items of all ranks together: THREADS a turn
+    const int e = e0 + rank * (THREADS / ranks) + tid / ranks;
     const bool ok = e < rows * UNITS;
     const int r = ok ? e / UNITS : 0, u = ok ? e % UNITS : 0;
     const uint32_t from = cluster_at(kw_smem(part + r * XROW + u * 8), j);
@@ -684,11 +682,10 @@ __device__ __forceinline__ void put_row(__half* to, const float (&acc)[8], float
                  kw_pack(acc[4] * inv, acc[5] * inv), kw_pack(acc[6] * inv, acc[7] * inv));
 }
 
-// A launch in clusters of `ranks` CTAs (of KJ_THREADS threads), as a programmatic
-// dependent.
+// A launch in clusters of `ranks` CTAs, as a programmatic dependent.
 template <class A>
-inline cudaError_t launch_clusters(void (*kernel)(const A), const A& a, size_t ctas, int ranks, size_t smem,
-                                   cudaStream_t st) {
+inline cudaError_t launch_clusters(void (*kernel)(const A), const A& a, size_t ctas, int threads, int ranks,
+                                   size_t smem, cudaStream_t st) {
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = programmatic_launch() ? 1 : 0;
@@ -700,7 +697,7 @@ inline cudaError_t launch_clusters(void (*kernel)(const A), const A& a, size_t c
   cfg.attrs = at;
   cfg.numAttrs = 2;
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(KJ_THREADS);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }

@@ -31,16 +31,14 @@ struct QShape {
   static constexpr int CODES = WARP_KEYS * HD / 2, SCALES = WARP_KEYS * HD / 16;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // bytes: K's and V's codes, K's and V's scales
   static constexpr int RING = STAGES * STAGE;         // of a warp
-  using Join = JoinShape<HD, ROWS>;
+  using Join = JoinShape<HD, ROWS, QA_WARPS>;
   static constexpr int XROW = Join::XROW;
   static constexpr int NODES = NT == 4 ? 32 : 16;     // rows of the tree's own tile (no more nodes than rows)
   static constexpr int TREE_OFF = ((QA_WARPS * RING > Join::EXCHANGE ? QA_WARPS * RING : Join::EXCHANGE) + 127) / 128 * 128;
   static constexpr int Q_OFF = TREE_OFF + 2 * NODES * HD * 2;
   static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, true>::Q_BYTES;
   static constexpr int END = SUM_OFF + KeyWarp<HD, NT, true>::SUM_BYTES;
-  static constexpr size_t SMEM = END;                  // the cut's kernel
-  static constexpr int PART_OFF = (END + 127) / 128 * 128;
-  static constexpr size_t SMEM_UNIT = PART_OFF + Join::PART;  // the clusters'
+  static constexpr size_t SMEM = END;
   static constexpr int RESIDENT = NT == 4 ? 2 : HD == 64 ? 6 : NT == 2 ? 3 : 4;
 };
 
@@ -329,14 +327,28 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
 // their warps 32 at a time, and the results are joined through distributed shared
 // memory: no cut to be found, no second kernel.
 // ---------------------------------------------------------------------------
+constexpr int QU_WARPS = 8, QU_THREADS = 32 * QU_WARPS;
+
+template <int HD, int NT>
+struct UShape : QShape<HD, NT> {
+  using Q = QShape<HD, NT>;
+  using Join = JoinShape<HD, Q::ROWS, QU_WARPS>;
+  static constexpr int TREE_OFF = ((QU_WARPS * Q::RING > Join::EXCHANGE ? QU_WARPS * Q::RING : Join::EXCHANGE) + 127) / 128 * 128;
+  static constexpr int Q_OFF = TREE_OFF + 2 * Q::NODES * HD * 2;
+  static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, true>::Q_BYTES;
+  static constexpr int PART_OFF = (SUM_OFF + KeyWarp<HD, NT, true>::SUM_BYTES + 127) / 128 * 128;
+  static constexpr size_t SMEM = PART_OFF + Join::PART;
+  static constexpr int RESIDENT = NT == 4 ? 1 : HD == 64 ? 3 : NT == 2 ? 1 : 2;
+};
+
 struct UnitArgs {
   TreeArgs t;
   int ranks;
 };
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_unit_kernel(const UnitArgs u) {
-  using Sh = QShape<HD, NT>;
+__global__ void __launch_bounds__(QU_THREADS, UShape<HD, NT>::RESIDENT) q4_unit_kernel(const UnitArgs u) {
+  using Sh = UShape<HD, NT>;
   using KW = KeyWarp<HD, NT, true>;
   constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, UNITS = HD / 8;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -354,7 +366,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_unit_
   const int from = max(q.lo / WARP_KEYS, sink_steps);
   const int steps = sink_steps + max(0, (q.len + WARP_KEYS - 1) / WARP_KEYS - from);
   auto step_base = [&](int i) { return (i < sink_steps ? i : from + i - sink_steps) * WARP_KEYS; };
-  const int warps = u.ranks * QA_WARPS, gw = rank * QA_WARPS + warp;
+  const int warps = u.ranks * QU_WARPS, gw = rank * QU_WARPS + warp;
   const int nodes0 = 16 * (warps - 1 - gw);  // the tree's nodes of this warp: the last warps have few steps
   const bool has_nodes = warps - 1 - gw < 2 && nodes0 < q.m;
   const bool runs = a.page_size % WARP_KEYS == 0;
@@ -375,7 +387,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_unit_
     const int e1 = q.sinks > 0 ? min(held, (q.sinks - 1) / a.page_size + 1) : 0;
     const int e0 = max(q.lo < q.len ? q.lo / a.page_size : held, e1);
     const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
-    for (int e = tid; e < e1 + max(0, held - e0); e += QA_THREADS) {
+    for (int e = tid; e < e1 + max(0, held - e0); e += QU_THREADS) {
       const int p = row[e < e1 ? e : e0 + e - e1];
       bad |= p < 0 || p >= a.n_pages;
     }
@@ -388,14 +400,14 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_unit_
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (st == 0 || rank != 0) return;
     const int m = a.n_nodes != nullptr ? a.n_nodes[s] : a.nt, nodes = m < 0 || m > a.nt ? a.nt : m;
-    for (int e = tid; e < nodes * a.G * UNITS; e += QA_THREADS) {
+    for (int e = tid; e < nodes * a.G * UNITS; e += QU_THREADS) {
       const int r = e / UNITS, node = node_of(a, r);
       *reinterpret_cast<uint4*>(a.out + (((int64_t)s * a.nt + node) * a.nq + kvh * a.G + r - node * a.G) * HD +
                                 e % UNITS * 8) = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
     }
     return;
   }
-  KW::put_queries(qs, sums, tid, QA_THREADS, a.scale_log2 < 0.0f, [&](int r) -> const __half* {
+  KW::put_queries(qs, sums, tid, QU_THREADS, a.scale_log2 < 0.0f, [&](int r) -> const __half* {
     if (r >= M) return nullptr;
     const int node = node_of(a, r);
     return a.q + ((int64_t)s * a.nt + node) * a.q_stride + (kvh * a.G + r - node * a.G) * HD;
@@ -425,7 +437,7 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_unit_
   if (has_nodes)
     step_nodes(kw, rows, kn0 + f16_off<HD>(nodes0, 0), vn0 + f16_off<HD>(nodes0, 0), qs, scale, nodes0);
   __syncthreads();  // the rings have been read
-  join_unit(kw, smem, Sh::PART_OFF, rank, u.ranks, M, [&](int r, int x, const float (&acc)[8], float l) {
+  join_unit<QU_WARPS>(kw, smem, Sh::PART_OFF, rank, u.ranks, M, [&](int r, int x, const float (&acc)[8], float l) {
     const int node = node_of(a, r);
     put_row(a.out + (((int64_t)s * a.nt + node) * a.nq + kvh * a.G + r - node * a.G) * HD + x * 8, acc, l);
   });
@@ -456,25 +468,28 @@ cudaError_t launch_q4_rows(const TreeArgs& a, int n_cta, cudaStream_t st) {
          : a.rows == 16 ? launch_q4<HD, 2>(a, n_cta, st)
                         : launch_q4<HD, 4>(a, n_cta, st);
 }
-// CTAs of a unit in the clusters' form, or 0 for the cut's: by the most positions that a
-// sequence can have (its table's, the window's) for the CTAs that are resident, two an
-// SM: a warp has UNIT_STEPS steps of 32 positions at most.  Twice the CTAs are taken as long
-// as those fit and each warp keeps a step.
-constexpr int UNIT_STEPS = 4;
+// CTAs of a unit in the clusters' form, or 0 for the cut's: up to eight (clusters of more
+// leave SMs of a GPC unused), as many as are resident, one an SM, and keep a step of 32
+// positions for each warp, by the most positions that a sequence can have (its table's,
+// the window's).  With up to eight steps for a warp the clusters are faster where they fill
+// the SMs (4 sequences of 8000 positions 18.8 us against 24.3, 32 of 1000 17.2 against
+// 25.3), with up to three anywhere (one sequence of 1000 8.1 against 9.7; of 16000, eight
+// steps on 64 SMs, 17.2 against 14.9).
 int unit_ranks(const TreeArgs& a) {
   const int64_t units = (int64_t)a.n_seq * a.nkv, all = (int64_t)a.max_pages * a.page_size;
   const int64_t most = a.window > 0 ? std::min<int64_t>(all, (int64_t)a.window + a.sinks + 2 * WARP_KEYS) : all;
-  const int64_t steps = (most + WARP_KEYS - 1) / WARP_KEYS, ctas = 2 * device_sms();
-  if (units > ctas || units * steps > UNIT_STEPS * QA_WARPS * ctas) return 0;
+  const int64_t steps = (most + WARP_KEYS - 1) / WARP_KEYS, sms = device_sms();
+  if (units > 2 * sms) return 0;
   int ranks = 1;
-  while (ranks < 16 && units * ranks * 2 <= ctas && steps >= (int64_t)QA_WARPS * ranks * 2) ranks *= 2;
-  return ranks;
+  while (ranks < 8 && units * ranks * 2 <= sms && steps >= (int64_t)QU_WARPS * ranks * 2) ranks *= 2;
+  return steps <= (int64_t)QU_WARPS * ranks * (4 * units * ranks >= 3 * sms ? 8 : 3) ? ranks : 0;
 }
 
 template <int HD, int NT>
 cudaError_t launch_unit(const TreeArgs& a, int ranks, cudaStream_t st) {
   const UnitArgs u = {a, ranks};
-  return launch_clusters(q4_unit_kernel<HD, NT>, u, (size_t)a.n_seq * a.nkv * ranks, ranks, QShape<HD, NT>::SMEM_UNIT, st);
+  return launch_clusters(q4_unit_kernel<HD, NT>, u, (size_t)a.n_seq * a.nkv * ranks, QU_THREADS, ranks,
+                         UShape<HD, NT>::SMEM, st);
 }
 template <int HD>
 cudaError_t launch_unit_rows(const TreeArgs& a, int ranks, cudaStream_t st) {
@@ -488,8 +503,7 @@ void init_q4() {
   cudaFuncSetAttribute(q4_attn_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)QShape<HD, NT>::SMEM);
   cudaFuncSetAttribute(q4_unit_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)QShape<HD, NT>::SMEM_UNIT);
-  cudaFuncSetAttribute(q4_unit_kernel<HD, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                       (int)UShape<HD, NT>::SMEM);
 }
 
 }  // namespace
