@@ -64,7 +64,7 @@ __device__ __forceinline__ int join_lanes(uint32_t (&lo)[REGS], uint32_t (&hi)[R
 template <int HD, bool Q4>
 __global__ void __launch_bounds__(DG_THREADS, Q4 ? 6 : 4)
 digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __restrict__ slots,
-              const int32_t* __restrict__ pos0, int split, int32_t* __restrict__ status) {
+              const int32_t* __restrict__ pos0, uint32_t split, int32_t* __restrict__ status) {
   constexpr int ROW = Q4 ? HD / 2 : HD * 2, LANES = ROW / (Q4 ? 8 : 16), PER = 32 / LANES;  // bytes; lanes and rows of a load
   constexpr int REGS = Q4 ? 8 : 4, U = Q4 ? 8 : 16;
   constexpr int BIT = LANES == 16 ? 4 : LANES == 8 ? 3 : 2;
@@ -72,13 +72,11 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
   constexpr int KEPT = REGS >> (5 - BIT);
   grid_dep_begin();
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * DG_WARPS + (threadIdx.x >> 5);
-  const int y = (int)(w % split);
-  const long long unit = w / split;
-  const int h = (int)(unit % dg.n_kv_heads), layer = (int)(unit / dg.n_kv_heads % dg.n_layers);
-  const long long i_ = unit / dg.n_kv_heads / dg.n_layers;
-  if (i_ >= n) return;
-  const int i = (int)i_, slot = slots[i], p0 = pos0 != nullptr ? pos0[i] : 0;
+  // (32 bits: the host sees to it)
+  const uint32_t w = blockIdx.x * DG_WARPS + (threadIdx.x >> 5), unit = w / split, y = w - unit * split;
+  const uint32_t il = unit / dg.n_kv_heads, h = unit - il * dg.n_kv_heads, i = il / dg.n_layers, layer = il - i * dg.n_layers;
+  if (i >= (uint32_t)n) return;
+  const int slot = slots[i], p0 = pos0 != nullptr ? pos0[i] : 0;
   int st = 0, len = 0;
   if (slot < 0 || slot >= dg.n_slots)
     st |= SPEC_ST_SLOT;
@@ -94,12 +92,13 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
     if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_PAGE;
     if (lane == 0) status[i] = st;
   }
-  for (int64_t b = (int64_t)p0 / block + y; b < nb; b += split) {
-    const int in_page = (int)b % per, pg = row[(int)b / per];
+  for (uint32_t b = (uint32_t)p0 / block + y; b < (uint32_t)nb; b += split) {
+    const uint32_t e = b / per, in_page = b - e * per;
+    const int pg = row[e];
     if (pg < 0 || pg >= dg.n_pages) continue;
     const int64_t head = (int64_t)pg * dg.n_kv_heads + h;
     const int64_t r0 = (int64_t)layer * keys.layer_stride + head * dg.page_size + in_page * block;
-    const int rows = (int)min((int64_t)block, len - b * block);
+    const int rows = min(block, len - (int)b * block);
     uint32_t lo[REGS], hi[REGS];
 #pragma unroll
     for (int x = 0; x < REGS; x++) {
@@ -172,7 +171,7 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
 // two (the first head again in the places behind), so that the maximum over them is taken in
 // registers and by exchanges.
 // ---------------------------------------------------------------------------
-constexpr int SC_THREADS = 256, SC_WARPS = SC_THREADS / 32, SC_ROWS = 64;
+constexpr int SC_THREADS = 128, SC_WARPS = SC_THREADS / 32, SC_ROWS = 64;
 
 struct ScoreArgs {
   spec_digest dg;
@@ -206,8 +205,8 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
   grid_dep_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const spec_digest& dg = a.dg;
-  const int chunk = blockIdx.x % a.chunks, grp = blockIdx.x / a.chunks % a.groups;
-  const int h = blockIdx.x / a.chunks / a.groups % dg.n_kv_heads, s = blockIdx.x / a.chunks / a.groups / dg.n_kv_heads;
+  const int y = blockIdx.x / a.chunks, chunk = blockIdx.x - y * a.chunks, sh = y / a.groups, grp = y - sh * a.groups;
+  const int s = sh / dg.n_kv_heads, h = sh - s * dg.n_kv_heads;
   const int slot = a.slots[s], m = a.n_nodes != nullptr ? a.n_nodes[s] : a.nt;
   int st = 0, len = 0;
   if (slot < 0 || slot >= dg.n_slots)
@@ -222,7 +221,7 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
   if (chunk == 0 && grp == 0 && h == 0) {
     bool bad = false;
     if (st == 0)
-      for (int64_t e = tid; e * per < nb; e += SC_THREADS) bad |= row[e] < 0 || row[e] >= dg.n_pages;
+      for (int e = tid; e <= (nb - 1) / per && nb > 0; e += SC_THREADS) bad |= row[e] < 0 || row[e] >= dg.n_pages;
     if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
     if (tid == 0) a.status[s] = st;
     st &= ~SPEC_ST_PAGE;
@@ -357,8 +356,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   __shared__ int s_n, s_found[3];
   grid_dep_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t r = blockIdx.x;
-  const int h = (int)(r % a.nkv), node = (int)(r / a.nkv % a.nt), s = (int)(r / a.nkv / a.nt);
+  const int r = blockIdx.x, sn = r / a.nkv, h = r - sn * a.nkv, s = sn / a.nt, node = sn - s * a.nt;
   const int slot = a.slots[s], m = a.n_nodes != nullptr ? a.n_nodes[s] : a.nt;
   int st = 0, len = 0;
   if (slot < 0 || slot >= a.n_slots)
@@ -369,7 +367,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   const int nb = (int)(((int64_t)max(len, 0) + a.block - 1) / a.block);
   if (len < 0 || nb > a.ld) st |= SPEC_ST_FULL;
   if (h == 0 && node == 0 && tid == 0) a.status[s] = st;
-  int32_t* out = a.blocks + r * a.keep;
+  int32_t* out = a.blocks + (int64_t)r * a.keep;
   if ((st & SPEC_ST_TREE) == 0 && node >= m) return;
   const int k = st != 0 ? 0 : min(nb, a.keep);
   for (int j = k + tid; j < a.keep; j += THREADS) out[j] = -1;
@@ -379,7 +377,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   }
   // Of the blocks [a.first, nb - a.last) `need` are chosen, the others are.  A key is
   // never 0, which stands for no block.
-  const float* x = a.scores + r * a.ld;
+  const float* x = a.scores + (int64_t)r * a.ld;
   const int end = nb - a.last, need = k - a.first - a.last;
   auto to_key = [&](float f) -> uint32_t { return f != f ? 0xFF800000u : logit_key(f); };
   auto key_of = [&](int j) -> uint32_t { return j >= a.first && j < end ? to_key(x[j]) : 0u; };
@@ -637,7 +635,7 @@ int launch_digest(const spec_digest* dg, const Keys& keys, bool q4, int n, const
   if (slots == nullptr || status == nullptr) return fail(SPEC_E_INVALID, "null argument");
   if (n < 1) return fail(SPEC_E_SHAPE, "n >= 1 required");
   const double units = (double)n * dg->n_layers * dg->n_kv_heads;
-  if (units > INT32_MAX) return fail(SPEC_E_SHAPE, "n * n_layers * n_kv_heads too large");
+  if (units > (1 << 30)) return fail(SPEC_E_SHAPE, "n * n_layers * n_kv_heads too large");
   // warps of a unit: as many as keep the SMs full, when the blocks are many
   const int64_t most = (int64_t)dg->max_pages * (dg->page_size / dg->block);
   const int64_t fit = std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)(device_sms() * 64 / units)));
@@ -647,7 +645,7 @@ int launch_digest(const spec_digest* dg, const Keys& keys, bool q4, int n, const
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto kernel = dg->head_dim == 128 ? (q4 ? digest_kernel<128, true> : digest_kernel<128, false>)
                                     : (q4 ? digest_kernel<64, true> : digest_kernel<64, false>);
-  const cudaError_t e = launch_dependent(kernel, grid, DG_THREADS, 0, st, *dg, keys, n, slots, pos0, split, status);
+  const cudaError_t e = launch_dependent(kernel, grid, DG_THREADS, 0, st, *dg, keys, n, slots, pos0, (uint32_t)split, status);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("block digest: ") + cudaGetErrorString(e));
   return SPEC_OK;
 }
@@ -727,10 +725,10 @@ extern "C" int spec_block_scores(const spec_digest* dg, int layer, int n_seq, co
   a.GP = 1 << a.gp_shift;
   a.nodes = std::min(nt, SC_ROWS / a.GP);
   a.groups = (nt + a.nodes - 1) / a.nodes;
-  // a tile of 16 blocks a warp, until there are CTAs for four an SM
+  // a tile of 16 blocks a warp, until there are CTAs for eight an SM
   const int64_t most = std::min<int64_t>(ld, (int64_t)dg->max_pages * (dg->page_size / dg->block));
   const double units = (double)n_seq * dg->n_kv_heads * a.groups;
-  const int64_t fill = std::max<int64_t>(1, (int64_t)(4 * device_sms() / units));
+  const int64_t fill = std::max<int64_t>(1, (int64_t)(8 * device_sms() / units));
   a.chunks = (int)std::min<int64_t>((most + 16 * SC_WARPS - 1) / (16 * SC_WARPS), fill);
   if (units * a.chunks > INT32_MAX) return fail(SPEC_E_SHAPE, "n_seq * nt * n_kv_heads too large");
   const int tiles = (a.nodes * a.GP + 7) / 8;

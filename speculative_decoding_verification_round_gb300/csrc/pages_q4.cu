@@ -133,10 +133,10 @@ constexpr int CQ_ROWS = 32, CQ_FLIGHT = 2, PQ_WARPS = PQ_THREADS / 32;
 struct RowPlace {
   int64_t at[CQ_ROWS];
 };
-__device__ __forceinline__ void place_rows(const spec_pages_q4& kv, int layer, const int32_t* row, int64_t pos0, int r0,
-                                           int r1, RowPlace& p) {
+__device__ __forceinline__ void place_rows(const spec_pages_q4& kv, int layer, const int32_t* row, int pos0, int r0, int r1,
+                                           RowPlace& p) {
   for (int j = r0 + threadIdx.x; j < r1; j += PQ_THREADS) {
-    const int64_t pos = pos0 + j, e = pos / kv.page_size;
+    const int pos = pos0 + j, e = pos / kv.page_size;  // (below 2^31)
     p.at[j - r0] = ((int64_t)layer * kv.layer_stride + (int64_t)row[e] * kv.n_kv_heads * kv.page_size + pos -
                     e * kv.page_size) * (kv.head_dim / 32);
   }
