@@ -14,8 +14,9 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // digests: a warp per block, 16 bytes (of codes 8) a lane and load, several rows of the
-// block a load, up to 16 loads in flight; the lanes that hold the same channels are joined
-// at the end, each keeping the half of the registers that the other one gives away
+// block a load, the next eight loads (of the next block, too) in flight under the
+// comparisons; the lanes that hold the same channels are joined at the end, each keeping
+// the half of the registers that the other one gives away
 // ---------------------------------------------------------------------------
 constexpr int DG_THREADS = 128, DG_WARPS = DG_THREADS / 32;
 
@@ -62,11 +63,11 @@ __device__ __forceinline__ int join_lanes(uint32_t (&lo)[REGS], uint32_t (&hi)[R
 }
 
 template <int HD, bool Q4>
-__global__ void __launch_bounds__(DG_THREADS, Q4 ? 6 : 4)
+__global__ void __launch_bounds__(DG_THREADS, Q4 ? 5 : 4)
 digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __restrict__ slots,
               const int32_t* __restrict__ pos0, uint32_t split, int32_t* __restrict__ status) {
   constexpr int ROW = Q4 ? HD / 2 : HD * 2, LANES = ROW / (Q4 ? 8 : 16), PER = 32 / LANES;  // bytes; lanes and rows of a load
-  constexpr int REGS = Q4 ? 8 : 4, U = Q4 ? 8 : 16;
+  constexpr int REGS = Q4 ? 8 : 4, U = 8, ROWS = U * PER;  // rows in flight
   constexpr int BIT = LANES == 16 ? 4 : LANES == 8 ? 3 : 2;
   using Load = typename std::conditional<Q4, uint2, uint4>::type;
   constexpr int KEPT = REGS >> (5 - BIT);
@@ -92,52 +93,75 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
     if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_PAGE;
     if (lane == 0) status[i] = st;
   }
-  for (uint32_t b = (uint32_t)p0 / block + y; b < (uint32_t)nb; b += split) {
-    const uint32_t e = b / per, in_page = b - e * per;
-    const int pg = row[e];
-    if (pg < 0 || pg >= dg.n_pages) continue;
-    const int64_t head = (int64_t)pg * dg.n_kv_heads + h;
-    const int64_t r0 = (int64_t)layer * keys.layer_stride + head * dg.page_size + in_page * block;
-    const int rows = min(block, len - (int)b * block);
-    uint32_t lo[REGS], hi[REGS];
+  const uint32_t count = nb, l = lane % LANES;
+  auto page_of = [&](uint32_t b) { return b < count ? row[b / per] : -1; };
+  auto rows_of = [&](uint32_t b) { return min(block, len - (int)b * block); };
+  struct Part {
+    Load v[U];
+    uint32_t s[U];
+  };
+  // rows r0 ... r0 + ROWS - 1 of block b (a row again where it has no more: that changes nothing)
+  auto load = [&](uint32_t b, int pg, int r0, Part& p) {
+    if (b >= count || pg < 0 || pg >= dg.n_pages) return;
+    const int64_t first = (int64_t)layer * keys.layer_stride + ((int64_t)pg * dg.n_kv_heads + h) * dg.page_size + b % per * block;
+    const int last = rows_of(b) - 1;
+    const uint8_t* src = keys.rows + first * ROW + l * (uint32_t)sizeof(Load);
+    const __half* sc = Q4 ? keys.scales + first * (HD / 32) + l / 2 : nullptr;
 #pragma unroll
-    for (int x = 0; x < REGS; x++) {
-      lo[x] = 0x7C007C00u;
-      hi[x] = 0xFC00FC00u;
+    for (int u = 0; u < U; u++) {
+      const int at = min(r0 + u * PER + lane / LANES, last);
+      p.v[u] = __ldg(reinterpret_cast<const Load*>(src + at * ROW));
+      if (Q4) p.s[u] = __half_as_ushort(__ldg(sc + at * (HD / 32)));
     }
-    const uint8_t* src = keys.rows + r0 * ROW + (lane % LANES) * (int)sizeof(Load);
-    const __half* sc = Q4 ? keys.scales + r0 * (HD / 32) + lane % LANES / 2 : nullptr;
-    for (int r = 0; r < rows; r += PER * U) {
-      Load v[U];
-      uint32_t s[U];
+  };
+  uint32_t b = (uint32_t)p0 / block + y;
+  int pg = page_of(b), pg_next = page_of(b + split), r0 = 0;
+  Part now, next;
+  load(b, pg, 0, now);
+  uint32_t lo[REGS], hi[REGS];
+  while (b < count) {
+    const bool end = r0 + ROWS >= rows_of(b);
+    const uint32_t b1 = end ? b + split : b;
+    const int pg1 = end ? pg_next : pg, r1 = end ? 0 : r0 + ROWS;
+    load(b1, pg1, r1, next);
+    if (end) pg_next = page_of(b1 + split);
+    if (r0 == 0) {
 #pragma unroll
-      for (int u = 0; u < U; u++) {
-        if (u > 0 && r + u * PER >= rows) break;
-        const int at = min(r + u * PER + lane / LANES, rows - 1);  // (a row again changes nothing)
-        v[u] = __ldg(reinterpret_cast<const Load*>(src + at * ROW));
-        if (Q4) s[u] = __half_as_ushort(__ldg(sc + at * (HD / 32))) * 0x10001u;
-      }
-#pragma unroll
-      for (int u = 0; u < U; u++) {
-        if (u > 0 && r + u * PER >= rows) break;
-        uint32_t q[4] = {v[u].x, v[u].y, 0u, 0u};
-        if constexpr (!Q4) {
-          q[2] = v[u].z;
-          q[3] = v[u].w;
-        }
-#pragma unroll
-        for (int x = 0; x < REGS; x++) {
-          // codes: word x / 4; elements 0, 2 | 1, 3 | 16, 18 | 17, 19 of its four
-          const uint32_t val = !Q4 ? q[x % 4]
-                                   : kw_hmul2(x & 2 ? q4_high(q[x / 4] >> (x & 1 ? 8 : 0))
-                                                    : q4_low(q[x / 4] >> (x & 1 ? 8 : 0)), s[u]);
-          lo[x] = min2(lo[x], val);
-          hi[x] = max2(hi[x], val);
-        }
+      for (int x = 0; x < REGS; x++) {
+        lo[x] = 0x7C007C00u;
+        hi[x] = 0xFC00FC00u;
       }
     }
-    const int reg0 = join_lanes<REGS, BIT>(lo, hi), l = lane % LANES;
-    uint16_t* to = dg.data + (int64_t)layer * dg.layer_stride + (head * per + in_page) * (2 * HD);
+    const int many = rows_of(b) - r0;
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (u > 0 && u * PER >= many) break;
+      uint32_t q[4] = {now.v[u].x, now.v[u].y, 0u, 0u};
+      if constexpr (!Q4) {
+        q[2] = now.v[u].z;
+        q[3] = now.v[u].w;
+      }
+      const uint32_t s2 = now.s[u] * 0x10001u;
+#pragma unroll
+      for (int x = 0; x < REGS; x++) {
+        // codes: word x / 4; elements 0, 2 | 1, 3 | 16, 18 | 17, 19 of its four
+        const uint32_t val = !Q4 ? q[x % 4]
+                                 : kw_hmul2(x & 2 ? q4_high(q[x / 4] >> (x & 1 ? 8 : 0))
+                                                  : q4_low(q[x / 4] >> (x & 1 ? 8 : 0)), s2);
+        lo[x] = min2(lo[x], val);
+        hi[x] = max2(hi[x], val);
+      }
+    }
+    const uint32_t done = b;
+    const int page = pg;
+    now = next;
+    b = b1;
+    pg = pg1;
+    r0 = r1;
+    if (!end || page < 0 || page >= dg.n_pages) continue;
+    const int64_t head = (int64_t)page * dg.n_kv_heads + h;
+    const int reg0 = join_lanes<REGS, BIT>(lo, hi);
+    uint16_t* to = dg.data + (int64_t)layer * dg.layer_stride + (head * per + done % per) * (2 * HD);
     if (!Q4) {  // word l * 4 + reg of the row
 #pragma unroll
       for (int x = 0; x < KEPT; x++) {
@@ -171,7 +195,7 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
 // two (the first head again in the places behind), so that the maximum over them is taken in
 // registers and by exchanges.
 // ---------------------------------------------------------------------------
-constexpr int SC_THREADS = 128, SC_WARPS = SC_THREADS / 32, SC_ROWS = 64;
+constexpr int SC_THREADS = 256, SC_WARPS = SC_THREADS / 32, SC_ROWS = 64;
 
 struct ScoreArgs {
   spec_digest dg;
@@ -274,53 +298,66 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
   const int64_t out0 = (((int64_t)s * a.nt + node0) * dg.n_kv_heads + h) * a.ld, node_ld = (int64_t)dg.n_kv_heads * a.ld;
   for (int b0 = mine; b0 < nb; b0 += a.chunks * SC_WARPS * 16) {
     if (b0 != mine) load(b0);
-    float top[4];  // of a node with more than 8 heads
-    for (int n = 0; n < tiles; n++) {
-      float lo[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float top[2];  // of a node with more than 8 heads
+    auto put = [&](int node, int half, float value) {
+      const int b = b0 + 8 * half + g;
+      if (b < nb && node < nodes) a.scores[out0 + node * node_ld + b] = value;
+    };
+    for (int n0 = 0; n0 < tiles; n0 += 2) {  // two tiles' products, four sums, at a time
+      float sum[2][2][4];
+#pragma unroll
+      for (int z = 0; z < 2; z++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) sum[z][0][e] = sum[z][1][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < LOADS / 2; i++) {
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-          const uint32_t at = qs + ((n * STEPS + 2 * i + k) * 32 + lane) * 8;
-          const uint2 ql = kw_lds64(at), qh = kw_lds64(at + STEPS * 128);
           const uint4 &l0 = v[0][i], &l1 = v[1][i], &h0 = v[0][i + LOADS / 2], &h1 = v[1][i + LOADS / 2];
           const uint32_t al[4] = {k ? l0.z : l0.x, k ? l1.z : l1.x, k ? l0.w : l0.y, k ? l1.w : l1.y};
           const uint32_t ah[4] = {k ? h0.z : h0.x, k ? h1.z : h1.x, k ? h0.w : h0.y, k ? h1.w : h1.y};
-          mma_16816(lo, al, ql.x, ql.y);
-          mma_16816(hi, ah, qh.x, qh.y);
+#pragma unroll
+          for (int z = 0; z < 2; z++) {
+            // (the last of an odd number twice)
+            const uint32_t at = qs + ((min(n0 + z, tiles - 1) * STEPS + 2 * i + k) * 32 + lane) * 8;
+            const uint2 ql = kw_lds64(at), qh = kw_lds64(at + STEPS * 128);
+            mma_16816(sum[z][0], al, ql.x, ql.y);
+            mma_16816(sum[z][1], ah, qh.x, qh.y);
+          }
         }
       }
-      // (block g, rows 2t, 2t + 1), (block 8 + g, ...)
-      float x[4];
 #pragma unroll
-      for (int e = 0; e < 4; e++) x[e] = there[e >> 1] ? lo[e] + hi[e] : -INFINITY;
-      auto put = [&](int node, int half, float value) {
-        const int b = b0 + 8 * half + g;
-        if (b < nb && node < nodes) a.scores[out0 + node * node_ld + b] = value;
-      };
-      if (a.GP == 1) {
+      for (int z = 0; z < 2; z++) {
+        const int n = n0 + z;
+        if (n >= tiles) break;
+        // (block g, rows 2t, 2t + 1), (block 8 + g, ...)
+        float x[4];
 #pragma unroll
-        for (int e = 0; e < 4; e++) put(8 * n + 2 * t + (e & 1), e >> 1, x[e]);
-      } else {
-        float y[2] = {max_nan(x[0], x[1]), max_nan(x[2], x[3])};
-        if (a.GP >= 4)
+        for (int e = 0; e < 4; e++) x[e] = there[e >> 1] ? sum[z][0][e] + sum[z][1][e] : -INFINITY;
+        if (a.GP == 1) {
 #pragma unroll
-          for (int e = 0; e < 2; e++) y[e] = max_nan(y[e], __shfl_xor_sync(0xffffffffu, y[e], 1));
-        if (a.GP >= 8)
-#pragma unroll
-          for (int e = 0; e < 2; e++) y[e] = max_nan(y[e], __shfl_xor_sync(0xffffffffu, y[e], 2));
-        if (a.GP <= 8) {
-          const int shift = a.GP == 2 ? 0 : a.GP == 4 ? 1 : 2;  // lanes t of a node
-          if ((t & ((1 << shift) - 1)) == 0)
-#pragma unroll
-            for (int e = 0; e < 2; e++) put((8 >> (shift + 1)) * n + (t >> shift), e, y[e]);
+          for (int e = 0; e < 4; e++) put(8 * n + 2 * t + (e & 1), e >> 1, x[e]);
         } else {
-          const int part = n & (a.GP / 8 - 1);
+          float y[2] = {max_nan(x[0], x[1]), max_nan(x[2], x[3])};
+          if (a.GP >= 4)
 #pragma unroll
-          for (int e = 0; e < 2; e++) top[e] = part == 0 ? y[e] : max_nan(top[e], y[e]);
-          if (part == a.GP / 8 - 1 && t == 0)
+            for (int e = 0; e < 2; e++) y[e] = max_nan(y[e], __shfl_xor_sync(0xffffffffu, y[e], 1));
+          if (a.GP >= 8)
 #pragma unroll
-            for (int e = 0; e < 2; e++) put(n / (a.GP / 8), e, top[e]);
+            for (int e = 0; e < 2; e++) y[e] = max_nan(y[e], __shfl_xor_sync(0xffffffffu, y[e], 2));
+          if (a.GP <= 8) {
+            const int shift = a.gp_shift - 1;  // lanes t of a node
+            if ((t & ((1 << shift) - 1)) == 0)
+#pragma unroll
+              for (int e = 0; e < 2; e++) put((4 >> shift) * n + (t >> shift), e, y[e]);
+          } else {
+            const int part = n & (a.GP / 8 - 1);
+#pragma unroll
+            for (int e = 0; e < 2; e++) top[e] = part == 0 ? y[e] : max_nan(top[e], y[e]);
+            if (part == a.GP / 8 - 1 && t == 0)
+#pragma unroll
+              for (int e = 0; e < 2; e++) put(n >> (a.gp_shift - 3), e, top[e]);
+          }
         }
       }
     }
@@ -329,12 +366,13 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
 
 // ---------------------------------------------------------------------------
 // selection: a CTA per row, a row's keys (its scores as whole numbers in the same
-// order) in registers, four neighbours and THREADS * 4 behind the next four.  The
-// k-th largest key lies in a bin of a histogram of the eight highest bits in which the
-// row's keys differ; of the bin's keys, mostly a few dozen, each is ranked against the
-// others (192 x 8 rows of 2048: 15 us with the k-th key's bits found one by one
-// by counts).  The chosen blocks are marked in a bit map, whose words then are written
-// out in order.
+// order) in registers, neighbours in neighbouring lanes.  The k-th largest key lies in a
+// bin of a histogram of the ten highest bits in which the row's keys differ; of the
+// bin's keys, mostly a few, each is ranked against the others (192 x 8 rows of 2048: 15
+// us with the k-th key's bits found one by one by counts, 13 with eight bits, whose bins
+// most keys share, 11.8 so).  A warp's vote over
+// a key of each lane is a word of the map of the chosen blocks, whose words then are
+// written out in order, a thread one.
 // ---------------------------------------------------------------------------
 struct SelectArgs {
   const int32_t* len;
@@ -350,10 +388,12 @@ struct SelectArgs {
 
 template <int THREADS, int PER>
 __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
-  constexpr int WARPS = THREADS / 32, SPAN = THREADS * PER, CAND = 256;
-  __shared__ int s_sum[2][WARPS];
-  __shared__ uint32_t s_bits[SPAN / 32], s_mm[2][WARPS], s_hist[256], s_cand[CAND], s_key;
-  __shared__ int s_n, s_found[3];
+  constexpr int WARPS = THREADS / 32, SPAN = THREADS * PER, CAND = 256, WORDS = SPAN / 32;
+  constexpr int BIN_BITS = THREADS <= 64 ? 9 : 10, BINS = 1 << BIN_BITS, EACH = BINS / THREADS;
+  constexpr int HIST = BINS + BINS / 32;  // (a word more for each 32: a thread's bins are neighbours)
+  static_assert(WORDS <= THREADS && PER <= 32, "a word a thread, a lane for each of a thread's keys");
+  __shared__ int s_sum[2][WARPS], s_n, s_found[3];
+  __shared__ uint32_t s_bits[2][WORDS], s_mm[2][WARPS], s_hist[HIST], s_cand[CAND], s_key;
   grid_dep_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = blockIdx.x, sn = r / a.nkv, h = r - sn * a.nkv, s = sn / a.nt, node = sn - s * a.nt;
@@ -379,59 +419,67 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   // never 0, which stands for no block.
   const float* x = a.scores + (int64_t)r * a.ld;
   const int end = nb - a.last, need = k - a.first - a.last;
-  auto to_key = [&](float f) -> uint32_t { return f != f ? 0xFF800000u : logit_key(f); };
-  auto key_of = [&](int j) -> uint32_t { return j >= a.first && j < end ? to_key(x[j]) : 0u; };
-  const bool one = nb <= SPAN, vec = ((reinterpret_cast<uintptr_t>(x) & 15u) == 0);
+  const bool one = nb <= SPAN;
   uint32_t key[PER];
-  // block of key i of this thread, in the span from c0 on
-  auto block_of = [&](int c0, int i) { return c0 + (i >> 2) * (THREADS * 4) + tid * 4 + (i & 3); };
-  auto load = [&](int c0) {
+  auto load = [&](int c0) {  // key i: block c0 + i THREADS + tid
+    float f[PER];
 #pragma unroll
-    for (int i = 0; i < PER; i += 4) {
-      const int j = block_of(c0, i);
-      if (vec && j >= a.first && j + 3 < end) {
-        const float4 f = *reinterpret_cast<const float4*>(x + j);
-        key[i] = to_key(f.x);
-        key[i + 1] = to_key(f.y);
-        key[i + 2] = to_key(f.z);
-        key[i + 3] = to_key(f.w);
-      } else {
+    for (int i = 0; i < PER; i++) {
+      const int j = c0 + i * THREADS + tid;
+      f[i] = j >= a.first && j < end ? x[j] : 0.0f;
+    }
 #pragma unroll
-        for (int y = 0; y < 4; y++) key[i + y] = key_of(j + y);
-      }
+    for (int i = 0; i < PER; i++) {
+      const int j = c0 + i * THREADS + tid;
+      key[i] = j >= a.first && j < end ? (f[i] != f[i] ? 0xFF800000u : logit_key(f[i])) : 0u;
     }
   };
-  int which = 0;
-  auto count = [&](uint32_t t) {  // keys >= t
-    int c = 0;
-    if (one) {
-#pragma unroll
-      for (int i = 0; i < PER; i++) c += key[i] >= t;
-    } else {
-      for (int j = a.first + tid; j < end; j += THREADS) c += key_of(j) >= t;
-    }
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (WARPS > 1) {
-      if (lane == 0) s_sum[which][warp] = c;
-      __syncthreads();
-      c = lane < WARPS ? s_sum[which][lane] : 0;
-      c = __reduce_add_sync(0xffffffffu, c);
-      which ^= 1;
-    }
-    return c;
-  };
-  // f of every key but 0
+  // f of every key of the row but 0 (longer rows are read again for each use)
   auto each_key = [&](auto&& f) {
-    if (one) {
+    for (int c0 = 0; c0 < nb; c0 += SPAN) {
+      if (!one) load(c0);
 #pragma unroll
       for (int i = 0; i < PER; i++)
         if (key[i] != 0u) f(key[i]);
-    } else {
-      for (int j = a.first + tid; j < end; j += THREADS) f(key_of(j));
     }
   };
+  int which = 0;
+  auto count = [&](uint32_t t) {  // keys >= t > 0
+    int c = 0;
+    each_key([&](uint32_t y) { c += y >= t; });
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) s_sum[which][warp] = c;
+    __syncthreads();
+    c = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_sum[which][lane] : 0);
+    which ^= 1;
+    return c;
+  };
+  // exclusive sum over the CTA's threads; *all: the whole
+  auto scan = [&](int v, int* all) {
+    int at = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, at, off);
+      if (lane >= off) at += z;
+    }
+    int total = __shfl_sync(0xffffffffu, at, 31), before = at - v;
+    if (WARPS > 1) {
+      __syncthreads();
+      if (lane == 31) s_sum[0][warp] = at;
+      __syncthreads();
+      total = 0;
+#pragma unroll 4
+      for (int w = 0; w < WARPS; w++) {
+        const int c = s_sum[0][w];
+        if (w < warp) before += c;
+        total += c;
+      }
+    }
+    *all = total;
+    return before;
+  };
   load(0);
-  for (int b = tid; b < 256; b += THREADS) s_hist[b] = 0u;
+  for (int b = tid; b < HIST; b += THREADS) s_hist[b] = 0u;
   if (tid == 0) s_n = 0;
   // the bits that all keys have in common
   uint32_t lo = 0xFFFFFFFFu, hi = 0u;
@@ -446,44 +494,36 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
     s_mm[1][warp] = lo;
   }
   __syncthreads();
-  if (WARPS > 1) {
-    hi = __reduce_max_sync(0xffffffffu, lane < WARPS ? s_mm[0][lane] : 0u);
-    lo = __reduce_min_sync(0xffffffffu, lane < WARPS ? s_mm[1][lane] : 0xFFFFFFFFu);
-  }
+  hi = __reduce_max_sync(0xffffffffu, lane < WARPS ? s_mm[0][lane] : 0u);
+  lo = __reduce_min_sync(0xffffffffu, lane < WARPS ? s_mm[1][lane] : 0xFFFFFFFFu);
   // t: the largest number that `need` keys reach (above all keys if none is needed); reach: how
   // many do
   uint32_t t = need > 0 ? lo : 0xFFFFFFFFu;
   int reach = need > 0 ? end - a.first : 0;
   if (need > 0 && hi != lo) {
-    const int top = 31 - __clz((int)(hi ^ lo)), shift = max(0, top - 7);
+    const int top = 31 - __clz((int)(hi ^ lo)), shift = max(0, top - (BIN_BITS - 1));
     const uint32_t bins = 2u << (top - shift);
     t = hi & ~((2u << top) - 1u);
-    each_key([&](uint32_t y) { atomicAdd(&s_hist[(y >> shift) & (bins - 1u)], 1u); });
+    auto place = [](uint32_t b) { return b + (b >> 5); };
+    each_key([&](uint32_t y) { atomicAdd(&s_hist[place((y >> shift) & (bins - 1u))], 1u); });
     __syncthreads();
-    if (warp == 0) {  // eight bins a lane, from the highest on
-      int c[8], mine = 0;
+    // EACH bins a thread, from the highest on
+    int c[EACH], mine = 0, all;
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        c[i] = (int)s_hist[255 - 8 * lane - i];
-        mine += c[i];
-      }
-      int at = mine;
+    for (int i = 0; i < EACH; i++) {
+      c[i] = (int)s_hist[place(BINS - 1 - EACH * tid - i)];
+      mine += c[i];
+    }
+    int over = scan(mine, &all);
+    if (over < need && need <= over + mine) {
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, at, off);
-        if (lane >= off) at += z;
-      }
-      int above = at - mine;
-      if (above < need && need <= at) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          if (above < need && need <= above + c[i]) {
-            s_found[0] = 255 - 8 * lane - i;
-            s_found[1] = above;
-            s_found[2] = c[i];
-          }
-          above += c[i];
+      for (int i = 0; i < EACH; i++) {
+        if (over < need && need <= over + c[i]) {
+          s_found[0] = BINS - 1 - EACH * tid - i;
+          s_found[1] = over;
+          s_found[2] = c[i];
         }
+        over += c[i];
       }
     }
     __syncthreads();
@@ -525,86 +565,49 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   }
   // Where more reach it than are needed, the search has come to its end: t is a key, and
   // of the equal ones the lowest blocks are taken.
-  const int ties = reach > need ? need - count(t + 1u) : INT_MAX;
+  const int ties = reach > need ? need - count(t + 1u) : 0;
+  const bool tied = reach > need;
   int base = 0, ties_before = 0;
   for (int c0 = 0; c0 < nb; c0 += SPAN) {
-    if (c0 > 0) {
-      load(c0);
-      __syncthreads();  // the bit map has been read
+    if (!one) load(c0);
+    // a vote a key: blocks c0 + i THREADS + 32 warp ... + 31; lane i keeps the word
+    uint32_t word = 0u, equal = 0u;
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      const uint32_t v = __ballot_sync(0xffffffffu, need > 0 && key[i] >= t);
+      if (lane == i) word = v;
     }
+    if (tied)
 #pragma unroll
-    for (int i0 = 0; i0 < PER; i0 += 4) {
-      // ties in order: those of the threads in front, of the fours of a chunk
-      uint32_t mine = 0u;
-      int eq = 0;
-#pragma unroll
-      for (int y = 0; y < 4; y++) {
-        const int j = block_of(c0, i0 + y);
-        const uint32_t kk = key[i0 + y];
-        const bool in = j < nb && (j < a.first || j >= end || (need > 0 && kk >= t));
-        const bool tie = in && ties != INT_MAX && kk == t;
-        if (in && !tie) mine |= 1u << y;
-        if (tie) {
-          mine |= 16u << y;
-          eq++;
-        }
+      for (int i = 0; i < PER; i++) {
+        const uint32_t v = __ballot_sync(0xffffffffu, key[i] == t);
+        if (lane == i) equal = v;
       }
-      if (ties != INT_MAX) {
-        int before = eq;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int z = __shfl_up_sync(0xffffffffu, before, off);
-          if (lane >= off) before += z;
-        }
-        __syncthreads();
-        if (lane == 31) s_sum[0][warp] = before;
-        __syncthreads();
-        int all = 0;
-        before += ties_before - eq;
-        for (int w = 0; w < WARPS; w++) {
-          if (w < warp) before += s_sum[0][w];
-          all += s_sum[0][w];
-        }
-        ties_before += all;
-#pragma unroll
-        for (int y = 0; y < 4; y++)
-          if (mine >> (4 + y) & 1) {
-            if (before < ties) mine |= 1u << y;
-            before++;
-          }
-      }
-      // eight threads make a word of the map
-      uint32_t bits = (mine & 15u) << (4 * (lane & 7));
-#pragma unroll
-      for (int off = 1; off < 8; off <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, off);
-      if ((lane & 7) == 0) s_bits[(i0 * THREADS + tid * 4) / 32] = bits;
+    if (lane < PER) {
+      s_bits[0][lane * WARPS + warp] = word & ~equal;
+      s_bits[1][lane * WARPS + warp] = equal;
     }
     __syncthreads();
-    // the words in order, a thread one (SPAN / 32 <= THREADS)
-    static_assert(SPAN / 32 <= THREADS, "a word a thread");
-    uint32_t w = tid < SPAN / 32 ? s_bits[tid] : 0u;
-    const int c = __popc(w);
-    int at = c;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int z = __shfl_up_sync(0xffffffffu, at, off);
-      if (lane >= off) at += z;
+    uint32_t w = 0u;
+    if (tid < WORDS) {
+      w = s_bits[0][tid];
+      equal = s_bits[1][tid];
+      // the first and the last ones
+      const int j0 = c0 + 32 * tid;
+      auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+      w |= below(a.first - j0) | (below(nb - j0) & ~below(end - j0));
     }
-    if (WARPS > 1) {
-      if (lane == 31) s_sum[1][warp] = at;
-      __syncthreads();
+    int all;
+    if (tied) {
+      const int before = ties_before + scan(tid < WORDS ? __popc(equal) : 0, &all);
+      if (tid < WORDS)
+        for (int left = ties - before; left > 0 && equal != 0u; left--, equal &= equal - 1u) w |= equal & -equal;
+      ties_before += all;
     }
-    int all = at;
-    if (WARPS > 1) {
-      all = 0;
-      for (int x2 = 0; x2 < WARPS; x2++) {
-        if (x2 < warp) at += s_sum[1][x2];
-        all += s_sum[1][x2];
-      }
-    }
-    at += base - c;
+    int at = base + scan(__popc(w), &all);
     base += all;
     for (; w != 0u; w &= w - 1u) out[at++] = c0 + tid * 32 + __ffs(w) - 1;
+    __syncthreads();  // the map has been read
   }
 }
 
@@ -759,8 +762,9 @@ extern "C" int spec_block_select(const int32_t* len, int n_slots, int block, int
                         n_last, blocks, status};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t grid = (size_t)rows;
-  // 16 keys a thread, up to 16384 a row (longer ones are read again for every bit); scores
-  // past a row's last block cost threads without keys, so the class goes by ld
+  // 16 keys a thread (1536 rows of 2048: 11.8 us, with 32 12.0, with 64 17.3, with 8 12.7), up to
+  // 16384 a row (longer ones are read again for each use); the host knows no row's length,
+  // but no row has more blocks than ld
   const cudaError_t e = ld <= 512    ? launch_dependent(select_kernel<32, 16>, grid, 32, 0, st, a)
                         : ld <= 1024 ? launch_dependent(select_kernel<64, 16>, grid, 64, 0, st, a)
                         : ld <= 2048 ? launch_dependent(select_kernel<128, 16>, grid, 128, 0, st, a)
