@@ -199,7 +199,7 @@ __global__ void __launch_bounds__((BShape<HD, NT, Q4>::THREADS)) block_attn_kern
   __syncthreads();
   KW kw;
   kw.begin();
-  const int gk = Q4 ? key_row(kw.g) : kw.g;
+  const int gk = kw.g;
   const float scale = fabsf(a.scale_log2);
   int stage = 0;
   for (int u = gw; u < steps; u += warps) {

@@ -6,14 +6,15 @@
 // fill a tile of 8 instead of half of one of 16.  What the layout of the
 // fragments asks of K, V and Q is met by choosing the order of the dimensions
 // and keys, which no sum depends on:
-//   4-bit K  lane (g, t) takes the word t of each block of 32 elements of its
-//            keys: a nibble by itself is a (subnormal) fp16 number u 2^-24, so
-//            that four masks and three shifts give eight elements of the
-//            operand.  u = q + 8: the accumulator starts at -8 2^-24 sum q of the
-//            block, and the block's scale multiplies it in fp32.
-//   4-bit V  lane (g, t) takes the 16 (64 dimensions: 8) elements g of the keys t,
-//            t + 4, t + 8, t + 12, pairs of keys in one register: the number
-//            1024 + u by its bits, minus 1032, times the pair's scales, both
+//   4-bit K  lane (g, t) takes the word t of each block of 32 elements of its keys: a
+//            nibble by itself is a (subnormal) fp16 number, u 2^-24 or, four bits
+//            higher, u 2^-20, so that four masks and a shift give eight elements of the
+//            operand.  Both kinds have a sum of their own; u = q + 8: the first one
+//            starts at -8 2^-24 sum q of the block, and the block's scale multiplies
+//            them in fp32.
+//   4-bit V  ldmatrix turns 16 bits, four elements, of eight keys to pairs of keys:
+//            lane (g, t) has elements 2g, 2g + 1, 16 + 2g, 17 + 2g of each block of keys 2t, 2t + 1.
+//            The number 1024 + u by its bits, minus 1032, times the pair's scales, both
 //            exact in fp16 (a scale has eight significant bits, u - 8 three).
 // A row's elements so belong to the accumulator tiles in another order than in
 // fp16 (dim_of).
@@ -130,15 +131,11 @@ __device__ __forceinline__ uint32_t q4_high(uint32_t x) {  // (1024 + 16 u) / 16
 __device__ __forceinline__ bool odd_half(uint32_t v) { return (v & 0x7C00u) == 0x7C00u; }  // infinite or NaN
 __device__ __forceinline__ bool odd_pair(uint32_t v) { return odd_half(v) || odd_half(v >> 16); }
 
-// The row of a group of eight that holds the group's key k: its even keys in
-// front, so that the four of one load lie in different banks.
-__device__ __forceinline__ int key_row(int k) { return (k >> 1 & 3) | (k & 1) << 2; }
-
-// A row of codes: HD / 2 bytes, 16-byte chunk c of row r at c ^ q4_swz(r).  (Rows 8 on have
-// the same one, rows 4 on its lowest bit turned.)
+// A row of codes: HD / 2 bytes, 16-byte chunk c of row r at c ^ q4_swz(r), so that a chunk
+// of eight rows, read as words or by ldmatrix, lies in all banks.
 template <int HD>
 __device__ __forceinline__ int q4_swz(int r) {
-  return HD == 128 ? (r & 2) | (r >> 2 & 1) : r >> 2 & 1;
+  return HD == 128 ? r >> 1 & 3 : r >> 2 & 1;
 }
 // A row of fp16: HD * 2 bytes, 16-byte unit u of row r at u ^ (r & 7).
 template <int HD>
@@ -172,9 +169,7 @@ struct KeyWarp {
 
   // The dimension of accumulator tile m's row `half` (0: g, 1: g + 8).
   __device__ __forceinline__ int dim_of(int m, int half) const {
-    if (!Q4) return 16 * m + 8 * half + g;
-    if (HD == 128) return 32 * (g >> 1) + 8 * (g & 1) + m + 16 * half;
-    return 32 * (g >> 2) + 4 * (g & 3) + m + 16 * half;
+    return Q4 ? 32 * (m >> 1) + 16 * half + 2 * g + (m & 1) : 16 * m + 8 * half + g;
   }
 
   // Query fragments: entry e of (step, n, lane), row(r): row r's data or null.
@@ -220,12 +215,12 @@ struct KeyWarp {
   }
 
   // x = 2^-24 K Q^T of KT tiles of 16 rows of codes at `ks` (their scales at `ss`).
-  // Lane (g, t): keys key_row(g) and 8 + of each tile, rows 2t, 2t + 1 of each n.
+  // Lane (g, t): keys g and g + 8 of each tile, rows 2t, 2t + 1 of each n.
   template <int KT>
   __device__ __forceinline__ void scores_q4(uint32_t ks, uint32_t ss, uint32_t qs, uint32_t sums,
                                             float (&x)[KT][NT][4]) const {
-    const int lane = g * 4 + t, kr = key_row(g);
-    const uint32_t k0 = ks + kr * (HD / 2) + 4 * t + (q4_swz<HD>(kr) << 4), s0 = ss + kr * (HD / 16);
+    const int lane = g * 4 + t;
+    const uint32_t k0 = ks + g * (HD / 2) + 4 * t + (q4_swz<HD>(g) << 4), s0 = ss + g * (HD / 16);
     uint32_t sc[KT][2][BLOCKS / 2];
 #pragma unroll
     for (int i = 0; i < KT; i++)
@@ -248,30 +243,28 @@ struct KeyWarp {
       for (int i = 0; i < KT; i++)
 #pragma unroll
         for (int h = 0; h < 2; h++) w[i][h] = kw_lds32(kb + (16 * i + 8 * h) * (HD / 2));
-      float acc[KT][NT][4];
+      float low[KT][NT][4], high[KT][NT][4];  // of elements 0-15 and of 16-31, these 16 times
+      uint32_t al[KT][4], ah[KT][4];
 #pragma unroll
-      for (int half = 0; half < 2; half++) {
-        uint32_t a[KT][4];
+      for (int i = 0; i < KT; i++)
 #pragma unroll
-        for (int i = 0; i < KT; i++)
+        for (int h = 0; h < 2; h++) {
+          const uint32_t v = w[i][h] >> 8;
+          al[i][h] = w[i][h] & 0x000F000Fu;
+          al[i][2 + h] = v & 0x000F000Fu;
+          ah[i][h] = w[i][h] & 0x00F000F0u;
+          ah[i][2 + h] = v & 0x00F000F0u;
+        }
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const uint32_t v = half ? w[i][h] >> 4 : w[i][h];
-            a[i][h] = v & 0x000F000Fu;
-            a[i][2 + h] = (v >> 8) & 0x000F000Fu;
-          }
+      for (int n = 0; n < NT; n++) {
+        const uint2 ql = kw_lds64(qs + ((2 * b * NT + n) * 32 + lane) * 8);
+        const uint2 qh = kw_lds64(qs + (((2 * b + 1) * NT + n) * 32 + lane) * 8);
+        const uint4 cc = kw_lds128(sums + ((b * NT + n) * 4 + t) * 16);
+        const float c[4] = {__uint_as_float(cc.x), __uint_as_float(cc.y), __uint_as_float(cc.z), __uint_as_float(cc.w)};
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-          const uint2 q = kw_lds64(qs + (((2 * b + half) * NT + n) * 32 + lane) * 8);
-          if (half == 0) {
-            const uint4 cc = kw_lds128(sums + ((b * NT + n) * 4 + t) * 16);
-            const float c[4] = {__uint_as_float(cc.x), __uint_as_float(cc.y), __uint_as_float(cc.z), __uint_as_float(cc.w)};
-#pragma unroll
-            for (int i = 0; i < KT; i++) mma_16816_c(acc[i][n], a[i], q.x, q.y, c);
-          } else {
-#pragma unroll
-            for (int i = 0; i < KT; i++) mma_16816(acc[i][n], a[i], q.x, q.y);
-          }
+        for (int i = 0; i < KT; i++) {
+          mma_16816_c(low[i][n], al[i], ql.x, ql.y, c);
+          mma_16816_zero(high[i][n], ah[i], qh.x, qh.y);
         }
       }
 #pragma unroll
@@ -282,19 +275,21 @@ struct KeyWarp {
 #pragma unroll
           for (int n = 0; n < NT; n++) {
             float* y = &x[i][n][2 * h];
-            const float* z = &acc[i][n][2 * h];
+            const float* l = &low[i][n][2 * h];
+            const float* u = &high[i][n][2 * h];
+            float z0, z1;
+            kw_fma2(z0, z1, u[0], u[1], 0.0625f, 0.0625f, l[0], l[1]);
             if (b == 0)
-              kw_mul2(y[0], y[1], z[0], z[1], s, s);
+              kw_mul2(y[0], y[1], z0, z1, s, s);
             else
-              kw_fma2(y[0], y[1], z[0], z[1], s, s, y[0], y[1]);
+              kw_fma2(y[0], y[1], z0, z1, s, s, y[0], y[1]);
           }
         }
     }
   }
   static constexpr float CODE_UNIT = 0x1p24f;  // of these scores
 
-  // K Q^T of one tile of 16 fp16 rows.  Keys in the order of the rows (not Q4) or
-  // in the codes' (Q4).
+  // K Q^T of one tile of 16 fp16 rows.
   __device__ __forceinline__ void scores_f16(uint32_t ks, uint32_t qs, float (&x)[NT][4]) const {
     const int lane = g * 4 + t;
 #pragma unroll
@@ -303,7 +298,7 @@ struct KeyWarp {
       if (Q4) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          const int r = 8 * h + key_row(g);
+          const int r = 8 * h + g;
           const uint2 v = kw_lds64(ks + f16_off<HD>(r, 2 * step + (t >> 1)) + 8 * (t & 1));
           a[h] = __byte_perm(v.x, v.y, 0x5410);
           a[2 + h] = __byte_perm(v.x, v.y, 0x7632);
@@ -401,36 +396,41 @@ struct KeyWarp {
 
   // O += P V of one tile of 16 rows of codes at `vs`, scales at `ss`.
   __device__ __forceinline__ void values_q4(uint32_t vs, uint32_t ss, const float (&p)[NT][4]) {
-    constexpr int WORDS = HD / 64;
     uint32_t hi[NT][2], lo[NT][2];
     split(p, hi, lo);
-    uint32_t w[4][WORDS], s[4];  // keys t, t + 4, t + 8, t + 12
-    const int block = HD == 128 ? g >> 1 : g >> 2;
-    const uint32_t v0 = vs + t * (HD / 2) + ((block ^ q4_swz<HD>(t)) << 4) + (HD == 128 ? 8 * (g & 1) : 4 * (g & 3)),
-                   s00 = ss + t * (HD / 16) + 2 * block;
+    // the scales of keys 2t, 2t + 1 | 2t + 8, 2t + 9 of each block
+    uint32_t s[BLOCKS][2];
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const uint32_t at = (k & 1 ? v0 ^ 16u : v0) + 4 * k * (HD / 2);
+    for (int h = 0; h < 2; h++) {
+      const uint32_t at = ss + (2 * t + 8 * h) * (HD / 16);
+      uint32_t a[2], b[2];
       if (HD == 128) {
-        const uint2 v = kw_lds64(at);
-        w[k][0] = v.x;
-        w[k][WORDS - 1] = v.y;
+        const uint4 v = kw_lds128(at);  // both keys'
+        a[0] = v.x, a[1] = v.y, b[0] = v.z, b[1] = v.w;
       } else {
-        w[k][0] = kw_lds32(at);
+        const uint2 v = kw_lds64(at);
+        a[0] = v.x, b[0] = v.y;
       }
-      s[k] = kw_lds16(s00 + 4 * k * (HD / 16));
+#pragma unroll
+      for (int x = 0; x < BLOCKS; x++) s[x][h] = __byte_perm(a[x >> 1], b[x >> 1], x & 1 ? 0x7632 : 0x5410);
     }
-    const uint32_t s0 = s[0] | s[1] << 16, s1 = s[2] | s[3] << 16;
+    const int lane = g * 4 + t, key = lane & 15;
+    const uint32_t v0 = vs + key * (HD / 2) + (((lane >> 4) ^ q4_swz<HD>(key)) << 4);
 #pragma unroll
-    for (int j = 0; j < WORDS; j++)
+    for (int c = 0; c < BLOCKS; c += 2) {
+      uint32_t w[4];  // blocks c, c + 1 of keys 0-7 and 8-15
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(v0 ^ (c << 4)));
 #pragma unroll
-      for (int i = 0; i < 4; i++) {  // a byte: elements i and 16 + i of the word's
-        const uint32_t sel = i | i << 4 | (4 + i) << 8 | (4 + i) << 12;
-        const uint32_t x0 = __byte_perm(w[0][j], w[1][j], sel), x1 = __byte_perm(w[2][j], w[3][j], sel);
-        const uint32_t a[4] = {kw_hmul2(q4_low(x0), s0), kw_hmul2(q4_high(x0), s0), kw_hmul2(q4_low(x1), s1),
-                               kw_hmul2(q4_high(x1), s1)};
-        add(4 * j + i, a, hi, lo);
-      }
+      for (int b = 0; b < 2; b++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          const uint32_t x0 = j ? w[2 * b] >> 8 : w[2 * b], x1 = j ? w[2 * b + 1] >> 8 : w[2 * b + 1];
+          const uint32_t a[4] = {kw_hmul2(q4_low(x0), s[c + b][0]), kw_hmul2(q4_high(x0), s[c + b][0]),
+                                 kw_hmul2(q4_low(x1), s[c + b][1]), kw_hmul2(q4_high(x1), s[c + b][1])};
+          add(2 * (c + b) + j, a, hi, lo);
+        }
+    }
   }
 
   // The same of 16 fp16 rows.
@@ -448,34 +448,22 @@ struct KeyWarp {
         add(m, a, hi, lo);
       }
     } else {
-      // this lane's dimensions: MTILES neighbours, and those 16 behind
-      const int d0 = dim_of(0, 0);
-      uint32_t v[4][2][MTILES / 2];
+      // elements 2g, 2g + 1 of each half of a block
 #pragma unroll
-      for (int k = 0; k < 4; k++)
+      for (int b = 0; b < BLOCKS; b++) {
+        uint32_t v[4][2];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const uint32_t at = vs + f16_off<HD>(t + 4 * k, (d0 + 16 * h) >> 3) + 2 * (d0 & 7);
-          if (HD == 128) {
-            const uint4 x = kw_lds128(at);
-            v[k][h][0] = x.x;
-            v[k][h][1] = x.y;
-            v[k][h][MTILES / 2 - 2] = x.z;
-            v[k][h][MTILES / 2 - 1] = x.w;
-          } else {
-            const uint2 x = kw_lds64(at);
-            v[k][h][0] = x.x;
-            v[k][h][1] = x.y;
-          }
+        for (int k = 0; k < 4; k++)
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+            v[k][h] = kw_lds32(vs + f16_off<HD>(2 * t + (k & 1) + 8 * (k >> 1), 4 * b + 2 * h + (g >> 2)) + 4 * (g & 3));
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          const uint32_t sel = j ? 0x7632 : 0x5410;
+          const uint32_t a[4] = {__byte_perm(v[0][0], v[1][0], sel), __byte_perm(v[0][1], v[1][1], sel),
+                                 __byte_perm(v[2][0], v[3][0], sel), __byte_perm(v[2][1], v[3][1], sel)};
+          add(2 * b + j, a, hi, lo);
         }
-#pragma unroll
-      for (int m = 0; m < MTILES; m++) {
-        const uint32_t sel = m & 1 ? 0x7632 : 0x5410;
-        const uint32_t a[4] = {__byte_perm(v[0][0][m >> 1], v[1][0][m >> 1], sel),
-                               __byte_perm(v[0][1][m >> 1], v[1][1][m >> 1], sel),
-                               __byte_perm(v[2][0][m >> 1], v[3][0][m >> 1], sel),
-                               __byte_perm(v[2][1][m >> 1], v[3][1][m >> 1], sel)};
-        add(m, a, hi, lo);
       }
     }
   }
@@ -486,7 +474,7 @@ struct KeyWarp {
   __device__ __forceinline__ void values_slow(const float (&p)[NT][4], F&& value) {
 #pragma unroll 1
     for (int k = 0; k < 16; k++) {
-      const int src = (k & 7) << 2 | t, r = (k & 8) + key_row(k & 7);
+      const int src = (k & 7) << 2 | t;
       float pr[NT][2];
       bool any = false;
 #pragma unroll
@@ -502,7 +490,7 @@ struct KeyWarp {
       for (int m = 0; m < MTILES; m++)
 #pragma unroll
         for (int half = 0; half < 2; half++) {
-          const float v = value(r, dim_of(m, half));
+          const float v = value(k, dim_of(m, half));
 #pragma unroll
           for (int n = 0; n < NT; n++)
 #pragma unroll

@@ -48,7 +48,7 @@ struct UnitRows {
   const TreeArgs& a;
   const TreeSmem& tree;
   int len, row0, M;
-  // bits of the keys (key_row(g), 8 + key_row(g), ...) of 32 positions from `base` on that row r
+  // bits of the keys (g, 8 + g, ...) of 32 positions from `base` on that row r
   // sees, or of 16 nodes from `base` on
   __device__ __forceinline__ uint32_t visible(bool nodes, int base, int r, int gk) const {
     const int m = row0 + r, node = m < M ? node_of(a, m) : 0;
@@ -82,7 +82,7 @@ __device__ __forceinline__ void step_codes(KeyWarp<HD, NT, true>& kw, const Unit
   using Sh = QShape<HD, NT>;
   constexpr int KT = NT == 4 ? 1 : 2;  // tiles of 16 keys at a time
   const uint32_t vs = ks + Sh::CODES, kss = vs + Sh::CODES, vss = kss + Sh::SCALES;
-  const int lane = threadIdx.x & 31, gk = key_row(kw.g);
+  const int lane = threadIdx.x & 31, gk = kw.g;
   bool odd = false;
   if (masked)  // this lane's position's scales
 #pragma unroll
@@ -125,7 +125,7 @@ __device__ __forceinline__ void step_codes(KeyWarp<HD, NT, true>& kw, const Unit
 template <int HD, int NT>
 __device__ __forceinline__ void step_nodes(KeyWarp<HD, NT, true>& kw, const UnitRows<HD, NT>& rows, uint32_t ks,
                                            uint32_t vs, uint32_t qs, float scale, int node0) {
-  const int lane = threadIdx.x & 31, gk = key_row(kw.g);
+  const int lane = threadIdx.x & 31, gk = kw.g;
   float x[1][NT][4];
   kw.scores_f16(ks, qs, x[0]);
 #pragma unroll
