@@ -165,6 +165,10 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
                  int32_t* __restrict__ new_len, int blocks, int32_t* __restrict__ status) {
   __shared__ RowPlace place;
   __shared__ int s_node[CQ_ROWS];
+  // (No early launch of what follows: its waiting CTAs would take the room of the next ones here,
+  // 20.4 us for 8 entries' commit and read instead of 16.4; without programmatic
+  // launches 20.6.)
+  grid_dep_wait();
   const int i = blockIdx.x / (kv.n_layers * blocks);
   const int layer = blockIdx.x / blocks % kv.n_layers, blk = blockIdx.x % blocks;
   const int slot = slots[i], np = n_path[i];
@@ -242,6 +246,7 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
 // The lengths advanced in place, after every CTA of the commit has read them.
 __global__ void q4_advance_kernel(int n, const int32_t* __restrict__ slots, const int32_t* __restrict__ n_path,
                                   int32_t* len, const int32_t* __restrict__ status) {
+  grid_dep_wait();
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i < n && status[i] == 0) len[slots[i]] += n_path[i];
 }
@@ -270,6 +275,7 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
                const int32_t* __restrict__ n_pos, uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                int64_t layer_stride, int blocks, int32_t* __restrict__ status) {
   __shared__ RowPlace place;
+  grid_dep_wait();
   const int i = blockIdx.x / (kv.n_layers * blocks);
   const int layer = blockIdx.x / blocks % kv.n_layers, blk = blockIdx.x % blocks;
   const int slot = slots[i], np = n_pos[i], p0 = pos0[i];
@@ -415,8 +421,7 @@ int check_list(const void* a, const void* status, int n) {
   if (n < 1) return fail(SPEC_E_SHAPE, "n >= 1 required");
   return SPEC_OK;
 }
-int launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+int launched(const char* what, cudaError_t e) {
   return e == cudaSuccess ? SPEC_OK : fail(SPEC_E_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 // Rows of fp16 in or out beside the cache.
@@ -483,7 +488,7 @@ extern "C" int spec_pages_q4_copy(const spec_pages_q4* kv, int n, const int32_t*
   if (grid > INT32_MAX) return fail(SPEC_E_SHAPE, "n * n_layers * page too large");
   q4_copy_kernel<<<(unsigned)grid, PQ_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(*kv, n, src, dst, n_pos, c,
                                                                                           status);
-  return launched("4-bit page copy");
+  return launched("4-bit page copy", cudaGetLastError());
 }
 
 extern "C" int spec_pages_q4_fork(const spec_pages_q4* kv, int n, const int32_t* src, const int32_t* dst,
@@ -515,8 +520,7 @@ extern "C" int spec_pages_q4_extend(const spec_pages_q4* kv, int n, const int32_
   if (rc != SPEC_OK) return rc;
   const cudaError_t e = launch_dependent(q4_cow_kernel, (size_t)n * kv->n_layers * c.per_layer(), PQ_THREADS, 0, st,
                                          *kv, slots, (const int32_t*)copies, c);
-  if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("4-bit page extend: ") + cudaGetErrorString(e));
-  return SPEC_OK;
+  return launched("4-bit page extend", e);
 }
 
 extern "C" int spec_pages_q4_commit(const spec_pages_q4* kv, int n, const int32_t* slots, int nt,
@@ -536,11 +540,13 @@ extern "C" int spec_pages_q4_commit(const spec_pages_q4* kv, int n, const int32_
   const bool in_place = new_len == nullptr || a == b;
   if (!in_place && a < b + bytes && b < a + bytes)
     return fail(SPEC_E_INVALID, "new_len overlaps len without being len");
-  q4_commit_kernel<<<(unsigned)(n * kv->n_layers * blocks), PQ_THREADS, 0, st>>>(
-      *kv, n, slots, nt, k_new, v_new, new_layer_stride, path, n_path, in_place ? nullptr : new_len, blocks, status);
-  if (in_place)
-    q4_advance_kernel<<<(n + 127) / 128, 128, 0, st>>>(n, slots, n_path, kv->len, status);
-  return launched("4-bit page commit");
+  cudaError_t e = launch_dependent(q4_commit_kernel, (size_t)n * kv->n_layers * blocks, PQ_THREADS, 0, st, *kv, n, slots,
+                                   nt, k_new, v_new, new_layer_stride, path, n_path, in_place ? nullptr : new_len, blocks,
+                                   status);
+  if (e == cudaSuccess && in_place)
+    e = launch_dependent(q4_advance_kernel, (size_t)(n + 127) / 128, 128, 0, st, n, slots, n_path, kv->len,
+                         (const int32_t*)status);
+  return launched("4-bit page commit", e);
 }
 
 extern "C" int spec_pages_q4_read(const spec_pages_q4* kv, int n, const int32_t* slots, int nt, const int32_t* pos0,
@@ -552,7 +558,8 @@ extern "C" int spec_pages_q4_read(const spec_pages_q4* kv, int n, const int32_t*
   if (rc == SPEC_OK) rc = check_rows(kv, n, nt, k, v, &layer_stride);
   if (rc != SPEC_OK) return rc;
   const int blocks = (nt + CQ_ROWS - 1) / CQ_ROWS;
-  q4_read_kernel<<<(unsigned)(n * kv->n_layers * blocks), PQ_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      *kv, slots, nt, pos0, n_pos, k, v, layer_stride, blocks, status);
-  return launched("4-bit page read");
+  return launched("4-bit page read",
+                  launch_dependent(q4_read_kernel, (size_t)n * kv->n_layers * blocks, PQ_THREADS, 0,
+                                   reinterpret_cast<cudaStream_t>(stream), *kv, slots, nt, pos0, n_pos, k, v,
+                                   layer_stride, blocks, status));
 }
