@@ -705,7 +705,8 @@ typedef struct {
 } spec_pages_q4;
 
 /* spec_pages_copy, _fork, _extend and _free for a cache in 4 bits: the same
- * arguments, rules and status bits. */
+ * arguments, rules and status bits.  (A page's digests, below, are not copied with
+ * it.) */
 int spec_pages_q4_copy(const spec_pages_q4* kv, int n, const int32_t* src, const int32_t* dst,
                        const int32_t* n_pos, int32_t* status, void* stream);
 int spec_pages_q4_fork(const spec_pages_q4* kv, int n, const int32_t* src, const int32_t* dst,
@@ -744,8 +745,10 @@ int spec_pages_q4_read(const spec_pages_q4* kv, int n, const int32_t* slots, int
                        int64_t layer_stride, int32_t* status, void* stream);
 
 /* spec_tree_attn over a cache in 4 bits: the same arguments and rules.  The
- * trees' own keys and values, q and out are fp16.  Keys are multiplied as they
- * are, code by code, with the scale in fp32; values as fp16. */
+ * trees' own keys and values, q and out are fp16.  With up to 32 query rows a kv
+ * head (nodes x query heads of it) keys are multiplied as they are, code by code,
+ * with the scale in fp32, and values as fp16; with more, both as fp16 (and
+ * spec_tree_set_wait_budget holds). */
 int spec_tree_attn_q4(const spec_pages_q4* kv, int layer, const spec_tree* t, const uint16_t* q,
                       int64_t q_stride, const uint16_t* k_new, const uint16_t* v_new,
                       int64_t kv_stride, uint16_t* out, void* workspace, size_t workspace_bytes,
@@ -775,8 +778,8 @@ typedef struct {
  * every layer, from all committed positions of these blocks (device int32 [n];
  * pos0 NULL: from 0 on; the last block may be filled partly).  After a commit pos0 is the length in
  * front of it; after an extension with a copy of a page it is the start of that
- * page.  A NaN among a channel's keys makes both of its values NaN.  `kv` has the digest's sizes
- * (its table and len are not looked at).  Slots may be named more than once.
+ * page.  A NaN among a channel's keys makes both of its values NaN.  `kv` has the
+ * digest's sizes and a layer stride of whole rows (its table and len are not looked at).  Slots may be named more than once.
  * status: SPEC_ST_SLOT (slot out of range), SPEC_ST_FULL (pos0 below 0, or a length that the table cannot
  * have), SPEC_ST_PAGE (no valid page for some block; the others are done). */
 int spec_block_digest(const spec_digest* dg, const spec_pages* kv, int n, const int32_t* slots,
@@ -789,7 +792,8 @@ int spec_block_digest_q4(const spec_digest* dg, const spec_pages_q4* kv, int n, 
  * kv head's query heads,
  *   scores[s][i][h][j] = max over the heads g of h: sum_d max(q_gd lo_jd, q_gd hi_jd)
  * (without the softmax's scale; fp32 sums), for the blocks j that hold positions
- * [0, len).
+ * [0, len).  An infinite or NaN digest or query makes the scores that it has a part in
+ * infinite or NaN.  For a negative softmax scale, pass -q.
  *   slots, n_nodes  as in spec_tree; at most 64 query heads a kv head
  *   q       fp16 as in spec_tree_attn
  *   scores  fp32 [n_seq][nt][n_kv_heads][ld]; what no block stands for, and rows of nodes >=
@@ -827,6 +831,8 @@ int spec_block_select(const int32_t* len, int n_slots, int block, int n_seq, con
  *           SPEC_ST_BLOCK for a block outside [0, len); the query heads of such a row are NaN.
  *           Rows of nodes >= n_nodes of status and out are left as they were (bad counts: all
  *           nt rows are NaN with SPEC_ST_TREE)
+ * An infinite or NaN value in a row that a node sees makes its result infinite or NaN in that
+ * channel; rows past len, and those of blocks on no list, may hold anything.
  * out overlaps none of the inputs.  A row's bits do not depend on the call's other rows, but
  * they may on how many there are. */
 int spec_block_attn(const spec_pages* kv, int layer, const spec_tree* t, int block, int n_keep,

@@ -752,6 +752,18 @@ def _one_device(first, others):
     return device if all(t is None or t.is_cuda or t.is_pinned() for t in (first, *(t for t, _ in others))) else -2
 
 
+def _struct(x, kinds, device=None):
+    """The struct of a cache or digest of one of `kinds` (another's has other
+    fields), for a call on `device`."""
+    if not isinstance(x, kinds):
+        names = " or ".join(k.__name__ for k in (kinds if isinstance(kinds, tuple) else (kinds,)))
+        raise TypeError(f"{type(x).__name__}: {names} is required")
+    if device is not None and x.device not in (device, -1):
+        raise ValueError("pages on another device than the current one" if x.device >= 0 else
+                         "pages in host memory that is not pinned")
+    return x.ref if isinstance(x, KVPages) else x._ref
+
+
 class KVPagesQ4:
     """A paged KV cache in 4 bits (spec_pages_q4) over the caller's tensors,
     which it keeps alive: codes uint8 [n_layers][n_pages][n_kv_heads][page_size]
@@ -779,43 +791,42 @@ class KVPagesQ4:
         self.pages = spec_pages_q4(k_qs.data_ptr(), v_qs.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                    int(strides.pop()), n_layers, n_pages, n_kv_heads, page_size, 32 * blocks,
                                    n_slots, max_pages, _ptr(table), _ptr(refs), _ptr(lens))
-        self.ref = ctypes.byref(self.pages)
-
-    at = KVPages.at
+        self._ref = ctypes.byref(self.pages)
 
 
 def spec_pages_q4_copy(kv: KVPagesQ4, n: int, src, dst, status, n_pos=None, stream=None):
     """spec_pages_copy for a cache in 4 bits."""
     d, st = _here(stream)
-    _check(lib().spec_pages_q4_copy(kv.at(d), int(n), _dev(src, d), _dev(dst, d), _dev(n_pos, d), _dev(status, d),
-                                    st))
+    _check(lib().spec_pages_q4_copy(_struct(kv, KVPagesQ4, d), int(n), _dev(src, d), _dev(dst, d), _dev(n_pos, d),
+                                    _dev(status, d), st))
 
 
 def spec_pages_q4_fork(kv: KVPagesQ4, n: int, src, dst, status, stream=None):
     """spec_pages_fork for a cache in 4 bits."""
     d, st = _here(stream)
-    _check(lib().spec_pages_q4_fork(kv.at(d), int(n), _dev(src, d), _dev(dst, d), _dev(status, d), st))
+    _check(lib().spec_pages_q4_fork(_struct(kv, KVPagesQ4, d), int(n), _dev(src, d), _dev(dst, d), _dev(status, d),
+                                    st))
 
 
 def spec_pages_q4_extend(kv: KVPagesQ4, n: int, slots, n_new, copies, status, stream=None):
     """spec_pages_extend for a cache in 4 bits."""
     d, st = _here(stream)
-    _check(lib().spec_pages_q4_extend(kv.at(d), int(n), _dev(slots, d), _dev(n_new, d), _dev(copies, d),
-                                      _dev(status, d), st))
+    _check(lib().spec_pages_q4_extend(_struct(kv, KVPagesQ4, d), int(n), _dev(slots, d), _dev(n_new, d),
+                                      _dev(copies, d), _dev(status, d), st))
 
 
 def spec_pages_q4_free(kv: KVPagesQ4, n: int, slots, status, stream=None):
     """spec_pages_free for a cache in 4 bits."""
     d, st = _here(stream)
-    _check(lib().spec_pages_q4_free(kv.at(d), int(n), _dev(slots, d), _dev(status, d), st))
+    _check(lib().spec_pages_q4_free(_struct(kv, KVPagesQ4, d), int(n), _dev(slots, d), _dev(status, d), st))
 
 
 def spec_pages_q4_commit(kv: KVPagesQ4, n: int, slots, nt: int, k_new, v_new, path, n_path, status,
                          new_len=None, new_layer_stride: int = 0, stream=None):
     """spec_pages_commit into a cache in 4 bits: fp16 rows are quantised on their way."""
     d, st = _here(stream)
-    _check(lib().spec_pages_q4_commit(kv.at(d), int(n), _dev(slots, d), int(nt), _dev(k_new, d), _dev(v_new, d),
-                                      int(new_layer_stride), _dev(path, d), _dev(n_path, d), _dev(new_len, d),
+    _check(lib().spec_pages_q4_commit(_struct(kv, KVPagesQ4, d), int(n), _dev(slots, d), int(nt), _dev(k_new, d),
+                                      _dev(v_new, d), int(new_layer_stride), _dev(path, d), _dev(n_path, d), _dev(new_len, d),
                                       _dev(status, d), st))
 
 
@@ -824,14 +835,15 @@ def spec_pages_q4_read(kv: KVPagesQ4, n: int, slots, nt: int, pos0, n_pos, k, v,
     """Positions pos0[i] + j, j < n_pos[i], of slot slots[i] as fp16 into row j of
     entry i of k and v [n_layers][n][nt][n_kv_heads][head_dim]."""
     d, st = _here(stream)
-    _check(lib().spec_pages_q4_read(kv.at(d), int(n), _dev(slots, d), int(nt), _dev(pos0, d), _dev(n_pos, d),
-                                    _dev(k, d), _dev(v, d), int(layer_stride), _dev(status, d), st))
+    _check(lib().spec_pages_q4_read(_struct(kv, KVPagesQ4, d), int(n), _dev(slots, d), int(nt), _dev(pos0, d),
+                                    _dev(n_pos, d), _dev(k, d), _dev(v, d), int(layer_stride), _dev(status, d), st))
 
 
 def spec_tree_attn_q4_workspace(kv: KVPagesQ4, n_seq: int, nt: int, n_q_heads: int) -> int:
     """Bytes of workspace that spec_tree_attn_q4 needs for trees of this size."""
     b = SZ()
-    _check(lib().spec_tree_attn_q4_workspace(kv.ref, int(n_seq), int(nt), int(n_q_heads), ctypes.byref(b)))
+    _check(lib().spec_tree_attn_q4_workspace(_struct(kv, KVPagesQ4), int(n_seq), int(nt), int(n_q_heads),
+                                             ctypes.byref(b)))
     return b.value
 
 
@@ -842,7 +854,7 @@ def spec_tree_attn_q4(kv: KVPagesQ4, layer: int, n_seq: int, slots, nt: int, n_q
     """spec_tree_attn over a cache in 4 bits."""
     d, st = _here(stream)
     t = spec_tree(n_seq, nt, n_q_heads, window, sinks, scale, _dev(slots, d), _dev(parents, d), _dev(n_nodes, d))
-    _check(lib().spec_tree_attn_q4(kv.at(d), int(layer), ctypes.byref(t), _dev(q, d), int(q_stride),
+    _check(lib().spec_tree_attn_q4(_struct(kv, KVPagesQ4, d), int(layer), ctypes.byref(t), _dev(q, d), int(q_stride),
                                    _dev(k_new, d), _dev(v_new, d), int(kv_stride), _dev(out, d),
                                    _dev(workspace, d), workspace.numel() * workspace.element_size(),
                                    _dev(status, d), st))
@@ -868,9 +880,7 @@ class KVDigest:
         self._keep = (data, table, lens)
         self.pages = spec_digest(data.data_ptr(), data.stride(0), n_layers, n_pages, n_kv_heads, per * int(block),
                                  head_dim, int(block), n_slots, max_pages, _ptr(table), _ptr(lens))
-        self.ref = ctypes.byref(self.pages)
-
-    at = KVPages.at
+        self._ref = ctypes.byref(self.pages)
 
 
 def spec_block_digest(dg: KVDigest, kv, n: int, slots, status, pos0=None, stream=None):
@@ -878,11 +888,13 @@ def spec_block_digest(dg: KVDigest, kv, n: int, slots, status, pos0=None, stream
     every layer; kv: a KVPages or KVPagesQ4 (spec_block_digest_q4)."""
     d, st = _here(stream)
     call = lib().spec_block_digest_q4 if isinstance(kv, KVPagesQ4) else lib().spec_block_digest
-    _check(call(dg.at(d), kv.at(d), int(n), _dev(slots, d), _dev(pos0, d), _dev(status, d), st))
+    _check(call(_struct(dg, KVDigest, d), _struct(kv, (KVPagesQ4, KVPages), d), int(n), _dev(slots, d),
+                _dev(pos0, d), _dev(status, d), st))
 
 
 def spec_block_digest_q4(dg: KVDigest, kv: KVPagesQ4, n: int, slots, status, pos0=None, stream=None):
     """spec_block_digest of a cache in 4 bits."""
+    _struct(kv, KVPagesQ4)
     spec_block_digest(dg, kv, n, slots, status, pos0, stream)
 
 
@@ -896,8 +908,8 @@ def spec_block_scores(dg: KVDigest, layer: int, n_seq: int, slots, nt: int, n_q_
                       status, n_nodes=None, q_stride: int = 0, stream=None):
     """Every block's score for each node's query: scores fp32 [n_seq][nt][n_kv_heads][ld]."""
     d, st = _here(stream)
-    _check(lib().spec_block_scores(dg.at(d), int(layer), int(n_seq), _dev(slots, d), int(nt), _dev(n_nodes, d),
-                                   int(n_q_heads), _dev(q, d), int(q_stride), _dev(scores, d),
+    _check(lib().spec_block_scores(_struct(dg, KVDigest, d), int(layer), int(n_seq), _dev(slots, d), int(nt),
+                                   _dev(n_nodes, d), int(n_q_heads), _dev(q, d), int(q_stride), _dev(scores, d),
                                    _rows_of_scores(scores), _dev(status, d), st))
 
 
@@ -906,6 +918,8 @@ def spec_block_select(lens, block: int, n_seq: int, slots, nt: int, n_kv_heads: 
     """The first n_first, the last n_last and the largest-scored others of a row's
     blocks, ascending, -1 behind: blocks int32 [n_seq][nt][n_kv_heads][n_keep]."""
     d, st = _here(stream)
+    if lens.element_size() != 4 or lens.is_floating_point() or not lens.is_contiguous():
+        raise ValueError("lens: a contiguous int32 tensor is required")
     _check(lib().spec_block_select(_dev(lens, d), lens.numel(), int(block), int(n_seq), _dev(slots, d), int(nt),
                                    _dev(n_nodes, d), int(n_kv_heads), _dev(scores, d), _rows_of_scores(scores),
                                    int(n_keep), int(n_first), int(n_last), _dev(blocks, d), _dev(status, d), st))
@@ -920,10 +934,11 @@ def spec_block_attn(kv, layer: int, n_seq: int, slots, nt: int, n_q_heads: int, 
     d, st = _here(stream)
     t = spec_tree(n_seq, nt, n_q_heads, 0, 0, scale, _dev(slots, d), _dev(parents, d), _dev(n_nodes, d))
     call = lib().spec_block_attn_q4 if isinstance(kv, KVPagesQ4) else lib().spec_block_attn
-    _check(call(kv.at(d), int(layer), ctypes.byref(t), int(block), int(n_keep), _dev(blocks, d), _dev(q, d),
-                int(q_stride), _dev(k_new, d), _dev(v_new, d), int(kv_stride), _dev(out, d), _dev(status, d), st))
+    _check(call(_struct(kv, (KVPagesQ4, KVPages), d), int(layer), ctypes.byref(t), int(block), int(n_keep),
+                _dev(blocks, d), _dev(q, d), int(q_stride), _dev(k_new, d), _dev(v_new, d), int(kv_stride), _dev(out, d), _dev(status, d), st))
 
 
 def spec_block_attn_q4(kv: KVPagesQ4, *args, **kw):
     """spec_block_attn over a cache in 4 bits."""
+    _struct(kv, KVPagesQ4)
     spec_block_attn(kv, *args, **kw)

@@ -19,7 +19,6 @@
 
 namespace {
 
-
 struct BlockArgs {
   const uint8_t* k;  // the layer's rows of fp16, or codes
   const uint8_t* v;
@@ -255,10 +254,29 @@ __global__ void __launch_bounds__((BShape<HD, NT, Q4>::THREADS)) block_attn_kern
             [&](int r, int u, const float (&acc)[8], float l) { put_row(out + r * HD + u * 8, acc, l); });
 }
 
+// CTAs of a unit, as long as every warp has two steps of the list: of fp16 as many as are
+// resident, two an SM, up to 16 (one node over 64 blocks of 64: 8.9 us, with up to eight
+// 9.9); of codes, with twice the warps, one an SM, up to eight (8 sequences of one node
+// over 64 blocks of 64: 17.3 us, with half the warps 20.8), and of fp16 with the longest
+// lists, too, where the shared memory holds one: sixteen SMs may be more than a GPC has.
 template <int HD, int NT, bool Q4>
-cudaError_t launch_block(const BlockArgs& a, size_t units, cudaStream_t st) {
-  return launch_clusters(block_attn_kernel<HD, NT, Q4>, a, units * a.ranks, BShape<HD, NT, Q4>::THREADS, a.ranks,
-                         BShape<HD, NT, Q4>::smem(a.path_rows, a.keep), st);
+int launch_block(BlockArgs& a, double units, int block, cudaStream_t st) {
+  using Sh = BShape<HD, NT, Q4>;
+  const size_t smem = Sh::smem(a.path_rows, a.keep);
+  const int64_t steps = ((int64_t)a.keep * block + Sh::KEYS - 1) / Sh::KEYS;
+  const int fit = !Q4 && smem <= 113 * 1024 ? 2 : 1;
+  a.ranks = 1;
+  while (a.ranks < 8 * fit && units * a.ranks * 2 <= fit * device_sms() && steps >= (int64_t)2 * Sh::WARPS * a.ranks * 2)
+    a.ranks *= 2;
+  if (units * a.ranks > INT32_MAX) return fail(SPEC_E_SHAPE, "n_seq * nt * n_q_heads too large");
+  const cudaError_t e = launch_clusters(block_attn_kernel<HD, NT, Q4>, a, (size_t)units * a.ranks, Sh::THREADS, a.ranks,
+                                        smem, st);
+  if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("block attention: ") + cudaGetErrorString(e));
+  return SPEC_OK;
+}
+template <int HD, bool Q4>
+int launch_block_rows(BlockArgs& a, double units, int NT, int block, cudaStream_t st) {
+  return NT == 1 ? launch_block<HD, 1, Q4>(a, units, block, st) : launch_block<HD, 2, Q4>(a, units, block, st);
 }
 
 template <int HD, int NT, bool Q4>
@@ -320,22 +338,8 @@ int launch_block_attn(const spec_pages* book, const BlockPlanes& planes, const s
   a.out = reinterpret_cast<__half*>(out);
   a.status = status;
   const double units = (double)t->n_seq * t->nt * a.nkv * a.row_blocks;
-  // CTAs of a unit, as long as every warp has two steps of the list: of fp16 as many as are
-  // resident, two an SM, up to 16 (one node over 64 blocks of 64: 8.9 us, with up to eight
-  // 9.9); of codes, with twice the warps, one an SM, up to eight (8 sequences of one node
-  // over 64 blocks of 64: 17.3 us, with half the warps 20.8)
-  const int64_t steps = ((int64_t)n_keep * block + (q4 ? 31 : 15)) / (q4 ? 32 : 16);
-  const int most = q4 ? 8 : 16, fit = q4 ? 1 : 2, warps = q4 ? 8 : 4;
-  a.ranks = 1;
-  while (a.ranks < most && units * a.ranks * 2 <= fit * device_sms() && steps >= (int64_t)2 * warps * a.ranks * 2)
-    a.ranks *= 2;
-  if (units * a.ranks > INT32_MAX) return fail(SPEC_E_SHAPE, "n_seq * nt * n_q_heads too large");
-  const size_t n = (size_t)units;
-  const cudaError_t e =
-      q4 ? (hd == 128 ? (NT == 1 ? launch_block<128, 1, true>(a, n, st) : launch_block<128, 2, true>(a, n, st))
-                      : (NT == 1 ? launch_block<64, 1, true>(a, n, st) : launch_block<64, 2, true>(a, n, st)))
-         : (hd == 128 ? (NT == 1 ? launch_block<128, 1, false>(a, n, st) : launch_block<128, 2, false>(a, n, st))
-                      : (NT == 1 ? launch_block<64, 1, false>(a, n, st) : launch_block<64, 2, false>(a, n, st)));
-  if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("block attention: ") + cudaGetErrorString(e));
-  return SPEC_OK;
+  return hd == 128 ? (q4 ? launch_block_rows<128, true>(a, units, NT, block, st)
+                          : launch_block_rows<128, false>(a, units, NT, block, st))
+                   : (q4 ? launch_block_rows<64, true>(a, units, NT, block, st)
+                         : launch_block_rows<64, false>(a, units, NT, block, st));
 }

@@ -356,6 +356,168 @@ def test_what_is_not_selected_may_be_anything(dev):
         assert np.isnan(got[0, 4]).all() and (got[1, 4] == 7.0).all()
 
 
+@pytest.mark.parametrize("hd,nq,scale", [(64, 8, -0.25), (128, 24, 0.3), (128, 8, None)])
+def test_strides_scales_and_a_block_named_twice(dev, hd, nq, scale):
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    for q4 in (False, True):
+        g = np.random.default_rng([hd, nq, q4])
+        c = make(sv, dev, g, q4, nq, 2, hd, [310, 64], 5, 32, scale=scale, counts=[5, 4])
+        x = Blocks(c, 16)
+        lists = x.lists(g, 7)
+        lists[0, 2, 0, :5] = [3, 19, 3, 3, 0]  # (19: six positions)
+        want = x.attend(lists)
+        assert (x.st[0] == 0).all() and (x.st[1, :4] == 0).all()
+        x.check_attention(want, lists)
+
+        def apart(a, row):
+            buf = torch.full((c.n * c.nt, row), float("nan"), dtype=torch.float16, device=dev)
+            buf[:, :a[0, 0].size] = c.T(a).view(c.n * c.nt, -1)
+            return buf
+        qs, ks = nq * hd + 8, 2 * hd + 40
+        got = x.attend(lists, q=apart(c.q, qs), k_new=apart(c.kn, ks), v_new=apart(c.vn, ks), q_stride=qs, kv_stride=ks)
+        assert np.array_equal(got.view(np.uint16), want.view(np.uint16))
+        q = c.q.copy()
+        q[0, 1, 2, 3] = np.nan
+        got = x.attend(lists, q=c.T(q))
+        odd = np.zeros(got.shape[:3], bool)
+        odd[0, 1, 2] = True
+        assert np.isnan(got[odd]).all() and np.array_equal(got[~odd].view(np.uint16), want[~odd].view(np.uint16))
+
+
+@pytest.mark.parametrize("hd,nq,nt", [(128, 20, 64), (128, 8, 17), (64, 8, 1)])
+def test_the_longest_lists(dev, hd, nq, nt):
+    """4096 places, most of them empty, the blocks anywhere."""
+    import speculative_decoding_verification_round_gb300 as sv
+    for q4 in (False, True):
+        g = np.random.default_rng([hd, nt])
+        c = make(sv, dev, g, q4, nq, 1, hd, [700], nt, 32, layers=1)
+        x = Blocks(c, 16)
+        lists = np.full((1, nt, 1, 4096), -1, np.int32)
+        for i in range(nt):
+            ids = g.permutation(44)[:i % 7 + 1]
+            lists[0, i, 0, g.permutation(4096)[:len(ids)]] = ids
+        lists[0, 0, 0, [0, 4095]] = [0, 43]
+        got = x.attend(lists, chain=False)
+        assert (x.st == 0).all()
+        x.check_attention(got, lists)
+
+
+def test_digests_of_copied_pages(dev):
+    """A branch whose shared last page is copied when it grows: digests of the copy
+    from the page's start on, the other branch's as they were."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(13)
+    layers, nkv, page, block, hd, n_pages = 2, 2, 32, 16, 64, 9
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    shape = (layers, n_pages, nkv, page, hd // 32)
+    planes = [torch.zeros(shape + (16,), dtype=torch.uint8, device=dev) for _ in range(2)] + [
+        torch.zeros(shape, dtype=torch.float16, device=dev) for _ in range(2)]
+    table, lens, refs = i32([[-1] * 4] * 2), i32([0, 0]), i32([0] * n_pages)
+    kv = sv.KVPagesQ4(*planes, table, lens, refs)
+    data = torch.full((layers, n_pages, nkv, page // block, 2, hd), 5.0, dtype=torch.float16, device=dev)
+    dg = sv.KVDigest(data, block, table, lens)
+    st, copies = i32([9]), i32([[9, 9]])
+
+    def grow(slot, rows, pos0):
+        k = torch.from_numpy(g.standard_normal((layers, 1, rows, nkv, hd)).astype(np.float16)).to(dev)
+        sv.spec_pages_q4_extend(kv, 1, i32([slot]), i32([rows]), copies, st)
+        assert st.tolist() == [0]
+        sv.spec_pages_q4_commit(kv, 1, i32([slot]), rows, k, k.flip(2), None, i32([rows]), st)
+        assert st.tolist() == [0]
+        sv.spec_block_digest(dg, kv, 1, i32([slot]), st, pos0=i32([pos0]))
+        assert st.tolist() == [0]
+
+    def check(slot):
+        n = lens[slot].item()
+        rows = [torch.zeros((layers, 1, n, nkv, hd), dtype=torch.float16, device=dev) for _ in range(2)]
+        sv.spec_pages_q4_read(kv, 1, i32([slot]), n, i32([0]), i32([n]), rows[0], rows[1], st)
+        assert st.tolist() == [0]
+        k, d, t = rows[0][:, 0].cpu().numpy(), data.cpu().numpy(), table[slot].tolist()
+        for layer in range(layers):
+            for h in range(nkv):
+                for j in range(-(-n // block)):
+                    got = d[layer, t[j * block // page], h, j * block % page // block]
+                    assert np.array_equal(got, lc.digest(k[layer, j * block:(j + 1) * block, h])), (slot, layer, h, j)
+
+    grow(0, 70, 0)
+    check(0)
+    sv.spec_pages_q4_fork(kv, 1, i32([0]), i32([1]), st)
+    assert st.tolist() == [0]
+    check(1)
+    grow(1, 20, 64)  # 70 positions: the copied page begins with 64
+    assert copies[0, 0].item() == table[0, 2].item() and copies[0, 1].item() == table[1, 2].item()
+    check(0), check(1)
+    grow(0, 30, 64)
+    check(0), check(1)
+
+
+def test_captured_rounds(dev):
+    """Rounds whose lengths grow on the device, captured once: commit in place, digests
+    of what is new, scores, selection, both attentions; replayed, they are the eager ones."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    nq, nkv, hd, page, block, nt, n, keep, max_pages, layers = 8, 2, 128, 64, 32, 5, 2, 4, 6, 2
+    g = np.random.default_rng(17)
+    T = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    f16 = lambda *s: T(g.standard_normal(s).astype(np.float16))  # noqa: E731
+    prompt, kn, vn, q = f16(layers, n, 200, nkv, hd), f16(layers, n, nt, nkv, hd), f16(layers, n, nt, nkv, hd), f16(n, nt, nq, hd)
+    pages = g.permutation(n * max_pages).reshape(n, max_pages).astype(np.int32)
+
+    class Run:
+        def __init__(self):
+            shape = (layers, n * max_pages, nkv, page, hd // 32)
+            planes = [torch.zeros(shape + (16,), dtype=torch.uint8, device=dev) for _ in range(2)] + [
+                torch.zeros(shape, dtype=torch.float16, device=dev) for _ in range(2)]
+            self.lens, self.st = T(np.zeros(n, np.int32)), T(np.full(n, 9, np.int32))
+            self.kv = sv.KVPagesQ4(*planes, T(pages), self.lens)
+            self.dg = sv.KVDigest(torch.zeros((layers, n * max_pages, nkv, page // block, 2, hd), dtype=torch.float16, device=dev), block,
+                                  self.kv._keep[4], self.lens)
+            self.slots, self.n_path, self.path = T(np.array([1, 0], np.int32)), T(np.array([3, 2], np.int32)), T(
+                np.array([[0, 2, 4, 0, 0], [0, 1, 0, 0, 0]], np.int32))
+            self.pos0 = torch.zeros(n, dtype=torch.int32, device=dev)
+            self.scores = torch.zeros((n, nt, nkv, max_pages * 2), device=dev)
+            self.blocks = torch.zeros((n, nt, nkv, keep), dtype=torch.int32, device=dev)
+            self.outs = [torch.zeros((n, nt, nq, hd), dtype=torch.float16, device=dev) for _ in range(2)]
+            self.row_st = torch.zeros((n, nt, nkv), dtype=torch.int32, device=dev)
+            self.ws = torch.empty(sv.spec_tree_attn_q4_workspace(self.kv, n, nt, nq), dtype=torch.uint8, device=dev)
+            self.bad = torch.zeros((), dtype=torch.int32, device=dev)
+            sv.spec_pages_q4_commit(self.kv, n, self.slots, 200, prompt, prompt, None, T(np.array([200, 61], np.int32)), self.st)
+            sv.spec_block_digest(self.dg, self.kv, n, self.slots, self.st)
+
+        def round(self):
+            a = (n, self.slots, nt)
+            self.pos0.copy_(self.lens.index_select(0, self.slots))
+            sv.spec_pages_q4_commit(self.kv, n, self.slots, nt, kn, vn, self.path, self.n_path, self.st)
+            self.bad |= self.st.max()
+            sv.spec_block_digest(self.dg, self.kv, n, self.slots, self.st, pos0=self.pos0)
+            self.bad |= self.st.max()
+            sv.spec_block_scores(self.dg, 1, *a, nq, q, self.scores, self.st)
+            self.bad |= self.st.max()
+            sv.spec_block_select(self.lens, block, *a, nkv, self.scores, keep, self.blocks, self.st)
+            self.bad |= self.st.max()
+            sv.spec_block_attn(self.kv, 1, *a, nq, block, keep, self.blocks, q, kn[1], vn[1], self.outs[0], self.row_st)
+            self.bad |= self.row_st.max()
+            sv.spec_tree_attn_q4(self.kv, 1, *a, nq, q, kn[1], vn[1], self.outs[1], self.ws, self.st)
+            self.bad |= self.st.max()
+
+    eager, replayed, first = Run(), Run(), Run()
+    first.round()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        replayed.round()
+    assert replayed.lens.tolist() == [61, 200]  # (captured, not run)
+    for step in range(1, 5):
+        eager.round()
+        graph.replay()
+        assert eager.lens.tolist() == replayed.lens.tolist() == [61 + 2 * step, 200 + 3 * step]
+        assert eager.bad.item() == replayed.bad.item() == 0
+        for a, b in zip(eager.outs + [eager.scores, eager.blocks], replayed.outs + [replayed.scores, replayed.blocks]):
+            assert torch.equal(a, b) and (a.dtype != torch.float16 or torch.isfinite(a).all())
+
+
 def test_all_blocks_are_the_whole_context(dev):
     """Lists that name every block: the attention of spec_tree_attn."""
     import speculative_decoding_verification_round_gb300 as sv

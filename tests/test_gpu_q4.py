@@ -184,6 +184,37 @@ def test_nothing_of_what_is_masked_gets_in(dev, hd, nq, nt):
     assert np.isfinite(got[0]).all() and np.isnan(got[1, :, :nq // 2]).all() and np.isfinite(got[1, :, nq // 2:]).all()
 
 
+@pytest.mark.parametrize("hd,nt", [(64, 1), (128, 4), (64, 8), (128, 9), (64, 40)])
+def test_strides_and_other_rows_queries(dev, hd, nt):
+    """Rows of q, k_new and v_new apart, and planes whose layers are apart, with NaN
+    between; a NaN in one row's query is that row's alone."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng([hd, nt])
+    c = Q4Case(sv, dev, g, 8, 2, hd, [300, 0, 77], nt, 16, counts=[nt, nt, max(1, nt - 1)])
+    want = c.call()
+    c.check(want)
+
+    def apart(x, row):
+        buf = torch.full((c.n * nt, row), float("nan"), dtype=torch.float16, device=dev)
+        buf[:, :x[0, 0].size] = c.T(x).view(c.n * nt, -1)
+        return buf
+    qs, ks = 8 * hd + 24, 2 * hd + 8
+    layers = [torch.full((t.shape[0], t.shape[1] + 3, *t.shape[2:]), 0x7F if t.dtype == torch.uint8 else float("nan"), dtype=t.dtype,
+                         device=dev)[:, :t.shape[1]] for t in c.pool()._keep[:4]]
+    for a, b in zip(layers, c.pool()._keep):
+        a.copy_(b)
+    kv = sv.KVPagesQ4(*layers, c.T(c.table), c.T(c.slot_len))
+    got = c.call(kv, q=apart(c.q, qs), k_new=apart(c.kn, ks), v_new=apart(c.vn, ks), q_stride=qs, kv_stride=ks)
+    assert c.status.tolist() == [0] * 3 and np.array_equal(got.view(np.uint16), want.view(np.uint16))
+    q = c.q.copy()
+    q[0, nt - 1, 3, 5], q[2, 0, 6, hd - 1] = np.nan, np.inf
+    got = c.call(q=c.T(q))
+    odd = np.zeros(got.shape[:3], bool)
+    odd[0, nt - 1, 3] = odd[2, 0, 6] = True
+    assert np.isnan(got[odd]).all() and np.array_equal(got[~odd].view(np.uint16), want[~odd].view(np.uint16))
+
+
 def test_infinities_of_the_trees_own_rows(dev):
     import speculative_decoding_verification_round_gb300 as sv
     g = np.random.default_rng(14)
@@ -394,6 +425,33 @@ def test_commit_and_read_refusals(dev):
     assert (out[:, :7] == 3.0).all() and (out[:, 8] == 3.0).all() and (out[:, 7, 1:] == 3.0).all()
     want = lc.values(before[0][:, 0, :, 0], before[1][:, 0, :, 0])
     assert np.array_equal(out[:, 7, 0].cpu().numpy().astype(np.float64), want)
+
+
+def test_rows_with_layers_apart(dev):
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(3)
+    layers, n, nt, nkv, hd, page = 3, 2, 40, 2, 64, 16
+    table = g.permutation(8).reshape(2, 4).astype(np.int32)
+    c = Planes(sv, dev, g, layers, 8, nkv, page, hd, table, [3, 9])
+    rows = [random_rows(g, (layers, n, nt, nkv, hd)) for _ in range(2)]
+    step = n * nt * nkv * hd + 80
+    bufs = [torch.full((layers, step), float("nan"), dtype=torch.float16, device=dev) for _ in range(4)]
+    for b, x in zip(bufs, rows):
+        b[:, :step - 80] = c.T(x).view(layers, -1)
+    slots, n_path, st = c.T(np.array([1, 0], np.int32)), c.T(np.array([nt, 33], np.int32)), c.T(np.array([9, 9], np.int32))
+    pos0 = c.T(np.array([9, 3], np.int32))
+    sv.spec_pages_q4_commit(c.kv, n, slots, nt, bufs[0], bufs[1], None, n_path, st, new_layer_stride=step)
+    assert st.tolist() == [0, 0] and c.kv._keep[5].tolist() == [36, 49]
+    sv.spec_pages_q4_read(c.kv, n, slots, nt, pos0, n_path, bufs[2], bufs[3], st, layer_stride=step)
+    assert st.tolist() == [0, 0]
+    for w in range(2):
+        got = bufs[2 + w].cpu().numpy()
+        assert np.isnan(got[:, step - 80:]).all()
+        got = got[:, :step - 80].reshape(layers, n, nt, nkv, hd)
+        want = lc.values(*lc.pack(*lc.quantise(rows[w])))
+        assert np.array_equal(got[:, 0], want[:, 0]) and np.array_equal(got[:, 1, :33], want[:, 1, :33])
+        assert np.isnan(got[:, 1, 33:]).all()
 
 
 @pytest.mark.parametrize("hd,nkv,page", [(128, 8, 64), (64, 1, 5), (32, 3, 16)])
