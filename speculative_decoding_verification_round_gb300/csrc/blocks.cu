@@ -62,10 +62,29 @@ __device__ __forceinline__ int join_lanes(uint32_t (&lo)[REGS], uint32_t (&hi)[R
   return reg0;
 }
 
+// Blocks and pages: a division only where a page has no power of two of blocks.
+struct PageBlocks {
+  int shift, per, per_shift;  // log2 of the block, blocks of a page and their log2 (-1: none)
+  __device__ __forceinline__ int blocks(int len) const {
+    return (int)(((uint32_t)len + (1u << shift) - 1u) >> shift);  // (len is at most 2^31 - 1)
+  }
+  __device__ __forceinline__ int page(uint32_t b) const { return (int)(per_shift >= 0 ? b >> per_shift : b / (uint32_t)per); }
+  __device__ __forceinline__ int at(uint32_t b) const { return (int)b - page(b) * per; }
+};
+int log2_of(int x) {  // -1: not a power of two
+  int n = 0;
+  while (1 << n < x && n < 30) n++;
+  return 1 << n == x ? n : -1;
+}
+PageBlocks page_blocks(const spec_digest* dg) {
+  const int per = dg->page_size / dg->block;
+  return {log2_of(dg->block), per, log2_of(per)};
+}
+
 template <int HD, bool Q4>
 __global__ void __launch_bounds__(DG_THREADS, Q4 ? 5 : 4)
 digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __restrict__ slots,
-              const int32_t* __restrict__ pos0, uint32_t split, int32_t* __restrict__ status) {
+              const int32_t* __restrict__ pos0, uint32_t split, const PageBlocks pb, int32_t* __restrict__ status) {
   constexpr int ROW = Q4 ? HD / 2 : HD * 2, LANES = ROW / (Q4 ? 8 : 16), PER = 32 / LANES;  // bytes; lanes and rows of a load
   constexpr int REGS = Q4 ? 8 : 4, U = 8, ROWS = U * PER;  // rows in flight
   constexpr int BIT = LANES == 16 ? 4 : LANES == 8 ? 3 : 2;
@@ -84,17 +103,17 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
   else
     len = dg.len[slot];
   if (p0 < 0 || len < 0 || len > dg.max_pages * dg.page_size) st |= SPEC_ST_FULL;
-  const int block = dg.block, per = dg.page_size / block, nb = st == 0 ? (int)(((int64_t)len + block - 1) / block) : 0;
+  const int block = dg.block, per = pb.per, nb = st == 0 ? pb.blocks(len) : 0, b0 = max(p0, 0) >> pb.shift;
   const int32_t* row = dg.table + (int64_t)(st == 0 ? slot : 0) * dg.max_pages;
   if (h == 0 && layer == 0 && y == 0) {  // the entry's status
     bool bad = false;
-    if (p0 / block < nb)
-      for (int e = p0 / block / per + lane; e <= (nb - 1) / per; e += 32) bad |= row[e] < 0 || row[e] >= dg.n_pages;
+    if (st == 0 && b0 < nb)
+      for (int e = pb.page(b0) + lane; e <= pb.page(nb - 1); e += 32) bad |= row[e] < 0 || row[e] >= dg.n_pages;
     if (__any_sync(0xffffffffu, bad)) st |= SPEC_ST_PAGE;
     if (lane == 0) status[i] = st;
   }
   const uint32_t count = nb, l = lane % LANES;
-  auto page_of = [&](uint32_t b) { return b < count ? row[b / per] : -1; };
+  auto page_of = [&](uint32_t b) { return b < count ? row[pb.page(b)] : -1; };
   auto rows_of = [&](uint32_t b) { return min(block, len - (int)b * block); };
   struct Part {
     Load v[U];
@@ -103,7 +122,7 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
   // rows r0 ... r0 + ROWS - 1 of block b (a row again where it has no more: that changes nothing)
   auto load = [&](uint32_t b, int pg, int r0, Part& p) {
     if (b >= count || pg < 0 || pg >= dg.n_pages) return;
-    const int64_t first = (int64_t)layer * keys.layer_stride + ((int64_t)pg * dg.n_kv_heads + h) * dg.page_size + b % per * block;
+    const int64_t first = (int64_t)layer * keys.layer_stride + ((int64_t)pg * dg.n_kv_heads + h) * dg.page_size + pb.at(b) * block;
     const int last = rows_of(b) - 1;
     const uint8_t* src = keys.rows + first * ROW + l * (uint32_t)sizeof(Load);
     const __half* sc = Q4 ? keys.scales + first * (HD / 32) + l / 2 : nullptr;
@@ -114,7 +133,7 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
       if (Q4) p.s[u] = __half_as_ushort(__ldg(sc + at * (HD / 32)));
     }
   };
-  uint32_t b = (uint32_t)p0 / block + y;
+  uint32_t b = (uint32_t)b0 + y;
   int pg = page_of(b), pg_next = page_of(b + split), r0 = 0;
   Part now, next;
   load(b, pg, 0, now);
@@ -161,7 +180,7 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
     if (!end || page < 0 || page >= dg.n_pages) continue;
     const int64_t head = (int64_t)page * dg.n_kv_heads + h;
     const int reg0 = join_lanes<REGS, BIT>(lo, hi);
-    uint16_t* to = dg.data + (int64_t)layer * dg.layer_stride + (head * per + done % per) * (2 * HD);
+    uint16_t* to = dg.data + (int64_t)layer * dg.layer_stride + (head * per + pb.at(done)) * (2 * HD);
     if (!Q4) {  // word l * 4 + reg of the row
 #pragma unroll
       for (int x = 0; x < KEPT; x++) {
@@ -209,6 +228,7 @@ struct ScoreArgs {
   int32_t* status;
   int nodes, groups;  // nodes of a CTA, CTAs for a sequence's nodes
   int chunks;         // CTAs for a sequence's blocks
+  PageBlocks pb;
 };
 
 template <int HD>
@@ -238,14 +258,13 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
   else
     len = dg.len[slot];
   if (m < 0 || m > a.nt) st |= SPEC_ST_TREE;
-  const int block = dg.block, per = dg.page_size / block;
-  const int nb = (int)(((int64_t)max(len, 0) + block - 1) / block);
+  const int per = a.pb.per, nb = a.pb.blocks(max(len, 0));
   if (len < 0 || len > dg.max_pages * dg.page_size || nb > a.ld) st |= SPEC_ST_FULL;
   const int32_t* row = dg.table + (int64_t)(st == 0 ? slot : 0) * dg.max_pages;
   if (chunk == 0 && grp == 0 && h == 0) {
     bool bad = false;
     if (st == 0)
-      for (int e = tid; e <= (nb - 1) / per && nb > 0; e += SC_THREADS) bad |= row[e] < 0 || row[e] >= dg.n_pages;
+      for (int e = tid; nb > 0 && e <= a.pb.page(nb - 1); e += SC_THREADS) bad |= row[e] < 0 || row[e] >= dg.n_pages;
     if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
     if (tid == 0) a.status[s] = st;
     st &= ~SPEC_ST_PAGE;
@@ -261,7 +280,7 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
   auto load = [&](int b0) {
 #pragma unroll
     for (int half = 0; half < 2; half++) {
-      const int b = b0 + 8 * half + g, e = b / per, pg = b < nb ? row[e] : -1;
+      const int b = b0 + 8 * half + g, e = a.pb.page(b), pg = b < nb ? row[e] : -1;
       there[half] = pg >= 0 && pg < dg.n_pages;
       const uint4* src = reinterpret_cast<const uint4*>(
           dg.data + (int64_t)a.layer * dg.layer_stride +
@@ -370,13 +389,13 @@ __global__ void __launch_bounds__(SC_THREADS) scores_kernel(const ScoreArgs a) {
 // bin of a histogram of the ten highest bits in which the row's keys differ; of the
 // bin's keys, mostly a few, each is ranked against the others (192 x 8 rows of 2048: 15
 // us with the k-th key's bits found one by one by counts, 13 with eight bits, whose bins
-// most keys share, 11.8 so).  A warp's vote over
-// a key of each lane is a word of the map of the chosen blocks, whose words then are
-// written out in order, a thread one.
+// most keys share; 10.2 so with ten CTAs an SM, 10.5 with nine, 11.4 with eleven, for
+// which registers are spilled).  A warp's vote over a key of each lane is a word of the
+// map of the chosen blocks, whose words then are written out in order, a thread one.
 // ---------------------------------------------------------------------------
 struct SelectArgs {
   const int32_t* len;
-  int n_slots, block, n_seq, nt, nkv;
+  int n_slots, shift, n_seq, nt, nkv;  // shift: log2 of the block
   const int32_t* slots;
   const int32_t* n_nodes;
   const float* scores;
@@ -387,13 +406,13 @@ struct SelectArgs {
 };
 
 template <int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) select_kernel(const SelectArgs a) {
   constexpr int WARPS = THREADS / 32, SPAN = THREADS * PER, CAND = 256, WORDS = SPAN / 32;
   constexpr int BIN_BITS = THREADS <= 64 ? 9 : 10, BINS = 1 << BIN_BITS, EACH = BINS / THREADS;
-  constexpr int HIST = BINS + BINS / 32;  // (a word more for each 32: a thread's bins are neighbours)
   static_assert(WORDS <= THREADS && PER <= 32, "a word a thread, a lane for each of a thread's keys");
   __shared__ int s_sum[2][WARPS], s_n, s_found[3];
-  __shared__ uint32_t s_bits[2][WORDS], s_mm[2][WARPS], s_hist[HIST], s_cand[CAND], s_key;
+  __shared__ __align__(16) uint32_t s_hist[BINS];
+  __shared__ uint32_t s_bits[2][WORDS], s_mm[2][WARPS], s_cand[CAND], s_key;
   grid_dep_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = blockIdx.x, sn = r / a.nkv, h = r - sn * a.nkv, s = sn / a.nt, node = sn - s * a.nt;
@@ -404,7 +423,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   else
     len = a.len[slot];
   if (m < 0 || m > a.nt) st |= SPEC_ST_TREE;
-  const int nb = (int)(((int64_t)max(len, 0) + a.block - 1) / a.block);
+  const int nb = (int)(((uint32_t)max(len, 0) + (1u << a.shift) - 1u) >> a.shift);
   if (len < 0 || nb > a.ld) st |= SPEC_ST_FULL;
   if (h == 0 && node == 0 && tid == 0) a.status[s] = st;
   int32_t* out = a.blocks + (int64_t)r * a.keep;
@@ -419,6 +438,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
   // never 0, which stands for no block.
   const float* x = a.scores + (int64_t)r * a.ld;
   const int end = nb - a.last, need = k - a.first - a.last;
+  const uint32_t many = (uint32_t)max(end - a.first, 0);
   const bool one = nb <= SPAN;
   uint32_t key[PER];
   auto load = [&](int c0) {  // key i: block c0 + i THREADS + tid
@@ -426,12 +446,12 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
 #pragma unroll
     for (int i = 0; i < PER; i++) {
       const int j = c0 + i * THREADS + tid;
-      f[i] = j >= a.first && j < end ? x[j] : 0.0f;
+      f[i] = (uint32_t)(j - a.first) < many ? x[j] : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < PER; i++) {
       const int j = c0 + i * THREADS + tid;
-      key[i] = j >= a.first && j < end ? (f[i] != f[i] ? 0xFF800000u : logit_key(f[i])) : 0u;
+      key[i] = (uint32_t)(j - a.first) < many ? (f[i] != f[i] ? 0xFF800000u : logit_key(f[i])) : 0u;
     }
   };
   // f of every key of the row but 0 (longer rows are read again for each use)
@@ -479,7 +499,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
     return before;
   };
   load(0);
-  for (int b = tid; b < HIST; b += THREADS) s_hist[b] = 0u;
+  for (int b = tid; b < BINS; b += THREADS) s_hist[b] = 0u;
   if (tid == 0) s_n = 0;
   // the bits that all keys have in common
   uint32_t lo = 0xFFFFFFFFu, hi = 0u;
@@ -504,22 +524,25 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
     const int top = 31 - __clz((int)(hi ^ lo)), shift = max(0, top - (BIN_BITS - 1));
     const uint32_t bins = 2u << (top - shift);
     t = hi & ~((2u << top) - 1u);
-    auto place = [](uint32_t b) { return b + (b >> 5); };
-    each_key([&](uint32_t y) { atomicAdd(&s_hist[place((y >> shift) & (bins - 1u))], 1u); });
+    // bins from the highest on
+    each_key([&](uint32_t y) { atomicAdd(&s_hist[~(y >> shift) & (bins - 1u)], 1u); });
     __syncthreads();
-    // EACH bins a thread, from the highest on
-    int c[EACH], mine = 0, all;
+    // EACH bins a thread
+    using Some = typename std::conditional<EACH % 4 == 0, int4, typename std::conditional<EACH == 2, int2, int>::type>::type;
+    constexpr int EVERY = sizeof(Some) / 4;
+    __align__(16) int c[EACH];
+    int mine = 0, all;
 #pragma unroll
-    for (int i = 0; i < EACH; i++) {
-      c[i] = (int)s_hist[place(BINS - 1 - EACH * tid - i)];
-      mine += c[i];
-    }
+    for (int i = 0; i < EACH; i += EVERY)
+      *reinterpret_cast<Some*>(c + i) = *reinterpret_cast<const Some*>(s_hist + EACH * tid + i);
+#pragma unroll
+    for (int i = 0; i < EACH; i++) mine += c[i];
     int over = scan(mine, &all);
     if (over < need && need <= over + mine) {
 #pragma unroll
       for (int i = 0; i < EACH; i++) {
         if (over < need && need <= over + c[i]) {
-          s_found[0] = BINS - 1 - EACH * tid - i;
+          s_found[0] = EACH * tid + i;
           s_found[1] = over;
           s_found[2] = c[i];
         }
@@ -527,7 +550,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectArgs a) {
       }
     }
     __syncthreads();
-    const uint32_t bin = (uint32_t)s_found[0];
+    const uint32_t bin = bins - 1u - (uint32_t)s_found[0];
     const int above = s_found[1], in_bin = s_found[2], rest = need - above;
     t |= bin << shift;
     reach = above + in_bin;
@@ -648,7 +671,8 @@ int launch_digest(const spec_digest* dg, const Keys& keys, bool q4, int n, const
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto kernel = dg->head_dim == 128 ? (q4 ? digest_kernel<128, true> : digest_kernel<128, false>)
                                     : (q4 ? digest_kernel<64, true> : digest_kernel<64, false>);
-  const cudaError_t e = launch_dependent(kernel, grid, DG_THREADS, 0, st, *dg, keys, n, slots, pos0, (uint32_t)split, status);
+  const cudaError_t e = launch_dependent(kernel, grid, DG_THREADS, 0, st, *dg, keys, n, slots, pos0, (uint32_t)split,
+                                         page_blocks(dg), status);
   if (e != cudaSuccess) return fail(SPEC_E_CUDA, std::string("block digest: ") + cudaGetErrorString(e));
   return SPEC_OK;
 }
@@ -711,6 +735,7 @@ extern "C" int spec_block_scores(const spec_digest* dg, int layer, int n_seq, co
     return fail(SPEC_E_SHAPE, "ld outside [1, 2^31], or scores too large");
   ScoreArgs a;
   a.dg = *dg;
+  a.pb = page_blocks(dg);
   a.layer = layer;
   a.n_seq = n_seq;
   a.nt = nt;
@@ -758,11 +783,11 @@ extern "C" int spec_block_select(const int32_t* len, int n_slots, int block, int
   const double rows = (double)n_seq * nt * n_kv_heads;
   if (rows > INT32_MAX || ld < 1 || ld > (1ll << 31) || rows * ld > 4.0e15)
     return fail(SPEC_E_SHAPE, "n_seq * nt * n_kv_heads or ld too large");
-  const SelectArgs a = {len, n_slots, block, n_seq, nt, n_kv_heads, slots, n_nodes, scores, ld, n_keep, n_first,
+  const SelectArgs a = {len, n_slots, log2_of(block), n_seq, nt, n_kv_heads, slots, n_nodes, scores, ld, n_keep, n_first,
                         n_last, blocks, status};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t grid = (size_t)rows;
-  // 16 keys a thread (1536 rows of 2048: 11.8 us, with 32 12.0, with 64 17.3, with 8 12.7), up to
+  // 16 keys a thread (1536 rows of 2048: with 32 2% slower, with 64 47%, with 8 8%), up to
   // 16384 a row (longer ones are read again for each use); the host knows no row's length,
   // but no row has more blocks than ld
   const cudaError_t e = ld <= 512    ? launch_dependent(select_kernel<32, 16>, grid, 32, 0, st, a)
