@@ -901,7 +901,7 @@ def spec_block_digest_q4(dg: KVDigest, kv: KVPagesQ4, n: int, slots, status, pos
 def _rows_of_scores(scores):
     if scores.element_size() != 4 or not scores.is_floating_point() or not scores.is_contiguous():
         raise ValueError("scores: a contiguous fp32 tensor [n_seq][nt][n_kv_heads][blocks] is required")
-    return scores.shape[-1]
+    return scores.size(-1)
 
 
 def spec_block_scores(dg: KVDigest, layer: int, n_seq: int, slots, nt: int, n_q_heads: int, q, scores,

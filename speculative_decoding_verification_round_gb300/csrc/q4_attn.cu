@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(QU_THREADS, UShape<HD, NT>::RESIDENT) q4_unit_
   constexpr int ROWS = Sh::ROWS, STAGES = Sh::STAGES, UNITS = HD / 8;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ TreeSmem s_tree;
-  grid_dep_begin();
+  // (the same, called in a row: a window of 4096 for 16 sequences 11.5 us instead of 11.7 to 14;
+  // in a graph 11.2 instead of 10.9)
+  grid_dep_wait();
   const TreeArgs& a = u.t;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % u.ranks, unit = blockIdx.x / u.ranks, kvh = unit % a.nkv, s = unit / a.nkv;
