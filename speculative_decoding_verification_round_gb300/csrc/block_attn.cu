@@ -9,6 +9,10 @@
 // results are joined in the CTA, the CTAs' through distributed shared memory: no
 // workspace, no second launch.  All rows of a unit see the same keys, so that
 // nothing is masked but the end of the last block.
+//
+// Measured (32 heads over 8 of 128): one node over 64 blocks of 64 in fp16 (17 MB) 8.9 us:
+// launch, list, page, two steps a warp, the cluster's join; 12 x 8 nodes over 64 blocks of 32
+// in 4 bits (226 MB named, 163 read) 53 us: the chain of q4_attn.cu, issue slots 54% used.
 #include <climits>
 #include <math.h>
 

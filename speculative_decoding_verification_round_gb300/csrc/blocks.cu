@@ -1,6 +1,12 @@
 // blocks.cu -- which blocks of a cache a query attends to: digests of the
 // blocks (spec_block_digest), scores from them (spec_block_scores), and the
 // selection of the largest (spec_block_select).
+//
+// Measured: 12 prompts of 4095 positions in 4 bits, 8 heads of 128, blocks of 32 (28 MB) 13 us,
+// in fp16 (101 MB) 21: the least and largest of the codes' values cost as many
+// instructions as the fp16 rows cost bytes (ALU pipe 63%); scores of their 12 x 16 nodes, 40
+// heads over 8, 9 us; a decode step of 2 sequences over 2048 blocks, digests and scores, 8.8 us in
+// two launches.
 #include <climits>
 #include <math.h>
 

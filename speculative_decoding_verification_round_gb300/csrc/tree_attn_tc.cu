@@ -10,7 +10,9 @@
 //                warps K's and two V's, into rings of two and three
 //                128-position buffers (16-byte cp.async, written in the MMA's
 //                128-byte-swizzled layout; K as a K-major operand, V as an
-//                MN-major one, so that neither is transposed)
+//                MN-major one, so that neither is transposed); of a cache in
+//                4 bits warps 14 and 15 as well, codes and scales in registers on
+//                their way to the same tiles
 //   warps 12, 13 issue S_j = Q_j K^T and O_j += P_j V, one stream each
 //   warps 0-3, 4-7  two streams j = 0, 1: a thread owns a row; it reads its
 //                scores from tensor memory, keeps the running maximum and sum
@@ -43,6 +45,11 @@
 // With weights of one fp16 number these were 181, 48 and 24.  Not kept: the high
 // parts' product under the forming of the low ones (57 -> 56 us), rings of three
 // K and two V buffers (57 -> 59; 4 x 63 nodes each).
+//
+// Over a cache in 4 bits 4 x 16 nodes over 65536 positions (302 MB) take 184 us, 1.7 a
+// tile of 64 rows: a stream's chain and the loading warps' arithmetic (four loading
+// warps with the codes in shared memory took 228, and 159 with tiles of zeros); 4 x 63
+// nodes over 8191 positions 54 us (57 with the four).
 #include <math.h>
 
 #include "common.cuh"
@@ -57,24 +64,23 @@ constexpr int K_RING = 2, V_RING = 3, TC_RING = K_RING + V_RING;
 constexpr int TC_THREADS = 512;
 constexpr int PROD_WARP = 8, MMA_WARP = 12, ALLOC_WARP = 14;
 constexpr int PROD_THREADS = 64;  // of K's loads, and of V's
-// Registers a thread: the softmax keeps a row's 128 scores.  Both pairs of
-// warpgroups together hold the 512 x 128 of the launch.
-constexpr int REGS_SOFTMAX = 200, REGS_OTHER = 56;
+// Registers a thread: the softmax keeps a row's 128 scores, a loading warp of a cache
+// in 4 bits a quarter of a tile (with 56 it spills: 4 x 32 nodes over 65536 positions 272
+// us, with 72 246).  Both pairs of warpgroups together hold the 512 x 128 of the launch.
+template <bool Q4>
+constexpr int REGS_SOFTMAX = Q4 ? 184 : 200;
+template <bool Q4>
+constexpr int REGS_OTHER = 256 - REGS_SOFTMAX<Q4>;
 constexpr float P_BIAS = 12.0f;  // log2 of the factor of weights and sum
 constexpr float P_SLACK = 3.0f;  // growth of the maximum before O is rescaled
 constexpr int P_LO = 64;         // columns from the weights' high parts to their low ones
 
-// Q4: a cache in 4 bits.  V's ring is a buffer shorter then, and each loading warp
-// has a ring of three half tiles of codes (32 rows) behind the tiles.
-template <int HD, bool Q4>
+template <int HD>
 struct TcShape {
   static constexpr int TILE = TC_KEYS * HD * 2;  // bytes of a Q, K or V tile
   static constexpr int SUB = TC_KEYS * 128;      // bytes of its 64-dimension part
   static constexpr int RING_OFF = 2 * TILE;
-  static constexpr int VR = Q4 ? V_RING - 1 : V_RING;
-  static constexpr int CODES_OFF = RING_OFF + (K_RING + VR) * TILE;
-  static constexpr int CODES = 32 * (HD / 2 + HD / 16), CODE_SLOTS = 3;  // bytes of a half tile
-  static constexpr int END = CODES_OFF + (Q4 ? 4 * CODE_SLOTS * CODES : 0);
+  static constexpr int END = RING_OFF + TC_RING * TILE;
 };
 
 struct TcSmall {
@@ -91,9 +97,9 @@ struct TcSmall {
 };
 constexpr int SMALL_MAX = 3072;
 static_assert(sizeof(TcSmall) <= SMALL_MAX, "behind the tiles");
-template <int HD, bool Q4>
+template <int HD>
 constexpr size_t tc_smem() {
-  return (size_t)TcShape<HD, Q4>::END + SMALL_MAX;
+  return (size_t)TcShape<HD>::END + SMALL_MAX;
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
@@ -213,7 +219,7 @@ __device__ __forceinline__ uint32_t low_bits(long long n) {
 
 template <int HD, int ROWS, bool Q4>
 __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeArgs a) {
-  using Sh = TcShape<HD, Q4>;
+  using Sh = TcShape<HD>;
   constexpr bool TWO = ROWS == 256;
   constexpr int UNITS = HD / 8, CH = HD / 32;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
   if (tid == 0) {
     sh.at = start;
     for (int i = 0; i < TC_RING; i++) {
-      mbar_init(bar(sh.full[i]), PROD_THREADS);
+      mbar_init(bar(sh.full[i]), Q4 ? 4 * 32 : PROD_THREADS);
       mbar_init(bar(sh.empty[i]), TWO ? 2 : 1);  // the streams that read it
     }
     mbar_init(bar(sh.q_full), 256);
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
     uint32_t slot, turn;
   };
   auto item_k = [](uint32_t x) { return Item{x % K_RING, x / K_RING}; };
-  auto item_v = [](uint32_t x) { return Item{K_RING + x % (uint32_t)Sh::VR, x / (uint32_t)Sh::VR}; };
+  auto item_v = [](uint32_t x) { return Item{K_RING + x % V_RING, x / V_RING}; };
 
   // (out of shared memory: nothing is known about them, and kept in registers, here)
   int s = sh.at.s;
@@ -307,78 +313,193 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
            (a.window > 0 && base + TC_KEYS > q.sinks && base < q.lo + SPEC_MAX_TREE);
   };
 
-  if (warp >= PROD_WARP && warp < PROD_WARP + 4) {
-    // ======================================================= the loads
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-    const bool is_k = warp < PROD_WARP + 2;
-    const int pw = warp & 1;                         // rows 64 pw .. 64 pw + 63 of a tile
-    constexpr int RPP = 32 / UNITS, PASSES = 64 / RPP;  // rows a pass of the warp
-    const int u = lane % UNITS, sub = lane / UNITS;
-    // where this lane's chunk of row RPP p + sub goes: the swizzle repeats every 8 rows
-    uint32_t dst8[8 / RPP];
+  if (warp >= PROD_WARP) {
+    // (one instruction of the whole warpgroup)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER<Q4>));
+    if (Q4 && (warp < MMA_WARP || warp >= MMA_WARP + 2)) {
+      // ======================================================= the loads of a cache in 4 bits
+      // Six warps, three for K and three for V, have every third quarter (32 rows) of the
+      // tiles: a lane a block of 32 elements, eight rows a quarter of the warp (whose 16-byte
+      // stores so lie in different banks).  The next quarter's codes and scales are on their way
+      // in registers while this one's become fp16.
+      const bool is_k = warp < PROD_WARP + 2 || warp == MMA_WARP + 2;
+      const int part = warp >= MMA_WARP ? 2 : warp & 1;
+      constexpr int CH4 = HD / 32;
+      const int b = HD == 128 ? lane >> 3 : lane >> 3 & 1;
+      auto row_at = [&](int it) { return (lane & 7) + 8 * (HD == 128 ? it : (lane >> 4) + 2 * it); };  // of the quarter
+      const uint8_t* qs = (is_k ? a.k_qs : a.v_qs) + b * 16;
+      const __half* scales = (is_k ? a.k_scales : a.v_scales) + b;
+      uint4 w[CH4];
+      uint32_t sc[CH4];
+      auto lookup = [&](int c) {  // the cache row of this lane's position of quarter c of the piece
+        const int t = t0 + (c >> 2);
+        if ((c >> 2) >= n || t == q.tiles - 1) return ~0u;
+        const int pos = tile_base(t) + 32 * (c & 3) + lane;
+        if (pos >= q.len) return ~0u;
+        const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+        const int pg = a.table[(int64_t)q.slot * a.max_pages + e];
+        if (pg < 0 || pg >= a.n_pages) return ~0u;
+        return ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
+      };
+      auto fetch = [&](uint32_t at, int it) {
+        const uint32_t x = __shfl_sync(0xffffffffu, at, row_at(it));
+        w[it] = make_uint4(0u, 0u, 0u, 0u);
+        sc[it] = 0u;
+        if (x != ~0u) {
+          w[it] = __ldg(reinterpret_cast<const uint4*>(qs + (uint64_t)x * (HD / 2)));
+          sc[it] = __half_as_ushort(__ldg(scales + (uint64_t)x * CH4));
+        }
+      };
+      // a quarter of the tree's own rows, those with infinities or NaN marked and taken out of V's
+      auto load_fresh = [&](uint32_t buf, int quarter) {
+        const __half* src = (is_k ? a.k_new : a.v_new) + (int64_t)s * a.nt * a.kv_stride + kvh * HD;
+        uint32_t bad = 0u;
+#pragma unroll 1
+        for (int e0 = lane; e0 < 32 * UNITS; e0 += 32 * CH4) {
+          uint4 v[CH4];
 #pragma unroll
-    for (int p = 0; p < 8 / RPP; p++)
-      dst8[p] = (uint32_t)((u >> 3) * Sh::SUB) + sw128_off(64 * pw + RPP * p + sub, u & 7);
-    auto dst_off = [&](int p) { return dst8[p % (8 / RPP)] + (uint32_t)(p / (8 / RPP)) * 1024u; };
-    const __half* pool = (is_k ? a.k : a.v) + u * 8;
-    const __half* fresh = (is_k ? a.k_new : a.v_new) + u * 8;
-    struct Rows {
-      uint32_t at[2];  // cache rows of the tile's rows lane and lane + 32 of the warp's 64
-    };
-    auto lookup = [&](int t) {
-      Rows x = {{~0u, ~0u}};
-      if (t == q.tiles - 1) return x;
-      const int base = tile_base(t) + 64 * pw + lane;
-      const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
+          for (int x = 0; x < CH4; x++) {
+            const int e = e0 + 32 * x, node = 32 * quarter + e / UNITS;
+            v[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (node < q.m) v[x] = *reinterpret_cast<const uint4*>(src + node * a.kv_stride + e % UNITS * 8);
+          }
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int pos = base + 32 * h;
-        if (pos < q.len) {
-          const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
-          const int pg = row[e];
-          if (pg >= 0 && pg < a.n_pages)
-            x.at[h] = ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
+          for (int x = 0; x < CH4; x++) {
+            const int e = e0 + 32 * x, r = e / UNITS, u = e % UNITS;
+            if (!is_k && odd_chunk(v[x])) {
+              bad |= 1u << r;
+              v[x] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            const uint32_t to = buf + (u >> 3) * Sh::SUB + sw128_off(32 * quarter + r, u & 7);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(v[x].x), "r"(v[x].y), "r"(v[x].z), "r"(v[x].w)
+                         : "memory");
+          }
+        }
+        return bad;
+      };
+      bool go = true;
+      for (long long left = my_tiles; left > 0 && go; left -= n, off += n, tile0 += n, seg++) {
+        next_piece(left);
+        uint32_t ahead = lookup(part + 3);
+        {
+          const uint32_t at = lookup(part);
+#pragma unroll
+          for (int it = 0; it < CH4; it++) fetch(at, it);
+        }
+        for (int c = part; c < 4 * n; c += 3) {
+          const int t = t0 + (c >> 2), quarter = c & 3;
+          const Item item = is_k ? item_k(tile0 + (c >> 2)) : item_v(tile0 + (c >> 2));
+          const uint32_t slot = item.slot, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
+          const uint32_t at = ahead;
+          ahead = lookup(c + 6);
+          go = __all_sync(0xffffffffu, wait(sh.empty[slot], item.turn + 1));
+          if (!go) break;
+          const bool tree = t == q.tiles - 1, masked = !is_k && (tree || tile_masked(t));
+          uint32_t bad = 0u;
+          if (tree) {
+            bad = load_fresh(buf, quarter);
+          } else {
+#pragma unroll
+            for (int it = 0; it < CH4; it++) {
+              const int r = row_at(it), row = 32 * quarter + r;
+              if (masked && odd_half(sc[it])) {
+                bad |= 1u << r;
+                sc[it] = 0u;
+              }
+              const uint32_t s2 = sc[it] * 0x10001u;
+              auto put = [&](int u, uint32_t wa, uint32_t wb, bool high) {
+                auto two = [&](uint32_t x) { return kw_hmul2(high ? q4_high(x) : q4_low(x), s2); };
+                const uint32_t to = buf + (u >> 3) * Sh::SUB + sw128_off(row, u & 7);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to),
+                             "r"(two(__byte_perm(wa, wa, 0x1100))), "r"(two(__byte_perm(wa, wa, 0x3322))),
+                             "r"(two(__byte_perm(wb, wb, 0x1100))), "r"(two(__byte_perm(wb, wb, 0x3322)))
+                             : "memory");
+              };
+              put(4 * b, w[it].x, w[it].y, false);
+              put(4 * b + 1, w[it].z, w[it].w, false);
+              put(4 * b + 2, w[it].x, w[it].y, true);
+              put(4 * b + 3, w[it].z, w[it].w, true);
+              fetch(at, it);
+            }
+          }
+          if (masked) {
+            bad = __reduce_or_sync(0xffffffffu, bad);
+            if (lane == 0) reinterpret_cast<uint32_t*>(sh.bad[slot])[quarter] = bad;
+          }
+          fence_proxy_async();
+          mbar_arrive(bar(sh.full[slot]));
         }
       }
-      return x;
-    };
-    // the tree's own rows to a tile
-    auto load_fresh = [&](uint32_t buf) {
-      const __half* src = fresh + (int64_t)s * a.nt * a.kv_stride + kvh * HD;
-#pragma unroll 4
-      for (int p = 0; p < PASSES; p++) {
-        const int r = 64 * pw + RPP * p + sub;
-        const bool ok = r < q.m;
-        cp16(buf + dst_off(p), src + (ok ? r : 0) * a.kv_stride, ok);
-      }
-    };
-    // a masked tile's V: chunks with infinities or NaN, which 0 * inf would spread to
-    // rows that do not see them, are taken out here and added by the rows that do
-    auto take_out = [&](uint32_t buf) {
-      unsigned long long bad = 0ull;
-#pragma unroll 4
-      for (int p = 0; p < PASSES; p++) {
-        const uint32_t at = buf + dst_off(p);
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-        if (odd_chunk(v)) {
-          bad |= 1ull << (RPP * p + sub);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
-        }
-      }
-      return bad;
-    };
-    auto mark = [&](uint32_t slot, unsigned long long bad) {
+    } else if (warp < MMA_WARP) {
+      // ======================================================= the loads
+      const bool is_k = warp < PROD_WARP + 2;
+      const int pw = warp & 1;                         // rows 64 pw .. 64 pw + 63 of a tile
+      constexpr int RPP = 32 / UNITS, PASSES = 64 / RPP;  // rows a pass of the warp
+      const int u = lane % UNITS, sub = lane / UNITS;
+      // where this lane's chunk of row RPP p + sub goes: the swizzle repeats every 8 rows
+      uint32_t dst8[8 / RPP];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-      if (lane == 0) sh.bad[slot][pw] = bad;
-    };
-    bool go = true;
-    for (long long left = my_tiles; left > 0 && go; left -= n, off += n, tile0 += n, seg++) {
-      next_piece(left);
-      // the rows of the next tile are looked up while this one waits for its buffer
-      Rows next = lookup(t0);
-      if constexpr (!Q4) {
+      for (int p = 0; p < 8 / RPP; p++)
+        dst8[p] = (uint32_t)((u >> 3) * Sh::SUB) + sw128_off(64 * pw + RPP * p + sub, u & 7);
+      auto dst_off = [&](int p) { return dst8[p % (8 / RPP)] + (uint32_t)(p / (8 / RPP)) * 1024u; };
+      const __half* pool = (is_k ? a.k : a.v) + u * 8;
+      const __half* fresh = (is_k ? a.k_new : a.v_new) + u * 8;
+      struct Rows {
+        uint32_t at[2];  // cache rows of the tile's rows lane and lane + 32 of the warp's 64
+      };
+      auto lookup = [&](int t) {
+        Rows x = {{~0u, ~0u}};
+        if (t == q.tiles - 1) return x;
+        const int base = tile_base(t) + 64 * pw + lane;
+        const int32_t* row = a.table + (int64_t)q.slot * a.max_pages;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int pos = base + 32 * h;
+          if (pos < q.len) {
+            const int e = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+            const int pg = row[e];
+            if (pg >= 0 && pg < a.n_pages)
+              x.at[h] = ((uint32_t)pg * a.nkv + kvh) * a.page_size + (uint32_t)(pos - e * a.page_size);
+          }
+        }
+        return x;
+      };
+      // the tree's own rows to a tile
+      auto load_fresh = [&](uint32_t buf) {
+        const __half* src = fresh + (int64_t)s * a.nt * a.kv_stride + kvh * HD;
+#pragma unroll 4
+        for (int p = 0; p < PASSES; p++) {
+          const int r = 64 * pw + RPP * p + sub;
+          const bool ok = r < q.m;
+          cp16(buf + dst_off(p), src + (ok ? r : 0) * a.kv_stride, ok);
+        }
+      };
+      // a masked tile's V: chunks with infinities or NaN, which 0 * inf would spread to
+      // rows that do not see them, are taken out here and added by the rows that do
+      auto take_out = [&](uint32_t buf) {
+        unsigned long long bad = 0ull;
+#pragma unroll 4
+        for (int p = 0; p < PASSES; p++) {
+          const uint32_t at = buf + dst_off(p);
+          uint4 v;
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+          if (odd_chunk(v)) {
+            bad |= 1ull << (RPP * p + sub);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+          }
+        }
+        return bad;
+      };
+      auto mark = [&](uint32_t slot, unsigned long long bad) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+        if (lane == 0) sh.bad[slot][pw] = bad;
+      };
+      bool go = true;
+      for (long long left = my_tiles; left > 0 && go; left -= n, off += n, tile0 += n, seg++) {
+        next_piece(left);
+        // the rows of the next tile are looked up while this one waits for its buffer
+        Rows next = lookup(t0);
         for (int i = 0; i < n; i++) {
           const int t = t0 + i;
           const Item item = is_k ? item_k(tile0 + i) : item_v(tile0 + i);
@@ -406,190 +527,101 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
           fence_proxy_async();
           mbar_arrive(bar(sh.full[slot]));
         }
-      } else {
-        // codes and scales of half tiles, three of them on their way, become the tile's
-        // rows: a block of 32 elements a lane, eight rows a quarter of the warp (whose 16-byte
-        // stores so lie in different banks)
-        constexpr int CB = HD / 2, SB = HD / 16, CH4 = HD / 32, PER4 = 32 / CH4;
-        const uint32_t ring = sm0 + Sh::CODES_OFF + (warp - PROD_WARP) * (Sh::CODE_SLOTS * Sh::CODES);
-        const uint8_t* qs = is_k ? a.k_qs : a.v_qs;
-        const __half* scales = is_k ? a.k_scales : a.v_scales;
-        auto swz = [](int r) { return HD == 128 ? r >> 1 & 3 : r >> 2 & 1; };
-        auto stage = [&](int c) {  // half tile c of the piece
-          const int i = c >> 1, t = t0 + i;
-          if (i < n && t != q.tiles - 1) {
-            const uint32_t at = c & 1 ? next.at[1] : next.at[0], to = ring + (c % Sh::CODE_SLOTS) * Sh::CODES;
-            const int u4 = lane % CH4;
-#pragma unroll
-            for (int p = 0; p < CH4; p++) {
-              const int r = p * PER4 + lane / CH4;
-              const uint32_t x = __shfl_sync(0xffffffffu, at, r);
-              const bool ok = x != ~0u;
-              cp16(to + r * CB + ((u4 ^ swz(r)) << 4), qs + (uint64_t)(ok ? x : 0u) * CB + u4 * 16, ok);
-            }
-            const bool ok = at != ~0u;
-            kw_copy<SB>(to + 32 * CB + lane * SB, scales + (uint64_t)(ok ? at : 0u) * CH4, ok);
-          }
-          asm volatile("cp.async.commit_group;");
-          if ((c & 1) && i + 1 < n) next = lookup(t + 1);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // ======================================================= the products
+      // One warp per stream, which runs as a whole and issues through one
+      // elected lane: with warp-uniform control an MMA of 128 x 128 x 16 issues
+      // in less than the 64 cycles that it takes, under a branch on the lane in
+      // about 110.
+      const int j = warp - MMA_WARP;
+      if (j < 2) {
+        // a negative scale: the scores' sign is turned by the MMA (negated A),
+        // so that a row's maximum is the maximum of what is read
+        const uint32_t id_s = idesc_f16(TC_KEYS) | (a.scale_log2 < 0.0f ? 1u << 13 : 0u);
+        const uint32_t id_o = idesc_f16(HD) | (1u << 16);
+        const uint64_t d_q = smem_desc_sw128(sm0 + (TWO ? j * Sh::TILE : 0));
+        const uint64_t d_k = smem_desc_sw128(sm0 + Sh::RING_OFF), d_v = smem_desc_mn(sm0 + Sh::RING_OFF, Sh::SUB);
+        const uint32_t tS = tmem + j * 128, tO = tmem + 256 + j * 128;
+        uint32_t n_p = 0;  // the stream's tiles so far
+        // Whether the products go on, by what this lane has waited for: once a
+        // wait has given up nothing is issued any more, while the turns below are
+        // still handed over.
+        bool go = true;
+        auto wait_item = [&](const Item& item) {
+          go = wait(sh.full[item.slot], item.turn) && go;
+          __syncwarp();
+          fence_proxy_async();  // the copies, to the tensor core's proxy
         };
-        __syncwarp();  // the last piece's half tiles have been read
-        stage(0);
-        stage(1);
-        unsigned long long bad = 0ull;
-        for (int c = 0; c < 2 * n; c++) {
-          const int t = t0 + (c >> 1), half = c & 1;
-          const Item item = is_k ? item_k(tile0 + (c >> 1)) : item_v(tile0 + (c >> 1));
-          const uint32_t slot = item.slot, buf = sm0 + Sh::RING_OFF + slot * Sh::TILE;
-          __syncwarp();  // half tile c - 1 has been read
-          stage(c + 2);
-          if (half == 0) {
-            go = __all_sync(0xffffffffu, wait(sh.empty[slot], item.turn + 1));
-            if (!go) break;
-            bad = 0ull;
-          }
-          if (t == q.tiles - 1) {  // (both halves at once)
-            if (half == 1) continue;
-            load_fresh(buf);
-            if (is_k) {
-              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(sh.full[slot])) : "memory");
-              continue;
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            mark(slot, take_out(buf));
-            fence_proxy_async();
-            mbar_arrive(bar(sh.full[slot]));
-            continue;
-          }
-          const bool masked = !is_k && tile_masked(t);
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
-          __syncwarp();
-          const uint32_t from = ring + (c % Sh::CODE_SLOTS) * Sh::CODES;
-#pragma unroll 2
-          for (int it = 0; it < CH4; it++) {
-            const int r = HD == 128 ? (lane & 7) + 8 * it : (lane & 7) + 8 * ((lane >> 4) + 2 * it);
-            const int b = HD == 128 ? lane >> 3 : lane >> 3 & 1, row = 64 * pw + 32 * half + r;
-            const uint4 w = kw_lds128(from + r * CB + ((b ^ swz(r)) << 4));
-            uint32_t sc = kw_lds16(from + 32 * CB + r * SB + 2 * b);
-            if (masked && odd_half(sc)) {
-              bad |= 1ull << (32 * half + r);
-              sc = 0u;
-            }
-            const uint32_t s2 = sc * 0x10001u;
-            auto put = [&](int u, uint32_t wa, uint32_t wb, bool high) {
-              auto two = [&](uint32_t x) { return kw_hmul2(high ? q4_high(x) : q4_low(x), s2); };
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + (u >> 3) * Sh::SUB + sw128_off(row, u & 7)),
-                           "r"(two(__byte_perm(wa, wa, 0x1100))), "r"(two(__byte_perm(wa, wa, 0x3322))),
-                           "r"(two(__byte_perm(wb, wb, 0x1100))), "r"(two(__byte_perm(wb, wb, 0x3322)))
-                           : "memory");
-            };
-            put(4 * b, w.x, w.y, false);
-            put(4 * b + 1, w.z, w.w, false);
-            put(4 * b + 2, w.x, w.y, true);
-            put(4 * b + 3, w.z, w.w, true);
-          }
-          if (half == 1) {
-            if (masked) mark(slot, bad);
-            fence_proxy_async();
-            mbar_arrive(bar(sh.full[slot]));
-          }
-        }
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp >= MMA_WARP) {
-    // ======================================================= the products
-    // One warp per stream, which runs as a whole and issues through one
-    // elected lane: with warp-uniform control an MMA of 128 x 128 x 16 issues
-    // in less than the 64 cycles that it takes, under a branch on the lane in
-    // about 110.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-    const int j = warp - MMA_WARP;
-    if (j < 2) {
-      // a negative scale: the scores' sign is turned by the MMA (negated A),
-      // so that a row's maximum is the maximum of what is read
-      const uint32_t id_s = idesc_f16(TC_KEYS) | (a.scale_log2 < 0.0f ? 1u << 13 : 0u);
-      const uint32_t id_o = idesc_f16(HD) | (1u << 16);
-      const uint64_t d_q = smem_desc_sw128(sm0 + (TWO ? j * Sh::TILE : 0));
-      const uint64_t d_k = smem_desc_sw128(sm0 + Sh::RING_OFF), d_v = smem_desc_mn(sm0 + Sh::RING_OFF, Sh::SUB);
-      const uint32_t tS = tmem + j * 128, tO = tmem + 256 + j * 128;
-      uint32_t n_p = 0;  // the stream's tiles so far
-      // Whether the products go on, by what this lane has waited for: once a
-      // wait has given up nothing is issued any more, while the turns below are
-      // still handed over.
-      bool go = true;
-      auto wait_item = [&](const Item& item) {
-        go = wait(sh.full[item.slot], item.turn) && go;
-        __syncwarp();
-        fence_proxy_async();  // the copies, to the tensor core's proxy
-      };
-      auto scores = [&](const Item& item) {
-        wait_item(item);
-        const uint64_t dk = d_k + item.slot * (uint32_t)(Sh::TILE >> 4);
-        if (elect_one() && go) {
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; kk++) {
-            const uint32_t o = ((kk >> 2) * Sh::SUB + (kk & 3) * 32) >> 4;
-            tc_mma(tS, d_q + o, dk + o, id_s, kk > 0);
-          }
-          tc_commit(bar(sh.s_full[j]));
-          tc_commit(bar(sh.empty[item.slot]));
-        }
-        __syncwarp();
-      };
-      // The streams take turns, each with its P V and its next S in one go: were
-      // both streams' products mixed, both would wait for theirs, and then
-      // both be in their softmax, with the tensor core idle.  These barriers
-      // have no limit of their own, and need none: both warps go through the
-      // same pieces and tiles whatever their bounded waits say, and meet
-      // between two pieces, so that no barrier is arrived at twice.
-      auto hand_over = [](int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); };
-      auto take_over = [](int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); };
-      constexpr int TURN_0_1 = 4, TURN_1_0 = 5, START_0_1 = 6, PIECE = 7;
-      for (long long left = my_tiles; left > 0; left -= n, off += n, tile0 += n, seg++) {
-        next_piece(left);
-        const int step = TWO ? 1 : 2;
-        int i = TWO ? 0 : j;
-        if (seg > 0) take_over(PIECE);
-        go = wait(sh.q_full, seg) && go;  // (without a tile, too: a phase each piece)
-        __syncwarp();
-        if (i >= n) continue;
-        if (j == 1) take_over(START_0_1);
-        scores(item_k(tile0 + i));
-        if (j == 0 && (TWO || n > 1)) hand_over(START_0_1);
-        for (; i < n; i += step) {
-          const Item vi = item_v(tile0 + i);
-          const uint64_t dv = d_v + vi.slot * (uint32_t)(Sh::TILE >> 4);
-          wait_item(vi);
-          go = wait(sh.p_ready[j], n_p++) && go;
-          __syncwarp();
-          tc_fence_after();
-          if (j == 1 || i > 0) take_over(j == 1 ? TURN_0_1 : TURN_1_0);
+        auto scores = [&](const Item& item) {
+          wait_item(item);
+          const uint64_t dk = d_k + item.slot * (uint32_t)(Sh::TILE >> 4);
           if (elect_one() && go) {
-#pragma unroll 1  // (sixteen in a row take registers that this warp does not have)
-            for (int lo = 0; lo <= P_LO; lo += P_LO)
 #pragma unroll
-              for (int kk = 0; kk < TC_KEYS / 16; kk++)
-                tc_mma_ta(tO, tS + lo + 8 * kk, dv + ((kk * 2048) >> 4), id_o, 1u);
-            tc_commit(bar(sh.empty[vi.slot]));
-            if (i + step >= n) tc_commit(bar(sh.o_done[j]));  // the stream's last tile
+            for (int kk = 0; kk < HD / 16; kk++) {
+              const uint32_t o = ((kk >> 2) * Sh::SUB + (kk & 3) * 32) >> 4;
+              tc_mma(tS, d_q + o, dk + o, id_s, kk > 0);
+            }
+            tc_commit(bar(sh.s_full[j]));
+            tc_commit(bar(sh.empty[item.slot]));
           }
           __syncwarp();
-          if (i + step < n) scores(item_k(tile0 + i + step));
-          if (TWO ? j == 0 || i + 1 < n : i + 1 < n) hand_over(j == 0 ? TURN_0_1 : TURN_1_0);
+        };
+        // The streams take turns, each with its P V and its next S in one go: were
+        // both streams' products mixed, both would wait for theirs, and then
+        // both be in their softmax, with the tensor core idle.  These barriers
+        // have no limit of their own, and need none: both warps go through the
+        // same pieces and tiles whatever their bounded waits say, and meet
+        // between two pieces, so that no barrier is arrived at twice.
+        auto hand_over = [](int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); };
+        auto take_over = [](int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); };
+        constexpr int TURN_0_1 = 4, TURN_1_0 = 5, START_0_1 = 6, PIECE = 7;
+        for (long long left = my_tiles; left > 0; left -= n, off += n, tile0 += n, seg++) {
+          next_piece(left);
+          const int step = TWO ? 1 : 2;
+          int i = TWO ? 0 : j;
+          if (seg > 0) take_over(PIECE);
+          go = wait(sh.q_full, seg) && go;  // (without a tile, too: a phase each piece)
+          __syncwarp();
+          if (i >= n) continue;
+          if (j == 1) take_over(START_0_1);
+          scores(item_k(tile0 + i));
+          if (j == 0 && (TWO || n > 1)) hand_over(START_0_1);
+          for (; i < n; i += step) {
+            const Item vi = item_v(tile0 + i);
+            const uint64_t dv = d_v + vi.slot * (uint32_t)(Sh::TILE >> 4);
+            wait_item(vi);
+            go = wait(sh.p_ready[j], n_p++) && go;
+            __syncwarp();
+            tc_fence_after();
+            if (j == 1 || i > 0) take_over(j == 1 ? TURN_0_1 : TURN_1_0);
+            if (elect_one() && go) {
+#pragma unroll 1  // (sixteen in a row take registers that this warp does not have)
+              for (int lo = 0; lo <= P_LO; lo += P_LO)
+#pragma unroll
+                for (int kk = 0; kk < TC_KEYS / 16; kk++)
+                  tc_mma_ta(tO, tS + lo + 8 * kk, dv + ((kk * 2048) >> 4), id_o, 1u);
+              tc_commit(bar(sh.empty[vi.slot]));
+              if (i + step >= n) tc_commit(bar(sh.o_done[j]));  // the stream's last tile
+            }
+            __syncwarp();
+            if (i + step < n) scores(item_k(tile0 + i + step));
+            if (TWO ? j == 0 || i + 1 < n : i + 1 < n) hand_over(j == 0 ? TURN_0_1 : TURN_1_0);
+          }
         }
+        // the products that were issued have ended before this CTA's memory is
+        // another's: with the full budget, whether a wait has given up or not
+        if (elect_one()) tc_commit(bar(sh.drain[j]));
+        __syncwarp();
+        if (!mbar_wait(bar(sh.drain[j]), 0u, LIN_WAIT_TRIES)) *abort_flag = 1;
       }
-      // the products that were issued have ended before this CTA's memory is
-      // another's: with the full budget, whether a wait has given up or not
-      if (elect_one()) tc_commit(bar(sh.drain[j]));
       __syncwarp();
-      if (!mbar_wait(bar(sh.drain[j]), 0u, LIN_WAIT_TRIES)) *abort_flag = 1;
     }
-    __syncwarp();
   } else {
     // ======================================================= the softmax
     check_others<TC_THREADS>(a, ROWS, TC_SHIFT, n_cta, 8);  // (here, as the first keys are on their way)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX<Q4>));
     const int j = warp >> 2, r = tid & 127;  // stream, lane of tensor memory
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + j * 128, tO = tmem + lanes + 256 + j * 128;
@@ -949,7 +981,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
 
 template <int HD, int ROWS, bool Q4>
 cudaError_t launch(const TreeArgs& a, int n_cta, cudaStream_t st) {
-  return launch_dependent(tree_attn_tc_kernel<HD, ROWS, Q4>, n_cta + 1, TC_THREADS, tc_smem<HD, Q4>(), st, a);
+  return launch_dependent(tree_attn_tc_kernel<HD, ROWS, Q4>, n_cta + 1, TC_THREADS, tc_smem<HD>(), st, a);
 }
 
 template <int HD, bool Q4>
@@ -962,7 +994,7 @@ cudaError_t launch_rows(const TreeArgs& a, int n_cta, cudaStream_t st) {
 template <int HD, int ROWS, bool Q4>
 void init() {
   cudaFuncSetAttribute(tree_attn_tc_kernel<HD, ROWS, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)tc_smem<HD, Q4>());
+                       (int)tc_smem<HD>());
 }
 template <int HD, bool Q4>
 void init_rows() {
