@@ -4,7 +4,7 @@
 //
 // Measured: 12 prompts of 4095 positions in 4 bits, 8 heads of 128, blocks of 32 (28 MB) 13 us,
 // in fp16 (101 MB) 21: the least and largest of the codes' values cost as many
-// instructions as the fp16 rows cost bytes (ALU pipe 63%); scores of their 12 x 16 nodes, 40
+// instructions as the fp16 rows cost bytes (ALU pipe 60%); scores of their 12 x 16 nodes, 40
 // heads over 8, 9 us; a decode step of 2 sequences over 2048 blocks, digests and scores, 8.8 us in
 // two launches.
 #include <climits>

@@ -8,8 +8,9 @@
 //
 // Measured: two prompts of 4097 rows, 8 layers, 8 heads of 128 (253 MB of fp16, 71 of codes
 // and scales): commit 73 us, 4.4 TB/s, 68% of the issue slots: the arithmetic of the
-// quantisation; reading back 64 us, where a plain fill of as many bytes takes 62: the
-// writes.  12 paths of up to 16 nodes in 40 layers: 11 and 7 us: the launch, then slot,
+// quantisation; reading back 65 us, 5.0 TB/s, reads and writes together (a plain write of its
+// output alone takes 37).  A head's rows to a warp, whose codes are neighbours, 78 and 63;
+// more rows in flight, more and fewer rows a CTA, stores of 32 bytes: no better.  12 paths of up to 16 nodes in 40 layers: 11 and 7 us: the launch, then slot,
 // length and page in front of the first row.
 #include <algorithm>
 #include <climits>

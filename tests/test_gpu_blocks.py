@@ -6,6 +6,7 @@ import pytest
 
 from oracle import long_context as lc
 from oracle import tree
+from test_gpu_attn import attn_model
 from test_gpu_q4 import Q4Case
 from test_gpu_tree import Case
 
@@ -451,6 +452,46 @@ def test_digests_of_copied_pages(dev):
     check(0), check(1)
     grow(0, 30, 64)
     check(0), check(1)
+
+
+def test_the_models_own_cache(dev):
+    """A model's slots as pages: digests beside them, a selection, attention over lists of
+    all blocks as tree attention."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(18)
+    nq, nkv, hd, nt, max_ctx, block, n = 8, 2, 128, 7, 224, 32, 150
+    m = attn_model(sv, dev, g, nq, nkv, hd, max_ctx, nt, 3)
+    kv = sv.spec_model_pages(m)
+    f16 = lambda *s: torch.from_numpy(g.standard_normal(s).astype(np.float16)).to(dev)  # noqa: E731
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    kc, vc = f16(nkv, n, hd), f16(nkv, n, hd)
+    sv.spec_kv_fill(m, 0, 1, 0, n, kc, vc)
+    sv.spec_state_set(m, [1], n_past=[n], anchor=[3])
+    layers = kv.pages.n_layers
+    data = torch.zeros((layers, 3, nkv, max_ctx // block, 2, hd), dtype=torch.float16, device=dev)
+    lens, slots, st = i32([0, n, 0]), i32([1]), i32([9])
+    dg = sv.KVDigest(data, block, i32([[0], [1], [2]]), lens)
+    sv.spec_block_digest(dg, kv, 1, slots, st)
+    assert st.item() == 0
+    k = kc.cpu().numpy()
+    for h in range(nkv):
+        for j in range(5):
+            assert np.array_equal(data[0, 1, h, j].cpu().numpy(), lc.digest(k[h, block * j:block * (j + 1)]))
+    q, kn, vn = f16(1, nt, nq, hd), f16(1, nt, nkv, hd), f16(1, nt, nkv, hd)
+    scores = torch.zeros((1, nt, nkv, max_ctx // block), device=dev)
+    blocks, row_st = i32(np.zeros((1, nt, nkv, 5)).tolist()), i32(np.zeros((1, nt, nkv)).tolist())
+    sv.spec_block_scores(dg, 0, 1, slots, nt, nq, q, scores, st)
+    sv.spec_block_select(lens, block, 1, slots, nt, nkv, scores, 5, blocks, st)
+    assert st.item() == 0 and (blocks == i32([0, 1, 2, 3, 4])).all()
+    outs = [torch.zeros((1, nt, nq, hd), dtype=torch.float16, device=dev) for _ in range(2)]
+    sv.spec_block_attn(kv, 0, 1, slots, nt, nq, block, 5, blocks, q, kn, vn, outs[0], row_st)
+    ws = torch.empty(sv.spec_tree_attn_workspace(kv, 1, nt, nq), dtype=torch.uint8, device=dev)
+    sv.spec_tree_attn(kv, 0, 1, slots, nt, nq, q, kn, vn, outs[1], ws, st)
+    assert st.item() == 0 and (row_st == 0).all()
+    # each within half an fp16 step (and the far smaller fp32 error) of the same value
+    err = (outs[0].double() - outs[1].double()).abs()
+    assert (err <= 2.0 ** -10 * outs[1].double().abs() + 2.0 ** -16).all()
 
 
 def test_captured_rounds(dev):
