@@ -412,7 +412,7 @@ struct SelectArgs {
 };
 
 template <int THREADS, int PER>
-__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS == 128 && PER == 16 ? 10 : 1) select_kernel(const SelectArgs a) {
   constexpr int WARPS = THREADS / 32, SPAN = THREADS * PER, CAND = 256, WORDS = SPAN / 32;
   constexpr int BIN_BITS = THREADS <= 64 ? 9 : 10, BINS = 1 << BIN_BITS, EACH = BINS / THREADS;
   static_assert(WORDS <= THREADS && PER <= 32, "a word a thread, a lane for each of a thread's keys");
@@ -795,10 +795,16 @@ extern "C" int spec_block_select(const int32_t* len, int n_slots, int block, int
                         n_last, blocks, status};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t grid = (size_t)rows;
-  // 16 keys a thread (1536 rows of 2048: with 32 2% slower, with 64 47%, with 8 8%), up to
-  // 16384 a row (longer ones are read again for each use); the host knows no row's length,
-  // but no row has more blocks than ld
-  const cudaError_t e = ld <= 512    ? launch_dependent(select_kernel<32, 16>, grid, 32, 0, st, a)
+  // 16 keys a thread (1536 rows of 2048: with 32 2% slower, with 64 47%, with 8 28%), up to
+  // 16384 a row (longer ones are read again for each use); for no more rows than SMs, each
+  // with an SM to itself, 4 (8 rows of 500 3.3 us, with 8 3.8, with 16 4.9) or 8 (of 2048 3.8, 3.7,
+  // 4.4; of 4096 5.8, 4.3, 4.5; of 8192 with 8 7.2, with 16 5.7).  The host knows no row's length, but no row has more blocks than ld.
+  const bool few = rows <= device_sms() && ld <= 4096;
+  const cudaError_t e = few ? (ld <= 512    ? launch_dependent(select_kernel<128, 4>, grid, 128, 0, st, a)
+                               : ld <= 1024 ? launch_dependent(select_kernel<256, 4>, grid, 256, 0, st, a)
+                               : ld <= 2048 ? launch_dependent(select_kernel<256, 8>, grid, 256, 0, st, a)
+                                            : launch_dependent(select_kernel<512, 8>, grid, 512, 0, st, a))
+                        : ld <= 512  ? launch_dependent(select_kernel<32, 16>, grid, 32, 0, st, a)
                         : ld <= 1024 ? launch_dependent(select_kernel<64, 16>, grid, 64, 0, st, a)
                         : ld <= 2048 ? launch_dependent(select_kernel<128, 16>, grid, 128, 0, st, a)
                         : ld <= 4096 ? launch_dependent(select_kernel<256, 16>, grid, 256, 0, st, a)

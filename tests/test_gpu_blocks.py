@@ -273,6 +273,32 @@ def test_selections(dev, nb, keep):
                     assert got[b, i, h].tolist() == lc.select(x[b, i, h] + np.float32(0), nb, keep, first, last), (b, i, h)
 
 
+@pytest.mark.parametrize("n,nt,nkv,nb,keep", [(1, 2, 3, 700, 30), (2, 2, 2, 3000, 64), (4, 9, 6, 77, 5), (5, 8, 8, 500, 64),
+                                             (4, 16, 5, 1000, 9), (3, 64, 2, 2040, 200), (6, 12, 4, 4090, 33)])
+def test_selections_of_few_and_many_rows(dev, n, nt, nkv, nb, keep):
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng([nb, n])
+    x = np.round(20 + 3 * g.standard_normal((n, nt, nkv, nb)) ** 3, 2).astype(np.float32)
+    lens = g.integers(0, nb * 32 + 1, n).astype(np.int32)
+    lens[0] = nb * 32
+    counts = g.integers(0, nt + 1, n).astype(np.int32)
+    counts[0] = nt
+    T = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    st = torch.full((n,), 9, dtype=torch.int32, device=dev)
+    out = torch.full((n, nt, nkv, keep), 77, dtype=torch.int32, device=dev)
+    sv.spec_block_select(T(lens), 32, n, T(np.arange(n, dtype=np.int32)), nt, nkv, T(x), keep, out, st, n_nodes=T(counts))
+    assert st.tolist() == [0] * n
+    got = out.cpu().numpy()
+    for b in range(n):
+        assert (got[b, counts[b]:] == 77).all()
+        blocks = -(-int(lens[b]) // 32)
+        for i in range(counts[b]):
+            for h in range(nkv):
+                want = lc.select(x[b, i, h], blocks, keep, 1, 1)
+                assert got[b, i, h].tolist() == want + [-1] * (keep - len(want)), (b, i, h)
+
+
 def test_selection_refusals(dev):
     import torch
     import speculative_decoding_verification_round_gb300 as sv
