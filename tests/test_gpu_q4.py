@@ -253,6 +253,29 @@ def test_repeated_calls_agree(dev, nq, nkv, hd, n, longest, nt):
         assert torch.equal(out.view(torch.int16), want.view(torch.int16))
 
 
+def test_two_streams_at_once(dev):
+    """Calls of all three kernels, two of each at a time with workspaces of their own."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    for nq, lens, nt in ((8, [300, 90], 1), (16, [20000, 90], 3), (40, [900, 130], 9)):
+        sides = []
+        for i in range(2):
+            c = Q4Case(sv, dev, np.random.default_rng([nt, i]), nq, 2, 128, lens, nt, 32, layers=1)
+            want = c.call()
+            c.check(want)
+            kv = c.pool()
+            ws = torch.empty(sv.spec_tree_attn_q4_workspace(kv, 2, nt, nq), dtype=torch.uint8, device=dev)
+            args = [c.T(a) for a in (c.slots, c.q, c.kn, c.vn, c.parents)]
+            sides.append((kv, ws, args, c.out.clone(), torch.zeros_like(c.out), c.status, torch.cuda.Stream()))
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for kv, ws, (slots, q, kn, vn, par), want, out, st, stream in sides:
+                sv.spec_tree_attn_q4(kv, 0, 2, slots, nt, nq, q, kn, vn, out, ws, st, parents=par, stream=stream)
+        torch.cuda.synchronize()
+        for _, _, _, want, out, st, _ in sides:
+            assert torch.equal(out, want) and st.tolist() == [0, 0]
+
+
 def test_waits_that_give_up(dev):
     """Every CTA's first wait for scores gives up at once: its sequences are NaN
     with SPEC_ST_TIMEOUT, and the next call is served."""
