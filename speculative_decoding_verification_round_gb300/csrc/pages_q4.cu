@@ -8,10 +8,10 @@
 //
 // Measured: two prompts of 4097 rows, 8 layers, 8 heads of 128 (253 MB of fp16, 71 of codes
 // and scales): commit 73 us, 4.4 TB/s, 68% of the issue slots: the arithmetic of the
-// quantisation; reading back 65 us, 5.0 TB/s, reads and writes together (a plain write of its
-// output alone takes 37).  A head's rows to a warp, whose codes are neighbours, 78 and 63;
-// more rows in flight, more and fewer rows a CTA, stores of 32 bytes: no better.  12 paths of up to 16 nodes in 40 layers: 11 and 7 us: the launch, then slot,
-// length and page in front of the first row.
+// quantisation; reading back 53.5 us, 6.1 TB/s, reads and writes together.  A head's rows to
+// a warp, whose codes are neighbours, 78 and 63 (with 32 rows a CTA in the read 65); more rows
+// in flight or stores of 32 bytes: no better.  12 paths of up to 16 nodes in 40 layers: 10.5
+// and 6.3 us: the launch, then slot, length and page in front of the first row.
 #include <algorithm>
 #include <climits>
 
@@ -135,15 +135,18 @@ __device__ __forceinline__ Half quantise(const uint4& low, const uint4& high) {
 // warp takes 512 neighbouring elements of K or V, half a block a lane, of every row (every
 // second, fourth or eighth one where a row is shorter than 2048 elements), so that what a
 // lane's place in the row is, is found once; CQ_FLIGHT rows are in flight.
-constexpr int CQ_ROWS = 32, CQ_FLIGHT = 2, PQ_WARPS = PQ_THREADS / 32;
+constexpr int CQ_ROWS = 32, CQ_FLIGHT = 2;
+constexpr int RQ_THREADS = 128;  // of the read, with 8 or 16 rows
 
 // Where the rows of a CTA lie in the cache (of head 0), in blocks.
+template <int ROWS>
 struct RowPlace {
-  int64_t at[CQ_ROWS];
+  int64_t at[ROWS];
 };
+template <int THREADS, int ROWS>
 __device__ __forceinline__ void place_rows(const spec_pages_q4& kv, int layer, const int32_t* row, int pos0, int r0, int r1,
-                                           RowPlace& p) {
-  for (int j = r0 + threadIdx.x; j < r1; j += PQ_THREADS) {
+                                           RowPlace<ROWS>& p) {
+  for (int j = r0 + threadIdx.x; j < r1; j += THREADS) {
     const int pos = pos0 + j, e = pos / kv.page_size;  // (below 2^31)
     p.at[j - r0] = ((int64_t)layer * kv.layer_stride + (int64_t)row[e] * kv.n_kv_heads * kv.page_size + pos -
                     e * kv.page_size) * (kv.head_dim / 32);
@@ -153,11 +156,12 @@ __device__ __forceinline__ void place_rows(const spec_pages_q4& kv, int layer, c
 // them, below r1), this lane's first element e of a row (and eight from e + 16 on), and how many
 // blocks behind the row's place (of head 0) its block is; `ok` false for lanes past the
 // row.  Whole warps.
-template <class F>
+template <int THREADS, class F>
 __device__ __forceinline__ void each_piece(const spec_pages_q4& kv, int r0, int r1, F&& f) {
   const int nb = kv.head_dim / 32, blocks = kv.n_kv_heads * nb, per = (blocks + 15) / 16;
-  const int lane = threadIdx.x & 31, step = per >= PQ_WARPS / 2 ? 1 : PQ_WARPS / 2 / per;
-  for (int item = threadIdx.x >> 5; item < per * step * 2; item += PQ_WARPS) {
+  constexpr int WARPS = THREADS / 32;
+  const int lane = threadIdx.x & 31, step = per >= WARPS / 2 ? 1 : WARPS / 2 / per;
+  for (int item = threadIdx.x >> 5; item < per * step * 2; item += WARPS) {
     const int part = item >> 1, phase = part / per, b = (part - phase * per) * 16 + (lane >> 1);
     const bool ok = b < blocks;
     const int h = ok ? b / nb : 0, e = ok ? 32 * b + 8 * (lane & 1) : 0;
@@ -171,7 +175,7 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
                  const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new, int64_t new_layer_stride,
                  const int32_t* __restrict__ path, const int32_t* __restrict__ n_path,
                  int32_t* __restrict__ new_len, int blocks, int32_t* __restrict__ status) {
-  __shared__ RowPlace place;
+  __shared__ RowPlace<CQ_ROWS> place;
   __shared__ int s_node[CQ_ROWS];
   // (No early launch of what follows: its waiting CTAs would take the room of the next ones here,
   // 20.4 us for 8 entries' commit and read instead of 16.4; without programmatic
@@ -207,7 +211,7 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
       else if (kv.refs != nullptr && kv.refs[p] != 1)
         bits |= SPEC_ST_SHARED;
     }
-    place_rows(kv, layer, row, len, r0, r1, place);
+    place_rows<PQ_THREADS>(kv, layer, row, len, r0, r1, place);
     for (int j = r0 + threadIdx.x; j < r1; j += PQ_THREADS) s_node[j - r0] = pth != nullptr ? pth[j] : j;
   }
   if (__syncthreads_or(bits))
@@ -222,7 +226,7 @@ q4_commit_kernel(const spec_pages_q4 kv, int n, const int32_t* __restrict__ slot
   const int64_t src0 = (int64_t)layer * new_layer_stride + (int64_t)i * nt * node;
   const int l = threadIdx.x & 1;
   constexpr int U = CQ_FLIGHT;
-  each_piece(kv, r0, r1, [&](int which, int r, int step, int e, int64_t block, bool ok) {
+  each_piece<PQ_THREADS>(kv, r0, r1, [&](int which, int r, int step, int e, int64_t block, bool ok) {
     const uint16_t* src = (which ? v_new : k_new) + src0 + e;
     uint4 x[U][2];
 #pragma unroll
@@ -278,11 +282,12 @@ __device__ __forceinline__ uint4 eight_values(uint2 c, uint32_t s) {
 }
 
 // Rows out of the cache.
-__global__ void __launch_bounds__(PQ_THREADS, 6)
+template <int ROWS>
+__global__ void __launch_bounds__(RQ_THREADS, 12)
 q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt, const int32_t* __restrict__ pos0,
                const int32_t* __restrict__ n_pos, uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                int64_t layer_stride, int blocks, int32_t* __restrict__ status) {
-  __shared__ RowPlace place;
+  __shared__ RowPlace<ROWS> place;
   grid_dep_wait();
   const int i = blockIdx.x / (kv.n_layers * blocks);
   const int layer = blockIdx.x / blocks % kv.n_layers, blk = blockIdx.x % blocks;
@@ -292,12 +297,12 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
   if (np < 0 || np > nt) st |= SPEC_ST_TREE;
   if (p0 < 0 || (int64_t)p0 + max(np, 0) > (int64_t)kv.max_pages * kv.page_size) st |= SPEC_ST_FULL;
   const int32_t* row = kv.table + (int64_t)(st == 0 ? slot : 0) * kv.max_pages;
-  const int r0 = blk * CQ_ROWS, r1 = min(np, r0 + CQ_ROWS);
+  const int r0 = blk * ROWS, r1 = min(np, r0 + ROWS);
   bool bad = false;
   if (st == 0 && np > 0) {
     const int e1 = (int)(((int64_t)p0 + np - 1) / kv.page_size);
-    for (int e = p0 / kv.page_size + threadIdx.x; e <= e1; e += PQ_THREADS) bad |= row[e] < 0 || row[e] >= kv.n_pages;
-    place_rows(kv, layer, row, p0, r0, r1, place);
+    for (int e = p0 / kv.page_size + threadIdx.x; e <= e1; e += RQ_THREADS) bad |= row[e] < 0 || row[e] >= kv.n_pages;
+    place_rows<RQ_THREADS>(kv, layer, row, p0, r0, r1, place);
   }
   if (__syncthreads_or(bad)) st |= SPEC_ST_PAGE;
   if (layer == 0 && blk == 0 && threadIdx.x == 0) status[i] = st;
@@ -306,7 +311,7 @@ q4_read_kernel(const spec_pages_q4 kv, const int32_t* __restrict__ slots, int nt
   const int64_t dst0 = (int64_t)layer * layer_stride + (int64_t)i * nt * node;
   const int l = threadIdx.x & 1;
   constexpr int U = CQ_FLIGHT;
-  each_piece(kv, r0, r1, [&](int which, int r, int step, int e, int64_t block, bool ok) {
+  each_piece<RQ_THREADS>(kv, r0, r1, [&](int which, int r, int step, int e, int64_t block, bool ok) {
     const uint2* codes = reinterpret_cast<const uint2*>(which ? kv.v_qs : kv.k_qs) + 2 * block + l;
     const uint16_t* scales = (which ? kv.v_scales : kv.k_scales) + block;
     uint2 c[U];
@@ -444,7 +449,7 @@ int check_rows(const spec_pages_q4* kv, int n, int nt, const void* k, const void
   if (*stride == 0) *stride = layer;
   if (*stride % 8 != 0 || (kv->n_layers > 1 && *stride < layer))
     return fail(SPEC_E_SHAPE, "the rows' layer stride must be a multiple of 8 and hold a layer's rows");
-  if ((double)n * kv->n_layers * ((nt + CQ_ROWS - 1) / CQ_ROWS) > INT32_MAX)
+  if ((double)n * kv->n_layers * ((nt + 7) / 8) > INT32_MAX)
     return fail(SPEC_E_SHAPE, "n * n_layers * nt too large");
   return SPEC_OK;
 }
@@ -565,9 +570,13 @@ extern "C" int spec_pages_q4_read(const spec_pages_q4* kv, int n, const int32_t*
   if (rc == SPEC_OK && (pos0 == nullptr || n_pos == nullptr)) rc = fail(SPEC_E_INVALID, "null argument");
   if (rc == SPEC_OK) rc = check_rows(kv, n, nt, k, v, &layer_stride);
   if (rc != SPEC_OK) return rc;
-  const int blocks = (nt + CQ_ROWS - 1) / CQ_ROWS;
+  // 8 rows a CTA where CTAs of 16 would be more than are resident (2 prompts of 4097 in 8 layers
+  // 53.5 us instead of 57.5, with 32 rows 64; 12 entries of 16 in 40 layers, which are, 7.2 and 6.3)
+  const int64_t entries = (int64_t)n * kv->n_layers;
+  const bool many = entries * ((nt + 15) / 16) > 12 * (int64_t)device_sms();
+  const int rows = many ? 8 : 16, blocks = (nt + rows - 1) / rows;
   return launched("4-bit page read",
-                  launch_dependent(q4_read_kernel, (size_t)n * kv->n_layers * blocks, PQ_THREADS, 0,
-                                   reinterpret_cast<cudaStream_t>(stream), *kv, slots, nt, pos0, n_pos, k, v,
-                                   layer_stride, blocks, status));
+                  launch_dependent(many ? q4_read_kernel<8> : q4_read_kernel<16>, (size_t)entries * blocks, RQ_THREADS, 0,
+                                   reinterpret_cast<cudaStream_t>(stream), *kv, slots, nt, pos0, n_pos, k, v, layer_stride,
+                                   blocks, status));
 }

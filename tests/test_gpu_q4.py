@@ -477,6 +477,30 @@ def test_rows_with_layers_apart(dev):
         assert np.isnan(got[:, 1, 33:]).all()
 
 
+@pytest.mark.parametrize("hd,nkv,page", [(64, 2, 48), (96, 1, 100)])
+def test_prompts_in_and_out(dev, hd, nkv, page):
+    """Rows enough for several waves of CTAs."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(hd)
+    layers, n, nt = 8, 2, 2003
+    max_pages = -(-nt // page) + 1
+    table = g.permutation(2 * max_pages).reshape(2, max_pages).astype(np.int32)
+    c = Planes(sv, dev, g, layers, 2 * max_pages, nkv, page, hd, table, [3, 0])
+    rows = [random_rows(g, (layers, n, nt, nkv, hd)) for _ in range(2)]
+    n_path = np.array([nt, 1500], np.int32)
+    slots, st = c.T(np.array([1, 0], np.int32)), c.T(np.array([9, 9], np.int32))
+    sv.spec_pages_q4_commit(c.kv, n, slots, nt, c.T(rows[0]), c.T(rows[1]), None, c.T(n_path), st)
+    assert st.tolist() == [0, 0]
+    out = [torch.full((layers, n, nt, nkv, hd), 3.0, dtype=torch.float16, device=dev) for _ in range(2)]
+    sv.spec_pages_q4_read(c.kv, n, slots, nt, c.T(np.array([0, 3], np.int32)), c.T(n_path), out[0], out[1], st)
+    assert st.tolist() == [0, 0]
+    for w in range(2):
+        want = lc.values(*lc.pack(*lc.quantise(rows[w]))).astype(np.float16)
+        want[:, 1, 1500:] = 3.0
+        assert np.array_equal(out[w].cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("hd,nkv,page", [(128, 8, 64), (64, 1, 5), (32, 3, 16)])
 def test_copies_of_pages(dev, hd, nkv, page):
     import torch
