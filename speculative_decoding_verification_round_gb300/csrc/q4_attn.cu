@@ -48,7 +48,9 @@ struct QShape {
   static constexpr int SUM_OFF = Q_OFF + KeyWarp<HD, NT, true>::Q_BYTES;
   static constexpr int END = SUM_OFF + KeyWarp<HD, NT, true>::SUM_BYTES;
   static constexpr size_t SMEM = END;
-  static constexpr int RESIDENT = NT == 4 ? 2 : HD == 64 ? (NT == 2 ? 5 : 6) : NT == 2 ? 3 : 4;
+  // (with fewer registers a thread and more CTAs a warp has less under way at a time: 16 rows of 64
+  // dimensions 122 us with three, 130 with five; of 128 108 with three, 121 with four)
+  static constexpr int RESIDENT = NT == 4 ? 2 : HD == 64 ? (NT == 2 ? 3 : 4) : NT == 2 ? 3 : 4;
 };
 
 // What a unit's rows see.
