@@ -12,8 +12,8 @@
 // TB/s; with one node (4 rows a kv head) over 65536 82 us, 3.7 TB/s.  The loads alone
 // run at 5.4 TB/s; what bounds it is a warp's chain of codes to operands, products and
 // weights, about 24 instructions a position of 8 rows, with 12 to 16 warps an SM (issue
-// slots 51% used, the tensor pipe 45%).  Two to four stages, 3 to 6 CTAs an SM and one or two
-// tiles of keys at a time lie within 5% of each other.  One node over 8191 positions 12.0 us,
+// slots 51% used, the tensor pipe 45%).  Other stages, CTAs an SM and keys at a time are up to
+// 12% slower.  One node over 8191 positions 12.0 us,
 // of 16 sequences in a window of 4096 (14 heads over 2 of 64) 11.2: launch, lookups, one or
 // two steps a warp, the join.
 #include <math.h>
