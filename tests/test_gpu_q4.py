@@ -325,6 +325,28 @@ def test_refused_sequences(dev):
         assert np.isnan(got[1:7]).all()
 
 
+@pytest.mark.parametrize("nt,longest", [(20, 400), (2, 20000), (4, 20000)])
+def test_refused_sequences_of_large_calls(dev, nt, longest):
+    """The same of the kernels for many rows and for long tables."""
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(19)
+    c = Q4Case(sv, dev, g, 8, 2, 64, [longest, 190, 200, 70, 60, 130], nt, 64, counts=[nt, nt, nt, nt, nt + 1, nt - 1], layers=1)
+    c.slots[1] = -1
+    c.table[c.slots[2], 3] = -5
+    c.slot_len[c.slots[3]] = -1
+    c.parents[5, nt - 2] = nt - 2
+    got = c.call()
+    assert c.status.tolist() == [0, tree.ST_SLOT, tree.ST_PAGE, tree.ST_PAGE, tree.ST_TREE, tree.ST_TREE]
+    c.check(got, [0])
+    assert np.isnan(got[1:5]).all() and np.isnan(got[5, :nt - 1]).all()
+    c.parents[5, nt - 2] = -1
+    c.table[c.slots[0], longest // 128] = 10 ** 6  # in the middle of the long one
+    got = c.call()
+    assert c.status.tolist() == [tree.ST_PAGE, tree.ST_SLOT, tree.ST_PAGE, tree.ST_PAGE, tree.ST_TREE, 0]
+    c.check(got, [5])
+    assert np.isnan(got[:5]).all()
+
+
 # ---------------------------------------------------------------------------
 # rows into the cache and out of it
 # ---------------------------------------------------------------------------
