@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(QA_THREADS, QShape<HD, NT>::RESIDENT) q4_attn_
 }
 
 // ---------------------------------------------------------------------------
-// Small calls: a cluster of CTAs has a unit (sequence, kv head), its positions are dealt to
-// their warps 32 at a time, and the results are joined through distributed shared
+// Small calls, and short sequences: a cluster of CTAs has a unit (sequence, kv head), its
+// positions are dealt to their warps 32 at a time, and the results are joined through distributed shared
 // memory: no cut to be found, no second kernel.
 // ---------------------------------------------------------------------------
 constexpr int QU_WARPS = 8, QU_THREADS = 32 * QU_WARPS;
@@ -488,18 +488,21 @@ cudaError_t launch_q4_rows(const TreeArgs& a, int n_cta, cudaStream_t st) {
 // CTAs of a unit in the clusters' form, or 0 for the cut's: up to eight (clusters of more
 // leave SMs of a GPC unused), as many as are resident, one an SM, and keep a step of 32
 // positions for each warp, by the most positions that a sequence can have (its table's,
-// the window's).  With up to eight steps for a warp the clusters are faster where they fill
-// the SMs (4 sequences of 8000 positions 18.8 us against 24.3, 32 of 1000 17.2 against
-// 25.3), with up to three anywhere (one sequence of 1000 8.1 against 9.7; of 16000, eight
-// steps on 64 SMs, 17.2 against 14.9).
+// the window's).  Where the clusters fill the SMs they are faster with up to eight steps for a
+// warp (4 sequences of 8000 positions 18.4 us against 24.4, 32 of 1000 16.4 against 25.0), and
+// with up to 8 rows sixteen (32 of 4000 42 against 51, 40 of 4000 60 and 58), however many
+// units there are (200 of 300, 14 heads over 2 of 64, 8.4 against 17.8; 16 rows, 100 of
+// 1000, 76 and 66: not there); with up to three steps anywhere (one sequence of 1000 8.2 against
+// 10.0; of 16000, eight steps on 64 SMs, 16.7 and 14.1).
 int unit_ranks(const TreeArgs& a) {
   const int64_t units = (int64_t)a.n_seq * a.nkv, all = (int64_t)a.max_pages * a.page_size;
   const int64_t most = a.window > 0 ? std::min<int64_t>(all, (int64_t)a.window + a.sinks + 2 * WARP_KEYS) : all;
   const int64_t steps = (most + WARP_KEYS - 1) / WARP_KEYS, sms = device_sms();
-  if (units > 2 * sms) return 0;
+  const int most_steps = a.rows == 8 ? 16 : 8;
+  if (units > 2 * sms) return a.rows == 8 && steps <= (int64_t)QU_WARPS * most_steps ? 1 : 0;
   int ranks = 1;
   while (ranks < 8 && units * ranks * 2 <= sms && steps >= (int64_t)QU_WARPS * ranks * 2) ranks *= 2;
-  return steps <= (int64_t)QU_WARPS * ranks * (4 * units * ranks >= 3 * sms ? 8 : 3) ? ranks : 0;
+  return steps <= (int64_t)QU_WARPS * ranks * (4 * units * ranks >= 3 * sms ? most_steps : 3) ? ranks : 0;
 }
 
 template <int HD, int NT>
