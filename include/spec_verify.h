@@ -688,8 +688,10 @@ int spec_sample_workspace(int R, int V, size_t* bytes);
  * u = q + 8), and an element's value is scale * q, q in [-8, 7].
  * spec_pages_q4_commit makes scales of at most eight significant bits, with
  * which every value is exact in fp16; other scales are taken, too, their
- * values then being rounded to fp16 where rows are attended to or read.  An
- * infinite or NaN scale makes its elements infinite or NaN. */
+ * values then being rounded to fp16 where rows are attended to or read (above
+ * 8188 to infinities where the product passes fp16's range).  An infinite or NaN
+ * scale makes its elements infinite or NaN.  Rows that do not see a position know
+ * nothing of its scale. */
 typedef struct {
   uint8_t* k_qs; /* [n_layers][n_pages][n_kv_heads][page_size][head_dim / 32][16] */
   uint8_t* v_qs;

@@ -129,7 +129,14 @@ __device__ __forceinline__ uint32_t q4_high(uint32_t x) {  // (1024 + 16 u) / 16
   return kw_hfma2(lop3_and_or(x, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u);
 }
 __device__ __forceinline__ bool odd_half(uint32_t v) { return (v & 0x7C00u) == 0x7C00u; }  // infinite or NaN
+// A scale that makes infinities or NaN of codes: one itself, or 8192 and more, 8 times which fp16 does not hold.
+__device__ __forceinline__ bool odd_scale(uint32_t v) { return (v & 0x7FFFu) >= 0x7000u; }
 __device__ __forceinline__ bool odd_pair(uint32_t v) { return odd_half(v) || odd_half(v >> 16); }
+
+// What code u stands for: the product rounded to fp16, as kw_hmul2 makes it.
+__device__ __forceinline__ float q4_value(int u, float scale) {
+  return __half2float(__float2half_rn((float)(u - 8) * scale));
+}
 
 // A row of codes: HD / 2 bytes, 16-byte chunk c of row r at c ^ q4_swz(r), so that a chunk
 // of eight rows, read as words or by ldmatrix, lies in all banks.

@@ -97,7 +97,7 @@ __device__ __forceinline__ void step_codes(KeyWarp<HD, NT, true>& kw, const Unit
   bool odd = false;
   if (masked)  // this lane's position's scales
 #pragma unroll
-    for (int b = 0; b < HD / 32; b++) odd |= odd_half(kw_lds16(vss + lane * (HD / 16) + 2 * b));
+    for (int b = 0; b < HD / 32; b++) odd |= odd_scale(kw_lds16(vss + lane * (HD / 16) + 2 * b));
   odd = __any_sync(0xffffffffu, odd);
 #pragma unroll
   for (int i0 = 0; i0 < WARP_KEYS / 16; i0 += KT) {
@@ -124,7 +124,7 @@ __device__ __forceinline__ void step_codes(KeyWarp<HD, NT, true>& kw, const Unit
           const int b = d >> 5, j = d & 31;
           const uint32_t w = kw_lds32(vt + r * (HD / 2) + ((b ^ q4_swz<HD>(r)) << 4) + (j & 12));
           const int u = (w >> (8 * (j & 3) + (j >> 4) * 4)) & 15;
-          return (float)(u - 8) * kw_half(kw_lds16(st + r * (HD / 16) + 2 * b), 0);
+          return q4_value(u, kw_half(kw_lds16(st + r * (HD / 16) + 2 * b), 0));
         });
       else
         kw.values_q4(vt, st, x[i]);

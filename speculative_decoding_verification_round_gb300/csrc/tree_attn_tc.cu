@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
 #pragma unroll
             for (int it = 0; it < CH4; it++) {
               const int r = row_at(it), row = 32 * quarter + r;
-              if (masked && odd_half(sc[it])) {
+              if (masked && odd_scale(sc[it])) {
                 bad |= 1u << r;
                 sc[it] = 0u;
               }
@@ -803,11 +803,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
                     src += cached * HD;
                   }
                   if constexpr (Q4) {
-                    if (!tree) {  // blocks of 32 whose scale is infinite or NaN
+                    if (!tree) {  // blocks of 32 with such a scale
 #pragma unroll 1
                       for (int d = 0; d < CH; d++) {
                         const uint32_t sc = __half_as_ushort(a.v_scales[cached * CH + d]);
-                        if (!odd_half(sc)) continue;  // (the warp's)
+                        if (!odd_scale(sc)) continue;  // (the warp's)
                         uint32_t o[32];
                         tm_ld32(tO + 32 * d, o);
                         tm_wait_ld(o);
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_attn_tc_kernel(const TreeA
 #pragma unroll
                           for (int e = 0; e < 32; e++) {
                             const int u = ww[(e & 15) >> 2] >> (8 * (e & 3) + (e >> 4) * 4) & 15;
-                            o[e] = __float_as_uint(fmaf(p, half_of(sc, 0) * (float)(u - 8), __uint_as_float(o[e])));
+                            o[e] = __float_as_uint(fmaf(p, q4_value(u, half_of(sc, 0)), __uint_as_float(o[e])));
                           }
                         }
                         __syncwarp();
