@@ -258,6 +258,8 @@ __global__ void __launch_bounds__((BShape<HD, NT, Q4>::THREADS)) block_attn_kern
             [&](int r, int u, const float (&acc)[8], float l) { put_row(out + r * HD + u * 8, acc, l); });
 }
 
+constexpr size_t SM_SMEM = 228 * 1024;     // of an SM
+constexpr size_t FIXED_SMEM = 1024 + 256;  // of a CTA beside what its launch asks for: the system's, the static arrays
 // CTAs of a unit, as long as every warp has two steps of the list: of fp16 as many as are
 // resident, two an SM, up to 16 (one node over 64 blocks of 64: 8.9 us, with up to eight
 // 9.9); of codes, with twice the warps, one an SM, up to eight (8 sequences of one node
@@ -268,7 +270,7 @@ int launch_block(BlockArgs& a, double units, int block, cudaStream_t st) {
   using Sh = BShape<HD, NT, Q4>;
   const size_t smem = Sh::smem(a.path_rows, a.keep);
   const int64_t steps = ((int64_t)a.keep * block + Sh::KEYS - 1) / Sh::KEYS;
-  const int fit = !Q4 && smem <= 113 * 1024 ? 2 : 1;
+  const int fit = !Q4 && 2 * (smem + FIXED_SMEM) <= SM_SMEM ? 2 : 1;
   a.ranks = 1;
   while (a.ranks < 8 * fit && units * a.ranks * 2 <= fit * device_sms() && steps >= (int64_t)2 * Sh::WARPS * a.ranks * 2)
     a.ranks *= 2;
