@@ -722,7 +722,7 @@ int spec_pages_q4_free(const spec_pages_q4* kv, int n, const int32_t* slots, int
  * bits; the fp16 rows are quantised on their way.  Of 32 elements x, m is the
  * one of the largest magnitude (the first of several):
  *   scale = -m / 8, rounded to eight significant bits (to even) and then to fp16,
- *           its magnitude at most 8160;
+ *           its magnitude at most 8160; +0 where that is 0;
  *   q     = x / scale (fp32), rounded to a whole number (to even), kept in [-8, 7];
  *           0 where the scale is 0.
  * Elements that are not all finite get a NaN for their scale (and q = 0): whoever

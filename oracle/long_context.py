@@ -13,7 +13,7 @@ import numpy as np
 # ---------------------------------------------------------------------------
 def block_scale(m):
     """The scale of a block whose element of the largest magnitude is m: -m / 8
-    with eight significant bits (to even), on fp16's grid, at most 8160."""
+    with eight significant bits (to even), on fp16's grid, at most 8160, 0 without a sign."""
     d = -float(m) / 8.0
     if d == 0.0:
         return 0.0
@@ -21,7 +21,7 @@ def block_scale(m):
     r = math.ldexp(_even(mant * 256.0), ex - 8)        # eight bits
     if r < 2.0 ** -14:                                 # fp16's subnormal grid
         r = _even(r * 2.0 ** 24) * 2.0 ** -24
-    return math.copysign(min(r, 8160.0), d)
+    return math.copysign(min(r, 8160.0), d) if r != 0.0 else 0.0
 
 
 def _even(x):

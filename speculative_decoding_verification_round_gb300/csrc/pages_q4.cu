@@ -106,7 +106,7 @@ __device__ __forceinline__ Half quantise(const uint4& low, const uint4& high) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
   if (d == 0.0f) inv = 0.0f;
   const bool small = __any_sync(0xffffffffu, fabsf(d) < 0x1p-13f);
-  out.scale = fine ? __half_as_ushort(__float2half_rn(d)) : 0x7E00u;
+  out.scale = fine ? __half_as_ushort(__float2half_rn(d + 0.0f)) : 0x7E00u;  // (-0 to 0)
   const uint64_t inv2 = pair_of(inv, inv), neg2 = pair_of(-d, -d), magic = pair_of(12582912.0f, 12582912.0f),
                  back = pair_of(-12582912.0f, -12582912.0f);
   uint32_t u[8];

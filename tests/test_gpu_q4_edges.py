@@ -9,7 +9,7 @@ import pytest
 from captured import launches
 from oracle import long_context as lc
 from oracle import tree
-from test_gpu_q4 import Q4Case
+from test_gpu_q4 import Planes, Q4Case, random_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,36 @@ def test_values_are_rounded_to_fp16(dev, kernel, hd, rows, nq, nt):
         # cancel -- then the reciprocal and the product once each
         low, high = ((want + e * mag).astype(np.float16) for e in (-2.0 ** -20, 2.0 ** -20))
         assert ((got[b] >= low) & (got[b] <= high)).all()
+
+
+# ---------------------------------------------------------------------------
+# rows into the cache
+# ---------------------------------------------------------------------------
+def test_a_scale_of_zero_is_positive(dev):
+    """Blocks of zeros of either sign, and of values whose scale rounds to 0, get the same bits
+    whatever the blocks beside them hold."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng(8)
+    nt, nkv, hd, page = 6, 4, 128, 8
+    rows = random_rows(g, (1, 1, nt, nkv, hd))
+    blocks = rows.reshape(nt, nkv * hd // 32, 32)
+    blocks[0, ::2] = 0
+    blocks[1, ::2] = -0.0
+    blocks[2, ::2, ::3] = 0
+    blocks[2, ::2, 1::3] = blocks[2, ::2, 2::3] = -0.0
+    blocks[3, ::2] = 2.0 ** -24 * g.integers(-3, 4, blocks[3, ::2].shape)
+    blocks[4:, ::4] = 0
+    blocks[5, 2::4] = -0.0
+    blocks[1::2, 1::2] = np.where(np.arange(32) % 2 == 0, 1.5, -1.5)  # (a tie of both signs)
+    c = Planes(sv, dev, g, 1, 1, nkv, page, hd, [[0]], [0])
+    st = torch.full((1,), 9, dtype=torch.int32, device=dev)
+    sv.spec_pages_q4_commit(c.kv, 1, c.T(np.array([0], np.int32)), nt, c.T(rows), c.T(rows), None,
+                            c.T(np.array([nt], np.int32)), st)
+    assert st.tolist() == [0]
+    codes, scales = lc.pack(*lc.quantise(rows[0, 0]))
+    zero = (scales == 0).swapaxes(0, 1)
+    assert zero.sum() == 4 * 8 + 4 + 8
+    for got, scale in zip(c.planes()[::2], c.planes()[1::2]):
+        assert np.array_equal(got[0, 0, :, :nt], codes.swapaxes(0, 1))
+        assert (scale[0, 0, :, :nt].view(np.uint16)[zero] == 0).all()
