@@ -135,6 +135,192 @@ def test_values_are_rounded_to_fp16(dev, kernel, hd, rows, nq, nt):
         low, high = ((want + e * mag).astype(np.float16) for e in (-2.0 ** -20, 2.0 ** -20))
         assert ((got[b] >= low) & (got[b] <= high)).all()
 
+# ---------------------------------------------------------------------------
+# every position counts
+# ---------------------------------------------------------------------------
+LONGER = [(*f, long) for f in FORMS for long in ([(5000, 2900)] if f in UNIT else [(1500, 700)] if f in TC else [(9000, 300)])]
+
+
+class Edges(Q4Case):
+    """Long contexts, in which a row's weights go further down."""
+
+    def check(self, got, seqs=None):
+        """Q4Case.check's bound but for what a pair of fp16 numbers loses of a weight w: two
+        numbers of 2^12 w, each off by up to 2^-25 (half of fp16's smallest step), together 2^-36 of the
+        row's largest, for each key, however small its w is.  It counts times the key's own |v|, not
+        times the row's weighted |v|: where the keys of almost all of the weight have zeros
+        in a channel, the latter is next to nothing."""
+        for b in range(self.n) if seqs is None else seqs:
+            m = int(self.counts[b])
+            assert (got[b, m:] == np.float16(7.0)).all(), b
+            kc, vc = self.cached(0, b), self.cached(1, b)
+            ref, mag, dots = tree.tree_attention(self.q[b, :m], kc, vc, self.kn[b, :m], self.vn[b, :m],
+                                                 self.parents[b, :m].tolist(), self.window, self.sinks, self.scale)
+            scale = abs(self.scale or self.hd ** -0.5)
+            q1 = np.abs(self.q[b, :m].astype(np.float64)).reshape(m, self.nkv, -1, self.hd // 32, 32).sum(-1)
+            at = np.arange(self.lens[b])
+            s = np.abs(self.ks[self.layer][self.table[self.slots[b], at // self.page], :, at % self.page].astype(np.float64))
+            worst = np.einsum("mhgb,phb->mhgp", q1, np.nan_to_num(s)).max(-1).reshape(m, self.nq)
+            ds = (self.hd + 4) * 2.0 ** -23 * scale * dots + 40 * 24 * 2.0 ** -23 * scale * worst
+            rel = np.expm1(2 * ds) + 2.0 ** -20 + ((self.lens[b] + m) / 8 + 64) * 2.0 ** -23
+            far = 2.0 ** -36 * (np.abs(vc.astype(np.float64)).sum(0) + np.abs(self.vn[b, :m].astype(np.float64)).sum(0))
+            bound = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + 1.01 * rel[..., None] * mag + np.repeat(
+                far, self.nq // self.nkv, 0)[None]
+            err = np.abs(got[b, :m].astype(np.float64) - ref)
+            assert np.isfinite(got[b, :m]).all() and (err <= bound).all(), (b, float(np.max(err - bound)))
+
+
+def long_case(dev, g, kernel, hd, rows, nq, nt, long, windowed, **kw):
+    """A long context; with a window, tiles of sinks and of the window and whole ones between them that nobody sees."""
+    import speculative_decoding_verification_round_gb300 as sv
+    cut = kernel == "q4_attn_kernel"
+    c = Edges(sv, dev, g, nq, 2, hd, list(long), nt, 64 if windowed else 48, window=(6250 if cut else 450) if windowed else 0,
+               sinks=170 if windowed else 0, layers=1, **kw)
+    assert kernel_of(c) == (kernel, hd, rows)
+    return c
+
+
+@pytest.mark.parametrize("windowed", [False, True])
+@pytest.mark.parametrize(KEYS + ",long", LONGER)
+def test_values_of_all_positions(dev, kernel, hd, rows, nq, nt, long, windowed):
+    """No scores: every row is the mean of what it sees.  Each position has a value in one
+    channel of one kv head alone, so that one that is left out, counted twice or seen by the wrong
+    rows moves a channel by far more than a rounding."""
+    g = np.random.default_rng([hd, nt, 3])
+    c = long_case(dev, g, kernel, hd, rows, nq, nt, long, windowed, counts=[nt, max(1, nt - 1)])
+    c.q[:], c.vn[:] = 0, 0
+    c.vc[:], c.vs[:] = 0x88, 1
+    for b in range(2):
+        where = g.permutation(np.arange(c.lens[b]) % (2 * hd))  # [positions] -> kv head and channel
+        for p, (h, d) in enumerate(zip(where // hd, where % hd)):
+            u = int(g.integers(9, 16))
+            c.vc[0, c.table[c.slots[b], p // c.page], h, p % c.page, d // 32, d % 16] = u | 0x80 if d % 32 < 16 else u << 4 | 8
+    c.v = lc.values(c.vc, c.vs).astype(np.float16)
+    got = c.call()
+    assert c.status.tolist() == [0, 0]
+    for b in range(2):
+        v = c.cached(1, b).astype(np.float64)
+        for i in range(int(c.counts[b])):
+            cached, nodes = tree.visible(c.lens[b], c.parents[b, :c.counts[b]].tolist(), i, c.window, c.sinks)
+            want = np.repeat(v[cached].sum(0) / (len(cached) + len(nodes)), nq // 2, 0)
+            # whole numbers times 2^12, exact in fp32, but for 2^-22 of them (the weights' two parts), which
+            # round up to 70 products and 100 sums of warps and CTAs by 2^-23 each
+            bound = (2.0 ** -11 + 2.0 ** -15) * np.abs(want) + 2.0 ** -25
+            assert (np.abs(got[b, i].astype(np.float64) - want) <= bound).all(), (b, i)
+        assert (got[b, c.counts[b]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("windowed", [False, True])
+@pytest.mark.parametrize(KEYS + ",long", LONGER)
+def test_keys_at_the_edges(dev, kernel, hd, rows, nq, nt, long, windowed):
+    """Each row's query has one channel; a hundred positions around the edges of warps' steps, tiles, pages,
+    sinks, window and length have keys in one, which weigh e^16 times what the others do."""
+    g = np.random.default_rng([hd, nt, 4])
+    c = long_case(dev, g, kernel, hd, rows, nq, nt, long, windowed, counts=[nt, max(1, nt - 1)], scale=1.0)
+    c.kc[:], c.ks[:], c.kn[:], c.q[:] = 0x88, -0.5, 0, 0
+    dims = np.stack([g.permutation(hd)[:rows_] for rows_ in [min(8, nt * nq // 2)] * 2])  # of each kv head
+    for i in range(nt):
+        for h in range(nq):
+            of = dims[h // (nq // 2)]
+            c.q[:, i, h, of[(i * (nq // 2) + h) % len(of)]] = 4
+    for b in range(2):
+        n = c.lens[b]
+        lo = n - c.window + 1 if c.window else n // 2
+        edges = {0, 32, 128, c.page, 2 * c.page, c.sinks, c.sinks + 32, lo, lo + 1, lo + 2, lo // 32 * 32, lo // 128 * 128, lo // c.page * c.page,
+                 lo // 128 * 128 + 128, n // 32 * 32, n // 128 * 128, n // c.page * c.page, n, n // 2 // 32 * 32, (n + lo) // 2 // c.page * c.page}
+        at = sorted({p for e in edges for p in (e - 1, e, e + 1) if 0 <= p < n} | set(g.integers(0, n, 30).tolist()))
+        for j, p in enumerate(g.permutation(at)):
+            for h in range(2):
+                d = dims[h][j % dims.shape[1]]
+                c.kc[0, c.table[c.slots[b], p // c.page], h, p % c.page, d // 32, d % 16] = 0x80 if d % 32 < 16 else 0x08
+    c.k = lc.values(c.kc, c.ks).astype(np.float16)
+    got = c.call()
+    assert c.status.tolist() == [0, 0]
+    c.check(got)
+
+
+# ---------------------------------------------------------------------------
+# the cut on what the other forms are tested with in test_gpu_q4.py
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize(KEYS, CUT)
+def test_the_cut_matches_the_reference(dev, kernel, hd, rows, nq, nt):
+    """Without and with a window and sinks, chains and trees, a negative scale, values near both ends of fp16."""
+    g = np.random.default_rng([hd, nt, 5])
+    for windowed, kind, scale in ((False, "tree", None), (True, "tree", None), (True, "chain", -0.25), (False, "forest", 0.5)):
+        c = long_case(dev, g, kernel, hd, rows, nq, nt, (9000, 300), windowed, counts=[nt, max(1, nt - 1)], kind=kind,
+                      scale=scale)
+        got = c.call()
+        assert c.status.tolist() == [0, 0]
+        c.check(got)
+        assert np.array_equal(c.call().view(np.uint16), got.view(np.uint16))
+    for e in (-24, -16, 12):
+        c.vs[:] = np.sign(c.vs) * np.exp2(e) * (1 if e < -18 else 1.9921875)
+        c.v = lc.values(c.vc, c.vs).astype(np.float16)
+        c.vn[:] = (c.vn / np.abs(c.vn.astype(np.float64)).max() * 2.0 ** max(e, -20)).astype(np.float16)
+        c.check(c.call())
+
+
+@pytest.mark.parametrize(KEYS, CUT)
+def test_nothing_masked_gets_into_the_cut(dev, kernel, hd, rows, nq, nt):
+    """Scales of NaN and infinity behind the length, in front of the window and between sinks and window; infinities
+    of other branches' rows; a NaN that the first nodes see."""
+    g = np.random.default_rng([hd, nt, 6])
+    c = long_case(dev, g, kernel, hd, rows, nq, nt, (9000, 300), True, counts=[nt, max(1, nt - 1)])
+    if nt > 1:
+        c.parents[:, 1:] = 0
+    c.check(c.call())
+    seen = np.zeros(c.ks.shape[1:4:2], bool)
+    for b in range(2):
+        for p in range(c.lens[b]):
+            if p < 170 or p > c.lens[b] - c.window:
+                seen[c.table[c.slots[b], p // 64], p % 64] = True
+    c.ks[:, :, :] = np.where(seen[None, :, None, :, None], c.ks, np.float16(np.nan))
+    c.vs[:, :, :] = np.where(seen[None, :, None, :, None], c.vs, np.float16(np.inf))
+    good = c.call()
+    c.check(good)
+    last = int(c.counts[0]) - 1
+    if nt > 1:  # a row of its own, of which the others know nothing
+        kn, vn = c.kn.copy(), c.vn.copy()
+        c.vn[0, last], c.kn[1, 0] = -np.inf, np.nan
+        got = c.call()
+        assert np.isneginf(got[0, last]).all()
+        assert np.isnan(got[1, :c.counts[1]]).all()  # (everyone's root)
+        c.kn, c.vn = kn, vn
+        got[0, last], got[1] = good[0, last], good[1]
+        c.check(got)
+    p = c.lens[0] - c.window + 1
+    c.vs[:, c.table[c.slots[0], p // 64], :, p % 64] = np.nan
+    got = c.call()
+    assert np.isnan(got[0, 0]).all()  # (the others are one deeper)
+    assert np.array_equal(got[0, 1:].view(np.uint16), good[0, 1:].view(np.uint16))
+    assert np.array_equal(got[1].view(np.uint16), good[1].view(np.uint16))
+
+
+@pytest.mark.parametrize(KEYS, CUT)
+def test_strides_of_the_cut(dev, kernel, hd, rows, nq, nt):
+    """Rows of q, k_new and v_new apart, with NaN between; a NaN in one row's query is that row's alone."""
+    import torch
+    g = np.random.default_rng([hd, nt, 7])
+    c = long_case(dev, g, kernel, hd, rows, nq, nt, (9000, 300), False)
+    want = c.call()
+    c.check(want)
+
+    def apart(x, row):
+        buf = torch.full((c.n * nt, row), float("nan"), dtype=torch.float16, device=dev)
+        buf[:, :x[0, 0].size] = c.T(x).view(c.n * nt, -1)
+        return buf
+    qs, ks = nq * hd + 24, 2 * hd + 8
+    got = c.call(q=apart(c.q, qs), k_new=apart(c.kn, ks), v_new=apart(c.vn, ks), q_stride=qs, kv_stride=ks)
+    assert np.array_equal(got.view(np.uint16), want.view(np.uint16))
+    q = c.q.copy()
+    q[0, nt - 1, 1, 5], q[1, 0, nq - 1, hd - 1] = np.nan, np.inf
+    got = c.call(q=c.T(q))
+    odd = np.zeros(got.shape[:3], bool)
+    odd[0, nt - 1, 1] = odd[1, 0, nq - 1] = True
+    assert np.isnan(got[odd]).all()
+    got[odd] = want[odd]
+    c.check(got)
+
 
 # ---------------------------------------------------------------------------
 # rows into the cache
