@@ -239,6 +239,26 @@ def test_keys_at_the_edges(dev, kernel, hd, rows, nq, nt, long, windowed):
     c.check(got)
 
 
+@pytest.mark.parametrize(KEYS, FORMS)
+def test_pages_that_nobody_sees_may_be_gone(dev, kernel, hd, rows, nq, nt):
+    """Between the sinks and the window a table may hold anything; a missing page that is seen is reported."""
+    g = np.random.default_rng([hd, nt, 9])
+    c = case_of(dev, g, kernel, hd, rows, nq, nt)
+    want = c.call()
+    c.check(want)
+    lo = c.lens[0] - c.window + 1
+    row = c.table[c.slots[0]]
+    row[1:lo // 32] = np.where(np.arange(1, lo // 32) % 2 == 0, -1, 10 ** 6)
+    got = c.call()
+    assert c.status.tolist() == [0, 0] and np.array_equal(got.view(np.uint16), want.view(np.uint16))
+    for e, page in ((lo // 32, -1), (0, 10 ** 6), ((c.lens[0] - 1) // 32, -3)):
+        held, row[e] = row[e], page
+        got = c.call()
+        row[e] = held
+        assert c.status.tolist() == [tree.ST_PAGE, 0] and np.isnan(got[0]).all()
+        assert np.array_equal(got[1].view(np.uint16), want[1].view(np.uint16))
+
+
 # ---------------------------------------------------------------------------
 # the cut on what the other forms are tested with in test_gpu_q4.py
 # ---------------------------------------------------------------------------
