@@ -816,7 +816,8 @@ int spec_block_scores(const spec_digest* dg, int layer, int n_seq, const int32_t
  *           n_nodes are left as they were
  *   status  int32 [n_seq]: SPEC_ST_SLOT, SPEC_ST_TREE (node count), SPEC_ST_FULL (a length
  *           below 0, or more blocks than ld): the rows are -1 then
- * 1 <= n_keep <= 4096, n_first + n_last <= n_keep. */
+ * 1 <= n_keep <= 4096, n_first + n_last <= n_keep.  A row is read by as many threads as
+ * ld asks for: an ld not far above the most blocks of a sequence is the fastest. */
 int spec_block_select(const int32_t* len, int n_slots, int block, int n_seq, const int32_t* slots,
                       int nt, const int32_t* n_nodes, int n_kv_heads, const float* scores, int64_t ld,
                       int n_keep, int n_first, int n_last, int32_t* blocks, int32_t* status,

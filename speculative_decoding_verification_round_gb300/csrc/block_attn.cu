@@ -11,8 +11,11 @@
 // nothing is masked but the end of the last block.
 //
 // Measured (32 heads over 8 of 128): one node over 64 blocks of 64 in fp16 (17 MB) 8.9 us:
-// launch, list, page, two steps a warp, the cluster's join; 12 x 8 nodes over 64 blocks of 32
-// in 4 bits (226 MB named, 163 read) 53 us: the chain of q4_attn.cu, issue slots 54% used.
+// launch, list, page, four steps a warp, of which two are on their way at a time, the cluster's
+// join; 8 x 1 such nodes (134 MB) 26 us, 12 x 8 nodes over 64 blocks of 32 (807 MB named, 593 read) 103: the DRAM 71%
+// busy.  In 4 bits 8 x 1 node (38 MB) 16.6 us: two CTAs a unit, eight steps a warp, 12% of the
+// SMs' warps; 12 x 8 nodes (226 MB named, 165 read) 53: the chain of q4_attn.cu, issue slots 54%
+// used.
 #include <climits>
 #include <math.h>
 

@@ -2,11 +2,12 @@
 // blocks (spec_block_digest), scores from them (spec_block_scores), and the
 // selection of the largest (spec_block_select).
 //
-// Measured: 12 prompts of 4095 positions in 4 bits, 8 heads of 128, blocks of 32 (28 MB) 13 us,
-// in fp16 (101 MB) 21: the least and largest of the codes' values cost as many
-// instructions as the fp16 rows cost bytes (ALU pipe 60%); scores of their 12 x 16 nodes, 40
-// heads over 8, 9 us; a decode step of 2 sequences over 2048 blocks, digests and scores, 8.8 us in
-// two launches.
+// Measured: 12 prompts of 4095 positions in one layer, 8 heads of 128, blocks of 32: in 4 bits (28
+// MB) 13.9 us, ten layers at a time 104: the minima and maxima of the codes' values (ALU pipe
+// 60%, issue slots 59%); in fp16 (101 MB) 21, ten layers 176, 6.1 TB/s: a call of one layer is three
+// blocks a warp, start and end.  Scores of their 12 x 16 nodes, 40 heads over 8, 9 us: 192
+// CTAs of 64 places, of which five heads leave three of eight empty.  A decode step of 2
+// sequences over 2048 blocks, digests and scores, 9.0 us in two launches.
 #include <climits>
 #include <math.h>
 
@@ -96,7 +97,7 @@ digest_kernel(const spec_digest dg, const Keys keys, int n, const int32_t* __res
   constexpr int BIT = LANES == 16 ? 4 : LANES == 8 ? 3 : 2;
   using Load = typename std::conditional<Q4, uint2, uint4>::type;
   constexpr int KEPT = REGS >> (5 - BIT);
-  grid_dep_wait();  // (nothing behind starts early: 12.7 us of 12 prompts instead of 13.0)
+  grid_dep_wait();  // (nothing behind starts early: 2% less for 12 prompts)
   const int lane = threadIdx.x & 31;
   // (32 bits: the host sees to it)
   const uint32_t w = blockIdx.x * DG_WARPS + (threadIdx.x >> 5), unit = w / split, y = w - unit * split;
@@ -669,8 +670,8 @@ int launch_digest(const spec_digest* dg, const Keys& keys, bool q4, int n, const
   const double units = (double)n * dg->n_layers * dg->n_kv_heads;
   if (units > (1 << 30)) return fail(SPEC_E_SHAPE, "n * n_layers * n_kv_heads too large");
   // warps of a unit: two waves of what is resident, where the blocks are that many (12 prompts
-  // of 4095 in 4 bits 13.0 us with three waves, 13.6 so, 14.2 with one; a step's new blocks of 2
-  // sequences, for which most warps have nothing to do, with their scores 9.6, 8.9 and 8.4)
+  // of 4095 in 4 bits are 4% faster with three waves, 4% slower with one; a step's new blocks of 2
+  // sequences, for which most warps have nothing to do, with their scores 9.6, 8.9 and 8.4 us)
   const int64_t most = (int64_t)dg->max_pages * (dg->page_size / dg->block);
   const int64_t fit = std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)(device_sms() * 40 / units)));
   const int64_t rounds = (most + fit - 1) / fit;

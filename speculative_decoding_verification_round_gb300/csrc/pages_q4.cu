@@ -11,7 +11,11 @@
 // quantisation; reading back 53.5 us, 6.1 TB/s, reads and writes together.  A head's rows to
 // a warp, whose codes are neighbours, 78 and 63 (with 32 rows a CTA in the read 65); more rows
 // in flight or stores of 32 bytes: no better.  12 paths of up to 16 nodes in 40 layers: 10.5
-// and 6.3 us: the launch, then slot, length and page in front of the first row.
+// and 6.3 us: the launch, then slot, length, page and a barrier in front of the first row (the
+// commit's own rows, which hang on the path alone, are loaded behind that, too).
+// 12 pages of 64 positions copied in 40 layers 14.0 us (floor 10.4; fp16 42 and 37); extending 48 branches of
+// half a shared page 37 (floor 10.2; fp16 52 and 36): issue slots 70%, a division a word, scales
+// two bytes at a time.
 #include <algorithm>
 #include <climits>
 

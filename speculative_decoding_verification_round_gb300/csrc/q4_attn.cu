@@ -13,9 +13,10 @@
 // run at 5.4 TB/s; what bounds it is a warp's chain of codes to operands, products and
 // weights, about 24 instructions a position of 8 rows, with 12 to 16 warps an SM (issue
 // slots 51% used, the tensor pipe 45%).  Other stages, CTAs an SM and keys at a time are up to
-// 12% slower.  One node over 8191 positions 12.0 us,
-// of 16 sequences in a window of 4096 (14 heads over 2 of 64) 11.2: launch, lookups, one or
-// two steps a warp, the join.
+// 12% slower.  One node over 8191 positions 12.3 us: a tile of 128 a CTA, 520 of them, whose 65
+// results a unit a second kernel joins; 16 sequences in a window of 4096 (14 heads over 2
+// of 64) 11.3: four CTAs a unit, one an SM, 131 steps of 32 positions over their 32 warps,
+// four or five each.
 #include <math.h>
 
 #include <algorithm>
@@ -486,14 +487,23 @@ cudaError_t launch_q4_rows(const TreeArgs& a, int n_cta, cudaStream_t st) {
                         : launch_q4<HD, 4>(a, n_cta, st);
 }
 // CTAs of a unit in the clusters' form, or 0 for the cut's: up to eight (clusters of more
-// leave SMs of a GPC unused), as many as are resident, one an SM, and keep a step of 32
-// positions for each warp, by the most positions that a sequence can have (its table's,
-// the window's).  Where the clusters fill the SMs they are faster with up to eight steps for a
-// warp (4 sequences of 8000 positions 18.4 us against 24.4, 32 of 1000 16.4 against 25.0), and
-// with up to 8 rows sixteen (32 of 4000 42 against 51, 40 of 4000 60 and 58), however many
-// units there are (200 of 300, 14 heads over 2 of 64, 8.4 against 17.8; 16 rows, 100 of
-// 1000, 76 and 66: not there); with up to three steps anywhere (one sequence of 1000 8.2 against
-// 10.0; of 16000, eight steps on 64 SMs, 16.7 and 14.1).
+// leave SMs of a GPC unused), one an SM, as long as each warp has a step of 32 positions.  The
+// lengths are on the device; what counts here is the most positions that a sequence can
+// have: its table's, or the window's.  Clusters take
+//   up to three steps a warp anywhere (one sequence of 1000 positions 8.2 us against the cut's
+//   10.0; of 16000, eight steps on 64 SMs, 16.7 and 14.1: not there);
+//   up to eight where the CTAs are three quarters of the SMs, and with up to 8 rows up to sixteen;
+//   of more than two units an SM those with up to 8 rows (160 of 300, 14 heads over 2 of 64, 8.0
+//   against 17; 16 rows, 100 of 1000, 76 and 66: not there).
+// With tables of 4096 positions and up to 8 rows 20 to 28, 39 to 56 and 77 to 113 units so go
+// to the cut, all others to clusters.  These and the cut there, 8 kv heads of 128, n sequences of
+// 4000: n = 4 12.5 and 18.0, 8 17.7 and 26.5, 16 27 and 32, 20 40 and 38, 32 42 and 53, 40 62
+// and 59, 64 79 and 82; of 1000 in such tables 16 11.6 and 17.0, 64 29 and 30.  What this
+// costs are batches of one long sequence among short ones, of which the cut gives all CTAs a
+// part: 4000 beside 100 for each of the others n = 16 25.6 and 15.5, 36 26 and 16.5, 64 27 and 23;
+// lengths spread evenly up to 4000 n = 16 25 and 20, 36 33 and 39, 64 51 and 58.  Between the
+// ranges two CTAs a unit would be faster for 5 to 9 sequences (5 of 4000 21.4 us by the cut, 17.4 so;
+// 10 22 and 24).
 int unit_ranks(const TreeArgs& a) {
   const int64_t units = (int64_t)a.n_seq * a.nkv, all = (int64_t)a.max_pages * a.page_size;
   const int64_t most = a.window > 0 ? std::min<int64_t>(all, (int64_t)a.window + a.sinks + 2 * WARP_KEYS) : all;
