@@ -259,6 +259,53 @@ def test_pages_that_nobody_sees_may_be_gone(dev, kernel, hd, rows, nq, nt):
         assert np.array_equal(got[1].view(np.uint16), want[1].view(np.uint16))
 
 
+@pytest.mark.parametrize(KEYS, [UNIT[2], UNIT[4], *CUT[:2], *CUT[4:], TC[1], TC[2], TC[4]])
+def test_planes_of_more_than_4_gigabytes(dev, kernel, hd, rows, nq, nt):
+    """Pages behind 2^32 bytes of codes: attention, copies, commit and reading back."""
+    import torch
+    import speculative_decoding_verification_round_gb300 as sv
+    g = np.random.default_rng([hd, nt, 10])
+    c = case_of(dev, g, kernel, hd, rows, nq, nt)
+    want = c.call()
+    c.check(want)
+    used = c.ks.shape[1]
+    first = (1 << 32) // (2 * 32 * hd // 2) + 5
+    big = [torch.empty((1, first + used, *a.shape[2:]), dtype=torch.uint8 if a.dtype == np.uint8 else torch.float16, device=dev)
+           for a in (c.kc, c.vc, c.ks, c.vs)]
+    for t, a in zip(big, (c.kc, c.vc, c.ks, c.vs)):
+        t[:, :used] = c.T(a)
+    assert big[0].numel() > 1 << 32
+    # every page to the end, by the operator
+    st = torch.full((used,), 9, dtype=torch.int32, device=dev)
+    ids = torch.arange(used, dtype=torch.int32, device=dev)
+    table = c.T(np.where(c.table >= 0, c.table + first, c.table).astype(np.int32))
+    kv = sv.KVPagesQ4(*big, table, c.T(c.slot_len))
+    sv.spec_pages_q4_copy(kv, used, ids, ids + first, st)
+    assert (st == 0).all()
+    for t in big:
+        t[:, :used] = 0
+    got = c.call(kv)
+    assert c.status.tolist() == [0, 0] and np.array_equal(got.view(np.uint16), want.view(np.uint16))
+    # the last positions read back, then written over with the nodes' rows
+    n = c.lens[0]
+    pos0, n_pos = (torch.tensor([x], dtype=torch.int32, device=dev) for x in (n - 40, 40))
+    out = [torch.zeros((1, 1, 40, 2, hd), dtype=torch.float16, device=dev) for _ in range(2)]
+    slot = c.T(c.slots[:1])
+    sv.spec_pages_q4_read(kv, 1, slot, 40, pos0, n_pos, out[0], out[1], st)
+    assert int(st[0]) == 0
+    for o, which in zip(out, (0, 1)):
+        assert np.array_equal(o[0, 0].cpu().numpy(), c.cached(which, 0)[n - 40:])
+    m = min(nt, n - n // 32 * 32)  # (no page is missing)
+    kv._keep[-2][int(c.slots[0])] = n - m
+    count = torch.tensor([m], dtype=torch.int32, device=dev)
+    sv.spec_pages_q4_commit(kv, 1, slot, nt, c.T(c.kn[None, :1]), c.T(c.vn[None, :1]), None, count, st)
+    assert int(st[0]) == 0 and int(kv._keep[-2][int(c.slots[0])]) == n
+    sv.spec_pages_q4_read(kv, 1, slot, 40, pos0, n_pos, out[0], out[1], st)
+    for o, x, which in zip(out, (c.kn, c.vn), (0, 1)):
+        rows_ = np.concatenate([c.cached(which, 0)[n - 40:n - m].astype(np.float64), lc.values(*lc.pack(*lc.quantise(x[0, :m])))])
+        assert np.array_equal(o[0, 0].cpu().numpy().astype(np.float64), rows_)
+
+
 # ---------------------------------------------------------------------------
 # the cut on what the other forms are tested with in test_gpu_q4.py
 # ---------------------------------------------------------------------------
